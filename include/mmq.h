@@ -39,6 +39,13 @@
  *                              integer dot per sub-block, folded in f32 per
  *                              sub-block); slower, kept as the reference form
  *                              on the GPU and for q8_0
+ *   positions + cache append . mmq_rope_append (rotary q and k, k and v into the
+ *                              paged cache)
+ *   attention, new tokens .... mmq_attn_decode (1..16 new tokens per sequence
+ *                              over the paged cache)
+ *   bounded cache ............ mmq_kv_evict (by accumulated attention weight)
+ *   drafted tokens ........... mmq_spec_verify (speculative sampling's test and
+ *                              resampling)
  *   diagnostics .............. mmq_debug_subdots_* (the int32 dots themselves),
  *                              mmq_probe_tensor_peak, mmq_debug_fault_inject
  *                              (test-only)
@@ -109,10 +116,12 @@ enum {
     MMQ_ERR_DRIVER = -7,    /* the driver could not build a TMA tensor map         */
     MMQ_ERR_CUDA = -8,      /* (mmq_check_status) a CUDA error is pending          */
     MMQ_ERR_SCRATCH = -9,   /* the call needs more than the library's static scratch */
-    MMQ_ERR_DEVICE = -10    /* current device index >= 64 (the library's per-device tables) */
+    MMQ_ERR_DEVICE = -10,   /* current device index >= 64 (the library's per-device tables) */
+    MMQ_ERR_INDEX = -11     /* (mmq_check_status) a page id, length, count or token that a
+                               kernel read from device memory was out of range          */
 };
 
-/* Library ABI version; bumped on any signature or format change. */
+/* Library ABI version; bumped on any change of a signature or format (not when calls are added). */
 int mmq_version(void);
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -411,6 +420,140 @@ int mmq_debug_subdots_q5K(const void *w, const uint16_t *xh, int32_t *out,
                           int T, int O, int K, mmq_stream_t stream);
 int mmq_debug_subdots_q8_0(const void *w, const uint16_t *xh, int32_t *out,
                            int T, int O, int K, mmq_stream_t stream);
+
+/*
+ * Paged key-value cache of one layer
+ * ----------------------------------
+ * Entry `slot` (0-based, in order of arrival) of sequence b lies in page
+ * table[b*cols + slot / page_size] at offset slot % page_size:
+ *     k element d of head h:  k[page*k_page + h*k_head + offset*k_slot + d]
+ * and v likewise with its own strides (in elements; multiples of 8, so that
+ * every row of `dim` values starts on 16 bytes).  Pages may be in any order
+ * and table entries past a sequence's length may hold anything.  `weight` and
+ * `pos` are per entry and head, [pages][heads][page_size], through the same
+ * table: the attention weight the entry has received so far, and its
+ * position; either may be NULL where the call does not need it.  len[b] is
+ * the sequence's number of entries, the new tokens of the running step
+ * included: the caller raises it once per step, before the step's first
+ * layer, and lowers it after mmq_kv_evict or a rejected draft.
+ * A page id outside 0..pages-1, or a len outside 0..cols*page_size, makes the
+ * kernel skip that access (the entry reads as absent) and report
+ * MMQ_ERR_INDEX through mmq_check_status.
+ */
+enum { MMQ_F16 = 0, MMQ_BF16 = 1, MMQ_F32 = 2 };
+
+typedef struct mmq_kv_cache {
+    void *k, *v;                      /* f16 or bf16 pools                              */
+    float *weight;                    /* [pages][heads][page_size] or NULL              */
+    int32_t *pos;                     /* [pages][heads][page_size] or NULL              */
+    const int32_t *table;             /* [seqs][cols] page ids                          */
+    const int32_t *len;               /* [seqs] entries                                 */
+    int64_t k_page, k_head, k_slot;   /* strides of k in elements                       */
+    int64_t v_page, v_head, v_slot;   /* strides of v in elements                       */
+    int64_t pages;                    /* pages in each pool, 1 .. 2^31-1                */
+    int dtype;                        /* MMQ_F16 or MMQ_BF16 (k and v)                  */
+    int heads;                        /* key-value heads                                */
+    int dim;                          /* values per head: a multiple of 8, 8 .. 256     */
+    int page_size;                    /* entries per page, >= 1                         */
+    int seqs;                         /* sequences, 0 .. 65535                          */
+    int cols;                         /* pages per table row; cols*page_size <= 2^30    */
+} mmq_kv_cache;
+
+/*
+ * Rotary positions, and the append of the new tokens' keys and values.
+ * Rows i = b*new_tokens + t, t < new_tokens, of q [.][q_heads][dim], k and v
+ * [.][heads][dim] are f32, ldq/ldk/ldv floats apart (multiples of 4), as the
+ * projections leave them.  Of every q and k head the first `rot` values (even,
+ * 2..dim) are rotated in rot/2 pairs, the rest passes through; pair i is
+ * (i, i + rot/2), or (2i, 2i+1) with interleaved != 0:
+ *     (a, b) -> magnitude * (a cos - b sin, a sin + b cos),
+ *     angle of pair i at position x = 2 pi frac(x * freq[i] / 2^64).
+ * freq [rot/2] holds turns per position as 64-bit fractions: the product
+ * wraps exactly, so the angle is as good at position 2^30 as at 0, and a
+ * scaling for long contexts is a change of the table (ops.rope_table).
+ * pos [seqs*new_tokens] int32.  q_out [.][q_heads][dim], rows ldo floats
+ * apart, may be q itself (ldo == ldq).  new_len [seqs] (NULL: new_tokens
+ * each) says how many of a sequence's rows are there: row t < new_len[b] goes
+ * to slot len[b] - new_len[b] + t of every head, rounded to the cache's type
+ * (nearest even); a row past it gets q_out = 0 and is not stored.  Where the
+ * cache has them, `weight` of a new entry is set to 0 and `pos` to the row's
+ * position.  Slots must not repeat within a call.
+ */
+int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, int rot, float magnitude,
+                    int interleaved, const float *q, int64_t ldq, const float *k, int64_t ldk,
+                    const float *v, int64_t ldv, const int32_t *pos, const int32_t *new_len,
+                    float *q_out, int64_t ldo, int q_heads, int new_tokens, mmq_stream_t stream);
+
+/*
+ * Attention of the newest tokens over the cache (decode, or drafted tokens
+ * scored together).  q rows as above (rotated), q head j reads key-value head
+ * j / (q_heads/heads); row t < new_len[b] (NULL: new_tokens) of sequence b
+ * sees the slots below len[b] - new_len[b] + t + 1:
+ *     s = scale * q.k,  p = exp(s - max) / sum,  out = sum p v
+ * out [seqs*new_tokens][q_heads][dim] f32, contiguous.  A row that sees no
+ * slot, or with t >= new_len[b], gets 0.  What a row does not see has no
+ * influence on it, whatever it holds (stale NaN or Inf included).  Statistics
+ * and sums are f32; q and p enter the tensor core as sums of two f16 (three
+ * bf16) parts, so products carry f32's precision.  Results do not depend on
+ * timing: they repeat bit for bit.
+ * accumulate != 0 adds to cache->weight, for every entry a sequence has, the
+ * sum of p over its rows and the query heads of the key-value head.
+ * 1 <= new_tokens <= 16, q_heads a multiple of heads, scale finite.
+ * `work` and `counters` as mmq_attn_sizes says; the counters are zero before
+ * the first call and every call leaves them zero.  Calls that share them must
+ * be ordered (one stream).
+ */
+int mmq_attn_sizes(const mmq_kv_cache *cache, int q_heads, int new_tokens, int accumulate,
+                   int64_t *work_floats, int64_t *n_counters);
+int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_t ldq, const int32_t *new_len,
+                    float *out, int q_heads, int new_tokens, float scale, int accumulate,
+                    float *work, int32_t *counters, mmq_stream_t stream);
+
+/*
+ * Eviction: every sequence with more than `budget` entries is cut down to
+ * `budget` for each head by itself.  Entries with pos >= keep_from[b] rank
+ * first, the others by `weight`; the first `budget` stay, ties going to the
+ * lower slot.  Those that stay in a slot past the budget move, in order of
+ * their slots, into the slots below it that became free, in order: nothing
+ * else moves, and the order of slots is not the order of positions any more
+ * (the attention does not need it: keys carry their rotation).  k and v move
+ * in place; the bookkeeping of slots 0 .. min(len, budget)-1 is written to
+ * weight_out and pos_out (the layout of weight and pos, no overlap with
+ * them), which the caller uses from then on, so that a call leaves `weight`
+ * and `pos` as they were.  Slots past that keep what they held.  Weights must
+ * not be NaN.  cache->len is not changed: the caller lowers it to the budget
+ * once all layers are done.  The pages of a sequence's first `budget` slots
+ * must not be shared with another.
+ * cols*page_size <= 262144.  `work` holds mmq_evict_sizes' count of ints.
+ */
+int mmq_evict_sizes(const mmq_kv_cache *cache, int budget, int64_t *work_ints);
+int mmq_kv_evict(const mmq_kv_cache *cache, int budget, const int32_t *keep_from, float *weight_out,
+                 int32_t *pos_out, int32_t *work, mmq_stream_t stream);
+
+/*
+ * Verification of drafted tokens (speculative sampling).  target
+ * [seqs][drafts+1][vocab] and draft [seqs][drafts][vocab] are probabilities
+ * of one type (MMQ_F16, MMQ_BF16 or MMQ_F32), contiguous; draft NULL means
+ * drafts that were not sampled (probability 1 for the drafted token).
+ * tokens [seqs][drafts]; uniform [seqs][drafts+1] in [0, 1); count [seqs]
+ * (NULL: drafts each) the number of tokens drafted.  Draft i is accepted
+ * while  uniform[i] * draft_i(x) < target_i(x)  (f32, rounded once).  At the
+ * first draft a that is not, the token a is drawn from max(target_a -
+ * draft_a, 0); with all accepted, from target_count.  The drawing is exact in
+ * whole numbers, so it does not depend on the order of any sum: with
+ * w_j = round(2^40 max(p_j - q_j, 0)) (nearest even; the difference in f32,
+ * limited to 1), W their sum and u = floor(2^24 uniform[drafts]), the token is
+ * the lowest j with w_0 + ... + w_j > floor(W u / 2^24).  If W = 0 (the two
+ * agree), the target alone is drawn from; if that is 0 too, the token is 0.
+ * out [seqs][drafts+1] gets the accepted tokens, the drawn one, then -1;
+ * accepted [seqs] how many drafts were accepted.  A drafted token outside
+ * 0..vocab-1 is not accepted, and then the target alone is drawn from; a
+ * count outside 0..drafts is limited to it; both report MMQ_ERR_INDEX.
+ * 0 <= seqs <= 65535, 1 <= drafts <= 64, 1 <= vocab <= 2^20.
+ */
+int mmq_spec_verify(const void *target, const void *draft, int dtype, const int32_t *tokens,
+                    const float *uniform, const int32_t *count, int32_t *out, int32_t *accepted,
+                    int seqs, int drafts, int vocab, mmq_stream_t stream);
 
 /*
  * Diagnostic: measured warp-level tensor throughput of the current device,

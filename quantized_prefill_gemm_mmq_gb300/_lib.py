@@ -18,6 +18,13 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 
+class KVCacheC(ctypes.Structure):
+    """mmq_kv_cache of include/mmq.h."""
+    _fields_ = ([(n, _P) for n in ("k", "v", "weight", "pos", "table", "len")] +
+                [(n, _I64) for n in ("k_page", "k_head", "k_slot", "v_page", "v_head", "v_slot", "pages")] +
+                [(n, _I) for n in ("dtype", "heads", "dim", "page_size", "seqs", "cols")])
+
+
 # name -> (restype, argtypes); mirrors include/mmq.h
 SIGNATURES = {
     "mmq_version": (_I, []),
@@ -44,6 +51,12 @@ SIGNATURES = {
     "mmq_gemm_q6K_subblock": (_I, [_P, _P, _P, _P, _I, _I, _I, _P]),
     "mmq_debug_subdots_q4K": (_I, [_P, _P, _P, _I, _I, _I, _P]),
     "mmq_debug_subdots_q6K": (_I, [_P, _P, _P, _I, _I, _I, _P]),
+    "mmq_rope_append": (_I, [_P, _P, _I, ctypes.c_float, _I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I, _I, _P]),
+    "mmq_attn_sizes": (_I, [_P, _I, _I, _I, _P, _P]),
+    "mmq_attn_decode": (_I, [_P, _P, _I64, _P, _P, _I, _I, ctypes.c_float, _I, _P, _P, _P]),
+    "mmq_evict_sizes": (_I, [_P, _I, _P]),
+    "mmq_kv_evict": (_I, [_P, _I, _P, _P, _P, _P, _P]),
+    "mmq_spec_verify": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "mmq_check_status": (_I, [_P, _P]),
     "mmq_last_failure_info": (_I, [_P]),
     "mmq_debug_fault_inject": (_I, [_I, _I]),

@@ -220,6 +220,12 @@ extern "C" int mmq_check_status(mmq_stream_t stream, int *detail)
         const int zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         cudaMemcpyToSymbol(mmq::g_status, zero, sizeof(zero));
         for (int i = 0; i < 4; ++i) g_last_failure[i] = h[4 + i];
+    } else {
+        // nothing from the GEMMs: the decode-side operators' own status word
+        const int rc = mmq::take_serve_status(h);
+        if (rc != MMQ_OK) return rc;
+        if (h[0] != 0)
+            for (int i = 0; i < 4; ++i) g_last_failure[i] = 0;
     }
     if (detail)
         for (int i = 0; i < 4; ++i) detail[i] = h[i];

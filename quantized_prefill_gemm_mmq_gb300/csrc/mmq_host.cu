@@ -121,6 +121,7 @@ extern "C" const char *mmq_status_str(int status)
     case MMQ_ERR_CUDA: return "CUDA error pending on the stream";
     case MMQ_ERR_SCRATCH: return "split-K scratch needed exceeds the library's static scratch (4 Mi f32 partial sums, 8192 tiles)";
     case MMQ_ERR_DEVICE: return "current device index is beyond the library's per-device tables (64 devices)";
+    case MMQ_ERR_INDEX: return "a page id, length, count or token read on the device was out of range";
     default: return "unknown status";
     }
 }

@@ -18,6 +18,10 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 // Launch-error translation: clears the sticky-free error state and maps it.
 int launch_status();
 
+// Reads and clears the status word of the decode-side operators' translation
+// unit: eight ints as the GEMM unit's own.  MMQ_OK or MMQ_ERR_CUDA.
+int take_serve_status(int (&h)[8]);
+
 // 2-D tiled tensor map over a row-major array: `inner` elements per row of
 // `elem_bytes` each, `rows` rows, `row_stride_bytes` apart; box of
 // box_inner x box_rows elements; swizzle as given.  Returns MMQ_OK or

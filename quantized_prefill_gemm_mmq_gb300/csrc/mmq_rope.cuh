@@ -1,0 +1,233 @@
+// mmq_rope.cuh -- rotary positions on f32 q and k rows, and the append of the
+// new keys and values to the paged cache (mmq_rope_append).
+//
+// Pair (a, b) at position x turns by 2 pi frac(x f / 2^64), f being turns per
+// position as a 64-bit fraction.  The 64-bit product keeps the low 64 bits,
+// which is the fraction of the turns exactly; its high 32 bits as a signed
+// number, times 2^-31, are the half turns in [-1, 1) that sincospi takes, so
+// no range reduction is needed and no position is too large.
+//
+// Bound by memory: per row 8 B per q value (read, write) and 6 B per k and v
+// value.  One thread owns the same eight values (four pairs) of several heads,
+// so that it computes its four sines and cosines once for all of them; a
+// block's threads cover whole heads side by side, one block per row and part
+// of its heads.
+#pragma once
+
+namespace mmq {
+namespace {
+
+constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_BATCH = 4;        // heads whose loads a thread has in flight
+
+struct RopeParams {
+    mmq_kv_cache c;
+    const int64_t *freq;
+    const float *q, *k, *v;
+    const int32_t *pos, *new_len;
+    float *q_out;
+    int64_t ldq, ldk, ldv, ldo;
+    float magnitude;
+    int rot, interleaved, q_heads, new_tokens;
+    int heads_per_block;             // of the row's q_heads + 2*heads
+};
+
+// P pairs per thread: 4 where rot and dim are multiples of 8 (16-byte
+// accesses), else 1.
+template <typename T, int P>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopeParams p)
+{
+    const int D = p.c.dim, units = D / (2 * P);
+    const int u = threadIdx.x % units, hl = threadIdx.x / units, lanes = blockDim.x / units;
+    const int row = blockIdx.x, b = row / p.new_tokens, t = row - b * p.new_tokens;
+    const int total = p.q_heads + 2 * p.c.heads;
+    const int h0 = blockIdx.y * p.heads_per_block;
+    const int h1 = min(total, h0 + p.heads_per_block);
+    if (hl >= lanes) return;
+
+    const bool rotated = u * 2 * P < p.rot;
+    // element offsets of the thread's first and second P values within a head
+    int e0 = u * 2 * P, e1 = e0 + P;
+    if (rotated && !p.interleaved) {
+        e0 = u * P;
+        e1 = p.rot / 2 + u * P;
+    }
+    const int n = new_count(p.new_len, b, p.new_tokens, KID_ROPE);
+    const int len = cache_len(p.c, b, KID_ROPE);
+    const int slot = len - n + t;
+    bool live = t < n, store = live;
+    int64_t page = 0;
+    int off = 0;
+    if (live) {
+        if (slot < 0) {
+            record_error(MMQ_ERR_INDEX, KID_ROPE, SITE_LEN);
+            store = false;
+        } else {
+            const int col = slot / p.c.page_size;
+            off = slot - col * p.c.page_size;
+            const int pg = cache_page(p.c, b, col, KID_ROPE);
+            store = pg >= 0;
+            page = pg;
+        }
+    }
+    float cs[P], sn[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        cs[i] = 1.f;
+        sn[i] = 0.f;
+    }
+    const int x = __ldg(p.pos + row);
+    if (rotated && live) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const uint64_t turns = (uint64_t)(int64_t)x * (uint64_t)__ldg(p.freq + u * P + i);
+            sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+            sn[i] *= p.magnitude;
+            cs[i] *= p.magnitude;
+        }
+    }
+
+    for (int hb = h0 + hl; hb < h1; hb += lanes * ROPE_BATCH) {
+        float a[ROPE_BATCH][P], c[ROPE_BATCH][P];
+#pragma unroll
+        for (int i = 0; i < ROPE_BATCH; ++i) {
+            const int h = hb + i * lanes;
+            if (h >= h1 || !live) continue;
+            const float *src = h < p.q_heads ? p.q + row * p.ldq + (int64_t)h * D
+                               : h < p.q_heads + p.c.heads ? p.k + row * p.ldk + (int64_t)(h - p.q_heads) * D
+                                                           : p.v + row * p.ldv + (int64_t)(h - p.q_heads - p.c.heads) * D;
+            // values are not rotated: their halves lie side by side
+            const int s0 = h < p.q_heads + p.c.heads ? e0 : u * 2 * P, s1 = h < p.q_heads + p.c.heads ? e1 : u * 2 * P + P;
+            if constexpr (P == 4) {
+                if (rotated && p.interleaved && h < p.q_heads + p.c.heads) {
+                    const float4 lo = *reinterpret_cast<const float4 *>(src + s0), hi = *reinterpret_cast<const float4 *>(src + s1);
+                    a[i][0] = lo.x, c[i][0] = lo.y, a[i][1] = lo.z, c[i][1] = lo.w;
+                    a[i][2] = hi.x, c[i][2] = hi.y, a[i][3] = hi.z, c[i][3] = hi.w;
+                } else {
+                    *reinterpret_cast<float4 *>(a[i]) = *reinterpret_cast<const float4 *>(src + s0);
+                    *reinterpret_cast<float4 *>(c[i]) = *reinterpret_cast<const float4 *>(src + s1);
+                }
+            } else {
+                a[i][0] = src[s0];
+                c[i][0] = src[s1];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ROPE_BATCH; ++i) {
+            const int h = hb + i * lanes;
+            if (h >= h1) continue;
+            const bool is_v = h >= p.q_heads + p.c.heads;
+            const int d0 = is_v ? u * 2 * P : e0, d1 = is_v ? u * 2 * P + P : e1;
+            float y0[P], y1[P];
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                if (!live) {
+                    y0[j] = y1[j] = 0.f;
+                } else if (rotated && !is_v) {
+                    y0[j] = a[i][j] * cs[j] - c[i][j] * sn[j];
+                    y1[j] = a[i][j] * sn[j] + c[i][j] * cs[j];
+                } else {
+                    y0[j] = a[i][j];
+                    y1[j] = c[i][j];
+                }
+            }
+            if constexpr (P == 4) {
+                if (rotated && p.interleaved && !is_v) {     // back side by side
+                    const float z0[4] = {y0[0], y1[0], y0[1], y1[1]}, z1[4] = {y0[2], y1[2], y0[3], y1[3]};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        y0[j] = z0[j];
+                        y1[j] = z1[j];
+                    }
+                }
+            }
+            if (h < p.q_heads) {
+                float *dst = p.q_out + row * p.ldo + (int64_t)h * D;
+                if constexpr (P == 4) {
+                    *reinterpret_cast<float4 *>(dst + d0) = make_float4(y0[0], y0[1], y0[2], y0[3]);
+                    *reinterpret_cast<float4 *>(dst + d1) = make_float4(y1[0], y1[1], y1[2], y1[3]);
+                } else {
+                    dst[d0] = y0[0];
+                    dst[d1] = y1[0];
+                }
+                continue;
+            }
+            if (!store) continue;
+            const int kh = is_v ? h - p.q_heads - p.c.heads : h - p.q_heads;
+            T *dst = is_v ? static_cast<T *>(p.c.v) + page * p.c.v_page + kh * p.c.v_head + off * p.c.v_slot
+                          : static_cast<T *>(p.c.k) + page * p.c.k_page + kh * p.c.k_head + off * p.c.k_slot;
+            if constexpr (P == 4) {
+                const uint2 w0 = make_uint2(pack2<T>(y0[0], y0[1]), pack2<T>(y0[2], y0[3]));
+                const uint2 w1 = make_uint2(pack2<T>(y1[0], y1[1]), pack2<T>(y1[2], y1[3]));
+                if (d1 == d0 + 4) {
+                    *reinterpret_cast<uint4 *>(dst + d0) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                } else {
+                    *reinterpret_cast<uint2 *>(dst + d0) = w0;
+                    *reinterpret_cast<uint2 *>(dst + d1) = w1;
+                }
+            } else {
+                dst[d0] = to_cache<T>(y0[0]);
+                dst[d1] = to_cache<T>(y1[0]);
+            }
+            if (!is_v && u == 0) {
+                const int64_t e = (page * p.c.heads + kh) * p.c.page_size + off;
+                if (p.c.weight) p.c.weight[e] = 0.f;
+                if (p.c.pos) p.c.pos[e] = x;
+            }
+        }
+    }
+}
+
+template <typename T>
+int launch_rope(RopeParams &p, int sms, cudaStream_t stream)
+{
+    const int D = p.c.dim, total = p.q_heads + 2 * p.c.heads;
+    const bool wide = p.rot % 8 == 0;
+    const int units = wide ? D / 8 : D / 2;
+    const int lanes = ROPE_THREADS / units > 0 ? ROPE_THREADS / units : 1;
+    const int64_t rows = (int64_t)p.c.seqs * p.new_tokens;
+    // One block walks all heads of a row when there are rows enough to fill the
+    // device; with few rows, a row's heads are spread over blocks down to one
+    // pass of the block's lanes each.
+    const int64_t want = (int64_t)sms * 8;
+    int64_t parts = (want + rows - 1) / rows;
+    const int most = (total + lanes - 1) / lanes;
+    if (parts > most) parts = most;
+    if (parts < 1) parts = 1;
+    p.heads_per_block = (int)((total + parts - 1) / parts);
+    p.heads_per_block = (p.heads_per_block + lanes - 1) / lanes * lanes;
+    const dim3 grid((unsigned)rows, (unsigned)((total + p.heads_per_block - 1) / p.heads_per_block));
+    if (wide)
+        rope_append_kernel<T, 4><<<grid, units * lanes, 0, stream>>>(p);
+    else
+        rope_append_kernel<T, 1><<<grid, units * lanes, 0, stream>>>(p);
+    return launch_status();
+}
+
+}  // namespace
+}  // namespace mmq
+
+extern "C" int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, int rot, float magnitude,
+                               int interleaved, const float *q, int64_t ldq, const float *k, int64_t ldk,
+                               const float *v, int64_t ldv, const int32_t *pos, const int32_t *new_len, float *q_out,
+                               int64_t ldo, int q_heads, int new_tokens, mmq_stream_t stream)
+{
+    using namespace mmq;
+    int rc = check_cache(cache);
+    if (rc != MMQ_OK) return rc;
+    const int64_t D = cache->dim;
+    if (rot < 2 || rot > D || (rot & 1) || q_heads < 1 || q_heads > 65535 || new_tokens < 0 ||
+        (int64_t)cache->seqs * new_tokens > 0x7fffffff || ldq < q_heads * D || ldo < q_heads * D ||
+        ldk < cache->heads * D || ldv < cache->heads * D || (q == q_out && ldq != ldo))
+        return MMQ_ERR_SHAPE;
+    if (cache->seqs == 0 || new_tokens == 0) return MMQ_OK;
+    if (!freq || !q || !k || !v || !pos || !q_out) return MMQ_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || ((ldq | ldk | ldv | ldo) & 3))
+        return MMQ_ERR_ALIGN;
+    if ((rc = check_arch()) != MMQ_OK) return rc;
+    RopeParams p = {*cache, freq, q, k, v, pos, new_len, q_out, ldq, ldk, ldv, ldo, magnitude, rot, interleaved ? 1 : 0,
+                    q_heads, new_tokens, 0};
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return cache->dtype == MMQ_F16 ? launch_rope<__half>(p, sm_count(), st)
+                                   : launch_rope<__nv_bfloat16>(p, sm_count(), st);
+}

@@ -1,0 +1,258 @@
+// mmq_verify.cuh -- verification of drafted tokens (mmq_spec_verify).
+//
+// Draft i is accepted while u_i q_i(x) < p_i(x).  At the first that is not,
+// the token is drawn from max(p - q, 0), else from the target's last row, by
+// inverting the cumulative sum.  The sum is of whole numbers
+// w_j = round(2^40 max(p_j - q_j, 0)), so any order of adding gives the same,
+// and the row can be split over a cluster's CTAs, warps and lanes and still
+// draw what a serial sum would.
+//
+// A cluster per sequence.  Every CTA finds the first rejection by itself (a
+// few loads), sums its part of the row in spans of SPAN values, one span per
+// warp at a time, and keeps the spans' sums; the CTAs exchange their totals
+// through distributed shared memory; the one whose part the threshold falls
+// into reads the one span again and finds the value.  So the row is read
+// once.  Bound by memory: one or two rows of the vocabulary per sequence.
+#pragma once
+
+namespace mmq {
+namespace {
+
+namespace ver {
+constexpr int THREADS = 512;
+constexpr int WARPS = THREADS / 32;
+constexpr int PER = 8;                  // values per lane and span
+constexpr int SPAN = 32 * PER;
+constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_VOCAB = 1 << 20;
+constexpr int MAX_DRAFTS = 64;
+}  // namespace ver
+
+struct VerifyParams {
+    const void *target, *draft;
+    const int32_t *tokens;
+    const float *uniform;
+    const int32_t *count;
+    int32_t *out, *accepted;
+    int drafts, vocab, spans;           // spans per CTA
+};
+
+__device__ __forceinline__ float ver_f(float x) { return x; }
+__device__ __forceinline__ float ver_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float ver_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// w_j; q may be absent
+__device__ __forceinline__ unsigned long long ver_fixed(float p, float q)
+{
+    const float d = fminf(fmaxf(__fsub_rn(p, q), 0.f), 1.f);
+    return (unsigned long long)__float2ll_rn(d * 0x1p40f);
+}
+
+__device__ __forceinline__ unsigned long long cluster_ld64(uint32_t a)
+{
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+    return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(ver::THREADS) spec_verify_kernel(const VerifyParams p)
+{
+    using namespace ver;
+    extern __shared__ __align__(16) unsigned long long s_span[];    // [spans]
+    __shared__ unsigned long long s_total[2], s_warp[WARPS];
+    __shared__ int s_first, s_bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cluster_ctarank(), n_cta = (int)cluster_nctarank(), b = blockIdx.x / n_cta;
+    const int64_t V = p.vocab;
+    const T *target = static_cast<const T *>(p.target) + (int64_t)b * (p.drafts + 1) * V;
+    const T *draft = p.draft ? static_cast<const T *>(p.draft) + (int64_t)b * p.drafts * V : nullptr;
+    const int n = new_count(p.count, b, p.drafts, KID_VERIFY);
+
+    if (warp == 0) {                                        // the first rejection
+        int first = n;
+        bool bad = false;
+        for (int i0 = 0; i0 < n && first == n; i0 += 32) {
+            const int i = i0 + lane;
+            bool no = false, off = false;
+            if (i < n) {
+                const int x = __ldg(p.tokens + (int64_t)b * p.drafts + i);
+                off = x < 0 || x >= p.vocab;
+                if (off) {
+                    no = true;
+                } else {
+                    const float pt = ver_f(target[i * V + x]), q = draft ? ver_f(draft[i * V + x]) : 1.f;
+                    no = !(__fmul_rn(__ldg(p.uniform + (int64_t)b * (p.drafts + 1) + i), q) < pt);
+                }
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, no);
+            if (m) {
+                first = i0 + __ffs(m) - 1;
+                bad = __shfl_sync(0xffffffffu, off ? 1 : 0, __ffs(m) - 1) != 0;
+            }
+        }
+        if (lane == 0) {
+            s_first = first;
+            s_bad = bad;
+            if (bad && rank == 0) record_error(MMQ_ERR_INDEX, KID_VERIFY, SITE_TOKEN);
+        }
+    }
+    __syncthreads();
+    const int a = s_first;
+    const T *pr = target + a * V;
+    // what is taken off the target: the draft's row, or (draft == nullptr) the drafted token itself
+    const bool rejected = a < n && !s_bad;
+    const T *qr = rejected && draft ? draft + a * V : nullptr;
+    const int whole_tok = rejected && !draft ? __ldg(p.tokens + (int64_t)b * p.drafts + a) : -1;
+    const int lo = min(p.vocab, rank * p.spans * SPAN), hi = min(p.vocab, lo + p.spans * SPAN);
+
+    unsigned long long r = 0, before = 0, mine = 0;
+    for (int tries = 0; tries < 2; ++tries) {
+        const bool plain = tries == 1;                      // the target alone, if nothing of the difference is left
+        unsigned long long sum = 0;
+        for (int sp = warp; sp < p.spans; sp += WARPS) {
+            unsigned long long w = 0;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int jx = lo + sp * SPAN + k * 32 + lane;
+                if (jx < hi) {
+                    const float q = plain ? 0.f : qr ? ver_f(qr[jx]) : jx == whole_tok ? 1.f : 0.f;
+                    w += ver_fixed(ver_f(pr[jx]), q);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            if (lane == 0) s_span[sp] = w;
+            sum += w;
+        }
+        if (lane == 0) s_warp[warp] = sum;
+        __syncthreads();
+        if (tid == 0) {
+            unsigned long long t = 0;
+            for (int w = 0; w < WARPS; ++w) t += s_warp[w];
+            s_total[tries] = t;
+        }
+        cluster_sync_all();
+        unsigned long long total = 0;
+        before = 0;
+        for (int c = 0; c < n_cta; ++c) {
+            const unsigned long long t = cluster_ld64(cluster_map(smem_u32(&s_total[tries]), c));
+            if (c < rank) before += t;
+            total += t;
+        }
+        mine = s_total[tries];
+        const unsigned long long u = (unsigned long long)(__ldg(p.uniform + (int64_t)b * (p.drafts + 1) + p.drafts) * 0x1p24f);
+        r = (total >> 24) * u + (((total & 0xffffffull) * u) >> 24);     // floor(total u / 2^24), below total
+        if (total > 0 || tries == 1) {
+            if (total == 0) mine = 0;
+            // ---- the span, then the value, where the sum passes r
+            if (before <= r && r < before + mine && warp == 0) {
+                unsigned long long at = before;
+                int sp = 0;
+                for (int s0 = 0; s0 < p.spans; s0 += 32) {
+                    unsigned long long x = s0 + lane < p.spans ? s_span[s0 + lane] : 0, c = x;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const unsigned long long y = __shfl_up_sync(0xffffffffu, c, o);
+                        if (lane >= o) c += y;
+                    }
+                    const unsigned m = __ballot_sync(0xffffffffu, at + c > r);
+                    if (m) {
+                        const int f = __ffs(m) - 1;
+                        sp = s0 + f;
+                        at += __shfl_sync(0xffffffffu, c - x, f);
+                        break;
+                    }
+                    at += __shfl_sync(0xffffffffu, c, 31);
+                }
+                unsigned long long w[PER], x = 0;
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {             // eight neighbours per lane
+                    const int jx = lo + sp * SPAN + lane * PER + k;
+                    w[k] = 0;
+                    if (jx < hi) {
+                        const float q = plain ? 0.f : qr ? ver_f(qr[jx]) : jx == whole_tok ? 1.f : 0.f;
+                        w[k] = ver_fixed(ver_f(pr[jx]), q);
+                    }
+                    x += w[k];
+                }
+                unsigned long long c = x;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned long long y = __shfl_up_sync(0xffffffffu, c, o);
+                    if (lane >= o) c += y;
+                }
+                const unsigned m = __ballot_sync(0xffffffffu, at + c > r);
+                if (m && lane == __ffs(m) - 1) {
+                    at += c - x;
+                    int tok = 0;
+#pragma unroll
+                    for (int k = PER - 1; k >= 0; --k) {
+                        unsigned long long upto = at;
+#pragma unroll
+                        for (int i = 0; i <= k; ++i) upto += w[i];
+                        if (upto > r) tok = lo + sp * SPAN + lane * PER + k;
+                    }
+                    p.out[(int64_t)b * (p.drafts + 1) + a] = tok;
+                }
+            }
+            if (total == 0 && rank == 0 && tid == 0) p.out[(int64_t)b * (p.drafts + 1) + a] = 0;
+            break;
+        }
+        __syncthreads();
+    }
+    if (rank == 0) {
+        for (int i = tid; i <= p.drafts; i += THREADS)
+            if (i != a)
+                p.out[(int64_t)b * (p.drafts + 1) + i] = i < a ? __ldg(p.tokens + (int64_t)b * p.drafts + i) : -1;
+        if (tid == 0) p.accepted[b] = a;
+    }
+    cluster_sync_all();                                    // no CTA leaves while another may read its shared memory
+}
+
+template <typename T>
+int launch_verify(VerifyParams &p, int seqs, cudaStream_t stream)
+{
+    // CTAs per sequence: one per 4096 values, up to a cluster of eight
+    int cl = 1;
+    while (cl < ver::MAX_CLUSTER && p.vocab > 4096 * cl) cl *= 2;
+    const int per = (p.vocab + cl - 1) / cl;
+    p.spans = (per + ver::SPAN - 1) / ver::SPAN;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(seqs * cl));
+    cfg.blockDim = dim3(ver::THREADS);
+    cfg.dynamicSmemBytes = (size_t)p.spans * 8;            // at most 4 KB
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cl;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, spec_verify_kernel<T>, p) != cudaSuccess) return launch_status();
+    return launch_status();
+}
+
+}  // namespace
+}  // namespace mmq
+
+extern "C" int mmq_spec_verify(const void *target, const void *draft, int dtype, const int32_t *tokens,
+                               const float *uniform, const int32_t *count, int32_t *out, int32_t *accepted, int seqs,
+                               int drafts, int vocab, mmq_stream_t stream)
+{
+    using namespace mmq;
+    if (seqs < 0 || seqs > 65535 || drafts < 1 || drafts > ver::MAX_DRAFTS || vocab < 1 || vocab > ver::MAX_VOCAB ||
+        (dtype != MMQ_F16 && dtype != MMQ_BF16 && dtype != MMQ_F32))
+        return MMQ_ERR_SHAPE;
+    if (seqs == 0) return MMQ_OK;
+    if (!target || !tokens || !uniform || !out || !accepted) return MMQ_ERR_NULL;
+    if (!aligned16(target) || (draft && !aligned16(draft))) return MMQ_ERR_ALIGN;
+    const int rc = check_arch();
+    if (rc != MMQ_OK) return rc;
+    VerifyParams p = {target, draft, tokens, uniform, count, out, accepted, drafts, vocab, 0};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == MMQ_F32   ? launch_verify<float>(p, seqs, s)
+           : dtype == MMQ_F16 ? launch_verify<__half>(p, seqs, s)
+                              : launch_verify<__nv_bfloat16>(p, seqs, s);
+}

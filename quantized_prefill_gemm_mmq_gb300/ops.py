@@ -7,10 +7,11 @@ a non-zero status.  No arithmetic of the method happens here.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
-from ._lib import MMQError, load
+from ._lib import KVCacheC, MMQError, load
 
 BLOCK_BYTES = {"q4_K": 144, "q6_K": 210, "q5_K": 176, "q8_0": 272}   # bytes per 256 weights of a row
 
@@ -331,6 +332,333 @@ def debug_subdots(fmt: str, w: torch.Tensor, xh: torch.Tensor, O: int) -> torch.
         st = fn(_ptr(w), _ptr(xh), _ptr(out), T, O, K, _stream(xh.device))
     _check("mmq_debug_subdots", st)
     return out
+
+
+# ---------------------------------------------- decode: around the products ---
+
+CACHE_DTYPES = {torch.float16: 0, torch.bfloat16: 1}        # MMQ_F16, MMQ_BF16
+PROB_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+ATTN_NEW_MAX = 16         # mmq_attn_decode
+
+
+def _need(t, name, dtype, shape, dev):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {dev}")
+
+
+class KVCache:
+    """Paged key-value cache of one layer over the caller's tensors.
+
+    k, v    float16 or bfloat16 [pages][heads][page_size][dim], unit stride along dim,
+            the other strides free (multiples of 8): a transposed view of
+            [pages][page_size][heads][dim] is fine;
+    table   int32 [seqs][cols]: the page of every page_size entries of a sequence;
+    lens    int32 [seqs]: entries of each sequence, the running step's new tokens
+            included (raise it once per step, before the step's first layer);
+    weight  float32 [pages][heads][page_size], attention weight received so far, or None;
+    pos     int32 [pages][heads][page_size], positions of the entries, or None.
+
+    The tensors are the state: the object keeps references and their addresses, so
+    update them in place (set_bookkeeping exchanges weight and pos after kv_evict)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                 weight: torch.Tensor | None = None, pos: torch.Tensor | None = None):
+        _need_cuda(k, v, table, lens, weight, pos)
+        if k.dtype not in CACHE_DTYPES or k.dim() != 4 or v.dtype != k.dtype or v.shape != k.shape or v.device != k.device:
+            raise ValueError("k and v must be float16 or bfloat16 [pages][heads][page_size][dim], alike")
+        for t in (k, v):
+            if t.stride(3) != 1 or any(s % 8 for s in t.stride()[:3]) or t.data_ptr() % 16:
+                raise ValueError("k and v need unit stride along dim, the other strides multiples of 8, and 16-byte alignment")
+        if table.dim() != 2 or lens.dim() != 1 or lens.shape[0] != table.shape[0]:
+            raise ValueError("table must be [seqs][cols] and lens [seqs]")
+        pages, heads, page_size, dim = k.shape
+        seqs, cols = table.shape
+        _need(table, "table", torch.int32, (seqs, cols), k.device)
+        _need(lens, "lens", torch.int32, (seqs,), k.device)
+        self.k, self.v, self.table, self.lens = k, v, table, lens
+        self.heads, self.dim, self.page_size, self.seqs, self.cols = heads, dim, page_size, seqs, cols
+        self.device = k.device
+        self._c = KVCacheC(_ptr(k), _ptr(v), None, None, _ptr(table), _ptr(lens), *k.stride()[:3], *v.stride()[:3], pages,
+                           CACHE_DTYPES[k.dtype], heads, dim, page_size, seqs, cols)
+        self._ref = ctypes.byref(self._c)
+        self._work: dict = {}
+        self.set_bookkeeping(weight, pos)
+
+    def set_bookkeeping(self, weight: torch.Tensor | None, pos: torch.Tensor | None):
+        """Use these weight and pos tensors from now on."""
+        shape = tuple(self.k.shape[:3])
+        if weight is not None:
+            _need(weight, "weight", torch.float32, shape, self.device)
+        if pos is not None:
+            _need(pos, "pos", torch.int32, shape, self.device)
+        self.weight, self.pos = weight, pos
+        self._c.weight, self._c.pos = _ptr(weight), _ptr(pos)
+
+    @classmethod
+    def allocate(cls, seqs: int, cols: int, heads: int, dim: int, page_size: int = 64, dtype=torch.float16,
+                 device=None, track: bool = True) -> "KVCache":
+        """A cache of its own with room for cols*page_size entries per sequence, pages in order, empty."""
+        dev = torch.device(device if device is not None else "cuda")
+        shape = (seqs * cols, heads, page_size)
+        k, v = (torch.zeros(shape + (dim,), dtype=dtype, device=dev) for _ in range(2))
+        table = torch.arange(seqs * cols, dtype=torch.int32, device=dev).view(seqs, cols)
+        return cls(k, v, table, torch.zeros(seqs, dtype=torch.int32, device=dev),
+                   torch.zeros(shape, dtype=torch.float32, device=dev) if track else None,
+                   torch.zeros(shape, dtype=torch.int32, device=dev) if track else None)
+
+
+def _on(dev: torch.device, fn, *args) -> int:
+    """fn(*args, stream) with `dev` current, on its current stream."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return fn(*args, stream)
+    with torch.cuda.device(dev):
+        return fn(*args, stream)
+
+
+class RopeTable:
+    """Rotation of mmq_rope_append: freq int64 [rot/2] (turns per position as 64-bit
+    fractions), rot values of each head rotated, magnitude times the result."""
+
+    def __init__(self, freq: torch.Tensor, magnitude: float = 1.0):
+        _need_cuda(freq)
+        _need(freq, "freq", torch.int64, (freq.numel(),), freq.device)
+        self.freq, self.rot, self.magnitude = freq, 2 * freq.numel(), float(magnitude)
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, context: int = 4096,
+                     fast: float = 32.0, slow: float = 1.0) -> tuple[list[float], float]:
+    """(radians per position of the rot/2 pairs, magnitude), in float64.
+
+    Pair i turns by base^(-2i/rot) per position.  scaling "linear" divides positions by
+    `factor` (position interpolation).  "base" raises the base to base*factor^(rot/(rot-2)),
+    which stretches the slowest pair by `factor` and leaves the fastest.  "by_parts" (YaRN,
+    Peng et al. 2023) divides by `factor` the pairs that turn less than `slow` times over
+    `context` positions, keeps those that turn more than `fast` times, blends linearly
+    between, and scales the rotated values by 0.1 ln(factor) + 1."""
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and at least 2")
+    if base <= 0 or factor < 1 or context < 1 or fast <= slow:
+        raise ValueError("base > 0, factor >= 1, context >= 1 and fast > slow are needed")
+    if scaling == "base" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    inv = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    if scaling in ("none", "base"):
+        return inv, 1.0
+    if scaling == "linear":
+        return [f / factor for f in inv], 1.0
+    if scaling != "by_parts":
+        raise ValueError(f"unknown scaling {scaling!r}")
+    out = []
+    for f in inv:
+        keep = min(1.0, max(0.0, (context * f / (2 * math.pi) - slow) / (fast - slow)))
+        out.append(f * keep + f / factor * (1.0 - keep))
+    return out, 0.1 * math.log(factor) + 1.0
+
+
+def rope_fixed(inv: list[float]) -> list[int]:
+    """Radians per position as signed 64-bit fractions of a turn."""
+    return [((int(f / (2 * math.pi) * 2.0 ** 64) + (1 << 63)) % (1 << 64)) - (1 << 63) for f in inv]
+
+
+def rope_table(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, context: int = 4096,
+               fast: float = 32.0, slow: float = 1.0, device=None) -> RopeTable:
+    """The rotation table of rope_frequencies, on the device."""
+    inv, magnitude = rope_frequencies(rot, base, scaling, factor, context, fast, slow)
+    return RopeTable(torch.tensor(rope_fixed(inv), dtype=torch.int64).to(device if device is not None else "cuda"), magnitude)
+
+
+def _rows(t, name, heads, dim, dev):
+    """Row stride of f32 [rows][heads][dim] whose rows may lie apart."""
+    if t.dtype != torch.float32 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.device != dev:
+        raise ValueError(f"{name} must be float32 [rows][{heads}][{dim}] on {dev}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
+
+
+def _new_len(cache, new, rows):
+    if cache.seqs == 0 or rows % cache.seqs:
+        raise ValueError("rows must be a multiple of the cache's sequences")
+    if new is not None:
+        _need(new, "new", torch.int32, (cache.seqs,), cache.device)
+    return rows // cache.seqs
+
+
+def rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+                interleaved: bool = False, new: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotate the new tokens' q and k rows and append k and v to the cache; returns the rotated q.
+
+    q f32 [seqs*n][q_heads][dim], k and v f32 [seqs*n][heads][dim] (rows may be slices of
+    one wider product row), pos int32 [seqs*n] positions.  new int32 [seqs] limits how many
+    of a sequence's n rows are there; they become the last entries of cache.lens.  `out`
+    may be q."""
+    dev = cache.device
+    _need_cuda(q, k, v, pos, rope.freq)
+    if q.dim() != 3:
+        raise ValueError("q must be float32 [rows][q_heads][dim]")
+    rows, q_heads = q.shape[0], q.shape[1]
+    n = _new_len(cache, new, rows)
+    if k.shape[0] != rows or v.shape[0] != rows:
+        raise ValueError("q, k and v must have as many rows")
+    ldq, ldk, ldv = (_rows(t, s, h, cache.dim, dev) for t, s, h in
+                     ((q, "q", q_heads), (k, "k", cache.heads), (v, "v", cache.heads)))
+    _need(pos, "pos", torch.int32, (rows,), dev)
+    if rope.rot > cache.dim or rope.freq.device != dev:
+        raise ValueError("the table rotates more values than a head has, or is on another device")
+    if out is None:
+        out = torch.empty((rows, q_heads, cache.dim), dtype=torch.float32, device=dev)
+        ldo = q_heads * cache.dim
+    else:
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        ldo = _rows(out, "out", q_heads, cache.dim, dev)
+    st = _on(dev, load().mmq_rope_append, cache._ref, rope.freq.data_ptr(), rope.rot, rope.magnitude, int(interleaved),
+             q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, pos.data_ptr(),
+             new.data_ptr() if new is not None else None, out.data_ptr(), ldo, q_heads, n)
+    if st != 0:
+        raise MMQError("mmq_rope_append", st)
+    return out
+
+
+class AttnWorkspace:
+    """Caller-owned scratch of attn_decode: partial sums (and saved scores where weights
+    are accumulated) and segment counters, which start at zero and are left at zero.  Calls
+    that share one must be ordered (one stream)."""
+
+    def __init__(self, device, floats: int, counters: int):
+        self.work = torch.empty(max(4, floats), dtype=torch.float32, device=device)
+        self.counters = torch.zeros(max(1, counters), dtype=torch.int32, device=device)
+
+    def fits(self, floats: int, counters: int) -> bool:
+        return floats <= self.work.numel() and counters <= self.counters.numel()
+
+
+def attn_sizes(cache: KVCache, q_heads: int, new_tokens: int = 1, accumulate: bool = False) -> tuple[int, int]:
+    """(floats, counters) of attn_decode's workspace."""
+    nf, nc = ctypes.c_int64(0), ctypes.c_int64(0)
+    with torch.cuda.device(cache.device):
+        st = load().mmq_attn_sizes(cache._ref, q_heads, new_tokens, int(accumulate), ctypes.byref(nf), ctypes.byref(nc))
+    _check("mmq_attn_sizes", st)
+    return nf.value, nc.value
+
+
+def attn_workspace(cache: KVCache, q_heads: int, new_tokens: int = 1, accumulate: bool = False) -> AttnWorkspace:
+    return AttnWorkspace(cache.device, *attn_sizes(cache, q_heads, new_tokens, accumulate))
+
+
+def attn_decode(cache: KVCache, q: torch.Tensor, scale: float | None = None, new: torch.Tensor | None = None,
+                accumulate: bool = False, out: torch.Tensor | None = None,
+                workspace: AttnWorkspace | None = None) -> torch.Tensor:
+    """Attention of the newest n <= 16 tokens of every sequence over the cache; f32
+    [seqs*n][q_heads][dim].
+
+    q f32 [seqs*n][q_heads][dim], rotated; row t of a sequence sees the entries up to its
+    own (new int32 [seqs] limits the rows as in rope_append; rows past it get 0).  scale
+    defaults to dim^-0.5.  accumulate adds every entry's weight to cache.weight.  Without
+    `workspace` one is allocated for this call."""
+    dev = cache.device
+    _need_cuda(q)
+    if q.dim() != 3:
+        raise ValueError("q must be float32 [rows][q_heads][dim]")
+    rows, q_heads, dim = q.shape
+    n = _new_len(cache, new, rows)
+    ldq = _rows(q, "q", q_heads, cache.dim, dev)
+    if q_heads % cache.heads:
+        raise ValueError("q_heads must be a multiple of the cache's heads")
+    if not 1 <= n <= ATTN_NEW_MAX:
+        raise ValueError(f"1 to {ATTN_NEW_MAX} new tokens per sequence")
+    if accumulate and cache.weight is None:
+        raise ValueError("the cache keeps no weights")
+    if out is None:
+        out = torch.empty((rows, q_heads, dim), dtype=torch.float32, device=dev)
+    else:
+        _need(out, "out", torch.float32, (rows, q_heads, dim), dev)
+    key = (q_heads, n, accumulate)
+    sizes = cache._work.get(key)
+    if sizes is None:
+        sizes = cache._work[key] = attn_sizes(cache, q_heads, n, accumulate)
+    if workspace is None or not workspace.fits(*sizes):
+        workspace = AttnWorkspace(dev, *sizes)
+    st = _on(dev, load().mmq_attn_decode, cache._ref, q.data_ptr(), ldq, new.data_ptr() if new is not None else None,
+             out.data_ptr(), q_heads, n, dim ** -0.5 if scale is None else scale, int(accumulate),
+             workspace.work.data_ptr(), workspace.counters.data_ptr())
+    if st != 0:
+        raise MMQError("mmq_attn_decode", st)
+    return out
+
+
+def evict_workspace(cache: KVCache, budget: int) -> torch.Tensor:
+    """Scratch of kv_evict (int32)."""
+    n = ctypes.c_int64(0)
+    _check("mmq_evict_sizes", load().mmq_evict_sizes(cache._ref, budget, ctypes.byref(n)))
+    return torch.empty(max(1, n.value), dtype=torch.int32, device=cache.device)
+
+
+def kv_evict(cache: KVCache, budget: int, keep_from: torch.Tensor, weight_out: torch.Tensor, pos_out: torch.Tensor,
+             workspace: torch.Tensor | None = None):
+    """Cut every sequence down to `budget` entries per head: those with pos >= keep_from
+    [seqs] (int32) first, then those of the largest weight.  k and v are compacted in place;
+    the new bookkeeping goes to weight_out and pos_out (shaped as cache.weight), for
+    cache.set_bookkeeping.  Lower cache.lens to the budget (clamp_) once every layer that
+    shares it is done."""
+    dev = cache.device
+    if cache.weight is None or cache.pos is None:
+        raise ValueError("the cache keeps no weights or positions")
+    _need_cuda(keep_from, weight_out, pos_out)
+    shape = tuple(cache.weight.shape)
+    _need(keep_from, "keep_from", torch.int32, (cache.seqs,), dev)
+    _need(weight_out, "weight_out", torch.float32, shape, dev)
+    _need(pos_out, "pos_out", torch.int32, shape, dev)
+    if weight_out.data_ptr() == cache.weight.data_ptr() or pos_out.data_ptr() == cache.pos.data_ptr():
+        raise ValueError("weight_out and pos_out must not be the cache's own")
+    need = cache._work.get(budget)
+    if need is None:
+        n = ctypes.c_int64(0)
+        _check("mmq_evict_sizes", load().mmq_evict_sizes(cache._ref, budget, ctypes.byref(n)))
+        need = cache._work[budget] = n.value
+    if workspace is None:
+        workspace = torch.empty(max(1, need), dtype=torch.int32, device=dev)
+    elif workspace.dtype != torch.int32 or not workspace.is_contiguous() or workspace.device != dev or workspace.numel() < need:
+        raise ValueError("workspace must be evict_workspace(cache, budget) or larger")
+    st = _on(dev, load().mmq_kv_evict, cache._ref, budget, keep_from.data_ptr(), weight_out.data_ptr(), pos_out.data_ptr(),
+             workspace.data_ptr())
+    if st != 0:
+        raise MMQError("mmq_kv_evict", st)
+
+
+def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.Tensor, uniform: torch.Tensor,
+                count: torch.Tensor | None = None, out=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Verify drafted tokens against the target's probabilities (speculative sampling).
+
+    target [seqs][n+1][vocab] and draft [seqs][n][vocab] probabilities (f32, f16 or bf16,
+    alike; draft None: the drafts were not sampled), tokens int32 [seqs][n], uniform f32
+    [seqs][n+1] in [0, 1), count int32 [seqs] drafts there (None: n).  Returns (tokens
+    int32 [seqs][n+1]: the accepted ones, one drawn, then -1; accepted int32 [seqs]);
+    `out` may supply the two."""
+    _need_cuda(target, draft, tokens, uniform, count)
+    if target.dtype not in PROB_DTYPES or target.dim() != 3 or not target.is_contiguous() or target.shape[1] < 2:
+        raise ValueError("target must be contiguous float [seqs][drafts+1][vocab]")
+    dev = target.device
+    B, n1, V = target.shape
+    if draft is not None:
+        _need(draft, "draft", target.dtype, (B, n1 - 1, V), dev)
+    _need(tokens, "tokens", torch.int32, (B, n1 - 1), dev)
+    _need(uniform, "uniform", torch.float32, (B, n1), dev)
+    if count is not None:
+        _need(count, "count", torch.int32, (B,), dev)
+    if out is None:
+        res, acc = torch.empty((B, n1), dtype=torch.int32, device=dev), torch.empty((B,), dtype=torch.int32, device=dev)
+    else:
+        res, acc = out
+        _need(res, "out[0]", torch.int32, (B, n1), dev)
+        _need(acc, "out[1]", torch.int32, (B,), dev)
+    st = _on(dev, load().mmq_spec_verify, target.data_ptr(), draft.data_ptr() if draft is not None else None,
+             PROB_DTYPES[target.dtype], tokens.data_ptr(), uniform.data_ptr(),
+             count.data_ptr() if count is not None else None, res.data_ptr(), acc.data_ptr(), B, n1 - 1, V)
+    if st != 0:
+        raise MMQError("mmq_spec_verify", st)
+    return res, acc
 
 
 def check_status(device: torch.device | None = None):
