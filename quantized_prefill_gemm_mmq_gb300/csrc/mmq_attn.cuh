@@ -116,6 +116,14 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
     }
 }
 
+// 2^x to two ulp; 0 for -inf and where the result is below the normal range
+__device__ __forceinline__ float pow2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // quad = the four lanes that hold one row
 __device__ __forceinline__ float quad_max(float x)
 {
@@ -151,11 +159,12 @@ struct AttnParams {
     float *scores;           // [seqs*heads][rows][cap] in powers of two (weights only)
     float *lse;              // [seqs*heads][rows]
     int64_t cap;
+    FastDiv page_div;
 };
 
-// A place in the row of tiles: sequence, (head, row part), tile.
+// A place in the row of tiles: sequence, head, part of the rows, tile.
 struct AttnCursor {
-    int b, hr, tile, tiles, len;
+    int b, h, rt, tile, tiles, len;
 };
 
 template <int TILE>
@@ -165,12 +174,14 @@ __device__ __forceinline__ int attn_tiles(int len)
 }
 
 template <int TILE>
-__device__ __forceinline__ void attn_advance(const AttnParams &p, AttnCursor &u, int hrs)
+__device__ __forceinline__ void attn_advance(const AttnParams &p, AttnCursor &u)
 {
     if (++u.tile < u.tiles) return;
     u.tile = 0;
-    if (++u.hr < hrs) return;
-    u.hr = 0;
+    if (++u.rt < p.row_tiles) return;
+    u.rt = 0;
+    if (++u.h < p.c.heads) return;
+    u.h = 0;
     if (++u.b >= p.c.seqs) return;
     u.len = cache_len(p.c, u.b, KID_ATTN);
     u.tiles = attn_tiles<TILE>(u.len);
@@ -187,7 +198,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
     constexpr int CPR = DP / 8, RPP = THREADS / CPR, PASSES = TILE / RPP;   // 16-byte copies per row, rows per pass
 
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int2 s_row[2][TILE];
+    __shared__ ulonglong2 s_row[2][TILE];
     __shared__ long long s_scan[4];
     __shared__ long long s_base;
     __shared__ int s_b, s_last;
@@ -244,47 +255,50 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
     cur.tiles = attn_tiles<TILE>(cur.len);
     {
         const long long rem = u0 - s_base;
-        cur.hr = (int)(rem / cur.tiles);
-        cur.tile = (int)(rem - (long long)cur.hr * cur.tiles);
+        const int hr = (int)(rem / cur.tiles);
+        cur.tile = (int)(rem - (long long)hr * cur.tiles);
+        cur.h = hr / p.row_tiles;
+        cur.rt = hr - cur.h * p.row_tiles;
     }
     long long seg_base = u0 - cur.tile;                       // first tile of the segment at `cur`
-    AttnCursor ld = cur, inf = cur;                           // next tile to copy, next to look up
+    AttnCursor inf = cur;                                     // next tile to look up
 
-    // page and offset of entry `tid` of the tile at `inf`
+    // addresses of K and V of entry `tid` of the tile at `inf`; 0 if there is none
     auto look_up = [&](bool there) {
-        int2 r = make_int2(-1, 0);
-        if (there && tid < TILE) {
+        ulonglong2 r = make_ulonglong2(0, 0);
+        if (there) {
             const int slot = inf.tile * TILE + tid;
-            if (slot < inf.len) {
-                const int col = slot / p.c.page_size;
-                r = make_int2(cache_page(p.c, inf.b, col, KID_ATTN), slot - col * p.c.page_size);
+            if (tid < TILE && slot < inf.len) {
+                const int col = p.page_div.of(slot), off = slot - col * p.c.page_size;
+                const int64_t pg = cache_page(p.c, inf.b, col, KID_ATTN);
+                if (pg >= 0)
+                    r = make_ulonglong2(
+                        (unsigned long long)(static_cast<const T *>(p.c.k) + pg * p.c.k_page + inf.h * p.c.k_head + off * p.c.k_slot),
+                        (unsigned long long)(static_cast<const T *>(p.c.v) + pg * p.c.v_page + inf.h * p.c.v_head + off * p.c.v_slot));
             }
+            attn_advance<TILE>(p, inf);
         }
-        if (there) attn_advance<TILE>(p, inf, hrs);
         return r;
     };
+    // this thread's 16-byte piece of rows cr, cr + RPP, ...
     const int cc = tid % CPR, cr = tid / CPR;
+    const bool piece = cc * 8 < p.c.dim;
     auto copy = [&](int stage, int buf) {
-        const int h = ld.hr / p.row_tiles;
-        const T *kh = static_cast<const T *>(p.c.k) + h * p.c.k_head + cc * 8;
-        const T *vh = static_cast<const T *>(p.c.v) + h * p.c.v_head + cc * 8;
-        const uint32_t base = ring + stage * 2 * S::kHalf;
+        const uint32_t base = ring + stage * 2 * S::kHalf + cr * (DP * 2);
+        const ulonglong2 *rows = s_row[buf] + cr;
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
-            const int row = cr + i * RPP;
-            const int2 w = s_row[buf][row];
-            const bool there = w.x >= 0 && cc * 8 < p.c.dim;
-            const int64_t pg = there ? w.x : 0, of = there ? w.y : 0;
-            const uint32_t dst = base + row * (DP * 2) + ((cc ^ (row & 7)) << 4);
-            cp16(dst, there ? kh + pg * p.c.k_page + of * p.c.k_slot : p.c.k, there);
-            cp16(dst + S::kHalf, there ? vh + pg * p.c.v_page + of * p.c.v_slot : p.c.v, there);
+            const ulonglong2 w = rows[i * RPP];
+            const bool there = w.x != 0 && piece;
+            const uint32_t dst = base + i * RPP * (DP * 2) + ((cc ^ ((cr + i * RPP) & 7)) << 4);
+            cp16(dst, there ? reinterpret_cast<const uint8_t *>(w.x) + cc * 16 : p.c.k, there);
+            cp16(dst + S::kHalf, there ? reinterpret_cast<const uint8_t *>(w.y) + cc * 16 : p.c.v, there);
         }
-        attn_advance<TILE>(p, ld, hrs);
     };
 
     const long long n_units = u1 - u0;
     {
-        const int2 r0 = look_up(true), r1 = look_up(n_units > 1);
+        const ulonglong2 r0 = look_up(true), r1 = look_up(n_units > 1);
         if (tid < TILE) {
             s_row[0][tid] = r0;
             s_row[1][tid] = r1;
@@ -294,7 +308,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
         cp_commit();
         if (n_units > 1) copy(1, 1);
         cp_commit();
-        const int2 r2 = look_up(n_units > 2);
+        const ulonglong2 r2 = look_up(n_units > 2);
         __syncthreads();
         if (tid < TILE) s_row[0][tid] = r2;
     }
@@ -310,9 +324,9 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
         const int stage = (int)(i % STAGES);
         if (i + 2 < n_units) copy((int)((i + 2) % STAGES), (int)(i & 1));
         cp_commit();
-        const int2 nrow = look_up(i + 3 < n_units);
+        const ulonglong2 nrow = look_up(i + 3 < n_units);
 
-        const int h = cur.hr / p.row_tiles, rt = cur.hr - h * p.row_tiles;
+        const int h = cur.h, rt = cur.rt;
         if (fresh) {                              // a new segment: its query rows
             fresh = false;
             n_new = new_count(p.new_len, cur.b, p.new_tokens, KID_ATTN);
@@ -393,13 +407,13 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
             for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt][0], s[nt][1]));
             mx = quad_max(mx);
             const float ref = mx == -INFINITY ? 0.f : mx;     // nothing seen yet: every power is 0
-            const float alpha = exp2f(m - ref);
+            const float alpha = pow2(m - ref);
             m = mx;
             l *= alpha;
             uint32_t ph[NT / 2][4], pl[BF ? NT / 2 : 1][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float p0 = exp2f(s[nt][0] - ref) * 0x1p15f, p1 = exp2f(s[nt][1] - ref) * 0x1p15f;
+                const float p0 = pow2(s[nt][0] - ref) * 0x1p15f, p1 = pow2(s[nt][1] - ref) * 0x1p15f;
                 l += p0 + p1;
                 uint32_t lo;
                 split<T>(p0, p1, ph[nt / 2][(nt & 1) * 2], ph[nt / 2][(nt & 1) * 2 + 1], lo);
@@ -457,7 +471,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
         if (tid < TILE) s_row[(i + 1) & 1][tid] = nrow;
 
         const AttnCursor was = cur;
-        attn_advance<TILE>(p, cur, hrs);
+        attn_advance<TILE>(p, cur);
         if (i + 1 < n_units && cur.tile != 0) continue;
 
         // ---- the segment's end (or this CTA's): join the warps that split its entries
@@ -481,7 +495,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
                 __syncthreads();
                 if (tg < half) {
                     const float m2 = ml[g][0], l2 = ml[g][1], mm = fmaxf(m, m2), ref = mm == -INFINITY ? 0.f : mm;
-                    const float w1 = exp2f(m - ref), w2 = exp2f(m2 - ref);
+                    const float w1 = pow2(m - ref), w2 = pow2(m2 - ref);
                     m = mm;
                     l = l * w1 + l2 * w2;
 #pragma unroll
@@ -549,7 +563,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
                     for (long long c = c0; c <= c1; ++c) {
                         const long long sl = slot_of(c) * ROWS + r;
                         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(ml_all) + sl);
-                        const float w = exp2f(ml.x - ref);
+                        const float w = pow2(ml.x - ref);
                         tot += ml.y * w;
                         const float *src = p.part + sl * DP + lane;
 #pragma unroll
@@ -581,8 +595,8 @@ __global__ void __launch_bounds__(256) attn_weight_kernel(const AttnParams p)
     const float *s = p.scores + seg * p.rows * p.cap + slot, *lse = p.lse + seg * p.rows;
     float w = 0.f;
 #pragma unroll 4
-    for (int r = 0; r < p.rows; ++r) w += exp2f(__ldg(s + r * p.cap) - __ldg(lse + r));
-    const int col = slot / p.c.page_size, pg = cache_page(p.c, b, col, KID_ATTN);
+    for (int r = 0; r < p.rows; ++r) w += attn::pow2(__ldg(s + r * p.cap) - __ldg(lse + r));
+    const int col = p.page_div.of(slot), pg = cache_page(p.c, b, col, KID_ATTN);
     if (pg < 0) return;
     p.c.weight[((int64_t)pg * p.c.heads + h) * p.c.page_size + (slot - col * p.c.page_size)] += w;
 }
@@ -706,6 +720,7 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     p.lse = p.part + a.part_floats;
     p.cnt = counters;
     p.cap = a.cap;
+    p.page_div = FastDiv(cache->page_size);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     rc = cache->dtype == MMQ_F16 ? launch_attn_dp<__half>(p, a, save, s) : launch_attn_dp<__nv_bfloat16>(p, a, save, s);
     if (rc != MMQ_OK || !save) return rc;

@@ -16,6 +16,20 @@ namespace {
 enum { KID_ROPE = 32, KID_ATTN = 33, KID_EVICT = 34, KID_VERIFY = 35 };
 enum { SITE_LEN = 1, SITE_PAGE = 2, SITE_COUNT = 3, SITE_TOKEN = 4 };
 
+// Division of 0 <= n < 2^31 by a d >= 1 that is fixed for a launch: a high
+// product, an add and a shift (round-up method of Granlund and Montgomery).
+struct FastDiv {
+    uint32_t mul = 0;
+    int shift = 0;
+    FastDiv() = default;
+    explicit FastDiv(int d)
+    {
+        while ((1ll << shift) < d) ++shift;
+        mul = (uint32_t)((((1ull << shift) - (uint32_t)d) << 32) / (uint32_t)d + 1);
+    }
+    __device__ __forceinline__ int of(int n) const { return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift); }
+};
+
 // Checks of a cache descriptor that every call shares.
 inline int check_cache(const mmq_kv_cache *c)
 {
