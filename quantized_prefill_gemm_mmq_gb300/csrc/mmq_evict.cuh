@@ -9,13 +9,16 @@
 // (slots >= budget) and destinations (< budget) do not overlap, so the moves
 // need no order.
 //
-// Two launches.  evict_select_kernel: a cluster of CTAs per (sequence, head)
-// holds the keys in shared memory, finds the budget-th largest by three
-// passes of a radix search (11, 11 and 10 bits; the CTAs' histograms are
-// added through distributed shared memory), counts ties in slot order, and
-// writes the list of moves and the bookkeeping of the entries that stay in
-// place.  evict_move_kernel: 16-byte pieces of K and V, one per thread, and
-// the moved entries' bookkeeping.
+// Two launches.  evict_select_kernel: one CTA (a cluster of them where there
+// are few rows) per sequence and head holds the keys in shared memory, finds
+// the budget-th largest by three passes of a radix search (11, 11 and 10 bits;
+// a cluster adds its histograms through distributed shared memory), counts
+// ties in slot order, and writes the list of moves and the bookkeeping of the
+// entries that stay in place.  Slots are dealt to threads in stripes, so that
+// every pass reads memory side by side; the order of slots is kept by counting
+// per (stripe, warp) with ballots and one scan over those counts.
+// evict_move_kernel: a warp looks up 32 moves at once, one per lane, then
+// copies them one after the other, a 16-byte piece of K or V per lane.
 // Bound by memory: 8 B per entry and head for weight and position, 8 B for
 // each that stays, 8 dim B per move.
 #pragma once
@@ -24,13 +27,16 @@ namespace mmq {
 namespace {
 
 namespace evict {
-constexpr int THREADS = 512;
+constexpr int THREADS = 1024;
 constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int MAX_CLUSTER = 8;
-constexpr int MAX_CHUNK = 32768;       // keys per CTA: 128 KB
+constexpr int MAX_CHUNK = 32768;               // keys per CTA: 128 KB
+constexpr int MAX_STRIPES = MAX_CHUNK / THREADS;
+constexpr int MAX_COLS = 4096;                 // page ids kept in shared memory
+constexpr int BATCH = 4;                       // stripes whose loads a thread has in flight
 constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_BATCH = 4;          // pieces a thread has in flight
+constexpr int MOVE_BATCH = 8;                  // moves a warp has in flight
 }  // namespace evict
 
 struct EvictParams {
@@ -40,7 +46,8 @@ struct EvictParams {
     int32_t *pos_out;
     int32_t *count;         // [seqs*heads] moves
     int32_t *src, *dst;     // [seqs*heads][most] slots
-    int budget, most, chunk_cap;
+    int budget, most, chunk_cap, cols_cap;
+    FastDiv page_div;
 };
 
 // the address of `p` (this CTA's shared memory) in CTA `rank` of the cluster
@@ -81,53 +88,106 @@ __device__ __forceinline__ int block_prefix(int v, int *s, int &total)
     return before + x - v;
 }
 
+// Exclusive prefixes, in the order (stripe, warp), of counts that lane 0 of
+// every warp has put into cnt[stripe*WARPS + warp], in place; returns the sum.
+// One count per thread: stripes*WARPS <= THREADS.
+__device__ __forceinline__ int stripe_prefix(int *cnt, int stripes, int *s)
+{
+    __syncthreads();
+    const int i = threadIdx.x, v = i < stripes * evict::WARPS ? cnt[i] : 0;
+    int total;
+    const int before = block_prefix(v, s, total);
+    if (i < stripes * evict::WARPS) cnt[i] = before;
+    __syncthreads();
+    return total;
+}
+
 __global__ void __launch_bounds__(evict::THREADS) evict_select_kernel(const EvictParams p)
 {
     using namespace evict;
-    extern __shared__ __align__(16) uint32_t keys[];       // [chunk_cap]
-    __shared__ __align__(16) uint32_t hist[2][BINS];
+    extern __shared__ __align__(16) uint32_t keys[];       // [chunk_cap], then the page ids [cols_cap]
+    __shared__ uint32_t hist[2][BINS];
+    __shared__ int s_cnt[2][MAX_STRIPES * WARPS];
     __shared__ int s_scan[WARPS];
     __shared__ uint32_t s_digit, s_above;
     __shared__ uint32_t s_xchg[3];                        // ties, holes, moves of this CTA
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t below = (1u << lane) - 1;
     const int rank = (int)cluster_ctarank(), n_cta = (int)cluster_nctarank();
-    const int row = blockIdx.x / n_cta, b = row / p.c.heads, h = row - b * p.c.heads;
-    const int len = cache_len(p.c, b, KID_EVICT), ps = p.c.page_size;
-    const bool whole = len <= p.budget;                    // nothing to evict
+    const int row = blockIdx.x / n_cta, b = row / p.c.heads, h = row - b * p.c.heads, ps = p.c.page_size;
+    const int len = cache_len(p.c, b, KID_EVICT);
 
     const int chunk = (len + n_cta - 1) / n_cta;
     const int lo = min(len, rank * chunk), n = min(len, lo + chunk) - lo;
+    const int stripes = (n + THREADS - 1) / THREADS;
     const int keep_from = __ldg(p.keep_from + b);
 
-    // entry address of slot, or -1
-    auto entry = [&](int slot) -> int64_t {
-        const int col = slot / ps, pg = cache_page(p.c, b, col, KID_EVICT);
+    // page ids of this CTA's slots
+    int32_t *pages = reinterpret_cast<int32_t *>(keys + p.chunk_cap);
+    const int col0 = p.page_div.of(lo), cols = n > 0 ? p.page_div.of(lo + n - 1) - col0 + 1 : 0;
+    for (int i = tid; i < min(cols, p.cols_cap); i += THREADS) pages[i] = cache_page(p.c, b, col0 + i, KID_EVICT);
+    __syncthreads();
+    // entry index of slot lo + i in the bookkeeping, or -1
+    auto entry = [&](int i) -> int64_t {
+        const int slot = lo + i, col = p.page_div.of(slot);
+        const int pg = col - col0 < p.cols_cap ? pages[col - col0] : cache_page(p.c, b, col, KID_EVICT);
         return pg < 0 ? -1 : ((int64_t)pg * p.c.heads + h) * ps + (slot - col * ps);
     };
-
-    if (whole) {
-        for (int i = tid; i < n; i += THREADS) {
-            const int64_t e = entry(lo + i);
-            if (e < 0) continue;
-            p.weight_out[e] = __ldg(p.c.weight + e);
-            p.pos_out[e] = __ldg(p.c.pos + e);
+    // weight and position of the slots below `end` for which stay(i), to the new bookkeeping
+    auto keep_in_place = [&](int end, auto stay) {
+        for (int i0 = tid; i0 < end; i0 += THREADS * BATCH) {
+            int64_t e[BATCH];
+            float w[BATCH];
+            int32_t x[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int i = i0 + k * THREADS;
+                e[k] = i < end && stay(i) ? entry(i) : -1;
+                if (e[k] >= 0) {
+                    w[k] = __ldg(p.c.weight + e[k]);
+                    x[k] = __ldg(p.c.pos + e[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+                if (e[k] >= 0) {
+                    p.weight_out[e[k]] = w[k];
+                    p.pos_out[e[k]] = x[k];
+                }
         }
+    };
+
+    if (len <= p.budget) {                                 // nothing to evict: the whole cluster leaves
+        keep_in_place(n, [](int) { return true; });
         if (rank == 0 && tid == 0) p.count[row] = 0;
-        return;                                            // the whole cluster leaves
+        return;
     }
 
-    for (int i = tid; i < n; i += THREADS) {
-        const int64_t e = entry(lo + i);
-        uint32_t key = 0;
-        if (e >= 0) {
-            if (__ldg(p.c.pos + e) >= keep_from) {
-                key = 0xffffffffu;
-            } else {
-                const uint32_t u = __float_as_uint(__ldg(p.c.weight + e) + 0.f);    // -0 becomes 0
-                key = u ^ (u & 0x80000000u ? 0xffffffffu : 0x80000000u);
+    for (int i0 = tid; i0 < n; i0 += THREADS * BATCH) {
+        float w[BATCH];
+        int32_t x[BATCH];
+        bool there[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = i0 + k * THREADS;
+            const int64_t e = i < n ? entry(i) : -1;
+            there[k] = e >= 0;
+            if (there[k]) {
+                w[k] = __ldg(p.c.weight + e);
+                x[k] = __ldg(p.c.pos + e);
             }
         }
-        keys[i] = key;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = i0 + k * THREADS;
+            if (i >= n) continue;
+            uint32_t key = 0;
+            if (there[k]) {
+                const uint32_t u = __float_as_uint(w[k] + 0.f);                     // -0 becomes 0
+                key = x[k] >= keep_from ? 0xffffffffu : u ^ (u & 0x80000000u ? 0xffffffffu : 0x80000000u);
+            }
+            keys[i] = key;
+        }
     }
 
     // ---- the budget-th largest key, from its highest bits down
@@ -142,128 +202,140 @@ __global__ void __launch_bounds__(evict::THREADS) evict_select_kernel(const Evic
             const uint32_t k = keys[i];
             if ((k & mask) == prefix) atomicAdd(&hs[(k >> shift) & ((1u << bits) - 1)], 1u);
         }
-        cluster_sync_all();
-        // four bins per thread, from the highest down
-        const int top = BINS - 4 - 4 * tid;
-        uint32_t c[4] = {0, 0, 0, 0};
-        for (int r = 0; r < n_cta; ++r) {
-            const uint32_t a = cluster_map(smem_u32(hs + top), r);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) c[k] += cluster_ld(a + 4 * k);
+        // two bins per thread, from the highest down
+        const int top = BINS - 2 - 2 * tid;
+        uint32_t c0 = 0, c1 = 0;
+        if (n_cta == 1) {
+            __syncthreads();
+            c0 = hs[top];
+            c1 = hs[top + 1];
+        } else {
+            cluster_sync_all();
+            for (int r = 0; r < n_cta; ++r) {
+                const uint32_t a = cluster_map(smem_u32(hs + top), r);
+                c0 += cluster_ld(a);
+                c1 += cluster_ld(a + 4);
+            }
         }
         int total;
-        const int mine = (int)(c[0] + c[1] + c[2] + c[3]);
-        int before = block_prefix(mine, s_scan, total);
-        if (before < want && want <= before + mine) {
-#pragma unroll
-            for (int k = 3; k >= 0; --k) {
-                if (before < want && want <= before + (int)c[k]) {
-                    s_digit = (uint32_t)(top + k);
-                    s_above = (uint32_t)before;
-                }
-                before += (int)c[k];
-            }
+        const int before = block_prefix((int)(c0 + c1), s_scan, total);
+        if (before < want && want <= before + (int)c1) {
+            s_digit = (uint32_t)(top + 1);
+            s_above = (uint32_t)before;
+        } else if (before + (int)c1 < want && want <= before + (int)(c0 + c1)) {
+            s_digit = (uint32_t)top;
+            s_above = (uint32_t)before + c1;
         }
         __syncthreads();
         prefix |= s_digit << shift;
         mask |= ((1u << bits) - 1) << shift;
         want -= (int)s_above;
     }
-    // `want` of the keys equal to `prefix` stay, those in the lowest slots
-    const int per = (n + THREADS - 1) / THREADS | 1;       // odd: a thread's run of keys meets every bank
-    const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    int ties = 0, all;
-    for (int i = i0; i < i1; ++i) ties += keys[i] == prefix;
-    int tie_at = block_prefix(ties, s_scan, all);
-    if (tid == 0) s_xchg[0] = (uint32_t)all;
-    cluster_sync_all();
-    for (int r = 0; r < rank; ++r) tie_at += (int)cluster_ld(cluster_map(smem_u32(&s_xchg[0]), r));
-    int holes = 0, moves = 0;
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t k = keys[i];
-        const bool keep = k > prefix || (k == prefix && tie_at++ < want);
-        keys[i] = keep;
-        if (lo + i < p.budget)
-            holes += !keep;
-        else
-            moves += keep;
-    }
-    int hole_at = block_prefix(holes, s_scan, all);
-    if (tid == 0) s_xchg[1] = (uint32_t)all;
-    int move_at = block_prefix(moves, s_scan, all);
-    if (tid == 0) s_xchg[2] = (uint32_t)all;
-    cluster_sync_all();
-    int n_holes = 0;
-    for (int r = 0; r < n_cta; ++r) {
-        const int x = (int)cluster_ld(cluster_map(smem_u32(&s_xchg[1]), r));
-        const int y = (int)cluster_ld(cluster_map(smem_u32(&s_xchg[2]), r));
-        n_holes += x;
-        if (r < rank) {
-            hole_at += x;
-            move_at += y;
+    // sum over the CTAs before this one of what each has put into s_xchg[k], and over all
+    auto exchange = [&](int k, int mine, int &all) {
+        if (n_cta == 1) {
+            all = mine;
+            return 0;
         }
+        if (tid == 0) s_xchg[k] = (uint32_t)mine;
+        cluster_sync_all();
+        int before = 0;
+        all = 0;
+        for (int r = 0; r < n_cta; ++r) {
+            const int x = (int)cluster_ld(cluster_map(smem_u32(&s_xchg[k]), r));
+            if (r < rank) before += x;
+            all += x;
+        }
+        return before;
+    };
+
+    // ---- `want` of the keys equal to `prefix` stay, those in the lowest slots
+    int all;
+    for (int s = 0; s < stripes; ++s) {
+        const int i = s * THREADS + tid;
+        const unsigned tie = __ballot_sync(0xffffffffu, i < n && keys[i] == prefix);
+        if (lane == 0) s_cnt[0][s * WARPS + warp] = __popc(tie);
     }
-    if (rank == 0 && tid == 0) p.count[row] = n_holes;
+    const int ties = stripe_prefix(s_cnt[0], stripes, s_scan);
+    const int ties_before = exchange(0, ties, all);
+    // holes (given up below the budget) and moves (kept past it), 16 bits each: at most 32768 per CTA
+    const int edge = p.budget - lo;                        // slots i < edge lie below the budget
+    for (int s = 0; s < stripes; ++s) {
+        const int i = s * THREADS + tid;
+        const uint32_t k = i < n ? keys[i] : 0u;
+        const bool tie = i < n && k == prefix;
+        const unsigned m = __ballot_sync(0xffffffffu, tie);
+        const bool keep = i < n && (k > prefix || (tie && ties_before + s_cnt[0][s * WARPS + warp] + __popc(m & below) < want));
+        const unsigned out = __ballot_sync(0xffffffffu, i < n && i < edge && !keep);
+        const unsigned in = __ballot_sync(0xffffffffu, i >= edge && keep);
+        if (i < n) keys[i] = keep;
+        if (lane == 0) s_cnt[1][s * WARPS + warp] = __popc(out) | __popc(in) << 16;
+    }
+    const uint32_t both = (uint32_t)stripe_prefix(s_cnt[1], stripes, s_scan);
+    int holes, moves;
+    const int hole_at = exchange(1, (int)(both & 0xffffu), holes), move_at = exchange(2, (int)(both >> 16), moves);
+    if (rank == 0 && tid == 0) p.count[row] = holes;
     int32_t *src = p.src + (int64_t)row * p.most, *dst = p.dst + (int64_t)row * p.most;
-    for (int i = i0; i < i1; ++i) {
-        const bool keep = keys[i] != 0;
-        if (lo + i < p.budget) {
-            if (!keep) dst[hole_at++] = lo + i;
-        } else if (keep) {
-            src[move_at++] = lo + i;
-        }
+    for (int s = 0; s < stripes; ++s) {
+        const int i = s * THREADS + tid;
+        const bool keep = i < n && keys[i] != 0;
+        const unsigned out = __ballot_sync(0xffffffffu, i < n && i < edge && !keep);
+        const unsigned in = __ballot_sync(0xffffffffu, i >= edge && keep);
+        const uint32_t at = (uint32_t)s_cnt[1][s * WARPS + warp];
+        if (out >> lane & 1) dst[hole_at + (int)(at & 0xffffu) + __popc(out & below)] = lo + i;
+        if (in >> lane & 1) src[move_at + (int)(at >> 16) + __popc(in & below)] = lo + i;
     }
-    __syncthreads();
-    // bookkeeping of what stays in place
-    const int end = min(n, p.budget - lo);
-    for (int i = tid; i < end; i += THREADS) {
-        if (!keys[i]) continue;
-        const int64_t e = entry(lo + i);
-        if (e < 0) continue;
-        p.weight_out[e] = __ldg(p.c.weight + e);
-        p.pos_out[e] = __ldg(p.c.pos + e);
-    }
-    cluster_sync_all();                                    // no CTA leaves while another may read its shared memory
+    keep_in_place(min(n, edge), [&](int i) { return keys[i] != 0; });
+    if (n_cta > 1) cluster_sync_all();                     // no CTA leaves while another may read its shared memory
 }
 
 __global__ void __launch_bounds__(evict::MOVE_THREADS) evict_move_kernel(const EvictParams p)
 {
     using namespace evict;
     const int row = blockIdx.y, b = row / p.c.heads, h = row - b * p.c.heads, ps = p.c.page_size;
-    const int cpr = p.c.dim / 8, per_move = 2 * cpr;        // 16-byte pieces of an entry's k and v
-    const int64_t pieces = (int64_t)p.count[row] * per_move;
+    const int lane = threadIdx.x & 31;
+    const int cpr = p.c.dim / 8, n = p.count[row];          // 16-byte pieces of a row; moves
     const int32_t *src = p.src + (int64_t)row * p.most, *dst = p.dst + (int64_t)row * p.most;
-    for (int64_t at = (int64_t)blockIdx.x * MOVE_THREADS * MOVE_BATCH; at < pieces;
-         at += (int64_t)gridDim.x * MOVE_THREADS * MOVE_BATCH) {
-        uint4 w[MOVE_BATCH];
-        uint4 *to[MOVE_BATCH];
-#pragma unroll
-        for (int i = 0; i < MOVE_BATCH; ++i) {
-            const int64_t x = at + i * MOVE_THREADS + threadIdx.x;
-            to[i] = nullptr;
-            if (x >= pieces) continue;
-            const int mv = (int)(x / per_move), pc = (int)(x - (int64_t)mv * per_move);
-            const int s = src[mv], d = dst[mv];
-            const int sc = s / ps, dc = d / ps;
-            const int64_t sp = cache_page(p.c, b, sc, KID_EVICT), dp = cache_page(p.c, b, dc, KID_EVICT);
-            if (sp < 0 || dp < 0) continue;
-            const int so = s - sc * ps, dof = d - dc * ps;
-            const bool is_v = pc >= cpr;
-            uint8_t *base = static_cast<uint8_t *>(is_v ? p.c.v : p.c.k);
-            const int64_t P = is_v ? p.c.v_page : p.c.k_page, H = is_v ? p.c.v_head : p.c.k_head,
-                          S = is_v ? p.c.v_slot : p.c.k_slot;
-            const int64_t off = (int64_t)h * H + (is_v ? pc - cpr : pc) * 8;
-            w[i] = *reinterpret_cast<const uint4 *>(base + 2 * (sp * P + so * S + off));
-            to[i] = reinterpret_cast<uint4 *>(base + 2 * (dp * P + dof * S + off));
-            if (pc == 0) {
-                const int64_t e0 = (sp * p.c.heads + h) * ps + so, e1 = (dp * p.c.heads + h) * ps + dof;
+    const int warps = gridDim.x * (MOVE_THREADS / 32);
+    for (int m0 = 32 * (blockIdx.x * (MOVE_THREADS / 32) + (threadIdx.x >> 5)); m0 < n; m0 += 32 * warps) {
+        // this lane's move: page and offset of where it comes from and goes to
+        int sp = -1, so = 0, dp = -1, dof = 0;
+        if (m0 + lane < n) {
+            const int s = src[m0 + lane], d = dst[m0 + lane];
+            const int sc = p.page_div.of(s), dc = p.page_div.of(d);
+            so = s - sc * ps;
+            dof = d - dc * ps;
+            sp = cache_page(p.c, b, sc, KID_EVICT);
+            dp = cache_page(p.c, b, dc, KID_EVICT);
+            if (sp < 0 || dp < 0) {
+                sp = -1;
+            } else {
+                const int64_t e0 = ((int64_t)sp * p.c.heads + h) * ps + so, e1 = ((int64_t)dp * p.c.heads + h) * ps + dof;
                 p.weight_out[e1] = __ldg(p.c.weight + e0);
                 p.pos_out[e1] = __ldg(p.c.pos + e0);
             }
         }
+        const int here = min(32, n - m0);
+        for (int pc = lane; pc - lane < 2 * cpr; pc += 32) { // pieces of k, then of v (one round up to dim 128)
+            const bool is_v = pc >= cpr, mine = pc < 2 * cpr;
+            uint8_t *base = static_cast<uint8_t *>(is_v ? p.c.v : p.c.k) +
+                            2 * ((int64_t)h * (is_v ? p.c.v_head : p.c.k_head) + (is_v ? pc - cpr : pc) * 8);
+            const int64_t P = 2 * (is_v ? p.c.v_page : p.c.k_page), S = 2 * (is_v ? p.c.v_slot : p.c.k_slot);
+            for (int i0 = 0; i0 < here; i0 += MOVE_BATCH) {
+                uint4 w[MOVE_BATCH];
 #pragma unroll
-        for (int i = 0; i < MOVE_BATCH; ++i)
-            if (to[i]) *to[i] = w[i];
+                for (int k = 0; k < MOVE_BATCH; ++k) {
+                    const int64_t pg = __shfl_sync(0xffffffffu, sp, (i0 + k) & 31), of = __shfl_sync(0xffffffffu, so, (i0 + k) & 31);
+                    if (mine && i0 + k < here && pg >= 0) w[k] = *reinterpret_cast<const uint4 *>(base + pg * P + of * S);
+                }
+#pragma unroll
+                for (int k = 0; k < MOVE_BATCH; ++k) {
+                    const int ok = __shfl_sync(0xffffffffu, sp, (i0 + k) & 31);
+                    const int64_t pg = __shfl_sync(0xffffffffu, dp, (i0 + k) & 31), of = __shfl_sync(0xffffffffu, dof, (i0 + k) & 31);
+                    if (mine && i0 + k < here && ok >= 0) *reinterpret_cast<uint4 *>(base + pg * P + of * S) = w[k];
+                }
+            }
+        }
     }
 }
 
@@ -318,12 +390,15 @@ extern "C" int mmq_kv_evict(const mmq_kv_cache *cache, int budget, const int32_t
     p.dst = p.src + rows * p.most;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
+    p.page_div = FastDiv(cache->page_size);
+
     const int cap = cache->cols * cache->page_size;
-    // CTAs per row: one up to 4096 keys (eight per thread), then twice as many
-    // for twice the keys, up to a cluster of eight
+    // CTAs per row: as many as the keys need (32768 each), and, while rows are
+    // fewer than SMs, more as long as each still has 4096 keys (four per thread)
     int cl = 1;
-    while (cl < evict::MAX_CLUSTER && cap > 4096 * cl) cl *= 2;
+    while (cl < evict::MAX_CLUSTER && (cap > evict::MAX_CHUNK * cl || (rows * cl * 2 <= sm_count() && cap > 8192 * cl))) cl *= 2;
     p.chunk_cap = (cap + cl - 1) / cl;
+    p.cols_cap = cache->cols < evict::MAX_COLS ? cache->cols : evict::MAX_COLS;
     static bool attr_done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -332,14 +407,14 @@ extern "C" int mmq_kv_evict(const mmq_kv_cache *cache, int budget, const int32_t
     }
     if (!attr_done[dev]) {
         if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 evict::MAX_CHUNK * 4) != cudaSuccess)
+                                 (evict::MAX_CHUNK + evict::MAX_COLS) * 4) != cudaSuccess)
             return launch_status();
         attr_done[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * cl));
     cfg.blockDim = dim3(evict::THREADS);
-    cfg.dynamicSmemBytes = (size_t)p.chunk_cap * 4;
+    cfg.dynamicSmemBytes = (size_t)(p.chunk_cap + p.cols_cap) * 4;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -349,11 +424,10 @@ extern "C" int mmq_kv_evict(const mmq_kv_cache *cache, int budget, const int32_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return launch_status();
-    // rows in y; enough blocks along a row's moves to fill the device about four times
-    const int64_t pieces = (int64_t)p.most * (cache->dim / 4);
-    const int64_t per_block = evict::MOVE_THREADS * evict::MOVE_BATCH;
-    int64_t x = (pieces + per_block - 1) / per_block;
-    const int64_t enough = ((int64_t)sm_count() * 32 + rows - 1) / rows;
+    // rows in y; along a row, a warp per 32 moves, up to some eight blocks per SM
+    const int64_t per_block = evict::MOVE_THREADS;
+    int64_t x = (p.most + per_block - 1) / per_block;
+    const int64_t enough = ((int64_t)sm_count() * 8 + rows - 1) / rows;
     if (x > enough) x = enough;
     evict_move_kernel<<<dim3((unsigned)x, (unsigned)rows), evict::MOVE_THREADS, 0, s>>>(p);
     return launch_status();

@@ -18,7 +18,7 @@ namespace mmq {
 namespace {
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_BATCH = 4;        // heads whose loads a thread has in flight
+constexpr int ROPE_BATCH = 3;        // heads whose loads a thread has in flight
 
 struct RopeParams {
     mmq_kv_cache c;
@@ -30,6 +30,7 @@ struct RopeParams {
     float magnitude;
     int rot, interleaved, q_heads, new_tokens;
     int heads_per_block;             // of the row's q_heads + 2*heads
+    FastDiv page_div;
 };
 
 // P pairs per thread: 4 where rot and dim are multiples of 8 (16-byte
@@ -63,20 +64,42 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopePar
             record_error(MMQ_ERR_INDEX, KID_ROPE, SITE_LEN);
             store = false;
         } else {
-            const int col = slot / p.c.page_size;
+            const int col = p.page_div.of(slot);
             off = slot - col * p.c.page_size;
             const int pg = cache_page(p.c, b, col, KID_ROPE);
             store = pg >= 0;
             page = pg;
         }
     }
+    // The row's heads: q, k, v.  A batch of heads is loaded while the one before it is rotated and stored.
+    const int x = __ldg(p.pos + row);
+    float a[ROPE_BATCH][P], c[ROPE_BATCH][P];
+    auto load = [&](int hb) {
+#pragma unroll
+        for (int i = 0; i < ROPE_BATCH; ++i) {
+            const int h = hb + i * lanes;
+            if (h >= h1 || !live) continue;
+            const bool is_v = h >= p.q_heads + p.c.heads;
+            const float *src = h < p.q_heads ? p.q + row * p.ldq + (int64_t)h * D
+                               : !is_v       ? p.k + row * p.ldk + (int64_t)(h - p.q_heads) * D
+                                             : p.v + row * p.ldv + (int64_t)(h - p.q_heads - p.c.heads) * D;
+            const int s0 = is_v ? u * 2 * P : e0, s1 = is_v ? u * 2 * P + P : e1;
+            if constexpr (P == 4) {
+                *reinterpret_cast<float4 *>(a[i]) = *reinterpret_cast<const float4 *>(src + s0);
+                *reinterpret_cast<float4 *>(c[i]) = *reinterpret_cast<const float4 *>(src + s1);
+            } else {
+                a[i][0] = src[s0];
+                c[i][0] = src[s1];
+            }
+        }
+    };
+    load(h0 + hl);
     float cs[P], sn[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         cs[i] = 1.f;
         sn[i] = 0.f;
     }
-    const int x = __ldg(p.pos + row);
     if (rotated && live) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -88,67 +111,50 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopePar
     }
 
     for (int hb = h0 + hl; hb < h1; hb += lanes * ROPE_BATCH) {
-        float a[ROPE_BATCH][P], c[ROPE_BATCH][P];
+        float y0[ROPE_BATCH][P], y1[ROPE_BATCH][P];
 #pragma unroll
         for (int i = 0; i < ROPE_BATCH; ++i) {
-            const int h = hb + i * lanes;
-            if (h >= h1 || !live) continue;
-            const float *src = h < p.q_heads ? p.q + row * p.ldq + (int64_t)h * D
-                               : h < p.q_heads + p.c.heads ? p.k + row * p.ldk + (int64_t)(h - p.q_heads) * D
-                                                           : p.v + row * p.ldv + (int64_t)(h - p.q_heads - p.c.heads) * D;
-            // values are not rotated: their halves lie side by side
-            const int s0 = h < p.q_heads + p.c.heads ? e0 : u * 2 * P, s1 = h < p.q_heads + p.c.heads ? e1 : u * 2 * P + P;
-            if constexpr (P == 4) {
-                if (rotated && p.interleaved && h < p.q_heads + p.c.heads) {
-                    const float4 lo = *reinterpret_cast<const float4 *>(src + s0), hi = *reinterpret_cast<const float4 *>(src + s1);
-                    a[i][0] = lo.x, c[i][0] = lo.y, a[i][1] = lo.z, c[i][1] = lo.w;
-                    a[i][2] = hi.x, c[i][2] = hi.y, a[i][3] = hi.z, c[i][3] = hi.w;
-                } else {
-                    *reinterpret_cast<float4 *>(a[i]) = *reinterpret_cast<const float4 *>(src + s0);
-                    *reinterpret_cast<float4 *>(c[i]) = *reinterpret_cast<const float4 *>(src + s1);
+            const bool turn = rotated && hb + i * lanes < p.q_heads + p.c.heads;
+            if (P == 4 && turn && p.interleaved) {              // pairs side by side: (a0 a1) (a2 a3) (c0 c1) (c2 c3)
+                const float z[8] = {a[i][0], a[i][1], a[i][2 % P], a[i][3 % P], c[i][0], c[i][1 % P], c[i][2 % P], c[i][3 % P]};
+                float w[8];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    w[(2 * j) & 7] = z[(2 * j) & 7] * cs[j] - z[(2 * j + 1) & 7] * sn[j];
+                    w[(2 * j + 1) & 7] = z[(2 * j) & 7] * sn[j] + z[(2 * j + 1) & 7] * cs[j];
+                }
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    y0[i][j] = w[j];
+                    y1[i][j] = w[(P + j) & 7];
                 }
             } else {
-                a[i][0] = src[s0];
-                c[i][0] = src[s1];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    y0[i][j] = turn ? a[i][j] * cs[j] - c[i][j] * sn[j] : a[i][j];
+                    y1[i][j] = turn ? a[i][j] * sn[j] + c[i][j] * cs[j] : c[i][j];
+                }
             }
         }
+        load(hb + lanes * ROPE_BATCH);
 #pragma unroll
         for (int i = 0; i < ROPE_BATCH; ++i) {
             const int h = hb + i * lanes;
             if (h >= h1) continue;
             const bool is_v = h >= p.q_heads + p.c.heads;
             const int d0 = is_v ? u * 2 * P : e0, d1 = is_v ? u * 2 * P + P : e1;
-            float y0[P], y1[P];
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                if (!live) {
-                    y0[j] = y1[j] = 0.f;
-                } else if (rotated && !is_v) {
-                    y0[j] = a[i][j] * cs[j] - c[i][j] * sn[j];
-                    y1[j] = a[i][j] * sn[j] + c[i][j] * cs[j];
-                } else {
-                    y0[j] = a[i][j];
-                    y1[j] = c[i][j];
-                }
-            }
-            if constexpr (P == 4) {
-                if (rotated && p.interleaved && !is_v) {     // back side by side
-                    const float z0[4] = {y0[0], y1[0], y0[1], y1[1]}, z1[4] = {y0[2], y1[2], y0[3], y1[3]};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        y0[j] = z0[j];
-                        y1[j] = z1[j];
-                    }
-                }
-            }
             if (h < p.q_heads) {
                 float *dst = p.q_out + row * p.ldo + (int64_t)h * D;
+                if (!live) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) y0[i][j] = y1[i][j] = 0.f;
+                }
                 if constexpr (P == 4) {
-                    *reinterpret_cast<float4 *>(dst + d0) = make_float4(y0[0], y0[1], y0[2], y0[3]);
-                    *reinterpret_cast<float4 *>(dst + d1) = make_float4(y1[0], y1[1], y1[2], y1[3]);
+                    *reinterpret_cast<float4 *>(dst + d0) = *reinterpret_cast<float4 *>(y0[i]);
+                    *reinterpret_cast<float4 *>(dst + d1) = *reinterpret_cast<float4 *>(y1[i]);
                 } else {
-                    dst[d0] = y0[0];
-                    dst[d1] = y1[0];
+                    dst[d0] = y0[i][0];
+                    dst[d1] = y1[i][0];
                 }
                 continue;
             }
@@ -157,8 +163,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopePar
             T *dst = is_v ? static_cast<T *>(p.c.v) + page * p.c.v_page + kh * p.c.v_head + off * p.c.v_slot
                           : static_cast<T *>(p.c.k) + page * p.c.k_page + kh * p.c.k_head + off * p.c.k_slot;
             if constexpr (P == 4) {
-                const uint2 w0 = make_uint2(pack2<T>(y0[0], y0[1]), pack2<T>(y0[2], y0[3]));
-                const uint2 w1 = make_uint2(pack2<T>(y1[0], y1[1]), pack2<T>(y1[2], y1[3]));
+                const uint2 w0 = make_uint2(pack2<T>(y0[i][0], y0[i][1]), pack2<T>(y0[i][2], y0[i][3]));
+                const uint2 w1 = make_uint2(pack2<T>(y1[i][0], y1[i][1]), pack2<T>(y1[i][2], y1[i][3]));
                 if (d1 == d0 + 4) {
                     *reinterpret_cast<uint4 *>(dst + d0) = make_uint4(w0.x, w0.y, w1.x, w1.y);
                 } else {
@@ -166,8 +172,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopePar
                     *reinterpret_cast<uint2 *>(dst + d1) = w1;
                 }
             } else {
-                dst[d0] = to_cache<T>(y0[0]);
-                dst[d1] = to_cache<T>(y1[0]);
+                dst[d0] = to_cache<T>(y0[i][0]);
+                dst[d1] = to_cache<T>(y1[i][0]);
             }
             if (!is_v && u == 0) {
                 const int64_t e = (page * p.c.heads + kh) * p.c.page_size + off;
@@ -226,7 +232,7 @@ extern "C" int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, i
         return MMQ_ERR_ALIGN;
     if ((rc = check_arch()) != MMQ_OK) return rc;
     RopeParams p = {*cache, freq, q, k, v, pos, new_len, q_out, ldq, ldk, ldv, ldo, magnitude, rot, interleaved ? 1 : 0,
-                    q_heads, new_tokens, 0};
+                    q_heads, new_tokens, 0, FastDiv(cache->page_size)};
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return cache->dtype == MMQ_F16 ? launch_rope<__half>(p, sm_count(), st)
                                    : launch_rope<__nv_bfloat16>(p, sm_count(), st);

@@ -8,24 +8,30 @@
 // draw what a serial sum would.
 //
 // A cluster per sequence.  Every CTA finds the first rejection by itself (a
-// few loads), sums its part of the row in spans of SPAN values, one span per
-// warp at a time, and keeps the spans' sums; the CTAs exchange their totals
-// through distributed shared memory; the one whose part the threshold falls
-// into reads the one span again and finds the value.  So the row is read
-// once.  Bound by memory: one or two rows of the vocabulary per sequence.
+// few loads) and adds up its part of the row in spans of 32 x 16 bytes, two
+// spans per warp in flight, keeping the spans' sums; the CTAs exchange their
+// totals through distributed shared memory; the one whose part the threshold
+// falls into reads the one span again and finds the value.  So the row is read
+// once.  A row of an odd vocabulary does not start on 16 bytes: a lane then
+// takes its 16 bytes out of two aligned ones.
+// Bound by memory: one or two rows of the vocabulary per sequence.
 #pragma once
 
 namespace mmq {
 namespace {
 
 namespace ver {
-constexpr int THREADS = 512;
+constexpr int THREADS = 256;
+constexpr int PER_SM = 4;               // CTAs resident per SM: 64 registers a thread
 constexpr int WARPS = THREADS / 32;
-constexpr int PER = 8;                  // values per lane and span
-constexpr int SPAN = 32 * PER;
+constexpr int BATCH = 2;                // spans a warp has in flight
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX_VOCAB = 1 << 20;
 constexpr int MAX_DRAFTS = 64;
+template <typename T>
+constexpr int kPer = 16 / sizeof(T);    // values per lane and span
+template <typename T>
+constexpr int kSpan = 32 * kPer<T>;
 }  // namespace ver
 
 struct VerifyParams {
@@ -55,10 +61,59 @@ __device__ __forceinline__ unsigned long long cluster_ld64(uint32_t a)
     return v;
 }
 
+// 16 bytes of a row from value j on (any alignment of the row): zeros past hi
 template <typename T>
-__global__ void __launch_bounds__(ver::THREADS) spec_verify_kernel(const VerifyParams p)
+__device__ __forceinline__ uint4 ver_load(const T *row, int j, int hi)
+{
+    constexpr int N = ver::kPer<T>;
+    const T *at = row + j;
+    const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 15u);
+    // aligned words around the 16 bytes must lie in the row themselves: the ends are read value by value
+    if (j + N > hi || (odd != 0 && (j < N || j + 2 * N > hi))) {
+        T v[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            v[k] = T(0.f);
+            if (j + k < hi) v[k] = at[k];
+        }
+        return *reinterpret_cast<const uint4 *>(v);
+    }
+    const uint4 *a = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)15);
+    const uint4 x = __ldg(a);
+    if (odd == 0) return x;
+    const uint4 y = __ldg(a + 1);
+    // bytes odd .. odd+15 of the 32: by two words, by one, by bits
+    uint32_t w[7] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z}, last = y.w;
+    if (odd & 8) {
+        w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = last;
+    }
+    if (odd & 4) {
+        w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+    }
+    const uint32_t s = (odd & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
+}
+
+// The sum of the w_j of 16 bytes' worth of values; each of them in w.
+template <typename T>
+__device__ __forceinline__ unsigned long long ver_sum(const uint4 &pv, const uint4 &qv, unsigned long long (&w)[ver::kPer<T>])
+{
+    const T *p = reinterpret_cast<const T *>(&pv), *q = reinterpret_cast<const T *>(&qv);
+    unsigned long long s = 0;
+#pragma unroll
+    for (int k = 0; k < ver::kPer<T>; ++k) {
+        w[k] = ver_fixed(ver_f(p[k]), ver_f(q[k]));
+        s += w[k];
+    }
+    return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(ver::THREADS, ver::PER_SM) spec_verify_kernel(const VerifyParams p)
 {
     using namespace ver;
+    constexpr int PER = kPer<T>, SPAN = kSpan<T>;
     extern __shared__ __align__(16) unsigned long long s_span[];    // [spans]
     __shared__ unsigned long long s_total[2], s_warp[WARPS];
     __shared__ int s_first, s_bad;
@@ -106,24 +161,40 @@ __global__ void __launch_bounds__(ver::THREADS) spec_verify_kernel(const VerifyP
     const int whole_tok = rejected && !draft ? __ldg(p.tokens + (int64_t)b * p.drafts + a) : -1;
     const int lo = min(p.vocab, rank * p.spans * SPAN), hi = min(p.vocab, lo + p.spans * SPAN);
 
+    // the values of a lane: the row less what is taken off it
+    auto load_q = [&](int j, bool plain) {
+        if (plain || (!qr && (whole_tok < j || whole_tok >= j + PER))) return make_uint4(0u, 0u, 0u, 0u);
+        if (qr) return ver_load(qr, j, hi);
+        T v[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[k] = T(j + k == whole_tok ? 1.f : 0.f);
+        return *reinterpret_cast<const uint4 *>(v);
+    };
+
     unsigned long long r = 0, before = 0, mine = 0;
     for (int tries = 0; tries < 2; ++tries) {
         const bool plain = tries == 1;                      // the target alone, if nothing of the difference is left
         unsigned long long sum = 0;
-        for (int sp = warp; sp < p.spans; sp += WARPS) {
-            unsigned long long w = 0;
+        for (int sp = warp; sp < p.spans; sp += WARPS * BATCH) {
+            uint4 pv[BATCH], qv[BATCH];
 #pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                const int jx = lo + sp * SPAN + k * 32 + lane;
-                if (jx < hi) {
-                    const float q = plain ? 0.f : qr ? ver_f(qr[jx]) : jx == whole_tok ? 1.f : 0.f;
-                    w += ver_fixed(ver_f(pr[jx]), q);
+            for (int k = 0; k < BATCH; ++k) {
+                const int j = lo + (sp + k * WARPS) * SPAN + lane * PER;
+                pv[k] = qv[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (sp + k * WARPS < p.spans && j < hi) {
+                    pv[k] = ver_load(pr, j, hi);
+                    qv[k] = load_q(j, plain);
                 }
             }
 #pragma unroll
-            for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-            if (lane == 0) s_span[sp] = w;
-            sum += w;
+            for (int k = 0; k < BATCH; ++k) {
+                unsigned long long each[PER];
+                unsigned long long w = ver_sum<T>(pv[k], qv[k], each);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+                if (lane == 0 && sp + k * WARPS < p.spans) s_span[sp + k * WARPS] = w;
+                sum += w;
+            }
         }
         if (lane == 0) s_warp[warp] = sum;
         __syncthreads();
@@ -165,17 +236,14 @@ __global__ void __launch_bounds__(ver::THREADS) spec_verify_kernel(const VerifyP
                     }
                     at += __shfl_sync(0xffffffffu, c, 31);
                 }
-                unsigned long long w[PER], x = 0;
-#pragma unroll
-                for (int k = 0; k < PER; ++k) {             // eight neighbours per lane
-                    const int jx = lo + sp * SPAN + lane * PER + k;
-                    w[k] = 0;
-                    if (jx < hi) {
-                        const float q = plain ? 0.f : qr ? ver_f(qr[jx]) : jx == whole_tok ? 1.f : 0.f;
-                        w[k] = ver_fixed(ver_f(pr[jx]), q);
-                    }
-                    x += w[k];
+                unsigned long long w[PER];
+                const int j = lo + sp * SPAN + lane * PER;
+                uint4 pv = make_uint4(0u, 0u, 0u, 0u), qv = pv;
+                if (j < hi) {
+                    pv = ver_load(pr, j, hi);
+                    qv = load_q(j, plain);
                 }
+                const unsigned long long x = ver_sum<T>(pv, qv, w);
                 unsigned long long c = x;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -191,7 +259,7 @@ __global__ void __launch_bounds__(ver::THREADS) spec_verify_kernel(const VerifyP
                         unsigned long long upto = at;
 #pragma unroll
                         for (int i = 0; i <= k; ++i) upto += w[i];
-                        if (upto > r) tok = lo + sp * SPAN + lane * PER + k;
+                        if (upto > r) tok = j + k;
                     }
                     p.out[(int64_t)b * (p.drafts + 1) + a] = tok;
                 }
@@ -213,15 +281,16 @@ __global__ void __launch_bounds__(ver::THREADS) spec_verify_kernel(const VerifyP
 template <typename T>
 int launch_verify(VerifyParams &p, int seqs, cudaStream_t stream)
 {
-    // CTAs per sequence: one per 4096 values, up to a cluster of eight
+    // CTAs per sequence: one per 16 KB of a row, up to a cluster of eight
+    constexpr int each = 16384 / (int)sizeof(T);
     int cl = 1;
-    while (cl < ver::MAX_CLUSTER && p.vocab > 4096 * cl) cl *= 2;
+    while (cl < ver::MAX_CLUSTER && p.vocab > each * cl) cl *= 2;
     const int per = (p.vocab + cl - 1) / cl;
-    p.spans = (per + ver::SPAN - 1) / ver::SPAN;
+    p.spans = (per + ver::kSpan<T> - 1) / ver::kSpan<T>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(seqs * cl));
     cfg.blockDim = dim3(ver::THREADS);
-    cfg.dynamicSmemBytes = (size_t)p.spans * 8;            // at most 4 KB
+    cfg.dynamicSmemBytes = (size_t)p.spans * 8;            // at most 8 KB
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
