@@ -9,16 +9,15 @@
 // (slots >= budget) and destinations (< budget) do not overlap, so the moves
 // need no order.
 //
-// Two launches.  evict_select_kernel: one CTA (a cluster of them where there
-// are few rows) per sequence and head holds the keys in shared memory, finds
-// the budget-th largest by three passes of a radix search (11, 11 and 10 bits;
-// a cluster adds its histograms through distributed shared memory), counts
-// ties in slot order, and writes the list of moves and the bookkeeping of the
-// entries that stay in place.  Slots are dealt to threads in stripes, so that
-// every pass reads memory side by side; the order of slots is kept by counting
-// per (stripe, warp) with ballots and one scan over those counts.
-// evict_move_kernel: a warp looks up 32 moves at once, one per lane, then
-// copies them one after the other, a 16-byte piece of K or V per lane.
+// One launch: one CTA (a cluster of them where there are few rows) per
+// sequence and head holds the keys in shared memory, finds the budget-th
+// largest by three passes of a radix search (11, 11 and 10 bits; a cluster adds
+// its histograms through distributed shared memory), counts ties in slot
+// order, lists the moves, and makes them.  Slots are dealt to threads in
+// stripes, so that every pass reads memory side by side; the order of slots is
+// kept by counting per (stripe, warp) with ballots and one scan over those
+// counts.  For the moves a warp looks up 32 at once, one per lane, then copies
+// them one after the other, a 16-byte piece of K or V per lane.
 // Bound by memory: 8 B per entry and head for weight and position, 8 B for
 // each that stays, 8 dim B per move.
 #pragma once
@@ -27,15 +26,15 @@ namespace mmq {
 namespace {
 
 namespace evict {
-constexpr int THREADS = 1024;
+constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
+constexpr int PER_SM = 2;
 constexpr int BINS = 2048;
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX_CHUNK = 32768;               // keys per CTA: 128 KB
-constexpr int MAX_STRIPES = MAX_CHUNK / THREADS;
+constexpr int STRIPES = MAX_CHUNK / THREADS;   // at most
 constexpr int MAX_COLS = 4096;                 // page ids kept in shared memory
-constexpr int BATCH = 4;                       // stripes whose loads a thread has in flight
-constexpr int MOVE_THREADS = 256;
+constexpr int BATCH = 8;                       // stripes whose loads a thread has in flight
 constexpr int MOVE_BATCH = 8;                  // moves a warp has in flight
 }  // namespace evict
 
@@ -44,7 +43,6 @@ struct EvictParams {
     const int32_t *keep_from;
     float *weight_out;
     int32_t *pos_out;
-    int32_t *count;         // [seqs*heads] moves
     int32_t *src, *dst;     // [seqs*heads][most] slots
     int budget, most, chunk_cap, cols_cap;
     FastDiv page_div;
@@ -90,24 +88,33 @@ __device__ __forceinline__ int block_prefix(int v, int *s, int &total)
 
 // Exclusive prefixes, in the order (stripe, warp), of counts that lane 0 of
 // every warp has put into cnt[stripe*WARPS + warp], in place; returns the sum.
-// One count per thread: stripes*WARPS <= THREADS.
 __device__ __forceinline__ int stripe_prefix(int *cnt, int stripes, int *s)
 {
+    constexpr int PER = evict::STRIPES * evict::WARPS / evict::THREADS;
     __syncthreads();
-    const int i = threadIdx.x, v = i < stripes * evict::WARPS ? cnt[i] : 0;
-    int total;
-    const int before = block_prefix(v, s, total);
-    if (i < stripes * evict::WARPS) cnt[i] = before;
+    const int n = stripes * evict::WARPS, i = threadIdx.x * PER;
+    int v[PER], mine = 0, total;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        v[k] = i + k < n ? cnt[i + k] : 0;
+        mine += v[k];
+    }
+    int before = block_prefix(mine, s, total);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (i + k < n) cnt[i + k] = before;
+        before += v[k];
+    }
     __syncthreads();
     return total;
 }
 
-__global__ void __launch_bounds__(evict::THREADS) evict_select_kernel(const EvictParams p)
+__global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(const EvictParams p)
 {
     using namespace evict;
     extern __shared__ __align__(16) uint32_t keys[];       // [chunk_cap], then the page ids [cols_cap]
     __shared__ uint32_t hist[2][BINS];
-    __shared__ int s_cnt[2][MAX_STRIPES * WARPS];
+    __shared__ int s_cnt[2][STRIPES * WARPS];
     __shared__ int s_scan[WARPS];
     __shared__ uint32_t s_digit, s_above;
     __shared__ uint32_t s_xchg[3];                        // ties, holes, moves of this CTA
@@ -133,48 +140,21 @@ __global__ void __launch_bounds__(evict::THREADS) evict_select_kernel(const Evic
         const int pg = col - col0 < p.cols_cap ? pages[col - col0] : cache_page(p.c, b, col, KID_EVICT);
         return pg < 0 ? -1 : ((int64_t)pg * p.c.heads + h) * ps + (slot - col * ps);
     };
-    // weight and position of the slots below `end` for which stay(i), to the new bookkeeping
-    auto keep_in_place = [&](int end, auto stay) {
-        for (int i0 = tid; i0 < end; i0 += THREADS * BATCH) {
-            int64_t e[BATCH];
-            float w[BATCH];
-            int32_t x[BATCH];
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int i = i0 + k * THREADS;
-                e[k] = i < end && stay(i) ? entry(i) : -1;
-                if (e[k] >= 0) {
-                    w[k] = __ldg(p.c.weight + e[k]);
-                    x[k] = __ldg(p.c.pos + e[k]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k)
-                if (e[k] >= 0) {
-                    p.weight_out[e[k]] = w[k];
-                    p.pos_out[e[k]] = x[k];
-                }
-        }
-    };
-
-    if (len <= p.budget) {                                 // nothing to evict: the whole cluster leaves
-        keep_in_place(n, [](int) { return true; });
-        if (rank == 0 && tid == 0) p.count[row] = 0;
-        return;
-    }
-
+    const int edge = p.budget - lo;                        // slots i < edge lie below the budget
+    const bool whole = len <= p.budget;                    // nothing to evict
+    // Keys; and the bookkeeping of the slots below the budget as if they all
+    // stayed: a moved entry overwrites it later.
     for (int i0 = tid; i0 < n; i0 += THREADS * BATCH) {
+        int64_t e[BATCH];
         float w[BATCH];
         int32_t x[BATCH];
-        bool there[BATCH];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             const int i = i0 + k * THREADS;
-            const int64_t e = i < n ? entry(i) : -1;
-            there[k] = e >= 0;
-            if (there[k]) {
-                w[k] = __ldg(p.c.weight + e);
-                x[k] = __ldg(p.c.pos + e);
+            e[k] = i < n ? entry(i) : -1;
+            if (e[k] >= 0) {
+                w[k] = __ldg(p.c.weight + e[k]);
+                x[k] = __ldg(p.c.pos + e[k]);
             }
         }
 #pragma unroll
@@ -182,13 +162,18 @@ __global__ void __launch_bounds__(evict::THREADS) evict_select_kernel(const Evic
             const int i = i0 + k * THREADS;
             if (i >= n) continue;
             uint32_t key = 0;
-            if (there[k]) {
+            if (e[k] >= 0) {
                 const uint32_t u = __float_as_uint(w[k] + 0.f);                     // -0 becomes 0
                 key = x[k] >= keep_from ? 0xffffffffu : u ^ (u & 0x80000000u ? 0xffffffffu : 0x80000000u);
+                if (whole || i < edge) {
+                    p.weight_out[e[k]] = w[k];
+                    p.pos_out[e[k]] = x[k];
+                }
             }
-            keys[i] = key;
+            if (!whole) keys[i] = key;
         }
     }
+    if (whole) return;                                     // the whole cluster leaves
 
     // ---- the budget-th largest key, from its highest bits down
     uint32_t prefix = 0, mask = 0;
@@ -202,29 +187,37 @@ __global__ void __launch_bounds__(evict::THREADS) evict_select_kernel(const Evic
             const uint32_t k = keys[i];
             if ((k & mask) == prefix) atomicAdd(&hs[(k >> shift) & ((1u << bits) - 1)], 1u);
         }
-        // two bins per thread, from the highest down
-        const int top = BINS - 2 - 2 * tid;
-        uint32_t c0 = 0, c1 = 0;
+        // a few bins per thread, from the highest down
+        constexpr int PER = BINS / THREADS;
+        const int top = BINS - PER - PER * tid;
+        uint32_t c[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) c[k] = 0;
         if (n_cta == 1) {
             __syncthreads();
-            c0 = hs[top];
-            c1 = hs[top + 1];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) c[k] = hs[top + k];
         } else {
             cluster_sync_all();
             for (int r = 0; r < n_cta; ++r) {
                 const uint32_t a = cluster_map(smem_u32(hs + top), r);
-                c0 += cluster_ld(a);
-                c1 += cluster_ld(a + 4);
+#pragma unroll
+                for (int k = 0; k < PER; ++k) c[k] += cluster_ld(a + 4 * k);
             }
         }
-        int total;
-        const int before = block_prefix((int)(c0 + c1), s_scan, total);
-        if (before < want && want <= before + (int)c1) {
-            s_digit = (uint32_t)(top + 1);
-            s_above = (uint32_t)before;
-        } else if (before + (int)c1 < want && want <= before + (int)(c0 + c1)) {
-            s_digit = (uint32_t)top;
-            s_above = (uint32_t)before + c1;
+        int total, mine = 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) mine += (int)c[k];
+        int before = block_prefix(mine, s_scan, total);
+        if (before < want && want <= before + mine) {
+#pragma unroll
+            for (int k = PER - 1; k >= 0; --k) {
+                if (before < want && want <= before + (int)c[k]) {
+                    s_digit = (uint32_t)(top + k);
+                    s_above = (uint32_t)before;
+                }
+                before += (int)c[k];
+            }
         }
         __syncthreads();
         prefix |= s_digit << shift;
@@ -259,7 +252,6 @@ __global__ void __launch_bounds__(evict::THREADS) evict_select_kernel(const Evic
     const int ties = stripe_prefix(s_cnt[0], stripes, s_scan);
     const int ties_before = exchange(0, ties, all);
     // holes (given up below the budget) and moves (kept past it), 16 bits each: at most 32768 per CTA
-    const int edge = p.budget - lo;                        // slots i < edge lie below the budget
     for (int s = 0; s < stripes; ++s) {
         const int i = s * THREADS + tid;
         const uint32_t k = i < n ? keys[i] : 0u;
@@ -274,7 +266,6 @@ __global__ void __launch_bounds__(evict::THREADS) evict_select_kernel(const Evic
     const uint32_t both = (uint32_t)stripe_prefix(s_cnt[1], stripes, s_scan);
     int holes, moves;
     const int hole_at = exchange(1, (int)(both & 0xffffu), holes), move_at = exchange(2, (int)(both >> 16), moves);
-    if (rank == 0 && tid == 0) p.count[row] = holes;
     int32_t *src = p.src + (int64_t)row * p.most, *dst = p.dst + (int64_t)row * p.most;
     for (int s = 0; s < stripes; ++s) {
         const int i = s * THREADS + tid;
@@ -285,23 +276,20 @@ __global__ void __launch_bounds__(evict::THREADS) evict_select_kernel(const Evic
         if (out >> lane & 1) dst[hole_at + (int)(at & 0xffffu) + __popc(out & below)] = lo + i;
         if (in >> lane & 1) src[move_at + (int)(at >> 16) + __popc(in & below)] = lo + i;
     }
-    keep_in_place(min(n, edge), [&](int i) { return keys[i] != 0; });
-    if (n_cta > 1) cluster_sync_all();                     // no CTA leaves while another may read its shared memory
-}
-
-__global__ void __launch_bounds__(evict::MOVE_THREADS) evict_move_kernel(const EvictParams p)
-{
-    using namespace evict;
-    const int row = blockIdx.y, b = row / p.c.heads, h = row - b * p.c.heads, ps = p.c.page_size;
-    const int lane = threadIdx.x & 31;
-    const int cpr = p.c.dim / 8, n = p.count[row];          // 16-byte pieces of a row; moves
-    const int32_t *src = p.src + (int64_t)row * p.most, *dst = p.dst + (int64_t)row * p.most;
-    const int warps = gridDim.x * (MOVE_THREADS / 32);
-    for (int m0 = 32 * (blockIdx.x * (MOVE_THREADS / 32) + (threadIdx.x >> 5)); m0 < n; m0 += 32 * warps) {
+    // ---- the moves, dealt to the cluster's warps evenly, at most 32 at a time (the lists are in global memory: L2)
+    __syncthreads();
+    if (n_cta > 1) {
+        __threadfence();
+        cluster_sync_all();                                // also: no CTA leaves while another may read its shared memory
+    }
+    const int cpr = p.c.dim / 8;                           // 16-byte pieces of a row
+    const int share = min(32, (holes + WARPS * n_cta - 1) / (WARPS * n_cta));
+    for (int m0 = share * (warp * n_cta + rank); m0 < holes; m0 += share * WARPS * n_cta) {
         // this lane's move: page and offset of where it comes from and goes to
         int sp = -1, so = 0, dp = -1, dof = 0;
-        if (m0 + lane < n) {
-            const int s = src[m0 + lane], d = dst[m0 + lane];
+        const int here = min(share, holes - m0);
+        if (lane < here) {
+            const int s = __ldcg(src + m0 + lane), d = __ldcg(dst + m0 + lane);
             const int sc = p.page_div.of(s), dc = p.page_div.of(d);
             so = s - sc * ps;
             dof = d - dc * ps;
@@ -315,7 +303,6 @@ __global__ void __launch_bounds__(evict::MOVE_THREADS) evict_move_kernel(const E
                 p.pos_out[e1] = __ldg(p.c.pos + e0);
             }
         }
-        const int here = min(32, n - m0);
         for (int pc = lane; pc - lane < 2 * cpr; pc += 32) { // pieces of k, then of v (one round up to dim 128)
             const bool is_v = pc >= cpr, mine = pc < 2 * cpr;
             uint8_t *base = static_cast<uint8_t *>(is_v ? p.c.v : p.c.k) +
@@ -354,6 +341,36 @@ inline int evict_most(const mmq_kv_cache &c, int budget)
     return past < 1 ? 1 : past < budget ? past : budget;
 }
 
+inline int launch_evict(const EvictParams &p, int64_t rows, int cl, cudaStream_t s)
+{
+    static bool attr_done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return MMQ_ERR_ARCH;
+    }
+    if (!attr_done[dev]) {
+        if (cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (evict::MAX_CHUNK + evict::MAX_COLS) * 4) != cudaSuccess)
+            return launch_status();
+        attr_done[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * cl));
+    cfg.blockDim = dim3(evict::THREADS);
+    cfg.dynamicSmemBytes = (size_t)(p.chunk_cap + p.cols_cap) * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cl;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, evict_kernel, p) != cudaSuccess) return launch_status();
+    return launch_status();
+}
+
 }  // namespace
 }  // namespace mmq
 
@@ -362,7 +379,7 @@ extern "C" int mmq_evict_sizes(const mmq_kv_cache *cache, int budget, int64_t *w
     const int rc = mmq::evict_check(cache, budget);
     if (rc != MMQ_OK) return rc;
     if (!work_ints) return MMQ_ERR_NULL;
-    *work_ints = (int64_t)cache->seqs * cache->heads * (1 + 2 * (int64_t)mmq::evict_most(*cache, budget));
+    *work_ints = (int64_t)cache->seqs * cache->heads * 2 * (int64_t)mmq::evict_most(*cache, budget);
     return MMQ_OK;
 }
 
@@ -385,50 +402,18 @@ extern "C" int mmq_kv_evict(const mmq_kv_cache *cache, int budget, const int32_t
     p.pos_out = pos_out;
     p.budget = budget;
     p.most = evict_most(*cache, budget);
-    p.count = work;
-    p.src = work + rows;
+    p.src = work;
     p.dst = p.src + rows * p.most;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
     p.page_div = FastDiv(cache->page_size);
 
     const int cap = cache->cols * cache->page_size;
-    // CTAs per row: as many as the keys need (32768 each), and, while rows are
-    // fewer than SMs, more as long as each still has 4096 keys (four per thread)
+    // CTAs per row: as many as the keys need (32768 each), and more while all
+    // are resident and each still has 2048 keys
     int cl = 1;
-    while (cl < evict::MAX_CLUSTER && (cap > evict::MAX_CHUNK * cl || (rows * cl * 2 <= sm_count() && cap > 8192 * cl))) cl *= 2;
+    while (cl < evict::MAX_CLUSTER && (cap > evict::MAX_CHUNK * cl || (rows * cl * 2 <= evict::PER_SM * sm_count() && cap > 4096 * cl))) cl *= 2;
     p.chunk_cap = (cap + cl - 1) / cl;
     p.cols_cap = cache->cols < evict::MAX_COLS ? cache->cols : evict::MAX_COLS;
-    static bool attr_done[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return MMQ_ERR_ARCH;
-    }
-    if (!attr_done[dev]) {
-        if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (evict::MAX_CHUNK + evict::MAX_COLS) * 4) != cudaSuccess)
-            return launch_status();
-        attr_done[dev] = true;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * cl));
-    cfg.blockDim = dim3(evict::THREADS);
-    cfg.dynamicSmemBytes = (size_t)(p.chunk_cap + p.cols_cap) * 4;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cl;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return launch_status();
-    // rows in y; along a row, a warp per 32 moves, up to some eight blocks per SM
-    const int64_t per_block = evict::MOVE_THREADS;
-    int64_t x = (p.most + per_block - 1) / per_block;
-    const int64_t enough = ((int64_t)sm_count() * 8 + rows - 1) / rows;
-    if (x > enough) x = enough;
-    evict_move_kernel<<<dim3((unsigned)x, (unsigned)rows), evict::MOVE_THREADS, 0, s>>>(p);
-    return launch_status();
+    return launch_evict(p, rows, cl, s);
 }

@@ -8,10 +8,10 @@
 // no range reduction is needed and no position is too large.
 //
 // Bound by memory: per row 8 B per q value (read, write) and 6 B per k and v
-// value.  One thread owns the same eight values (four pairs) of several heads,
-// so that it computes its four sines and cosines once for all of them; a
-// block's threads cover whole heads side by side, one block per row and part
-// of its heads.
+// value.  One thread owns the same eight values (four pairs) of several heads;
+// a block's threads cover whole heads side by side, one block per row and part
+// of its heads.  The row's sines and cosines are computed once per block, while
+// the first heads' loads are in flight.
 #pragma once
 
 namespace mmq {
@@ -36,16 +36,15 @@ struct RopeParams {
 // P pairs per thread: 4 where rot and dim are multiples of 8 (16-byte
 // accesses), else 1.
 template <typename T, int P>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopeParams p)
+__global__ void __launch_bounds__(ROPE_THREADS, 4) rope_append_kernel(const RopeParams p)
 {
+    __shared__ __align__(16) float s_cos[128], s_sin[128];
     const int D = p.c.dim, units = D / (2 * P);
     const int u = threadIdx.x % units, hl = threadIdx.x / units, lanes = blockDim.x / units;
     const int row = blockIdx.x, b = row / p.new_tokens, t = row - b * p.new_tokens;
     const int total = p.q_heads + 2 * p.c.heads;
     const int h0 = blockIdx.y * p.heads_per_block;
     const int h1 = min(total, h0 + p.heads_per_block);
-    if (hl >= lanes) return;
-
     const bool rotated = u * 2 * P < p.rot;
     // element offsets of the thread's first and second P values within a head
     int e0 = u * 2 * P, e1 = e0 + P;
@@ -71,7 +70,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopePar
             page = pg;
         }
     }
-    // The row's heads: q, k, v.  A batch of heads is loaded while the one before it is rotated and stored.
+    // The row's heads: q, k, v.  A batch of heads is in flight at a time, the first while the sines are computed.
     const int x = __ldg(p.pos + row);
     float a[ROPE_BATCH][P], c[ROPE_BATCH][P];
     auto load = [&](int hb) {
@@ -94,67 +93,59 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopePar
         }
     };
     load(h0 + hl);
+    for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) {
+        const uint64_t turns = (uint64_t)(int64_t)x * (uint64_t)__ldg(p.freq + i);
+        float sine, cosine;
+        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sine, &cosine);
+        s_cos[i] = cosine * p.magnitude;
+        s_sin[i] = sine * p.magnitude;
+    }
+    __syncthreads();
+    if (hl >= lanes) return;
     float cs[P], sn[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        cs[i] = 1.f;
-        sn[i] = 0.f;
-    }
-    if (rotated && live) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const uint64_t turns = (uint64_t)(int64_t)x * (uint64_t)__ldg(p.freq + u * P + i);
-            sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn[i], &cs[i]);
-            sn[i] *= p.magnitude;
-            cs[i] *= p.magnitude;
-        }
+        cs[i] = rotated ? s_cos[u * P + i] : 1.f;
+        sn[i] = rotated ? s_sin[u * P + i] : 0.f;
     }
 
     for (int hb = h0 + hl; hb < h1; hb += lanes * ROPE_BATCH) {
-        float y0[ROPE_BATCH][P], y1[ROPE_BATCH][P];
-#pragma unroll
-        for (int i = 0; i < ROPE_BATCH; ++i) {
-            const bool turn = rotated && hb + i * lanes < p.q_heads + p.c.heads;
-            if (P == 4 && turn && p.interleaved) {              // pairs side by side: (a0 a1) (a2 a3) (c0 c1) (c2 c3)
-                const float z[8] = {a[i][0], a[i][1], a[i][2 % P], a[i][3 % P], c[i][0], c[i][1 % P], c[i][2 % P], c[i][3 % P]};
-                float w[8];
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    w[(2 * j) & 7] = z[(2 * j) & 7] * cs[j] - z[(2 * j + 1) & 7] * sn[j];
-                    w[(2 * j + 1) & 7] = z[(2 * j) & 7] * sn[j] + z[(2 * j + 1) & 7] * cs[j];
-                }
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    y0[i][j] = w[j];
-                    y1[i][j] = w[(P + j) & 7];
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    y0[i][j] = turn ? a[i][j] * cs[j] - c[i][j] * sn[j] : a[i][j];
-                    y1[i][j] = turn ? a[i][j] * sn[j] + c[i][j] * cs[j] : c[i][j];
-                }
-            }
-        }
-        load(hb + lanes * ROPE_BATCH);
+        if (hb != h0 + hl) load(hb);
 #pragma unroll
         for (int i = 0; i < ROPE_BATCH; ++i) {
             const int h = hb + i * lanes;
             if (h >= h1) continue;
-            const bool is_v = h >= p.q_heads + p.c.heads;
+            const bool is_v = h >= p.q_heads + p.c.heads, turn = rotated && !is_v;
             const int d0 = is_v ? u * 2 * P : e0, d1 = is_v ? u * 2 * P + P : e1;
+            float y0[P], y1[P];
+            if (P == 4 && turn && p.interleaved) {              // pairs side by side: (a0 a1) (a2 a3) (c0 c1) (c2 c3)
+#pragma unroll
+                for (int j = 0; j < P; j += 2) {
+                    const int n = (j + 1) % P, s = j / 2, w = (P / 2 + j / 2) % P;
+                    y0[j] = a[i][j] * cs[s] - a[i][n] * sn[s];
+                    y0[n] = a[i][j] * sn[s] + a[i][n] * cs[s];
+                    y1[j] = c[i][j] * cs[w] - c[i][n] * sn[w];
+                    y1[n] = c[i][j] * sn[w] + c[i][n] * cs[w];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    y0[j] = turn ? a[i][j] * cs[j] - c[i][j] * sn[j] : a[i][j];
+                    y1[j] = turn ? a[i][j] * sn[j] + c[i][j] * cs[j] : c[i][j];
+                }
+            }
             if (h < p.q_heads) {
                 float *dst = p.q_out + row * p.ldo + (int64_t)h * D;
                 if (!live) {
 #pragma unroll
-                    for (int j = 0; j < P; ++j) y0[i][j] = y1[i][j] = 0.f;
+                    for (int j = 0; j < P; ++j) y0[j] = y1[j] = 0.f;
                 }
                 if constexpr (P == 4) {
-                    *reinterpret_cast<float4 *>(dst + d0) = *reinterpret_cast<float4 *>(y0[i]);
-                    *reinterpret_cast<float4 *>(dst + d1) = *reinterpret_cast<float4 *>(y1[i]);
+                    *reinterpret_cast<float4 *>(dst + d0) = *reinterpret_cast<float4 *>(y0);
+                    *reinterpret_cast<float4 *>(dst + d1) = *reinterpret_cast<float4 *>(y1);
                 } else {
-                    dst[d0] = y0[i][0];
-                    dst[d1] = y1[i][0];
+                    dst[d0] = y0[0];
+                    dst[d1] = y1[0];
                 }
                 continue;
             }
@@ -163,8 +154,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopePar
             T *dst = is_v ? static_cast<T *>(p.c.v) + page * p.c.v_page + kh * p.c.v_head + off * p.c.v_slot
                           : static_cast<T *>(p.c.k) + page * p.c.k_page + kh * p.c.k_head + off * p.c.k_slot;
             if constexpr (P == 4) {
-                const uint2 w0 = make_uint2(pack2<T>(y0[i][0], y0[i][1]), pack2<T>(y0[i][2], y0[i][3]));
-                const uint2 w1 = make_uint2(pack2<T>(y1[i][0], y1[i][1]), pack2<T>(y1[i][2], y1[i][3]));
+                const uint2 w0 = make_uint2(pack2<T>(y0[0], y0[1]), pack2<T>(y0[2], y0[3]));
+                const uint2 w1 = make_uint2(pack2<T>(y1[0], y1[1]), pack2<T>(y1[2], y1[3]));
                 if (d1 == d0 + 4) {
                     *reinterpret_cast<uint4 *>(dst + d0) = make_uint4(w0.x, w0.y, w1.x, w1.y);
                 } else {
@@ -172,8 +163,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const RopePar
                     *reinterpret_cast<uint2 *>(dst + d1) = w1;
                 }
             } else {
-                dst[d0] = to_cache<T>(y0[i][0]);
-                dst[d1] = to_cache<T>(y1[i][0]);
+                dst[d0] = to_cache<T>(y0[0]);
+                dst[d1] = to_cache<T>(y1[0]);
             }
             if (!is_v && u == 0) {
                 const int64_t e = (page * p.c.heads + kh) * p.c.page_size + off;
@@ -195,7 +186,7 @@ int launch_rope(RopeParams &p, int sms, cudaStream_t stream)
     // One block walks all heads of a row when there are rows enough to fill the
     // device; with few rows, a row's heads are spread over blocks down to one
     // pass of the block's lanes each.
-    const int64_t want = (int64_t)sms * 8;
+    const int64_t want = (int64_t)sms * 4;                // resident blocks
     int64_t parts = (want + rows - 1) / rows;
     const int most = (total + lanes - 1) / lanes;
     if (parts > most) parts = most;
