@@ -50,9 +50,10 @@ template <int DP>
 struct Shape {
     static constexpr int kTile = DP == 64 ? 128 : 64;                 // entries per tile
     static constexpr int kHalf = kTile * DP * 2;                      // bytes of K (or V) per stage
-    static constexpr int kMerge = 2 * 8 * DP * 4;                     // two warps' sums
-    static constexpr int kSmem = STAGES * 2 * kHalf + kMerge;
+    static constexpr int kSmem = STAGES * 2 * kHalf;
     static constexpr int kPerSm = DP <= 128 ? 2 : 1;
+    static constexpr int kPad = DP + 8;                               // floats per row of a warp's sums in shared memory
+    static_assert(4 * 8 * kPad * 4 <= 2 * kHalf, "four warps' sums fit in one stage");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there)
@@ -136,6 +137,11 @@ __device__ __forceinline__ float quad_sum(float x)
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
+// 1 / sum, 0 for a row that saw nothing; a NaN stays one
+__device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : sum; }
+// log2 of a row's sum of powers, so that pow2(score - it) is its weight
+__device__ __forceinline__ float log_sum(float m, float sum) { return sum > 0.f ? m + log2f(sum) - P_EXP : INFINITY; }
+
 // whether one of two values has all exponent bits set
 template <typename T>
 __device__ __forceinline__ bool not_finite2(uint32_t u)
@@ -157,7 +163,7 @@ struct AttnParams {
     float *part;             // [2*grid][8*UG][DP] sums, then [2*grid][8*UG][2] (max, sum)
     int32_t *cnt;            // [seqs*heads*row_tiles]
     float *scores;           // [seqs*heads][rows][cap] in powers of two (weights only)
-    float *lse;              // [seqs*heads][rows]
+    float *lse;              // [seqs*heads][rows] (weights only, else NULL)
     int64_t cap;
     FastDiv page_div;
 };
@@ -187,7 +193,7 @@ __device__ __forceinline__ void attn_advance(const AttnParams &p, AttnCursor &u)
     u.tiles = attn_tiles<TILE>(u.len);
 }
 
-template <int DP, typename T, int UG, bool SAVE>
+template <int DP, typename T, int UG>
 __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_kernel(const AttnParams p)
 {
     using namespace attn;
@@ -199,11 +205,9 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
 
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ ulonglong2 s_row[2][TILE];
-    __shared__ long long s_scan[4];
-    __shared__ long long s_base;
-    __shared__ int s_b, s_last;
-    __shared__ float s_ml[2][8][2];
-    float *s_merge = reinterpret_cast<float *>(smem + STAGES * 2 * S::kHalf);
+    __shared__ int s_last;
+    __shared__ float2 s_ml[4][8];              // (max, sum) of every warp's rows
+    __shared__ float2 s_row_ml[ROWS];          // of the joined rows; the joining CTA: (max, 1 / sum)
     const uint32_t ring = smem_u32(smem);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -211,56 +215,42 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
     const int g = lane >> 2, j = lane & 3;
     const int hrs = p.c.heads * p.row_tiles;
 
-    // ---- this CTA's tiles [u0, u1) of all W
-    long long W, G, u0, u1;
-    {
-        const int ipt = (p.c.seqs + THREADS - 1) / THREADS;
-        const int b0 = min(p.c.seqs, tid * ipt), b1 = min(p.c.seqs, b0 + ipt);
-        long long sum = 0;
-        for (int b = b0; b < b1; ++b) sum += attn_tiles<TILE>(cache_len(p.c, b, KID_ATTN));
-        long long pre = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, pre, o);
-            if (lane >= o) pre += v;
-        }
-        if (lane == 31) s_scan[warp] = pre;
-        __syncthreads();
-        W = 0;
-        for (int w = 0; w < 4; ++w) {
-            if (w < warp) pre += s_scan[w];
-            W += s_scan[w];
-        }
-        W *= hrs;
-        G = W < gridDim.x ? W : gridDim.x;                    // CTAs with work: none between two of them is idle
-        if (blockIdx.x >= G) return;
-        u0 = W * blockIdx.x / G;
-        u1 = W * (blockIdx.x + 1) / G;
-        long long at = (pre - sum) * hrs;
-        if (at <= u0 && u0 < pre * hrs) {
-            int b = b0;
-            for (;; ++b) {
-                const long long n = (long long)attn_tiles<TILE>(cache_len(p.c, b, KID_ATTN)) * hrs;
-                if (u0 < at + n) break;
-                at += n;
-            }
-            s_b = b;
-            s_base = at;
-        }
-        __syncthreads();
-    }
+    // ---- this CTA's tiles [u0, u1) of all W: every warp for itself, 32 sequences at a time
+    int W = 0;
+    for (int b = lane; b < p.c.seqs; b += 32) W += attn_tiles<TILE>(cache_len(p.c, b, KID_ATTN));
+    W = __reduce_add_sync(0xffffffffu, W) * hrs;
+    const int G = min(W, (int)gridDim.x);                     // CTAs with work: none between two of them is idle
+    if ((int)blockIdx.x >= G) return;
+    const int u0 = (int)((long long)W * blockIdx.x / G), n_units = (int)((long long)W * (blockIdx.x + 1) / G) - u0;
     AttnCursor cur;
-    cur.b = s_b;
-    cur.len = cache_len(p.c, cur.b, KID_ATTN);
-    cur.tiles = attn_tiles<TILE>(cur.len);
     {
-        const long long rem = u0 - s_base;
-        const int hr = (int)(rem / cur.tiles);
-        cur.tile = (int)(rem - (long long)hr * cur.tiles);
+        int at = 0;                                           // first tile of sequence b
+        for (int b0 = 0;; b0 += 32) {
+            const int len = b0 + lane < p.c.seqs ? cache_len(p.c, b0 + lane, KID_ATTN) : 0;
+            const int tiles = b0 + lane < p.c.seqs ? attn_tiles<TILE>(len) : 0;
+            int upto = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, at + upto * hrs > u0);
+            if (past) {
+                const int f = __ffs(past) - 1;
+                cur.b = b0 + f;
+                cur.len = __shfl_sync(0xffffffffu, len, f);
+                cur.tiles = __shfl_sync(0xffffffffu, tiles, f);
+                at += (__shfl_sync(0xffffffffu, upto, f) - cur.tiles) * hrs;
+                break;
+            }
+            at += __shfl_sync(0xffffffffu, upto, 31) * hrs;
+        }
+        const int rem = u0 - at, hr = rem / cur.tiles;
+        cur.tile = rem - hr * cur.tiles;
         cur.h = hr / p.row_tiles;
         cur.rt = hr - cur.h * p.row_tiles;
     }
-    long long seg_base = u0 - cur.tile;                       // first tile of the segment at `cur`
+    int seg_base = u0 - cur.tile;                             // first tile of the segment at `cur`
     AttnCursor inf = cur;                                     // next tile to look up
 
     // addresses of K and V of entry `tid` of the tile at `inf`; 0 if there is none
@@ -296,7 +286,6 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
         }
     };
 
-    const long long n_units = u1 - u0;
     {
         const ulonglong2 r0 = look_up(true), r1 = look_up(n_units > 1);
         if (tid < TILE) {
@@ -318,16 +307,9 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
     int limit = 0, r_global = 0, n_new = 0;
     bool fresh = true;
 
-    for (long long i = 0; i < n_units; ++i) {
-        cp_wait<1>();
-        __syncthreads();
-        const int stage = (int)(i % STAGES);
-        if (i + 2 < n_units) copy((int)((i + 2) % STAGES), (int)(i & 1));
-        cp_commit();
-        const ulonglong2 nrow = look_up(i + 3 < n_units);
-
+    for (int i = 0; i < n_units; ++i) {
         const int h = cur.h, rt = cur.rt;
-        if (fresh) {                              // a new segment: its query rows
+        if (fresh) {                              // a new segment: its query rows, while its first tile is on the way
             fresh = false;
             n_new = new_count(p.new_len, cur.b, p.new_tokens, KID_ATTN);
             r_global = rt * ROWS + ug * 8 + g;
@@ -368,6 +350,13 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
             for (int dt = 0; dt < DT; ++dt) o[dt][0] = o[dt][1] = 0.f;
         }
 
+        cp_wait<1>();
+        __syncthreads();
+        const int stage = i % STAGES;
+        if (i + 2 < n_units) copy((i + 2) % STAGES, i & 1);
+        cp_commit();
+        const ulonglong2 nrow = look_up(i + 3 < n_units);
+
         const int base = cur.tile * TILE + tg * TW;           // the warp's first entry
         if (base < cur.len) {
             const uint32_t kb = ring + stage * 2 * S::kHalf + tg * TW * (DP * 2), vb = kb + S::kHalf;
@@ -393,7 +382,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
                 s[nt][0] = tok < limit ? (acc[0] + acc[2]) * sfac : -INFINITY;
                 s[nt][1] = tok + 1 < limit ? (acc[1] + acc[3]) * sfac : -INFINITY;
             }
-            if constexpr (SAVE) {
+            if (p.lse) {
                 if (r_global < p.rows) {
                     float *dst = p.scores + (((int64_t)cur.b * p.c.heads + h) * p.rows + r_global) * p.cap + base + 2 * j;
 #pragma unroll
@@ -474,109 +463,123 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
         attn_advance<TILE>(p, cur);
         if (i + 1 < n_units && cur.tile != 0) continue;
 
-        // ---- the segment's end (or this CTA's): join the warps that split its entries
+        // ---- the segment's end (or this CTA's): join the warps that split its entries.  Their sums go
+        // through the stage that was just used up: its next copies are issued after the next barrier.
         fresh = true;
         l = quad_sum(l);
-        if constexpr (TG > 1) {
+        float *sums = reinterpret_cast<float *>(smem + stage * 2 * S::kHalf);
+        __syncthreads();
+        if (r_global < p.rows) {
+            float *mine = sums + (warp * 8 + g) * S::kPad + 2 * j;
 #pragma unroll
-            for (int half = TG / 2; half >= 1; half >>= 1) {
-                float *mine = s_merge + (TG == 4 ? 0 : ug * 8 * DP) + (half == 2 ? (tg & 1) * 8 * DP : 0);
-                float(*ml)[2] = s_ml[TG == 4 ? (half == 2 ? tg & 1 : 0) : ug];
-                __syncthreads();
-                if (tg >= half && tg < 2 * half) {
+            for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<float2 *>(mine + dt * 8) = make_float2(o[dt][0], o[dt][1]);
+            if (j == 0) s_ml[warp][g] = make_float2(m, l);
+        }
+        __syncthreads();
+        const int rows_here = min(ROWS, p.rows - rt * ROWS);
+        const int64_t seg = (int64_t)was.b * p.c.heads + h;
+        const bool whole = seg_base >= u0 && was.tile + 1 == was.tiles;
+        // slot in the workspace of a part of a segment: 0 if it is the CTA's first, else 1
+        const int64_t part = 2 * (int64_t)blockIdx.x + (seg_base > u0 ? 1 : 0);
+        float *const ml_all = p.part + 2 * (int64_t)gridDim.x * ROWS * DP;
+        auto out_row = [&](int r) {
+            const int rg = rt * ROWS + r, t = rg / p.group;
+            return p.out + (((int64_t)was.b * p.new_tokens + t) * p.c.heads * p.group + h * p.group + (rg - t * p.group)) * (int64_t)p.c.dim;
+        };
+        constexpr int C4 = DP / 4;                            // 16-byte pieces of a row
+        for (int x = tid; x < rows_here * C4; x += THREADS) {
+            const int r = x / C4, c4 = x % C4, w0 = r / 8;    // row r: warps w0, w0 + UG, ...
+            float2 ml[TG];
+            float top = -INFINITY, tot = 0.f;
 #pragma unroll
-                    for (int dt = 0; dt < DT; ++dt)
-                        *reinterpret_cast<float2 *>(mine + g * DP + dt * 8 + 2 * j) = make_float2(o[dt][0], o[dt][1]);
-                    if (j == 0) {
-                        ml[g][0] = m;
-                        ml[g][1] = l;
-                    }
-                }
-                __syncthreads();
-                if (tg < half) {
-                    const float m2 = ml[g][0], l2 = ml[g][1], mm = fmaxf(m, m2), ref = mm == -INFINITY ? 0.f : mm;
-                    const float w1 = pow2(m - ref), w2 = pow2(m2 - ref);
-                    m = mm;
-                    l = l * w1 + l2 * w2;
+            for (int k = 0; k < TG; ++k) {
+                ml[k] = s_ml[w0 + k * UG][r & 7];
+                top = fmaxf(top, ml[k].x);
+            }
+            const float ref = top == -INFINITY ? 0.f : top;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) {
-                        const float2 x = *reinterpret_cast<const float2 *>(mine + g * DP + dt * 8 + 2 * j);
-                        o[dt][0] = o[dt][0] * w1 + x.x * w2;
-                        o[dt][1] = o[dt][1] * w1 + x.y * w2;
-                    }
-                }
+            for (int k = 0; k < TG; ++k) {
+                const float w = pow2(ml[k].x - ref);
+                const float4 v = *reinterpret_cast<const float4 *>(sums + ((w0 + k * UG) * 8 + (r & 7)) * S::kPad + c4 * 4);
+                tot = fmaf(ml[k].y, w, tot);
+                y.x = fmaf(v.x, w, y.x), y.y = fmaf(v.y, w, y.y), y.z = fmaf(v.z, w, y.z), y.w = fmaf(v.w, w, y.w);
+            }
+            if (whole) {
+                const float inv = inverse(tot);
+                if (c4 * 4 < p.c.dim)
+                    *reinterpret_cast<float4 *>(out_row(r) + c4 * 4) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+                if (p.lse && c4 == 0) p.lse[seg * p.rows + rt * ROWS + r] = log_sum(top, tot);
+            } else {
+                *reinterpret_cast<float4 *>(p.part + (part * ROWS + r) * DP + c4 * 4) = y;
+                if (c4 == 0) *reinterpret_cast<float2 *>(ml_all + (part * ROWS + r) * 2) = make_float2(top, tot);
             }
         }
-        const int t = r_global / p.group;
-        const int64_t seg = (int64_t)was.b * p.c.heads + h;
-        if (seg_base >= u0 && was.tile + 1 == was.tiles) {     // the whole segment is here
-            if (tg == 0 && r_global < p.rows) {
-                const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);     // NaN stays NaN
-                float *dst = p.out + (((int64_t)was.b * p.new_tokens + t) * p.c.heads * p.group + h * p.group +
-                                      (r_global - t * p.group)) * (int64_t)p.c.dim;
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
-                    if (dt * 8 < p.c.dim)
-                        *reinterpret_cast<float2 *>(dst + dt * 8 + 2 * j) = make_float2(o[dt][0] * inv, o[dt][1] * inv);
-                if (SAVE && j == 0) p.lse[seg * p.rows + r_global] = l > 0.f ? m + log2f(l) - P_EXP : INFINITY;
-            }
-        } else {
-            // part of a segment: slot 0 of this CTA if it is the CTA's first, else slot 1
-            const int64_t part = 2 * (int64_t)blockIdx.x + (seg_base > u0 ? 1 : 0);
-            float *ml_all = p.part + 2 * (int64_t)gridDim.x * ROWS * DP;
-            if (tg == 0) {
-                float *dst = p.part + (part * ROWS + ug * 8 + g) * DP;
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
-                    *reinterpret_cast<float2 *>(dst + dt * 8 + 2 * j) = make_float2(o[dt][0], o[dt][1]);
-                if (j == 0) *reinterpret_cast<float2 *>(ml_all + (part * ROWS + ug * 8 + g) * 2) = make_float2(m, l);
-            }
+        if (!whole) {
             // CTAs that hold tiles of the segment: those of its first and last tile, and all between
-            const long long c0 = ((seg_base + 1) * G - 1) / W, c1 = ((seg_base + was.tiles) * G - 1) / W;
+            const int c0 = (int)(((seg_base + 1ll) * G - 1) / W), c1 = (int)((((long long)seg_base + was.tiles) * G - 1) / W);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
                 int32_t *cnt = p.cnt + seg * p.row_tiles + rt;
-                const int32_t old = atomicAdd(cnt, 1);
-                s_last = old == (int32_t)(c1 - c0);
+                s_last = atomicAdd(cnt, 1) == c1 - c0;
                 if (s_last) *cnt = 0;
             }
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                const int rows_here = min(ROWS, p.rows - rt * ROWS);
                 // slot of CTA c: 1 only for the first, if the segment starts inside it
-                const long long first_u0 = W * c0 / G;
-                auto slot_of = [&](long long c) { return 2 * c + (c == c0 && seg_base > first_u0 ? 1 : 0); };
-                for (int r = warp; r < rows_here; r += 4) {
-                    float top = -INFINITY;
-                    for (long long c = c0 + lane; c <= c1; c += 32)
-                        top = fmaxf(top, __ldcg(ml_all + (slot_of(c) * ROWS + r) * 2));
-#pragma unroll
-                    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    constexpr int E = DP / 32;
-                    float sum[E], tot = 0.f;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) sum[e] = 0.f;
-#pragma unroll 4
-                    for (long long c = c0; c <= c1; ++c) {
-                        const long long sl = slot_of(c) * ROWS + r;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(ml_all) + sl);
-                        const float w = pow2(ml.x - ref);
-                        tot += ml.y * w;
-                        const float *src = p.part + sl * DP + lane;
-#pragma unroll
-                        for (int e = 0; e < E; ++e) sum[e] += __ldcg(src + e * 32) * w;
+                const int first = 2 * c0 + (seg_base > (int)((long long)W * c0 / G) ? 1 : 0);
+                auto slot_of = [&](int c) { return (int64_t)(c == c0 ? first : 2 * c); };
+                for (int r = warp; r < rows_here; r += 4) {   // the rows' statistics, CTAs side by side
+                    float top = -INFINITY, tot = 0.f;
+                    for (int c = c0 + lane; c <= c1; c += 32) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(ml_all) + slot_of(c) * ROWS + r);
+                        const float mx = fmaxf(top, ml.x), ref = mx == -INFINITY ? 0.f : mx;
+                        tot = tot * pow2(top - ref) + ml.y * pow2(ml.x - ref);
+                        top = mx;
                     }
-                    const float inv = tot > 0.f ? 1.f / tot : (tot == 0.f ? 0.f : tot);
-                    const int rg = rt * ROWS + r, tt = rg / p.group;
-                    float *dst = p.out + (((int64_t)was.b * p.new_tokens + tt) * p.c.heads * p.group + h * p.group +
-                                          (rg - tt * p.group)) * (int64_t)p.c.dim;
+                    float mx = top;
 #pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (e * 32 + lane < p.c.dim) dst[e * 32 + lane] = sum[e] * inv;
-                    if (SAVE && lane == 0) p.lse[seg * p.rows + rg] = tot > 0.f ? top + log2f(tot) - P_EXP : INFINITY;
+                    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    tot *= pow2(top - (mx == -INFINITY ? 0.f : mx));
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+                    if (lane == 0) {
+                        s_row_ml[r] = make_float2(mx == -INFINITY ? 0.f : mx, inverse(tot));
+                        if (p.lse) p.lse[seg * p.rows + rt * ROWS + r] = log_sum(mx, tot);
+                    }
+                }
+                __syncthreads();
+                // the sums: with few rows, groups of threads take every ways-th CTA each and join in shared memory
+                const int items = rows_here * C4, ways = items <= THREADS / 4 ? 4 : items <= THREADS / 2 ? 2 : 1;
+                const int per = THREADS / ways;
+                for (int x0 = 0; x0 < items; x0 += per) {
+                    const int x = x0 + tid % per, way = tid / per, r = x / C4, c4 = x % C4;
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float2 st = make_float2(0.f, 0.f);
+                    if (x < items) {
+                        st = s_row_ml[r];
+#pragma unroll 8
+                        for (int c = c0 + way; c <= c1; c += ways) {
+                            const int64_t sl = slot_of(c) * ROWS + r;
+                            const float w = pow2(__ldcg(ml_all + sl * 2) - st.x);
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * DP) + c4);
+                            y.x = fmaf(v.x, w, y.x), y.y = fmaf(v.y, w, y.y), y.z = fmaf(v.z, w, y.z), y.w = fmaf(v.w, w, y.w);
+                        }
+                    }
+                    if (ways > 1) {
+                        float4 *way_sums = reinterpret_cast<float4 *>(sums);
+                        way_sums[tid] = y;
+                        __syncthreads();
+                        if (way == 0)
+                            for (int k = 1; k < ways; ++k) {
+                                const float4 v = way_sums[tid + k * per];
+                                y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+                            }
+                    }
+                    if (way == 0 && x < items && c4 * 4 < p.c.dim)
+                        *reinterpret_cast<float4 *>(out_row(r) + c4 * 4) = make_float4(y.x * st.y, y.y * st.y, y.z * st.y, y.w * st.y);
                 }
             }
         }
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(256) attn_weight_kernel(const AttnParams p)
 
 struct AttnPlan {
     int dp, ug, rows, row_tiles, grid;
-    int64_t cap, part_floats, score_floats, lse_floats, counters;
+    int64_t tiles, cap, part_floats, score_floats, lse_floats, counters;
 };
 
 inline AttnPlan attn_plan(const mmq_kv_cache &c, int q_heads, int new_tokens, bool save)
@@ -615,9 +618,9 @@ inline AttnPlan attn_plan(const mmq_kv_cache &c, int q_heads, int new_tokens, bo
     a.ug = a.rows <= 8 ? 1 : a.rows <= 16 ? 2 : 4;
     a.row_tiles = (a.rows + 8 * a.ug - 1) / (8 * a.ug);
     const int tile = a.dp == 64 ? 128 : 64;
-    const int64_t most = ((int64_t)c.cols * c.page_size + tile - 1) / tile * c.seqs * c.heads * a.row_tiles;
+    a.tiles = ((int64_t)c.cols * c.page_size + tile - 1) / tile * c.seqs * c.heads * a.row_tiles;
     const int64_t full = (int64_t)sm_count() * (a.dp <= 128 ? 2 : 1);     // every CTA resident
-    a.grid = (int)(most < full ? most : full);
+    a.grid = (int)(a.tiles < full ? a.tiles : full);
     a.cap = ((int64_t)c.cols * c.page_size + 127) / 128 * 128;
     a.part_floats = 2 * (int64_t)a.grid * 8 * a.ug * (a.dp + 2);
     a.score_floats = save ? (int64_t)c.seqs * c.heads * a.rows * a.cap : 0;
@@ -634,10 +637,10 @@ inline int attn_check(const mmq_kv_cache *c, int q_heads, int new_tokens)
     return MMQ_OK;
 }
 
-template <int DP, typename T, int UG, bool SAVE>
+template <int DP, typename T, int UG>
 int launch_attn(const AttnParams &p, int grid, cudaStream_t stream)
 {
-    const auto kernel = attn_kernel<DP, T, UG, SAVE>;
+    const auto kernel = attn_kernel<DP, T, UG>;
     constexpr int smem = attn::Shape<DP>::kSmem;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -654,24 +657,19 @@ int launch_attn(const AttnParams &p, int grid, cudaStream_t stream)
     return launch_status();
 }
 
-template <int DP, typename T, int UG>
-int launch_attn_save(const AttnParams &p, int grid, bool save, cudaStream_t s)
-{
-    return save ? launch_attn<DP, T, UG, true>(p, grid, s) : launch_attn<DP, T, UG, false>(p, grid, s);
-}
 template <int DP, typename T>
-int launch_attn_ug(const AttnParams &p, const AttnPlan &a, bool save, cudaStream_t s)
+int launch_attn_ug(const AttnParams &p, const AttnPlan &a, cudaStream_t s)
 {
-    return a.ug == 1   ? launch_attn_save<DP, T, 1>(p, a.grid, save, s)
-           : a.ug == 2 ? launch_attn_save<DP, T, 2>(p, a.grid, save, s)
-                       : launch_attn_save<DP, T, 4>(p, a.grid, save, s);
+    return a.ug == 1   ? launch_attn<DP, T, 1>(p, a.grid, s)
+           : a.ug == 2 ? launch_attn<DP, T, 2>(p, a.grid, s)
+                       : launch_attn<DP, T, 4>(p, a.grid, s);
 }
 template <typename T>
-int launch_attn_dp(const AttnParams &p, const AttnPlan &a, bool save, cudaStream_t s)
+int launch_attn_dp(const AttnParams &p, const AttnPlan &a, cudaStream_t s)
 {
-    return a.dp == 64    ? launch_attn_ug<64, T>(p, a, save, s)
-           : a.dp == 128 ? launch_attn_ug<128, T>(p, a, save, s)
-                         : launch_attn_ug<256, T>(p, a, save, s);
+    return a.dp == 64    ? launch_attn_ug<64, T>(p, a, s)
+           : a.dp == 128 ? launch_attn_ug<128, T>(p, a, s)
+                         : launch_attn_ug<256, T>(p, a, s);
 }
 
 }  // namespace
@@ -685,6 +683,7 @@ extern "C" int mmq_attn_sizes(const mmq_kv_cache *cache, int q_heads, int new_to
     if (rc != MMQ_OK) return rc;
     if (!work_floats || !n_counters) return MMQ_ERR_NULL;
     const AttnPlan a = attn_plan(*cache, q_heads, new_tokens, accumulate != 0);
+    if (a.tiles > 0x7fffffff) return MMQ_ERR_SHAPE;
     *work_floats = a.part_floats + a.score_floats + a.lse_floats;
     *n_counters = a.counters;
     return MMQ_OK;
@@ -704,6 +703,7 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     if ((rc = check_arch()) != MMQ_OK) return rc;
     const bool save = accumulate != 0;
     const AttnPlan a = attn_plan(*cache, q_heads, new_tokens, save);
+    if (a.tiles > 0x7fffffff) return MMQ_ERR_SHAPE;       // tiles are counted in an int
     AttnParams p;
     p.c = *cache;
     p.q = q;
@@ -717,12 +717,12 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     p.row_tiles = a.row_tiles;
     p.scores = work;                                   // rows of a multiple of 128 floats: 16-byte aligned
     p.part = work + a.score_floats;
-    p.lse = p.part + a.part_floats;
+    p.lse = save ? p.part + a.part_floats : nullptr;
     p.cnt = counters;
     p.cap = a.cap;
     p.page_div = FastDiv(cache->page_size);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    rc = cache->dtype == MMQ_F16 ? launch_attn_dp<__half>(p, a, save, s) : launch_attn_dp<__nv_bfloat16>(p, a, save, s);
+    rc = cache->dtype == MMQ_F16 ? launch_attn_dp<__half>(p, a, s) : launch_attn_dp<__nv_bfloat16>(p, a, s);
     if (rc != MMQ_OK || !save) return rc;
     const dim3 grid((unsigned)(a.cap / 128 + 1) / 2, (unsigned)cache->heads, (unsigned)cache->seqs);
     attn_weight_kernel<<<grid, 256, 0, s>>>(p);

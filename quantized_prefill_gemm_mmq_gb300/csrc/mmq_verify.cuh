@@ -47,11 +47,23 @@ __device__ __forceinline__ float ver_f(float x) { return x; }
 __device__ __forceinline__ float ver_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ float ver_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// w_j; q may be absent
-__device__ __forceinline__ unsigned long long ver_fixed(float p, float q)
+// w = round(2^40 d), d = max(p - q, 0) limited to 1, in two parts: added to hi
+// the upper 17 bits, to lo the 23 below them (up to 2^23).  With 2^23 added, a
+// float's bits count in ones: the upper part by rounding down, the lower, of
+// the exact rest, to nearest even.  The bits of 2^23 itself, 0x4b000000, stay
+// in the sums: ver_join takes them off.
+__device__ __forceinline__ void ver_add(float p, float q, uint32_t &hi, uint32_t &lo)
 {
-    const float d = fminf(fmaxf(__fsub_rn(p, q), 0.f), 1.f);
-    return (unsigned long long)__float2ll_rn(d * 0x1p40f);
+    const float d = __saturatef(__fsub_rn(p, q));
+    const float t = __fmaf_rd(d, 0x1p17f, 0x1p23f);
+    const float rest = __fmaf_rn(d, 0x1p17f, -__fsub_rn(t, 0x1p23f));
+    hi += __float_as_uint(t);
+    lo += __float_as_uint(__fmaf_rn(rest, 0x1p23f, 0x1p23f));
+}
+// the sum of n values' w
+__device__ __forceinline__ unsigned long long ver_join(uint32_t hi, uint32_t lo, uint32_t n)
+{
+    return ((unsigned long long)(hi - n * 0x4b000000u) << 23) + (lo - n * 0x4b000000u);
 }
 
 __device__ __forceinline__ unsigned long long cluster_ld64(uint32_t a)
@@ -95,18 +107,15 @@ __device__ __forceinline__ uint4 ver_load(const T *row, int j, int hi)
                       __funnelshift_r(w[3], w[4], s));
 }
 
-// The sum of the w_j of 16 bytes' worth of values; each of them in w.
+// the sum of the w_j of 16 bytes' worth of values
 template <typename T>
-__device__ __forceinline__ unsigned long long ver_sum(const uint4 &pv, const uint4 &qv, unsigned long long (&w)[ver::kPer<T>])
+__device__ __forceinline__ unsigned long long ver_sum(const uint4 &pv, const uint4 &qv)
 {
     const T *p = reinterpret_cast<const T *>(&pv), *q = reinterpret_cast<const T *>(&qv);
-    unsigned long long s = 0;
+    uint32_t hi = 0, lo = 0;
 #pragma unroll
-    for (int k = 0; k < ver::kPer<T>; ++k) {
-        w[k] = ver_fixed(ver_f(p[k]), ver_f(q[k]));
-        s += w[k];
-    }
-    return s;
+    for (int k = 0; k < ver::kPer<T>; ++k) ver_add(ver_f(p[k]), ver_f(q[k]), hi, lo);
+    return ver_join(hi, lo, ver::kPer<T>);
 }
 
 template <typename T>
@@ -188,8 +197,7 @@ __global__ void __launch_bounds__(ver::THREADS, ver::PER_SM) spec_verify_kernel(
             }
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
-                unsigned long long each[PER];
-                unsigned long long w = ver_sum<T>(pv[k], qv[k], each);
+                unsigned long long w = ver_sum<T>(pv[k], qv[k]);
 #pragma unroll
                 for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
                 if (lane == 0 && sp + k * WARPS < p.spans) s_span[sp + k * WARPS] = w;
@@ -236,14 +244,13 @@ __global__ void __launch_bounds__(ver::THREADS, ver::PER_SM) spec_verify_kernel(
                     }
                     at += __shfl_sync(0xffffffffu, c, 31);
                 }
-                unsigned long long w[PER];
                 const int j = lo + sp * SPAN + lane * PER;
                 uint4 pv = make_uint4(0u, 0u, 0u, 0u), qv = pv;
                 if (j < hi) {
                     pv = ver_load(pr, j, hi);
                     qv = load_q(j, plain);
                 }
-                const unsigned long long x = ver_sum<T>(pv, qv, w);
+                const unsigned long long x = ver_sum<T>(pv, qv);
                 unsigned long long c = x;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -253,13 +260,14 @@ __global__ void __launch_bounds__(ver::THREADS, ver::PER_SM) spec_verify_kernel(
                 const unsigned m = __ballot_sync(0xffffffffu, at + c > r);
                 if (m && lane == __ffs(m) - 1) {
                     at += c - x;
-                    int tok = 0;
+                    const T *pk = reinterpret_cast<const T *>(&pv), *qk = reinterpret_cast<const T *>(&qv);
+                    int tok = -1;
 #pragma unroll
-                    for (int k = PER - 1; k >= 0; --k) {
-                        unsigned long long upto = at;
-#pragma unroll
-                        for (int i = 0; i <= k; ++i) upto += w[i];
-                        if (upto > r) tok = j + k;
+                    for (int k = 0; k < PER; ++k) {
+                        uint32_t h1 = 0, l1 = 0;
+                        ver_add(ver_f(pk[k]), ver_f(qk[k]), h1, l1);
+                        at += ver_join(h1, l1, 1);
+                        if (tok < 0 && at > r) tok = j + k;
                     }
                     p.out[(int64_t)b * (p.drafts + 1) + a] = tok;
                 }
