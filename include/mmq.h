@@ -498,16 +498,15 @@ int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, int rot, flo
  * timing: they repeat bit for bit.
  * accumulate != 0 adds to cache->weight, for every entry a sequence has, the
  * sum of p over its rows and the query heads of the key-value head.
- * 1 <= new_tokens <= 16, q_heads a multiple of heads, scale finite.
- * `work` and `counters` as mmq_attn_sizes says; the counters are zero before
- * the first call and every call leaves them zero.  Calls that share them must
+ * 1 <= new_tokens <= 16, q_heads a multiple (1 .. 128) of heads, scale finite.
+ * `work` holds the floats that mmq_attn_sizes says.  Calls that share it must
  * be ordered (one stream).
  */
 int mmq_attn_sizes(const mmq_kv_cache *cache, int q_heads, int new_tokens, int accumulate,
-                   int64_t *work_floats, int64_t *n_counters);
+                   int64_t *work_floats);
 int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_t ldq, const int32_t *new_len,
                     float *out, int q_heads, int new_tokens, float scale, int accumulate,
-                    float *work, int32_t *counters, mmq_stream_t stream);
+                    float *work, mmq_stream_t stream);
 
 /*
  * Eviction: every sequence with more than `budget` entries is cut down to

@@ -52,8 +52,8 @@ SIGNATURES = {
     "mmq_debug_subdots_q4K": (_I, [_P, _P, _P, _I, _I, _I, _P]),
     "mmq_debug_subdots_q6K": (_I, [_P, _P, _P, _I, _I, _I, _P]),
     "mmq_rope_append": (_I, [_P, _P, _I, ctypes.c_float, _I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I, _I, _P]),
-    "mmq_attn_sizes": (_I, [_P, _I, _I, _I, _P, _P]),
-    "mmq_attn_decode": (_I, [_P, _P, _I64, _P, _P, _I, _I, ctypes.c_float, _I, _P, _P, _P]),
+    "mmq_attn_sizes": (_I, [_P, _I, _I, _I, _P]),
+    "mmq_attn_decode": (_I, [_P, _P, _I64, _P, _P, _I, _I, ctypes.c_float, _I, _P, _P]),
     "mmq_evict_sizes": (_I, [_P, _I, _P]),
     "mmq_kv_evict": (_I, [_P, _I, _P, _P, _P, _P, _P]),
     "mmq_spec_verify": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P]),

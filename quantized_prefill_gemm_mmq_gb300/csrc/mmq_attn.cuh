@@ -12,28 +12,32 @@
 // and heads are numbered in a row, and the persistent grid's CTA c takes tiles
 // [c W/G, (c+1) W/G): every CTA reads the same amount whatever the lengths.
 // A run of tiles that belongs to one (sequence, head) is a segment; a CTA that
-// has all of a segment writes its output, the others leave their part (m, sum,
-// sum p v) in the workspace, and the last of them to arrive joins the parts in
-// CTA order.  The counters only say who is last: no result depends on timing.
+// has all of a segment writes its output, the others leave their part (max,
+// sum, sum p v) in the workspace, and a second launch joins the parts in CTA
+// order.  No result depends on timing.  (Joining by the last CTA to arrive,
+// with a counter per segment, took 7 to 14 us at the end of a launch with 33
+// parts of 20 rows: one CTA reads all parts of its segment.)
 //
 // Tiles.  K and V rows are gathered through the page table with 16-byte
-// cp.async into a three-stage ring (any page size and stride; entries past
+// cp.async into a ring of stages (any page size and stride; entries past
 // the length arrive as zeros), chunk-XOR swizzled so that ldmatrix reads
 // without bank conflicts.  The table entries of a tile are fetched one
 // iteration before its copies are issued.
 //
-// Products run on the warp-level tensor core, whose 16-row operand is filled
-// with eight query rows twice: the upper eight rows hold the rounded values
-// (f16 or bf16, the cache's type), the lower eight what rounding left, and the
-// two halves of the result are added.  For f16 that makes 22 bits of q and of
-// p; for bf16 a second product with a third part makes 24.  q is scaled by a
-// power of two per row to lie below 2 and p by 2^15, so that f16's range does
-// not clip either.  K and V are used as they are.  The sums over a tile's
-// entries stay in f32 and are added to the running sums with f32 FMAs.
+// Products run on the warp-level tensor core (16-row operand), with q and p
+// split into parts of the cache's type that add up to 22 bits (f16, two parts)
+// or 24 (bf16, three); K and V are used as they are.  Up to eight rows
+// (RP = 1): the operand's upper eight rows hold the first part, the lower eight
+// the second, and the two halves of the result are added; bf16's third part
+// takes a second product.  More rows (RP = 2): sixteen rows per operand, one
+// product per part.  q is scaled by a power of two per row to lie below 2, and
+// for f16 p carries 2^15, so that f16's range does not clip either.  The sums
+// over a tile's entries stay in f32 and are added to the running sums with f32
+// FMAs.
 //
-// UG warps of the four take eight rows each over the same entries and 4/UG
+// UG warps of the four take 8*RP rows each over the same entries and 4/UG
 // warps split a tile's entries (with their own running maximum, joined at the
-// segment's end), so that up to 8*UG rows share one read of the cache.
+// segment's end), so that up to 8*RP*UG rows share one read of the cache.
 #pragma once
 
 #include <type_traits>
@@ -43,17 +47,26 @@ namespace {
 
 namespace attn {
 constexpr int THREADS = 128;
-constexpr int STAGES = 3;
-constexpr float P_EXP = 15.f;         // p carries 2^15
 
-template <int DP>
+template <typename T>
+constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+template <typename T>
+constexpr float kExp = kBf16<T> ? 0.f : 15.f;      // p carries 2^kExp
+
+// DP: dim padded to 64, 128 or 256; RP, UG: see above
+template <int DP, int RP, int UG>
 struct Shape {
     static constexpr int kTile = DP == 64 ? 128 : 64;                 // entries per tile
+    static constexpr int kStages = 3;                                 // tiles in the ring
+    static constexpr int kPerSm = DP <= 128 ? 2 : 1;                  // CTAs resident per SM
     static constexpr int kHalf = kTile * DP * 2;                      // bytes of K (or V) per stage
-    static constexpr int kSmem = STAGES * 2 * kHalf;
-    static constexpr int kPerSm = DP <= 128 ? 2 : 1;
-    static constexpr int kPad = DP + 8;                               // floats per row of a warp's sums in shared memory
-    static_assert(4 * 8 * kPad * 4 <= 2 * kHalf, "four warps' sums fit in one stage");
+    static constexpr int kSmem = kStages * 2 * kHalf;
+    static constexpr int kRows = 8 * RP * UG;                         // rows per CTA
+    // the four warps' sums are joined in one stage's memory, in as many rounds of columns as fit
+    static constexpr int fit(int rounds) { return 4 * 8 * RP * (DP / rounds + 8) * 4 <= 2 * kHalf ? rounds : fit(rounds * 2); }
+    static constexpr int kRounds = fit(1);
+    static constexpr int kCols = DP / kRounds;
+    static constexpr int kPad = kCols + 8;                            // floats per row there: no bank conflicts
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there)
@@ -109,7 +122,7 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
     x -= h.x;
     y -= h.y;
     mid = pack2<T>(x, y);
-    if constexpr (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value) {
+    if constexpr (kBf16<T>) {
         const float2 m = unpack2<T>(mid);
         lo = pack2<T>(x - m.x, y - m.y);
     } else {
@@ -140,7 +153,8 @@ __device__ __forceinline__ float quad_sum(float x)
 // 1 / sum, 0 for a row that saw nothing; a NaN stays one
 __device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : sum; }
 // log2 of a row's sum of powers, so that pow2(score - it) is its weight
-__device__ __forceinline__ float log_sum(float m, float sum) { return sum > 0.f ? m + log2f(sum) - P_EXP : INFINITY; }
+template <typename T>
+__device__ __forceinline__ float log_sum(float m, float sum) { return sum > 0.f ? m + log2f(sum) - kExp<T> : INFINITY; }
 
 // whether one of two values has all exponent bits set
 template <typename T>
@@ -159,9 +173,9 @@ struct AttnParams {
     int64_t ldq;
     float scale_log2;        // scale * log2(e): exponentials are powers of two
     int new_tokens, group;   // rows per key-value head: r = t*group + g
-    int rows, row_tiles;     // rows, and parts of 8*UG rows
-    float *part;             // [2*grid][8*UG][DP] sums, then [2*grid][8*UG][2] (max, sum)
-    int32_t *cnt;            // [seqs*heads*row_tiles]
+    int rows, row_tiles;     // rows, and parts of kRows rows
+    float *part;             // [2*grid][kRows][DP] sums, then [2*grid][kRows][2] (max, sum)
+    int3 *parts;             // [seqs*heads][row_tiles]: first part, its CTA, last CTA (-1: output written)
     float *scores;           // [seqs*heads][rows][cap] in powers of two (weights only)
     float *lse;              // [seqs*heads][rows] (weights only, else NULL)
     int64_t cap;
@@ -193,21 +207,21 @@ __device__ __forceinline__ void attn_advance(const AttnParams &p, AttnCursor &u)
     u.tiles = attn_tiles<TILE>(u.len);
 }
 
-template <int DP, typename T, int UG>
-__global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_kernel(const AttnParams p)
+template <int DP, typename T, int RP, int UG>
+__global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm) attn_kernel(const AttnParams p)
 {
     using namespace attn;
-    using S = Shape<DP>;
-    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
-    constexpr int TILE = S::kTile, TG = 4 / UG, TW = TILE / TG;    // entries per warp and tile
-    constexpr int NT = TW / 8, KS = DP / 16, DT = DP / 8, ROWS = 8 * UG;
+    using S = Shape<DP, RP, UG>;
+    constexpr bool BF = kBf16<T>;
+    constexpr int PARTS = RP == 1 ? (BF ? 2 : 1) : (BF ? 3 : 2);     // products per tensor-core step
+    constexpr int TILE = S::kTile, STAGES = S::kStages, TG = 4 / UG, TW = TILE / TG;    // TW: entries per warp and tile
+    constexpr int NT = TW / 8, KS = DP / 16, DT = DP / 8, ROWS = S::kRows;
     constexpr int CPR = DP / 8, RPP = THREADS / CPR, PASSES = TILE / RPP;   // 16-byte copies per row, rows per pass
 
+    pdl_launch_dependents();       // the joining launch may start; it waits for this grid's end before it reads
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ ulonglong2 s_row[2][TILE];
-    __shared__ int s_last;
-    __shared__ float2 s_ml[4][8];              // (max, sum) of every warp's rows
-    __shared__ float2 s_row_ml[ROWS];          // of the joined rows; the joining CTA: (max, 1 / sum)
+    __shared__ ulonglong2 s_row[STAGES][TILE];
+    __shared__ float2 s_ml[4][8 * RP];         // (max, sum) of every warp's rows
     const uint32_t ring = smem_u32(smem);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -273,9 +287,9 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
     // this thread's 16-byte piece of rows cr, cr + RPP, ...
     const int cc = tid % CPR, cr = tid / CPR;
     const bool piece = cc * 8 < p.c.dim;
-    auto copy = [&](int stage, int buf) {
+    auto copy = [&](int stage) {
         const uint32_t base = ring + stage * 2 * S::kHalf + cr * (DP * 2);
-        const ulonglong2 *rows = s_row[buf] + cr;
+        const ulonglong2 *rows = s_row[stage] + cr;
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             const ulonglong2 w = rows[i * RPP];
@@ -287,81 +301,95 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
     };
 
     {
-        const ulonglong2 r0 = look_up(true), r1 = look_up(n_units > 1);
+        ulonglong2 r[STAGES];
+#pragma unroll
+        for (int k = 0; k < STAGES; ++k) r[k] = look_up(k < n_units);
         if (tid < TILE) {
-            s_row[0][tid] = r0;
-            s_row[1][tid] = r1;
+#pragma unroll
+            for (int k = 0; k < STAGES; ++k) s_row[k][tid] = r[k];
         }
         __syncthreads();
-        copy(0, 0);
-        cp_commit();
-        if (n_units > 1) copy(1, 1);
-        cp_commit();
-        const ulonglong2 r2 = look_up(n_units > 2);
-        __syncthreads();
-        if (tid < TILE) s_row[0][tid] = r2;
+#pragma unroll
+        for (int k = 0; k < STAGES - 1; ++k) {
+            if (k < n_units) copy(k);
+            cp_commit();
+        }
     }
 
-    uint32_t qa[KS][4], ql[BF ? KS : 1][2];      // query fragments: rounded | rest, and the third part
-    float o[DT][2], m = -INFINITY, l = 0.f, sfac = 0.f;
-    int limit = 0, r_global = 0, n_new = 0;
+    // the rows of this thread's quad: one (RP = 1) or two, eight apart
+    uint32_t qf[PARTS][KS][4];                   // query fragments
+    float o[DT][RP][2], m[RP], l[RP], sfac[RP];
+    int limit[RP], n_new = 0;
     bool fresh = true;
 
     for (int i = 0; i < n_units; ++i) {
         const int h = cur.h, rt = cur.rt;
+        const int row0 = rt * ROWS + ug * 8 * RP + g;
         if (fresh) {                              // a new segment: its query rows, while its first tile is on the way
             fresh = false;
             n_new = new_count(p.new_len, cur.b, p.new_tokens, KID_ATTN);
-            r_global = rt * ROWS + ug * 8 + g;
-            const int t = r_global / p.group;
-            const bool valid = r_global < p.rows && t < n_new;
-            limit = valid ? cur.len - n_new + t + 1 : 0;
-            const float *qr = p.q + ((int64_t)cur.b * p.new_tokens + (valid ? t : 0)) * p.ldq +
-                              (int64_t)(h * p.group + (valid ? r_global - t * p.group : 0)) * p.c.dim;
-            float2 x[KS][2];
-            float top = 0.f;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+            for (int rp = 0; rp < RP; ++rp) {
+                const int r = row0 + 8 * rp, t = r / p.group;
+                const bool valid = r < p.rows && t < n_new;
+                limit[rp] = valid ? cur.len - n_new + t + 1 : 0;
+                const float *qr = p.q + ((int64_t)cur.b * p.new_tokens + (valid ? t : 0)) * p.ldq +
+                                  (int64_t)(h * p.group + (valid ? r - t * p.group : 0)) * p.c.dim;
+                float2 x[KS][2];
+                float top = 0.f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int d = ks * 16 + e * 8 + 2 * j;
-                    x[ks][e] = valid && d < p.c.dim ? *reinterpret_cast<const float2 *>(qr + d) : make_float2(0.f, 0.f);
-                    top = fmaxf(top, fmaxf(fabsf(x[ks][e].x), fabsf(x[ks][e].y)));
-                }
-            top = quad_max(top);
-            // the row's power of two, away from f32's ends
-            int ex = (int)(__float_as_uint(top) >> 23) - 127;
-            ex = min(max(ex, -100), 100);
-            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-            sfac = p.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23);
+                for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                uint32_t l0, l1;
-                split<T>(x[ks][0].x * down, x[ks][0].y * down, qa[ks][0], qa[ks][1], l0);
-                split<T>(x[ks][1].x * down, x[ks][1].y * down, qa[ks][2], qa[ks][3], l1);
-                if constexpr (BF) {
-                    ql[ks][0] = l0;
-                    ql[ks][1] = l1;
-                }
+                    for (int e = 0; e < 2; ++e) {
+                        const int d = ks * 16 + e * 8 + 2 * j;
+                        x[ks][e] = valid && d < p.c.dim ? *reinterpret_cast<const float2 *>(qr + d) : make_float2(0.f, 0.f);
+                        top = fmaxf(top, fmaxf(fabsf(x[ks][e].x), fabsf(x[ks][e].y)));
+                    }
+                top = quad_max(top);
+                // the row's power of two, away from f32's ends; the sign of the scale goes to q, so that sfac > 0
+                int ex = (int)(__float_as_uint(top) >> 23) - 127;
+                ex = min(max(ex, -100), 100);
+                const float down = copysignf(__uint_as_float((uint32_t)(127 - ex) << 23), p.scale_log2);
+                sfac[rp] = fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + ex) << 23), 1e-37f);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t hi, mid, lo;
+                        split<T>(x[ks][e].x * down, x[ks][e].y * down, hi, mid, lo);
+                        if constexpr (RP == 1) {
+                            qf[0][ks][2 * e] = hi;
+                            qf[0][ks][2 * e + 1] = mid;
+                            if constexpr (BF) {
+                                qf[PARTS - 1][ks][2 * e] = lo;
+                                qf[PARTS - 1][ks][2 * e + 1] = 0;
+                            }
+                        } else {
+                            qf[0][ks][2 * e + rp] = hi;
+                            qf[1 % PARTS][ks][2 * e + rp] = mid;
+                            if constexpr (BF) qf[PARTS - 1][ks][2 * e + rp] = lo;
+                        }
+                    }
+                m[rp] = -INFINITY;
+                l[rp] = 0.f;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) o[dt][rp][0] = o[dt][rp][1] = 0.f;
             }
-            m = -INFINITY;
-            l = 0.f;
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) o[dt][0] = o[dt][1] = 0.f;
         }
-
-        cp_wait<1>();
+        cp_wait<STAGES - 2>();
         __syncthreads();
         const int stage = i % STAGES;
-        if (i + 2 < n_units) copy((i + 2) % STAGES, i & 1);
+        if (i + STAGES - 1 < n_units) copy((i + STAGES - 1) % STAGES);
         cp_commit();
-        const ulonglong2 nrow = look_up(i + 3 < n_units);
+        const ulonglong2 nrow = look_up(i + STAGES < n_units);    // its rows take the place of tile i's
 
         const int base = cur.tile * TILE + tg * TW;           // the warp's first entry
         if (base < cur.len) {
             const uint32_t kb = ring + stage * 2 * S::kHalf + tg * TW * (DP * 2), vb = kb + S::kHalf;
-            // ---- scores
-            float s[NT][2];
+            // ---- scores, before their row's factor
+            float s[NT][RP][2];
+            const int seen = cur.len - n_new + 1;             // entries that every row sees
+            const bool edge = base + TW > seen;               // some row may not see all of the warp's
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -371,52 +399,81 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
                 for (int k2 = 0; k2 < KS / 2; ++k2) {
                     uint32_t b[4];
                     ldsm4(b, ra + (((k2 * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
-                    mma16816<T>(acc, qa[2 * k2][0], qa[2 * k2][1], qa[2 * k2][2], qa[2 * k2][3], b[0], b[1]);
-                    mma16816<T>(acc, qa[2 * k2 + 1][0], qa[2 * k2 + 1][1], qa[2 * k2 + 1][2], qa[2 * k2 + 1][3], b[2], b[3]);
-                    if constexpr (BF) {
-                        mma16816<T>(acc, ql[2 * k2][0], 0u, ql[2 * k2][1], 0u, b[0], b[1]);
-                        mma16816<T>(acc, ql[2 * k2 + 1][0], 0u, ql[2 * k2 + 1][1], 0u, b[2], b[3]);
-                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int x = 0; x < PARTS; ++x) {
+                            const uint32_t(&a)[4] = qf[x][2 * k2 + e];
+                            mma16816<T>(acc, a[0], RP == 1 && x == 1 ? 0u : a[1], a[2], RP == 1 && x == 1 ? 0u : a[3], b[2 * e], b[2 * e + 1]);
+                        }
                 }
-                const int tok = base + nt * 8 + 2 * j;
-                s[nt][0] = tok < limit ? (acc[0] + acc[2]) * sfac : -INFINITY;
-                s[nt][1] = tok + 1 < limit ? (acc[1] + acc[3]) * sfac : -INFINITY;
+#pragma unroll
+                for (int rp = 0; rp < RP; ++rp)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) s[nt][rp][e] = RP == 1 ? acc[e] + acc[2 + e] : acc[2 * rp + e];
+            }
+            if (base + TW > min(limit[0], limit[RP - 1])) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int rp = 0; rp < RP; ++rp)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (base + nt * 8 + 2 * j + e >= limit[rp]) s[nt][rp][e] = -INFINITY;
             }
             if (p.lse) {
-                if (r_global < p.rows) {
-                    float *dst = p.scores + (((int64_t)cur.b * p.c.heads + h) * p.rows + r_global) * p.cap + base + 2 * j;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        *reinterpret_cast<float2 *>(dst + nt * 8) = make_float2(s[nt][0], s[nt][1]);
-                }
+                for (int rp = 0; rp < RP; ++rp)
+                    if (row0 + 8 * rp < p.rows) {
+                        float *dst = p.scores + (((int64_t)cur.b * p.c.heads + h) * p.rows + row0 + 8 * rp) * p.cap + base + 2 * j;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            *reinterpret_cast<float2 *>(dst + nt * 8) = make_float2(s[nt][rp][0] * sfac[rp], s[nt][rp][1] * sfac[rp]);
+                    }
             }
             // ---- running maximum, powers, sums
-            float mx = m;
+            float alpha[RP];
+            uint32_t pf[PARTS][NT / 2][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt][0], s[nt][1]));
-            mx = quad_max(mx);
-            const float ref = mx == -INFINITY ? 0.f : mx;     // nothing seen yet: every power is 0
-            const float alpha = pow2(m - ref);
-            m = mx;
-            l *= alpha;
-            uint32_t ph[NT / 2][4], pl[BF ? NT / 2 : 1][2];
+            for (int rp = 0; rp < RP; ++rp) {
+                float mx = s[0][rp][0];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float p0 = pow2(s[nt][0] - ref) * 0x1p15f, p1 = pow2(s[nt][1] - ref) * 0x1p15f;
-                l += p0 + p1;
-                uint32_t lo;
-                split<T>(p0, p1, ph[nt / 2][(nt & 1) * 2], ph[nt / 2][(nt & 1) * 2 + 1], lo);
-                if constexpr (BF) pl[nt / 2][nt & 1] = lo;
+                for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt][rp][0], s[nt][rp][1]));
+                mx = fmaxf(m[rp], quad_max(mx) * sfac[rp]);
+                const float ref = mx == -INFINITY ? 0.f : mx; // nothing seen yet: every power is 0
+                alpha[rp] = pow2(m[rp] - ref);
+                m[rp] = mx;
+                l[rp] *= alpha[rp];
+                const float shift = kExp<T> - ref;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float p0 = pow2(fmaf(s[nt][rp][0], sfac[rp], shift)), p1 = pow2(fmaf(s[nt][rp][1], sfac[rp], shift));
+                    l[rp] += p0 + p1;
+                    uint32_t hi, mid, lo;
+                    split<T>(p0, p1, hi, mid, lo);
+                    const int k = nt / 2, e = nt & 1;
+                    if constexpr (RP == 1) {
+                        pf[0][k][2 * e] = hi;
+                        pf[0][k][2 * e + 1] = mid;
+                        if constexpr (BF) {
+                            pf[PARTS - 1][k][2 * e] = lo;
+                            pf[PARTS - 1][k][2 * e + 1] = 0;
+                        }
+                    } else {
+                        pf[0][k][2 * e + rp] = hi;
+                        pf[1 % PARTS][k][2 * e + rp] = mid;
+                        if constexpr (BF) pf[PARTS - 1][k][2 * e + rp] = lo;
+                    }
+                }
             }
             // ---- p v.  Entries that only some of the rows see must not reach the others even as 0 * Inf:
             // if one of them is not finite, the products run once per new token with the entries beyond its
             // view cleared, each row taking the pass of its own token.
-            int pass = 0, passes = 1;
-            const int seen = cur.len - n_new + 1;             // entries that every row sees
-            if (n_new > 1 && base + TW > seen) {
+            int passes = 1;
+            if (n_new > 1 && edge) {
                 bool bad = false;
-                const int e0 = max(seen, base) - base, e1 = min(cur.len, base + TW) - base;
-                for (int e = max(e0, 0); e < e1; ++e)
+                const int e1 = min(cur.len, base + TW) - base;
+                for (int e = max(seen - base, 0); e < e1; ++e)
                     for (int w = lane; w < DP / 2; w += 32) {
                         uint32_t v;
                         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(vb + e * (DP * 2) + w * 4));
@@ -425,13 +482,18 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
                 if (__any_sync(0xffffffffu, bad)) passes = n_new;
             }
 #pragma unroll 1
-            for (; pass < passes; ++pass) {
+            for (int pass = 0; pass < passes; ++pass) {
                 const int view = passes > 1 ? seen + pass : 0x7fffffff;
-                const bool take = passes == 1 || limit == view;
-                const float keep = take ? alpha : 1.f;
+                bool take[RP];
+                float keep[RP];
+#pragma unroll
+                for (int rp = 0; rp < RP; ++rp) {
+                    take[rp] = passes == 1 || limit[rp] == view;
+                    keep[rp] = take[rp] ? alpha[rp] : 1.f;
+                }
 #pragma unroll
                 for (int d2 = 0; d2 < DT / 2; ++d2) {
-                    float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+                    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
                     for (int k = 0; k < NT / 2; ++k) {
                         uint32_t b[4];
@@ -443,21 +505,28 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
                             const uint32_t m1 = (tok + 8 < view ? 0xffffu : 0u) | (tok + 9 < view ? 0xffff0000u : 0u);
                             b[0] &= m0, b[1] &= m1, b[2] &= m0, b[3] &= m1;
                         }
-                        mma16816<T>(a0, ph[k][0], ph[k][1], ph[k][2], ph[k][3], b[0], b[1]);
-                        mma16816<T>(a1, ph[k][0], ph[k][1], ph[k][2], ph[k][3], b[2], b[3]);
-                        if constexpr (BF) {
-                            mma16816<T>(a0, pl[k][0], 0u, pl[k][1], 0u, b[0], b[1]);
-                            mma16816<T>(a1, pl[k][0], 0u, pl[k][1], 0u, b[2], b[3]);
+#pragma unroll
+                        for (int x = 0; x < PARTS; ++x) {
+                            const uint32_t(&a)[4] = pf[x][k];
+                            const uint32_t a1 = RP == 1 && x == 1 ? 0u : a[1], a3 = RP == 1 && x == 1 ? 0u : a[3];
+                            mma16816<T>(acc[0], a[0], a1, a[2], a3, b[0], b[1]);
+                            mma16816<T>(acc[1], a[0], a1, a[2], a3, b[2], b[3]);
                         }
                     }
-                    o[2 * d2][0] = fmaf(o[2 * d2][0], keep, take ? a0[0] + a0[2] : 0.f);
-                    o[2 * d2][1] = fmaf(o[2 * d2][1], keep, take ? a0[1] + a0[3] : 0.f);
-                    o[2 * d2 + 1][0] = fmaf(o[2 * d2 + 1][0], keep, take ? a1[0] + a1[2] : 0.f);
-                    o[2 * d2 + 1][1] = fmaf(o[2 * d2 + 1][1], keep, take ? a1[1] + a1[3] : 0.f);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int rp = 0; rp < RP; ++rp)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float add = RP == 1 ? acc[c][e] + acc[c][2 + e] : acc[c][2 * rp + e];
+                                float &y = o[2 * d2 + c][rp][e];
+                                y = fmaf(y, keep[rp], take[rp] ? add : 0.f);
+                            }
                 }
             }
         }
-        if (tid < TILE) s_row[(i + 1) & 1][tid] = nrow;
+        if (tid < TILE) s_row[stage][tid] = nrow;
 
         const AttnCursor was = cur;
         attn_advance<TILE>(p, cur);
@@ -466,16 +535,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
         // ---- the segment's end (or this CTA's): join the warps that split its entries.  Their sums go
         // through the stage that was just used up: its next copies are issued after the next barrier.
         fresh = true;
-        l = quad_sum(l);
         float *sums = reinterpret_cast<float *>(smem + stage * 2 * S::kHalf);
-        __syncthreads();
-        if (r_global < p.rows) {
-            float *mine = sums + (warp * 8 + g) * S::kPad + 2 * j;
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<float2 *>(mine + dt * 8) = make_float2(o[dt][0], o[dt][1]);
-            if (j == 0) s_ml[warp][g] = make_float2(m, l);
-        }
-        __syncthreads();
         const int rows_here = min(ROWS, p.rows - rt * ROWS);
         const int64_t seg = (int64_t)was.b * p.c.heads + h;
         const bool whole = seg_base >= u0 && was.tile + 1 == was.tiles;
@@ -486,146 +546,231 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP>::kPerSm) attn_k
             const int rg = rt * ROWS + r, t = rg / p.group;
             return p.out + (((int64_t)was.b * p.new_tokens + t) * p.c.heads * p.group + h * p.group + (rg - t * p.group)) * (int64_t)p.c.dim;
         };
-        constexpr int C4 = DP / 4;                            // 16-byte pieces of a row
-        for (int x = tid; x < rows_here * C4; x += THREADS) {
-            const int r = x / C4, c4 = x % C4, w0 = r / 8;    // row r: warps w0, w0 + UG, ...
-            float2 ml[TG];
-            float top = -INFINITY, tot = 0.f;
 #pragma unroll
-            for (int k = 0; k < TG; ++k) {
-                ml[k] = s_ml[w0 + k * UG][r & 7];
-                top = fmaxf(top, ml[k].x);
-            }
-            const float ref = top == -INFINITY ? 0.f : top;
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < TG; ++k) {
-                const float w = pow2(ml[k].x - ref);
-                const float4 v = *reinterpret_cast<const float4 *>(sums + ((w0 + k * UG) * 8 + (r & 7)) * S::kPad + c4 * 4);
-                tot = fmaf(ml[k].y, w, tot);
-                y.x = fmaf(v.x, w, y.x), y.y = fmaf(v.y, w, y.y), y.z = fmaf(v.z, w, y.z), y.w = fmaf(v.w, w, y.w);
-            }
-            if (whole) {
-                const float inv = inverse(tot);
-                if (c4 * 4 < p.c.dim)
-                    *reinterpret_cast<float4 *>(out_row(r) + c4 * 4) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-                if (p.lse && c4 == 0) p.lse[seg * p.rows + rt * ROWS + r] = log_sum(top, tot);
-            } else {
-                *reinterpret_cast<float4 *>(p.part + (part * ROWS + r) * DP + c4 * 4) = y;
-                if (c4 == 0) *reinterpret_cast<float2 *>(ml_all + (part * ROWS + r) * 2) = make_float2(top, tot);
-            }
+        for (int rp = 0; rp < RP; ++rp) {
+            l[rp] = quad_sum(l[rp]);
+            if (j == 0) s_ml[warp][g + 8 * rp] = make_float2(m[rp], l[rp]);
         }
-        if (!whole) {
-            // CTAs that hold tiles of the segment: those of its first and last tile, and all between
-            const int c0 = (int)(((seg_base + 1ll) * G - 1) / W), c1 = (int)((((long long)seg_base + was.tiles) * G - 1) / W);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                int32_t *cnt = p.cnt + seg * p.row_tiles + rt;
-                s_last = atomicAdd(cnt, 1) == c1 - c0;
-                if (s_last) *cnt = 0;
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                // slot of CTA c: 1 only for the first, if the segment starts inside it
-                const int first = 2 * c0 + (seg_base > (int)((long long)W * c0 / G) ? 1 : 0);
-                auto slot_of = [&](int c) { return (int64_t)(c == c0 ? first : 2 * c); };
-                for (int r = warp; r < rows_here; r += 4) {   // the rows' statistics, CTAs side by side
-                    float top = -INFINITY, tot = 0.f;
-                    for (int c = c0 + lane; c <= c1; c += 32) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(ml_all) + slot_of(c) * ROWS + r);
-                        const float mx = fmaxf(top, ml.x), ref = mx == -INFINITY ? 0.f : mx;
-                        tot = tot * pow2(top - ref) + ml.y * pow2(ml.x - ref);
-                        top = mx;
-                    }
-                    float mx = top;
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    tot *= pow2(top - (mx == -INFINITY ? 0.f : mx));
+        for (int round = 0; round < S::kRounds; ++round) {
+            __syncthreads();
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-                    if (lane == 0) {
-                        s_row_ml[r] = make_float2(mx == -INFINITY ? 0.f : mx, inverse(tot));
-                        if (p.lse) p.lse[seg * p.rows + rt * ROWS + r] = log_sum(mx, tot);
+            for (int rp = 0; rp < RP; ++rp)
+                if (row0 + 8 * rp < p.rows) {
+                    float *mine = sums + (warp * 8 * RP + g + 8 * rp) * S::kPad + 2 * j;
+#pragma unroll
+                    for (int x = 0; x < DT / S::kRounds; ++x) {
+                        const int dt = round * (DT / S::kRounds) + x;
+                        *reinterpret_cast<float2 *>(mine + x * 8) = make_float2(o[dt][rp][0], o[dt][rp][1]);
                     }
                 }
-                __syncthreads();
-                // the sums: with few rows, groups of threads take every ways-th CTA each and join in shared memory
-                const int items = rows_here * C4, ways = items <= THREADS / 4 ? 4 : items <= THREADS / 2 ? 2 : 1;
-                const int per = THREADS / ways;
-                for (int x0 = 0; x0 < items; x0 += per) {
-                    const int x = x0 + tid % per, way = tid / per, r = x / C4, c4 = x % C4;
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float2 st = make_float2(0.f, 0.f);
-                    if (x < items) {
-                        st = s_row_ml[r];
-#pragma unroll 8
-                        for (int c = c0 + way; c <= c1; c += ways) {
-                            const int64_t sl = slot_of(c) * ROWS + r;
-                            const float w = pow2(__ldcg(ml_all + sl * 2) - st.x);
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * DP) + c4);
-                            y.x = fmaf(v.x, w, y.x), y.y = fmaf(v.y, w, y.y), y.z = fmaf(v.z, w, y.z), y.w = fmaf(v.w, w, y.w);
-                        }
-                    }
-                    if (ways > 1) {
-                        float4 *way_sums = reinterpret_cast<float4 *>(sums);
-                        way_sums[tid] = y;
-                        __syncthreads();
-                        if (way == 0)
-                            for (int k = 1; k < ways; ++k) {
-                                const float4 v = way_sums[tid + k * per];
-                                y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
-                            }
-                    }
-                    if (way == 0 && x < items && c4 * 4 < p.c.dim)
-                        *reinterpret_cast<float4 *>(out_row(r) + c4 * 4) = make_float4(y.x * st.y, y.y * st.y, y.z * st.y, y.w * st.y);
+            __syncthreads();
+            constexpr int C4 = S::kCols / 4;                  // 16-byte pieces of a row
+            for (int x = tid; x < rows_here * C4; x += THREADS) {
+                const int r = x / C4, c4 = x % C4, w0 = r / (8 * RP), rw = r % (8 * RP);      // row r: warps w0, w0 + UG, ...
+                const int col = round * S::kCols + c4 * 4;
+                float2 ml[TG];
+                float top = -INFINITY, tot = 0.f;
+#pragma unroll
+                for (int k = 0; k < TG; ++k) {
+                    ml[k] = s_ml[w0 + k * UG][rw];
+                    top = fmaxf(top, ml[k].x);
+                }
+                const float ref = top == -INFINITY ? 0.f : top;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < TG; ++k) {
+                    const float w = pow2(ml[k].x - ref);
+                    const float4 v = *reinterpret_cast<const float4 *>(sums + ((w0 + k * UG) * 8 * RP + rw) * S::kPad + c4 * 4);
+                    tot = fmaf(ml[k].y, w, tot);
+                    y.x = fmaf(v.x, w, y.x), y.y = fmaf(v.y, w, y.y), y.z = fmaf(v.z, w, y.z), y.w = fmaf(v.w, w, y.w);
+                }
+                if (whole) {
+                    const float inv = inverse(tot);
+                    if (col < p.c.dim)
+                        *reinterpret_cast<float4 *>(out_row(r) + col) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+                    if (p.lse && col == 0) p.lse[seg * p.rows + rt * ROWS + r] = log_sum<T>(top, tot);
+                } else {
+                    *reinterpret_cast<float4 *>(p.part + (part * ROWS + r) * DP + col) = y;
+                    if (col == 0) *reinterpret_cast<float2 *>(ml_all + (part * ROWS + r) * 2) = make_float2(top, tot);
                 }
             }
         }
+        // The CTA with the segment's first tile says which CTAs hold parts of it: itself up to the one of the last
+        // tile (itself alone, and no part, if it holds all)
+        if (seg_base >= u0 && tid == 0)
+            p.parts[seg * p.row_tiles + rt] =
+                make_int3((int)part, (int)blockIdx.x, whole ? -1 : (int)((((long long)seg_base + was.tiles) * G - 1) / W));
         seg_base = u0 + i + 1;
     }
 }
 
-// weight[entry] += sum over the rows of 2^(score - log-sum): one thread per
-// entry reads its rows' saved scores (coalesced along the entries).
-__global__ void __launch_bounds__(256) attn_weight_kernel(const AttnParams p)
+// The second launch.  Blocks 0 .. seqs*heads*rows - 1 join the parts of one row
+// each, if it has any: groups of dim/4 threads take every ways-th part, four
+// in flight, with a running maximum, and meet in shared memory.  The blocks
+// after them (weights wanted) take WEIGHTS entries of a (sequence, head) each:
+// weight[entry] += sum over the rows of 2^(score - log-sum), the scores read
+// side by side along the entries, the log-sums of split rows from their parts.
+constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_WEIGHTS = 1024;
+constexpr int JOIN_ROWS = 2048;      // most rows of a key-value head
+
+template <typename T>
+__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int dp, int kept_rows, int grid, int64_t join_blocks,
+                                                                 int chunks)
 {
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int len = cache_len(p.c, b, KID_ATTN), slot = blockIdx.x * 256 + threadIdx.x;
-    if (slot >= len) return;
-    const int64_t seg = (int64_t)b * p.c.heads + h;
-    const float *s = p.scores + seg * p.rows * p.cap + slot, *lse = p.lse + seg * p.rows;
-    float w = 0.f;
+    using namespace attn;
+    __shared__ __align__(16) float4 s_y[JOIN_THREADS];
+    __shared__ float2 s_ml[JOIN_THREADS];
+    __shared__ float s_lse[JOIN_ROWS];
+    const int tid = threadIdx.x;
+    const float2 *ml_all = reinterpret_cast<const float2 *>(p.part + 2 * (int64_t)grid * kept_rows * dp);
+    pdl_wait();
+    if (blockIdx.x < join_blocks) {
+        const int64_t seg = blockIdx.x / p.rows;
+        const int r = (int)(blockIdx.x - seg * p.rows), rt = r / kept_rows, rr = r - rt * kept_rows;
+        const int3 at = p.parts[seg * p.row_tiles + rt];
+        if (at.z < 0) return;
+        const int per = dp / 4, ways = JOIN_THREADS / per, way = tid / per, col = (tid - way * per) * 4;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        float top = -INFINITY, tot = 0.f;
+        for (int c = at.y + way; c <= at.z; c += ways * 4) {
+            float2 ml[4];
+            float4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {                     // past the end: the last part again, without weight
+                const int cc = min(c + k * ways, at.z);
+                const int64_t sl = (int64_t)(cc == at.y ? at.x : 2 * cc) * kept_rows + rr;
+                ml[k] = __ldcg(ml_all + sl);
+                v[k] = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * dp + col));
+            }
+            const float mx = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
+            const float ref = mx == -INFINITY ? 0.f : mx, old = pow2(top - ref);
+            top = mx;
+            tot *= old;
+            y.x *= old, y.y *= old, y.z *= old, y.w *= old;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float w = c + k * ways <= at.z ? pow2(ml[k].x - ref) : 0.f;
+                if (w == 0.f) continue;                       // a part that saw nothing adds nothing
+                tot = fmaf(ml[k].y, w, tot);
+                y.x = fmaf(v[k].x, w, y.x), y.y = fmaf(v[k].y, w, y.y), y.z = fmaf(v[k].z, w, y.z), y.w = fmaf(v[k].w, w, y.w);
+            }
+        }
+        s_y[tid] = y;
+        s_ml[tid] = make_float2(top, tot);
+        __syncthreads();
+        if (way > 0 || col >= p.c.dim) return;
+        for (int k = 1; k < ways; ++k) top = fmaxf(top, s_ml[tid + k * per].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        tot = 0.f;
+        y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < ways; ++k) {
+            const float2 ml = s_ml[tid + k * per];
+            const float4 v = s_y[tid + k * per];
+            const float w = pow2(ml.x - ref);
+            tot = fmaf(ml.y, w, tot);
+            y.x = fmaf(v.x, w, y.x), y.y = fmaf(v.y, w, y.y), y.z = fmaf(v.z, w, y.z), y.w = fmaf(v.w, w, y.w);
+        }
+        const float inv = inverse(tot);
+        const int64_t b = seg / p.c.heads, h = seg - b * p.c.heads;
+        const int t = r / p.group;
+        *reinterpret_cast<float4 *>(p.out + ((b * p.new_tokens + t) * p.c.heads * p.group + h * p.group + (r - t * p.group)) * p.c.dim + col) =
+            make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+        return;
+    }
+    const int64_t x = blockIdx.x - join_blocks, seg = x / chunks;
+    const int b = (int)(seg / p.c.heads), h = (int)(seg - (int64_t)b * p.c.heads);
+    const int len = cache_len(p.c, b, KID_ATTN), first = (int)(x - seg * chunks) * JOIN_WEIGHTS;
+    if (first >= len) return;
+    for (int r = tid / 32; r < p.rows; r += JOIN_THREADS / 32) {          // a warp per row's log-sum
+        const int rt = r / kept_rows, rr = r - rt * kept_rows, lane = tid & 31;
+        const int3 at = p.parts[seg * p.row_tiles + rt];
+        float lse = 0.f;
+        if (at.z < 0) {
+            lse = __ldcg(p.lse + seg * p.rows + r);
+        } else {
+            float top = -INFINITY, tot = 0.f;
+            for (int c = at.y + lane; c <= at.z; c += 32) {
+                const float2 ml = __ldcg(ml_all + (int64_t)(c == at.y ? at.x : 2 * c) * kept_rows + rr);
+                const float mx = fmaxf(top, ml.x), ref = mx == -INFINITY ? 0.f : mx;
+                tot = tot * pow2(top - ref) + ml.y * pow2(ml.x - ref);
+                top = mx;
+            }
+            float mx = top;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            tot *= pow2(top - (mx == -INFINITY ? 0.f : mx));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+            lse = log_sum<T>(mx, tot);
+        }
+        if (lane == 0) s_lse[r] = lse;
+    }
+    __syncthreads();
+    const float *s = p.scores + seg * p.rows * p.cap;
+    for (int slot = first + tid; slot < min(len, first + JOIN_WEIGHTS); slot += JOIN_THREADS) {
+        float w = 0.f;
 #pragma unroll 4
-    for (int r = 0; r < p.rows; ++r) w += attn::pow2(__ldg(s + r * p.cap) - __ldg(lse + r));
-    const int col = p.page_div.of(slot), pg = cache_page(p.c, b, col, KID_ATTN);
-    if (pg < 0) return;
-    p.c.weight[((int64_t)pg * p.c.heads + h) * p.c.page_size + (slot - col * p.c.page_size)] += w;
+        for (int r = 0; r < p.rows; ++r) w += pow2(__ldcg(s + r * p.cap + slot) - s_lse[r]);
+        const int c = p.page_div.of(slot), pg = cache_page(p.c, b, c, KID_ATTN);
+        if (pg < 0) continue;
+        p.c.weight[((int64_t)pg * p.c.heads + h) * p.c.page_size + (slot - c * p.c.page_size)] += w;
+    }
 }
 
+// Which kernel: dim padded, rows per quad and warps along the rows.  Up to
+// eight rows, two parts share an operand; up to 16, 32 and 64 rows, one, two
+// and four warps take sixteen each, the remaining warps split the entries; for
+// heads above 128 sixteen rows do not fit the registers, and warps take eight.
+// More rows than a CTA takes are dealt to further CTAs, which read the cache
+// again (from L2).
 struct AttnPlan {
-    int dp, ug, rows, row_tiles, grid;
-    int64_t tiles, cap, part_floats, score_floats, lse_floats, counters;
+    int dp, rp, ug, rows, kept_rows, row_tiles, grid;
+    int64_t tiles, cap, part_floats, score_floats, lse_floats, parts;
 };
+
+template <typename F>
+auto attn_dispatch(int dp, int rp, int ug, F f)
+{
+    using std::integral_constant;
+    const auto with_ug = [&](auto DPc, auto RPc) {
+        return ug == 1   ? f(DPc, RPc, integral_constant<int, 1>())
+               : ug == 2 ? f(DPc, RPc, integral_constant<int, 2>())
+                         : f(DPc, RPc, integral_constant<int, 4>());
+    };
+    if (dp == 256) return with_ug(integral_constant<int, 256>(), integral_constant<int, 1>());
+    if (rp == 1)
+        return dp == 64 ? f(integral_constant<int, 64>(), integral_constant<int, 1>(), integral_constant<int, 1>())
+                        : f(integral_constant<int, 128>(), integral_constant<int, 1>(), integral_constant<int, 1>());
+    return dp == 64 ? with_ug(integral_constant<int, 64>(), integral_constant<int, 2>())
+                    : with_ug(integral_constant<int, 128>(), integral_constant<int, 2>());
+}
 
 inline AttnPlan attn_plan(const mmq_kv_cache &c, int q_heads, int new_tokens, bool save)
 {
     AttnPlan a;
     a.dp = c.dim <= 64 ? 64 : c.dim <= 128 ? 128 : 256;
     a.rows = q_heads / c.heads * new_tokens;
-    // warps along the rows: as few as cover them, so that the others split the entries
-    a.ug = a.rows <= 8 ? 1 : a.rows <= 16 ? 2 : 4;
-    a.row_tiles = (a.rows + 8 * a.ug - 1) / (8 * a.ug);
-    const int tile = a.dp == 64 ? 128 : 64;
+    a.rp = a.rows > 8 && a.dp <= 128 ? 2 : 1;
+    a.ug = a.rows <= 8 * a.rp ? 1 : a.rows <= 16 * a.rp ? 2 : 4;
+    const int rows = a.kept_rows = 8 * a.rp * a.ug;                      // per CTA
+    int tile = 0, per_sm = 0;
+    attn_dispatch(a.dp, a.rp, a.ug, [&](auto DPc, auto RPc, auto UGc) {
+        using S = attn::Shape<DPc.value, RPc.value, UGc.value>;
+        tile = S::kTile;
+        per_sm = S::kPerSm;
+        return 0;
+    });
+    a.row_tiles = (a.rows + rows - 1) / rows;
     a.tiles = ((int64_t)c.cols * c.page_size + tile - 1) / tile * c.seqs * c.heads * a.row_tiles;
-    const int64_t full = (int64_t)sm_count() * (a.dp <= 128 ? 2 : 1);     // every CTA resident
+    const int64_t full = (int64_t)sm_count() * per_sm;                   // every CTA resident
     a.grid = (int)(a.tiles < full ? a.tiles : full);
     a.cap = ((int64_t)c.cols * c.page_size + 127) / 128 * 128;
-    a.part_floats = 2 * (int64_t)a.grid * 8 * a.ug * (a.dp + 2);
+    a.part_floats = 2 * (int64_t)a.grid * rows * (a.dp + 2);
     a.score_floats = save ? (int64_t)c.seqs * c.heads * a.rows * a.cap : 0;
     a.lse_floats = save ? (int64_t)c.seqs * c.heads * a.rows : 0;
-    a.counters = (int64_t)c.seqs * c.heads * a.row_tiles;
+    a.parts = (int64_t)c.seqs * c.heads * a.row_tiles;
     return a;
 }
 
@@ -633,15 +778,17 @@ inline int attn_check(const mmq_kv_cache *c, int q_heads, int new_tokens)
 {
     const int rc = check_cache(c);
     if (rc != MMQ_OK) return rc;
-    if (q_heads < 1 || q_heads > 65535 || q_heads % c->heads || new_tokens < 1 || new_tokens > 16) return MMQ_ERR_SHAPE;
+    if (q_heads < 1 || q_heads > 65535 || q_heads % c->heads || q_heads / c->heads > 128 || new_tokens < 1 ||
+        new_tokens > 16)
+        return MMQ_ERR_SHAPE;
     return MMQ_OK;
 }
 
-template <int DP, typename T, int UG>
+template <int DP, typename T, int RP, int UG>
 int launch_attn(const AttnParams &p, int grid, cudaStream_t stream)
 {
-    const auto kernel = attn_kernel<DP, T, UG>;
-    constexpr int smem = attn::Shape<DP>::kSmem;
+    const auto kernel = attn_kernel<DP, T, RP, UG>;
+    constexpr int smem = attn::Shape<DP, RP, UG>::kSmem;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
@@ -657,53 +804,40 @@ int launch_attn(const AttnParams &p, int grid, cudaStream_t stream)
     return launch_status();
 }
 
-template <int DP, typename T>
-int launch_attn_ug(const AttnParams &p, const AttnPlan &a, cudaStream_t s)
-{
-    return a.ug == 1   ? launch_attn<DP, T, 1>(p, a.grid, s)
-           : a.ug == 2 ? launch_attn<DP, T, 2>(p, a.grid, s)
-                       : launch_attn<DP, T, 4>(p, a.grid, s);
-}
-template <typename T>
-int launch_attn_dp(const AttnParams &p, const AttnPlan &a, cudaStream_t s)
-{
-    return a.dp == 64    ? launch_attn_ug<64, T>(p, a, s)
-           : a.dp == 128 ? launch_attn_ug<128, T>(p, a, s)
-                         : launch_attn_ug<256, T>(p, a, s);
-}
-
 }  // namespace
 }  // namespace mmq
 
 extern "C" int mmq_attn_sizes(const mmq_kv_cache *cache, int q_heads, int new_tokens, int accumulate,
-                              int64_t *work_floats, int64_t *n_counters)
+                              int64_t *work_floats)
 {
     using namespace mmq;
     const int rc = attn_check(cache, q_heads, new_tokens);
     if (rc != MMQ_OK) return rc;
-    if (!work_floats || !n_counters) return MMQ_ERR_NULL;
+    if (!work_floats) return MMQ_ERR_NULL;
     const AttnPlan a = attn_plan(*cache, q_heads, new_tokens, accumulate != 0);
     if (a.tiles > 0x7fffffff) return MMQ_ERR_SHAPE;
-    *work_floats = a.part_floats + a.score_floats + a.lse_floats;
-    *n_counters = a.counters;
+    *work_floats = a.part_floats + a.score_floats + a.lse_floats + 3 * a.parts;
     return MMQ_OK;
 }
 
 extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_t ldq, const int32_t *new_len,
                                float *out, int q_heads, int new_tokens, float scale, int accumulate, float *work,
-                               int32_t *counters, mmq_stream_t stream)
+                               mmq_stream_t stream)
 {
     using namespace mmq;
     int rc = attn_check(cache, q_heads, new_tokens);
     if (rc != MMQ_OK) return rc;
     if (ldq < (int64_t)q_heads * cache->dim || !(scale - scale == 0.f)) return MMQ_ERR_SHAPE;
     if (cache->seqs == 0) return MMQ_OK;
-    if (!q || !out || !work || !counters || (accumulate && !cache->weight)) return MMQ_ERR_NULL;
+    if (!q || !out || !work || (accumulate && !cache->weight)) return MMQ_ERR_NULL;
     if (!aligned16(q) || (ldq & 3) || !aligned16(out) || !aligned16(work)) return MMQ_ERR_ALIGN;
     if ((rc = check_arch()) != MMQ_OK) return rc;
     const bool save = accumulate != 0;
     const AttnPlan a = attn_plan(*cache, q_heads, new_tokens, save);
-    if (a.tiles > 0x7fffffff) return MMQ_ERR_SHAPE;       // tiles are counted in an int
+    // tiles are counted in an int, and so are the second launch's blocks
+    if (a.tiles > 0x7fffffff ||
+        (int64_t)cache->seqs * cache->heads * (a.rows + (save ? (a.cap + JOIN_WEIGHTS - 1) / JOIN_WEIGHTS : 0)) > 0x7fffffff)
+        return MMQ_ERR_SHAPE;
     AttnParams p;
     p.c = *cache;
     p.q = q;
@@ -718,13 +852,27 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     p.scores = work;                                   // rows of a multiple of 128 floats: 16-byte aligned
     p.part = work + a.score_floats;
     p.lse = save ? p.part + a.part_floats : nullptr;
-    p.cnt = counters;
+    p.parts = reinterpret_cast<int3 *>(p.part + a.part_floats + a.lse_floats);
     p.cap = a.cap;
     p.page_div = FastDiv(cache->page_size);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    rc = cache->dtype == MMQ_F16 ? launch_attn_dp<__half>(p, a, s) : launch_attn_dp<__nv_bfloat16>(p, a, s);
-    if (rc != MMQ_OK || !save) return rc;
-    const dim3 grid((unsigned)(a.cap / 128 + 1) / 2, (unsigned)cache->heads, (unsigned)cache->seqs);
-    attn_weight_kernel<<<grid, 256, 0, s>>>(p);
+    rc = attn_dispatch(a.dp, a.rp, a.ug, [&](auto DPc, auto RPc, auto UGc) {
+        return cache->dtype == MMQ_F16 ? launch_attn<DPc.value, __half, RPc.value, UGc.value>(p, a.grid, s)
+                                       : launch_attn<DPc.value, __nv_bfloat16, RPc.value, UGc.value>(p, a.grid, s);
+    });
+    if (rc != MMQ_OK) return rc;
+    const int64_t segs = (int64_t)cache->seqs * cache->heads, join_blocks = segs * a.rows;
+    const int chunks = save ? (int)((a.cap + JOIN_WEIGHTS - 1) / JOIN_WEIGHTS) : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(join_blocks + segs * chunks));
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;     // its blocks start as the first launch's leave
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const auto join = cache->dtype == MMQ_F16 ? attn_join_kernel<__half> : attn_join_kernel<__nv_bfloat16>;
+    if (cudaLaunchKernelEx(&cfg, join, p, a.dp, a.kept_rows, a.grid, join_blocks, chunks) != cudaSuccess) return launch_status();
     return launch_status();
 }

@@ -522,29 +522,27 @@ def rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tenso
 
 
 class AttnWorkspace:
-    """Caller-owned scratch of attn_decode: partial sums (and saved scores where weights
-    are accumulated) and segment counters, which start at zero and are left at zero.  Calls
-    that share one must be ordered (one stream)."""
+    """Caller-owned scratch of attn_decode: the parts of split rows (and the scores where
+    weights are accumulated).  Calls that share one must be ordered (one stream)."""
 
-    def __init__(self, device, floats: int, counters: int):
+    def __init__(self, device, floats: int):
         self.work = torch.empty(max(4, floats), dtype=torch.float32, device=device)
-        self.counters = torch.zeros(max(1, counters), dtype=torch.int32, device=device)
 
-    def fits(self, floats: int, counters: int) -> bool:
-        return floats <= self.work.numel() and counters <= self.counters.numel()
+    def fits(self, floats: int) -> bool:
+        return floats <= self.work.numel()
 
 
-def attn_sizes(cache: KVCache, q_heads: int, new_tokens: int = 1, accumulate: bool = False) -> tuple[int, int]:
-    """(floats, counters) of attn_decode's workspace."""
-    nf, nc = ctypes.c_int64(0), ctypes.c_int64(0)
+def attn_sizes(cache: KVCache, q_heads: int, new_tokens: int = 1, accumulate: bool = False) -> int:
+    """Floats of attn_decode's workspace."""
+    nf = ctypes.c_int64(0)
     with torch.cuda.device(cache.device):
-        st = load().mmq_attn_sizes(cache._ref, q_heads, new_tokens, int(accumulate), ctypes.byref(nf), ctypes.byref(nc))
+        st = load().mmq_attn_sizes(cache._ref, q_heads, new_tokens, int(accumulate), ctypes.byref(nf))
     _check("mmq_attn_sizes", st)
-    return nf.value, nc.value
+    return nf.value
 
 
 def attn_workspace(cache: KVCache, q_heads: int, new_tokens: int = 1, accumulate: bool = False) -> AttnWorkspace:
-    return AttnWorkspace(cache.device, *attn_sizes(cache, q_heads, new_tokens, accumulate))
+    return AttnWorkspace(cache.device, attn_sizes(cache, q_heads, new_tokens, accumulate))
 
 
 def attn_decode(cache: KVCache, q: torch.Tensor, scale: float | None = None, new: torch.Tensor | None = None,
@@ -575,14 +573,14 @@ def attn_decode(cache: KVCache, q: torch.Tensor, scale: float | None = None, new
     else:
         _need(out, "out", torch.float32, (rows, q_heads, dim), dev)
     key = (q_heads, n, accumulate)
-    sizes = cache._work.get(key)
-    if sizes is None:
-        sizes = cache._work[key] = attn_sizes(cache, q_heads, n, accumulate)
-    if workspace is None or not workspace.fits(*sizes):
-        workspace = AttnWorkspace(dev, *sizes)
+    floats = cache._work.get(key)
+    if floats is None:
+        floats = cache._work[key] = attn_sizes(cache, q_heads, n, accumulate)
+    if workspace is None or not workspace.fits(floats):
+        workspace = AttnWorkspace(dev, floats)
     st = _on(dev, load().mmq_attn_decode, cache._ref, q.data_ptr(), ldq, new.data_ptr() if new is not None else None,
              out.data_ptr(), q_heads, n, dim ** -0.5 if scale is None else scale, int(accumulate),
-             workspace.work.data_ptr(), workspace.counters.data_ptr())
+             workspace.work.data_ptr())
     if st != 0:
         raise MMQError("mmq_attn_decode", st)
     return out

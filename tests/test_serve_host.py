@@ -44,7 +44,7 @@ def test_bad_caches(a, kw, status):
     lib = _lib.load()
     c, p, n = a.cache(**kw), a.p, a.null
     assert lib.mmq_rope_append(c, p, 64, 1.0, 0, p, 256, p, 128, p, 128, p, n, p, 256, 4, 1, n) == status
-    assert lib.mmq_attn_decode(c, p, 4 * 512, n, p, 4, 1, 0.1, 0, p, p, n) == status
+    assert lib.mmq_attn_decode(c, p, 4 * 512, n, p, 4, 1, 0.1, 0, p, n) == status
     assert lib.mmq_kv_evict(c, 4, p, a.odd, a.odd, p, n) == status
 
 
@@ -65,21 +65,22 @@ def test_rope_refusals(a):
 @needs_lib
 def test_attn_refusals(a):
     lib, c, p, n = _lib.load(), a.cache(), a.p, a.null
-    call = lambda q=p, ldq=256, out=p, qh=4, new=1, scale=0.1, acc=0, work=p, cnt=p, cache=c: lib.mmq_attn_decode(  # noqa: E731
-        cache, q, ldq, n, out, qh, new, scale, acc, work, cnt, n)
+    call = lambda q=p, ldq=256, out=p, qh=4, new=1, scale=0.1, acc=0, work=p, cache=c: lib.mmq_attn_decode(  # noqa: E731
+        cache, q, ldq, n, out, qh, new, scale, acc, work, n)
     assert call(qh=3) == -1 and call(qh=0) == -1 and call(new=0) == -1 and call(new=17) == -1 and call(ldq=255) == -1
     assert call(scale=float("nan")) == -1 and call(scale=float("inf")) == -1
-    assert call(q=n) == -6 and call(out=n) == -6 and call(work=n) == -6 and call(cnt=n) == -6
+    assert call(q=n) == -6 and call(out=n) == -6 and call(work=n) == -6
     assert call(acc=1, cache=a.cache(weight=None)) == -6
     assert call(q=a.odd) == -2 and call(ldq=258) == -2 and call(work=a.odd) == -2
     assert call(cache=a.cache(seqs=0)) == 0
-    nf, nc = ctypes.c_int64(), ctypes.c_int64()
-    assert lib.mmq_attn_sizes(c, 4, 1, 0, ctypes.byref(nf), None) == -6
-    assert lib.mmq_attn_sizes(c, 5, 1, 0, ctypes.byref(nf), ctypes.byref(nc)) == -1
-    assert lib.mmq_attn_sizes(c, 4, 1, 0, ctypes.byref(nf), ctypes.byref(nc)) == 0
+    nf = ctypes.c_int64()
+    assert lib.mmq_attn_sizes(c, 4, 1, 0, None) == -6
+    assert lib.mmq_attn_sizes(c, 5, 1, 0, ctypes.byref(nf)) == -1
+    assert lib.mmq_attn_sizes(c, 258, 1, 0, ctypes.byref(nf)) == -1       # 129 query heads for each
+    assert lib.mmq_attn_sizes(c, 4, 1, 0, ctypes.byref(nf)) == 0
     plain = nf.value
-    assert plain > 0 and nc.value == 2
-    assert lib.mmq_attn_sizes(c, 4, 1, 1, ctypes.byref(nf), ctypes.byref(nc)) == 0
+    assert plain > 0
+    assert lib.mmq_attn_sizes(c, 4, 1, 1, ctypes.byref(nf)) == 0
     assert nf.value >= plain + 2 * 2 * 128                     # a score for every row and slot besides
 
 
@@ -94,7 +95,7 @@ def test_evict_refusals(a):
     assert call(cache=a.cache(seqs=0)) == 0
     ni = ctypes.c_int64()
     assert lib.mmq_evict_sizes(a.cache(), 0, ctypes.byref(ni)) == -1
-    assert lib.mmq_evict_sizes(a.cache(), 100, ctypes.byref(ni)) == 0 and ni.value >= 2 * (1 + 2 * 28)
+    assert lib.mmq_evict_sizes(a.cache(), 100, ctypes.byref(ni)) == 0 and ni.value >= 2 * 2 * 28
 
 
 @needs_lib

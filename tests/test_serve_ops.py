@@ -168,7 +168,6 @@ def check_attention(ops, lens, N, Hq, H, dim, page, dtype, layout="hnd", new=Non
     out = ops.attn_decode(cache, q.cuda(), scale=scale, new=newt, accumulate=accumulate, workspace=ws)
     again = None if accumulate else ops.attn_decode(cache, q.cuda(), scale=scale, new=newt, workspace=ws)
     ops.check_status()
-    assert int(ws.counters.abs().sum()) == 0
     tab = cache.table.cpu()
     kp, vp = cache.k.cpu(), cache.v.cpu()
     sc = dim ** -0.5 if scale is None else scale
