@@ -26,18 +26,19 @@
 //
 // Products run on the warp-level tensor core (16-row operand), with q and p
 // split into parts of the cache's type that add up to 22 bits (f16, two parts)
-// or 24 (bf16, three); K and V are used as they are.  Up to eight rows
-// (RP = 1): the operand's upper eight rows hold the first part, the lower eight
-// the second, and the two halves of the result are added; bf16's third part
-// takes a second product.  More rows (RP = 2): sixteen rows per operand, one
-// product per part.  q is scaled by a power of two per row to lie below 2, and
+// or 24 (bf16, three); K and V are used as they are.  The parts of few rows
+// share one operand, and the result's parts are added: up to four rows of bf16
+// (MODE 0), rows 0-3 hold the first parts, 4-7 the second, 8-11 the third; up
+// to eight rows (MODE 1), the upper eight hold the first part, the lower eight
+// the second, and bf16's third takes a second product.  More rows (MODE 2):
+// sixteen rows per operand, one product per part.  q is scaled by a power of two per row to lie below 2, and
 // for f16 p carries 2^15, so that f16's range does not clip either.  The sums
 // over a tile's entries stay in f32 and are added to the running sums with f32
 // FMAs.
 //
-// UG warps of the four take 8*RP rows each over the same entries and 4/UG
+// UG warps of the four take these rows each over the same entries and 4/UG
 // warps split a tile's entries (with their own running maximum, joined at the
-// segment's end), so that up to 8*RP*UG rows share one read of the cache.
+// segment's end), so that up to 64 rows share one read of the cache.
 #pragma once
 
 #include <type_traits>
@@ -53,23 +54,28 @@ constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
 template <typename T>
 constexpr float kExp = kBf16<T> ? 0.f : 15.f;      // p carries 2^kExp
 
-// DP: dim padded to 64, 128 or 256; RP, UG: see above
-template <int DP, int RP, int UG>
+// DP: dim padded to 64, 128 or 256; MODE, UG: see above
+template <int DP, int MODE, int UG>
 struct Shape {
+    static constexpr int kPerWarp = MODE == 0 ? 4 : MODE == 1 ? 8 : 16;   // rows
     static constexpr int kTile = DP == 64 ? 128 : 64;                 // entries per tile
     static constexpr int kStages = 3;                                 // tiles in the ring
     static constexpr int kPerSm = DP <= 128 ? 2 : 1;                  // CTAs resident per SM
     static constexpr int kHalf = kTile * DP * 2;                      // bytes of K (or V) per stage
     static constexpr int kSmem = kStages * 2 * kHalf;
-    static constexpr int kRows = 8 * RP * UG;                         // rows per CTA
+    static constexpr int kRows = kPerWarp * UG;                       // rows per CTA
     // the four warps' sums are joined in one stage's memory, in as many rounds of columns as fit
-    static constexpr int fit(int rounds) { return 4 * 8 * RP * (DP / rounds + 8) * 4 <= 2 * kHalf ? rounds : fit(rounds * 2); }
+    static constexpr int fit(int rounds) { return 4 * kPerWarp * (DP / rounds + 8) * 4 <= 2 * kHalf ? rounds : fit(rounds * 2); }
     static constexpr int kRounds = fit(1);
     static constexpr int kCols = DP / kRounds;
     static constexpr int kPad = kCols + 8;                            // floats per row there: no bank conflicts
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there)
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool there)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
@@ -207,13 +213,14 @@ __device__ __forceinline__ void attn_advance(const AttnParams &p, AttnCursor &u)
     u.tiles = attn_tiles<TILE>(u.len);
 }
 
-template <int DP, typename T, int RP, int UG>
-__global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm) attn_kernel(const AttnParams p)
+template <int DP, typename T, int MODE, int UG>
+__global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPerSm) attn_kernel(const AttnParams p)
 {
     using namespace attn;
-    using S = Shape<DP, RP, UG>;
+    using S = Shape<DP, MODE, UG>;
     constexpr bool BF = kBf16<T>;
-    constexpr int PARTS = RP == 1 ? (BF ? 2 : 1) : (BF ? 3 : 2);     // products per tensor-core step
+    constexpr int RP = MODE == 2 ? 2 : 1;                            // rows per quad of lanes
+    constexpr int PARTS = MODE == 0 ? 1 : MODE == 1 ? (BF ? 2 : 1) : (BF ? 3 : 2);     // products per tensor-core step
     constexpr int TILE = S::kTile, STAGES = S::kStages, TG = 4 / UG, TW = TILE / TG;    // TW: entries per warp and tile
     constexpr int NT = TW / 8, KS = DP / 16, DT = DP / 8, ROWS = S::kRows;
     constexpr int CPR = DP / 8, RPP = THREADS / CPR, PASSES = TILE / RPP;   // 16-byte copies per row, rows per pass
@@ -221,12 +228,14 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
     pdl_launch_dependents();       // the joining launch may start; it waits for this grid's end before it reads
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ ulonglong2 s_row[STAGES][TILE];
-    __shared__ float2 s_ml[4][8 * RP];         // (max, sum) of every warp's rows
+    __shared__ float2 s_ml[4][S::kPerWarp];         // (max, sum) of every warp's rows
     const uint32_t ring = smem_u32(smem);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ug = warp % UG, tg = warp / UG;
     const int g = lane >> 2, j = lane & 3;
+    const int gr = MODE == 0 ? g & 3 : g;                     // the quad's (first) row in the warp
+    const bool holds = MODE != 0 || g < 4;                    // MODE 0: quads 4-7 compute the rows of 0-3 again
     const int hrs = p.c.heads * p.row_tiles;
 
     // ---- this CTA's tiles [u0, u1) of all W: every warp for itself, 32 sequences at a time
@@ -267,18 +276,20 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
     int seg_base = u0 - cur.tile;                             // first tile of the segment at `cur`
     AttnCursor inf = cur;                                     // next tile to look up
 
-    // addresses of K and V of entry `tid` of the tile at `inf`; 0 if there is none
+    // addresses of K and V of entry `tid` of the tile at `inf`; 0 past the length (an entry with a bad page, which is
+    // reported, reads the pool's first row)
     auto look_up = [&](bool there) {
         ulonglong2 r = make_ulonglong2(0, 0);
         if (there) {
             const int slot = inf.tile * TILE + tid;
             if (tid < TILE && slot < inf.len) {
-                const int col = p.page_div.of(slot), off = slot - col * p.c.page_size;
-                const int64_t pg = cache_page(p.c, inf.b, col, KID_ATTN);
-                if (pg >= 0)
-                    r = make_ulonglong2(
-                        (unsigned long long)(static_cast<const T *>(p.c.k) + pg * p.c.k_page + inf.h * p.c.k_head + off * p.c.k_slot),
-                        (unsigned long long)(static_cast<const T *>(p.c.v) + pg * p.c.v_page + inf.h * p.c.v_head + off * p.c.v_slot));
+                const int col = p.page_div.of(slot);
+                int off = slot - col * p.c.page_size;
+                int64_t pg = cache_page(p.c, inf.b, col, KID_ATTN);
+                if (pg < 0) pg = off = 0;
+                r = make_ulonglong2(
+                    (unsigned long long)(static_cast<const T *>(p.c.k) + pg * p.c.k_page + inf.h * p.c.k_head + off * p.c.k_slot),
+                    (unsigned long long)(static_cast<const T *>(p.c.v) + pg * p.c.v_page + inf.h * p.c.v_head + off * p.c.v_slot));
             }
             attn_advance<TILE>(p, inf);
         }
@@ -290,13 +301,23 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
     auto copy = [&](int stage) {
         const uint32_t base = ring + stage * 2 * S::kHalf + cr * (DP * 2);
         const ulonglong2 *rows = s_row[stage] + cr;
+        if (piece && s_row[stage][TILE - 1].x != 0) {         // a whole tile: its last entry is there
 #pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const ulonglong2 w = rows[i * RPP];
+                const uint32_t dst = base + i * RPP * (DP * 2) + ((cc ^ ((cr + i * RPP) & 7)) << 4);
+                cp16(dst, reinterpret_cast<const uint8_t *>(w.x) + cc * 16);
+                cp16(dst + S::kHalf, reinterpret_cast<const uint8_t *>(w.y) + cc * 16);
+            }
+            return;
+        }
+#pragma unroll 1
         for (int i = 0; i < PASSES; ++i) {
             const ulonglong2 w = rows[i * RPP];
             const bool there = w.x != 0 && piece;
             const uint32_t dst = base + i * RPP * (DP * 2) + ((cc ^ ((cr + i * RPP) & 7)) << 4);
-            cp16(dst, there ? reinterpret_cast<const uint8_t *>(w.x) + cc * 16 : p.c.k, there);
-            cp16(dst + S::kHalf, there ? reinterpret_cast<const uint8_t *>(w.y) + cc * 16 : p.c.v, there);
+            cp16_or_zero(dst, there ? reinterpret_cast<const uint8_t *>(w.x) + cc * 16 : p.c.k, there);
+            cp16_or_zero(dst + S::kHalf, there ? reinterpret_cast<const uint8_t *>(w.y) + cc * 16 : p.c.v, there);
         }
     };
 
@@ -316,7 +337,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
         }
     }
 
-    // the rows of this thread's quad: one (RP = 1) or two, eight apart
+    // the rows of this thread's quad: one, or two eight apart
     uint32_t qf[PARTS][KS][4];                   // query fragments
     float o[DT][RP][2], m[RP], l[RP], sfac[RP];
     int limit[RP], n_new = 0;
@@ -324,7 +345,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
 
     for (int i = 0; i < n_units; ++i) {
         const int h = cur.h, rt = cur.rt;
-        const int row0 = rt * ROWS + ug * 8 * RP + g;
+        const int row0 = rt * ROWS + ug * S::kPerWarp + gr;
         if (fresh) {                              // a new segment: its query rows, while its first tile is on the way
             fresh = false;
             n_new = new_count(p.new_len, cur.b, p.new_tokens, KID_ATTN);
@@ -357,7 +378,10 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
                     for (int e = 0; e < 2; ++e) {
                         uint32_t hi, mid, lo;
                         split<T>(x[ks][e].x * down, x[ks][e].y * down, hi, mid, lo);
-                        if constexpr (RP == 1) {
+                        if constexpr (MODE == 0) {
+                            qf[0][ks][2 * e] = g < 4 ? hi : mid;
+                            qf[0][ks][2 * e + 1] = g < 4 ? lo : 0u;
+                        } else if constexpr (RP == 1) {
                             qf[0][ks][2 * e] = hi;
                             qf[0][ks][2 * e + 1] = mid;
                             if constexpr (BF) {
@@ -392,7 +416,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
             const bool edge = base + TW > seen;               // some row may not see all of the warp's
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};     // two chains: even steps, odd steps
                 // lane's row address: entry nt*8 + lane%8, chunk group lane/8
                 const uint32_t ra = kb + (nt * 8 + (lane & 7)) * (DP * 2);
 #pragma unroll
@@ -404,13 +428,17 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
 #pragma unroll
                         for (int x = 0; x < PARTS; ++x) {
                             const uint32_t(&a)[4] = qf[x][2 * k2 + e];
-                            mma16816<T>(acc, a[0], RP == 1 && x == 1 ? 0u : a[1], a[2], RP == 1 && x == 1 ? 0u : a[3], b[2 * e], b[2 * e + 1]);
+                            mma16816<T>(acc[e], a[0], RP == 1 && x == 1 ? 0u : a[1], a[2], RP == 1 && x == 1 ? 0u : a[3], b[2 * e], b[2 * e + 1]);
                         }
                 }
 #pragma unroll
                 for (int rp = 0; rp < RP; ++rp)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) s[nt][rp][e] = RP == 1 ? acc[e] + acc[2 + e] : acc[2 * rp + e];
+                    for (int e = 0; e < 2; ++e) {
+                        float x = RP == 1 ? (acc[0][e] + acc[1][e]) + (acc[0][2 + e] + acc[1][2 + e]) : acc[0][2 * rp + e] + acc[1][2 * rp + e];
+                        if (MODE == 0) x += __shfl_xor_sync(0xffffffffu, x, 16);
+                        s[nt][rp][e] = x;
+                    }
             }
             if (base + TW > min(limit[0], limit[RP - 1])) {
 #pragma unroll
@@ -424,7 +452,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
             if (p.lse) {
 #pragma unroll
                 for (int rp = 0; rp < RP; ++rp)
-                    if (row0 + 8 * rp < p.rows) {
+                    if (holds && row0 + 8 * rp < p.rows) {
                         float *dst = p.scores + (((int64_t)cur.b * p.c.heads + h) * p.rows + row0 + 8 * rp) * p.cap + base + 2 * j;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -452,7 +480,10 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
                     uint32_t hi, mid, lo;
                     split<T>(p0, p1, hi, mid, lo);
                     const int k = nt / 2, e = nt & 1;
-                    if constexpr (RP == 1) {
+                    if constexpr (MODE == 0) {
+                        pf[0][k][2 * e] = g < 4 ? hi : mid;
+                        pf[0][k][2 * e + 1] = g < 4 ? lo : 0u;
+                    } else if constexpr (RP == 1) {
                         pf[0][k][2 * e] = hi;
                         pf[0][k][2 * e + 1] = mid;
                         if constexpr (BF) {
@@ -549,15 +580,21 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
 #pragma unroll
         for (int rp = 0; rp < RP; ++rp) {
             l[rp] = quad_sum(l[rp]);
-            if (j == 0) s_ml[warp][g + 8 * rp] = make_float2(m[rp], l[rp]);
+            if (j == 0 && holds) s_ml[warp][gr + 8 * rp] = make_float2(m[rp], l[rp]);
+        }
+        if constexpr (MODE == 0) {
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) o[dt][0][e] += __shfl_xor_sync(0xffffffffu, o[dt][0][e], 16);
         }
 #pragma unroll
         for (int round = 0; round < S::kRounds; ++round) {
             __syncthreads();
 #pragma unroll
             for (int rp = 0; rp < RP; ++rp)
-                if (row0 + 8 * rp < p.rows) {
-                    float *mine = sums + (warp * 8 * RP + g + 8 * rp) * S::kPad + 2 * j;
+                if (holds && row0 + 8 * rp < p.rows) {
+                    float *mine = sums + (warp * S::kPerWarp + gr + 8 * rp) * S::kPad + 2 * j;
 #pragma unroll
                     for (int x = 0; x < DT / S::kRounds; ++x) {
                         const int dt = round * (DT / S::kRounds) + x;
@@ -567,7 +604,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
             __syncthreads();
             constexpr int C4 = S::kCols / 4;                  // 16-byte pieces of a row
             for (int x = tid; x < rows_here * C4; x += THREADS) {
-                const int r = x / C4, c4 = x % C4, w0 = r / (8 * RP), rw = r % (8 * RP);      // row r: warps w0, w0 + UG, ...
+                const int r = x / C4, c4 = x % C4, w0 = r / S::kPerWarp, rw = r % S::kPerWarp;      // row r: warps w0, w0 + UG, ...
                 const int col = round * S::kCols + c4 * 4;
                 float2 ml[TG];
                 float top = -INFINITY, tot = 0.f;
@@ -581,7 +618,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
 #pragma unroll
                 for (int k = 0; k < TG; ++k) {
                     const float w = pow2(ml[k].x - ref);
-                    const float4 v = *reinterpret_cast<const float4 *>(sums + ((w0 + k * UG) * 8 * RP + rw) * S::kPad + c4 * 4);
+                    const float4 v = *reinterpret_cast<const float4 *>(sums + ((w0 + k * UG) * S::kPerWarp + rw) * S::kPad + c4 * 4);
                     tot = fmaf(ml[k].y, w, tot);
                     y.x = fmaf(v.x, w, y.x), y.y = fmaf(v.y, w, y.y), y.z = fmaf(v.z, w, y.z), y.w = fmaf(v.w, w, y.w);
                 }
@@ -611,7 +648,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, RP, UG>::kPerSm
 // after them (weights wanted) take WEIGHTS entries of a (sequence, head) each:
 // weight[entry] += sum over the rows of 2^(score - log-sum), the scores read
 // side by side along the entries, the log-sums of split rows from their parts.
-constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_THREADS = 128;
 constexpr int JOIN_WEIGHTS = 1024;
 constexpr int JOIN_ROWS = 2048;      // most rows of a key-value head
 
@@ -625,8 +662,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     __shared__ float s_lse[JOIN_ROWS];
     const int tid = threadIdx.x;
     const float2 *ml_all = reinterpret_cast<const float2 *>(p.part + 2 * (int64_t)grid * kept_rows * dp);
-    pdl_wait();
     if (blockIdx.x < join_blocks) {
+        pdl_wait();
         const int64_t seg = blockIdx.x / p.rows;
         const int r = (int)(blockIdx.x - seg * p.rows), rt = r / kept_rows, rr = r - rt * kept_rows;
         const int3 at = p.parts[seg * p.row_tiles + rt];
@@ -682,6 +719,21 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     const int64_t x = blockIdx.x - join_blocks, seg = x / chunks;
     const int b = (int)(seg / p.c.heads), h = (int)(seg - (int64_t)b * p.c.heads);
     const int len = cache_len(p.c, b, KID_ATTN), first = (int)(x - seg * chunks) * JOIN_WEIGHTS;
+    // what the first launch does not write is read before its end: page ids and the weights so far
+    constexpr int EACH = JOIN_WEIGHTS / JOIN_THREADS;
+    int64_t e[EACH];
+    float w[EACH];
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const int slot = first + tid + k * JOIN_THREADS;
+        e[k] = -1;
+        if (slot >= len) continue;
+        const int c = p.page_div.of(slot), pg = cache_page(p.c, b, c, KID_ATTN);
+        if (pg < 0) continue;
+        e[k] = ((int64_t)pg * p.c.heads + h) * p.c.page_size + (slot - c * p.c.page_size);
+        w[k] = p.c.weight[e[k]];
+    }
+    pdl_wait();
     if (first >= len) return;
     for (int r = tid / 32; r < p.rows; r += JOIN_THREADS / 32) {          // a warp per row's log-sum
         const int rt = r / kept_rows, rr = r - rt * kept_rows, lane = tid & 31;
@@ -709,42 +761,50 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     }
     __syncthreads();
     const float *s = p.scores + seg * p.rows * p.cap;
-    for (int slot = first + tid; slot < min(len, first + JOIN_WEIGHTS); slot += JOIN_THREADS) {
-        float w = 0.f;
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        if (e[k] < 0) continue;
+        float add = 0.f;
 #pragma unroll 4
-        for (int r = 0; r < p.rows; ++r) w += pow2(__ldcg(s + r * p.cap + slot) - s_lse[r]);
-        const int c = p.page_div.of(slot), pg = cache_page(p.c, b, c, KID_ATTN);
-        if (pg < 0) continue;
-        p.c.weight[((int64_t)pg * p.c.heads + h) * p.c.page_size + (slot - c * p.c.page_size)] += w;
+        for (int r = 0; r < p.rows; ++r) add += pow2(__ldcg(s + r * p.cap + first + tid + k * JOIN_THREADS) - s_lse[r]);
+        p.c.weight[e[k]] = w[k] + add;
     }
 }
 
-// Which kernel: dim padded, rows per quad and warps along the rows.  Up to
-// eight rows, two parts share an operand; up to 16, 32 and 64 rows, one, two
-// and four warps take sixteen each, the remaining warps split the entries; for
-// heads above 128 sixteen rows do not fit the registers, and warps take eight.
-// More rows than a CTA takes are dealt to further CTAs, which read the cache
-// again (from L2).
+// Which kernel: dim padded, rows per operand (MODE) and warps along the rows.
+// Up to 16, 32 and 64 rows, one, two and four warps take sixteen each, the
+// remaining warps split the entries; for heads above 128 sixteen rows do not
+// fit the registers, and warps take eight.  More rows than a CTA takes are dealt
+// to further CTAs, which read the cache again (from L2).
 struct AttnPlan {
-    int dp, rp, ug, rows, kept_rows, row_tiles, grid;
+    int dp, mode, ug, rows, kept_rows, row_tiles, grid;
     int64_t tiles, cap, part_floats, score_floats, lse_floats, parts;
 };
 
+// f(type, DP, MODE, UG) with the plan's kernel as compile-time values
 template <typename F>
-auto attn_dispatch(int dp, int rp, int ug, F f)
+int attn_dispatch(const AttnPlan &a, int dtype, F f)
 {
     using std::integral_constant;
-    const auto with_ug = [&](auto DPc, auto RPc) {
-        return ug == 1   ? f(DPc, RPc, integral_constant<int, 1>())
-               : ug == 2 ? f(DPc, RPc, integral_constant<int, 2>())
-                         : f(DPc, RPc, integral_constant<int, 4>());
+    const auto with_ug = [&](auto t, auto DPc, auto Mc) {
+        return a.ug == 1   ? f(t, DPc, Mc, integral_constant<int, 1>())
+               : a.ug == 2 ? f(t, DPc, Mc, integral_constant<int, 2>())
+                           : f(t, DPc, Mc, integral_constant<int, 4>());
     };
-    if (dp == 256) return with_ug(integral_constant<int, 256>(), integral_constant<int, 1>());
-    if (rp == 1)
-        return dp == 64 ? f(integral_constant<int, 64>(), integral_constant<int, 1>(), integral_constant<int, 1>())
-                        : f(integral_constant<int, 128>(), integral_constant<int, 1>(), integral_constant<int, 1>());
-    return dp == 64 ? with_ug(integral_constant<int, 64>(), integral_constant<int, 2>())
-                    : with_ug(integral_constant<int, 128>(), integral_constant<int, 2>());
+    const auto with_dp = [&](auto t, auto DPc) {
+        constexpr integral_constant<int, 1> one;
+        if constexpr (attn::kBf16<decltype(t)>) {
+            if (a.mode == 0) return f(t, DPc, integral_constant<int, 0>(), one);
+        }
+        if constexpr (DPc.value == 256) return with_ug(t, DPc, one);
+        else return a.mode == 1 ? f(t, DPc, one, one) : with_ug(t, DPc, integral_constant<int, 2>());
+    };
+    const auto with_type = [&](auto t) {
+        return a.dp == 64    ? with_dp(t, integral_constant<int, 64>())
+               : a.dp == 128 ? with_dp(t, integral_constant<int, 128>())
+                             : with_dp(t, integral_constant<int, 256>());
+    };
+    return dtype == MMQ_F16 ? with_type(__half()) : with_type(__nv_bfloat16());
 }
 
 inline AttnPlan attn_plan(const mmq_kv_cache &c, int q_heads, int new_tokens, bool save)
@@ -752,16 +812,18 @@ inline AttnPlan attn_plan(const mmq_kv_cache &c, int q_heads, int new_tokens, bo
     AttnPlan a;
     a.dp = c.dim <= 64 ? 64 : c.dim <= 128 ? 128 : 256;
     a.rows = q_heads / c.heads * new_tokens;
-    a.rp = a.rows > 8 && a.dp <= 128 ? 2 : 1;
-    a.ug = a.rows <= 8 * a.rp ? 1 : a.rows <= 16 * a.rp ? 2 : 4;
-    const int rows = a.kept_rows = 8 * a.rp * a.ug;                      // per CTA
+    a.mode = c.dtype == MMQ_BF16 && a.rows <= 4 ? 0 : a.rows <= 8 || a.dp == 256 ? 1 : 2;
+    const int per_warp = a.mode == 2 ? 16 : 8;
+    a.ug = a.rows <= per_warp ? 1 : a.rows <= 2 * per_warp ? 2 : 4;
     int tile = 0, per_sm = 0;
-    attn_dispatch(a.dp, a.rp, a.ug, [&](auto DPc, auto RPc, auto UGc) {
-        using S = attn::Shape<DPc.value, RPc.value, UGc.value>;
+    attn_dispatch(a, c.dtype, [&](auto, auto DPc, auto Mc, auto UGc) {
+        using S = attn::Shape<DPc.value, Mc.value, UGc.value>;
         tile = S::kTile;
         per_sm = S::kPerSm;
+        a.kept_rows = S::kRows;
         return 0;
     });
+    const int rows = a.kept_rows;                                        // per CTA
     a.row_tiles = (a.rows + rows - 1) / rows;
     a.tiles = ((int64_t)c.cols * c.page_size + tile - 1) / tile * c.seqs * c.heads * a.row_tiles;
     const int64_t full = (int64_t)sm_count() * per_sm;                   // every CTA resident
@@ -784,11 +846,11 @@ inline int attn_check(const mmq_kv_cache *c, int q_heads, int new_tokens)
     return MMQ_OK;
 }
 
-template <int DP, typename T, int RP, int UG>
+template <int DP, typename T, int MODE, int UG>
 int launch_attn(const AttnParams &p, int grid, cudaStream_t stream)
 {
-    const auto kernel = attn_kernel<DP, T, RP, UG>;
-    constexpr int smem = attn::Shape<DP, RP, UG>::kSmem;
+    const auto kernel = attn_kernel<DP, T, MODE, UG>;
+    constexpr int smem = attn::Shape<DP, MODE, UG>::kSmem;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
@@ -856,9 +918,8 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     p.cap = a.cap;
     p.page_div = FastDiv(cache->page_size);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    rc = attn_dispatch(a.dp, a.rp, a.ug, [&](auto DPc, auto RPc, auto UGc) {
-        return cache->dtype == MMQ_F16 ? launch_attn<DPc.value, __half, RPc.value, UGc.value>(p, a.grid, s)
-                                       : launch_attn<DPc.value, __nv_bfloat16, RPc.value, UGc.value>(p, a.grid, s);
+    rc = attn_dispatch(a, cache->dtype, [&](auto t, auto DPc, auto Mc, auto UGc) {
+        return launch_attn<DPc.value, decltype(t), Mc.value, UGc.value>(p, a.grid, s);
     });
     if (rc != MMQ_OK) return rc;
     const int64_t segs = (int64_t)cache->seqs * cache->heads, join_blocks = segs * a.rows;
