@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
     constexpr int NT = TW / 8, KS = DP / 16, DT = DP / 8, ROWS = S::kRows;
     constexpr int CPR = DP / 8, RPP = THREADS / CPR, PASSES = TILE / RPP;   // 16-byte copies per row, rows per pass
 
-    pdl_launch_dependents();       // the joining launch may start; it waits for this grid's end before it reads
+    pdl_wait();
+    pdl_launch_dependents();       // the joining launch may start; what this one writes it reads after this one's end
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ ulonglong2 s_row[STAGES][TILE];
     __shared__ float2 s_ml[4][S::kPerWarp];         // (max, sum) of every warp's rows
@@ -664,6 +665,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     const float2 *ml_all = reinterpret_cast<const float2 *>(p.part + 2 * (int64_t)grid * kept_rows * dp);
     if (blockIdx.x < join_blocks) {
         pdl_wait();
+        pdl_launch_dependents();
         const int64_t seg = blockIdx.x / p.rows;
         const int r = (int)(blockIdx.x - seg * p.rows), rt = r / kept_rows, rr = r - rt * kept_rows;
         const int3 at = p.parts[seg * p.row_tiles + rt];
@@ -734,6 +736,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
         w[k] = p.c.weight[e[k]];
     }
     pdl_wait();
+    pdl_launch_dependents();
     if (first >= len) return;
     for (int r = tid / 32; r < p.rows; r += JOIN_THREADS / 32) {          // a warp per row's log-sum
         const int rt = r / kept_rows, rr = r - rt * kept_rows, lane = tid & 31;
@@ -862,8 +865,7 @@ int launch_attn(const AttnParams &p, int grid, cudaStream_t stream)
             return launch_status();
         attr_done[dev] = true;
     }
-    kernel<<<grid, attn::THREADS, smem, stream>>>(p);
-    return launch_status();
+    return launch_pdl(kernel, dim3((unsigned)grid), attn::THREADS, smem, stream, 0, p);
 }
 
 }  // namespace
@@ -924,16 +926,6 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     if (rc != MMQ_OK) return rc;
     const int64_t segs = (int64_t)cache->seqs * cache->heads, join_blocks = segs * a.rows;
     const int chunks = save ? (int)((a.cap + JOIN_WEIGHTS - 1) / JOIN_WEIGHTS) : 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(join_blocks + segs * chunks));
-    cfg.blockDim = dim3(JOIN_THREADS);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;     // its blocks start as the first launch's leave
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     const auto join = cache->dtype == MMQ_F16 ? attn_join_kernel<__half> : attn_join_kernel<__nv_bfloat16>;
-    if (cudaLaunchKernelEx(&cfg, join, p, a.dp, a.kept_rows, a.grid, join_blocks, chunks) != cudaSuccess) return launch_status();
-    return launch_status();
+    return launch_pdl(join, dim3((unsigned)(join_blocks + segs * chunks)), JOIN_THREADS, 0, s, 0, p, a.dp, a.kept_rows, a.grid, join_blocks, chunks);
 }

@@ -49,6 +49,31 @@ inline int check_cache(const mmq_kv_cache *c)
     return MMQ_OK;
 }
 
+// Launch under programmatic dependent launch: the kernel may start while the
+// one before it in the stream finishes, and waits for that one's end (pdl_wait,
+// the first thing every kernel here does) before it touches memory.
+// cluster: CTAs per cluster, 0 for none.
+template <typename... P, typename... A>
+int launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return launch_status();
+    return launch_status();
+}
+
 // A sequence's length, limited to what its table row can hold.
 __device__ __forceinline__ int cache_len(const mmq_kv_cache &c, int b, int kid)
 {

@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
     __shared__ uint32_t s_xchg[3];                        // ties, holes, moves of this CTA
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t below = (1u << lane) - 1;
+    pdl_wait();
+    pdl_launch_dependents();
     const int rank = (int)cluster_ctarank(), n_cta = (int)cluster_nctarank();
     const int row = blockIdx.x / n_cta, b = row / p.c.heads, h = row - b * p.c.heads, ps = p.c.page_size;
     const int len = cache_len(p.c, b, KID_EVICT);
@@ -355,20 +357,7 @@ inline int launch_evict(const EvictParams &p, int64_t rows, int cl, cudaStream_t
             return launch_status();
         attr_done[dev] = true;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * cl));
-    cfg.blockDim = dim3(evict::THREADS);
-    cfg.dynamicSmemBytes = (size_t)(p.chunk_cap + p.cols_cap) * 4;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cl;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, evict_kernel, p) != cudaSuccess) return launch_status();
-    return launch_status();
+    return launch_pdl(evict_kernel, dim3((unsigned)(rows * cl)), evict::THREADS, (size_t)(p.chunk_cap + p.cols_cap) * 4, s, cl, p);
 }
 
 }  // namespace

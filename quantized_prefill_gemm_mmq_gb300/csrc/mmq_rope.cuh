@@ -39,6 +39,8 @@ template <typename T, int P>
 __global__ void __launch_bounds__(ROPE_THREADS, 4) rope_append_kernel(const RopeParams p)
 {
     __shared__ __align__(16) float s_cos[128], s_sin[128];
+    pdl_wait();
+    pdl_launch_dependents();
     const int D = p.c.dim, units = D / (2 * P);
     const int u = threadIdx.x % units, hl = threadIdx.x / units, lanes = blockDim.x / units;
     const int row = blockIdx.x, b = row / p.new_tokens, t = row - b * p.new_tokens;
@@ -194,11 +196,7 @@ int launch_rope(RopeParams &p, int sms, cudaStream_t stream)
     p.heads_per_block = (int)((total + parts - 1) / parts);
     p.heads_per_block = (p.heads_per_block + lanes - 1) / lanes * lanes;
     const dim3 grid((unsigned)rows, (unsigned)((total + p.heads_per_block - 1) / p.heads_per_block));
-    if (wide)
-        rope_append_kernel<T, 4><<<grid, units * lanes, 0, stream>>>(p);
-    else
-        rope_append_kernel<T, 1><<<grid, units * lanes, 0, stream>>>(p);
-    return launch_status();
+    return launch_pdl(wide ? rope_append_kernel<T, 4> : rope_append_kernel<T, 1>, grid, units * lanes, 0, stream, 0, p);
 }
 
 }  // namespace

@@ -128,6 +128,8 @@ __global__ void __launch_bounds__(ver::THREADS, ver::PER_SM) spec_verify_kernel(
     __shared__ int s_first, s_bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cluster_ctarank(), n_cta = (int)cluster_nctarank(), b = blockIdx.x / n_cta;
+    pdl_wait();
+    pdl_launch_dependents();
     const int64_t V = p.vocab;
     const T *target = static_cast<const T *>(p.target) + (int64_t)b * (p.drafts + 1) * V;
     const T *draft = p.draft ? static_cast<const T *>(p.draft) + (int64_t)b * p.drafts * V : nullptr;
@@ -295,20 +297,7 @@ int launch_verify(VerifyParams &p, int seqs, cudaStream_t stream)
     while (cl < ver::MAX_CLUSTER && p.vocab > each * cl) cl *= 2;
     const int per = (p.vocab + cl - 1) / cl;
     p.spans = (per + ver::kSpan<T> - 1) / ver::kSpan<T>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(seqs * cl));
-    cfg.blockDim = dim3(ver::THREADS);
-    cfg.dynamicSmemBytes = (size_t)p.spans * 8;            // at most 8 KB
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cl;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, spec_verify_kernel<T>, p) != cudaSuccess) return launch_status();
-    return launch_status();
+    return launch_pdl(spec_verify_kernel<T>, dim3((unsigned)(seqs * cl)), ver::THREADS, (size_t)p.spans * 8 /* <= 8 KB */, stream, cl, p);
 }
 
 }  // namespace

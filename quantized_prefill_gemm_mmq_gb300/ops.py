@@ -341,9 +341,9 @@ PROB_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 ATTN_NEW_MAX = 16         # mmq_attn_decode
 
 
-def _need(t, name, dtype, shape, dev):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {dev}")
+def _need(t, name, dtype, shape, index):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on CUDA device {index}")
 
 
 class KVCache:
@@ -373,11 +373,11 @@ class KVCache:
             raise ValueError("table must be [seqs][cols] and lens [seqs]")
         pages, heads, page_size, dim = k.shape
         seqs, cols = table.shape
-        _need(table, "table", torch.int32, (seqs, cols), k.device)
-        _need(lens, "lens", torch.int32, (seqs,), k.device)
+        self.device, self.index = k.device, k.get_device()
+        _need(table, "table", torch.int32, (seqs, cols), self.index)
+        _need(lens, "lens", torch.int32, (seqs,), self.index)
         self.k, self.v, self.table, self.lens = k, v, table, lens
         self.heads, self.dim, self.page_size, self.seqs, self.cols = heads, dim, page_size, seqs, cols
-        self.device = k.device
         self._c = KVCacheC(_ptr(k), _ptr(v), None, None, _ptr(table), _ptr(lens), *k.stride()[:3], *v.stride()[:3], pages,
                            CACHE_DTYPES[k.dtype], heads, dim, page_size, seqs, cols)
         self._ref = ctypes.byref(self._c)
@@ -388,9 +388,9 @@ class KVCache:
         """Use these weight and pos tensors from now on."""
         shape = tuple(self.k.shape[:3])
         if weight is not None:
-            _need(weight, "weight", torch.float32, shape, self.device)
+            _need(weight, "weight", torch.float32, shape, self.index)
         if pos is not None:
-            _need(pos, "pos", torch.int32, shape, self.device)
+            _need(pos, "pos", torch.int32, shape, self.index)
         self.weight, self.pos = weight, pos
         self._c.weight, self._c.pos = _ptr(weight), _ptr(pos)
 
@@ -407,13 +407,19 @@ class KVCache:
                    torch.zeros(shape, dtype=torch.int32, device=dev) if track else None)
 
 
-def _on(dev: torch.device, fn, *args) -> int:
-    """fn(*args, stream) with `dev` current, on its current stream."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return fn(*args, stream)
-    with torch.cuda.device(dev):
-        return fn(*args, stream)
+# The current stream's handle without the Stream object around it (2 us of every call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(call: str, fn, index: int, *args):
+    """fn(*args, stream) with device `index` current, on its current stream; raises on a status."""
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st != 0:
+        raise MMQError(call, st)
 
 
 class RopeTable:
@@ -422,7 +428,7 @@ class RopeTable:
 
     def __init__(self, freq: torch.Tensor, magnitude: float = 1.0):
         _need_cuda(freq)
-        _need(freq, "freq", torch.int64, (freq.numel(),), freq.device)
+        _need(freq, "freq", torch.int64, (freq.numel(),), freq.get_device())
         self.freq, self.rot, self.magnitude = freq, 2 * freq.numel(), float(magnitude)
 
 
@@ -468,21 +474,24 @@ def rope_table(rot: int, base: float = 10000.0, scaling: str = "none", factor: f
     return RopeTable(torch.tensor(rope_fixed(inv), dtype=torch.int64).to(device if device is not None else "cuda"), magnitude)
 
 
-def _rows(t, name, heads, dim, dev):
+def _rows(t, name, rows, heads, dim, index):
     """Row stride of f32 [rows][heads][dim] whose rows may lie apart."""
-    if t.dtype != torch.float32 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.device != dev:
-        raise ValueError(f"{name} must be float32 [rows][{heads}][{dim}] on {dev}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    if t.dtype is not torch.float32 or t.shape != (rows, heads, dim) or t.get_device() != index:
+        raise ValueError(f"{name} must be float32 [{rows}][{heads}][{dim}] on CUDA device {index}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
+    return st[0] if rows > 1 else max(st[0], heads * dim)
 
 
-def _new_len(cache, new, rows):
+def _q_shape(cache, q):
+    """(rows, query heads, new tokens per sequence) of q."""
+    if q.dim() != 3:
+        raise ValueError("q must be float32 [rows][q_heads][dim]")
+    rows, q_heads, _ = q.shape
     if cache.seqs == 0 or rows % cache.seqs:
         raise ValueError("rows must be a multiple of the cache's sequences")
-    if new is not None:
-        _need(new, "new", torch.int32, (cache.seqs,), cache.device)
-    return rows // cache.seqs
+    return rows, q_heads, rows // cache.seqs
 
 
 def rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
@@ -493,31 +502,24 @@ def rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tenso
     one wider product row), pos int32 [seqs*n] positions.  new int32 [seqs] limits how many
     of a sequence's n rows are there; they become the last entries of cache.lens.  `out`
     may be q."""
-    dev = cache.device
-    _need_cuda(q, k, v, pos, rope.freq)
-    if q.dim() != 3:
-        raise ValueError("q must be float32 [rows][q_heads][dim]")
-    rows, q_heads = q.shape[0], q.shape[1]
-    n = _new_len(cache, new, rows)
-    if k.shape[0] != rows or v.shape[0] != rows:
-        raise ValueError("q, k and v must have as many rows")
-    ldq, ldk, ldv = (_rows(t, s, h, cache.dim, dev) for t, s, h in
-                     ((q, "q", q_heads), (k, "k", cache.heads), (v, "v", cache.heads)))
-    _need(pos, "pos", torch.int32, (rows,), dev)
-    if rope.rot > cache.dim or rope.freq.device != dev:
+    index, dim = cache.index, cache.dim
+    rows, q_heads, n = _q_shape(cache, q)
+    ldq = _rows(q, "q", rows, q_heads, dim, index)
+    ldk = _rows(k, "k", rows, cache.heads, dim, index)
+    ldv = _rows(v, "v", rows, cache.heads, dim, index)
+    _need(pos, "pos", torch.int32, (rows,), index)
+    if new is not None:
+        _need(new, "new", torch.int32, (cache.seqs,), index)
+    if rope.rot > dim or rope.freq.get_device() != index:
         raise ValueError("the table rotates more values than a head has, or is on another device")
     if out is None:
-        out = torch.empty((rows, q_heads, cache.dim), dtype=torch.float32, device=dev)
-        ldo = q_heads * cache.dim
+        out = torch.empty((rows, q_heads, dim), dtype=torch.float32, device=cache.device)
+        ldo = q_heads * dim
     else:
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        ldo = _rows(out, "out", q_heads, cache.dim, dev)
-    st = _on(dev, load().mmq_rope_append, cache._ref, rope.freq.data_ptr(), rope.rot, rope.magnitude, int(interleaved),
-             q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, pos.data_ptr(),
-             new.data_ptr() if new is not None else None, out.data_ptr(), ldo, q_heads, n)
-    if st != 0:
-        raise MMQError("mmq_rope_append", st)
+        ldo = _rows(out, "out", rows, q_heads, dim, index)
+    _on("mmq_rope_append", load().mmq_rope_append, index, cache._ref, rope.freq.data_ptr(), rope.rot, rope.magnitude,
+        int(interleaved), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, pos.data_ptr(),
+        None if new is None else new.data_ptr(), out.data_ptr(), ldo, q_heads, n)
     return out
 
 
@@ -555,42 +557,41 @@ def attn_decode(cache: KVCache, q: torch.Tensor, scale: float | None = None, new
     own (new int32 [seqs] limits the rows as in rope_append; rows past it get 0).  scale
     defaults to dim^-0.5.  accumulate adds every entry's weight to cache.weight.  Without
     `workspace` one is allocated for this call."""
-    dev = cache.device
-    _need_cuda(q)
-    if q.dim() != 3:
-        raise ValueError("q must be float32 [rows][q_heads][dim]")
-    rows, q_heads, dim = q.shape
-    n = _new_len(cache, new, rows)
-    ldq = _rows(q, "q", q_heads, cache.dim, dev)
+    index, dim = cache.index, cache.dim
+    rows, q_heads, n = _q_shape(cache, q)
+    ldq = _rows(q, "q", rows, q_heads, dim, index)
     if q_heads % cache.heads:
         raise ValueError("q_heads must be a multiple of the cache's heads")
     if not 1 <= n <= ATTN_NEW_MAX:
         raise ValueError(f"1 to {ATTN_NEW_MAX} new tokens per sequence")
     if accumulate and cache.weight is None:
         raise ValueError("the cache keeps no weights")
+    if new is not None:
+        _need(new, "new", torch.int32, (cache.seqs,), index)
     if out is None:
-        out = torch.empty((rows, q_heads, dim), dtype=torch.float32, device=dev)
+        out = torch.empty((rows, q_heads, dim), dtype=torch.float32, device=cache.device)
     else:
-        _need(out, "out", torch.float32, (rows, q_heads, dim), dev)
+        _need(out, "out", torch.float32, (rows, q_heads, dim), index)
     key = (q_heads, n, accumulate)
     floats = cache._work.get(key)
     if floats is None:
         floats = cache._work[key] = attn_sizes(cache, q_heads, n, accumulate)
     if workspace is None or not workspace.fits(floats):
-        workspace = AttnWorkspace(dev, floats)
-    st = _on(dev, load().mmq_attn_decode, cache._ref, q.data_ptr(), ldq, new.data_ptr() if new is not None else None,
-             out.data_ptr(), q_heads, n, dim ** -0.5 if scale is None else scale, int(accumulate),
-             workspace.work.data_ptr())
-    if st != 0:
-        raise MMQError("mmq_attn_decode", st)
+        workspace = AttnWorkspace(cache.device, floats)
+    _on("mmq_attn_decode", load().mmq_attn_decode, index, cache._ref, q.data_ptr(), ldq, None if new is None else new.data_ptr(),
+        out.data_ptr(), q_heads, n, dim ** -0.5 if scale is None else scale, int(accumulate), workspace.work.data_ptr())
     return out
+
+
+def _evict_ints(cache: KVCache, budget: int) -> int:
+    n = ctypes.c_int64(0)
+    _check("mmq_evict_sizes", load().mmq_evict_sizes(cache._ref, budget, ctypes.byref(n)))
+    return n.value
 
 
 def evict_workspace(cache: KVCache, budget: int) -> torch.Tensor:
     """Scratch of kv_evict (int32)."""
-    n = ctypes.c_int64(0)
-    _check("mmq_evict_sizes", load().mmq_evict_sizes(cache._ref, budget, ctypes.byref(n)))
-    return torch.empty(max(1, n.value), dtype=torch.int32, device=cache.device)
+    return torch.empty(max(1, _evict_ints(cache, budget)), dtype=torch.int32, device=cache.device)
 
 
 def kv_evict(cache: KVCache, budget: int, keep_from: torch.Tensor, weight_out: torch.Tensor, pos_out: torch.Tensor,
@@ -600,29 +601,26 @@ def kv_evict(cache: KVCache, budget: int, keep_from: torch.Tensor, weight_out: t
     the new bookkeeping goes to weight_out and pos_out (shaped as cache.weight), for
     cache.set_bookkeeping.  Lower cache.lens to the budget (clamp_) once every layer that
     shares it is done."""
-    dev = cache.device
+    index = cache.index
     if cache.weight is None or cache.pos is None:
         raise ValueError("the cache keeps no weights or positions")
-    _need_cuda(keep_from, weight_out, pos_out)
-    shape = tuple(cache.weight.shape)
-    _need(keep_from, "keep_from", torch.int32, (cache.seqs,), dev)
-    _need(weight_out, "weight_out", torch.float32, shape, dev)
-    _need(pos_out, "pos_out", torch.int32, shape, dev)
+    if weight_out is None or pos_out is None:
+        raise ValueError("weight_out and pos_out are required")
+    shape = cache.weight.shape
+    _need(keep_from, "keep_from", torch.int32, (cache.seqs,), index)
+    _need(weight_out, "weight_out", torch.float32, shape, index)
+    _need(pos_out, "pos_out", torch.int32, shape, index)
     if weight_out.data_ptr() == cache.weight.data_ptr() or pos_out.data_ptr() == cache.pos.data_ptr():
         raise ValueError("weight_out and pos_out must not be the cache's own")
     need = cache._work.get(budget)
     if need is None:
-        n = ctypes.c_int64(0)
-        _check("mmq_evict_sizes", load().mmq_evict_sizes(cache._ref, budget, ctypes.byref(n)))
-        need = cache._work[budget] = n.value
+        need = cache._work[budget] = _evict_ints(cache, budget)
     if workspace is None:
-        workspace = torch.empty(max(1, need), dtype=torch.int32, device=dev)
-    elif workspace.dtype != torch.int32 or not workspace.is_contiguous() or workspace.device != dev or workspace.numel() < need:
+        workspace = torch.empty(max(1, need), dtype=torch.int32, device=cache.device)
+    elif workspace.dtype is not torch.int32 or workspace.get_device() != index or not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError("workspace must be evict_workspace(cache, budget) or larger")
-    st = _on(dev, load().mmq_kv_evict, cache._ref, budget, keep_from.data_ptr(), weight_out.data_ptr(), pos_out.data_ptr(),
-             workspace.data_ptr())
-    if st != 0:
-        raise MMQError("mmq_kv_evict", st)
+    _on("mmq_kv_evict", load().mmq_kv_evict, index, cache._ref, budget, keep_from.data_ptr(), weight_out.data_ptr(),
+        pos_out.data_ptr(), workspace.data_ptr())
 
 
 def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.Tensor, uniform: torch.Tensor,
@@ -634,28 +632,25 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.
     [seqs][n+1] in [0, 1), count int32 [seqs] drafts there (None: n).  Returns (tokens
     int32 [seqs][n+1]: the accepted ones, one drawn, then -1; accepted int32 [seqs]);
     `out` may supply the two."""
-    _need_cuda(target, draft, tokens, uniform, count)
-    if target.dtype not in PROB_DTYPES or target.dim() != 3 or not target.is_contiguous() or target.shape[1] < 2:
-        raise ValueError("target must be contiguous float [seqs][drafts+1][vocab]")
-    dev = target.device
+    dtype, index = PROB_DTYPES.get(target.dtype), target.get_device()
+    if dtype is None or index < 0 or target.dim() != 3 or target.shape[1] < 2 or not target.is_contiguous():
+        raise ValueError("target must be a contiguous CUDA tensor [seqs][drafts+1][vocab] of probabilities")
     B, n1, V = target.shape
     if draft is not None:
-        _need(draft, "draft", target.dtype, (B, n1 - 1, V), dev)
-    _need(tokens, "tokens", torch.int32, (B, n1 - 1), dev)
-    _need(uniform, "uniform", torch.float32, (B, n1), dev)
+        _need(draft, "draft", target.dtype, (B, n1 - 1, V), index)
+    _need(tokens, "tokens", torch.int32, (B, n1 - 1), index)
+    _need(uniform, "uniform", torch.float32, (B, n1), index)
     if count is not None:
-        _need(count, "count", torch.int32, (B,), dev)
+        _need(count, "count", torch.int32, (B,), index)
     if out is None:
+        dev = target.device
         res, acc = torch.empty((B, n1), dtype=torch.int32, device=dev), torch.empty((B,), dtype=torch.int32, device=dev)
     else:
         res, acc = out
-        _need(res, "out[0]", torch.int32, (B, n1), dev)
-        _need(acc, "out[1]", torch.int32, (B,), dev)
-    st = _on(dev, load().mmq_spec_verify, target.data_ptr(), draft.data_ptr() if draft is not None else None,
-             PROB_DTYPES[target.dtype], tokens.data_ptr(), uniform.data_ptr(),
-             count.data_ptr() if count is not None else None, res.data_ptr(), acc.data_ptr(), B, n1 - 1, V)
-    if st != 0:
-        raise MMQError("mmq_spec_verify", st)
+        _need(res, "out[0]", torch.int32, (B, n1), index)
+        _need(acc, "out[1]", torch.int32, (B,), index)
+    _on("mmq_spec_verify", load().mmq_spec_verify, index, target.data_ptr(), None if draft is None else draft.data_ptr(), dtype,
+        tokens.data_ptr(), uniform.data_ptr(), None if count is None else count.data_ptr(), res.data_ptr(), acc.data_ptr(), B, n1 - 1, V)
     return res, acc
 
 
