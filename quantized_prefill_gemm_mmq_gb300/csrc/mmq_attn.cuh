@@ -58,9 +58,9 @@ constexpr float kExp = kBf16<T> ? 0.f : 15.f;      // p carries 2^kExp
 template <int DP, int MODE, int UG>
 struct Shape {
     static constexpr int kPerWarp = MODE == 0 ? 4 : MODE == 1 ? 8 : 16;   // rows
-    static constexpr int kTile = DP == 64 ? 128 : 64;                 // entries per tile
+    static constexpr int kTile = DP == 64 ? 128 : DP == 256 && UG > 1 ? 32 : 64;      // entries per tile
     static constexpr int kStages = 3;                                 // tiles in the ring
-    static constexpr int kPerSm = DP <= 128 ? 2 : 1;                  // CTAs resident per SM
+    static constexpr int kPerSm = DP == 256 && UG == 1 ? 1 : 2;       // CTAs resident per SM
     static constexpr int kHalf = kTile * DP * 2;                      // bytes of K (or V) per stage
     static constexpr int kSmem = kStages * 2 * kHalf;
     static constexpr int kRows = kPerWarp * UG;                       // rows per CTA
@@ -185,7 +185,7 @@ struct AttnParams {
     float *scores;           // [seqs*heads][rows][cap] in powers of two (weights only)
     float *lse;              // [seqs*heads][rows] (weights only, else NULL)
     int64_t cap;
-    FastDiv page_div;
+    FastDiv page_div, group_div;
 };
 
 // A place in the row of tiles: sequence, head, part of the rows, tile.
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
             n_new = new_count(p.new_len, cur.b, p.new_tokens, KID_ATTN);
 #pragma unroll
             for (int rp = 0; rp < RP; ++rp) {
-                const int r = row0 + 8 * rp, t = r / p.group;
+                const int r = row0 + 8 * rp, t = p.group_div.of(r);
                 const bool valid = r < p.rows && t < n_new;
                 limit[rp] = valid ? cur.len - n_new + t + 1 : 0;
                 const float *qr = p.q + ((int64_t)cur.b * p.new_tokens + (valid ? t : 0)) * p.ldq +
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
         const int64_t part = 2 * (int64_t)blockIdx.x + (seg_base > u0 ? 1 : 0);
         float *const ml_all = p.part + 2 * (int64_t)gridDim.x * ROWS * DP;
         auto out_row = [&](int r) {
-            const int rg = rt * ROWS + r, t = rg / p.group;
+            const int rg = rt * ROWS + r, t = p.group_div.of(rg);
             return p.out + (((int64_t)was.b * p.new_tokens + t) * p.c.heads * p.group + h * p.group + (rg - t * p.group)) * (int64_t)p.c.dim;
         };
 #pragma unroll
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
         }
         const float inv = inverse(tot);
         const int64_t b = seg / p.c.heads, h = seg - b * p.c.heads;
-        const int t = r / p.group;
+        const int t = p.group_div.of(r);
         *reinterpret_cast<float4 *>(p.out + ((b * p.new_tokens + t) * p.c.heads * p.group + h * p.group + (r - t * p.group)) * p.c.dim + col) =
             make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
         return;
@@ -721,19 +721,31 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     const int64_t x = blockIdx.x - join_blocks, seg = x / chunks;
     const int b = (int)(seg / p.c.heads), h = (int)(seg - (int64_t)b * p.c.heads);
     const int len = cache_len(p.c, b, KID_ATTN), first = (int)(x - seg * chunks) * JOIN_WEIGHTS;
-    // what the first launch does not write is read before its end: page ids and the weights so far
+    // Eight neighbouring entries per thread.  What the first launch does not write is read before its end: page
+    // ids and the weights so far.
     constexpr int EACH = JOIN_WEIGHTS / JOIN_THREADS;
-    int64_t e[EACH];
+    static_assert(EACH == 8, "two 16-byte accesses");
+    const int mine = first + tid * EACH, n = min(EACH, len - mine);
+    const bool together = p.c.page_size % EACH == 0 && n == EACH;        // one page, 32-byte aligned
     float w[EACH];
+    float *at[EACH];
+    if (together) {
+        const int c = p.page_div.of(mine), pg = cache_page(p.c, b, c, KID_ATTN);
+        at[0] = pg < 0 ? nullptr : p.c.weight + ((int64_t)pg * p.c.heads + h) * p.c.page_size + (mine - c * p.c.page_size);
+        if (at[0]) {
+            *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(at[0]);
+            *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(at[0] + 4);
+        }
+    } else {
 #pragma unroll
-    for (int k = 0; k < EACH; ++k) {
-        const int slot = first + tid + k * JOIN_THREADS;
-        e[k] = -1;
-        if (slot >= len) continue;
-        const int c = p.page_div.of(slot), pg = cache_page(p.c, b, c, KID_ATTN);
-        if (pg < 0) continue;
-        e[k] = ((int64_t)pg * p.c.heads + h) * p.c.page_size + (slot - c * p.c.page_size);
-        w[k] = p.c.weight[e[k]];
+        for (int k = 0; k < EACH; ++k) {
+            at[k] = nullptr;
+            if (k >= n) continue;
+            const int c = p.page_div.of(mine + k), pg = cache_page(p.c, b, c, KID_ATTN);
+            if (pg < 0) continue;
+            at[k] = p.c.weight + ((int64_t)pg * p.c.heads + h) * p.c.page_size + (mine + k - c * p.c.page_size);
+            w[k] = *at[k];
+        }
     }
     pdl_wait();
     pdl_launch_dependents();
@@ -763,14 +775,27 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
         if (lane == 0) s_lse[r] = lse;
     }
     __syncthreads();
-    const float *s = p.scores + seg * p.rows * p.cap;
+    if (n <= 0) return;
+    const float *s = p.scores + seg * p.rows * p.cap + mine;             // 32-byte aligned, readable past len
+    float add[EACH];
 #pragma unroll
-    for (int k = 0; k < EACH; ++k) {
-        if (e[k] < 0) continue;
-        float add = 0.f;
-#pragma unroll 4
-        for (int r = 0; r < p.rows; ++r) add += pow2(__ldcg(s + r * p.cap + first + tid + k * JOIN_THREADS) - s_lse[r]);
-        p.c.weight[e[k]] = w[k] + add;
+    for (int k = 0; k < EACH; ++k) add[k] = 0.f;
+#pragma unroll 2
+    for (int r = 0; r < p.rows; ++r) {
+        const float4 a = __ldcg(reinterpret_cast<const float4 *>(s + r * p.cap));
+        const float4 c = __ldcg(reinterpret_cast<const float4 *>(s + r * p.cap) + 1);
+        const float l = s_lse[r], v[EACH] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) add[k] += pow2(v[k] - l);
+    }
+    if (together) {
+        if (!at[0]) return;
+        *reinterpret_cast<float4 *>(at[0]) = make_float4(w[0] + add[0], w[1] + add[1], w[2] + add[2], w[3] + add[3]);
+        *reinterpret_cast<float4 *>(at[0] + 4) = make_float4(w[4] + add[4], w[5] + add[5], w[6] + add[6], w[7] + add[7]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < EACH; ++k)
+            if (at[k]) *at[k] = w[k] + add[k];
     }
 }
 
@@ -894,7 +919,8 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     if (ldq < (int64_t)q_heads * cache->dim || !(scale - scale == 0.f)) return MMQ_ERR_SHAPE;
     if (cache->seqs == 0) return MMQ_OK;
     if (!q || !out || !work || (accumulate && !cache->weight)) return MMQ_ERR_NULL;
-    if (!aligned16(q) || (ldq & 3) || !aligned16(out) || !aligned16(work)) return MMQ_ERR_ALIGN;
+    if (!aligned16(q) || (ldq & 3) || !aligned16(out) || !aligned16(work) || (accumulate && !aligned16(cache->weight)))
+        return MMQ_ERR_ALIGN;
     if ((rc = check_arch()) != MMQ_OK) return rc;
     const bool save = accumulate != 0;
     const AttnPlan a = attn_plan(*cache, q_heads, new_tokens, save);
@@ -919,6 +945,7 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     p.parts = reinterpret_cast<int3 *>(p.part + a.part_floats + a.lse_floats);
     p.cap = a.cap;
     p.page_div = FastDiv(cache->page_size);
+    p.group_div = FastDiv(p.group);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     rc = attn_dispatch(a, cache->dtype, [&](auto t, auto DPc, auto Mc, auto UGc) {
         return launch_attn<DPc.value, decltype(t), Mc.value, UGc.value>(p, a.grid, s);

@@ -35,7 +35,7 @@ constexpr int MAX_CHUNK = 32768;               // keys per CTA: 128 KB
 constexpr int STRIPES = MAX_CHUNK / THREADS;   // at most
 constexpr int MAX_COLS = 4096;                 // page ids kept in shared memory
 constexpr int BATCH = 8;                       // stripes whose loads a thread has in flight
-constexpr int MOVE_BATCH = 8;                  // moves a warp has in flight
+constexpr int MOVE_BATCH = 3;                  // moves a warp has in flight
 }  // namespace evict
 
 struct EvictParams {
@@ -79,9 +79,10 @@ __device__ __forceinline__ int block_prefix(int v, int *s, int &total)
     int before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < evict::WARPS; ++w) {
-        if (w < warp) before += s[w];
-        total += s[w];
+    for (int w = 0; w < evict::WARPS; w += 4) {
+        const int4 q = *reinterpret_cast<const int4 *>(s + w);
+        before += (w < warp ? q.x : 0) + (w + 1 < warp ? q.y : 0) + (w + 2 < warp ? q.z : 0) + (w + 3 < warp ? q.w : 0);
+        total += (q.x + q.y) + (q.z + q.w);
     }
     return before + x - v;
 }
@@ -115,9 +116,9 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
     extern __shared__ __align__(16) uint32_t keys[];       // [chunk_cap], then the page ids [cols_cap]
     __shared__ uint32_t hist[2][BINS];
     __shared__ int s_cnt[2][STRIPES * WARPS];
-    __shared__ int s_scan[WARPS];
-    __shared__ uint32_t s_digit, s_above;
-    __shared__ uint32_t s_xchg[3];                        // ties, holes, moves of this CTA
+    __shared__ __align__(16) int s_scan[WARPS];
+    __shared__ uint32_t s_digit, s_above, s_match;
+    __shared__ uint32_t s_xchg[2];                        // ties; holes and moves of this CTA
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t below = (1u << lane) - 1;
     pdl_wait();
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
         uint32_t *hs = hist[pass & 1];
         for (int i = tid; i < BINS; i += THREADS) hs[i] = 0;
         __syncthreads();
+#pragma unroll 8
         for (int i = tid; i < n; i += THREADS) {
             const uint32_t k = keys[i];
             if ((k & mask) == prefix) atomicAdd(&hs[(k >> shift) & ((1u << bits) - 1)], 1u);
@@ -217,6 +219,7 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
                 if (before < want && want <= before + (int)c[k]) {
                     s_digit = (uint32_t)(top + k);
                     s_above = (uint32_t)before;
+                    s_match = c[k];
                 }
                 before += (int)c[k];
             }
@@ -226,49 +229,60 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
         mask |= ((1u << bits) - 1) << shift;
         want -= (int)s_above;
     }
-    // sum over the CTAs before this one of what each has put into s_xchg[k], and over all
-    auto exchange = [&](int k, int mine, int &all) {
-        if (n_cta == 1) {
-            all = mine;
-            return 0;
-        }
-        if (tid == 0) s_xchg[k] = (uint32_t)mine;
+    // What each CTA puts into s_xchg[k], two 16-bit counts: sums over the CTAs before this one, and of the lower
+    // one over all.
+    auto exchange = [&](int k, uint32_t mine, int &before_lo, int &before_hi) {
+        before_lo = before_hi = 0;
+        if (n_cta == 1) return (int)(mine & 0xffffu);
+        if (tid == 0) s_xchg[k] = mine;
         cluster_sync_all();
-        int before = 0;
-        all = 0;
+        int all = 0;
         for (int r = 0; r < n_cta; ++r) {
-            const int x = (int)cluster_ld(cluster_map(smem_u32(&s_xchg[k]), r));
-            if (r < rank) before += x;
-            all += x;
+            const uint32_t x = cluster_ld(cluster_map(smem_u32(&s_xchg[k]), r));
+            all += (int)(x & 0xffffu);
+            if (r < rank) {
+                before_lo += (int)(x & 0xffffu);
+                before_hi += (int)(x >> 16);
+            }
         }
-        return before;
+        return all;
     };
 
-    // ---- `want` of the keys equal to `prefix` stay, those in the lowest slots
-    int all;
-    for (int s = 0; s < stripes; ++s) {
-        const int i = s * THREADS + tid;
-        const unsigned tie = __ballot_sync(0xffffffffu, i < n && keys[i] == prefix);
-        if (lane == 0) s_cnt[0][s * WARPS + warp] = __popc(tie);
+    // ---- `want` of the s_match keys equal to `prefix` stay, those in the lowest slots: where that is not all of
+    // them, they are counted in order
+    const bool choose = (int)s_match > want;
+    int ties_before = 0, unused;
+    if (choose) {
+#pragma unroll 4
+        for (int s = 0; s < stripes; ++s) {
+            const int i = s * THREADS + tid;
+            const unsigned tie = __ballot_sync(0xffffffffu, i < n && keys[i] == prefix);
+            if (lane == 0) s_cnt[0][s * WARPS + warp] = __popc(tie);
+        }
+        const int ties = stripe_prefix(s_cnt[0], stripes, s_scan);
+        exchange(0, (uint32_t)ties, ties_before, unused);
     }
-    const int ties = stripe_prefix(s_cnt[0], stripes, s_scan);
-    const int ties_before = exchange(0, ties, all);
     // holes (given up below the budget) and moves (kept past it), 16 bits each: at most 32768 per CTA
+#pragma unroll 4
     for (int s = 0; s < stripes; ++s) {
         const int i = s * THREADS + tid;
         const uint32_t k = i < n ? keys[i] : 0u;
-        const bool tie = i < n && k == prefix;
-        const unsigned m = __ballot_sync(0xffffffffu, tie);
-        const bool keep = i < n && (k > prefix || (tie && ties_before + s_cnt[0][s * WARPS + warp] + __popc(m & below) < want));
+        bool keep = i < n && k >= prefix;
+        if (choose) {
+            const bool tie = i < n && k == prefix;
+            const unsigned m = __ballot_sync(0xffffffffu, tie);
+            if (tie) keep = ties_before + s_cnt[0][s * WARPS + warp] + __popc(m & below) < want;
+        }
         const unsigned out = __ballot_sync(0xffffffffu, i < n && i < edge && !keep);
         const unsigned in = __ballot_sync(0xffffffffu, i >= edge && keep);
         if (i < n) keys[i] = keep;
         if (lane == 0) s_cnt[1][s * WARPS + warp] = __popc(out) | __popc(in) << 16;
     }
     const uint32_t both = (uint32_t)stripe_prefix(s_cnt[1], stripes, s_scan);
-    int holes, moves;
-    const int hole_at = exchange(1, (int)(both & 0xffffu), holes), move_at = exchange(2, (int)(both >> 16), moves);
+    int hole_at, move_at;
+    const int holes = exchange(1, both, hole_at, move_at);
     int32_t *src = p.src + (int64_t)row * p.most, *dst = p.dst + (int64_t)row * p.most;
+#pragma unroll 4
     for (int s = 0; s < stripes; ++s) {
         const int i = s * THREADS + tid;
         const bool keep = i < n && keys[i] != 0;

@@ -8,12 +8,14 @@
 // draw what a serial sum would.
 //
 // A cluster per sequence.  Every CTA finds the first rejection by itself (a
-// few loads) and adds up its part of the row in spans of 32 x 16 bytes, two
-// spans per warp in flight, keeping the spans' sums; the CTAs exchange their
-// totals through distributed shared memory; the one whose part the threshold
-// falls into reads the one span again and finds the value.  So the row is read
-// once.  A row of an odd vocabulary does not start on 16 bytes: a lane then
-// takes its 16 bytes out of two aligned ones.
+// few loads) and adds up its part of the row in spans of 2 x 32 x 16 bytes, one
+// per warp at a time, keeping the spans' sums; the CTAs exchange their totals
+// through distributed shared memory; the one whose part the threshold falls
+// into reads the one span again and finds the value.  So the row is read once.
+// A row of an odd vocabulary does not start on 16 bytes: the parts are laid out
+// from the last 16-byte boundary before the target's row, and of the draft's
+// row, where it lies otherwise, a lane takes its 16 bytes out of two aligned
+// ones.
 // Bound by memory: one or two rows of the vocabulary per sequence.
 #pragma once
 
@@ -24,14 +26,14 @@ namespace ver {
 constexpr int THREADS = 256;
 constexpr int PER_SM = 4;               // CTAs resident per SM: 64 registers a thread
 constexpr int WARPS = THREADS / 32;
-constexpr int BATCH = 2;                // spans a warp has in flight
+constexpr int BATCH = 2;                // 16-byte pieces per lane and span
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX_VOCAB = 1 << 20;
 constexpr int MAX_DRAFTS = 64;
 template <typename T>
 constexpr int kPer = 16 / sizeof(T);    // values per lane and span
 template <typename T>
-constexpr int kSpan = 32 * kPer<T>;
+constexpr int kSpan = BATCH * 32 * kPer<T>;
 }  // namespace ver
 
 struct VerifyParams {
@@ -73,39 +75,40 @@ __device__ __forceinline__ unsigned long long cluster_ld64(uint32_t a)
     return v;
 }
 
-// 16 bytes of a row from value j on (any alignment of the row): zeros past hi
+// A row of n values.  load(j): the 16 bytes from value j on, zeros outside the
+// row.  `odd`: how far value j (a multiple of 16 bytes from `first`) lies past
+// a 16-byte boundary, the same for every j.
 template <typename T>
-__device__ __forceinline__ uint4 ver_load(const T *row, int j, int hi)
-{
-    constexpr int N = ver::kPer<T>;
-    const T *at = row + j;
-    const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 15u);
-    // aligned words around the 16 bytes must lie in the row themselves: the ends are read value by value
-    if (j + N > hi || (odd != 0 && (j < N || j + 2 * N > hi))) {
-        T v[N];
+struct VerRow {
+    const T *row;
+    uint32_t odd;
+    __device__ VerRow(const T *r, int first) : row(r), odd((uint32_t)(reinterpret_cast<uintptr_t>(r + first) & 15u)) {}
+    __device__ __forceinline__ uint4 load(int j, int n) const
+    {
+        constexpr int N = ver::kPer<T>;
+        // the aligned words around the 16 bytes must lie in the row themselves: its ends are read value by value
+        if (j < (odd ? N : 0) || j + (odd ? 2 * N : N) > n) {
+            T v[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            v[k] = T(0.f);
-            if (j + k < hi) v[k] = at[k];
+            for (int k = 0; k < N; ++k) {
+                v[k] = T(0.f);
+                if (j + k >= 0 && j + k < n) v[k] = row[j + k];
+            }
+            return *reinterpret_cast<const uint4 *>(v);
         }
-        return *reinterpret_cast<const uint4 *>(v);
+        const uint4 *a = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(row + j) - odd);
+        const uint4 x = __ldg(a);
+        if (odd == 0) return x;
+        const uint4 y = __ldg(a + 1);
+        // bytes odd .. odd+15 of the 32: by two words, by one, by bits
+        uint32_t w[6] = {x.x, x.y, x.z, x.w, y.x, y.y};
+        if (odd & 8) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = y.z, w[5] = y.w;
+        if (odd & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+        const uint32_t s = (odd & 3) * 8;
+        return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                          __funnelshift_r(w[3], w[4], s));
     }
-    const uint4 *a = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)15);
-    const uint4 x = __ldg(a);
-    if (odd == 0) return x;
-    const uint4 y = __ldg(a + 1);
-    // bytes odd .. odd+15 of the 32: by two words, by one, by bits
-    uint32_t w[7] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z}, last = y.w;
-    if (odd & 8) {
-        w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = last;
-    }
-    if (odd & 4) {
-        w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
-    }
-    const uint32_t s = (odd & 3) * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
-                      __funnelshift_r(w[3], w[4], s));
-}
+};
 
 // the sum of the w_j of 16 bytes' worth of values
 template <typename T>
@@ -170,12 +173,13 @@ __global__ void __launch_bounds__(ver::THREADS, ver::PER_SM) spec_verify_kernel(
     const bool rejected = a < n && !s_bad;
     const T *qr = rejected && draft ? draft + a * V : nullptr;
     const int whole_tok = rejected && !draft ? __ldg(p.tokens + (int64_t)b * p.drafts + a) : -1;
-    const int lo = min(p.vocab, rank * p.spans * SPAN), hi = min(p.vocab, lo + p.spans * SPAN);
-
+    // the CTA's first value: `origin` is up to 16 bytes before the row's start, on a boundary
+    const int origin = -(int)((reinterpret_cast<uintptr_t>(pr) & 15u) / sizeof(T)), lo = origin + rank * p.spans * SPAN;
+    const VerRow<T> prow(pr, origin), qrow(qr ? qr : pr, origin);
     // the values of a lane: the row less what is taken off it
     auto load_q = [&](int j, bool plain) {
         if (plain || (!qr && (whole_tok < j || whole_tok >= j + PER))) return make_uint4(0u, 0u, 0u, 0u);
-        if (qr) return ver_load(qr, j, hi);
+        if (qr) return qrow.load(j, p.vocab);
         T v[PER];
 #pragma unroll
         for (int k = 0; k < PER; ++k) v[k] = T(j + k == whole_tok ? 1.f : 0.f);
@@ -186,25 +190,25 @@ __global__ void __launch_bounds__(ver::THREADS, ver::PER_SM) spec_verify_kernel(
     for (int tries = 0; tries < 2; ++tries) {
         const bool plain = tries == 1;                      // the target alone, if nothing of the difference is left
         unsigned long long sum = 0;
-        for (int sp = warp; sp < p.spans; sp += WARPS * BATCH) {
+#pragma unroll 1
+        for (int sp = warp; sp < p.spans; sp += WARPS) {
             uint4 pv[BATCH], qv[BATCH];
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
-                const int j = lo + (sp + k * WARPS) * SPAN + lane * PER;
+                const int j = lo + sp * SPAN + (k * 32 + lane) * PER;
                 pv[k] = qv[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (sp + k * WARPS < p.spans && j < hi) {
-                    pv[k] = ver_load(pr, j, hi);
+                if (j < p.vocab) {
+                    pv[k] = prow.load(j, p.vocab);
                     qv[k] = load_q(j, plain);
                 }
             }
+            unsigned long long w = 0;
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                unsigned long long w = ver_sum<T>(pv[k], qv[k]);
+            for (int k = 0; k < BATCH; ++k) w += ver_sum<T>(pv[k], qv[k]);
 #pragma unroll
-                for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-                if (lane == 0 && sp + k * WARPS < p.spans) s_span[sp + k * WARPS] = w;
-                sum += w;
-            }
+            for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            if (lane == 0) s_span[sp] = w;
+            sum += w;
         }
         if (lane == 0) s_warp[warp] = sum;
         __syncthreads();
@@ -246,32 +250,39 @@ __global__ void __launch_bounds__(ver::THREADS, ver::PER_SM) spec_verify_kernel(
                     }
                     at += __shfl_sync(0xffffffffu, c, 31);
                 }
-                const int j = lo + sp * SPAN + lane * PER;
-                uint4 pv = make_uint4(0u, 0u, 0u, 0u), qv = pv;
-                if (j < hi) {
-                    pv = ver_load(pr, j, hi);
-                    qv = load_q(j, plain);
-                }
-                const unsigned long long x = ver_sum<T>(pv, qv);
-                unsigned long long c = x;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const unsigned long long y = __shfl_up_sync(0xffffffffu, c, o);
-                    if (lane >= o) c += y;
-                }
-                const unsigned m = __ballot_sync(0xffffffffu, at + c > r);
-                if (m && lane == __ffs(m) - 1) {
-                    at += c - x;
-                    const T *pk = reinterpret_cast<const T *>(&pv), *qk = reinterpret_cast<const T *>(&qv);
-                    int tok = -1;
-#pragma unroll
-                    for (int k = 0; k < PER; ++k) {
-                        uint32_t h1 = 0, l1 = 0;
-                        ver_add(ver_f(pk[k]), ver_f(qk[k]), h1, l1);
-                        at += ver_join(h1, l1, 1);
-                        if (tok < 0 && at > r) tok = j + k;
+                for (int half = 0; half < BATCH; ++half) {  // the span's pieces, in order
+                    const int j = lo + sp * SPAN + (half * 32 + lane) * PER;
+                    uint4 pv = make_uint4(0u, 0u, 0u, 0u), qv = pv;
+                    if (j < p.vocab) {
+                        pv = prow.load(j, p.vocab);
+                        qv = load_q(j, plain);
                     }
-                    p.out[(int64_t)b * (p.drafts + 1) + a] = tok;
+                    const unsigned long long x = ver_sum<T>(pv, qv);
+                    unsigned long long c = x;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const unsigned long long y = __shfl_up_sync(0xffffffffu, c, o);
+                        if (lane >= o) c += y;
+                    }
+                    const unsigned m = __ballot_sync(0xffffffffu, at + c > r);
+                    if (m == 0) {
+                        at += __shfl_sync(0xffffffffu, c, 31);
+                        continue;
+                    }
+                    if (lane == __ffs(m) - 1) {
+                        at += c - x;
+                        const T *pk = reinterpret_cast<const T *>(&pv), *qk = reinterpret_cast<const T *>(&qv);
+                        int tok = -1;
+#pragma unroll
+                        for (int k = 0; k < PER; ++k) {
+                            uint32_t h1 = 0, l1 = 0;
+                            ver_add(ver_f(pk[k]), ver_f(qk[k]), h1, l1);
+                            at += ver_join(h1, l1, 1);
+                            if (tok < 0 && at > r) tok = j + k;
+                        }
+                        p.out[(int64_t)b * (p.drafts + 1) + a] = tok;
+                    }
+                    break;
                 }
             }
             if (total == 0 && rank == 0 && tid == 0) p.out[(int64_t)b * (p.drafts + 1) + a] = 0;
@@ -295,7 +306,7 @@ int launch_verify(VerifyParams &p, int seqs, cudaStream_t stream)
     constexpr int each = 16384 / (int)sizeof(T);
     int cl = 1;
     while (cl < ver::MAX_CLUSTER && p.vocab > each * cl) cl *= 2;
-    const int per = (p.vocab + cl - 1) / cl;
+    const int per = (p.vocab + ver::kPer<T> + cl - 1) / cl;       // up to 16 bytes before the row's start besides
     p.spans = (per + ver::kSpan<T> - 1) / ver::kSpan<T>;
     return launch_pdl(spec_verify_kernel<T>, dim3((unsigned)(seqs * cl)), ver::THREADS, (size_t)p.spans * 8 /* <= 8 KB */, stream, cl, p);
 }
