@@ -396,14 +396,18 @@ class KVCache:
 
     @classmethod
     def allocate(cls, seqs: int, cols: int, heads: int, dim: int, page_size: int = 64, dtype=torch.float16,
-                 device=None, track: bool = True) -> "KVCache":
-        """A cache of its own with room for cols*page_size entries per sequence, pages in order, empty."""
+                 device=None, track: bool = True, share: "KVCache | None" = None) -> "KVCache":
+        """A cache of its own with room for cols*page_size entries per sequence, pages in order, empty;
+        with `share`, on the table and lengths of another layer's cache."""
         dev = torch.device(device if device is not None else "cuda")
         shape = (seqs * cols, heads, page_size)
         k, v = (torch.zeros(shape + (dim,), dtype=dtype, device=dev) for _ in range(2))
-        table = torch.arange(seqs * cols, dtype=torch.int32, device=dev).view(seqs, cols)
-        return cls(k, v, table, torch.zeros(seqs, dtype=torch.int32, device=dev),
-                   torch.zeros(shape, dtype=torch.float32, device=dev) if track else None,
+        if share is None:
+            table = torch.arange(seqs * cols, dtype=torch.int32, device=dev).view(seqs, cols)
+            lens = torch.zeros(seqs, dtype=torch.int32, device=dev)
+        else:
+            table, lens = share.table, share.lens
+        return cls(k, v, table, lens, torch.zeros(shape, dtype=torch.float32, device=dev) if track else None,
                    torch.zeros(shape, dtype=torch.int32, device=dev) if track else None)
 
 
