@@ -71,13 +71,10 @@ struct Shape {
     static constexpr int kPad = kCols + 8;                            // floats per row there: no bank conflicts
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
+// 16 bytes to shared memory: `size` (16 or 0) of them from src, zeros after
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t size)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool there)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -298,27 +295,27 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
     };
     // this thread's 16-byte piece of rows cr, cr + RPP, ...
     const int cc = tid % CPR, cr = tid / CPR;
-    const bool piece = cc * 8 < p.c.dim;
+    const uint32_t piece = cc * 8 < p.c.dim ? 16 : 0;         // past dim: zeros
     auto copy = [&](int stage) {
         const uint32_t base = ring + stage * 2 * S::kHalf + cr * (DP * 2);
         const ulonglong2 *rows = s_row[stage] + cr;
-        if (piece && s_row[stage][TILE - 1].x != 0) {         // a whole tile: its last entry is there
+        if (s_row[stage][TILE - 1].x != 0) {                  // a whole tile: its last entry is there
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
                 const ulonglong2 w = rows[i * RPP];
                 const uint32_t dst = base + i * RPP * (DP * 2) + ((cc ^ ((cr + i * RPP) & 7)) << 4);
-                cp16(dst, reinterpret_cast<const uint8_t *>(w.x) + cc * 16);
-                cp16(dst + S::kHalf, reinterpret_cast<const uint8_t *>(w.y) + cc * 16);
+                cp16(dst, reinterpret_cast<const uint8_t *>(w.x) + cc * piece, piece);
+                cp16(dst + S::kHalf, reinterpret_cast<const uint8_t *>(w.y) + cc * piece, piece);
             }
             return;
         }
 #pragma unroll 1
         for (int i = 0; i < PASSES; ++i) {
             const ulonglong2 w = rows[i * RPP];
-            const bool there = w.x != 0 && piece;
+            const uint32_t size = w.x != 0 ? piece : 0;
             const uint32_t dst = base + i * RPP * (DP * 2) + ((cc ^ ((cr + i * RPP) & 7)) << 4);
-            cp16_or_zero(dst, there ? reinterpret_cast<const uint8_t *>(w.x) + cc * 16 : p.c.k, there);
-            cp16_or_zero(dst + S::kHalf, there ? reinterpret_cast<const uint8_t *>(w.y) + cc * 16 : p.c.v, there);
+            cp16(dst, size ? reinterpret_cast<const uint8_t *>(w.x) + cc * 16 : p.c.k, size);
+            cp16(dst + S::kHalf, size ? reinterpret_cast<const uint8_t *>(w.y) + cc * 16 : p.c.v, size);
         }
     };
 
@@ -643,18 +640,20 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
     }
 }
 
-// The second launch.  Blocks 0 .. seqs*heads*rows - 1 join the parts of one row
-// each, if it has any: groups of dim/4 threads take every ways-th part, four
-// in flight, with a running maximum, and meet in shared memory.  The blocks
-// after them (weights wanted) take WEIGHTS entries of a (sequence, head) each:
-// weight[entry] += sum over the rows of 2^(score - log-sum), the scores read
-// side by side along the entries, the log-sums of split rows from their parts.
+// The second launch.  Its first blocks join the parts of rows, `row_blocks` of
+// them for the rows that a CTA of the first launch takes together, each every
+// row_blocks-th row, if the row has parts: groups of dim/4 threads take every
+// ways-th part, four in flight, with a running maximum, and meet in shared
+// memory.  The blocks after them (weights wanted) take JOIN_WEIGHTS entries of
+// a (sequence, head) each: weight[entry] += sum over the rows of
+// 2^(score - log-sum), the scores read side by side along the entries, the
+// log-sums of split rows from their parts, eight lanes to a row.
 constexpr int JOIN_THREADS = 128;
 constexpr int JOIN_WEIGHTS = 1024;
 constexpr int JOIN_ROWS = 2048;      // most rows of a key-value head
 
 template <typename T>
-__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int dp, int kept_rows, int grid, int64_t join_blocks,
+__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int dp, int kept_rows, int grid, int row_blocks, int64_t join_blocks,
                                                                  int chunks)
 {
     using namespace attn;
@@ -666,56 +665,60 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     if (blockIdx.x < join_blocks) {
         pdl_wait();
         pdl_launch_dependents();
-        const int64_t seg = blockIdx.x / p.rows;
-        const int r = (int)(blockIdx.x - seg * p.rows), rt = r / kept_rows, rr = r - rt * kept_rows;
-        const int3 at = p.parts[seg * p.row_tiles + rt];
+        const int64_t x = blockIdx.x / row_blocks, seg = x / p.row_tiles;
+        const int rt = (int)(x - seg * p.row_tiles);
+        const int3 at = p.parts[x];
         if (at.z < 0) return;
         const int per = dp / 4, ways = JOIN_THREADS / per, way = tid / per, col = (tid - way * per) * 4;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        float top = -INFINITY, tot = 0.f;
-        for (int c = at.y + way; c <= at.z; c += ways * 4) {
-            float2 ml[4];
-            float4 v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {                     // past the end: the last part again, without weight
-                const int cc = min(c + k * ways, at.z);
-                const int64_t sl = (int64_t)(cc == at.y ? at.x : 2 * cc) * kept_rows + rr;
-                ml[k] = __ldcg(ml_all + sl);
-                v[k] = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * dp + col));
-            }
-            const float mx = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
-            const float ref = mx == -INFINITY ? 0.f : mx, old = pow2(top - ref);
-            top = mx;
-            tot *= old;
-            y.x *= old, y.y *= old, y.z *= old, y.w *= old;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float w = c + k * ways <= at.z ? pow2(ml[k].x - ref) : 0.f;
-                if (w == 0.f) continue;                       // a part that saw nothing adds nothing
-                tot = fmaf(ml[k].y, w, tot);
-                y.x = fmaf(v[k].x, w, y.x), y.y = fmaf(v[k].y, w, y.y), y.z = fmaf(v[k].z, w, y.z), y.w = fmaf(v[k].w, w, y.w);
-            }
-        }
-        s_y[tid] = y;
-        s_ml[tid] = make_float2(top, tot);
-        __syncthreads();
-        if (way > 0 || col >= p.c.dim) return;
-        for (int k = 1; k < ways; ++k) top = fmaxf(top, s_ml[tid + k * per].x);
-        const float ref = top == -INFINITY ? 0.f : top;
-        tot = 0.f;
-        y = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < ways; ++k) {
-            const float2 ml = s_ml[tid + k * per];
-            const float4 v = s_y[tid + k * per];
-            const float w = pow2(ml.x - ref);
-            tot = fmaf(ml.y, w, tot);
-            y.x = fmaf(v.x, w, y.x), y.y = fmaf(v.y, w, y.y), y.z = fmaf(v.z, w, y.z), y.w = fmaf(v.w, w, y.w);
-        }
-        const float inv = inverse(tot);
+        const int rows_here = min(kept_rows, p.rows - rt * kept_rows);
         const int64_t b = seg / p.c.heads, h = seg - b * p.c.heads;
-        const int t = p.group_div.of(r);
-        *reinterpret_cast<float4 *>(p.out + ((b * p.new_tokens + t) * p.c.heads * p.group + h * p.group + (r - t * p.group)) * p.c.dim + col) =
-            make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+        for (int rr = (int)(blockIdx.x - x * row_blocks); rr < rows_here; rr += row_blocks) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            float top = -INFINITY, tot = 0.f;
+            for (int c = at.y + way; c <= at.z; c += ways * 4) {
+                float2 ml[4];
+                float4 v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {                 // past the end: the last part again, without weight
+                    const int cc = min(c + k * ways, at.z);
+                    const int64_t sl = (int64_t)(cc == at.y ? at.x : 2 * cc) * kept_rows + rr;
+                    ml[k] = __ldcg(ml_all + sl);
+                    v[k] = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * dp + col));
+                }
+                const float mx = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
+                const float ref = mx == -INFINITY ? 0.f : mx, old = pow2(top - ref);
+                top = mx;
+                tot *= old;
+                y.x *= old, y.y *= old, y.z *= old, y.w *= old;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float w = c + k * ways <= at.z ? pow2(ml[k].x - ref) : 0.f;
+                    if (w == 0.f) continue;                   // a part that saw nothing adds nothing
+                    tot = fmaf(ml[k].y, w, tot);
+                    y.x = fmaf(v[k].x, w, y.x), y.y = fmaf(v[k].y, w, y.y), y.z = fmaf(v[k].z, w, y.z), y.w = fmaf(v[k].w, w, y.w);
+                }
+            }
+            __syncthreads();                                  // the row before has been read
+            s_y[tid] = y;
+            s_ml[tid] = make_float2(top, tot);
+            __syncthreads();
+            if (way > 0 || col >= p.c.dim) continue;
+            for (int k = 1; k < ways; ++k) top = fmaxf(top, s_ml[tid + k * per].x);
+            const float ref = top == -INFINITY ? 0.f : top;
+            tot = 0.f;
+            y = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < ways; ++k) {
+                const float2 ml = s_ml[tid + k * per];
+                const float4 v = s_y[tid + k * per];
+                const float w = pow2(ml.x - ref);
+                tot = fmaf(ml.y, w, tot);
+                y.x = fmaf(v.x, w, y.x), y.y = fmaf(v.y, w, y.y), y.z = fmaf(v.z, w, y.z), y.w = fmaf(v.w, w, y.w);
+            }
+            const float inv = inverse(tot);
+            const int r = rt * kept_rows + rr, t = p.group_div.of(r);
+            *reinterpret_cast<float4 *>(p.out + ((b * p.new_tokens + t) * p.c.heads * p.group + h * p.group + (r - t * p.group)) * p.c.dim + col) =
+                make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+        }
         return;
     }
     const int64_t x = blockIdx.x - join_blocks, seg = x / chunks;
@@ -750,29 +753,24 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     pdl_wait();
     pdl_launch_dependents();
     if (first >= len) return;
-    for (int r = tid / 32; r < p.rows; r += JOIN_THREADS / 32) {          // a warp per row's log-sum
-        const int rt = r / kept_rows, rr = r - rt * kept_rows, lane = tid & 31;
-        const int3 at = p.parts[seg * p.row_tiles + rt];
-        float lse = 0.f;
-        if (at.z < 0) {
-            lse = __ldcg(p.lse + seg * p.rows + r);
-        } else {
-            float top = -INFINITY, tot = 0.f;
-            for (int c = at.y + lane; c <= at.z; c += 32) {
-                const float2 ml = __ldcg(ml_all + (int64_t)(c == at.y ? at.x : 2 * c) * kept_rows + rr);
-                const float mx = fmaxf(top, ml.x), ref = mx == -INFINITY ? 0.f : mx;
-                tot = tot * pow2(top - ref) + ml.y * pow2(ml.x - ref);
-                top = mx;
-            }
-            float mx = top;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            tot *= pow2(top - (mx == -INFINITY ? 0.f : mx));
-#pragma unroll
-            for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-            lse = log_sum<T>(mx, tot);
+    for (int r0 = 0; r0 < p.rows; r0 += JOIN_THREADS / 8) {               // eight lanes per row's log-sum
+        const int r = r0 + tid / 8, rt = r / kept_rows, rr = r - rt * kept_rows;
+        const int3 at = r < p.rows ? p.parts[seg * p.row_tiles + rt] : make_int3(0, 0, -1);
+        float top = -INFINITY, tot = 0.f;
+#pragma unroll 4
+        for (int c = at.y + tid % 8; c <= at.z; c += 8) {
+            const float2 ml = __ldcg(ml_all + (int64_t)(c == at.y ? at.x : 2 * c) * kept_rows + rr);
+            const float mx = fmaxf(top, ml.x), ref = mx == -INFINITY ? 0.f : mx;
+            tot = tot * pow2(top - ref) + ml.y * pow2(ml.x - ref);
+            top = mx;
         }
-        if (lane == 0) s_lse[r] = lse;
+        float mx = top;
+#pragma unroll
+        for (int o = 4; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        tot *= pow2(top - (mx == -INFINITY ? 0.f : mx));
+#pragma unroll
+        for (int o = 4; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+        if (r < p.rows && tid % 8 == 0) s_lse[r] = at.z < 0 ? __ldcg(p.lse + seg * p.rows + r) : log_sum<T>(mx, tot);
     }
     __syncthreads();
     if (n <= 0) return;
@@ -780,7 +778,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     float add[EACH];
 #pragma unroll
     for (int k = 0; k < EACH; ++k) add[k] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
     for (int r = 0; r < p.rows; ++r) {
         const float4 a = __ldcg(reinterpret_cast<const float4 *>(s + r * p.cap));
         const float4 c = __ldcg(reinterpret_cast<const float4 *>(s + r * p.cap) + 1);
@@ -951,8 +949,14 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
         return launch_attn<DPc.value, decltype(t), Mc.value, UGc.value>(p, a.grid, s);
     });
     if (rc != MMQ_OK) return rc;
-    const int64_t segs = (int64_t)cache->seqs * cache->heads, join_blocks = segs * a.rows;
+    const int64_t segs = (int64_t)cache->seqs * cache->heads;
+    // blocks for the rows of a segment's part: one each while that is at most sixteen blocks per SM
+    int64_t row_blocks = (int64_t)sm_count() * 16 / a.parts;
+    const int most = a.rows < a.kept_rows ? a.rows : a.kept_rows;
+    row_blocks = row_blocks < 1 ? 1 : row_blocks > most ? most : row_blocks;
+    const int64_t join_blocks = a.parts * row_blocks;
     const int chunks = save ? (int)((a.cap + JOIN_WEIGHTS - 1) / JOIN_WEIGHTS) : 0;
     const auto join = cache->dtype == MMQ_F16 ? attn_join_kernel<__half> : attn_join_kernel<__nv_bfloat16>;
-    return launch_pdl(join, dim3((unsigned)(join_blocks + segs * chunks)), JOIN_THREADS, 0, s, 0, p, a.dp, a.kept_rows, a.grid, join_blocks, chunks);
+    return launch_pdl(join, dim3((unsigned)(join_blocks + segs * chunks)), JOIN_THREADS, 0, s, 0, p, a.dp, a.kept_rows, a.grid,
+                      (int)row_blocks, join_blocks, chunks);
 }
