@@ -62,6 +62,13 @@ __device__ __forceinline__ uint32_t cluster_ld(uint32_t a)
     return v;
 }
 
+__device__ __forceinline__ uint4 cluster_ld4(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
 // Exclusive prefix over the block of one value per thread; `total` is the
 // block's sum.  s: WARPS ints of shared memory.
 __device__ __forceinline__ int block_prefix(int v, int *s, int &total)
@@ -114,7 +121,7 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
 {
     using namespace evict;
     extern __shared__ __align__(16) uint32_t keys[];       // [chunk_cap], then the page ids [cols_cap]
-    __shared__ uint32_t hist[2][BINS];
+    __shared__ __align__(16) uint32_t hist[2][BINS];
     __shared__ int s_cnt[2][STRIPES * WARPS];
     __shared__ __align__(16) int s_scan[WARPS];
     __shared__ uint32_t s_digit, s_above, s_match;
@@ -191,22 +198,23 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
             const uint32_t k = keys[i];
             if ((k & mask) == prefix) atomicAdd(&hs[(k >> shift) & ((1u << bits) - 1)], 1u);
         }
-        // a few bins per thread, from the highest down
-        constexpr int PER = BINS / THREADS;
+        // four bins per thread, from the highest down; a cluster's are added 16 bytes at a time
+        constexpr int PER = 4;
+        static_assert(BINS == PER * THREADS, "");
         const int top = BINS - PER - PER * tid;
         uint32_t c[PER];
-#pragma unroll
-        for (int k = 0; k < PER; ++k) c[k] = 0;
         if (n_cta == 1) {
             __syncthreads();
-#pragma unroll
-            for (int k = 0; k < PER; ++k) c[k] = hs[top + k];
+            *reinterpret_cast<uint4 *>(c) = *reinterpret_cast<const uint4 *>(hs + top);
         } else {
             cluster_sync_all();
-            for (int r = 0; r < n_cta; ++r) {
-                const uint32_t a = cluster_map(smem_u32(hs + top), r);
 #pragma unroll
-                for (int k = 0; k < PER; ++k) c[k] += cluster_ld(a + 4 * k);
+            for (int k = 0; k < PER; ++k) c[k] = 0;
+            const uint32_t a = smem_u32(hs + top);
+#pragma unroll 4
+            for (int r = 0; r < n_cta; ++r) {
+                const uint4 v = cluster_ld4(cluster_map(a, r));
+                c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
             }
         }
         int total, mine = 0;
@@ -414,8 +422,8 @@ extern "C" int mmq_kv_evict(const mmq_kv_cache *cache, int budget, const int32_t
     const int cap = cache->cols * cache->page_size;
     // CTAs per row: as many as the keys need (32768 each), and more while all
     // are resident and each still has 2048 keys
-    int cl = 1;
-    while (cl < evict::MAX_CLUSTER && (cap > evict::MAX_CHUNK * cl || (rows * cl * 2 <= evict::PER_SM * sm_count() && cap > 4096 * cl))) cl *= 2;
+    int cl = (cap + evict::MAX_CHUNK - 1) / evict::MAX_CHUNK;
+    while (cl < evict::MAX_CLUSTER && rows * (cl + 1) <= evict::PER_SM * sm_count() && cap > 2048 * cl) ++cl;
     p.chunk_cap = (cap + cl - 1) / cl;
     p.cols_cap = cache->cols < evict::MAX_COLS ? cache->cols : evict::MAX_COLS;
     return launch_evict(p, rows, cl, s);
