@@ -155,16 +155,17 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
     // Keys; and the bookkeeping of the slots below the budget as if they all
     // stayed: a moved entry overwrites it later.
     for (int i0 = tid; i0 < n; i0 += THREADS * BATCH) {
-        int64_t e[BATCH];
         float w[BATCH];
         int32_t x[BATCH];
+        uint32_t there = 0;
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             const int i = i0 + k * THREADS;
-            e[k] = i < n ? entry(i) : -1;
-            if (e[k] >= 0) {
-                w[k] = __ldg(p.c.weight + e[k]);
-                x[k] = __ldg(p.c.pos + e[k]);
+            const int64_t e = i < n ? entry(i) : -1;
+            if (e >= 0) {
+                w[k] = __ldg(p.c.weight + e);
+                x[k] = __ldg(p.c.pos + e);
+                there |= 1u << k;
             }
         }
 #pragma unroll
@@ -172,12 +173,13 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
             const int i = i0 + k * THREADS;
             if (i >= n) continue;
             uint32_t key = 0;
-            if (e[k] >= 0) {
+            if (there >> k & 1) {
                 const uint32_t u = __float_as_uint(w[k] + 0.f);                     // -0 becomes 0
                 key = x[k] >= keep_from ? 0xffffffffu : u ^ (u & 0x80000000u ? 0xffffffffu : 0x80000000u);
                 if (whole || i < edge) {
-                    p.weight_out[e[k]] = w[k];
-                    p.pos_out[e[k]] = x[k];
+                    const int64_t e = entry(i);
+                    p.weight_out[e] = w[k];
+                    p.pos_out[e] = x[k];
                 }
             }
             if (!whole) keys[i] = key;
