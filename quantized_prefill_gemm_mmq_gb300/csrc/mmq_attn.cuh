@@ -54,14 +54,15 @@ constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
 template <typename T>
 constexpr float kExp = kBf16<T> ? 0.f : 15.f;      // p carries 2^kExp
 
-// DP: dim padded to 64, 128 or 256; MODE, UG: see above
+// DP: dim padded to 64, 96, 128, 192 or 256; MODE, UG: see above
 template <int DP, int MODE, int UG>
 struct Shape {
     static constexpr int kPerWarp = MODE == 0 ? 4 : MODE == 1 ? 8 : 16;   // rows
-    static constexpr int kTile = DP == 64 ? 128 : DP == 256 && UG > 1 ? 32 : 64;      // entries per tile
-    static constexpr int kStages = 3;                                 // tiles in the ring
+    static constexpr int kTile = DP == 64 ? 128 : DP > 128 && UG > 1 ? 32 : 64;       // entries per tile
+    static constexpr int kStages = DP == 192 && UG == 1 ? 2 : 3;      // tiles in the ring
     static constexpr int kPerSm = DP == 256 && UG == 1 ? 1 : 2;       // CTAs resident per SM
-    static constexpr int kHalf = kTile * DP * 2;                      // bytes of K (or V) per stage
+    static constexpr int kStride = DP == 96 ? 256 : DP * 2;           // bytes from row to row: the swizzle takes eight pieces
+    static constexpr int kHalf = kTile * kStride;                     // bytes of K (or V) per stage
     static constexpr int kSmem = kStages * 2 * kHalf;
     static constexpr int kRows = kPerWarp * UG;                       // rows per CTA
     // the four warps' sums are joined in one stage's memory, in as many rounds of columns as fit
@@ -220,7 +221,8 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
     constexpr int PARTS = MODE == 0 ? 1 : MODE == 1 ? (BF ? 2 : 1) : (BF ? 3 : 2);     // products per tensor-core step
     constexpr int TILE = S::kTile, STAGES = S::kStages, TG = 4 / UG, TW = TILE / TG;    // TW: entries per warp and tile
     constexpr int NT = TW / 8, KS = DP / 16, DT = DP / 8, ROWS = S::kRows;
-    constexpr int CPR = DP / 8, RPP = THREADS / CPR, PASSES = TILE / RPP;   // 16-byte copies per row, rows per pass
+    constexpr int CPR = DP / 8, PASSES = TILE * CPR / THREADS;              // 16-byte copies per row, and per thread and tile
+    static_assert(TILE * CPR % THREADS == 0, "copies come out even");
 
     pdl_wait();
     pdl_launch_dependents();       // the joining launch may start; what this one writes it reads after this one's end
@@ -293,27 +295,34 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
         }
         return r;
     };
-    // this thread's 16-byte piece of rows cr, cr + RPP, ...
-    const int cc = tid % CPR, cr = tid / CPR;
-    const uint32_t piece = cc * 8 < p.c.dim ? 16 : 0;         // past dim: zeros
+    // This thread's 16-byte pieces of a tile: number tid + k*THREADS, row by row.  Past dim: zeros.
+    constexpr bool EVEN = THREADS % CPR == 0;                 // the same piece of every (THREADS/CPR)th row
     auto copy = [&](int stage) {
-        const uint32_t base = ring + stage * 2 * S::kHalf + cr * (DP * 2);
-        const ulonglong2 *rows = s_row[stage] + cr;
-        if (s_row[stage][TILE - 1].x != 0) {                  // a whole tile: its last entry is there
+        const uint32_t base = ring + stage * 2 * S::kHalf;
+        const bool full = s_row[stage][TILE - 1].x != 0;      // a whole tile: its last entry is there
+        auto place = [&](int k, int &row, int &cc, uint32_t &dst, uint32_t &piece) {
+            row = EVEN ? tid / CPR + k * (THREADS / CPR) : (tid + k * THREADS) / CPR;
+            cc = EVEN ? tid % CPR : (tid + k * THREADS) % CPR;
+            dst = base + row * S::kStride + ((cc ^ (row & 7)) << 4);
+            piece = cc * 8 < p.c.dim ? 16 : 0;
+        };
+        int row, cc;
+        uint32_t dst, piece;
+        if (full) {
 #pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                const ulonglong2 w = rows[i * RPP];
-                const uint32_t dst = base + i * RPP * (DP * 2) + ((cc ^ ((cr + i * RPP) & 7)) << 4);
+            for (int k = 0; k < PASSES; ++k) {
+                place(k, row, cc, dst, piece);
+                const ulonglong2 w = s_row[stage][row];
                 cp16(dst, reinterpret_cast<const uint8_t *>(w.x) + cc * piece, piece);
                 cp16(dst + S::kHalf, reinterpret_cast<const uint8_t *>(w.y) + cc * piece, piece);
             }
             return;
         }
 #pragma unroll 1
-        for (int i = 0; i < PASSES; ++i) {
-            const ulonglong2 w = rows[i * RPP];
+        for (int k = 0; k < PASSES; ++k) {
+            place(k, row, cc, dst, piece);
+            const ulonglong2 w = s_row[stage][row];
             const uint32_t size = w.x != 0 ? piece : 0;
-            const uint32_t dst = base + i * RPP * (DP * 2) + ((cc ^ ((cr + i * RPP) & 7)) << 4);
             cp16(dst, size ? reinterpret_cast<const uint8_t *>(w.x) + cc * 16 : p.c.k, size);
             cp16(dst + S::kHalf, size ? reinterpret_cast<const uint8_t *>(w.y) + cc * 16 : p.c.v, size);
         }
@@ -407,7 +416,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
 
         const int base = cur.tile * TILE + tg * TW;           // the warp's first entry
         if (base < cur.len) {
-            const uint32_t kb = ring + stage * 2 * S::kHalf + tg * TW * (DP * 2), vb = kb + S::kHalf;
+            const uint32_t kb = ring + stage * 2 * S::kHalf + tg * TW * S::kStride, vb = kb + S::kHalf;
             // ---- scores, before their row's factor
             float s[NT][RP][2];
             const int seen = cur.len - n_new + 1;             // entries that every row sees
@@ -416,7 +425,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
             for (int nt = 0; nt < NT; ++nt) {
                 float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};     // two chains: even steps, odd steps
                 // lane's row address: entry nt*8 + lane%8, chunk group lane/8
-                const uint32_t ra = kb + (nt * 8 + (lane & 7)) * (DP * 2);
+                const uint32_t ra = kb + (nt * 8 + (lane & 7)) * S::kStride;
 #pragma unroll
                 for (int k2 = 0; k2 < KS / 2; ++k2) {
                     uint32_t b[4];
@@ -505,7 +514,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                 for (int e = max(seen - base, 0); e < e1; ++e)
                     for (int w = lane; w < DP / 2; w += 32) {
                         uint32_t v;
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(vb + e * (DP * 2) + w * 4));
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(vb + e * S::kStride + (((w >> 2) ^ (e & 7)) << 4) + (w & 3) * 4));
                         bad |= not_finite2<T>(v);
                     }
                 if (__any_sync(0xffffffffu, bad)) passes = n_new;
@@ -527,7 +536,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                     for (int k = 0; k < NT / 2; ++k) {
                         uint32_t b[4];
                         const int e = k * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, ch = d2 * 2 + (lane >> 4);
-                        ldsm4t(b, vb + e * (DP * 2) + ((ch ^ (e & 7)) << 4));
+                        ldsm4t(b, vb + e * S::kStride + ((ch ^ (e & 7)) << 4));
                         if (passes > 1) {
                             const int tok = base + k * 16 + 2 * j;
                             const uint32_t m0 = (tok < view ? 0xffffu : 0u) | (tok + 1 < view ? 0xffff0000u : 0u);
@@ -822,12 +831,14 @@ int attn_dispatch(const AttnPlan &a, int dtype, F f)
         if constexpr (attn::kBf16<decltype(t)>) {
             if (a.mode == 0) return f(t, DPc, integral_constant<int, 0>(), one);
         }
-        if constexpr (DPc.value == 256) return with_ug(t, DPc, one);
+        if constexpr (DPc.value > 128) return with_ug(t, DPc, one);
         else return a.mode == 1 ? f(t, DPc, one, one) : with_ug(t, DPc, integral_constant<int, 2>());
     };
     const auto with_type = [&](auto t) {
         return a.dp == 64    ? with_dp(t, integral_constant<int, 64>())
+               : a.dp == 96  ? with_dp(t, integral_constant<int, 96>())
                : a.dp == 128 ? with_dp(t, integral_constant<int, 128>())
+               : a.dp == 192 ? with_dp(t, integral_constant<int, 192>())
                              : with_dp(t, integral_constant<int, 256>());
     };
     return dtype == MMQ_F16 ? with_type(__half()) : with_type(__nv_bfloat16());
@@ -836,9 +847,9 @@ int attn_dispatch(const AttnPlan &a, int dtype, F f)
 inline AttnPlan attn_plan(const mmq_kv_cache &c, int q_heads, int new_tokens, bool save)
 {
     AttnPlan a;
-    a.dp = c.dim <= 64 ? 64 : c.dim <= 128 ? 128 : 256;
+    a.dp = c.dim <= 64 ? 64 : c.dim <= 96 ? 96 : c.dim <= 128 ? 128 : c.dim <= 192 ? 192 : 256;
     a.rows = q_heads / c.heads * new_tokens;
-    a.mode = c.dtype == MMQ_BF16 && a.rows <= 4 ? 0 : a.rows <= 8 || a.dp == 256 ? 1 : 2;
+    a.mode = c.dtype == MMQ_BF16 && a.rows <= 4 ? 0 : a.rows <= 8 || a.dp > 128 ? 1 : 2;
     const int per_warp = a.mode == 2 ? 16 : 8;
     a.ug = a.rows <= per_warp ? 1 : a.rows <= 2 * per_warp ? 2 : 4;
     int tile = 0, per_sm = 0;
