@@ -64,6 +64,9 @@ struct Shape {
     static constexpr int kStride = DP == 96 ? 256 : DP * 2;           // bytes from row to row: the swizzle takes eight pieces
     static constexpr int kHalf = kTile * kStride;                     // bytes of K (or V) per stage
     static constexpr int kSmem = kStages * 2 * kHalf;
+    static constexpr bool kFull = DP == 128 && MODE == 2;             // registers are
+    static constexpr int kNg = kFull ? 1 : UG == 1 ? 2 : 8;           // eight-entry groups of scores at a time
+    static constexpr int kDg = kFull ? 2 : 4;                         // eight-value groups of sums at a time
     static constexpr int kRows = kPerWarp * UG;                       // rows per CTA
     // the four warps' sums are joined in one stage's memory, in as many rounds of columns as fit
     static constexpr int fit(int rounds) { return 4 * kPerWarp * (DP / rounds + 8) * 4 <= 2 * kHalf ? rounds : fit(rounds * 2); }
@@ -103,7 +106,7 @@ template <>
 __device__ __forceinline__ void mma16816<__half>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                  uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -111,7 +114,7 @@ template <>
 __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                         uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -232,7 +235,10 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
     const uint32_t ring = smem_u32(smem);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int ug = warp % UG, tg = warp / UG;
+    // which rows and entries the warp takes: turned by two in every other CTA of an SM, so that warps without rows
+    // (33 to 48 rows of 64) are not all on the same scheduler
+    const int turned = UG == 4 && blockIdx.x >= gridDim.x / 2 ? (warp + 2) % 4 : warp;
+    const int ug = turned % UG, tg = turned / UG;
     const int g = lane >> 2, j = lane & 3;
     const int gr = MODE == 0 ? g & 3 : g;                     // the quad's (first) row in the warp
     const bool holds = MODE != 0 || g < 4;                    // MODE 0: quads 4-7 compute the rows of 0-3 again
@@ -415,37 +421,50 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
         const ulonglong2 nrow = look_up(i + STAGES < n_units);    // its rows take the place of tile i's
 
         const int base = cur.tile * TILE + tg * TW;           // the warp's first entry
-        if (base < cur.len) {
+        if (base < cur.len && rt * ROWS + ug * S::kPerWarp < p.rows) {
             const uint32_t kb = ring + stage * 2 * S::kHalf + tg * TW * S::kStride, vb = kb + S::kHalf;
             // ---- scores, before their row's factor
             float s[NT][RP][2];
             const int seen = cur.len - n_new + 1;             // entries that every row sees
             const bool edge = base + TW > seen;               // some row may not see all of the warp's
+            // Independent chains of products side by side, since one takes some 20 cycles after the one before it:
+            // NG times eight entries at a time, each in one chain, or two (even and odd steps) where NG is small.
+            // (Sixteen rows of 128 values fill the registers: there more chains spill, and 163 us became 172.)
+            constexpr int CH = S::kNg <= 2 ? 2 : 1, NG = S::kNg < NT ? S::kNg : NT;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};     // two chains: even steps, odd steps
-                // lane's row address: entry nt*8 + lane%8, chunk group lane/8
-                const uint32_t ra = kb + (nt * 8 + (lane & 7)) * S::kStride;
+            for (int n0 = 0; n0 < NT; n0 += NG) {
+                float acc[NG][CH][4];
 #pragma unroll
-                for (int k2 = 0; k2 < KS / 2; ++k2) {
-                    uint32_t b[4];
-                    ldsm4(b, ra + (((k2 * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
+                for (int n = 0; n < NG; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int x = 0; x < CH; ++x) acc[n][x][0] = acc[n][x][1] = acc[n][x][2] = acc[n][x][3] = 0.f;
 #pragma unroll
-                        for (int x = 0; x < PARTS; ++x) {
-                            const uint32_t(&a)[4] = qf[x][2 * k2 + e];
-                            mma16816<T>(acc[e], a[0], RP == 1 && x == 1 ? 0u : a[1], a[2], RP == 1 && x == 1 ? 0u : a[3], b[2 * e], b[2 * e + 1]);
-                        }
-                }
+                for (int k2 = 0; k2 < KS / 2; ++k2)
 #pragma unroll
-                for (int rp = 0; rp < RP; ++rp)
+                    for (int n = 0; n < NG; ++n) {
+                        uint32_t b[4];                        // lane's row: entry nt*8 + lane%8, piece k2*4 + lane/8
+                        ldsm4(b, kb + ((n0 + n) * 8 + (lane & 7)) * S::kStride + (((k2 * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = RP == 1 ? (acc[0][e] + acc[1][e]) + (acc[0][2 + e] + acc[1][2 + e]) : acc[0][2 * rp + e] + acc[1][2 * rp + e];
-                        if (MODE == 0) x += __shfl_xor_sync(0xffffffffu, x, 16);
-                        s[nt][rp][e] = x;
+                        for (int x = 0; x < PARTS; ++x)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t(&a)[4] = qf[x][2 * k2 + e];
+                                mma16816<T>(acc[n][e % CH], a[0], RP == 1 && x == 1 ? 0u : a[1], a[2], RP == 1 && x == 1 ? 0u : a[3],
+                                            b[2 * e], b[2 * e + 1]);
+                            }
                     }
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int rp = 0; rp < RP; ++rp)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = acc[n][0][2 * rp + e];
+                            if (CH == 2) x += acc[n][CH - 1][2 * rp + e];
+                            if (RP == 1) x += CH == 2 ? acc[n][0][2 + e] + acc[n][CH - 1][2 + e] : acc[n][0][2 + e];
+                            if (MODE == 0) x += __shfl_xor_sync(0xffffffffu, x, 16);
+                            s[n0 + n][rp][e] = x;
+                        }
             }
             if (base + TW > min(limit[0], limit[RP - 1])) {
 #pragma unroll
@@ -530,36 +549,40 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                     keep[rp] = take[rp] ? alpha[rp] : 1.f;
                 }
 #pragma unroll
-                for (int d2 = 0; d2 < DT / 2; ++d2) {
-                    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                for (int dg = 0; dg < DT / S::kDg; ++dg) {    // kDg chains side by side
+                    float y[S::kDg][4];
 #pragma unroll
-                    for (int k = 0; k < NT / 2; ++k) {
-                        uint32_t b[4];
-                        const int e = k * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, ch = d2 * 2 + (lane >> 4);
-                        ldsm4t(b, vb + e * S::kStride + ((ch ^ (e & 7)) << 4));
-                        if (passes > 1) {
-                            const int tok = base + k * 16 + 2 * j;
-                            const uint32_t m0 = (tok < view ? 0xffffu : 0u) | (tok + 1 < view ? 0xffff0000u : 0u);
-                            const uint32_t m1 = (tok + 8 < view ? 0xffffu : 0u) | (tok + 9 < view ? 0xffff0000u : 0u);
-                            b[0] &= m0, b[1] &= m1, b[2] &= m0, b[3] &= m1;
+                    for (int c = 0; c < S::kDg; ++c) y[c][0] = y[c][1] = y[c][2] = y[c][3] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < NT / 2; ++k)
+#pragma unroll
+                        for (int d2 = 0; d2 < S::kDg / 2; ++d2) {
+                            uint32_t b[4];
+                            const int e = k * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, ch = dg * S::kDg + d2 * 2 + (lane >> 4);
+                            ldsm4t(b, vb + e * S::kStride + ((ch ^ (e & 7)) << 4));
+                            if (passes > 1) {
+                                const int tok = base + k * 16 + 2 * j;
+                                const uint32_t m0 = (tok < view ? 0xffffu : 0u) | (tok + 1 < view ? 0xffff0000u : 0u);
+                                const uint32_t m1 = (tok + 8 < view ? 0xffffu : 0u) | (tok + 9 < view ? 0xffff0000u : 0u);
+                                b[0] &= m0, b[1] &= m1, b[2] &= m0, b[3] &= m1;
+                            }
+#pragma unroll
+                            for (int x = 0; x < PARTS; ++x) {
+                                const uint32_t(&a)[4] = pf[x][k];
+                                const uint32_t a1 = RP == 1 && x == 1 ? 0u : a[1], a3 = RP == 1 && x == 1 ? 0u : a[3];
+                                mma16816<T>(y[2 * d2], a[0], a1, a[2], a3, b[0], b[1]);
+                                mma16816<T>(y[2 * d2 + 1], a[0], a1, a[2], a3, b[2], b[3]);
+                            }
                         }
 #pragma unroll
-                        for (int x = 0; x < PARTS; ++x) {
-                            const uint32_t(&a)[4] = pf[x][k];
-                            const uint32_t a1 = RP == 1 && x == 1 ? 0u : a[1], a3 = RP == 1 && x == 1 ? 0u : a[3];
-                            mma16816<T>(acc[0], a[0], a1, a[2], a3, b[0], b[1]);
-                            mma16816<T>(acc[1], a[0], a1, a[2], a3, b[2], b[3]);
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < S::kDg; ++c)
 #pragma unroll
                         for (int rp = 0; rp < RP; ++rp)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float add = RP == 1 ? acc[c][e] + acc[c][2 + e] : acc[c][2 * rp + e];
-                                float &y = o[2 * d2 + c][rp][e];
-                                y = fmaf(y, keep[rp], take[rp] ? add : 0.f);
+                                const float add = RP == 1 ? y[c][e] + y[c][2 + e] : y[c][2 * rp + e];
+                                float &sum = o[S::kDg * dg + c][rp][e];
+                                sum = fmaf(sum, keep[rp], take[rp] ? add : 0.f);
                             }
                 }
             }
@@ -587,7 +610,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
 #pragma unroll
         for (int rp = 0; rp < RP; ++rp) {
             l[rp] = quad_sum(l[rp]);
-            if (j == 0 && holds) s_ml[warp][gr + 8 * rp] = make_float2(m[rp], l[rp]);
+            if (j == 0 && holds) s_ml[turned][gr + 8 * rp] = make_float2(m[rp], l[rp]);
         }
         if constexpr (MODE == 0) {
 #pragma unroll
@@ -601,7 +624,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
 #pragma unroll
             for (int rp = 0; rp < RP; ++rp)
                 if (holds && row0 + 8 * rp < p.rows) {
-                    float *mine = sums + (warp * S::kPerWarp + gr + 8 * rp) * S::kPad + 2 * j;
+                    float *mine = sums + (turned * S::kPerWarp + gr + 8 * rp) * S::kPad + 2 * j;
 #pragma unroll
                     for (int x = 0; x < DT / S::kRounds; ++x) {
                         const int dt = round * (DT / S::kRounds) + x;
