@@ -426,6 +426,34 @@ def _on(call: str, fn, index: int, *args):
         raise MMQError(call, st)
 
 
+_BLOCKS: dict = {}          # (stream, shape, dtype) -> small outputs not handed out yet
+_BLOCK_SLOTS, _BLOCK_MAX = 64, 16384
+
+
+def _fresh(shape: tuple, dtype, device, index: int) -> torch.Tensor:
+    """An uninitialised output tensor.
+
+    Small ones (up to 16384 elements) are cut from a block of 64, each handed out once: an
+    allocation after a kernel launch takes 5 to 7 us of host time, as long as the smallest
+    calls themselves.  A block belongs to the stream it was allocated under, as the allocator
+    has it; while a graph is captured, outputs come from the graph's own memory."""
+    n = 1
+    for s in shape:
+        n *= s
+    if n > _BLOCK_MAX or index != torch.cuda.current_device() or torch.cuda.is_current_stream_capturing():
+        return torch.empty(shape, dtype=dtype, device=device)
+    key = (_raw_stream(index), shape, dtype)
+    try:
+        return _BLOCKS[key].pop()
+    except (KeyError, IndexError):
+        if len(_BLOCKS) >= 64:
+            _BLOCKS.clear()
+        slots = list(torch.empty((_BLOCK_SLOTS,) + shape, dtype=dtype, device=device).unbind(0))
+        out = slots.pop()
+        _BLOCKS[key] = slots
+        return out
+
+
 class RopeTable:
     """Rotation of mmq_rope_append: freq int64 [rot/2] (turns per position as 64-bit
     fractions), rot values of each head rotated, magnitude times the result."""
@@ -517,7 +545,7 @@ def rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tenso
     if rope.rot > dim or rope.freq.get_device() != index:
         raise ValueError("the table rotates more values than a head has, or is on another device")
     if out is None:
-        out = torch.empty((rows, q_heads, dim), dtype=torch.float32, device=cache.device)
+        out = _fresh((rows, q_heads, dim), torch.float32, cache.device, index)
         ldo = q_heads * dim
     else:
         ldo = _rows(out, "out", rows, q_heads, dim, index)
@@ -573,7 +601,7 @@ def attn_decode(cache: KVCache, q: torch.Tensor, scale: float | None = None, new
     if new is not None:
         _need(new, "new", torch.int32, (cache.seqs,), index)
     if out is None:
-        out = torch.empty((rows, q_heads, dim), dtype=torch.float32, device=cache.device)
+        out = _fresh((rows, q_heads, dim), torch.float32, cache.device, index)
     else:
         _need(out, "out", torch.float32, (rows, q_heads, dim), index)
     key = (q_heads, n, accumulate)
@@ -648,7 +676,7 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.
         _need(count, "count", torch.int32, (B,), index)
     if out is None:
         dev = target.device
-        res, acc = torch.empty((B, n1), dtype=torch.int32, device=dev), torch.empty((B,), dtype=torch.int32, device=dev)
+        res, acc = _fresh((B, n1), torch.int32, dev, index), _fresh((B,), torch.int32, dev, index)
     else:
         res, acc = out
         _need(res, "out[0]", torch.int32, (B, n1), index)

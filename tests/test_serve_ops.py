@@ -531,6 +531,35 @@ def test_verify_bad_tokens_and_counts_are_reported(ops):
     ops.check_status()
 
 
+# ---------------------------------------------------------------- outputs ---
+
+def test_outputs_are_the_callers(ops):
+    """Small outputs come out of shared blocks: none is handed out twice, on whatever stream, and a captured graph's
+    output is not one of them."""
+    cache = make_cache(ops, [30], 2, 64, 16)
+    qs = [torch.randn((1, 4, 64)).cuda() for _ in range(70)]
+    first = [ops.attn_decode(cache, q) for q in qs]
+    kept = [o.clone() for o in first]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = [ops.attn_decode(cache, q) for q in qs]
+    side.synchronize()
+    every = first + second
+    spans = sorted((o.data_ptr(), o.data_ptr() + o.numel() * 4) for o in every)
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+    assert all(torch.equal(a, b) for a, b in zip(first, kept)) and all(torch.equal(a, b) for a, b in zip(second, kept))
+    ws = ops.attn_workspace(cache, 4)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ops.attn_decode(cache, qs[3], workspace=ws)
+    more = [ops.attn_decode(cache, q) for q in qs]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, kept[3]) and all(torch.equal(a, b) for a, b in zip(more, kept))
+    assert not any(o.data_ptr() == out.data_ptr() for o in more)
+
+
 # --------------------------------------------------------------- refusals ---
 
 def test_refusals(ops):
