@@ -60,7 +60,7 @@ struct Shape {
     static constexpr int kPerWarp = MODE == 0 ? 4 : MODE == 1 ? 8 : 16;   // rows
     static constexpr int kTile = DP == 64 ? 128 : DP > 128 && UG > 1 ? 32 : 64;       // entries per tile
     static constexpr int kStages = DP == 192 && UG == 1 ? 2 : 3;      // tiles in the ring
-    static constexpr int kPerSm = DP == 256 && UG == 1 ? 1 : 2;       // CTAs resident per SM
+    static constexpr int kPerSm = 2;                                  // CTAs resident per SM
     static constexpr int kStride = DP == 96 ? 256 : DP * 2;           // bytes from row to row: the swizzle takes eight pieces
     static constexpr int kHalf = kTile * kStride;                     // bytes of K (or V) per stage
     static constexpr int kSmem = kStages * 2 * kHalf;
@@ -832,8 +832,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
 // Which kernel: dim padded, rows per operand (MODE) and warps along the rows.
 // Up to 16, 32 and 64 rows, one, two and four warps take sixteen each, the
 // remaining warps split the entries; for heads above 128 sixteen rows do not
-// fit the registers, and warps take eight.  More rows than a CTA takes are dealt
-// to further CTAs, which read the cache again (from L2).
+// fit the registers, and warps take eight.  Heads above 192 leave two warps of
+// four without rows rather than splitting 64 entries four ways: tiles of 32
+// let two CTAs share an SM (1 x 20000 entries of 8 heads, f16: 137 us against
+// 157).  More rows than a CTA takes are dealt to further CTAs, which read the
+// cache again (from L2).
 struct AttnPlan {
     int dp, mode, ug, rows, kept_rows, row_tiles, grid;
     int64_t tiles, cap, part_floats, score_floats, lse_floats, parts;
@@ -852,9 +855,11 @@ int attn_dispatch(const AttnPlan &a, int dtype, F f)
     const auto with_dp = [&](auto t, auto DPc) {
         constexpr integral_constant<int, 1> one;
         if constexpr (attn::kBf16<decltype(t)>) {
-            if (a.mode == 0) return f(t, DPc, integral_constant<int, 0>(), one);
+            if (a.mode == 0) return f(t, DPc, integral_constant<int, 0>(), integral_constant<int, DPc.value == 256 ? 2 : 1>());
         }
-        if constexpr (DPc.value > 128) return with_ug(t, DPc, one);
+        if constexpr (DPc.value == 256)
+            return a.ug == 2 ? f(t, DPc, one, integral_constant<int, 2>()) : f(t, DPc, one, integral_constant<int, 4>());
+        else if constexpr (DPc.value == 192) return with_ug(t, DPc, one);
         else return a.mode == 1 ? f(t, DPc, one, one) : with_ug(t, DPc, integral_constant<int, 2>());
     };
     const auto with_type = [&](auto t) {
@@ -874,7 +879,7 @@ inline AttnPlan attn_plan(const mmq_kv_cache &c, int q_heads, int new_tokens, bo
     a.rows = q_heads / c.heads * new_tokens;
     a.mode = c.dtype == MMQ_BF16 && a.rows <= 4 ? 0 : a.rows <= 8 || a.dp > 128 ? 1 : 2;
     const int per_warp = a.mode == 2 ? 16 : 8;
-    a.ug = a.rows <= per_warp ? 1 : a.rows <= 2 * per_warp ? 2 : 4;
+    a.ug = a.rows <= per_warp && a.dp < 256 ? 1 : a.rows <= 2 * per_warp ? 2 : 4;
     int tile = 0, per_sm = 0;
     attn_dispatch(a, c.dtype, [&](auto, auto DPc, auto Mc, auto UGc) {
         using S = attn::Shape<DPc.value, Mc.value, UGc.value>;
