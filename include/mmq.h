@@ -490,7 +490,7 @@ int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, int rot, flo
  * j / (q_heads/heads); row t < new_len[b] (NULL: new_tokens) of sequence b
  * sees the slots below len[b] - new_len[b] + t + 1:
  *     s = scale * q.k,  p = exp(s - max) / sum,  out = sum p v
- * out [seqs*new_tokens][q_heads][dim] f32, contiguous.  A row that sees no
+ * out [seqs*new_tokens][q_heads][dim] f32, contiguous, not q.  A row that sees no
  * slot, or with t >= new_len[b], gets 0.  What a row does not see has no
  * influence on it, whatever it holds (stale NaN or Inf included).  Statistics
  * and sums are f32; q and p enter the tensor core as sums of two f16 (three

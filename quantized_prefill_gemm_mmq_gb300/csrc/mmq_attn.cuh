@@ -21,8 +21,9 @@
 // Tiles.  K and V rows are gathered through the page table with 16-byte
 // cp.async into a ring of stages (any page size and stride; entries past
 // the length arrive as zeros), chunk-XOR swizzled so that ldmatrix reads
-// without bank conflicts.  The table entries of a tile are fetched one
-// iteration before its copies are issued.
+// without bank conflicts.  The addresses of a tile's rows are computed once,
+// an iteration before its copies are issued (per copy they were more than half
+// of all instructions: 131071 entries took 120 us).
 //
 // Products run on the warp-level tensor core (16-row operand), with q and p
 // split into parts of the cache's type that add up to 22 bits (f16, two parts)
@@ -31,14 +32,20 @@
 // (MODE 0), rows 0-3 hold the first parts, 4-7 the second, 8-11 the third; up
 // to eight rows (MODE 1), the upper eight hold the first part, the lower eight
 // the second, and bf16's third takes a second product.  More rows (MODE 2):
-// sixteen rows per operand, one product per part.  q is scaled by a power of two per row to lie below 2, and
-// for f16 p carries 2^15, so that f16's range does not clip either.  The sums
-// over a tile's entries stay in f32 and are added to the running sums with f32
-// FMAs.
+// sixteen rows per operand, one product per part.  q is scaled by a power of
+// two per row to lie below 2, and for f16 p carries 2^15, so that f16's range
+// does not clip either.  The sums over a tile's entries stay in f32 and are
+// added to the running sums with f32 FMAs.
 //
 // UG warps of the four take these rows each over the same entries and 4/UG
 // warps split a tile's entries (with their own running maximum, joined at the
 // segment's end), so that up to 64 rows share one read of the cache.
+//
+// Measured (a call, both launches): one token over 131071 entries of 8 heads of
+// 128, f16, 88 us = 6.1 TB/s; a ragged batch of 16 up to 32768, bf16, 190 us =
+// 6.7 TB/s (the copy rate is 6.8); over 513 entries of 32 heads 7.6 us; five
+// tokens of 8 sequences up to 4099, heads of 64 (20 rows), 28 us, where the
+// tensor pipe is 35 % active and two warps per scheduler set the pace.
 #pragma once
 
 #include <type_traits>
@@ -955,6 +962,7 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     if (rc != MMQ_OK) return rc;
     if (ldq < (int64_t)q_heads * cache->dim || !(scale - scale == 0.f)) return MMQ_ERR_SHAPE;
     if (cache->seqs == 0) return MMQ_OK;
+    if (out == q) return MMQ_ERR_SHAPE;                   // rows are read by several CTAs, at any time
     if (!q || !out || !work || (accumulate && !cache->weight)) return MMQ_ERR_NULL;
     if (!aligned16(q) || (ldq & 3) || !aligned16(out) || !aligned16(work) || (accumulate && !aligned16(cache->weight)))
         return MMQ_ERR_ALIGN;

@@ -51,7 +51,9 @@ inline int check_cache(const mmq_kv_cache *c)
 
 // Launch under programmatic dependent launch: the kernel may start while the
 // one before it in the stream finishes, and waits for that one's end (pdl_wait,
-// the first thing every kernel here does) before it touches memory.
+// the first thing every kernel here does) before it touches memory.  What the
+// one before may have written is read with plain loads, not through the
+// read-only path: that one promises data which nobody writes during the kernel.
 // cluster: CTAs per cluster, 0 for none.
 template <typename... P, typename... A>
 int launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster, A... args)
@@ -77,7 +79,7 @@ int launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaSt
 // A sequence's length, limited to what its table row can hold.
 __device__ __forceinline__ int cache_len(const mmq_kv_cache &c, int b, int kid)
 {
-    const int n = __ldg(c.len + b), cap = c.cols * c.page_size;
+    const int n = *(c.len + b), cap = c.cols * c.page_size;
     if (n >= 0 && n <= cap) return n;
     record_error(MMQ_ERR_INDEX, kid, SITE_LEN);
     return n < 0 ? 0 : cap;
@@ -86,7 +88,7 @@ __device__ __forceinline__ int cache_len(const mmq_kv_cache &c, int b, int kid)
 // Page of table column `col` of sequence b, or -1 (reported) if it is none.
 __device__ __forceinline__ int cache_page(const mmq_kv_cache &c, int b, int col, int kid)
 {
-    const int pg = __ldg(c.table + (int64_t)b * c.cols + col);
+    const int pg = *(c.table + (int64_t)b * c.cols + col);
     if (pg >= 0 && pg < c.pages) return pg;
     record_error(MMQ_ERR_INDEX, kid, SITE_PAGE);
     return -1;
@@ -96,7 +98,7 @@ __device__ __forceinline__ int cache_page(const mmq_kv_cache &c, int b, int col,
 __device__ __forceinline__ int new_count(const int32_t *new_len, int b, int most, int kid)
 {
     if (!new_len) return most;
-    const int n = __ldg(new_len + b);
+    const int n = *(new_len + b);
     if (n >= 0 && n <= most) return n;
     record_error(MMQ_ERR_INDEX, kid, SITE_COUNT);
     return n < 0 ? 0 : most;

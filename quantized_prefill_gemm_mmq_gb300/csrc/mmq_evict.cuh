@@ -19,7 +19,11 @@
 // counts.  For the moves a warp looks up 32 at once, one per lane, then copies
 // them one after the other, a 16-byte piece of K or V per lane.
 // Bound by memory: 8 B per entry and head for weight and position, 8 B for
-// each that stays, 8 dim B per move.
+// each that stays, 8 dim B per move; with few moves by the latency of the
+// selection's passes.
+// Measured: 16 sequences up to 32768 entries of 8 heads of 128 down to 4096,
+// 105 us, of which 72 us move 485 MB (6.7 TB/s); 1100 entries of 32 heads down
+// to 1024, 8.6 us.
 #pragma once
 
 namespace mmq {
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
     const int chunk = (len + n_cta - 1) / n_cta;
     const int lo = min(len, rank * chunk), n = min(len, lo + chunk) - lo;
     const int stripes = (n + THREADS - 1) / THREADS;
-    const int keep_from = __ldg(p.keep_from + b);
+    const int keep_from = *(p.keep_from + b);
 
     // page ids of this CTA's slots
     int32_t *pages = reinterpret_cast<int32_t *>(keys + p.chunk_cap);
@@ -163,8 +167,8 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
             const int i = i0 + k * THREADS;
             const int64_t e = i < n ? entry(i) : -1;
             if (e >= 0) {
-                w[k] = __ldg(p.c.weight + e);
-                x[k] = __ldg(p.c.pos + e);
+                w[k] = *(p.c.weight + e);
+                x[k] = *(p.c.pos + e);
                 there |= 1u << k;
             }
         }
@@ -325,8 +329,8 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
                 sp = -1;
             } else {
                 const int64_t e0 = ((int64_t)sp * p.c.heads + h) * ps + so, e1 = ((int64_t)dp * p.c.heads + h) * ps + dof;
-                p.weight_out[e1] = __ldg(p.c.weight + e0);
-                p.pos_out[e1] = __ldg(p.c.pos + e0);
+                p.weight_out[e1] = *(p.c.weight + e0);
+                p.pos_out[e1] = *(p.c.pos + e0);
             }
         }
         for (int pc = lane; pc - lane < 2 * cpr; pc += 32) { // pieces of k, then of v (one round up to dim 128)

@@ -65,12 +65,13 @@ def test_rope_refusals(a):
 @needs_lib
 def test_attn_refusals(a):
     lib, c, p, n = _lib.load(), a.cache(), a.p, a.null
-    call = lambda q=p, ldq=256, out=p, qh=4, new=1, scale=0.1, acc=0, work=p, cache=c: lib.mmq_attn_decode(  # noqa: E731
+    other = ctypes.c_void_p(p.value + 2048)
+    call = lambda q=p, ldq=256, out=other, qh=4, new=1, scale=0.1, acc=0, work=p, cache=c: lib.mmq_attn_decode(  # noqa: E731
         cache, q, ldq, n, out, qh, new, scale, acc, work, n)
     assert call(qh=3) == -1 and call(qh=0) == -1 and call(new=0) == -1 and call(new=17) == -1 and call(ldq=255) == -1
     assert call(scale=float("nan")) == -1 and call(scale=float("inf")) == -1
     assert call(q=n) == -6 and call(out=n) == -6 and call(work=n) == -6
-    assert call(acc=1, cache=a.cache(weight=None)) == -6
+    assert call(acc=1, cache=a.cache(weight=None)) == -6 and call(out=p) == -1           # q is read while out is written
     assert call(q=a.odd) == -2 and call(ldq=258) == -2 and call(work=a.odd) == -2
     assert call(cache=a.cache(seqs=0)) == 0
     nf = ctypes.c_int64()

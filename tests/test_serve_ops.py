@@ -444,6 +444,43 @@ def test_evict_longest(ops):
     assert torch.equal(cache.k.view(-1, 8)[:budget, 0].cpu().float(), want.remainder(1000).float())
 
 
+def test_chained_calls_see_each_other(ops):
+    """Append, attention with weights and eviction back to back (each may start while the one before it ends) and with
+    a synchronisation after every call: the same cache and outputs.  Pages of 16 put two heads' weights in one line."""
+    g = torch.Generator().manual_seed(11)
+    B, H, Hq, D, budget = 3, 4, 8, 64, 60
+    rows = [(torch.randn((B, Hq, D), generator=g).cuda(), torch.randn((B, H, D), generator=g).cuda(), torch.randn((B, H, D), generator=g).cuda())
+            for _ in range(24)]
+    table = ops.rope_table(D)
+    got = []
+    for sync in (False, True):
+        cache = make_cache(ops, [64, 70, 61], H, D, 16, seed=12, extra=60)
+        spare = (torch.zeros_like(cache.weight), torch.zeros_like(cache.pos))
+        cache.pos.copy_(torch.arange(cache.pos.numel(), dtype=torch.int32, device="cuda").view(cache.pos.shape) % 50)
+        ws, ew, outs = ops.attn_workspace(cache, Hq, 1, True), ops.evict_workspace(cache, budget), []
+        done = (lambda: torch.cuda.synchronize()) if sync else (lambda: None)
+        for i, (q, k, v) in enumerate(rows):
+            pos = torch.full((B,), 50 + i, dtype=torch.int32, device="cuda")
+            cache.lens.add_(1)
+            done()
+            qr = ops.rope_append(cache, table, q, k, v, pos)
+            done()
+            outs.append(ops.attn_decode(cache, qr, accumulate=True, workspace=ws))
+            done()
+            old = (cache.weight, cache.pos)
+            ops.kv_evict(cache, budget, pos - 5, *spare, workspace=ew)
+            done()
+            cache.set_bookkeeping(*spare)
+            spare = old
+            cache.lens.clamp_(max=budget)
+        ops.check_status()
+        got.append((torch.stack(outs), cache.k, cache.v, cache.weight, cache.pos, cache.table.long()))
+    (o1, k1, v1, w1, p1, t1), (o2, k2, v2, w2, p2, _) = got
+    pages = t1[:, :4].reshape(-1)                                    # the pages of the first 64 slots
+    assert torch.equal(o1, o2) and torch.equal(k1, k2) and torch.equal(v1, v2)
+    assert torch.equal(w1[pages], w2[pages]) and torch.equal(p1[pages], p2[pages])
+
+
 # ----------------------------------------------------------- verification ---
 
 def check_verify(ops, target, draft, tokens, uniform, count=None):
@@ -585,7 +622,7 @@ def test_refusals(ops):
                 lambda: ops.KVCache(cache.k, cache.v, cache.table, cache.lens[:1])):
         with pytest.raises(ValueError):
             bad()
-    for bad, status in ((lambda: ops.attn_decode(cache, q, scale=float("nan")), -1), (lambda: ops.attn_decode(cache, q, scale=float("inf")), -1),
+    for bad, status in ((lambda: ops.attn_decode(cache, q, scale=float("nan")), -1), (lambda: ops.attn_decode(cache, q, out=q), -1), (lambda: ops.attn_decode(cache, q, scale=float("inf")), -1),
                         (lambda: ops.evict_workspace(cache, 0), -1)):
         with pytest.raises(MMQError) as e:
             bad()
