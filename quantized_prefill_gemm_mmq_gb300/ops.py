@@ -413,45 +413,34 @@ class KVCache:
 
 # The current stream's handle without the Stream object around it (2 us of every call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_capturing = torch.cuda.is_current_stream_capturing
+_current = torch.cuda.current_device
 
-
-def _on(call: str, fn, index: int, *args):
-    """fn(*args, stream) with device `index` current, on its current stream; raises on a status."""
-    if index == torch.cuda.current_device():
-        st = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args, _raw_stream(index))
-    if st != 0:
-        raise MMQError(call, st)
-
-
-_BLOCKS: dict = {}          # (stream, shape, dtype) -> small outputs not handed out yet
+_BLOCKS: dict = {}          # (device, stream, shape, dtype) -> small outputs not handed out yet
 _BLOCK_SLOTS, _BLOCK_MAX = 64, 16384
 
 
-def _fresh(shape: tuple, dtype, device, index: int) -> torch.Tensor:
-    """An uninitialised output tensor.
+def _fresh(shape: tuple, dtype, device, stream: int) -> torch.Tensor:
+    """An uninitialised output tensor for the current stream (its handle) of the current device.
 
     Small ones (up to 16384 elements) are cut from a block of 64, each handed out once: an
     allocation after a kernel launch takes 5 to 7 us of host time, as long as the smallest
     calls themselves.  A block belongs to the stream it was allocated under, as the allocator
     has it; while a graph is captured, outputs come from the graph's own memory."""
-    n = 1
-    for s in shape:
-        n *= s
-    if n > _BLOCK_MAX or index != torch.cuda.current_device() or torch.cuda.is_current_stream_capturing():
+    key = (device, stream, shape, dtype)      # the default stream's handle is the same on every device
+    slots = _BLOCKS.get(key)
+    if slots and not _capturing():
+        try:
+            return slots.pop()
+        except IndexError:      # another thread took the last one
+            pass
+    if math.prod(shape) > _BLOCK_MAX or _capturing():
         return torch.empty(shape, dtype=dtype, device=device)
-    key = (_raw_stream(index), shape, dtype)
-    try:
-        return _BLOCKS[key].pop()
-    except (KeyError, IndexError):
-        if len(_BLOCKS) >= 64:
-            _BLOCKS.clear()
-        slots = list(torch.empty((_BLOCK_SLOTS,) + shape, dtype=dtype, device=device).unbind(0))
-        out = slots.pop()
-        _BLOCKS[key] = slots
-        return out
+    if len(_BLOCKS) >= 64:
+        _BLOCKS.clear()
+    block = torch.empty((_BLOCK_SLOTS * shape[0],) + tuple(shape[1:]), dtype=dtype, device=device)
+    slots = _BLOCKS[key] = list(torch.unsafe_split(block, shape[0], 0))
+    return slots.pop()
 
 
 class RopeTable:
@@ -462,6 +451,7 @@ class RopeTable:
         _need_cuda(freq)
         _need(freq, "freq", torch.int64, (freq.numel(),), freq.get_device())
         self.freq, self.rot, self.magnitude = freq, 2 * freq.numel(), float(magnitude)
+        self.index, self.ptr = freq.get_device(), freq.data_ptr()
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, context: int = 4096,
@@ -506,24 +496,23 @@ def rope_table(rot: int, base: float = 10000.0, scaling: str = "none", factor: f
     return RopeTable(torch.tensor(rope_fixed(inv), dtype=torch.int64).to(device if device is not None else "cuda"), magnitude)
 
 
-def _rows(t, name, rows, heads, dim, index):
-    """Row stride of f32 [rows][heads][dim] whose rows may lie apart."""
-    if t.dtype is not torch.float32 or t.shape != (rows, heads, dim) or t.get_device() != index:
-        raise ValueError(f"{name} must be float32 [{rows}][{heads}][{dim}] on CUDA device {index}")
+def _rows(t, name, heads, dim, index):
+    """Row stride of f32 [rows][heads][dim], shape checked, whose rows may lie apart."""
+    if t.dtype is not torch.float32 or t.get_device() != index:
+        raise ValueError(f"{name} must be float32 on CUDA device {index}")
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-    return st[0] if rows > 1 else max(st[0], heads * dim)
+    return st[0] if t.shape[0] > 1 else max(st[0], heads * dim)
 
 
-def _q_shape(cache, q):
+def _q_shape(cache, shape):
     """(rows, query heads, new tokens per sequence) of q."""
-    if q.dim() != 3:
-        raise ValueError("q must be float32 [rows][q_heads][dim]")
-    rows, q_heads, _ = q.shape
-    if cache.seqs == 0 or rows % cache.seqs:
+    if len(shape) != 3 or shape[2] != cache.dim:
+        raise ValueError(f"q must be [rows][q_heads][{cache.dim}]")
+    if cache.seqs == 0 or shape[0] % cache.seqs:
         raise ValueError("rows must be a multiple of the cache's sequences")
-    return rows, q_heads, rows // cache.seqs
+    return shape[0], shape[1], shape[0] // cache.seqs
 
 
 def rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
@@ -534,24 +523,32 @@ def rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tenso
     one wider product row), pos int32 [seqs*n] positions.  new int32 [seqs] limits how many
     of a sequence's n rows are there; they become the last entries of cache.lens.  `out`
     may be q."""
-    index, dim = cache.index, cache.dim
-    rows, q_heads, n = _q_shape(cache, q)
-    ldq = _rows(q, "q", rows, q_heads, dim, index)
-    ldk = _rows(k, "k", rows, cache.heads, dim, index)
-    ldv = _rows(v, "v", rows, cache.heads, dim, index)
+    index, dim, heads = cache.index, cache.dim, cache.heads
+    if index != _current():
+        with torch.cuda.device(index):
+            return rope_append(cache, rope, q, k, v, pos, interleaved, new, out)
+    shape = q.shape
+    rows, q_heads, n = _q_shape(cache, shape)
+    if k.shape != (rows, heads, dim) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{rows}][{heads}][{dim}]")
+    ldq, ldk, ldv = _rows(q, "q", q_heads, dim, index), _rows(k, "k", heads, dim, index), _rows(v, "v", heads, dim, index)
     _need(pos, "pos", torch.int32, (rows,), index)
     if new is not None:
         _need(new, "new", torch.int32, (cache.seqs,), index)
-    if rope.rot > dim or rope.freq.get_device() != index:
+    if rope.rot > dim or rope.index != index:
         raise ValueError("the table rotates more values than a head has, or is on another device")
+    stream = _raw_stream(index)
     if out is None:
-        out = _fresh((rows, q_heads, dim), torch.float32, cache.device, index)
-        ldo = q_heads * dim
+        out, ldo = _fresh(shape, torch.float32, cache.device, stream), q_heads * dim
     else:
-        ldo = _rows(out, "out", rows, q_heads, dim, index)
-    _on("mmq_rope_append", load().mmq_rope_append, index, cache._ref, rope.freq.data_ptr(), rope.rot, rope.magnitude,
-        int(interleaved), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, pos.data_ptr(),
-        None if new is None else new.data_ptr(), out.data_ptr(), ldo, q_heads, n)
+        if out.shape != shape:
+            raise ValueError("out must have q's shape")
+        ldo = _rows(out, "out", q_heads, dim, index)
+    st = load().mmq_rope_append(cache._ref, rope.ptr, rope.rot, rope.magnitude, int(interleaved), q.data_ptr(), ldq, k.data_ptr(), ldk,
+                                v.data_ptr(), ldv, pos.data_ptr(), None if new is None else new.data_ptr(), out.data_ptr(), ldo,
+                                q_heads, n, stream)
+    if st != 0:
+        raise MMQError("mmq_rope_append", st)
     return out
 
 
@@ -561,9 +558,10 @@ class AttnWorkspace:
 
     def __init__(self, device, floats: int):
         self.work = torch.empty(max(4, floats), dtype=torch.float32, device=device)
+        self.floats, self.ptr, self.index = self.work.numel(), self.work.data_ptr(), self.work.get_device()
 
     def fits(self, floats: int) -> bool:
-        return floats <= self.work.numel()
+        return floats <= self.floats
 
 
 def attn_sizes(cache: KVCache, q_heads: int, new_tokens: int = 1, accumulate: bool = False) -> int:
@@ -590,28 +588,38 @@ def attn_decode(cache: KVCache, q: torch.Tensor, scale: float | None = None, new
     defaults to dim^-0.5.  accumulate adds every entry's weight to cache.weight.  Without
     `workspace` one is allocated for this call."""
     index, dim = cache.index, cache.dim
-    rows, q_heads, n = _q_shape(cache, q)
-    ldq = _rows(q, "q", rows, q_heads, dim, index)
-    if q_heads % cache.heads:
-        raise ValueError("q_heads must be a multiple of the cache's heads")
-    if not 1 <= n <= ATTN_NEW_MAX:
-        raise ValueError(f"1 to {ATTN_NEW_MAX} new tokens per sequence")
+    if index != _current():
+        with torch.cuda.device(index):
+            return attn_decode(cache, q, scale, new, accumulate, out, workspace)
+    shape = q.shape
+    key = (shape, accumulate)
+    plan = cache._work.get(key)
+    if plan is None:                                     # what depends on the shape alone
+        rows, q_heads, n = _q_shape(cache, shape)
+        if q_heads % cache.heads:
+            raise ValueError("q_heads must be a multiple of the cache's heads")
+        if not 1 <= n <= ATTN_NEW_MAX:
+            raise ValueError(f"1 to {ATTN_NEW_MAX} new tokens per sequence")
+        plan = cache._work[key] = (q_heads, n, attn_sizes(cache, q_heads, n, accumulate))
+    q_heads, n, floats = plan
+    ldq = _rows(q, "q", q_heads, dim, index)
     if accumulate and cache.weight is None:
         raise ValueError("the cache keeps no weights")
     if new is not None:
         _need(new, "new", torch.int32, (cache.seqs,), index)
+    stream = _raw_stream(index)
     if out is None:
-        out = _fresh((rows, q_heads, dim), torch.float32, cache.device, index)
+        out = _fresh(shape, torch.float32, cache.device, stream)
     else:
-        _need(out, "out", torch.float32, (rows, q_heads, dim), index)
-    key = (q_heads, n, accumulate)
-    floats = cache._work.get(key)
-    if floats is None:
-        floats = cache._work[key] = attn_sizes(cache, q_heads, n, accumulate)
+        _need(out, "out", torch.float32, shape, index)
     if workspace is None or not workspace.fits(floats):
         workspace = AttnWorkspace(cache.device, floats)
-    _on("mmq_attn_decode", load().mmq_attn_decode, index, cache._ref, q.data_ptr(), ldq, None if new is None else new.data_ptr(),
-        out.data_ptr(), q_heads, n, dim ** -0.5 if scale is None else scale, int(accumulate), workspace.work.data_ptr())
+    elif workspace.index != index:
+        raise ValueError(f"workspace must be on CUDA device {index}")
+    st = load().mmq_attn_decode(cache._ref, q.data_ptr(), ldq, None if new is None else new.data_ptr(), out.data_ptr(), q_heads, n,
+                                dim ** -0.5 if scale is None else scale, int(accumulate), workspace.ptr, stream)
+    if st != 0:
+        raise MMQError("mmq_attn_decode", st)
     return out
 
 
@@ -633,16 +641,20 @@ def kv_evict(cache: KVCache, budget: int, keep_from: torch.Tensor, weight_out: t
     the new bookkeeping goes to weight_out and pos_out (shaped as cache.weight), for
     cache.set_bookkeeping.  Lower cache.lens to the budget (clamp_) once every layer that
     shares it is done."""
-    index = cache.index
-    if cache.weight is None or cache.pos is None:
+    index, weight = cache.index, cache.weight
+    if index != _current():
+        with torch.cuda.device(index):
+            return kv_evict(cache, budget, keep_from, weight_out, pos_out, workspace)
+    if weight is None or cache.pos is None:
         raise ValueError("the cache keeps no weights or positions")
     if weight_out is None or pos_out is None:
         raise ValueError("weight_out and pos_out are required")
-    shape = cache.weight.shape
+    shape = weight.shape
     _need(keep_from, "keep_from", torch.int32, (cache.seqs,), index)
     _need(weight_out, "weight_out", torch.float32, shape, index)
     _need(pos_out, "pos_out", torch.int32, shape, index)
-    if weight_out.data_ptr() == cache.weight.data_ptr() or pos_out.data_ptr() == cache.pos.data_ptr():
+    wp, pp = weight_out.data_ptr(), pos_out.data_ptr()
+    if wp == weight.data_ptr() or pp == cache.pos.data_ptr():
         raise ValueError("weight_out and pos_out must not be the cache's own")
     need = cache._work.get(budget)
     if need is None:
@@ -651,8 +663,9 @@ def kv_evict(cache: KVCache, budget: int, keep_from: torch.Tensor, weight_out: t
         workspace = torch.empty(max(1, need), dtype=torch.int32, device=cache.device)
     elif workspace.dtype is not torch.int32 or workspace.get_device() != index or not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError("workspace must be evict_workspace(cache, budget) or larger")
-    _on("mmq_kv_evict", load().mmq_kv_evict, index, cache._ref, budget, keep_from.data_ptr(), weight_out.data_ptr(),
-        pos_out.data_ptr(), workspace.data_ptr())
+    st = load().mmq_kv_evict(cache._ref, budget, keep_from.data_ptr(), wp, pp, workspace.data_ptr(), _raw_stream(index))
+    if st != 0:
+        raise MMQError("mmq_kv_evict", st)
 
 
 def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.Tensor, uniform: torch.Tensor,
@@ -665,24 +678,32 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.
     int32 [seqs][n+1]: the accepted ones, one drawn, then -1; accepted int32 [seqs]);
     `out` may supply the two."""
     dtype, index = PROB_DTYPES.get(target.dtype), target.get_device()
-    if dtype is None or index < 0 or target.dim() != 3 or target.shape[1] < 2 or not target.is_contiguous():
+    shape = target.shape
+    if dtype is None or index < 0 or len(shape) != 3 or shape[1] < 2 or not target.is_contiguous():
         raise ValueError("target must be a contiguous CUDA tensor [seqs][drafts+1][vocab] of probabilities")
-    B, n1, V = target.shape
+    if index != _current():
+        with torch.cuda.device(index):
+            return spec_verify(target, draft, tokens, uniform, count, out)
+    B, n1, V = shape
     if draft is not None:
         _need(draft, "draft", target.dtype, (B, n1 - 1, V), index)
     _need(tokens, "tokens", torch.int32, (B, n1 - 1), index)
     _need(uniform, "uniform", torch.float32, (B, n1), index)
     if count is not None:
         _need(count, "count", torch.int32, (B,), index)
+    stream = _raw_stream(index)
     if out is None:
         dev = target.device
-        res, acc = _fresh((B, n1), torch.int32, dev, index), _fresh((B,), torch.int32, dev, index)
+        res, acc = _fresh((B, n1), torch.int32, dev, stream), _fresh((B,), torch.int32, dev, stream)
     else:
         res, acc = out
         _need(res, "out[0]", torch.int32, (B, n1), index)
         _need(acc, "out[1]", torch.int32, (B,), index)
-    _on("mmq_spec_verify", load().mmq_spec_verify, index, target.data_ptr(), None if draft is None else draft.data_ptr(), dtype,
-        tokens.data_ptr(), uniform.data_ptr(), None if count is None else count.data_ptr(), res.data_ptr(), acc.data_ptr(), B, n1 - 1, V)
+    st = load().mmq_spec_verify(target.data_ptr(), None if draft is None else draft.data_ptr(), dtype, tokens.data_ptr(),
+                                uniform.data_ptr(), None if count is None else count.data_ptr(), res.data_ptr(), acc.data_ptr(),
+                                B, n1 - 1, V, stream)
+    if st != 0:
+        raise MMQError("mmq_spec_verify", st)
     return res, acc
 
 
