@@ -661,6 +661,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                 }
                 if (whole) {
                     const float inv = inverse(tot);
+                    if (inv == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);      // saw nothing: its 0 * Inf must not show
                     if (col < p.c.dim)
                         *reinterpret_cast<float4 *>(out_row(r) + col) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
                     if (p.lse && col == 0) p.lse[seg * p.rows + rt * ROWS + r] = log_sum<T>(top, tot);

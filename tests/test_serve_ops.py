@@ -259,6 +259,25 @@ def test_attn_masked_entries_do_not_reach_earlier_rows(ops, bad, dtype, dim, gro
         assert not bool(torch.isfinite(got[b * N + 2:b * N + 4]).any())
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype,dim,group", [(torch.float16, 128, 1), (torch.bfloat16, 64, 1), (torch.bfloat16, 128, 4), (torch.bfloat16, 256, 4)])
+def test_attn_rows_that_are_not_there_stay_zero(ops, bad, dtype, dim, group):
+    # an entry that the other rows see is not finite; in one CTA's segments and in split ones
+    N, lens, new = 3, [20, 90, 4000, 5], [1, 2, 1, 0]
+    cache = make_cache(ops, lens, 2, dim, 16, dtype)
+    tab = cache.table.cpu()
+    for b in range(4):
+        cache.v[ref.slot_place(tab, 16, b, 0)[0], :, 0] = bad
+    q = torch.randn((12, 2 * group, dim), generator=torch.Generator().manual_seed(6)).cuda()
+    for accumulate in (False, True):
+        got = ops.attn_decode(cache, q, new=torch.tensor(new, dtype=torch.int32).cuda(), accumulate=accumulate)
+        ops.check_status()
+        for b in range(4):
+            assert not bool(torch.isfinite(got[b * N:b * N + new[b]]).any())
+            assert bool((got[b * N + new[b]:(b + 1) * N] == 0).all())
+        assert bool(torch.isfinite(cache.weight).all())
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_attn_long_split(ops, dtype):
     # one sequence over many CTAs, and a ragged batch whose CTAs hold several segments
