@@ -763,9 +763,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     }
     const int64_t x = blockIdx.x - join_blocks, seg = x / chunks;
     const int b = (int)(seg / p.c.heads), h = (int)(seg - (int64_t)b * p.c.heads);
-    const int len = cache_len(p.c, b, KID_ATTN), first = (int)(x - seg * chunks) * JOIN_WEIGHTS;
-    // Eight neighbouring entries per thread.  What the first launch does not write is read before its end: page
-    // ids and the weights so far.
+    const int len = cache_len<true>(p.c, b, KID_ATTN), first = (int)(x - seg * chunks) * JOIN_WEIGHTS;
+    // Eight neighbouring entries per thread.  What the first launch does not write is read before its end: lengths,
+    // page ids and the weights so far.  (The first launch lets this one start only after the launches before it have
+    // ended.)  From L2, since nothing before pdl_wait says that lines left in L1 are of today.
     constexpr int EACH = JOIN_WEIGHTS / JOIN_THREADS;
     static_assert(EACH == 8, "two 16-byte accesses");
     const int mine = first + tid * EACH, n = min(EACH, len - mine);
@@ -773,21 +774,21 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     float w[EACH];
     float *at[EACH];
     if (together) {
-        const int c = p.page_div.of(mine), pg = cache_page(p.c, b, c, KID_ATTN);
+        const int c = p.page_div.of(mine), pg = cache_page<true>(p.c, b, c, KID_ATTN);
         at[0] = pg < 0 ? nullptr : p.c.weight + ((int64_t)pg * p.c.heads + h) * p.c.page_size + (mine - c * p.c.page_size);
         if (at[0]) {
-            *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(at[0]);
-            *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(at[0] + 4);
+            *reinterpret_cast<float4 *>(w) = __ldcg(reinterpret_cast<const float4 *>(at[0]));
+            *reinterpret_cast<float4 *>(w + 4) = __ldcg(reinterpret_cast<const float4 *>(at[0] + 4));
         }
     } else {
 #pragma unroll
         for (int k = 0; k < EACH; ++k) {
             at[k] = nullptr;
             if (k >= n) continue;
-            const int c = p.page_div.of(mine + k), pg = cache_page(p.c, b, c, KID_ATTN);
+            const int c = p.page_div.of(mine + k), pg = cache_page<true>(p.c, b, c, KID_ATTN);
             if (pg < 0) continue;
             at[k] = p.c.weight + ((int64_t)pg * p.c.heads + h) * p.c.page_size + (mine + k - c * p.c.page_size);
-            w[k] = *at[k];
+            w[k] = __ldcg(at[k]);
         }
     }
     pdl_wait();
@@ -925,7 +926,7 @@ int launch_attn(const AttnParams &p, int grid, cudaStream_t stream)
     const auto kernel = attn_kernel<DP, T, MODE, UG>;
     constexpr int smem = attn::Shape<DP, MODE, UG>::kSmem;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         cudaGetLastError();
         return MMQ_ERR_ARCH;
     }

@@ -50,8 +50,8 @@ inline int check_cache(const mmq_kv_cache *c)
 }
 
 // Launch under programmatic dependent launch: the kernel may start while the
-// one before it in the stream finishes, and waits for that one's end (pdl_wait,
-// the first thing every kernel here does) before it touches memory.  What the
+// one before it in the stream finishes, and waits for that one's end (pdl_wait)
+// before it touches memory, the attention's joining launch excepted.  What the
 // one before may have written is read with plain loads, not through the
 // read-only path: that one promises data which nobody writes during the kernel.
 // cluster: CTAs per cluster, 0 for none.
@@ -76,19 +76,22 @@ int launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaSt
     return launch_status();
 }
 
-// A sequence's length, limited to what its table row can hold.
+// A sequence's length, limited to what its table row can hold.  L2: not through L1 (reads before pdl_wait).
+template <bool L2 = false>
 __device__ __forceinline__ int cache_len(const mmq_kv_cache &c, int b, int kid)
 {
-    const int n = *(c.len + b), cap = c.cols * c.page_size;
+    const int n = L2 ? __ldcg(c.len + b) : *(c.len + b), cap = c.cols * c.page_size;
     if (n >= 0 && n <= cap) return n;
     record_error(MMQ_ERR_INDEX, kid, SITE_LEN);
     return n < 0 ? 0 : cap;
 }
 
 // Page of table column `col` of sequence b, or -1 (reported) if it is none.
+template <bool L2 = false>
 __device__ __forceinline__ int cache_page(const mmq_kv_cache &c, int b, int col, int kid)
 {
-    const int pg = *(c.table + (int64_t)b * c.cols + col);
+    const int32_t *at = c.table + (int64_t)b * c.cols + col;
+    const int pg = L2 ? __ldcg(at) : *at;
     if (pg >= 0 && pg < c.pages) return pg;
     record_error(MMQ_ERR_INDEX, kid, SITE_PAGE);
     return -1;

@@ -375,7 +375,7 @@ inline int launch_evict(const EvictParams &p, int64_t rows, int cl, cudaStream_t
 {
     static bool attr_done[64];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         cudaGetLastError();
         return MMQ_ERR_ARCH;
     }
