@@ -497,7 +497,10 @@ int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, int rot, flo
  * bf16) parts, so products carry f32's precision.  Results do not depend on
  * timing: they repeat bit for bit.
  * accumulate != 0 adds to cache->weight, for every entry a sequence has, the
- * sum of p over its rows and the query heads of the key-value head.
+ * sum of p over its rows and the query heads of the key-value head.  Sequences
+ * may share pages (a common beginning), but not then: two of them would add to
+ * the same weight at the same time.  An entry that is not finite makes the
+ * rows that see it not finite.
  * 1 <= new_tokens <= 16, q_heads a multiple (1 .. 128) of heads, scale finite.
  * `work` holds the floats that mmq_attn_sizes says.  Calls that share it must
  * be ordered (one stream).

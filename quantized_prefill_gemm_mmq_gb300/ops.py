@@ -585,8 +585,8 @@ def attn_decode(cache: KVCache, q: torch.Tensor, scale: float | None = None, new
 
     q f32 [seqs*n][q_heads][dim], rotated; row t of a sequence sees the entries up to its
     own (new int32 [seqs] limits the rows as in rope_append; rows past it get 0).  scale
-    defaults to dim^-0.5.  accumulate adds every entry's weight to cache.weight.  Without
-    `workspace` one is allocated for this call."""
+    defaults to dim^-0.5.  accumulate adds every entry's weight to cache.weight (no
+    page may belong to two sequences then).  Without `workspace` one is allocated for this call."""
     index, dim = cache.index, cache.dim
     if index != _current():
         with torch.cuda.device(index):

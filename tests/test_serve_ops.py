@@ -285,6 +285,13 @@ def test_attn_long_split(ops, dtype):
     check_attention(ops, [5000] + [3] * 40 + [900], 1, 8, 8, 64, 16, dtype, seed=10)
 
 
+def test_attn_shared_pages(ops):
+    # two sequences with a common beginning in the same pages
+    cache = make_cache(ops, [100, 130], 2, 64, 16)
+    cache.table[1, :5] = cache.table[0, :5]
+    check_attention(ops, [100, 130], 1, 4, 2, 64, 16, torch.float16, cache=cache)
+
+
 def test_attn_many_sequences(ops):
     check_attention(ops, [1 + (37 * i) % 90 for i in range(300)], 1, 2, 1, 64, 16, torch.float16, seed=4)
 
