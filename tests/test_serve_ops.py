@@ -278,6 +278,14 @@ def test_attn_rows_that_are_not_there_stay_zero(ops, bad, dtype, dim, group):
         assert bool(torch.isfinite(cache.weight).all())
 
 
+@pytest.mark.parametrize("H,group,N,dim,dtype", [(1, 128, 16, 64, torch.bfloat16), (2, 20, 5, 128, torch.float16), (1, 71, 1, 192, torch.bfloat16),
+                                                 (1, 33, 3, 256, torch.float16), (1, 12, 3, 96, torch.bfloat16)])
+def test_attn_many_rows(ops, H, group, N, dim, dtype):
+    # more rows than a CTA takes at once, up to the most there may be; and warps without rows
+    for accumulate in (False, True):
+        check_attention(ops, [150, 40], N, H * group, H, dim, 16, dtype, accumulate=accumulate, seed=group)
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_attn_long_split(ops, dtype):
     # one sequence over many CTAs, and a ragged batch whose CTAs hold several segments
@@ -388,6 +396,37 @@ def test_bad_page_and_length_are_reported(ops):
     assert torch.equal(a, b)
 
 
+def test_bad_pages_are_not_written(ops):
+    """Append and eviction skip entries whose page is none, report it, and write the others."""
+    from quantized_prefill_gemm_mmq_gb300._lib import MMQError
+    cache = make_cache(ops, [40, 40], 2, 64, 16)
+    pages = cache.table.clone()
+    for bad in (-1, cache.k.shape[0]):
+        rows = [torch.randn((2, h, 64)).cuda() for h in (4, 2, 2)]
+        cache.table[0, 2] = bad
+        k, v = cache.k.clone(), cache.v.clone()
+        out = ops.rope_append(cache, ops.rope_table(64), *rows, torch.tensor([39, 39], dtype=torch.int32).cuda())
+        with pytest.raises(MMQError) as e:
+            ops.check_status()
+        assert e.value.status == -11 and bool(torch.isfinite(out).all())
+        changed = ((cache.k != k) | (cache.v != v)).flatten(1).any(1).nonzero().flatten().tolist()
+        assert changed == [int(pages[1, 2])]
+    cache.lens.fill_(41)
+    cache.pos.zero_()
+    k, v = cache.k.clone(), cache.v.clone()
+    wo, po = torch.full_like(cache.weight, -7.0), torch.full_like(cache.pos, -7)
+    ops.kv_evict(cache, 20, torch.tensor([1, 1], dtype=torch.int32).cuda(), wo, po)
+    with pytest.raises(MMQError) as e:
+        ops.check_status()
+    assert e.value.status == -11
+    allowed = set(pages[:, :2].flatten().tolist())                   # the pages of slots below the budget
+    for got, was in ((cache.k, k), (cache.v, v), (wo, torch.full_like(wo, -7.0)), (po, torch.full_like(po, -7))):
+        assert set((got != was).flatten(1).any(1).nonzero().flatten().tolist()) <= allowed
+    cache.table.copy_(pages)
+    ops.attn_decode(cache, rows[0])
+    ops.check_status()
+
+
 # --------------------------------------------------------------- eviction ---
 
 def check_evict(ops, lens, H, dim, page, budget, recent, dtype=torch.float16, layout="hnd", weights="random", seed=2, extra=0):
@@ -468,6 +507,27 @@ def test_evict_longest(ops):
     want[budget - 1000:] = torch.arange(n - 1000, n, dtype=torch.int32)
     assert torch.equal(po.view(-1)[:budget].cpu(), want)
     assert torch.equal(cache.k.view(-1, 8)[:budget, 0].cpu().float(), want.remainder(1000).float())
+
+
+def test_evict_offsets_past_32_bits(ops):
+    """Pools of more than 2^31 elements: an entry of the last page moves into the page before it."""
+    pages, page, H, dim = 33000, 64, 8, 128
+    k = torch.empty((pages, H, page, dim), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    last = [pages - 2, pages - 1]
+    table = torch.tensor([last], dtype=torch.int32, device="cuda")
+    k[last], v[last] = torch.randn((2, 2, H, page, dim), device="cuda").bfloat16().unbind(0)
+    w, pos = torch.zeros((pages, H, page), device="cuda"), torch.zeros((pages, H, page), dtype=torch.int32, device="cuda")
+    w[last] = 1.0
+    w[pages - 2, :, 5] = 0.5
+    pos[pages - 1, :, 36] = 100
+    cache = ops.KVCache(k, v, table, torch.tensor([101], dtype=torch.int32, device="cuda"), w, pos)
+    want_k, want_v = k[pages - 1, :, 36].clone(), v[pages - 1, :, 36].clone()
+    wo, po = torch.zeros_like(w), torch.zeros_like(pos)
+    ops.kv_evict(cache, 100, torch.tensor([100], dtype=torch.int32, device="cuda"), wo, po)
+    ops.check_status()
+    assert torch.equal(k[pages - 2, :, 5], want_k) and torch.equal(v[pages - 2, :, 5], want_v)
+    assert bool((wo[pages - 2] == 1).all()) and bool((po[pages - 2, :, 5] == 100).all())
 
 
 def test_chained_calls_see_each_other(ops):
