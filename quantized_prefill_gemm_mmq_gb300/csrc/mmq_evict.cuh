@@ -11,19 +11,22 @@
 //
 // One launch: one CTA (a cluster of them where there are few rows) per
 // sequence and head holds the keys in shared memory, finds the budget-th
-// largest by three passes of a radix search (11, 11 and 10 bits; a cluster adds
-// its histograms through distributed shared memory), counts ties in slot
-// order, lists the moves, and makes them.  Slots are dealt to threads in
-// stripes, so that every pass reads memory side by side; the order of slots is
-// kept by counting per (stripe, warp) with ballots and one scan over those
-// counts.  For the moves a warp looks up 32 at once, one per lane, then copies
-// them one after the other, a 16-byte piece of K or V per lane.
+// largest by up to three passes of a radix search (11, 11 and 10 bits), counts
+// ties in slot order, lists the moves, and makes them.  The CTAs of a cluster
+// read of each other's histograms, through distributed shared memory, the sums
+// of 32 bins each and then the 32 bins they need (all 2048 bins of eight CTAs
+// took 2 us a pass: 30 rows of 43382 entries 37 us, now 17).  Slots are dealt
+// to threads in stripes, so that every pass reads memory side by side, four
+// slots at a time where the pages allow; what happens to the 32 slots of a
+// warp is a word of bits, and one scan over the words' counts keeps the order
+// of slots.  For the moves a warp looks up 32 at once, one per lane, then
+// copies them one after the other, a 16-byte piece of K or V per lane.
 // Bound by memory: 8 B per entry and head for weight and position, 8 B for
 // each that stays, 8 dim B per move; with few moves by the latency of the
 // selection's passes.
 // Measured: 16 sequences up to 32768 entries of 8 heads of 128 down to 4096,
-// 105 us, of which 72 us move 485 MB (6.7 TB/s); 1100 entries of 32 heads down
-// to 1024, 8.6 us.
+// 98 us, of which 72 us move 485 MB (6.7 TB/s); 1100 entries of 32 heads down
+// to 1024, 7.3 us.
 #pragma once
 
 namespace mmq {
@@ -34,11 +37,13 @@ constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int PER_SM = 2;
 constexpr int BINS = 2048;
+constexpr int GROUPS = BINS / 32;
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX_CHUNK = 32768;               // keys per CTA: 128 KB
 constexpr int STRIPES = MAX_CHUNK / THREADS;   // at most
 constexpr int MAX_COLS = 4096;                 // page ids kept in shared memory
-constexpr int BATCH = 8;                       // stripes whose loads a thread has in flight
+constexpr int BATCH = 8;                       // slots whose loads a thread has in flight,
+constexpr int BATCH4 = 3;                      // and groups of four
 constexpr int MOVE_BATCH = 3;                  // moves a warp has in flight
 }  // namespace evict
 
@@ -49,6 +54,7 @@ struct EvictParams {
     int32_t *pos_out;
     int32_t *src, *dst;     // [seqs*heads][most] slots
     int budget, most, chunk_cap, cols_cap;
+    int wide;               // four slots at a time: pages of a multiple of four, bookkeeping on 16 bytes
     FastDiv page_div;
 };
 
@@ -66,10 +72,10 @@ __device__ __forceinline__ uint32_t cluster_ld(uint32_t a)
     return v;
 }
 
-__device__ __forceinline__ uint4 cluster_ld4(uint32_t a)
+__device__ __forceinline__ unsigned long long cluster_ld64(uint32_t a)
 {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
     return v;
 }
 
@@ -98,9 +104,10 @@ __device__ __forceinline__ int block_prefix(int v, int *s, int &total)
     return before + x - v;
 }
 
-// Exclusive prefixes, in the order (stripe, warp), of counts that lane 0 of
-// every warp has put into cnt[stripe*WARPS + warp], in place; returns the sum.
-__device__ __forceinline__ int stripe_prefix(int *cnt, int stripes, int *s)
+// Exclusive prefixes of count(w) over the words w = stripe*WARPS + warp, the
+// order of slots, into cnt; returns the sum.
+template <typename F>
+__device__ __forceinline__ int stripe_prefix(int *cnt, int stripes, int *s, F count)
 {
     constexpr int PER = evict::STRIPES * evict::WARPS / evict::THREADS;
     __syncthreads();
@@ -108,7 +115,7 @@ __device__ __forceinline__ int stripe_prefix(int *cnt, int stripes, int *s)
     int v[PER], mine = 0, total;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        v[k] = i + k < n ? cnt[i + k] : 0;
+        v[k] = i + k < n ? count(i + k) : 0;
         mine += v[k];
     }
     int before = block_prefix(mine, s, total);
@@ -126,7 +133,9 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
     using namespace evict;
     extern __shared__ __align__(16) uint32_t keys[];       // [chunk_cap], then the page ids [cols_cap]
     __shared__ __align__(16) uint32_t hist[2][BINS];
-    __shared__ int s_cnt[2][STRIPES * WARPS];
+    __shared__ __align__(8) uint32_t s_group[2][GROUPS];
+    __shared__ uint32_t s_bits[STRIPES * WARPS];
+    __shared__ int s_cnt[STRIPES * WARPS];
     __shared__ __align__(16) int s_scan[WARPS];
     __shared__ uint32_t s_digit, s_above, s_match;
     __shared__ uint32_t s_xchg[2];                        // ties; holes and moves of this CTA
@@ -138,7 +147,7 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
     const int row = blockIdx.x / n_cta, b = row / p.c.heads, h = row - b * p.c.heads, ps = p.c.page_size;
     const int len = cache_len(p.c, b, KID_EVICT);
 
-    const int chunk = (len + n_cta - 1) / n_cta;
+    const int chunk = ((len + n_cta - 1) / n_cta + 3) & ~3;
     const int lo = min(len, rank * chunk), n = min(len, lo + chunk) - lo;
     const int stripes = (n + THREADS - 1) / THREADS;
     const int keep_from = *(p.keep_from + b);
@@ -157,36 +166,79 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
     const int edge = p.budget - lo;                        // slots i < edge lie below the budget
     const bool whole = len <= p.budget;                    // nothing to evict
     // Keys; and the bookkeeping of the slots below the budget as if they all
-    // stayed: a moved entry overwrites it later.
-    for (int i0 = tid; i0 < n; i0 += THREADS * BATCH) {
-        float w[BATCH];
-        int32_t x[BATCH];
-        uint32_t there = 0;
+    // stayed: a moved entry overwrites it later.  Where four slots lie side by
+    // side (`wide`) a thread takes them at once.  Keys past n are 0, the last in order.
+    auto key_of = [&](float w, int32_t x) {
+        const uint32_t u = __float_as_uint(w + 0.f);       // -0 becomes 0
+        return x >= keep_from ? 0xffffffffu : u ^ (u & 0x80000000u ? 0xffffffffu : 0x80000000u);
+    };
+    if (p.wide) {
+        for (int i0 = 4 * tid; i0 < n; i0 += 4 * THREADS * BATCH4) {
+            float4 w[BATCH4];
+            int4 x[BATCH4];
+            int64_t e[BATCH4];
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const int i = i0 + k * THREADS;
-            const int64_t e = i < n ? entry(i) : -1;
-            if (e >= 0) {
-                w[k] = *(p.c.weight + e);
-                x[k] = *(p.c.pos + e);
-                there |= 1u << k;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const int i = i0 + k * THREADS;
-            if (i >= n) continue;
-            uint32_t key = 0;
-            if (there >> k & 1) {
-                const uint32_t u = __float_as_uint(w[k] + 0.f);                     // -0 becomes 0
-                key = x[k] >= keep_from ? 0xffffffffu : u ^ (u & 0x80000000u ? 0xffffffffu : 0x80000000u);
-                if (whole || i < edge) {
-                    const int64_t e = entry(i);
-                    p.weight_out[e] = w[k];
-                    p.pos_out[e] = x[k];
+            for (int k = 0; k < BATCH4; ++k) {
+                const int i = i0 + k * 4 * THREADS;
+                e[k] = i < n ? entry(i) : -1;
+                if (e[k] >= 0) {
+                    w[k] = *reinterpret_cast<const float4 *>(p.c.weight + e[k]);
+                    x[k] = *reinterpret_cast<const int4 *>(p.c.pos + e[k]);
                 }
             }
-            if (!whole) keys[i] = key;
+#pragma unroll
+            for (int k = 0; k < BATCH4; ++k) {
+                const int i = i0 + k * 4 * THREADS;
+                if (i >= n) continue;
+                const bool there = e[k] >= 0;
+                const int stay = there ? min(n, edge) - i : 0;        // entries to write, of four
+                if (stay >= 4) {
+                    *reinterpret_cast<float4 *>(p.weight_out + e[k]) = w[k];
+                    *reinterpret_cast<int4 *>(p.pos_out + e[k]) = x[k];
+                } else if (stay > 0) {
+                    const float ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                    const int xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        if (j < stay) {
+                            p.weight_out[e[k] + j] = ws[j];
+                            p.pos_out[e[k] + j] = xs[j];
+                        }
+                }
+                if (whole) continue;
+                uint4 key = make_uint4(0u, 0u, 0u, 0u);
+                if (there) {
+                    key.x = key_of(w[k].x, x[k].x);
+                    if (i + 1 < n) key.y = key_of(w[k].y, x[k].y);
+                    if (i + 2 < n) key.z = key_of(w[k].z, x[k].z);
+                    if (i + 3 < n) key.w = key_of(w[k].w, x[k].w);
+                }
+                *reinterpret_cast<uint4 *>(keys + i) = key;
+            }
+        }
+    } else {
+        for (int i0 = tid; i0 < ((n + 3) & ~3); i0 += THREADS * BATCH) {
+            float w[BATCH];
+            int32_t x[BATCH];
+            int64_t e[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int i = i0 + k * THREADS;
+                e[k] = i < n ? entry(i) : -1;
+                if (e[k] >= 0) {
+                    w[k] = *(p.c.weight + e[k]);
+                    x[k] = *(p.c.pos + e[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int i = i0 + k * THREADS;
+                if (e[k] >= 0 && (whole || i < edge)) {
+                    p.weight_out[e[k]] = w[k];
+                    p.pos_out[e[k]] = x[k];
+                }
+                if (!whole && i < ((n + 3) & ~3)) keys[i] = e[k] >= 0 ? key_of(w[k], x[k]) : 0u;
+            }
         }
     }
     if (whole) return;                                     // the whole cluster leaves
@@ -194,54 +246,92 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
     // ---- the budget-th largest key, from its highest bits down
     uint32_t prefix = 0, mask = 0;
     int want = p.budget;                                   // of the keys that match the prefix
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         uint32_t *hs = hist[pass & 1];
         for (int i = tid; i < BINS; i += THREADS) hs[i] = 0;
         __syncthreads();
-#pragma unroll 8
-        for (int i = tid; i < n; i += THREADS) {
-            const uint32_t k = keys[i];
-            if ((k & mask) == prefix) atomicAdd(&hs[(k >> shift) & ((1u << bits) - 1)], 1u);
+#pragma unroll 2
+        for (int i = 4 * tid; i < n; i += 4 * THREADS) {
+            const uint4 k = *reinterpret_cast<const uint4 *>(keys + i);
+            auto add = [&](uint32_t x) {
+                if ((x & mask) == prefix) atomicAdd(&hs[(x >> shift) & ((1u << bits) - 1)], 1u);
+            };
+            add(k.x);
+            add(k.y);
+            add(k.z);
+            add(k.w);
         }
-        // four bins per thread, from the highest down; a cluster's are added 16 bytes at a time
-        constexpr int PER = 4;
-        static_assert(BINS == PER * THREADS, "");
-        const int top = BINS - PER - PER * tid;
-        uint32_t c[PER];
-        if (n_cta == 1) {
-            __syncthreads();
-            *reinterpret_cast<uint4 *>(c) = *reinterpret_cast<const uint4 *>(hs + top);
-        } else {
-            cluster_sync_all();
-#pragma unroll
-            for (int k = 0; k < PER; ++k) c[k] = 0;
-            const uint32_t a = smem_u32(hs + top);
-#pragma unroll 4
-            for (int r = 0; r < n_cta; ++r) {
-                const uint4 v = cluster_ld4(cluster_map(a, r));
-                c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
-            }
+        // sums of 32 bins each: eight threads of four
+        static_assert(BINS == 4 * THREADS && GROUPS * 32 == BINS && GROUPS == 64, "");
+        __syncthreads();
+        {
+            const uint4 v = *reinterpret_cast<const uint4 *>(hs + 4 * tid);
+            uint32_t x = (v.x + v.y) + (v.z + v.w);
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            x += __shfl_xor_sync(0xffffffffu, x, 4);
+            if ((tid & 7) == 0) s_group[pass & 1][tid / 8] = x;
         }
-        int total, mine = 0;
+        if (n_cta == 1) __syncthreads();
+        else cluster_sync_all();
+        // One warp finds the group of bins, two per lane from the highest down, then the bin, one per lane: of the
+        // other CTAs' histograms it reads 64 sums and 32 bins, all CTAs' at once (past the last: that one's again).
+        if (warp == 0) {
+            const uint32_t *pair = &s_group[pass & 1][GROUPS - 2 - 2 * lane];
+            uint32_t first = 0, second = 0;                // the higher group's and the lower one's
+            if (n_cta == 1) {
+                first = pair[1];
+                second = pair[0];
+            } else {
+                unsigned long long v[MAX_CLUSTER];
 #pragma unroll
-        for (int k = 0; k < PER; ++k) mine += (int)c[k];
-        int before = block_prefix(mine, s_scan, total);
-        if (before < want && want <= before + mine) {
+                for (int r = 0; r < MAX_CLUSTER; ++r) v[r] = cluster_ld64(cluster_map(smem_u32(pair), min(r, n_cta - 1)));
 #pragma unroll
-            for (int k = PER - 1; k >= 0; --k) {
-                if (before < want && want <= before + (int)c[k]) {
-                    s_digit = (uint32_t)(top + k);
-                    s_above = (uint32_t)before;
-                    s_match = c[k];
+                for (int r = 0; r < MAX_CLUSTER; ++r) {
+                    first += r < n_cta ? (uint32_t)(v[r] >> 32) : 0u;
+                    second += r < n_cta ? (uint32_t)v[r] : 0u;
                 }
-                before += (int)c[k];
+            }
+            auto before = [&](int x) {                     // exclusive prefix over the lanes
+                int y = x;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int z = __shfl_up_sync(0xffffffffu, y, o);
+                    if (lane >= o) y += z;
+                }
+                return y - x;
+            };
+            int above = before((int)(first + second));
+            const unsigned m = __ballot_sync(0xffffffffu, above < want && want <= above + (int)(first + second));
+            const bool lower = want > above + (int)first;
+            if (lower) above += (int)first;
+            const int f = __ffs(m) - 1, group = __shfl_sync(0xffffffffu, GROUPS - 1 - 2 * lane - (lower ? 1 : 0), f);
+            above = __shfl_sync(0xffffffffu, above, f);
+            const int bin = group * 32 + 31 - lane;
+            int c = 0;
+            if (n_cta == 1) {
+                c = (int)hs[bin];
+            } else {
+                uint32_t v[MAX_CLUSTER];
+#pragma unroll
+                for (int r = 0; r < MAX_CLUSTER; ++r) v[r] = cluster_ld(cluster_map(smem_u32(hs + bin), min(r, n_cta - 1)));
+#pragma unroll
+                for (int r = 0; r < MAX_CLUSTER; ++r) c += r < n_cta ? (int)v[r] : 0;
+            }
+            above += before(c);
+            if (above < want && want <= above + c) {
+                s_digit = (uint32_t)bin;
+                s_above = (uint32_t)above;
+                s_match = (uint32_t)c;
             }
         }
         __syncthreads();
         prefix |= s_digit << shift;
         mask |= ((1u << bits) - 1) << shift;
         want -= (int)s_above;
+        if (want == (int)s_match) break;                   // all that match stay: lower bits do not matter
     }
     // What each CTA puts into s_xchg[k], two 16-bit counts: sums over the CTAs before this one, and of the lower
     // one over all.
@@ -250,16 +340,10 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
         if (n_cta == 1) return (int)(mine & 0xffffu);
         if (tid == 0) s_xchg[k] = mine;
         cluster_sync_all();
-        int all = 0;
-        for (int r = 0; r < n_cta; ++r) {
-            const uint32_t x = cluster_ld(cluster_map(smem_u32(&s_xchg[k]), r));
-            all += (int)(x & 0xffffu);
-            if (r < rank) {
-                before_lo += (int)(x & 0xffffu);
-                before_hi += (int)(x >> 16);
-            }
-        }
-        return all;
+        const uint32_t x = lane < n_cta ? cluster_ld(cluster_map(smem_u32(&s_xchg[k]), lane)) : 0u;
+        before_lo = (int)__reduce_add_sync(0xffffffffu, lane < rank ? x & 0xffffu : 0u);
+        before_hi = (int)__reduce_add_sync(0xffffffffu, lane < rank ? x >> 16 : 0u);
+        return (int)__reduce_add_sync(0xffffffffu, x & 0xffffu);
     };
 
     // ---- `want` of the s_match keys equal to `prefix` stay, those in the lowest slots: where that is not all of
@@ -271,40 +355,46 @@ __global__ void __launch_bounds__(evict::THREADS, evict::PER_SM) evict_kernel(co
         for (int s = 0; s < stripes; ++s) {
             const int i = s * THREADS + tid;
             const unsigned tie = __ballot_sync(0xffffffffu, i < n && keys[i] == prefix);
-            if (lane == 0) s_cnt[0][s * WARPS + warp] = __popc(tie);
+            if (lane == 0) s_bits[s * WARPS + warp] = tie;
         }
-        const int ties = stripe_prefix(s_cnt[0], stripes, s_scan);
+        const int ties = stripe_prefix(s_cnt, stripes, s_scan, [&](int w) { return __popc(s_bits[w]); });
         exchange(0, (uint32_t)ties, ties_before, unused);
     }
-    // holes (given up below the budget) and moves (kept past it), 16 bits each: at most 32768 per CTA
+    // holes (given up below the budget) and moves (kept past it): a bit each for the 32 slots of a (stripe, warp), and
+    // their counts, 16 bits each: at most 32768 per CTA
+    auto under = [&](int w) {                              // the bits of slots below the budget
+        const int k = edge - w * 32;
+        return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
+    };
 #pragma unroll 4
     for (int s = 0; s < stripes; ++s) {
         const int i = s * THREADS + tid;
         const uint32_t k = i < n ? keys[i] : 0u;
-        bool keep = i < n && k >= prefix;
+        bool keep = k >= prefix;
         if (choose) {
             const bool tie = i < n && k == prefix;
             const unsigned m = __ballot_sync(0xffffffffu, tie);
-            if (tie) keep = ties_before + s_cnt[0][s * WARPS + warp] + __popc(m & below) < want;
+            if (tie) keep = ties_before + s_cnt[s * WARPS + warp] + __popc(m & below) < want;
         }
-        const unsigned out = __ballot_sync(0xffffffffu, i < n && i < edge && !keep);
-        const unsigned in = __ballot_sync(0xffffffffu, i >= edge && keep);
-        if (i < n) keys[i] = keep;
-        if (lane == 0) s_cnt[1][s * WARPS + warp] = __popc(out) | __popc(in) << 16;
+        const unsigned m = __ballot_sync(0xffffffffu, i < n && keep != (i < edge));
+        if (lane == 0) s_bits[s * WARPS + warp] = m;
     }
-    const uint32_t both = (uint32_t)stripe_prefix(s_cnt[1], stripes, s_scan);
+    const uint32_t both = (uint32_t)stripe_prefix(s_cnt, stripes, s_scan, [&](int w) {
+        const uint32_t m = s_bits[w], u = under(w);
+        return __popc(m & u) | __popc(m & ~u) << 16;
+    });
     int hole_at, move_at;
     const int holes = exchange(1, both, hole_at, move_at);
     int32_t *src = p.src + (int64_t)row * p.most, *dst = p.dst + (int64_t)row * p.most;
 #pragma unroll 4
     for (int s = 0; s < stripes; ++s) {
+        const int w = s * WARPS + warp;
+        const uint32_t m = s_bits[w];
+        if ((m >> lane & 1) == 0) continue;
+        const uint32_t u = under(w), at = (uint32_t)s_cnt[w];
         const int i = s * THREADS + tid;
-        const bool keep = i < n && keys[i] != 0;
-        const unsigned out = __ballot_sync(0xffffffffu, i < n && i < edge && !keep);
-        const unsigned in = __ballot_sync(0xffffffffu, i >= edge && keep);
-        const uint32_t at = (uint32_t)s_cnt[1][s * WARPS + warp];
-        if (out >> lane & 1) dst[hole_at + (int)(at & 0xffffu) + __popc(out & below)] = lo + i;
-        if (in >> lane & 1) src[move_at + (int)(at >> 16) + __popc(in & below)] = lo + i;
+        if (u >> lane & 1) dst[hole_at + (int)(at & 0xffffu) + __popc(m & u & below)] = lo + i;
+        else src[move_at + (int)(at >> 16) + __popc(m & ~u & below)] = lo + i;
     }
     // ---- the moves, dealt to the cluster's warps evenly, at most 32 at a time (the lists are in global memory: L2)
     __syncthreads();
@@ -430,7 +520,8 @@ extern "C" int mmq_kv_evict(const mmq_kv_cache *cache, int budget, const int32_t
     // are resident and each still has 2048 keys
     int cl = (cap + evict::MAX_CHUNK - 1) / evict::MAX_CHUNK;
     while (cl < evict::MAX_CLUSTER && rows * (cl + 1) <= evict::PER_SM * sm_count() && cap > 2048 * cl) ++cl;
-    p.chunk_cap = (cap + cl - 1) / cl;
+    p.chunk_cap = ((cap + cl - 1) / cl + 3) & ~3;
+    p.wide = cache->page_size % 4 == 0 && aligned16(cache->weight) && aligned16(cache->pos) && aligned16(weight_out) && aligned16(pos_out);
     p.cols_cap = cache->cols < evict::MAX_COLS ? cache->cols : evict::MAX_COLS;
     return launch_evict(p, rows, cl, s);
 }

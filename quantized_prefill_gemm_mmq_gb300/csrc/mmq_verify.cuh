@@ -71,13 +71,6 @@ __device__ __forceinline__ unsigned long long ver_join(uint32_t hi, uint32_t lo,
     return ((unsigned long long)(hi - n * 0x4b000000u) << 23) + (lo - n * 0x4b000000u);
 }
 
-__device__ __forceinline__ unsigned long long cluster_ld64(uint32_t a)
-{
-    unsigned long long v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-    return v;
-}
-
 // A row of n values.  load(j): the 16 bytes from value j on, zeros outside the
 // row.  `odd`: how far value j (a multiple of 16 bytes from `first`) lies past
 // a 16-byte boundary, the same for every j.
