@@ -17,9 +17,11 @@
 // row, where it lies otherwise, a lane takes its 16 bytes out of two aligned
 // ones.
 // Bound by memory (one or two rows of the vocabulary per sequence) and, near
-// it, by some fourteen instructions per value.
-// Measured: 64 sequences of 7 drafts over 128001 values in bf16 13 us (2.1
-// TB/s; the first 2.5 us find the rejections), 3 drafts over 32000 5 us.
+// it, by some eleven instructions per value, so a span that lies inside the rows
+// is loaded without the checks that the rows' ends need (64 sequences: 13.3 us
+// with the checks everywhere and a 64-bit sum by shuffles, 11.7 without).
+// Measured: 64 sequences of 7 drafts over 128001 values in bf16 11.7 us (2.4
+// TB/s; the first 2.5 us find the rejections), 3 drafts over 32000 4.5 us.
 #pragma once
 
 namespace mmq {
@@ -71,6 +73,21 @@ __device__ __forceinline__ unsigned long long ver_join(uint32_t hi, uint32_t lo,
     return ((unsigned long long)(hi - n * 0x4b000000u) << 23) + (lo - n * 0x4b000000u);
 }
 
+// bytes odd .. odd+15 of the 32 in x and y; odd is the same for the whole warp
+__device__ __forceinline__ uint4 ver_shift(const uint4 &x, const uint4 &y, uint32_t odd)
+{
+    const uint32_t s = (odd & 3) * 8;
+    const auto by = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e) {
+        return make_uint4(__funnelshift_r(a, b, s), __funnelshift_r(b, c, s), __funnelshift_r(c, d, s), __funnelshift_r(d, e, s));
+    };
+    switch (odd >> 2) {
+    case 0: return by(x.x, x.y, x.z, x.w, y.x);
+    case 1: return by(x.y, x.z, x.w, y.x, y.y);
+    case 2: return by(x.z, x.w, y.x, y.y, y.z);
+    default: return by(x.w, y.x, y.y, y.z, y.w);
+    }
+}
+
 // A row of n values.  load(j): the 16 bytes from value j on, zeros outside the
 // row.  `odd`: how far value j (a multiple of 16 bytes from `first`) lies past
 // a 16-byte boundary, the same for every j.
@@ -96,25 +113,40 @@ struct VerRow {
         const uint4 x = *a;
         if (odd == 0) return x;
         const uint4 y = *(a + 1);
-        // bytes odd .. odd+15 of the 32: by two words, by one, by bits
-        uint32_t w[6] = {x.x, x.y, x.z, x.w, y.x, y.y};
-        if (odd & 8) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = y.z, w[5] = y.w;
-        if (odd & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
-        const uint32_t s = (odd & 3) * 8;
-        return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
-                          __funnelshift_r(w[3], w[4], s));
+        return ver_shift(x, y, odd);
     }
 };
 
-// the sum of the w_j of 16 bytes' worth of values
+// ver_add of two values, with packed products and sums: one instruction for two
+__device__ __forceinline__ void ver_add2(float p0, float p1, float q0, float q1, uint32_t &hi, uint32_t &lo)
+{
+    const float d0 = __saturatef(__fsub_rn(p0, q0)), d1 = __saturatef(__fsub_rn(p1, q1));
+    uint32_t t0, t1, l0, l1;
+    asm("{\n\t"
+        ".reg .b64 d, t, m, r, c17, c23;\n\t"
+        "mov.b64 d, {%4, %5};\n\t"
+        "mov.b64 c17, {%6, %6};\n\t"
+        "mov.b64 c23, {%7, %7};\n\t"
+        "fma.rm.f32x2 t, d, c17, c23;\n\t"
+        "sub.rn.f32x2 m, c23, t;\n\t"
+        "fma.rn.f32x2 r, d, c17, m;\n\t"
+        "fma.rn.f32x2 r, r, c23, c23;\n\t"
+        "mov.b64 {%0, %1}, t;\n\t"
+        "mov.b64 {%2, %3}, r;\n\t"
+        "}"
+        : "=r"(t0), "=r"(t1), "=r"(l0), "=r"(l1)
+        : "f"(d0), "f"(d1), "f"(0x1p17f), "f"(0x1p23f));
+    hi += t0 + t1;
+    lo += l0 + l1;
+}
+
+// adds the w_j of 16 bytes' worth of values to hi and lo
 template <typename T>
-__device__ __forceinline__ unsigned long long ver_sum(const uint4 &pv, const uint4 &qv)
+__device__ __forceinline__ void ver_sum(const uint4 &pv, const uint4 &qv, uint32_t &hi, uint32_t &lo)
 {
     const T *p = reinterpret_cast<const T *>(&pv), *q = reinterpret_cast<const T *>(&qv);
-    uint32_t hi = 0, lo = 0;
 #pragma unroll
-    for (int k = 0; k < ver::kPer<T>; ++k) ver_add(ver_f(p[k]), ver_f(q[k]), hi, lo);
-    return ver_join(hi, lo, ver::kPer<T>);
+    for (int k = 0; k < ver::kPer<T>; k += 2) ver_add2(ver_f(p[k]), ver_f(p[k + 1]), ver_f(q[k]), ver_f(q[k + 1]), hi, lo);
 }
 
 template <typename T>
@@ -186,23 +218,47 @@ __global__ void __launch_bounds__(ver::THREADS, ver::PER_SM) spec_verify_kernel(
     for (int tries = 0; tries < 2; ++tries) {
         const bool plain = tries == 1;                      // the target alone, if nothing of the difference is left
         unsigned long long sum = 0;
-#pragma unroll 1
+#pragma unroll (sizeof(T) == 4 ? 1 : 2)                  // two f32 spans do not fit the registers
         for (int sp = warp; sp < p.spans; sp += WARPS) {
             uint4 pv[BATCH], qv[BATCH];
+            const int j0 = lo + sp * SPAN;
+            // a span whose 16-byte words all lie in the rows, and where nothing but a draft's row is taken off
+            if (j0 >= PER && j0 + SPAN + PER <= p.vocab && (qr || plain || whole_tok < j0 || whole_tok >= j0 + SPAN)) {
+                const bool with = qr && !plain;
+                const uint4 *a = reinterpret_cast<const uint4 *>(pr + j0) + lane;
+                const uint4 *c = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(qrow.row + j0) - qrow.odd) + lane;
+                uint4 next[BATCH];
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int j = lo + sp * SPAN + (k * 32 + lane) * PER;
-                pv[k] = qv[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (j < p.vocab) {
-                    pv[k] = prow.load(j, p.vocab);
-                    qv[k] = load_q(j, plain);
+                for (int k = 0; k < BATCH; ++k) {
+                    pv[k] = a[k * 32];
+                    qv[k] = next[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (with) {
+                        qv[k] = c[k * 32];
+                        if (qrow.odd) next[k] = c[k * 32 + 1];
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) qv[k] = ver_shift(qv[k], next[k], qrow.odd);
+            } else {
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int j = j0 + (k * 32 + lane) * PER;
+                    pv[k] = qv[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (j < p.vocab) {
+                        pv[k] = prow.load(j, p.vocab);
+                        qv[k] = load_q(j, plain);
+                    }
                 }
             }
-            unsigned long long w = 0;
+            uint32_t hi = 0, low = 0;
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) w += ver_sum<T>(pv[k], qv[k]);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            for (int k = 0; k < BATCH; ++k) ver_sum<T>(pv[k], qv[k], hi, low);
+            // the warp's: per lane hi is up to 2^21 and low up to 2^27, the latter added in two parts
+            hi -= BATCH * PER * 0x4b000000u;
+            low -= BATCH * PER * 0x4b000000u;
+            const unsigned long long w = ((unsigned long long)__reduce_add_sync(0xffffffffu, hi) << 23) +
+                                         ((unsigned long long)__reduce_add_sync(0xffffffffu, low >> 16) << 16) +
+                                         __reduce_add_sync(0xffffffffu, low & 0xffffu);
             if (lane == 0) s_span[sp] = w;
             sum += w;
         }
@@ -253,7 +309,9 @@ __global__ void __launch_bounds__(ver::THREADS, ver::PER_SM) spec_verify_kernel(
                         pv = prow.load(j, p.vocab);
                         qv = load_q(j, plain);
                     }
-                    const unsigned long long x = ver_sum<T>(pv, qv);
+                    uint32_t hi = 0, low = 0;
+                    ver_sum<T>(pv, qv, hi, low);
+                    const unsigned long long x = ver_join(hi, low, PER);
                     unsigned long long c = x;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
