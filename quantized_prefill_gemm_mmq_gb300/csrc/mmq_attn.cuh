@@ -233,6 +233,10 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
     constexpr int NT = TW / 8, KS = DP / 16, DT = DP / 8, ROWS = S::kRows;
     constexpr int CPR = DP / 8, PASSES = TILE * CPR / THREADS;              // 16-byte copies per row, and per thread and tile
     static_assert(TILE * CPR % THREADS == 0, "copies come out even");
+    // A page id is loaded an iteration before the address it gives is computed: under load a miss in L1 takes longer
+    // than a tile (11 sequences of 4637 in pages of 16, f16, heads of 64: 90 us and 75).  Not where the registers are
+    // full, and the place that waits is spilled (bf16, 16 rows of 128: 51 us and 54; 60 rows of 64: 63 and 70).
+    constexpr bool AHEAD = !(BF && (S::kFull || (DP == 64 && UG == 4) || (DP == 192 && UG == 2)));
 
     pdl_wait();
     pdl_launch_dependents();       // the joining launch may start; what this one writes it reads after this one's end
@@ -289,22 +293,34 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
     int seg_base = u0 - cur.tile;                             // first tile of the segment at `cur`
     AttnCursor inf = cur;                                     // next tile to look up
 
-    // addresses of K and V of entry `tid` of the tile at `inf`; 0 past the length (an entry with a bad page, which is
-    // reported, reads the pool's first row)
+    // Where entry `tid` of the tile at `inf` lies, and its row's addresses: 0 past the length; an entry with a bad page,
+    // which is reported, gets the pool's first row.
+    struct Place {
+        int page, off, h;                                     // off: slot within the page, -1 for none
+    };
     auto look_up = [&](bool there) {
-        ulonglong2 r = make_ulonglong2(0, 0);
+        Place r = {0, -1, 0};
         if (there) {
             const int slot = inf.tile * TILE + tid;
             if (tid < TILE && slot < inf.len) {
                 const int col = p.page_div.of(slot);
-                int off = slot - col * p.c.page_size;
-                int64_t pg = cache_page(p.c, inf.b, col, KID_ATTN);
-                if (pg < 0) pg = off = 0;
-                r = make_ulonglong2(
-                    (unsigned long long)(static_cast<const T *>(p.c.k) + pg * p.c.k_page + inf.h * p.c.k_head + off * p.c.k_slot),
-                    (unsigned long long)(static_cast<const T *>(p.c.v) + pg * p.c.v_page + inf.h * p.c.v_head + off * p.c.v_slot));
+                r.off = slot - col * p.c.page_size;
+                r.page = *(p.c.table + (int64_t)inf.b * p.c.cols + col);
+                r.h = inf.h;
             }
             attn_advance<TILE>(p, inf);
+        }
+        return r;
+    };
+    auto addresses = [&](const Place &x) {
+        ulonglong2 r = make_ulonglong2(0, 0);
+        if (x.off >= 0) {
+            int64_t pg = checked_page(p.c, x.page, KID_ATTN);
+            int off = x.off;
+            if (pg < 0) pg = off = 0;
+            r = make_ulonglong2(
+                (unsigned long long)(static_cast<const T *>(p.c.k) + pg * p.c.k_page + x.h * p.c.k_head + off * p.c.k_slot),
+                (unsigned long long)(static_cast<const T *>(p.c.v) + pg * p.c.v_page + x.h * p.c.v_head + off * p.c.v_slot));
         }
         return r;
     };
@@ -341,14 +357,15 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
         }
     };
 
+    Place next;                                               // in the tile STAGES ahead
     {
-        ulonglong2 r[STAGES];
+        Place r[STAGES];
 #pragma unroll
         for (int k = 0; k < STAGES; ++k) r[k] = look_up(k < n_units);
-        if (tid < TILE) {
+        if (AHEAD) next = look_up(STAGES < n_units);
 #pragma unroll
-            for (int k = 0; k < STAGES; ++k) s_row[k][tid] = r[k];
-        }
+        for (int k = 0; k < STAGES; ++k)
+            if (tid < TILE) s_row[k][tid] = addresses(r[k]);
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < STAGES - 1; ++k) {
@@ -425,7 +442,10 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
         const int stage = i % STAGES;
         if (i + STAGES - 1 < n_units) copy((i + STAGES - 1) % STAGES);
         cp_commit();
-        const ulonglong2 nrow = look_up(i + STAGES < n_units);    // its rows take the place of tile i's
+        // the rows of tile i + STAGES take the place of tile i's, which has been copied
+        if (AHEAD && tid < TILE) s_row[stage][tid] = addresses(next);
+        next = look_up(i + STAGES + AHEAD < n_units);
+        const ulonglong2 late = AHEAD ? make_ulonglong2(0, 0) : addresses(next);
 
         const int base = cur.tile * TILE + tg * TW;           // the warp's first entry
         if (base < cur.len && rt * ROWS + ug * S::kPerWarp < p.rows) {
@@ -594,7 +614,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                 }
             }
         }
-        if (tid < TILE) s_row[stage][tid] = nrow;
+        if (!AHEAD && tid < TILE) s_row[stage][tid] = late;
 
         const AttnCursor was = cur;
         attn_advance<TILE>(p, cur);

@@ -86,15 +86,20 @@ __device__ __forceinline__ int cache_len(const mmq_kv_cache &c, int b, int kid)
     return n < 0 ? 0 : cap;
 }
 
+// A page id from the table, or -1 (reported) if it is none.
+__device__ __forceinline__ int checked_page(const mmq_kv_cache &c, int pg, int kid)
+{
+    if (pg >= 0 && pg < c.pages) return pg;
+    record_error(MMQ_ERR_INDEX, kid, SITE_PAGE);
+    return -1;
+}
+
 // Page of table column `col` of sequence b, or -1 (reported) if it is none.
 template <bool L2 = false>
 __device__ __forceinline__ int cache_page(const mmq_kv_cache &c, int b, int col, int kid)
 {
     const int32_t *at = c.table + (int64_t)b * c.cols + col;
-    const int pg = L2 ? __ldcg(at) : *at;
-    if (pg >= 0 && pg < c.pages) return pg;
-    record_error(MMQ_ERR_INDEX, kid, SITE_PAGE);
-    return -1;
+    return checked_page(c, L2 ? __ldcg(at) : *at, kid);
 }
 
 // new tokens of sequence b, limited to 0..most
