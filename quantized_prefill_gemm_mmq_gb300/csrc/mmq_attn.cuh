@@ -31,7 +31,8 @@
 // share one operand, and the result's parts are added: up to four rows of bf16
 // (MODE 0), rows 0-3 hold the first parts, 4-7 the second, 8-11 the third; up
 // to eight rows (MODE 1), the upper eight hold the first part, the lower eight
-// the second, and bf16's third takes a second product.  More rows (MODE 2):
+// the second, and bf16's third takes a second product into the lower ones (the
+// tensor core cuts its sums off, so the large part's takes as few as it can).  More rows (MODE 2):
 // sixteen rows per operand, one product per part.  q is scaled by a power of
 // two per row to lie below 2, and for f16 p carries 2^15, so that f16's range
 // does not clip either.  The sums over a tile's entries stay in f32 and are
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
     // A page id is loaded an iteration before the address it gives is computed: under load a miss in L1 takes longer
     // than a tile (11 sequences of 4637 in pages of 16, f16, heads of 64: 90 us and 75).  Not where the registers are
     // full, and the place that waits is spilled (bf16, 16 rows of 128: 51 us and 54; 60 rows of 64: 63 and 70).
-    constexpr bool AHEAD = !(BF && (S::kFull || (DP == 64 && UG == 4) || (DP == 192 && UG == 2)));
+    constexpr bool AHEAD = !(BF && (S::kFull || (DP == 64 && UG == 4)));
 
     pdl_wait();
     pdl_launch_dependents();       // the joining launch may start; what this one writes it reads after this one's end
@@ -422,8 +423,8 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                             qf[0][ks][2 * e] = hi;
                             qf[0][ks][2 * e + 1] = mid;
                             if constexpr (BF) {
-                                qf[PARTS - 1][ks][2 * e] = lo;
-                                qf[PARTS - 1][ks][2 * e + 1] = 0;
+                                qf[PARTS - 1][ks][2 * e] = 0;
+                                qf[PARTS - 1][ks][2 * e + 1] = lo;
                             }
                         } else {
                             qf[0][ks][2 * e + rp] = hi;
@@ -455,9 +456,10 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
             const int seen = cur.len - n_new + 1;             // entries that every row sees
             const bool edge = base + TW > seen;               // some row may not see all of the warp's
             // Independent chains of products side by side, since one takes some 20 cycles after the one before it:
-            // NG times eight entries at a time, each in one chain, or two (even and odd steps) where NG is small.
-            // (Sixteen rows of 128 values fill the registers: there more chains spill, and 163 us became 172.)
-            constexpr int CH = S::kNg <= 2 ? 2 : 1, NG = S::kNg < NT ? S::kNg : NT;
+            // NG times eight entries at a time, each in one chain, or two (even and odd steps) where NG is small: a
+            // shorter chain is also cut off less.  (Sixteen rows of 128 values fill the registers: there more chains
+            // spill, and 163 us became 172; so do eight rows of 256 in bf16, 78 us became 82.)
+            constexpr int NG = S::kNg < NT ? S::kNg : NT, CH = NG <= 2 && !(BF && MODE == 1 && DP == 256) ? 2 : 1;
 #pragma unroll
             for (int n0 = 0; n0 < NT; n0 += NG) {
                 float acc[NG][CH][4];
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const uint32_t(&a)[4] = qf[x][2 * k2 + e];
-                                mma16816<T>(acc[n][e % CH], a[0], RP == 1 && x == 1 ? 0u : a[1], a[2], RP == 1 && x == 1 ? 0u : a[3],
+                                mma16816<T>(acc[n][e % CH], RP == 1 && x == 1 ? 0u : a[0], a[1], RP == 1 && x == 1 ? 0u : a[2], a[3],
                                             b[2 * e], b[2 * e + 1]);
                             }
                     }
@@ -540,8 +542,8 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                         pf[0][k][2 * e] = hi;
                         pf[0][k][2 * e + 1] = mid;
                         if constexpr (BF) {
-                            pf[PARTS - 1][k][2 * e] = lo;
-                            pf[PARTS - 1][k][2 * e + 1] = 0;
+                            pf[PARTS - 1][k][2 * e] = 0;
+                            pf[PARTS - 1][k][2 * e + 1] = lo;
                         }
                     } else {
                         pf[0][k][2 * e + rp] = hi;
@@ -596,9 +598,9 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
 #pragma unroll
                             for (int x = 0; x < PARTS; ++x) {
                                 const uint32_t(&a)[4] = pf[x][k];
-                                const uint32_t a1 = RP == 1 && x == 1 ? 0u : a[1], a3 = RP == 1 && x == 1 ? 0u : a[3];
-                                mma16816<T>(y[2 * d2], a[0], a1, a[2], a3, b[0], b[1]);
-                                mma16816<T>(y[2 * d2 + 1], a[0], a1, a[2], a3, b[2], b[3]);
+                                const uint32_t a0 = RP == 1 && x == 1 ? 0u : a[0], a2 = RP == 1 && x == 1 ? 0u : a[2];
+                                mma16816<T>(y[2 * d2], a0, a[1], a2, a[3], b[0], b[1]);
+                                mma16816<T>(y[2 * d2 + 1], a0, a[1], a2, a[3], b[2], b[3]);
                             }
                         }
 #pragma unroll
