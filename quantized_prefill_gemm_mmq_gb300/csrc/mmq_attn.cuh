@@ -43,10 +43,10 @@
 // segment's end), so that up to 64 rows share one read of the cache.
 //
 // Measured (a call, both launches): one token over 131071 entries of 8 heads of
-// 128, f16, 88 us = 6.1 TB/s; a ragged batch of 16 up to 32768, bf16, 190 us =
-// 6.7 TB/s (the copy rate is 6.8); over 513 entries of 32 heads 7.6 us; five
-// tokens of 8 sequences up to 4099, heads of 64 (20 rows), 28 us, where the
-// tensor pipe is 35 % active and two warps per scheduler set the pace.
+// 128, f16, 86 us = 6.3 TB/s; a ragged batch of 16 up to 32768, bf16, 186 us =
+// 6.8 TB/s (the copy rate is 6.8); over 513 entries of 32 heads 7.7 us; five
+// tokens of 8 sequences up to 4099, heads of 64 (20 rows), 27 us, where the
+// tensor pipe is 27 % active and two warps per scheduler set the pace.
 #pragma once
 
 #include <type_traits>
