@@ -493,6 +493,13 @@ def test_evict_long(ops, length, extra, weights):
     check_evict(ops, [length, 50], 1, 8, 64, length // 3, 40, weights=weights, extra=extra)
 
 
+@pytest.mark.parametrize("page", [7, 10, 12])
+@pytest.mark.parametrize("weights", ["random", "ties", "equal"])
+def test_evict_pages_across_clusters(ops, page, weights):
+    # pages that do and do not hold whole groups of four slots; lengths that end inside a group, in a part of a cluster
+    check_evict(ops, [6001, 2050, 4099, 3], 1, 16, page, 1001, 300, weights=weights, extra=3000)
+
+
 def test_evict_longest(ops):
     """The most slots a row may have, ties everywhere: the lowest slots stay and nothing moves."""
     n, budget = 262144, 100000
