@@ -62,19 +62,19 @@ constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
 template <typename T>
 constexpr float kExp = kBf16<T> ? 0.f : 15.f;      // p carries 2^kExp
 
-// DP: dim padded to 64, 96, 128, 192 or 256; MODE, UG: see above
+// DP: dim padded to 64, 80 (as 96 it took 5 to 14 % longer), 96, 128, 192 or 256; MODE, UG: see above
 template <int DP, int MODE, int UG>
 struct Shape {
     static constexpr int kPerWarp = MODE == 0 ? 4 : MODE == 1 ? 8 : 16;   // rows
     static constexpr int kTile = DP == 64 ? 128 : DP > 128 && UG > 1 ? 32 : 64;       // entries per tile
     static constexpr int kStages = DP == 192 && UG == 1 ? 2 : 3;      // tiles in the ring
     static constexpr int kPerSm = 2;                                  // CTAs resident per SM
-    static constexpr int kStride = DP == 96 ? 256 : DP * 2;           // bytes from row to row: the swizzle takes eight pieces
+    static constexpr int kStride = DP == 80 || DP == 96 ? 256 : DP * 2;           // bytes from row to row: the swizzle takes eight pieces
     static constexpr int kHalf = kTile * kStride;                     // bytes of K (or V) per stage
     static constexpr int kSmem = kStages * 2 * kHalf;
     static constexpr bool kFull = DP == 128 && MODE == 2;             // registers are
     static constexpr int kNg = kFull ? 1 : UG == 1 ? 2 : 8;           // eight-entry groups of scores at a time
-    static constexpr int kDg = kFull ? 2 : 4;                         // eight-value groups of sums at a time
+    static constexpr int kDg = kFull ? 2 : DP == 80 ? 10 : 4;                         // eight-value groups of sums at a time
     static constexpr int kRows = kPerWarp * UG;                       // rows per CTA
     // the four warps' sums are joined in one stage's memory, in as many rounds of columns as fit
     static constexpr int fit(int rounds) { return 4 * kPerWarp * (DP / rounds + 8) * 4 <= 2 * kHalf ? rounds : fit(rounds * 2); }
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
 #pragma unroll
                     for (int x = 0; x < CH; ++x) acc[n][x][0] = acc[n][x][1] = acc[n][x][2] = acc[n][x][3] = 0.f;
 #pragma unroll
-                for (int k2 = 0; k2 < KS / 2; ++k2)
+                for (int k2 = 0; k2 < (KS + 1) / 2; ++k2)       // an odd last step: half of what is loaded is not used
 #pragma unroll
                     for (int n = 0; n < NG; ++n) {
                         uint32_t b[4];                        // lane's row: entry nt*8 + lane%8, piece k2*4 + lane/8
@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                         for (int x = 0; x < PARTS; ++x)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
+                                if (2 * k2 + e >= KS) continue;
                                 const uint32_t(&a)[4] = qf[x][2 * k2 + e];
                                 mma16816<T>(acc[n][e % CH], RP == 1 && x == 1 ? 0u : a[0], a[1], RP == 1 && x == 1 ? 0u : a[2], a[3],
                                             b[2 * e], b[2 * e + 1]);
@@ -895,6 +896,7 @@ int attn_dispatch(const AttnPlan &a, int dtype, F f)
     };
     const auto with_type = [&](auto t) {
         return a.dp == 64    ? with_dp(t, integral_constant<int, 64>())
+               : a.dp == 80  ? with_dp(t, integral_constant<int, 80>())
                : a.dp == 96  ? with_dp(t, integral_constant<int, 96>())
                : a.dp == 128 ? with_dp(t, integral_constant<int, 128>())
                : a.dp == 192 ? with_dp(t, integral_constant<int, 192>())
@@ -906,7 +908,7 @@ int attn_dispatch(const AttnPlan &a, int dtype, F f)
 inline AttnPlan attn_plan(const mmq_kv_cache &c, int q_heads, int new_tokens, bool save)
 {
     AttnPlan a;
-    a.dp = c.dim <= 64 ? 64 : c.dim <= 96 ? 96 : c.dim <= 128 ? 128 : c.dim <= 192 ? 192 : 256;
+    a.dp = c.dim <= 64 ? 64 : c.dim <= 80 ? 80 : c.dim <= 96 ? 96 : c.dim <= 128 ? 128 : c.dim <= 192 ? 192 : 256;
     a.rows = q_heads / c.heads * new_tokens;
     a.mode = c.dtype == MMQ_BF16 && a.rows <= 4 ? 0 : a.rows <= 8 || a.dp > 128 ? 1 : 2;
     const int per_warp = a.mode == 2 ? 16 : 8;
