@@ -167,9 +167,13 @@ __device__ __forceinline__ float quad_sum(float x)
 
 // 1 / sum, 0 for a row that saw nothing; a NaN stays one
 __device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : sum; }
-// log2 of a row's sum of powers, so that pow2(score - it) is its weight
+// A row's maximum and a factor: pow2(score - x) * y is an entry's weight, at most 1 however large the scores.  (Their
+// log-sum in one number is off by whole powers of two where m is past 2^24.)  A row that saw nothing adds nothing.
 template <typename T>
-__device__ __forceinline__ float log_sum(float m, float sum) { return sum > 0.f ? m + log2f(sum) - kExp<T> : INFINITY; }
+__device__ __forceinline__ float2 row_norm(float m, float sum)
+{
+    return sum > 0.f ? make_float2(m, (kBf16<T> ? 1.f : 32768.f) / sum) : make_float2(INFINITY, 0.f);
+}
 
 // whether one of two values has all exponent bits set
 template <typename T>
@@ -192,7 +196,7 @@ struct AttnParams {
     float *part;             // [2*grid][kRows][DP] sums, then [2*grid][kRows][2] (max, sum)
     int3 *parts;             // [seqs*heads][row_tiles]: first part, its CTA, last CTA (-1: output written)
     float *scores;           // [seqs*heads][rows][cap] in powers of two (weights only)
-    float *lse;              // [seqs*heads][rows] (weights only, else NULL)
+    float2 *norm;            // [seqs*heads][rows] of whole rows, see row_norm (weights only, else NULL)
     int64_t cap;
     FastDiv page_div, group_div;
 };
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                         for (int e = 0; e < 2; ++e)
                             if (base + nt * 8 + 2 * j + e >= limit[rp]) s[nt][rp][e] = -INFINITY;
             }
-            if (p.lse) {
+            if (p.norm) {
 #pragma unroll
                 for (int rp = 0; rp < RP; ++rp)
                     if (holds && row0 + 8 * rp < p.rows) {
@@ -523,15 +527,17 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                 float mx = s[0][rp][0];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt][rp][0], s[nt][rp][1]));
-                mx = fmaxf(m[rp], quad_max(mx) * sfac[rp]);
+                // The maximum is kept before the row's factor, and scores are multiplied after it is taken off: the
+                // largest gives kExp exactly.  (As fma(s, sfac, -max of s*sfac) past 2^24, where the rounded maximum
+                // is off by whole numbers, p left f16's range and finite inputs gave NaN.)
+                mx = fmaxf(m[rp], quad_max(mx));
                 const float ref = mx == -INFINITY ? 0.f : mx; // nothing seen yet: every power is 0
-                alpha[rp] = pow2(m[rp] - ref);
+                alpha[rp] = pow2((m[rp] - ref) * sfac[rp]);
                 m[rp] = mx;
                 l[rp] *= alpha[rp];
-                const float shift = kExp<T> - ref;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float p0 = pow2(fmaf(s[nt][rp][0], sfac[rp], shift)), p1 = pow2(fmaf(s[nt][rp][1], sfac[rp], shift));
+                    const float p0 = pow2(fmaf(s[nt][rp][0] - ref, sfac[rp], kExp<T>)), p1 = pow2(fmaf(s[nt][rp][1] - ref, sfac[rp], kExp<T>));
                     l[rp] += p0 + p1;
                     uint32_t hi, mid, lo;
                     split<T>(p0, p1, hi, mid, lo);
@@ -640,7 +646,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
 #pragma unroll
         for (int rp = 0; rp < RP; ++rp) {
             l[rp] = quad_sum(l[rp]);
-            if (j == 0 && holds) s_ml[turned][gr + 8 * rp] = make_float2(m[rp], l[rp]);
+            if (j == 0 && holds) s_ml[turned][gr + 8 * rp] = make_float2(m[rp] * sfac[rp], l[rp]);
         }
         if constexpr (MODE == 0) {
 #pragma unroll
@@ -687,7 +693,7 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                     if (inv == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);      // saw nothing: its 0 * Inf must not show
                     if (col < p.c.dim)
                         *reinterpret_cast<float4 *>(out_row(r) + col) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-                    if (p.lse && col == 0) p.lse[seg * p.rows + rt * ROWS + r] = log_sum<T>(top, tot);
+                    if (p.norm && col == 0) p.norm[seg * p.rows + rt * ROWS + r] = row_norm<T>(top, tot);
                 } else {
                     *reinterpret_cast<float4 *>(p.part + (part * ROWS + r) * DP + col) = y;
                     if (col == 0) *reinterpret_cast<float2 *>(ml_all + (part * ROWS + r) * 2) = make_float2(top, tot);
@@ -709,20 +715,22 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
 // ways-th part, four in flight, with a running maximum, and meet in shared
 // memory.  The blocks after them (weights wanted) take JOIN_WEIGHTS entries of
 // a (sequence, head) each: weight[entry] += sum over the rows of
-// 2^(score - log-sum), the scores read side by side along the entries, the
-// log-sums of split rows from their parts, eight lanes to a row.
+// 2^(score - maximum) / sum, the scores read side by side along the entries,
+// maxima and sums of split rows from their parts, eight lanes to a row.
+// Seven blocks per SM (72 registers, 8 bytes spilled): with six, 30 sequences of
+// 1500 with five tokens of bf16 and weights took 99 us, and take 94.
 constexpr int JOIN_THREADS = 128;
 constexpr int JOIN_WEIGHTS = 1024;
 constexpr int JOIN_ROWS = 2048;      // most rows of a key-value head
 
 template <typename T>
-__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int dp, int kept_rows, int grid, int row_blocks, int64_t join_blocks,
+__global__ void __launch_bounds__(JOIN_THREADS, 7) attn_join_kernel(const AttnParams p, int dp, int kept_rows, int grid, int row_blocks, int64_t join_blocks,
                                                                  int chunks)
 {
     using namespace attn;
     __shared__ __align__(16) float4 s_y[JOIN_THREADS];
     __shared__ float2 s_ml[JOIN_THREADS];
-    __shared__ float s_lse[JOIN_ROWS];
+    __shared__ float2 s_norm[JOIN_ROWS];
     const int tid = threadIdx.x;
     const float2 *ml_all = reinterpret_cast<const float2 *>(p.part + 2 * (int64_t)grid * kept_rows * dp);
     if (blockIdx.x < join_blocks) {
@@ -817,7 +825,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     pdl_wait();
     pdl_launch_dependents();
     if (first >= len) return;
-    for (int r0 = 0; r0 < p.rows; r0 += JOIN_THREADS / 8) {               // eight lanes per row's log-sum
+    for (int r0 = 0; r0 < p.rows; r0 += JOIN_THREADS / 8) {               // eight lanes per row's sum
         const int r = r0 + tid / 8, rt = r / kept_rows, rr = r - rt * kept_rows;
         const int3 at = r < p.rows ? p.parts[seg * p.row_tiles + rt] : make_int3(0, 0, -1);
         float top = -INFINITY, tot = 0.f;
@@ -834,7 +842,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
         tot *= pow2(top - (mx == -INFINITY ? 0.f : mx));
 #pragma unroll
         for (int o = 4; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-        if (r < p.rows && tid % 8 == 0) s_lse[r] = at.z < 0 ? __ldcg(p.lse + seg * p.rows + r) : log_sum<T>(mx, tot);
+        if (r < p.rows && tid % 8 == 0) s_norm[r] = at.z < 0 ? __ldcg(p.norm + seg * p.rows + r) : row_norm<T>(mx, tot);
     }
     __syncthreads();
     if (n <= 0) return;
@@ -846,9 +854,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     for (int r = 0; r < p.rows; ++r) {
         const float4 a = __ldcg(reinterpret_cast<const float4 *>(s + r * p.cap));
         const float4 c = __ldcg(reinterpret_cast<const float4 *>(s + r * p.cap) + 1);
-        const float l = s_lse[r], v[EACH] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+        const float2 f = s_norm[r];
+        const float v[EACH] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
 #pragma unroll
-        for (int k = 0; k < EACH; ++k) add[k] += pow2(v[k] - l);
+        for (int k = 0; k < EACH; ++k) add[k] = fmaf(pow2(v[k] - f.x), f.y, add[k]);
     }
     if (together) {
         if (!at[0]) return;
@@ -871,7 +880,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
 // cache again (from L2).
 struct AttnPlan {
     int dp, mode, ug, rows, kept_rows, row_tiles, grid;
-    int64_t tiles, cap, part_floats, score_floats, lse_floats, parts;
+    int64_t tiles, cap, part_floats, score_floats, norm_floats, parts;
 };
 
 // f(type, DP, MODE, UG) with the plan's kernel as compile-time values
@@ -929,7 +938,7 @@ inline AttnPlan attn_plan(const mmq_kv_cache &c, int q_heads, int new_tokens, bo
     a.cap = ((int64_t)c.cols * c.page_size + 127) / 128 * 128;
     a.part_floats = 2 * (int64_t)a.grid * rows * (a.dp + 2);
     a.score_floats = save ? (int64_t)c.seqs * c.heads * a.rows * a.cap : 0;
-    a.lse_floats = save ? (int64_t)c.seqs * c.heads * a.rows : 0;
+    a.norm_floats = save ? 2 * (int64_t)c.seqs * c.heads * a.rows : 0;
     a.parts = (int64_t)c.seqs * c.heads * a.row_tiles;
     return a;
 }
@@ -975,7 +984,7 @@ extern "C" int mmq_attn_sizes(const mmq_kv_cache *cache, int q_heads, int new_to
     if (!work_floats) return MMQ_ERR_NULL;
     const AttnPlan a = attn_plan(*cache, q_heads, new_tokens, accumulate != 0);
     if (a.tiles > 0x7fffffff) return MMQ_ERR_SHAPE;
-    *work_floats = a.part_floats + a.score_floats + a.lse_floats + 3 * a.parts;
+    *work_floats = a.part_floats + a.score_floats + a.norm_floats + 3 * a.parts;
     return MMQ_OK;
 }
 
@@ -1012,8 +1021,8 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     p.row_tiles = a.row_tiles;
     p.scores = work;                                   // rows of a multiple of 128 floats: 16-byte aligned
     p.part = work + a.score_floats;
-    p.lse = save ? p.part + a.part_floats : nullptr;
-    p.parts = reinterpret_cast<int3 *>(p.part + a.part_floats + a.lse_floats);
+    p.norm = save ? reinterpret_cast<float2 *>(p.part + a.part_floats) : nullptr;        // 8-byte aligned: part_floats is even
+    p.parts = reinterpret_cast<int3 *>(p.part + a.part_floats + a.norm_floats);
     p.cap = a.cap;
     p.page_div = FastDiv(cache->page_size);
     p.group_div = FastDiv(p.group);
