@@ -763,8 +763,10 @@ __global__ void __launch_bounds__(JOIN_THREADS, 7) attn_join_kernel(const AttnPa
                 y.x *= old, y.y *= old, y.z *= old, y.w *= old;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float w = c + k * ways <= at.z ? pow2(ml[k].x - ref) : 0.f;
-                    if (w == 0.f) continue;                   // a part that saw nothing adds nothing
+                    // A part that saw nothing (its sum is 0) adds nothing, whatever its entries hold.  One that saw
+                    // something is added even if its weight is 0: a NaN, or 0 * Inf, has to come through.
+                    if (c + k * ways > at.z || ml[k].y == 0.f) continue;
+                    const float w = pow2(ml[k].x - ref);
                     tot = fmaf(ml[k].y, w, tot);
                     y.x = fmaf(v[k].x, w, y.x), y.y = fmaf(v[k].y, w, y.y), y.z = fmaf(v[k].z, w, y.z), y.w = fmaf(v[k].w, w, y.w);
                 }

@@ -58,3 +58,57 @@ def test_attn_large_scores(ops, dim, group, N, qscale, dtype):
                         clear += 1
             assert bool((weight[pages, h].reshape(-1)[:n] >= won * (1 - 2.0 ** -18)).all())
     assert clear > 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype,dim,group,N", [(torch.float16, 64, 1, 1), (torch.bfloat16, 128, 4, 1), (torch.bfloat16, 64, 3, 3),
+                                               (torch.float16, 128, 8, 4), (torch.float16, 256, 2, 1)])
+def test_attn_queries_that_are_not_finite(ops, bad, dtype, dim, group, N):
+    """A row of q that is not finite gives a row that is not, in one CTA's segments and in split ones; the other rows
+    do not change."""
+    cache = make_cache(ops, [20000, 40], 2, dim, 64, dtype)
+    q = torch.randn((2 * N, 2 * group, dim), generator=torch.Generator().manual_seed(7)).cuda()
+    want = ops.attn_decode(cache, q)
+    rows = [(0, 0), (2 * N - 1, 2 * group - 1)]         # of the long sequence and of the short one
+    for r, h in rows:
+        q[r, h, 3] = bad
+    got = ops.attn_decode(cache, q)
+    ops.check_status()
+    same = torch.ones((2 * N, 2 * group), dtype=torch.bool)
+    for r, h in rows:
+        assert not bool(torch.isfinite(got[r, h]).any())
+        same[r, h] = False
+    assert torch.equal(got[same.cuda()], want[same.cuda()])
+
+
+@pytest.mark.parametrize("dtype,dim,group", [(torch.float16, 64, 1), (torch.bfloat16, 128, 4), (torch.float16, 128, 8), (torch.float16, 256, 2)])
+def test_attn_runs_of_entries_that_are_not_finite(ops, dtype, dim, group):
+    """Keys that are NaN over a run that fills whole parts of a split sequence, or infinite values where the scores are
+    so low that their probability is 0: every row sees them, so no row is finite."""
+    n, page = 20000, 64
+    g = torch.Generator().manual_seed(8)
+    q = torch.randn((1, group, dim), generator=g).cuda()
+    for which in ("k", "v"):
+        cache = make_cache(ops, [n], 1, dim, page, dtype)
+        pages = cache.table[0, 100:200].long()           # entries 6400 .. 12799
+        if which == "k":
+            cache.k[pages] = float("nan")
+        else:
+            cache.v[pages] = float("inf")
+            cache.k[pages] = 0                           # scores of 0; each row has an entry of score 4000 besides
+            cache.k[cache.table[0, 0].long(), :, :group] = (q[0] * (4000.0 / q[0].square().sum(-1, keepdim=True))).to(dtype)
+        got = ops.attn_decode(cache, q, scale=1.0)
+        ops.check_status()
+        assert not bool(torch.isfinite(got).any()), which
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_attn_split_rows_that_see_nothing_are_zero(ops, dtype):
+    """Rows that are not there, over parts that hold Inf values: 0, also where the parts of a long sequence are joined."""
+    N, group, dim = 3, 2, 64
+    cache = make_cache(ops, [20000], 2, dim, 64, dtype)
+    cache.v[cache.table[0].long(), :, 5] = float("inf")
+    q = torch.randn((N, 2 * group, dim), generator=torch.Generator().manual_seed(6)).cuda()
+    got = ops.attn_decode(cache, q, new=torch.tensor([1], dtype=torch.int32).cuda())
+    ops.check_status()
+    assert not bool(torch.isfinite(got[0]).any()) and bool((got[1:] == 0).all())
