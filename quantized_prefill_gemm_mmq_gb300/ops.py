@@ -413,34 +413,7 @@ class KVCache:
 
 # The current stream's handle without the Stream object around it (2 us of every call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
-_capturing = torch.cuda.is_current_stream_capturing
 _current = torch.cuda.current_device
-
-_BLOCKS: dict = {}          # (device, stream, shape, dtype) -> small outputs not handed out yet
-_BLOCK_SLOTS, _BLOCK_MAX = 64, 16384
-
-
-def _fresh(shape: tuple, dtype, device, stream: int) -> torch.Tensor:
-    """An uninitialised output tensor for the current stream (its handle) of the current device.
-
-    Small ones (up to 16384 elements) are cut from a block of 64, each handed out once: an
-    allocation after a kernel launch takes 5 to 7 us of host time, as long as the smallest
-    calls themselves.  A block belongs to the stream it was allocated under, as the allocator
-    has it; while a graph is captured, outputs come from the graph's own memory."""
-    key = (device, stream, shape, dtype)      # the default stream's handle is the same on every device
-    slots = _BLOCKS.get(key)
-    if slots and not _capturing():
-        try:
-            return slots.pop()
-        except IndexError:      # another thread took the last one
-            pass
-    if math.prod(shape) > _BLOCK_MAX or _capturing():
-        return torch.empty(shape, dtype=dtype, device=device)
-    if len(_BLOCKS) >= 64:
-        _BLOCKS.clear()
-    block = torch.empty((_BLOCK_SLOTS * shape[0],) + tuple(shape[1:]), dtype=dtype, device=device)
-    slots = _BLOCKS[key] = list(torch.unsafe_split(block, shape[0], 0))
-    return slots.pop()
 
 
 class RopeTable:
@@ -539,7 +512,7 @@ def rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tenso
         raise ValueError("the table rotates more values than a head has, or is on another device")
     stream = _raw_stream(index)
     if out is None:
-        out, ldo = _fresh(shape, torch.float32, cache.device, stream), q_heads * dim
+        out, ldo = torch.empty(shape, dtype=torch.float32, device=cache.device), q_heads * dim
     else:
         if out.shape != shape:
             raise ValueError("out must have q's shape")
@@ -609,7 +582,7 @@ def attn_decode(cache: KVCache, q: torch.Tensor, scale: float | None = None, new
         _need(new, "new", torch.int32, (cache.seqs,), index)
     stream = _raw_stream(index)
     if out is None:
-        out = _fresh(shape, torch.float32, cache.device, stream)
+        out = torch.empty(shape, dtype=torch.float32, device=cache.device)
     else:
         _need(out, "out", torch.float32, shape, index)
     if workspace is None or not workspace.fits(floats):
@@ -694,7 +667,7 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.
     stream = _raw_stream(index)
     if out is None:
         dev = target.device
-        res, acc = _fresh((B, n1), torch.int32, dev, stream), _fresh((B,), torch.int32, dev, stream)
+        res, acc = torch.empty((B, n1), dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev)
     else:
         res, acc = out
         _need(res, "out[0]", torch.int32, (B, n1), index)

@@ -112,3 +112,43 @@ def test_attn_split_rows_that_see_nothing_are_zero(ops, dtype):
     got = ops.attn_decode(cache, q, new=torch.tensor([1], dtype=torch.int32).cuda())
     ops.check_status()
     assert not bool(torch.isfinite(got[0]).any()) and bool((got[1:] == 0).all())
+
+
+# ---------------------------------------------------------------- outputs ---
+
+def output_calls(ops, dim):
+    """name -> call returning new output tensors; shapes that depend on dim."""
+    cache = make_cache(ops, [30], 2, dim, 16)
+    q, k, v = (torch.randn((1, h, dim), generator=torch.Generator().manual_seed(h)).cuda() for h in (4, 2, 2))
+    table, pos = ops.rope_table(dim), torch.full((1,), 29, dtype=torch.int32).cuda()
+    target = torch.softmax(torch.randn((dim, 3, 50), generator=torch.Generator().manual_seed(9)), -1).cuda()
+    drafted, uniform = torch.zeros((dim, 2), dtype=torch.int32).cuda(), torch.full((dim, 3), 0.5).cuda()
+    return {"attn": lambda: [ops.attn_decode(cache, q)], "rope": lambda: [ops.rope_append(cache, table, q, k, v, pos)],
+            "verify": lambda: list(ops.spec_verify(target, None, drafted, uniform))}
+
+
+@pytest.mark.parametrize("name", ["attn", "rope", "verify"])
+def test_outputs_own_their_storage(ops, name):
+    call = output_calls(ops, 40)[name]
+    outs = [o for _ in range(6) for o in call()]
+    for o in outs:
+        assert o.untyped_storage().nbytes() == o.numel() * o.element_size() and o.storage_offset() == 0
+    kept = [o.clone() for o in outs]
+    for i, o in enumerate(outs):                        # growing one output leaves every other one alone
+        o.resize_((3 * o.shape[0],) + tuple(o.shape[1:])).fill_(-5)
+        assert all(torch.equal(a, b) for a, b in zip(outs[i + 1:], kept[i + 1:]))
+        assert all(bool((a == -5).all()) for a in outs[:i + 1])
+
+
+@pytest.mark.parametrize("name,dim", [("attn", 48), ("rope", 56), ("verify", 24)])
+def test_outputs_after_a_call_in_inference_mode(ops, name, dim):
+    call = output_calls(ops, dim)[name]
+    with torch.inference_mode():
+        call()
+    for o in call():
+        assert not o.is_inference()
+        o.add_(1)
+        if o.is_floating_point():                        # and autograd may keep it
+            w = torch.ones((), device="cuda", requires_grad=True)
+            (o * w).sum().backward()
+            assert bool(torch.isfinite(w.grad))
