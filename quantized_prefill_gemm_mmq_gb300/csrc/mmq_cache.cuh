@@ -2,6 +2,7 @@
 // checks on the host, slot lookup and type conversion on the device.
 #pragma once
 
+#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -49,6 +50,10 @@ inline int check_cache(const mmq_kv_cache *c)
     return MMQ_OK;
 }
 
+// Whether this process has launched a kernel of this unit (or captured one): before that its status word need not be
+// read, which costs a status check 8 us, and the first one 14 ms for loading the unit.
+std::atomic<bool> g_launched{false};
+
 // Launch under programmatic dependent launch: the kernel may start while the
 // one before it in the stream finishes, and waits for that one's end (pdl_wait)
 // before it touches memory, the attention's joining launch excepted.  What the
@@ -72,6 +77,7 @@ int launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaSt
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 0 ? 2 : 1;
+    g_launched.store(true, std::memory_order_relaxed);
     if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return launch_status();
     return launch_status();
 }

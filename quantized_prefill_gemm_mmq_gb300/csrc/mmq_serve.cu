@@ -30,6 +30,7 @@ int sm_count()
 
 int take_serve_status(int (&h)[8])
 {
+    if (!g_launched.load(std::memory_order_relaxed)) return MMQ_OK;        // h as the caller left it: zeros
     if (cudaMemcpyFromSymbol(h, g_status, sizeof(h)) != cudaSuccess) {
         cudaGetLastError();
         return MMQ_ERR_CUDA;

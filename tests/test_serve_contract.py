@@ -6,6 +6,10 @@ from odd places.
 Tolerances are those of test_serve_ops.py, or equality."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -152,3 +156,35 @@ def test_outputs_after_a_call_in_inference_mode(ops, name, dim):
             w = torch.ones((), device="cuda", requires_grad=True)
             (o * w).sum().backward()
             assert bool(torch.isfinite(w.grad))
+
+
+# ----------------------------------------------------------------- errors ---
+
+CHECKS = """
+import time, torch
+from quantized_prefill_gemm_mmq_gb300 import ops
+
+def check():
+    best = 1e9
+    for _ in range(30):
+        t = time.perf_counter()
+        for _ in range(50):
+            ops.check_status()
+        best = min(best, time.perf_counter() - t)
+    return best
+
+ops.quantize_q8_1(torch.randn((4, 512), device="cuda"))
+before = check()
+target = torch.full((1, 2, 4), 0.25, device="cuda")
+ops.spec_verify(target, None, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.zeros((1, 2), device="cuda"))
+print(before / check())
+"""
+
+
+def test_status_checks_of_programs_without_these_operators(ops):
+    """A process that has launched none of them does not pay for their status word: it is a second copy from the device,
+    about a third of a check's time."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CHECKS], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
+    assert float(r.stdout) < 0.85
