@@ -568,11 +568,13 @@ int mmq_spec_verify(const void *target, const void *draft, int dtype, const int3
 int mmq_probe_tensor_peak(int kind, double *tmacs, mmq_stream_t stream);
 
 /*
- * Waits for `stream`, then reports and clears the library's device status
- * word for the current device: MMQ_OK, MMQ_ERR_TIMEOUT (a kernel's pipeline
+ * Waits for `stream`, then reports and clears a device status word of the
+ * library for the current device: MMQ_OK, MMQ_ERR_TIMEOUT (a kernel's pipeline
  * wait ran past its limit; the kernel stopped early and its output is
- * invalid) or MMQ_ERR_CUDA (the stream reported a CUDA error).  If
- * `detail` is non-NULL it receives 4 ints: code, kernel id, wait site,
+ * invalid), MMQ_ERR_INDEX (a decode-side operator read an index that is out
+ * of range) or MMQ_ERR_CUDA (the stream reported a CUDA error).  If
+ * `detail` is non-NULL it receives 4 ints: code, kernel id, site (a wait, or
+ * for MMQ_ERR_INDEX 1 = length, 2 = page id, 3 = count, 4 = token),
  * linear block index of the first failure.
  */
 int mmq_check_status(mmq_stream_t stream, int *detail);

@@ -680,17 +680,29 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.
     return res, acc
 
 
+# MMQ_ERR_INDEX: kernel ids and sites of csrc/mmq_cache.cuh
+_INDEX_KERNELS = {32: "rotary append", 33: "attention", 34: "eviction", 35: "verification"}
+_INDEX_SITES = {1: "a sequence's length", 2: "a page id", 3: "a count of new or drafted tokens", 4: "a drafted token"}
+_ERR_INDEX = -11
+
+
+def _failure(st: int, detail, info) -> str:
+    """What mmq_check_status reported, in words."""
+    if st == _ERR_INDEX:
+        return f"{_INDEX_KERNELS.get(detail[1], detail[1])}: {_INDEX_SITES.get(detail[2], detail[2])} (block {detail[3]})"
+    return (f"kernel (id {detail[1]}, site {detail[2]}, block {detail[3]}; waited {info[0]} us over "
+            f"{info[1]} polls for parity {info[2]} of the barrier at shared address {info[3]})")
+
+
 def check_status(device: torch.device | None = None):
     """Synchronise the current stream and raise if a kernel reported an error."""
     dev = device or torch.device("cuda", torch.cuda.current_device())
-    detail = (ctypes.c_int * 4)()
+    detail, info = (ctypes.c_int * 4)(), (ctypes.c_int * 4)()
     with torch.cuda.device(dev):
         st = load().mmq_check_status(_stream(dev), detail)
     if st != 0:
-        info = (ctypes.c_int * 4)()
         load().mmq_last_failure_info(info)
-        raise MMQError(f"kernel (id {detail[1]}, site {detail[2]}, block {detail[3]}; waited {info[0]} us over "
-                       f"{info[1]} polls for parity {info[2]} of the barrier at shared address {info[3]})", st)
+        raise MMQError(_failure(st, detail, info), st)
 
 
 def tensor_peak_tmacs(kind: str = "int8", device: torch.device | None = None) -> float:

@@ -188,3 +188,15 @@ def test_status_checks_of_programs_without_these_operators(ops):
     r = subprocess.run([sys.executable, "-c", CHECKS], cwd=root, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr
     assert float(r.stdout) < 0.85
+
+
+def test_index_errors_say_what_they_are(ops):
+    from quantized_prefill_gemm_mmq_gb300._lib import MMQError
+    cache = make_cache(ops, [100, 50], 2, 64, 16)
+    q = torch.randn((2, 4, 64)).cuda()
+    cache.table[0, 2] = -1
+    ops.attn_decode(cache, q)
+    with pytest.raises(MMQError, match="attention: a page id") as e:
+        ops.check_status()
+    assert e.value.status == -11 and "barrier" not in str(e.value)
+    ops.check_status()
