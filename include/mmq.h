@@ -576,6 +576,9 @@ int mmq_probe_tensor_peak(int kind, double *tmacs, mmq_stream_t stream);
  * `detail` is non-NULL it receives 4 ints: code, kernel id, site (a wait, or
  * for MMQ_ERR_INDEX 1 = length, 2 = page id, 3 = count, 4 = token),
  * linear block index of the first failure.
+ * The products and the decode-side operators have a word each, and a call
+ * reports one, the products' first: where both hold an error, the next call
+ * reports the other, so call until MMQ_OK to have all.
  */
 int mmq_check_status(mmq_stream_t stream, int *detail);
 

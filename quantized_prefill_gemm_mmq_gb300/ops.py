@@ -683,7 +683,7 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.
 # MMQ_ERR_INDEX: kernel ids and sites of csrc/mmq_cache.cuh
 _INDEX_KERNELS = {32: "rotary append", 33: "attention", 34: "eviction", 35: "verification"}
 _INDEX_SITES = {1: "a sequence's length", 2: "a page id", 3: "a count of new or drafted tokens", 4: "a drafted token"}
-_ERR_INDEX = -11
+_ERR_CUDA, _ERR_INDEX = -8, -11
 
 
 def _failure(st: int, detail, info) -> str:
@@ -695,14 +695,25 @@ def _failure(st: int, detail, info) -> str:
 
 
 def check_status(device: torch.device | None = None):
-    """Synchronise the current stream and raise if a kernel reported an error."""
+    """Synchronise the current stream and raise if a kernel reported an error.
+
+    The products and the decode-side operators have a status word each; where both hold an
+    error, the one raised has the products' status and names both."""
     dev = device or torch.device("cuda", torch.cuda.current_device())
-    detail, info = (ctypes.c_int * 4)(), (ctypes.c_int * 4)()
+    first, what = 0, []
     with torch.cuda.device(dev):
-        st = load().mmq_check_status(_stream(dev), detail)
-    if st != 0:
-        load().mmq_last_failure_info(info)
-        raise MMQError(_failure(st, detail, info), st)
+        for _ in range(2):                       # mmq_check_status clears what it reports
+            detail, info = (ctypes.c_int * 4)(), (ctypes.c_int * 4)()
+            st = load().mmq_check_status(_stream(dev), detail)
+            if st == 0:
+                break
+            load().mmq_last_failure_info(info)
+            what.append(_failure(st, detail, info))
+            first = first or st
+            if st == _ERR_CUDA:
+                break
+    if first != 0:
+        raise MMQError("; ".join(what), first)
 
 
 def tensor_peak_tmacs(kind: str = "int8", device: torch.device | None = None) -> float:

@@ -200,3 +200,28 @@ def test_index_errors_say_what_they_are(ops):
         ops.check_status()
     assert e.value.status == -11 and "barrier" not in str(e.value)
     ops.check_status()
+
+
+def test_pending_errors_are_reported_together(ops):
+    """A product's wait that ran out and an attention call's bad page, both before the check: one error names both, and
+    the next check is clean."""
+    from quantized_prefill_gemm_mmq_gb300 import _lib, synth
+    lib = _lib.load()
+    cache = make_cache(ops, [100, 50], 2, 64, 16)
+    rows = torch.randn((2, 4, 64)).cuda()
+    w = torch.from_numpy(synth.make_weights("q4_K", 512, 1024, 81)).cuda()
+    x = torch.from_numpy(synth.make_x(256, 1024, 82, outliers=True)).cuda()
+    _, ds, _, xa = ops.quantize_q8_1(x, want_qs=False, want_xh=False)
+    ops.check_status()
+    try:
+        assert lib.mmq_debug_fault_inject(1, 1000) == 0  # withhold a copy; the wait for it gives up after 1 ms
+        ops.gemm("q4_K", w, xa, ds, 512)
+        torch.cuda.synchronize()
+    finally:
+        assert lib.mmq_debug_fault_inject(0, 0) == 0
+    cache.table[0, 2] = -1
+    ops.attn_decode(cache, rows)
+    with pytest.raises(_lib.MMQError) as e:
+        ops.check_status()
+    assert e.value.status == -5 and "barrier" in str(e.value) and "attention: a page id" in str(e.value)
+    ops.check_status()
