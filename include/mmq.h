@@ -526,7 +526,8 @@ int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_t ldq, cons
  * not be NaN.  cache->len is not changed: the caller lowers it to the budget
  * once all layers are done.  The pages of a sequence's first `budget` slots
  * must not be shared with another.
- * cols*page_size <= 262144.  `work` holds mmq_evict_sizes' count of ints.
+ * cols*page_size <= 262144, seqs*heads <= 268435455.  `work` holds
+ * mmq_evict_sizes' count of ints.
  */
 int mmq_evict_sizes(const mmq_kv_cache *cache, int budget, int64_t *work_ints);
 int mmq_kv_evict(const mmq_kv_cache *cache, int budget, const int32_t *keep_from, float *weight_out,

@@ -450,7 +450,9 @@ inline int evict_check(const mmq_kv_cache *c, int budget)
 {
     const int rc = check_cache(c);
     if (rc != MMQ_OK) return rc;
-    if (budget < 1 || (int64_t)c->cols * c->page_size > evict::MAX_CLUSTER * evict::MAX_CHUNK) return MMQ_ERR_SHAPE;
+    if (budget < 1 || (int64_t)c->cols * c->page_size > evict::MAX_CLUSTER * evict::MAX_CHUNK ||
+        (int64_t)c->seqs * c->heads > 0x7fffffff / evict::MAX_CLUSTER)        // a cluster per row in the grid's x
+        return MMQ_ERR_SHAPE;
     return MMQ_OK;
 }
 
@@ -500,7 +502,6 @@ extern "C" int mmq_kv_evict(const mmq_kv_cache *cache, int budget, const int32_t
     if (!cache->weight || !cache->pos || !keep_from || !weight_out || !pos_out || !work) return MMQ_ERR_NULL;
     if (weight_out == cache->weight || pos_out == cache->pos) return MMQ_ERR_SHAPE;
     const int64_t rows = (int64_t)cache->seqs * cache->heads;
-    if (rows > 65535) return MMQ_ERR_SHAPE;                // one grid row each
     if ((rc = check_arch()) != MMQ_OK) return rc;
     EvictParams p;
     p.c = *cache;

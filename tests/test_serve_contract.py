@@ -225,3 +225,24 @@ def test_pending_errors_are_reported_together(ops):
         ops.check_status()
     assert e.value.status == -5 and "barrier" in str(e.value) and "attention: a page id" in str(e.value)
     ops.check_status()
+
+
+def test_evict_more_than_65535_rows(ops):
+    """Eviction of 2100 sequences of 32 heads: what evict_workspace sizes, kv_evict takes."""
+    B, H, page, dim, n, budget = 2100, 32, 4, 8, 4, 3
+    g = torch.Generator().manual_seed(13)
+    k = torch.randn((B, H, page, dim), generator=g).half().cuda()
+    v = torch.randn((B, H, page, dim), generator=g).half().cuda()
+    table = torch.randperm(B, generator=g).to(torch.int32).view(B, 1).cuda()
+    w = torch.stack([torch.randperm(page, generator=g) for _ in range(B * H)]).view(B, H, page).float().cuda()
+    pos = torch.arange(page, dtype=torch.int32).expand(B, H, page).contiguous().cuda()
+    cache = ops.KVCache(k, v, table, torch.full((B,), n, dtype=torch.int32).cuda(), w, pos)
+    want, gone = {}, w == 0
+    for name, x in (("k", k), ("v", v), ("w", w), ("pos", pos)):
+        want[name] = x.clone()                           # one entry goes per page and head: the last takes its place
+        want[name][gone] = x[:, :, page - 1:].expand(x.shape[:3] + x.shape[3:])[gone]
+    wo, po = torch.zeros_like(w), torch.zeros_like(pos)
+    ops.kv_evict(cache, budget, torch.full((B,), n, dtype=torch.int32).cuda(), wo, po, workspace=ops.evict_workspace(cache, budget))
+    ops.check_status()
+    for got, name in ((k, "k"), (v, "v"), (wo, "w"), (po, "pos")):
+        assert torch.equal(got[:, :, :budget], want[name][:, :, :budget])

@@ -135,3 +135,14 @@ def test_rope_frequencies():
     for bad in (dict(rot=3), dict(rot=0), dict(rot=8, factor=0.5, scaling="linear"), dict(rot=8, scaling="other"), dict(rot=8, fast=1.0, slow=1.0)):
         with pytest.raises(ValueError):
             ops.rope_frequencies(**bad)
+
+
+@needs_lib
+def test_evict_sizes_refuses_what_evict_does(a):
+    lib, p, n = _lib.load(), a.p, a.null
+    ni = ctypes.c_int64()
+    for kw, ok in ((dict(seqs=2048, heads=32), True), (dict(seqs=65535, heads=4096), True), (dict(seqs=65535, heads=4097), False),
+                   (dict(seqs=65535, heads=65535), False), (dict(cols=16385), False)):
+        assert lib.mmq_evict_sizes(a.cache(**kw), 100, ctypes.byref(ni)) == (0 if ok else -1)
+        # nothing is launched: with `work` missing, a cache that fits is refused for that alone
+        assert lib.mmq_kv_evict(a.cache(**kw), 100, p, a.odd, a.odd, n, n) == (-6 if ok else -1)
