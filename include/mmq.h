@@ -502,6 +502,10 @@ int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, int rot, flo
  * the same weight at the same time.  An entry that is not finite makes the
  * rows that see it not finite.
  * 1 <= new_tokens <= 16, q_heads a multiple (1 .. 128) of heads, scale finite.
+ * Refused too (MMQ_ERR_SHAPE, by both calls) are caches of more than 2^31-1
+ * tiles (32 to 128 entries of a sequence's cols*page_size, for each head), and
+ * more than 2^31-1 of seqs * heads * (rows per key-value head, plus one per
+ * 1024 of cols*page_size if weights are accumulated).
  * `work` holds the floats that mmq_attn_sizes says.  Calls that share it must
  * be ordered (one stream).
  */

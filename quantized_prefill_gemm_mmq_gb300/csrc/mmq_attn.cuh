@@ -955,6 +955,13 @@ inline int attn_check(const mmq_kv_cache *c, int q_heads, int new_tokens)
     return MMQ_OK;
 }
 
+// Whether a plan fits: tiles are counted in an int, and so are the second launch's blocks.
+inline bool attn_fits(const mmq_kv_cache &c, const AttnPlan &a, bool save)
+{
+    const int64_t chunks = save ? (a.cap + JOIN_WEIGHTS - 1) / JOIN_WEIGHTS : 0;
+    return a.tiles <= 0x7fffffff && (int64_t)c.seqs * c.heads * (a.rows + chunks) <= 0x7fffffff;
+}
+
 template <int DP, typename T, int MODE, int UG>
 int launch_attn(const AttnParams &p, int grid, cudaStream_t stream)
 {
@@ -985,7 +992,7 @@ extern "C" int mmq_attn_sizes(const mmq_kv_cache *cache, int q_heads, int new_to
     if (rc != MMQ_OK) return rc;
     if (!work_floats) return MMQ_ERR_NULL;
     const AttnPlan a = attn_plan(*cache, q_heads, new_tokens, accumulate != 0);
-    if (a.tiles > 0x7fffffff) return MMQ_ERR_SHAPE;
+    if (!attn_fits(*cache, a, accumulate != 0)) return MMQ_ERR_SHAPE;
     *work_floats = a.part_floats + a.score_floats + a.norm_floats + 3 * a.parts;
     return MMQ_OK;
 }
@@ -1006,10 +1013,7 @@ extern "C" int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_
     if ((rc = check_arch()) != MMQ_OK) return rc;
     const bool save = accumulate != 0;
     const AttnPlan a = attn_plan(*cache, q_heads, new_tokens, save);
-    // tiles are counted in an int, and so are the second launch's blocks
-    if (a.tiles > 0x7fffffff ||
-        (int64_t)cache->seqs * cache->heads * (a.rows + (save ? (a.cap + JOIN_WEIGHTS - 1) / JOIN_WEIGHTS : 0)) > 0x7fffffff)
-        return MMQ_ERR_SHAPE;
+    if (!attn_fits(*cache, a, save)) return MMQ_ERR_SHAPE;
     AttnParams p;
     p.c = *cache;
     p.q = q;

@@ -146,3 +146,19 @@ def test_evict_sizes_refuses_what_evict_does(a):
         assert lib.mmq_evict_sizes(a.cache(**kw), 100, ctypes.byref(ni)) == (0 if ok else -1)
         # nothing is launched: with `work` missing, a cache that fits is refused for that alone
         assert lib.mmq_kv_evict(a.cache(**kw), 100, p, a.odd, a.odd, n, n) == (-6 if ok else -1)
+
+
+@needs_lib
+def test_attn_sizes_refuses_what_attention_does(a):
+    lib, p, n = _lib.load(), a.p, a.null
+    other, nf = ctypes.c_void_p(p.value + 2048), ctypes.c_int64()
+    for kw, new, acc, ok in ((dict(seqs=65535, heads=16384, cols=8), 1, 1, True),
+                             (dict(seqs=65535, heads=16384, cols=8), 2, 0, True),
+                             (dict(seqs=65535, heads=16384, cols=8), 2, 1, False),      # three blocks: two rows, one of entries
+                             (dict(seqs=65535, heads=16384, cols=8), 3, 0, False),
+                             (dict(seqs=65535, heads=16384, cols=24), 1, 0, False)):    # three tiles
+        heads = kw["heads"]
+        c = a.cache(**kw)
+        assert lib.mmq_attn_sizes(c, heads, new, acc, ctypes.byref(nf)) == (0 if ok else -1)
+        if not ok:                                            # never launched
+            assert lib.mmq_attn_decode(c, p, heads * 64, n, other, heads, new, 0.1, acc, p, n) < 0
