@@ -476,7 +476,7 @@ def _rows(t, name, heads, dim, index):
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-    return st[0] if t.shape[0] > 1 else max(st[0], heads * dim)
+    return st[0] if t.shape[0] > 1 else heads * dim          # the distance of one row from the next does not matter
 
 
 def _q_shape(cache, shape):

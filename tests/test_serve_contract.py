@@ -246,3 +246,15 @@ def test_evict_more_than_65535_rows(ops):
     ops.check_status()
     for got, name in ((k, "k"), (v, "v"), (wo, "w"), (po, "pos")):
         assert torch.equal(got[:, :, :budget], want[name][:, :, :budget])
+
+
+def test_one_row_of_a_product_of_odd_width(ops):
+    """The distance between rows does not matter where there is one: a slice of a row of any width is taken."""
+    cache = make_cache(ops, [30], 2, 64, 16)
+    wide = torch.randn((1, 8 * 64 + 3)).cuda()
+    q, k, v = (wide[:, a * 64:b * 64].view(1, b - a, 64) for a, b in ((0, 4), (4, 6), (6, 8)))
+    pos, table = torch.full((1,), 29, dtype=torch.int32).cuda(), ops.rope_table(64)
+    want = ops.rope_append(cache, table, q.contiguous(), k.contiguous(), v.contiguous(), pos)
+    assert torch.equal(ops.rope_append(cache, table, q, k, v, pos), want)
+    assert torch.equal(ops.attn_decode(cache, q), ops.attn_decode(cache, q.contiguous()))
+    ops.check_status()
