@@ -10,7 +10,8 @@ probabilities, and drops the rejected ones.  Per layer:
 
     q8_1 quantisation + products (q, k, v, o, gate, up, down)
     rope_append    rotary q and k; k and v into the paged cache
-    attn_decode    attention of the new tokens, adding up what each entry got
+    attn_decode    attention of the new tokens, adding up what each entry got; rows of
+                   drafts add nothing until it is known which of them stay
     kv_evict       once the cache is `slack` entries past its budget
 
 Norms, residuals and sampling inputs are plain torch.
@@ -76,9 +77,15 @@ class Decoder:
         self.entries = 0                                      # the host's copy of the length
         self.work = {n: ops.attn_workspace(self.caches[0], heads, n, True) for n in range(1, CHUNK + 1)}
         self.evict_work = None
+        self.held = None                                      # q rows per layer whose weights are not added yet
 
-    def forward(self, tokens):
-        """Logits of the new tokens [n <= 16][vocab]; they become the cache's last entries."""
+    def forward(self, tokens, drafts=0):
+        """Logits of the new tokens [n <= 16][vocab]; they become the cache's last entries.
+
+        With drafts among them, what the rows attend to is added to the entries' weights only
+        when drop() says which stay: a draft that is turned down must not steer an eviction."""
+        self.drop(0)
+        self.held = [] if drafts else None
         n = len(tokens)
         self.lens.add_(n)
         self.entries += n
@@ -89,7 +96,9 @@ class Decoder:
             q, k, v = layer.product(("q", "k", "v"), norm(x))
             q = ops.rope_append(cache, self.rope, norm(q.view(n, self.heads, self.dim)), norm(k.view(n, self.kv_heads, self.dim)),
                                 v.view(n, self.kv_heads, self.dim), pos)
-            a = ops.attn_decode(cache, q, accumulate=True, workspace=self.work[n])
+            a = ops.attn_decode(cache, q, accumulate=not drafts, workspace=self.work[n])
+            if drafts:
+                self.held.append(q)
             o, = layer.product(("o",), norm(a.view(n, -1)))
             x = x + norm(o)
             gate, up = layer.product(("gate", "up"), norm(x))
@@ -98,12 +107,20 @@ class Decoder:
         return norm(x) @ self.embed.T * x.shape[-1] ** -0.5
 
     def drop(self, n):
-        """Take the last n entries back (rejected drafts)."""
-        self.lens.sub_(n)
-        self.entries -= n
-        self.next_pos -= n
+        """Take the last n entries back (rejected drafts), and add the weights of the rows that stay."""
+        if n:
+            self.lens.sub_(n)
+            self.entries -= n
+            self.next_pos -= n
+        if self.held:
+            rows = self.held[0].shape[0]
+            stay = torch.full((1,), rows - n, dtype=torch.int32, device=self.dev)
+            for cache, q in zip(self.caches, self.held):
+                ops.attn_decode(cache, q, new=stay, accumulate=True, workspace=self.work[rows])
+            self.held = None
 
     def evict(self, budget, recent):
+        self.drop(0)
         keep_from = torch.full((1,), self.next_pos - recent, dtype=torch.int32, device=self.dev)
         if self.evict_work is None:
             self.evict_work = ops.evict_workspace(self.caches[0], budget)
@@ -137,7 +154,7 @@ def generate(model, prompt, steps, budget, slack=32, drafts=3, temperature=0.05,
     for _ in range(steps):
         guess = draft(history, drafts)
         n = len(guess)
-        target = torch.softmax(model.forward([history[-1]] + guess) / temperature, -1)[None]
+        target = torch.softmax(model.forward([history[-1]] + guess, drafts=n) / temperature, -1)[None]
         uniform = torch.rand((1, n + 1), generator=g, device=model.dev)
         if n:
             tokens, accepted = ops.spec_verify(target.contiguous(), None, torch.tensor([guess], dtype=torch.int32, device=model.dev), uniform)

@@ -497,7 +497,11 @@ int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, int rot, flo
  * bf16) parts, so products carry f32's precision.  Results do not depend on
  * timing: they repeat bit for bit.
  * accumulate != 0 adds to cache->weight, for every entry a sequence has, the
- * sum of p over its rows and the query heads of the key-value head.  Sequences
+ * sum of p over its rows and the query heads of the key-value head.  Rows of
+ * drafted tokens add theirs like any other, and a shorter len does not take
+ * that back: attend drafts without accumulating, and once it is known how many
+ * stay, call again with the same q, len lowered, new_len = the rows that stay,
+ * and accumulate.  What rows that are not finite add is unspecified.  Sequences
  * may share pages (a common beginning), but not then: two of them would add to
  * the same weight at the same time.  An entry that is not finite makes the
  * rows that see it not finite.

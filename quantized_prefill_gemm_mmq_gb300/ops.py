@@ -559,7 +559,9 @@ def attn_decode(cache: KVCache, q: torch.Tensor, scale: float | None = None, new
     q f32 [seqs*n][q_heads][dim], rotated; row t of a sequence sees the entries up to its
     own (new int32 [seqs] limits the rows as in rope_append; rows past it get 0).  scale
     defaults to dim^-0.5.  accumulate adds every entry's weight to cache.weight (no
-    page may belong to two sequences then).  Without `workspace` one is allocated for this call."""
+    page may belong to two sequences then).  Drafted rows are attended without it, and those
+    that stay again with it, once lens is lowered (new: how many), since a rejected row's
+    weights cannot be taken back.  Without `workspace` one is allocated for this call."""
     index, dim = cache.index, cache.dim
     if index != _current():
         with torch.cuda.device(index):

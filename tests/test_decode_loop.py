@@ -75,3 +75,37 @@ def test_generate_with_eviction(ex):
         for h in range(pos.shape[1]):
             have = set(pos[:, h].tolist())
             assert len(have) == m.entries and all(x in have for x in range(m.next_pos - 12, m.next_pos))
+
+
+def live_weights(m, cache):
+    """[heads][entries]"""
+    return cache.weight[cache.table[0].long()].transpose(0, 1).flatten(1)[:, :m.entries]
+
+
+def test_dropped_drafts_leave_no_trace_in_the_weights(ex):
+    """What eviction goes by: every row that stayed hands out one unit per query head, a rejected draft's row nothing."""
+    tokens = list(range(20))
+    a, b = ex.Decoder(**SMALL), ex.Decoder(**SMALL)
+    for m in (a, b):
+        m.forward(tokens[:16])
+    a.forward([16, 17, 900, 901], drafts=3)                    # three drafts, the first accepted
+    a.drop(2)
+    b.forward([16])
+    b.forward([17])
+    for m in (a, b):
+        m.forward([18])
+    for ca, cb in zip(a.caches, b.caches):
+        wa, wb = live_weights(a, ca), live_weights(b, cb)
+        assert wa.shape == wb.shape == (2, 19)
+        assert torch.allclose(wa.sum(1), torch.full_like(wa.sum(1), 19 * 4.0), rtol=1e-4)
+        assert float((wa - wb).abs().max()) <= 2e-2 * float(wb.max())
+
+
+def test_generate_counts_no_rejected_rows(ex):
+    prompt = torch.randint(0, 50, (90,), generator=torch.Generator().manual_seed(4)).tolist()
+    m = ex.Decoder(**{**SMALL, "vocab": 60})
+    _, (drafted, accepted, evictions) = ex.generate(m, prompt, steps=30, budget=1000, temperature=2.0)
+    assert drafted > accepted > 0 and evictions == 0           # warm enough that drafts are turned down
+    for c in m.caches:
+        total = live_weights(m, c).sum(1)
+        assert torch.allclose(total, torch.full_like(total, m.entries * 4.0), rtol=1e-4)
