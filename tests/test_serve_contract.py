@@ -258,3 +258,83 @@ def test_one_row_of_a_product_of_odd_width(ops):
     assert torch.equal(ops.rope_append(cache, table, q, k, v, pos), want)
     assert torch.equal(ops.attn_decode(cache, q), ops.attn_decode(cache, q.contiguous()))
     ops.check_status()
+
+
+# ----------------------------------------------- further sizes and ranges ---
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim", [72, 80])
+@pytest.mark.parametrize("group,N", [(20, 1), (8, 5), (35, 2), (13, 6)])
+def test_attn_many_rows_of_80(ops, dtype, dim, group, N):
+    """Two and four warps along 20 to 78 rows of heads of 72 and 80."""
+    for accumulate in (False, True):
+        check_attention(ops, [150, N, 129], N, group, 1, dim, 16, dtype, new=[N, N, N - 1], accumulate=accumulate,
+                        seed=group, fill=float("inf"))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("group", [1, 20])
+def test_attn_long_split_of_80(ops, dtype, group):
+    check_attention(ops, [20000, 40], 1, group, 1, 80, 64, dtype, seed=9)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype,group", [(torch.float16, 1), (torch.bfloat16, 5), (torch.float16, 12)])
+def test_attn_masked_entries_do_not_reach_earlier_rows_of_80(ops, bad, dtype, group):
+    N, lens = 4, [67, 131]
+    cache = make_cache(ops, lens, 2, 80, 16, dtype)
+    q = torch.randn((8, 2 * group, 80), generator=torch.Generator().manual_seed(5)).cuda()
+    want = ops.attn_decode(cache, q)
+    tab = cache.table.cpu()
+    for b, n in enumerate(lens):                         # the last new entry is not finite
+        pg, off = ref.slot_place(tab, 16, b, n - 1)
+        cache.v[pg, :, off] = bad
+        cache.k[pg, :, off] = bad
+    got = ops.attn_decode(cache, q)
+    ops.check_status()
+    for b in range(2):
+        a, w = got[b * N:b * N + 3], want[b * N:b * N + 3]
+        assert float((a - w).abs().max()) <= 2.0 ** -18 * float(w.abs().max())
+        assert not bool(torch.isfinite(got[b * N + 3]).any())
+
+
+def verify_counts(target, draft, n):
+    """How often each token comes first, over the n x n pairs of midpoint uniforms: [drafted][token], in whole numbers."""
+    u = (np.arange(n) + 0.5) / n
+    V, counts = len(target), np.zeros((len(target), len(target)), np.int64)
+    whole = lambda x: [round(float(min(max(y, np.float32(0)), np.float32(1))) * 2 ** 40) for y in x]  # noqa: E731
+    rest = whole(target - draft)
+    cum = np.cumsum(np.array(rest, dtype=object))
+    redraw = np.zeros(V, np.int64)
+    for x in u:
+        r = cum[-1] * int(x * 2 ** 24) >> 24
+        redraw[next(j for j in range(V) if cum[j] > r)] += 1
+    for x in range(V):
+        accepted = int((u.astype(np.float32) * draft[x] < target[x]).sum())
+        counts[x] = (n - accepted) * redraw
+        counts[x, x] += n * accepted
+    return counts
+
+
+def test_verify_counts(ops):
+    """Accepted or redrawn, the first token over a grid of 2^16 pairs of uniforms: the counts themselves, which follow
+    the target to within the grid's steps."""
+    n = 1 << 8
+    target = np.array([0.3, 0.25, 0.2, 0.1, 0.05, 0.05, 0.03, 0.02], np.float32)
+    draft = np.array([0.1, 0.1, 0.1, 0.1, 0.15, 0.15, 0.15, 0.15], np.float32)
+    counts = verify_counts(target, draft, n)
+    u = (torch.arange(n) + 0.5) / n
+    pairs = torch.stack((u.repeat_interleave(n), u.repeat(n)), 1)
+    t, d = torch.from_numpy(target).cuda(), torch.from_numpy(draft).cuda()
+    for x in range(8):
+        got = torch.zeros(8, dtype=torch.int64)
+        for part in pairs.split(n * n // 4):
+            B = part.shape[0]
+            tokens, _ = ops.spec_verify(t.expand(B, 2, 8).contiguous(), d.expand(B, 1, 8).contiguous(),
+                                        torch.full((B, 1), x, dtype=torch.int32).cuda(), part.contiguous().cuda())
+            got += torch.bincount(tokens[:, 0].cpu().long(), minlength=8)
+        assert got.tolist() == counts[x].tolist()
+    # an acceptance threshold and both ends of a redrawn token's interval lie within half a step of their place, so a
+    # token is off by at most a step of 1/n for its own acceptance, and the redrawn share (below 1) by one of 1/n more
+    total = (draft[:, None].astype(np.float64) * counts).sum(0) / n ** 2
+    assert float(np.abs(total - target).max()) <= 2 / n
