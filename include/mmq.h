@@ -436,9 +436,10 @@ int mmq_debug_subdots_q8_0(const void *w, const uint16_t *xh, int32_t *out,
  * the sequence's number of entries, the new tokens of the running step
  * included: the caller raises it once per step, before the step's first
  * layer, and lowers it after mmq_kv_evict or a rejected draft.
- * A page id outside 0..pages-1, or a len outside 0..cols*page_size, is never
- * followed: nothing is written there, results that depend on it are
- * unspecified, and mmq_check_status reports MMQ_ERR_INDEX.
+ * A page id outside 0..pages-1 is never followed: nothing is written there,
+ * and results that depend on it are unspecified.  A len outside
+ * 0..cols*page_size is taken as 0: the sequence's table row is not followed.
+ * mmq_check_status reports either as MMQ_ERR_INDEX.
  */
 enum { MMQ_F16 = 0, MMQ_BF16 = 1, MMQ_F32 = 2 };
 

@@ -82,14 +82,15 @@ int launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaSt
     return launch_status();
 }
 
-// A sequence's length, limited to what its table row can hold.  L2: not through L1 (reads before pdl_wait).
+// A sequence's length; 0 (reported) if its table row cannot hold it: table entries past the real length may hold other
+// sequences' pages, which the largest length would reach.  L2: not through L1 (reads before pdl_wait).
 template <bool L2 = false>
 __device__ __forceinline__ int cache_len(const mmq_kv_cache &c, int b, int kid)
 {
     const int n = L2 ? __ldcg(c.len + b) : *(c.len + b), cap = c.cols * c.page_size;
     if (n >= 0 && n <= cap) return n;
     record_error(MMQ_ERR_INDEX, kid, SITE_LEN);
-    return n < 0 ? 0 : cap;
+    return 0;
 }
 
 // A page id from the table, or -1 (reported) if it is none.

@@ -338,3 +338,39 @@ def test_verify_counts(ops):
     # token is off by at most a step of 1/n for its own acceptance, and the redrawn share (below 1) by one of 1/n more
     total = (draft[:, None].astype(np.float64) * counts).sum(0) / n ** 2
     assert float(np.abs(total - target).max()) <= 2 / n
+
+
+@pytest.mark.parametrize("bad", [81, 1 << 29, -1])
+def test_bad_lengths_write_nothing(ops, bad):
+    """A sequence whose length is out of range is taken as empty: the table entries past its real length, which may hold
+    another's pages, are not followed."""
+    from quantized_prefill_gemm_mmq_gb300._lib import MMQError
+    rows = [torch.randn((2, h, 64), generator=torch.Generator().manual_seed(h)).cuda() for h in (4, 2, 2)]
+    pos, table = torch.full((2,), 39, dtype=torch.int32).cuda(), ops.rope_table(64)
+    results = []
+    for first in (0, bad):
+        cache = make_cache(ops, [40, 40], 2, 64, 16, extra=40)         # five pages: 80 entries
+        cache.table[0, 2:] = cache.table[1, :3]
+        before = [t.clone() for t in (cache.k, cache.v, cache.weight, cache.pos)]
+        cache.lens[0] = first
+        ops.rope_append(cache, table, *rows, pos)
+        with pytest.raises(MMQError) as e:                             # one new token does not fit no entries either
+            ops.check_status()
+        assert e.value.status == -11
+        out = ops.attn_decode(cache, rows[0], accumulate=True)
+        assert bool((out[0] == 0).all())
+        wo, po = torch.full_like(cache.weight, -7.0), torch.full_like(cache.pos, -7)
+        ops.kv_evict(cache, 39, torch.tensor([0, 30], dtype=torch.int32).cuda(), wo, po)
+        if first == 0:
+            ops.check_status()
+        else:
+            with pytest.raises(MMQError) as e:
+                ops.check_status()
+            assert e.value.status == -11
+        own = sorted(set(cache.table[1].tolist()))
+        others = [p for p in range(cache.k.shape[0]) if p not in own]
+        for got, was in zip((cache.k, cache.v, cache.weight, cache.pos), before):
+            assert torch.equal(got[others], was[others])
+        assert bool((wo[others] == -7).all()) and bool((po[others] == -7).all())
+        results.append([t.cpu() for t in (cache.k, cache.v, cache.weight, cache.pos, wo, po, out)])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
