@@ -88,9 +88,9 @@ template <bool L2 = false>
 __device__ __forceinline__ int cache_len(const mmq_kv_cache &c, int b, int kid)
 {
     const int n = L2 ? __ldcg(c.len + b) : *(c.len + b), cap = c.cols * c.page_size;
-    if (n >= 0 && n <= cap) return n;
-    record_error(MMQ_ERR_INDEX, kid, SITE_LEN);
-    return 0;
+    const int r = (unsigned)n <= (unsigned)cap ? n : 0;
+    if (r != n) record_error(MMQ_ERR_INDEX, kid, SITE_LEN);
+    return r;
 }
 
 // A page id from the table, or -1 (reported) if it is none.
