@@ -34,7 +34,7 @@
 // the second, and bf16's third takes a second product into the lower ones (the
 // tensor core cuts its sums off, so the large part's takes as few as it can).  More rows (MODE 2):
 // sixteen rows per operand, one product per part.  q is scaled by a power of
-// two per row to lie below 2, and for f16 p carries 2^15, so that f16's range
+// two per row to lie below 4, and for f16 p carries 2^15, so that f16's range
 // does not clip either.  The sums over a tile's entries stay in f32 and are
 // added to the running sums with f32 FMAs.
 //
@@ -409,9 +409,10 @@ __global__ void __launch_bounds__(attn::THREADS, attn::Shape<DP, MODE, UG>::kPer
                         top = fmaxf(top, fmaxf(fabsf(x[ks][e].x), fabsf(x[ks][e].y)));
                     }
                 top = quad_max(top);
-                // the row's power of two, away from f32's ends; the sign of the scale goes to q, so that sfac > 0
+                // the row's power of two, where it and its inverse are normal numbers (q then lies below 4 at most); the
+                // sign of the scale goes to q, so that sfac > 0
                 int ex = (int)(__float_as_uint(top) >> 23) - 127;
-                ex = min(max(ex, -100), 100);
+                ex = min(max(ex, -126), 126);
                 const float down = copysignf(__uint_as_float((uint32_t)(127 - ex) << 23), p.scale_log2);
                 sfac[rp] = fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + ex) << 23), 1e-37f);
 #pragma unroll

@@ -374,3 +374,10 @@ def test_bad_lengths_write_nothing(ops, bad):
         assert bool((wo[others] == -7).all()) and bool((po[others] == -7).all())
         results.append([t.cpu() for t in (cache.k, cache.v, cache.weight, cache.pos, wo, po, out)])
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("qscale,scale", [(1e36, 1e-36), (1e-37, 1e36)])
+@pytest.mark.parametrize("group,N", [(1, 1), (4, 3)])
+def test_attn_queries_at_the_ends_of_f32(ops, group, N, qscale, scale, dtype):
+    check_attention(ops, [300, 20], N, 2 * group, 2, 128, 16, dtype, qscale=qscale, scale=scale)
