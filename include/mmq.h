@@ -478,7 +478,9 @@ typedef struct mmq_kv_cache {
  * to slot len[b] - new_len[b] + t of every head, rounded to the cache's type
  * (nearest even); a row past it gets q_out = 0 and is not stored.  Where the
  * cache has them, `weight` of a new entry is set to 0 and `pos` to the row's
- * position.  Slots must not repeat within a call.
+ * position.  Slots must not repeat within a call.  A new_len outside
+ * 0..new_tokens is limited to it, here and in mmq_attn_decode, and a row whose
+ * slot would be negative is not stored; both report MMQ_ERR_INDEX.
  */
 int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, int rot, float magnitude,
                     int interleaved, const float *q, int64_t ldq, const float *k, int64_t ldk,
@@ -494,9 +496,10 @@ int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, int rot, flo
  * out [seqs*new_tokens][q_heads][dim] f32, contiguous, not q.  A row that sees no
  * slot, or with t >= new_len[b], gets 0.  What a row does not see has no
  * influence on it, whatever it holds (stale NaN or Inf included).  Statistics
- * and sums are f32; q and p enter the tensor core as sums of two f16 (three
- * bf16) parts, so products carry f32's precision.  Results do not depend on
- * timing: they repeat bit for bit.
+ * and sums are f32.  q and p enter the tensor core as sums of two f16 parts (22
+ * bits of the row's largest |q|, and of the row's largest p) or three bf16 parts
+ * (24 bits); against 64 bits the output is off by 3e-7 to 1e-6 of its norm, as
+ * an f32 computation is.  Results do not depend on timing: they repeat bit for bit.
  * accumulate != 0 adds to cache->weight, for every entry a sequence has, the
  * sum of p over its rows and the query heads of the key-value head.  Rows of
  * drafted tokens add theirs like any other, and a shorter len does not take
@@ -511,8 +514,10 @@ int mmq_rope_append(const mmq_kv_cache *cache, const int64_t *freq, int rot, flo
  * tiles (32 to 128 entries of a sequence's cols*page_size, for each head), and
  * more than 2^31-1 of seqs * heads * (rows per key-value head, plus one per
  * 1024 of cols*page_size if weights are accumulated).
- * `work` holds the floats that mmq_attn_sizes says.  Calls that share it must
- * be ordered (one stream).
+ * `work` holds the floats that mmq_attn_sizes says: the parts of split rows (a
+ * few MB whatever the lengths), and with accumulate a score for each of seqs *
+ * q_heads * new_tokens rows and cols*page_size slots besides.  Calls that share
+ * it must be ordered (one stream).
  */
 int mmq_attn_sizes(const mmq_kv_cache *cache, int q_heads, int new_tokens, int accumulate,
                    int64_t *work_floats);

@@ -4,7 +4,8 @@
 // Per query row r (a token t and a query head of the key-value head's group):
 //     s = scale q.k,  p = exp(s - m),  out = sum p v / sum p
 // in one pass over the cache with a running maximum m: when a tile raises m,
-// what was summed so far is multiplied by exp(m_old - m_new).
+// what was summed so far is multiplied by exp(m_old - m_new).  m is taken off
+// before the multiplication by scale, so that scores may be of any size.
 //
 // Work.  The cache is read once; everything else is small, so the kernel is
 // bound by memory (4 dim bytes per entry and head) as long as the rows that
@@ -32,21 +33,26 @@
 // (MODE 0), rows 0-3 hold the first parts, 4-7 the second, 8-11 the third; up
 // to eight rows (MODE 1), the upper eight hold the first part, the lower eight
 // the second, and bf16's third takes a second product into the lower ones (the
-// tensor core cuts its sums off, so the large part's takes as few as it can).  More rows (MODE 2):
-// sixteen rows per operand, one product per part.  q is scaled by a power of
-// two per row to lie below 4, and for f16 p carries 2^15, so that f16's range
-// does not clip either.  The sums over a tile's entries stay in f32 and are
+// tensor core cuts its sums off, so the large part's takes as few as it can).
+// More rows (MODE 2): sixteen rows per operand, one product per part.  q is
+// scaled by a power of two per row to lie below 4, and for f16 p carries 2^15,
+// so that f16's range does not clip either.  The sums over a tile's entries stay in f32 and are
 // added to the running sums with f32 FMAs.
 //
 // UG warps of the four take these rows each over the same entries and 4/UG
 // warps split a tile's entries (with their own running maximum, joined at the
 // segment's end), so that up to 64 rows share one read of the cache.
 //
-// Measured (a call, both launches): one token over 131071 entries of 8 heads of
-// 128, f16, 86 us = 6.3 TB/s; a ragged batch of 16 up to 32768, bf16, 186 us =
-// 6.8 TB/s (the copy rate is 6.8); over 513 entries of 32 heads 7.7 us; five
-// tokens of 8 sequences up to 4099, heads of 64 (20 rows), 27 us, where the
-// tensor pipe is 27 % active and two warps per scheduler set the pace.
+// Measured (device time, both launches): one token over 131071 entries of 8
+// heads of 128, f16, 85 us = 6.3 TB/s; a ragged batch of 16 up to 32768, bf16,
+// 186 us = 6.8 TB/s (the copy rate is 6.8); over 513 entries of 32 heads 7.4 us;
+// five tokens of 8 sequences up to 4099, heads of 64 (20 rows), 27 us, where the
+// tensor pipe is 27 % active and two warps per scheduler set the pace.  More
+// rows cost more: 8 sequences of 4096 entries of 8 heads of 128 in bf16 take 34
+// us with 8 rows, 50 with 16, 62 with 32 and 106 with 64.  Some kernels of many
+// rows spill: <256, bf16, 1, 4> 504 bytes, <128, bf16, 2, 4> 360,
+// <64, bf16, 2, 4> 332, <80, bf16, 2, 4> 244, <128, bf16, 2, 1> 184,
+// <128, half, 2, 4> 136, the others at most 52.
 #pragma once
 
 #include <type_traits>
@@ -878,8 +884,8 @@ __global__ void __launch_bounds__(JOIN_THREADS, 7) attn_join_kernel(const AttnPa
 // remaining warps split the entries; for heads above 128 sixteen rows do not
 // fit the registers, and warps take eight.  Heads above 192 leave two warps of
 // four without rows rather than splitting 64 entries four ways: tiles of 32
-// let two CTAs share an SM (1 x 20000 entries of 8 heads, f16: 137 us against
-// 157).  More rows than a CTA takes are dealt to further CTAs, which read the
+// let two CTAs share an SM (8 sequences of 20000 entries of 256 values, f16: 137
+// us against 158).  More rows than a CTA takes are dealt to further CTAs, which read the
 // cache again (from L2).
 struct AttnPlan {
     int dp, mode, ug, rows, kept_rows, row_tiles, grid;

@@ -26,7 +26,8 @@
 // selection's passes.
 // Measured: 16 sequences up to 32768 entries of 8 heads of 128 down to 4096,
 // 98 us, of which 72 us move 485 MB (6.7 TB/s); 1100 entries of 32 heads down
-// to 1024, 7.3 us.
+// to 1024, 7.4 us.  Planned by what the table has room for, since lengths are on
+// the device: shared memory and the cluster follow cols*page_size.
 #pragma once
 
 namespace mmq {

