@@ -43,6 +43,11 @@
  *                              paged cache)
  *   attention, new tokens .... mmq_attn_decode (1..16 new tokens per sequence
  *                              over the paged cache)
+ *   attention, prompts ....... mmq_attn_prefill (any number of new tokens; capped
+ *                              scores, distance bias, window, prefix, documents)
+ *   norms + positions + append mmq_norm_rope_append (normed q and k heads, positions
+ *                              with several axes)
+ *   trees of drafts .......... mmq_attn_tree, then mmq_kv_keep for the accepted path
  *   bounded cache ............ mmq_kv_evict (by accumulated attention weight)
  *   drafted tokens ........... mmq_spec_verify (speculative sampling's test and
  *                              resampling)
@@ -526,6 +531,89 @@ int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_t ldq, cons
                     float *work, mmq_stream_t stream);
 
 /*
+ * mmq_rope_append with a norm of every q and k head before the rotation, and
+ * positions with several axes:
+ *     y = x * rsqrt(mean of x^2 over the head + eps) * w,
+ * w = q_norm or k_norm, f32 [dim] (NULL: that side is rotated as it is; a
+ * model that keeps w - 1 adds the 1).  Pair i turns by the row's position on
+ * axis[i] (int32 [rot/2], 0..axes-1; NULL with one axis): pos int32
+ * [axes][seqs*new_tokens], of which axis 0 goes to the cache's `pos`.  An axis
+ * outside 0..axes-1 counts as 0 and is reported as MMQ_ERR_INDEX.  The
+ * squares are added in f32.  q_out is f32 or the cache's type (q_dtype),
+ * rounded once, rows ldo values apart (multiples of 4, or of 8); it may be q
+ * itself where it is f32 and ldo == ldq.  Everything else, ragged counts and
+ * reported errors among it, is as in mmq_rope_append.  1 <= axes <= 8, eps >= 0.
+ */
+int mmq_norm_rope_append(const mmq_kv_cache *cache, const int64_t *freq, const int32_t *axis, int rot, float magnitude,
+                         int interleaved, const float *q_norm, const float *k_norm, float eps, const float *q, int64_t ldq,
+                         const float *k, int64_t ldk, const float *v, int64_t ldv, const int32_t *pos, int axes,
+                         const int32_t *new_len, void *q_out, int64_t ldo, int q_dtype, int q_heads, int new_tokens,
+                         mmq_stream_t stream);
+
+/*
+ * Attention of any number of new tokens over the cache: prompts, chunks of
+ * them, and single tokens of models whose scores are capped or biased.  q is
+ * of the cache's type, rows [seqs*new_tokens][q_heads][dim], ldq values apart
+ * (a multiple of 8); q head j reads key-value head j / (q_heads/heads).  Row t
+ * < new_len[b] (NULL: new_tokens) of sequence b stands at slot i = len[b] -
+ * new_len[b] + t and sees the slots lo <= j < hi,
+ *     hi = i + 1, or prefix[b] where that is more (limited to len[b]): the
+ *          first prefix[b] slots see one another whole (NULL: none do);
+ *     lo = max(0, i - window + 1) (window 0: 0), or first[row] where that is
+ *          more (int32 [seqs*new_tokens]: where the row's document begins;
+ *          NULL: 0):
+ *     s = scale q.k;  cap > 0: s = cap tanh(s / cap);
+ *     slopes (f32 [q_heads], or NULL): s += slopes[head] (j - i);
+ *     p = exp(s - max) / sum,  out = sum p v
+ * out [seqs*new_tokens][q_heads][dim], contiguous, not q, is f32 or of the
+ * cache's type.  A row that sees nothing, or with t >= new_len[b], gets 0.  What
+ * a row does not see has no influence on it, whatever it holds (NaN or Inf
+ * included); a row that sees a V entry which is not finite, or a score that is
+ * NaN or +Inf, is not finite.  Scores, maxima and sums are f32; p enters the
+ * tensor core rounded to the cache's type (11 or 8 bits), and an f32 `out` is
+ * not rounded besides.  Results do not depend on timing.
+ * new_tokens >= 1, q_heads a multiple (1 .. 128) of heads, scale finite,
+ * 0 <= cap <= 1024, window >= 0.  A len outside 0..cols*page_size counts as 0, a
+ * new_len outside 0..new_tokens is limited to it, one above len counts as 0;
+ * all are reported as MMQ_ERR_INDEX.  Sequences may share pages.  Refused too
+ * (MMQ_ERR_SHAPE, by both calls) are more than 2^31-1 tiles: cols*page_size /
+ * 128 (64 for heads above 128) for each key-value head and 128 rows of it.
+ * `work` holds the floats that mmq_prefill_sizes says (at most some 80 MB).
+ * Calls that share it must be ordered (one stream).
+ */
+int mmq_prefill_sizes(const mmq_kv_cache *cache, int q_heads, int new_tokens, int64_t *work_floats);
+int mmq_attn_prefill(const mmq_kv_cache *cache, const void *q, int64_t ldq, const int32_t *new_len, const int32_t *prefix,
+                     const int32_t *first, const float *slopes, void *out, int out_dtype, int q_heads, int new_tokens,
+                     float scale, float cap, int window, float *work, mmq_stream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens.  The new_len[b] (NULL: new_tokens)
+ * last entries of a sequence are the tree's nodes; row t sees every slot
+ * before them from first[row] on (NULL: all), and of the nodes those whose bit
+ * is set in tree[b*new_tokens + t] (bit j: node j; its own bit too, if it is
+ * to see itself) and that lie at or after first[row].  Bits past the sequence's
+ * nodes are ignored.  Everything else is as in mmq_attn_prefill, `work` among
+ * it (mmq_prefill_sizes).  new_tokens <= 64.
+ */
+int mmq_attn_tree(const mmq_kv_cache *cache, const void *q, int64_t ldq, const uint64_t *tree, const int32_t *new_len,
+                  const int32_t *first, void *out, int out_dtype, int q_heads, int new_tokens, float scale, float cap,
+                  float *work, mmq_stream_t stream);
+
+/*
+ * What stays of a tree: of the last n = new_len[b] (NULL: nodes) entries of
+ * sequence b, entry keep[b*width + i] moves to place i of them, for i <
+ * count[b] (NULL: width), in every head, with its weight and position where
+ * the cache has them.  keep is ascending; an index that is not, or not below n,
+ * leaves its place as it was and is reported as MMQ_ERR_INDEX, as are a count
+ * outside 0..width and a new_len outside 0..nodes, which are limited to that.
+ * cache->len is not changed: the caller lowers it by n - count[b] once all
+ * layers are done.  The pages of the last n entries must not be shared.
+ * 0 <= width <= nodes <= 64; keep int32 [seqs][width].
+ */
+int mmq_kv_keep(const mmq_kv_cache *cache, const int32_t *keep, const int32_t *count, const int32_t *new_len, int width,
+                int nodes, mmq_stream_t stream);
+
+/*
  * Eviction: every sequence with more than `budget` entries is cut down to
  * `budget` for each head by itself.  Entries with pos >= keep_from[b] rank
  * first, the others by `weight`; the first `budget` stay, ties going to the
@@ -586,14 +674,14 @@ int mmq_probe_tensor_peak(int kind, double *tmacs, mmq_stream_t stream);
  * Waits for `stream`, then reports and clears a device status word of the
  * library for the current device: MMQ_OK, MMQ_ERR_TIMEOUT (a kernel's pipeline
  * wait ran past its limit; the kernel stopped early and its output is
- * invalid), MMQ_ERR_INDEX (a decode-side operator read an index that is out
- * of range) or MMQ_ERR_CUDA (the stream reported a CUDA error).  If
+ * invalid), MMQ_ERR_INDEX (an operator around the cache read an index that is
+ * out of range) or MMQ_ERR_CUDA (the stream reported a CUDA error).  If
  * `detail` is non-NULL it receives 4 ints: code, kernel id, site (a wait, or
- * for MMQ_ERR_INDEX 1 = length, 2 = page id, 3 = count, 4 = token),
- * linear block index of the first failure.
- * The products and the decode-side operators have a word each, and a call
- * reports one, the products' first: where both hold an error, the next call
- * reports the other, so call until MMQ_OK to have all.
+ * for MMQ_ERR_INDEX 1 = length, 2 = page id, 3 = count, 4 = token, 5 = axis,
+ * 6 = node), linear block index of the first failure.
+ * The products, the decode-side operators, and those for prompts and trees have
+ * a word each, and a call reports one, in this order: where several hold an
+ * error, the next call reports the next, so call until MMQ_OK to have all.
  */
 int mmq_check_status(mmq_stream_t stream, int *detail);
 

@@ -57,6 +57,12 @@ SIGNATURES = {
     "mmq_evict_sizes": (_I, [_P, _I, _P]),
     "mmq_kv_evict": (_I, [_P, _I, _P, _P, _P, _P, _P]),
     "mmq_spec_verify": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
+    "mmq_norm_rope_append": (_I, [_P, _P, _P, _I, ctypes.c_float, _I, _P, _P, ctypes.c_float, _P, _I64, _P, _I64, _P, _I64, _P, _I, _P, _P, _I64,
+                                  _I, _I, _I, _P]),
+    "mmq_prefill_sizes": (_I, [_P, _I, _I, _P]),
+    "mmq_attn_prefill": (_I, [_P, _P, _I64, _P, _P, _P, _P, _P, _I, _I, _I, ctypes.c_float, ctypes.c_float, _I, _P, _P]),
+    "mmq_attn_tree": (_I, [_P, _P, _I64, _P, _P, _P, _P, _I, _I, _I, ctypes.c_float, ctypes.c_float, _P, _P]),
+    "mmq_kv_keep": (_I, [_P, _P, _P, _P, _I, _I, _P]),
     "mmq_check_status": (_I, [_P, _P]),
     "mmq_last_failure_info": (_I, [_P]),
     "mmq_debug_fault_inject": (_I, [_I, _I]),

@@ -14,8 +14,8 @@ namespace mmq {
 namespace {
 
 // kernel ids and sites in the status word
-enum { KID_ROPE = 32, KID_ATTN = 33, KID_EVICT = 34, KID_VERIFY = 35 };
-enum { SITE_LEN = 1, SITE_PAGE = 2, SITE_COUNT = 3, SITE_TOKEN = 4 };
+enum { KID_ROPE = 32, KID_ATTN = 33, KID_EVICT = 34, KID_VERIFY = 35, KID_PREFILL = 36, KID_NORM = 37, KID_KEEP = 38 };
+enum { SITE_LEN = 1, SITE_PAGE = 2, SITE_COUNT = 3, SITE_TOKEN = 4, SITE_AXIS = 5, SITE_NODE = 6 };
 
 // Division of 0 <= n < 2^31 by a d >= 1 that is fixed for a launch: a high
 // product, an add and a shift (round-up method of Granlund and Montgomery).
@@ -48,6 +48,20 @@ inline int check_cache(const mmq_kv_cache *c)
         ((c->k_page | c->k_head | c->k_slot | c->v_page | c->v_head | c->v_slot) & 7))
         return MMQ_ERR_ALIGN;
     return MMQ_OK;
+}
+
+// streaming multiprocessors of the current device, looked up once per device
+int sm_count()
+{
+    static int sms[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+    if (sms[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 152;
+        sms[dev] = n;
+    }
+    return sms[dev];
 }
 
 // Whether this process has launched a kernel of this unit (or captured one): before that its status word need not be

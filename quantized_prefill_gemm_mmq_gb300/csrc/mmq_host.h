@@ -21,6 +21,8 @@ int launch_status();
 // Reads and clears the status word of the decode-side operators' translation
 // unit: eight ints as the GEMM unit's own.  MMQ_OK or MMQ_ERR_CUDA.
 int take_serve_status(int (&h)[8]);
+// The same of the unit with the operators for prompts and trees of drafts.
+int take_prompt_status(int (&h)[8]);
 
 // 2-D tiled tensor map over a row-major array: `inner` elements per row of
 // `elem_bytes` each, `rows` rows, `row_stride_bytes` apart; box of

@@ -1,0 +1,1000 @@
+// mmq_prefill.cuh -- attention of any number of new tokens over the paged cache
+// (mmq_attn_prefill), and of a tree of drafted tokens (mmq_attn_tree).
+//
+// Row i of a sequence (its slot) sees the slots lo <= j < hi, or for a tree all
+// slots before the nodes and the nodes of its 64-bit word:
+//     s = scale q.k;  s = cap tanh(s / cap);  s += slope (j - i)
+//     p = exp(s - m),  out = sum p v / sum p
+// in one pass over the entries with a running maximum m.  m is only raised where
+// a tile's largest score lies more than 8 powers of two above it, so that the
+// sums so far are multiplied again in few tiles.
+//
+// Work.  The `group` query heads that share a key-value head are rows beside the
+// tokens: row r is token r / group and head r % group.  A unit is 128 or 256
+// rows of one sequence and head.  K and V tiles are gathered through the page
+// table into a ring in shared memory, 128-byte swizzled; S = Q K^T and O += P V
+// run on the tensor core (tcgen05, accumulators in tensor memory), one thread
+// issuing; a warpgroup per 128 rows reads S (one row per thread), writes P over
+// it in the cache's type and keeps m and the sum in f32.  V is used as it lies:
+// its operand is the transposed form of the same swizzle.  With 256 rows the two
+// halves take turns, so that the tensor core works on one while the other's
+// exponentials are computed, and one K and V tile serves both; with up to 128
+// rows S has two buffers instead.
+//
+// Where units are many, every CTA takes one, the longest first.  Otherwise all
+// tiles of all units are numbered in a row and every CTA takes an equal part;
+// units that are cut leave (max, sum, sum p v) in the workspace, and a second
+// launch joins them in order.
+#pragma once
+
+#include <type_traits>
+
+namespace mmq {
+namespace {
+
+namespace pre {
+constexpr int LOADERS = 2;            // warps
+constexpr int LAG = 2;                // copies a loader has under way before it waits for the oldest
+constexpr int MAX_SLOTS = 12;
+constexpr uint32_t SMEM = 232448 - 1024;            // dynamic, with slack for alignment
+
+enum { W_Q = 1, W_K, W_V, W_P, W_S, W_EMPTY, W_QEMPTY, W_PV, W_DRAIN };     // sites of waits
+
+template <typename T>
+constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+// p carries 2^kLift: f16 keeps 11 bits down to 2^-21 of the row's largest, and 2^(kLift + 8) still fits
+template <typename T>
+constexpr float kLift = kBf<T> ? 0.f : 7.f;
+constexpr float kLazy = 8.f;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t size)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// 2^x to two ulp; 0 for -inf and where the result is below the normal range
+__device__ __forceinline__ float pow2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// kind::f16 descriptor: f16 or bf16 operands, f32 sums, A K-major; B K-major or (mn) with its N values contiguous
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t idesc(int n, bool mn)
+{
+    return (1u << 4) | ((kBf<T> ? 1u : 0u) << 7) | ((kBf<T> ? 1u : 0u) << 10) | ((mn ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Operand whose N values lie contiguous, 64 to a 128-byte swizzled row of one k: eight rows are an atom of 1024 bytes,
+// the next eight k follow it, the next 64 values of N are `chunk` bytes on.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t chunk)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((chunk >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+}  // namespace pre
+
+struct PrefillParams {
+    mmq_kv_cache c;
+    const void *q;
+    const int32_t *new_len, *prefix, *first;
+    const uint64_t *tree;
+    const float *slopes;
+    void *out;
+    int64_t ldq;
+    float scale_log2;          // scale * log2(e)
+    float cap_in, cap_out;     // 2 log2(e) scale / cap, cap log2(e); cap_out 0: no cap
+    int out_f32, window;
+    int new_tokens, group, q_heads;
+    int rows, row_tiles;       // rows per sequence and key-value head, units of them
+    int whole;                 // one unit per CTA
+    int part_rows;             // rows of a part
+    int chunks, ksteps;        // 64-value pieces and 16-value steps of a head
+    int slots;                 // of the ring
+    float *part;               // [2*grid][part_rows][dim], then [2*grid][part_rows] (max, sum), then [grid] int2 (unit, last CTA)
+    float2 *part_ml;
+    int2 *joins;
+    FastDiv page_div, group_div;
+};
+
+// What a unit's rows see.
+struct PrefillRow {
+    int lo, hi;
+};
+
+struct PrefillUnit {
+    int b, h, rt;
+    int len, n, ctx, prefix;   // ctx: entries before the new ones; prefix 0 for none
+    int t0, t1;                // tiles
+    int max_lo, min_hi;        // every live row sees max_lo <= j < min_hi
+};
+
+__device__ __forceinline__ PrefillRow prefill_row(const PrefillParams &p, const PrefillUnit &u, int t, bool with_first)
+{
+    PrefillRow r;
+    const int i = u.ctx + t;
+    r.hi = p.tree ? u.len : max(i + 1, u.prefix);
+    r.lo = p.window > 0 ? max(0, i - p.window + 1) : 0;
+    if (with_first && p.first) r.lo = max(r.lo, *(p.first + (int64_t)u.b * p.new_tokens + t));
+    return r;
+}
+
+// Lengths and counts of sequence b.
+__device__ __forceinline__ void prefill_sequence(const PrefillParams &p, PrefillUnit &u)
+{
+    u.len = cache_len(p.c, u.b, KID_PREFILL);
+    u.n = new_count(p.new_len, u.b, p.new_tokens, KID_PREFILL);
+    if (u.n > u.len) {                            // more new tokens than entries: the first of them are not there
+        record_error(MMQ_ERR_INDEX, KID_PREFILL, SITE_LEN);
+        u.n = 0;
+    }
+    u.ctx = u.len - u.n;
+    u.prefix = p.prefix ? min(max(*(p.prefix + u.b), 0), u.len) : 0;
+}
+
+// Tiles of unit (b, rt) as far as lengths, window and prefix say: the same for every head, and without reading `first`.
+template <int RT, int TN>
+__device__ __forceinline__ int2 prefill_span(const PrefillParams &p, const PrefillUnit &u)
+{
+    const int ta = p.group_div.of(u.rt * RT), tb = min(p.group_div.of(min(p.rows, (u.rt + 1) * RT) - 1), u.n - 1);
+    if (ta > tb) return make_int2(0, 0);
+    const int lo = prefill_row(p, u, ta, false).lo, hi = prefill_row(p, u, tb, false).hi;
+    return lo < hi ? make_int2(lo / TN, (hi + TN - 1) / TN) : make_int2(0, 0);
+}
+
+// The unit's tiles within [t0, t1), and what all of its rows see; by a whole warp.
+template <int RT, int TN>
+__device__ __forceinline__ void prefill_bounds(const PrefillParams &p, PrefillUnit &u)
+{
+    const int ta = p.group_div.of(u.rt * RT), tb = min(p.group_div.of(min(p.rows, (u.rt + 1) * RT) - 1), u.n - 1);
+    int lo = 0x7fffffff;
+    u.max_lo = 0;
+    u.min_hi = 0x7fffffff;
+    if (ta > tb) {
+        u.t0 = u.t1 = 0;
+        return;
+    }
+    if (p.first) {
+        for (int t = ta + (int)(threadIdx.x & 31); t <= tb; t += 32) {
+            const PrefillRow r = prefill_row(p, u, t, true);
+            lo = min(lo, r.lo);
+            u.max_lo = max(u.max_lo, r.lo);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        u.max_lo = __reduce_max_sync(0xffffffffu, u.max_lo);
+    } else {
+        lo = prefill_row(p, u, ta, false).lo;
+        u.max_lo = prefill_row(p, u, tb, false).lo;
+    }
+    const int hi = prefill_row(p, u, tb, false).hi;
+    u.min_hi = p.tree ? u.ctx : prefill_row(p, u, ta, false).hi;
+    u.t0 = max(u.t0, lo / TN);
+    u.t1 = min(u.t1, (hi + TN - 1) / TN);
+    if (lo >= hi || u.t0 >= u.t1) u.t0 = u.t1 = 0;
+}
+
+// Runs of tiles that a CTA takes, one unit (or part of one) after the other.  Every warp walks them by itself.  Units are
+// numbered (sequence, rows, head): the heads of one (sequence, rows) pair have the same span of tiles.
+template <int RT, int TN>
+struct PrefillWalk {
+    const PrefillParams &p;
+    PrefillUnit u;
+    int left;                  // tiles still to come
+    int at;                    // tile within the unit's span where the next run starts
+    int2 span;
+    bool begins, ends;         // the run has the unit's first, last tile
+    int total, grid;           // split: tiles of all units, CTAs that have some
+    int place;                 // split: tiles of all units up to the run's end
+    int rest;                  // tiles of the unit after the run
+
+    __device__ __forceinline__ explicit PrefillWalk(const PrefillParams &q) : p(q) {}
+    __device__ __forceinline__ static int count(int2 s) { return max(1, s.y - s.x); }        // an empty unit still has outputs
+
+    __device__ __forceinline__ void start()
+    {
+        at = place = 0;
+        if (p.whole) {
+            const int per = p.c.seqs * p.c.heads;
+            const int back = (int)blockIdx.x / per, bh = (int)blockIdx.x - back * per;
+            u.rt = p.row_tiles - 1 - back;
+            u.b = bh / p.c.heads;
+            u.h = bh - u.b * p.c.heads;
+            prefill_sequence(p, u);
+            span = prefill_span<RT, TN>(p, u);
+            left = count(span);
+            return;
+        }
+        const int lane = threadIdx.x & 31, pairs = p.c.seqs * p.row_tiles;
+        auto tiles_of = [&](int i) {
+            if (i >= pairs) return 0;
+            PrefillUnit w;
+            w.b = i / p.row_tiles;
+            w.rt = i - w.b * p.row_tiles;
+            prefill_sequence(p, w);
+            return count(prefill_span<RT, TN>(p, w));
+        };
+        int W = 0;
+        for (int i = lane; i < pairs; i += 32) W += tiles_of(i);
+        total = W = __reduce_add_sync(0xffffffffu, W) * p.c.heads;
+        grid = min(W, (int)gridDim.x);
+        left = 0;
+        if ((int)blockIdx.x >= grid) return;
+        place = (int)((long long)W * blockIdx.x / grid);
+        left = (int)((long long)W * (blockIdx.x + 1) / grid) - place;
+        int before = 0;                                       // tiles before pair i0
+        for (int i0 = 0;; i0 += 32) {
+            const int mine = tiles_of(i0 + lane);
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, before + upto * p.c.heads > place);
+            if (past) {
+                const int f = __ffs(past) - 1, each = __shfl_sync(0xffffffffu, mine, f);
+                const int rem = place - before - (__shfl_sync(0xffffffffu, upto, f) - each) * p.c.heads;
+                u.b = (i0 + f) / p.row_tiles;
+                u.rt = i0 + f - u.b * p.row_tiles;
+                u.h = rem / each;
+                at = rem - u.h * each;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31) * p.c.heads;
+        }
+        prefill_sequence(p, u);
+        span = prefill_span<RT, TN>(p, u);
+    }
+
+    // The next run, false when there is none.
+    __device__ __forceinline__ bool next(bool first)
+    {
+        if (left <= 0) return false;
+        if (!first) {
+            at = 0;
+            if (++u.h == p.c.heads) {
+                u.h = 0;
+                if (++u.rt == p.row_tiles) {
+                    u.rt = 0;
+                    ++u.b;
+                    prefill_sequence(p, u);
+                }
+                span = prefill_span<RT, TN>(p, u);
+            }
+        }
+        const int all = count(span), take = min(left, all - at);
+        begins = at == 0;
+        ends = at + take == all;
+        left -= take;
+        place += take;
+        rest = all - at - take;
+        u.t0 = span.x + at;
+        u.t1 = min(span.y, span.x + at + take);
+        prefill_bounds<RT, TN>(p, u);
+        return true;
+    }
+};
+
+template <typename T, int NQ, int TN>
+struct PrefillShape {
+    static constexpr int RT = 128 * NQ;
+    static constexpr int kThreads = (4 * NQ + 1 + pre::LOADERS) * 32;
+    static constexpr int kBuf = 2;                             // S buffers: one per half, or two for the only half
+    static constexpr int kO = kBuf * TN;                       // tensor-memory column of the sums
+    static constexpr int kOPitch = (512 - kO) / NQ;
+    static constexpr int kMaxDim = kOPitch < 256 ? kOPitch / 64 * 64 : 256;
+};
+
+template <typename T, int NQ, int TN>
+__global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p)
+{
+    using namespace pre;
+    using S = PrefillShape<T, NQ, TN>;
+    constexpr int RT = S::RT, SOFT = 4 * NQ;                   // softmax warps; then the issuing warp, then the loaders
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t s_bar[3 + 2 * MAX_SLOTS + 3 * 2];
+    __shared__ uint32_t s_tmem, s_abort;
+    __shared__ uint32_t s_bad[MAX_SLOTS][LOADERS][TN / 32];    // entries of a V tile that were not finite and are taken as 0
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile uint32_t *abort = &s_abort;
+
+    const uint32_t q_bytes = (uint32_t)p.chunks * (128 * 128), slot_bytes = (uint32_t)p.chunks * (TN * 128);
+    const uint32_t ring = base + NQ * q_bytes;
+    const uint32_t bar0 = smem_u32(s_bar);
+    const uint32_t b_qfull = bar0, b_qempty = bar0 + 8, b_drain = bar0 + 16;
+    const uint32_t b_full = bar0 + 24, b_empty = b_full + 8 * MAX_SLOTS;
+    const uint32_t b_s = b_empty + 8 * MAX_SLOTS, b_p = b_s + 16, b_pv = b_p + 16;
+
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        mbar_init(b_qfull, LOADERS);
+        mbar_init(b_qempty, 1);
+        mbar_init(b_drain, 1);
+        for (int i = 0; i < MAX_SLOTS; ++i) {
+            mbar_init(b_full + 8 * i, LOADERS);
+            mbar_init(b_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b_s + 8 * i, 1);
+            mbar_init(b_p + 8 * i, 4);
+            mbar_init(b_pv + 8 * i, 1);
+        }
+        fence_mbar_init();
+    }
+    // Tensor memory is taken after the launch before has ended: its blocks may still have to take theirs.
+    pdl_wait();
+    if (warp == SOFT) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
+    if (!p.whole && threadIdx.x == 0) p.joins[blockIdx.x] = make_int2(-1, 0);          // also if a wait runs out
+
+    PrefillWalk<RT, TN> w(p);
+    w.start();
+
+    if (warp < SOFT) {
+        // ------------------------------------------------------------------ softmax: one row per thread
+        const int half = warp >> 2, quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t o_col = tmem + lanes + S::kO + half * S::kOPitch;
+        const int dcols = p.ksteps * 16;
+        const bool general = p.cap_out != 0.f || p.slopes || !(p.scale_log2 > 0.f);
+        const float c = general ? 1.f : p.scale_log2;
+        int g = 0, runs = 0, vslot = 1, vphase = 0;
+        int2 join = make_int2(-1, 0);
+        for (bool first = true; w.next(first); first = false) {
+            const PrefillUnit &u = w.u;
+            const int r = u.rt * RT + half * 128 + quarter * 32 + lane;
+            const int t = p.group_div.of(min(r, p.rows - 1));
+            const bool live = r < p.rows && t < u.n;
+            const int head = u.h * p.group + (min(r, p.rows - 1) - t * p.group);
+            PrefillRow see = {0, 0};
+            if (live) see = prefill_row(p, u, t, true);
+            uint64_t word = 0;
+            if (p.tree && live) {
+                word = p.tree[(int64_t)u.b * p.new_tokens + t];
+                if (u.n < 64) word &= (1ull << u.n) - 1;
+                see.hi = u.ctx;
+            }
+            const bool any = __any_sync(0xffffffffu, live);
+            // what every live row of this warp sees
+            const int max_lo = __reduce_max_sync(0xffffffffu, live ? see.lo : 0);
+            const int min_hi = __reduce_min_sync(0xffffffffu, live ? see.hi : 0x7fffffff);
+            const float slope = p.slopes && live ? p.slopes[head] * 1.44269504088896341f : 0.f;
+            float m = -INFINITY, l = 0.f;
+            bool poison = false;
+
+            for (int tile = u.t0; tile < u.t1; ++tile, ++g) {
+                const int sb = NQ == 2 ? half : g & 1, sph = NQ == 2 ? g & 1 : (g >> 1) & 1;
+                const uint32_t s_col = tmem + lanes + sb * TN;
+                if (!mbar_wait_warp(b_s + 8 * sb, sph, abort, KID_PREFILL, W_S)) goto done;
+                tc_fence_after();
+                if (any) {
+                    uint32_t x[TN];
+#pragma unroll
+                    for (int k = 0; k < TN; k += 32) tmem_ld32(s_col + k, reinterpret_cast<uint32_t(&)[32]>(x[k]));
+#pragma unroll
+                    for (int k = 0; k < TN; k += 32) tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
+                    const int e0 = tile * TN;
+                    if (general) {
+                        const float bias = slope * (float)(e0 - u.ctx - t);
+                        if (p.cap_out != 0.f) {
+                            // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+#pragma unroll
+                            for (int k = 0; k < TN; ++k) {
+                                const float e = pow2(__uint_as_float(x[k]) * p.cap_in);
+                                const float y = fmaf(-2.f * p.cap_out, rcp(1.f + e), p.cap_out);
+                                x[k] = __float_as_uint(y + fmaf(slope, (float)k, bias));
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < TN; ++k)
+                                x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), p.scale_log2, fmaf(slope, (float)k, bias)));
+                        }
+                    }
+                    if (e0 < max_lo || e0 + TN > min_hi) {
+                        uint32_t bits[TN / 32];
+#pragma unroll
+                        for (int k = 0; k < TN / 32; ++k) {
+                            const int a = min(max(see.lo - e0 - 32 * k, 0), 32), z = min(max(see.hi - e0 - 32 * k, 0), 32);
+                            const uint32_t from = a == 32 ? 0u : 0xffffffffu << a, to = z == 32 ? 0xffffffffu : (1u << z) - 1u;
+                            bits[k] = from & to;
+                            if (p.tree) {
+                                const int d = e0 + 32 * k - u.ctx;          // node of the word's first entry
+                                uint32_t nodes = 0;
+                                if (d >= 0 && d < 64) nodes = (uint32_t)(word >> d);
+                                else if (d < 0 && d > -32) nodes = (uint32_t)(word << -d);
+                                bits[k] |= nodes & from;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!(bits[k] >> j & 1u)) x[32 * k + j] = 0xff800000u;
+                        }
+                        // entries of V that are not finite were taken as 0 in this tile: a row that sees one is not finite
+                        if (!mbar_wait_warp(b_full + 8 * vslot, vphase, abort, KID_PREFILL, W_V)) goto done;
+#pragma unroll
+                        for (int k = 0; k < TN / 32; ++k) {
+                            uint32_t bad = 0;
+#pragma unroll
+                            for (int i = 0; i < LOADERS; ++i) bad |= *(volatile uint32_t *)&s_bad[vslot][i][k];
+                            poison |= (bad & bits[k]) != 0;
+                        }
+                    }
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < TN; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(x[k]));
+                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    const bool raise = mx > m && !((mx - m) * c <= kLazy);
+                    if (__any_sync(0xffffffffu, raise)) {
+                        float f = 1.f;
+                        if (raise) {
+                            const bool exact = fabsf(m * c) < 4096.f && fabsf(mx * c) < 4096.f;
+                            f = pow2(exact ? __fmul_rn(m, c) - __fmul_rn(mx, c) : (m - mx) * c);
+                            m = mx;
+                            l *= f;
+                        }
+                        if (tile != u.t0) {
+                            if (NQ == 1) {                     // the last product may still be adding
+                                if (!mbar_wait_warp(b_pv, (g - 1) & 1, abort, KID_PREFILL, W_PV)) goto done;
+                                tc_fence_after();
+                            }
+                            for (int d = 0; d < dcols; d += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(o_col + d, o);
+                                tmem_ld_wait16(o);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_st16(o_col + d, o);
+                            }
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.f : m * c;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float off = kLift<T> - mc;           // m c is rounded once, the same wherever it is used
+                    if (__all_sync(0xffffffffu, fabsf(mc) < 4096.f)) {
+#pragma unroll
+                        for (int k = 0; k < TN; k += 2) {
+                            const float a = pow2(fmaf(__uint_as_float(x[k]), c, off)), b = pow2(fmaf(__uint_as_float(x[k + 1]), c, off));
+                            sum[k / 2 & 3] += a + b;
+                            x[k / 2] = pack2<T>(a, b);
+                        }
+                    } else {                                   // m is taken off first in rows of such scores, and in these alone
+                        const bool large = !(fabsf(mc) < 4096.f);
+                        const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                        for (int k = 0; k < TN; k += 2) {
+                            const float u0 = __uint_as_float(x[k]), u1 = __uint_as_float(x[k + 1]);
+                            const float a = pow2(large ? fmaf(u0 - ms, c, kLift<T>) : fmaf(u0, c, off));
+                            const float b = pow2(large ? fmaf(u1 - ms, c, kLift<T>) : fmaf(u1, c, off));
+                            sum[k / 2 & 3] += a + b;
+                            x[k / 2] = pack2<T>(a, b);
+                        }
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+                    for (int k = 0; k < TN / 2; k += 32) tmem_st32(s_col + k, reinterpret_cast<uint32_t(&)[32]>(x[k]));
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p + 8 * sb);
+                vslot += 2;
+                if (vslot >= p.slots) {
+                    vslot -= p.slots;
+                    vphase ^= 1;
+                }
+            }
+
+            // the run's sums
+            const bool some = u.t0 < u.t1;
+            if (some) {
+                if (!mbar_wait_warp(b_pv + 8 * half, NQ == 2 ? runs & 1 : (g - 1) & 1, abort, KID_PREFILL, W_PV)) goto done;
+                tc_fence_after();
+                ++runs;
+            }
+            if (poison) l = NAN;
+            if (!live) l = 0.f;
+            const bool whole = w.begins && w.ends;
+            const int64_t row = ((int64_t)u.b * p.new_tokens + t) * p.q_heads + head;
+            const int in_part = half * 128 + quarter * 32 + lane;
+            const int64_t part = 2ll * blockIdx.x + (w.begins ? 1 : 0);
+            const float f = !whole ? 1.f : l > 0.f ? 1.f / l : l;   // a NaN stays one
+            const bool sums = some && !(l == 0.f);
+            if (__any_sync(0xffffffffu, r < p.rows)) {
+                for (int d = 0; d < p.c.dim; d += 16) {
+                    uint32_t o[16];
+                    if (some) {
+                        tmem_ld16(o_col + d, o);
+                        tmem_ld_wait16(o);
+                    }
+                    if (r < p.rows) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = sums ? __float_as_uint(__uint_as_float(o[k]) * f) : 0u;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8) {
+                            if (d + e >= p.c.dim) break;
+                            if (!whole || p.out_f32) {
+                                float *dst = whole ? static_cast<float *>(p.out) + row * p.c.dim + d + e
+                                                   : p.part + (part * p.part_rows + in_part) * p.c.dim + d + e;
+                                *reinterpret_cast<uint4 *>(dst) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                                *reinterpret_cast<uint4 *>(dst + 4) = make_uint4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
+                            } else {
+                                uint32_t h[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    h[k] = pack2<T>(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * p.c.dim + d + e) =
+                                    make_uint4(h[0], h[1], h[2], h[3]);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!whole && r < p.rows) p.part_ml[part * p.part_rows + in_part] = make_float2(m, l);
+            }
+            tc_fence_before();
+            if (w.begins && !w.ends) {                         // the CTA's last run: who has the rest of the unit
+                const long long end = w.place + w.rest;        // the owner of tile x is the last CTA that starts at or before it
+                join = make_int2((u.b * p.row_tiles + u.rt) * p.c.heads + u.h, (int)((end * w.grid - 1) / w.total));
+            }
+        }
+        if (join.x >= 0 && threadIdx.x == 0) p.joins[blockIdx.x] = join;
+    } else if (warp == SOFT) {
+        // ------------------------------------------------------------------ one thread issues the products
+        constexpr uint32_t kIdS = idesc<T>(TN, false);
+        const uint32_t id_o = idesc<T>(p.ksteps * 16, true);
+        int g = 0, runs = 0, slot = 0, phase = 0;              // slot: of the next tile's K
+        auto product_s = [&](int i, int sb, int at) {          // half i, S buffer sb, K in slot `at`
+            const uint32_t a = base + i * q_bytes, b = ring + at * slot_bytes;
+            for (int k = 0; k < p.ksteps; ++k)
+                umma_f16(tmem + sb * TN, sdesc_k_sw128(a + (k >> 2) * (128 * 128) + (k & 3) * 32),
+                         sdesc_k_sw128(b + (k >> 2) * (TN * 128) + (k & 3) * 32), kIdS, k > 0);
+            umma_commit(b_s + 8 * sb);
+        };
+        auto product_o = [&](int i, int sb, int at, bool add) {
+            const uint32_t b = ring + at * slot_bytes;
+#pragma unroll
+            for (int k = 0; k < TN / 16; ++k)
+                umma_f16_ts(tmem + S::kO + i * S::kOPitch, tmem + sb * TN + 8 * k, sdesc_mn_sw128(b + k * 2048, TN * 128), id_o,
+                            add || k > 0);
+        };
+        auto waits = [&](uint32_t bar, int parity, int site) {
+            const bool ok = mbar_wait(bar, (uint32_t)parity, abort, KID_PREFILL, site);
+            tc_fence_after();
+            return ok;
+        };
+        auto run = [&](int nt) {
+            if (!waits(b_qfull, runs & 1, W_Q) || !waits(b_full + 8 * slot, phase, W_K)) return false;
+            for (int i = 0; i < NQ; ++i) product_s(i, NQ == 2 ? i : g & 1, slot);
+            umma_commit(b_empty + 8 * slot);
+            if (nt == 1) umma_commit(b_qempty);
+            for (int j = 0; j < nt; ++j, ++g) {
+                int vs = slot + 1, vp = phase;
+                if (vs >= p.slots) vs = 0, vp ^= 1;
+                int ks = vs + 1, kp = vp;
+                if (ks >= p.slots) ks = 0, kp ^= 1;
+                const bool more = j + 1 < nt;
+                if (NQ == 1 && more) {                         // the next scores, while this tile's are worked on
+                    if (!waits(b_full + 8 * ks, kp, W_K)) return false;
+                    product_s(0, (g + 1) & 1, ks);
+                    umma_commit(b_empty + 8 * ks);
+                    if (j + 2 == nt) umma_commit(b_qempty);
+                }
+                for (int i = 0; i < NQ; ++i) {
+                    const int sb = NQ == 2 ? i : g & 1;
+                    if (!waits(b_p + 8 * sb, NQ == 2 ? g & 1 : (g >> 1) & 1, W_P)) return false;
+                    if (i == 0 && !waits(b_full + 8 * vs, vp, W_V)) return false;
+                    product_o(i, sb, vs, j > 0);
+                    if (i == NQ - 1) umma_commit(b_empty + 8 * vs);
+                    if (NQ == 1 || !more) umma_commit(b_pv + 8 * i);
+                    if (NQ == 2 && more) {
+                        if (i == 0 && !waits(b_full + 8 * ks, kp, W_K)) return false;
+                        product_s(i, sb, ks);
+                        if (i == NQ - 1) {
+                            umma_commit(b_empty + 8 * ks);
+                            if (j + 2 == nt) umma_commit(b_qempty);
+                        }
+                    }
+                }
+                slot = ks;
+                phase = kp;
+            }
+            ++runs;
+            return true;
+        };
+        for (bool first = true; w.next(first); first = false) {
+            const int nt = w.u.t1 - w.u.t0;
+            if (nt <= 0) continue;
+            bool ok = true;
+            if (lane == 0) ok = run(nt);
+            if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+        }
+        if (lane == 0) {                                       // nothing is under way when tensor memory is given back
+            umma_commit(b_drain);
+            uint32_t never = 0;
+            mbar_wait(b_drain, 0, &never, KID_PREFILL, W_DRAIN);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ loaders
+        const int lw = warp - SOFT - 1;
+        const int pieces = p.ksteps * 2;                       // 16-byte pieces of a row, past `dim` zeros
+        const int step_row = 32 / pieces, step_piece = 32 - step_row * pieces;
+        const int row0 = lane / pieces, piece0 = lane - row0 * pieces;
+        constexpr int BATCH = TN / 32 / LOADERS;               // batches of 32 rows per warp and tile
+        struct Pending {
+            uint32_t bar;                                      // 0: nothing to announce
+            int slot;                                          // of a V tile to look through, or -1
+        };
+        Pending queue[LAG];
+#pragma unroll
+        for (int i = 0; i < LAG; ++i) queue[i] = {0u, -1};
+        // 32 rows whose addresses the lanes hold (null: zeros), `pitch` bytes between their 64-value chunks
+        auto copy_rows = [&](const T *at, uint32_t dst, int first_row, uint32_t pitch) {
+            int row = row0, piece = piece0;
+            for (int i = 0; i < pieces; ++i) {
+                const T *src = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, (unsigned long long)at, row));
+                const bool there = src != nullptr && piece * 8 < p.c.dim;
+                const int rr = first_row + row;
+                cp16(dst + (piece >> 3) * pitch + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4),
+                     there ? static_cast<const void *>(src + piece * 8) : p.c.k, there ? 16u : 0u);
+                row += step_row;
+                piece += step_piece;
+                if (piece >= pieces) piece -= pieces, ++row;
+            }
+        };
+        // An entry of V that is not finite, in a tile that some row sees in part only: taken as 0, and noted.
+        auto look_through = [&](int slot) {
+            const uint32_t at = ring + slot * slot_bytes;
+            for (int k = lane; k < TN / 32; k += 32) s_bad[slot][lw][k] = 0;
+            __syncwarp();
+            for (int bt = 0; bt < BATCH; ++bt) {
+                const int first_row = (bt * LOADERS + lw) * 32;
+                int row = row0, piece = piece0;
+                for (int i = 0; i < pieces; ++i) {
+                    const int rr = first_row + row;
+                    const uint32_t a = at + (piece >> 3) * (TN * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4);
+                    uint32_t v[4];
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
+                    constexpr uint32_t e = kBf<T> ? 0x7f80u : 0x7c00u;
+                    bool bad = false;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) bad |= (v[k] & e) == e || (v[k] & (e << 16)) == (e << 16);
+                    if (bad) {
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+                        atomicOr(&s_bad[slot][lw][rr >> 5], 1u << (rr & 31));
+                    }
+                    row += step_row;
+                    piece += step_piece;
+                    if (piece >= pieces) piece -= pieces, ++row;
+                }
+            }
+        };
+        auto announce = [&](const Pending &d) {                // the oldest copies have arrived
+            if (d.bar == 0) return;
+            if (d.slot >= 0) look_through(d.slot);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(d.bar);
+        };
+        auto push = [&](uint32_t bar, int slot) {
+            cp_commit();
+            cp_wait<LAG>();
+            announce(queue[0]);
+#pragma unroll
+            for (int i = 0; i + 1 < LAG; ++i) queue[i] = queue[i + 1];
+            queue[LAG - 1] = {bar, slot};
+        };
+        auto flush = [&]() {
+            cp_wait<0>();
+#pragma unroll
+            for (int i = 0; i < LAG; ++i) {
+                announce(queue[i]);
+                queue[i] = {0u, -1};
+            }
+        };
+        // Before a wait that others may have to end with what is still under way here.
+        auto waits = [&](uint32_t bar, int parity, int site) {
+            if (__shfl_sync(0xffffffffu, mbar_try_wait(bar, (uint32_t)parity) ? 1 : 0, 0)) return true;
+            flush();
+            return mbar_wait_warp(bar, (uint32_t)parity, abort, KID_PREFILL, site);
+        };
+        int runs = 0, slot = 0, phase = 0;
+        auto run = [&](const PrefillUnit &u) {
+            if (!waits(b_qempty, (runs & 1) ^ 1, W_QEMPTY)) return false;
+            for (int bt = lw; bt < RT / 32; bt += LOADERS) {
+                const int r = u.rt * RT + bt * 32 + lane, t = p.group_div.of(min(r, p.rows - 1));
+                const bool live = r < p.rows && t < u.n;
+                const T *at = live ? static_cast<const T *>(p.q) + ((int64_t)u.b * p.new_tokens + t) * p.ldq +
+                                         (int64_t)(u.h * p.group + (r - t * p.group)) * p.c.dim
+                                   : nullptr;
+                copy_rows(at, base + (bt >> 2) * q_bytes, (bt & 3) * 32, 128 * 128);
+            }
+            push(b_qfull, -1);
+            for (int tile = u.t0; tile < u.t1; ++tile) {
+                const T *ka[BATCH], *va[BATCH];
+#pragma unroll
+                for (int bt = 0; bt < BATCH; ++bt) {
+                    const int e = tile * TN + (bt * LOADERS + lw) * 32 + lane;
+                    ka[bt] = va[bt] = nullptr;
+                    if (e < u.len) {
+                        const int col = p.page_div.of(e);
+                        int off = e - col * p.c.page_size;
+                        int64_t pg = cache_page(p.c, u.b, col, KID_PREFILL);
+                        if (pg < 0) pg = off = 0;
+                        ka[bt] = static_cast<const T *>(p.c.k) + pg * p.c.k_page + u.h * p.c.k_head + off * p.c.k_slot;
+                        va[bt] = static_cast<const T *>(p.c.v) + pg * p.c.v_page + u.h * p.c.v_head + off * p.c.v_slot;
+                    }
+                }
+                const bool cut = tile * TN < u.max_lo || (tile + 1) * TN > u.min_hi;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (!waits(b_empty + 8 * slot, phase ^ 1, W_EMPTY)) return false;
+#pragma unroll
+                    for (int bt = 0; bt < BATCH; ++bt)
+                        copy_rows(kv ? va[bt] : ka[bt], ring + slot * slot_bytes, (bt * LOADERS + lw) * 32, TN * 128);
+                    push(b_full + 8 * slot, kv && cut ? slot : -1);
+                    if (++slot == p.slots) slot = 0, phase ^= 1;
+                }
+            }
+            ++runs;
+            return true;
+        };
+        for (bool first = true; w.next(first); first = false)
+            if (w.u.t0 < w.u.t1 && !run(w.u)) break;
+        flush();
+    }
+done:
+    tc_fence_before();
+    __syncthreads();
+    if (warp == SOFT) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of the unit that CTA blockIdx.x starts and does not end: one row per warp.
+template <typename T>
+__global__ void __launch_bounds__(128) prefill_join_kernel(const __grid_constant__ PrefillParams p, int rt_rows)
+{
+    using namespace pre;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int2 join = p.joins[blockIdx.x];
+    if (join.x < 0) return;
+    const int lane = threadIdx.x & 31, n = join.y - (int)blockIdx.x + 1;
+    const int pair = join.x / p.c.heads, h = join.x - pair * p.c.heads, b = pair / p.row_tiles, rt = pair - b * p.row_tiles;
+    const float c = p.cap_out != 0.f || p.slopes || !(p.scale_log2 > 0.f) ? 1.f : p.scale_log2;
+    const int rows = min(rt_rows, p.rows - rt * rt_rows);
+    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 4) {
+        // the part that begins the unit is its CTA's second, the others are their CTAs' first
+        auto at = [&](int i) { return (2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.part_rows + r; };
+        float top = -INFINITY;
+        for (int i = lane; i < n; i += 32) {
+            const float2 ml = p.part_ml[at(i)];
+            if (ml.y > 0.f) top = fmaxf(top, ml.x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float sum = 0.f;
+        float4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            float wt = 0.f;
+            if (i0 + lane < n) {
+                const float2 ml = p.part_ml[at(i0 + lane)];
+                if (ml.y > 0.f) {
+                    const bool exact = fabsf(ml.x * c) < 4096.f && fabsf(top * c) < 4096.f;
+                    wt = pow2(exact ? __fmul_rn(ml.x, c) - __fmul_rn(top, c) : (ml.x - top) * c);
+                }
+                sum += ml.y > 0.f ? wt * ml.y : ml.y;          // 0, or a NaN
+            }
+            const int k = min(32, n - i0);
+#pragma unroll 4
+            for (int i = 0; i < k; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, wt, i);
+                if (wi == 0.f) continue;
+                const float4 *src = reinterpret_cast<const float4 *>(p.part + at(i0 + i) * p.c.dim);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int d = lane + 32 * e;
+                    if (d * 4 >= p.c.dim) continue;
+                    const float4 v = src[d];
+                    acc[e].x = fmaf(wi, v.x, acc[e].x);
+                    acc[e].y = fmaf(wi, v.y, acc[e].y);
+                    acc[e].z = fmaf(wi, v.z, acc[e].z);
+                    acc[e].w = fmaf(wi, v.w, acc[e].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float f = sum > 0.f ? 1.f / sum : sum;           // a row that saw nothing is 0, a NaN stays one
+        const int rr = rt * rt_rows + r, t = p.group_div.of(rr);
+        const int64_t row = ((int64_t)b * p.new_tokens + t) * p.q_heads + h * p.group + (rr - t * p.group);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int d = lane + 32 * e;
+            if (d * 4 >= p.c.dim) continue;
+            const float4 v = make_float4(acc[e].x * f, acc[e].y * f, acc[e].z * f, acc[e].w * f);
+            if (p.out_f32) *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * p.c.dim + 4 * d) = v;
+            else
+                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + row * p.c.dim + 4 * d) =
+                    make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+        }
+    }
+}
+
+namespace pre {
+// How a call is cut up: the same for the sizes and the launch.
+struct Plan {
+    int rows, row_tiles, rt, tn, whole, grid, part_rows, slots, chunks, ksteps;
+    int64_t floats;
+    uint32_t smem;
+};
+
+inline int make_plan(const mmq_kv_cache *c, int q_heads, int new_tokens, Plan &q)
+{
+    if (q_heads < 1 || q_heads > 65535 || q_heads % c->heads || q_heads / c->heads > 128 || new_tokens < 1 ||
+        (int64_t)new_tokens * (q_heads / c->heads) > 0x7fffff00 || (int64_t)c->seqs * new_tokens > 0x7fffffff)
+        return MMQ_ERR_SHAPE;
+    q.rows = new_tokens * (q_heads / c->heads);
+    // 256 rows share a tile of K and V where there are that many and tensor memory holds their sums
+    q.rt = q.rows > 128 && c->dim <= 192 ? 256 : 128;
+    q.tn = c->dim <= 128 ? 128 : 64;
+    q.row_tiles = (q.rows + q.rt - 1) / q.rt;
+    q.chunks = (c->dim + 63) / 64;
+    q.ksteps = (c->dim + 15) / 16;
+    const int64_t units = (int64_t)c->seqs * c->heads * q.row_tiles, cap = (int64_t)c->cols * c->page_size;
+    if (units > 0x7fffffff || units * ((cap + q.tn - 1) / q.tn) > 0x7fffffff) return MMQ_ERR_SHAPE;
+    const int sms = sm_count();
+    q.whole = q.row_tiles > 1 && units >= 3ll * sms;
+    q.grid = q.whole ? (int)units : sms;
+    q.part_rows = q.rows < q.rt ? q.rows : q.rt;
+    q.floats = q.whole ? 4 : 2ll * sms * q.part_rows * (c->dim + 2) + 2ll * sms;
+    const uint32_t slot = (uint32_t)q.chunks * q.tn * 128, queries = (uint32_t)q.chunks * q.rt * 128;
+    q.slots = (int)((SMEM - 1024 - queries) / slot);
+    if (q.slots > MAX_SLOTS) q.slots = MAX_SLOTS;
+    q.smem = queries + q.slots * slot + 1024;
+    return MMQ_OK;
+}
+
+template <typename T, int NQ, int TN>
+int launch(const PrefillParams &p, const Plan &q, cudaStream_t stream)
+{
+    static std::atomic<unsigned long long> set{0};             // devices whose limit is raised
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return launch_status();
+    if (!(set.load(std::memory_order_relaxed) >> dev & 1)) {
+        if (cudaFuncSetAttribute(prefill_kernel<T, NQ, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM) != cudaSuccess)
+            return launch_status();
+        set.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    int rc = launch_pdl(prefill_kernel<T, NQ, TN>, dim3((unsigned)q.grid), PrefillShape<T, NQ, TN>::kThreads, q.smem, stream, 0, p);
+    if (rc != MMQ_OK || q.whole) return rc;
+    const int by = (q.part_rows + 3) / 4;
+    return launch_pdl(prefill_join_kernel<T>, dim3((unsigned)q.grid, (unsigned)(by < 16 ? by : 16)), 128, 0, stream, 0, p, q.rt);
+}
+
+template <typename T>
+int launch_any(const PrefillParams &p, const Plan &q, cudaStream_t stream)
+{
+    if (q.rt == 256) return q.tn == 128 ? launch<T, 2, 128>(p, q, stream) : launch<T, 2, 64>(p, q, stream);
+    return q.tn == 128 ? launch<T, 1, 128>(p, q, stream) : launch<T, 1, 64>(p, q, stream);
+}
+
+struct Call {
+    const void *q;
+    int64_t ldq;
+    const int32_t *new_len, *prefix, *first;
+    const uint64_t *tree;
+    const float *slopes;
+    void *out;
+    int out_dtype, q_heads, new_tokens;
+    float scale, cap;
+    int window;
+    float *work;
+};
+
+int attend(const mmq_kv_cache *cache, const Call &a, mmq_stream_t stream)
+{
+    int rc = check_cache(cache);
+    if (rc != MMQ_OK) return rc;
+    Plan q;
+    if ((rc = make_plan(cache, a.q_heads, a.new_tokens, q)) != MMQ_OK) return rc;
+    if ((a.out_dtype != MMQ_F32 && a.out_dtype != cache->dtype) || a.ldq < (int64_t)a.q_heads * cache->dim || !isfinite(a.scale) ||
+        !(a.cap >= 0.f && a.cap <= 1024.f) || a.window < 0 || (a.q && a.q == a.out))
+        return MMQ_ERR_SHAPE;
+    if (cache->seqs == 0) return MMQ_OK;
+    if (!a.q || !a.out || !a.work) return MMQ_ERR_NULL;
+    if (!aligned16(a.q) || !aligned16(a.out) || !aligned16(a.work) || (a.ldq & 7)) return MMQ_ERR_ALIGN;
+    if ((rc = check_arch()) != MMQ_OK) return rc;
+    PrefillParams p = {};
+    p.c = *cache;
+    p.q = a.q;
+    p.new_len = a.new_len;
+    p.prefix = a.prefix;
+    p.first = a.first;
+    p.tree = a.tree;
+    p.slopes = a.slopes;
+    p.out = a.out;
+    p.ldq = a.ldq;
+    p.scale_log2 = a.scale * 1.44269504088896341f;
+    if (a.cap > 0.f) {
+        p.cap_in = 2.f * 1.44269504088896341f * (a.scale / a.cap);
+        p.cap_out = a.cap * 1.44269504088896341f;
+    }
+    p.out_f32 = a.out_dtype == MMQ_F32;
+    p.window = a.window;
+    p.new_tokens = a.new_tokens;
+    p.group = a.q_heads / cache->heads;
+    p.q_heads = a.q_heads;
+    p.rows = q.rows;
+    p.row_tiles = q.row_tiles;
+    p.whole = q.whole;
+    p.part_rows = q.part_rows;
+    p.chunks = q.chunks;
+    p.ksteps = q.ksteps;
+    p.slots = q.slots;
+    p.part = a.work;
+    p.part_ml = reinterpret_cast<float2 *>(a.work + 2ll * q.grid * q.part_rows * cache->dim);
+    p.joins = reinterpret_cast<int2 *>(p.part_ml + 2ll * q.grid * q.part_rows);
+    p.page_div = FastDiv(cache->page_size);
+    p.group_div = FastDiv(p.group);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return cache->dtype == MMQ_F16 ? launch_any<__half>(p, q, st) : launch_any<__nv_bfloat16>(p, q, st);
+}
+}  // namespace pre
+
+}  // namespace
+}  // namespace mmq
+
+extern "C" int mmq_prefill_sizes(const mmq_kv_cache *cache, int q_heads, int new_tokens, int64_t *work_floats)
+{
+    using namespace mmq;
+    const int rc = check_cache(cache);
+    if (rc != MMQ_OK) return rc;
+    if (!work_floats) return MMQ_ERR_NULL;
+    pre::Plan q;
+    const int st = pre::make_plan(cache, q_heads, new_tokens, q);
+    if (st != MMQ_OK) return st;
+    *work_floats = q.floats;
+    return MMQ_OK;
+}
+
+extern "C" int mmq_attn_prefill(const mmq_kv_cache *cache, const void *q, int64_t ldq, const int32_t *new_len, const int32_t *prefix,
+                                const int32_t *first, const float *slopes, void *out, int out_dtype, int q_heads, int new_tokens,
+                                float scale, float cap, int window, float *work, mmq_stream_t stream)
+{
+    return mmq::pre::attend(cache, {q, ldq, new_len, prefix, first, nullptr, slopes, out, out_dtype, q_heads, new_tokens, scale, cap, window, work},
+                            stream);
+}
+
+extern "C" int mmq_attn_tree(const mmq_kv_cache *cache, const void *q, int64_t ldq, const uint64_t *tree, const int32_t *new_len,
+                             const int32_t *first, void *out, int out_dtype, int q_heads, int new_tokens, float scale, float cap,
+                             float *work, mmq_stream_t stream)
+{
+    using namespace mmq;
+    const int rc = check_cache(cache);
+    if (rc != MMQ_OK) return rc;
+    if (new_tokens > 64) return MMQ_ERR_SHAPE;
+    if (cache->seqs > 0 && !tree) return MMQ_ERR_NULL;
+    return pre::attend(cache, {q, ldq, new_len, nullptr, first, tree, nullptr, out, out_dtype, q_heads, new_tokens, scale, cap, 0, work}, stream);
+}

@@ -10,24 +10,6 @@
 
 namespace mmq {
 
-namespace {
-
-// streaming multiprocessors of the current device, looked up once per device
-int sm_count()
-{
-    static int sms[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-    if (sms[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 152;
-        sms[dev] = n;
-    }
-    return sms[dev];
-}
-
-}  // namespace
-
 int take_serve_status(int (&h)[8])
 {
     if (!g_launched.load(std::memory_order_relaxed)) return MMQ_OK;        // h as the caller left it: zeros

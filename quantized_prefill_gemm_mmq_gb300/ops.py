@@ -339,6 +339,8 @@ def debug_subdots(fmt: str, w: torch.Tensor, xh: torch.Tensor, O: int) -> torch.
 CACHE_DTYPES = {torch.float16: 0, torch.bfloat16: 1}        # MMQ_F16, MMQ_BF16
 PROB_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 ATTN_NEW_MAX = 16         # mmq_attn_decode
+TREE_MAX = 64             # mmq_attn_tree, mmq_kv_keep
+ROPE_AXES_MAX = 8         # mmq_norm_rope_append
 
 
 def _need(t, name, dtype, shape, index):
@@ -417,14 +419,20 @@ _current = torch.cuda.current_device
 
 
 class RopeTable:
-    """Rotation of mmq_rope_append: freq int64 [rot/2] (turns per position as 64-bit
-    fractions), rot values of each head rotated, magnitude times the result."""
+    """Rotation of mmq_rope_append and mmq_norm_rope_append: freq int64 [rot/2] (turns per
+    position as 64-bit fractions), rot values of each head rotated, magnitude times the
+    result; axis int32 [rot/2], which of `axes` positions each pair turns by (None: one axis)."""
 
-    def __init__(self, freq: torch.Tensor, magnitude: float = 1.0):
-        _need_cuda(freq)
+    def __init__(self, freq: torch.Tensor, magnitude: float = 1.0, axis: torch.Tensor | None = None, axes: int = 1):
+        _need_cuda(freq, axis)
         _need(freq, "freq", torch.int64, (freq.numel(),), freq.get_device())
+        if axis is not None:
+            _need(axis, "axis", torch.int32, (freq.numel(),), freq.get_device())
+        elif axes != 1:
+            raise ValueError("several axes need `axis`")
         self.freq, self.rot, self.magnitude = freq, 2 * freq.numel(), float(magnitude)
-        self.index, self.ptr = freq.get_device(), freq.data_ptr()
+        self.axis, self.axes = axis, axes
+        self.index, self.ptr, self.axis_ptr = freq.get_device(), freq.data_ptr(), None if axis is None else axis.data_ptr()
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, context: int = 4096,
@@ -462,17 +470,49 @@ def rope_fixed(inv: list[float]) -> list[int]:
     return [((int(f / (2 * math.pi) * 2.0 ** 64) + (1 << 63)) % (1 << 64)) - (1 << 63) for f in inv]
 
 
+def rope_axes(rot: int, sections: list[int], alternate: bool = False) -> list[int]:
+    """Which axis each of the rot/2 pairs turns by: sections[a] pairs of axis a, one block after
+    the other; or alternating (pair i to axis i % axes) as long as that axis has pairs left,
+    the rest to axis 0."""
+    if len(sections) < 1 or len(sections) > ROPE_AXES_MAX or min(sections) < 0 or sum(sections) != rot // 2:
+        raise ValueError(f"sections must be 1 to {ROPE_AXES_MAX} counts that add up to rot/2")
+    if not alternate:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    n = len(sections)
+    return [i % n if i // n < sections[i % n] else 0 for i in range(rot // 2)]
+
+
 def rope_table(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, context: int = 4096,
-               fast: float = 32.0, slow: float = 1.0, device=None) -> RopeTable:
-    """The rotation table of rope_frequencies, on the device."""
+               fast: float = 32.0, slow: float = 1.0, device=None, sections: list[int] | None = None,
+               alternate: bool = False) -> RopeTable:
+    """The rotation table of rope_frequencies, on the device; with `sections`, for positions with
+    several axes (rope_axes)."""
     inv, magnitude = rope_frequencies(rot, base, scaling, factor, context, fast, slow)
-    return RopeTable(torch.tensor(rope_fixed(inv), dtype=torch.int64).to(device if device is not None else "cuda"), magnitude)
+    dev = device if device is not None else "cuda"
+    axis = None if sections is None else torch.tensor(rope_axes(rot, sections, alternate), dtype=torch.int32).to(dev)
+    return RopeTable(torch.tensor(rope_fixed(inv), dtype=torch.int64).to(dev), magnitude, axis, 1 if sections is None else len(sections))
 
 
-def _rows(t, name, heads, dim, index):
-    """Row stride of f32 [rows][heads][dim], shape checked, whose rows may lie apart."""
-    if t.dtype is not torch.float32 or t.get_device() != index:
-        raise ValueError(f"{name} must be float32 on CUDA device {index}")
+_DTYPE_IDS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _at(t):
+    """Address of a tensor that may be missing."""
+    return None if t is None else t.data_ptr()
+
+
+def _out_dtype(cache, out_dtype, out, default):
+    """Type of an output that is float32 or of the cache's type."""
+    dtype = out_dtype if out_dtype is not None else out.dtype if out is not None else default
+    if dtype is not torch.float32 and dtype is not cache.k.dtype:
+        raise ValueError(f"the output is float32 or {cache.k.dtype}")
+    return dtype
+
+
+def _rows(t, name, heads, dim, index, dtype=torch.float32):
+    """Row stride of [rows][heads][dim] (f32 unless said), shape checked, whose rows may lie apart."""
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be {str(dtype)[6:]} on CUDA device {index}")
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{name}: a row's heads must be contiguous")
@@ -508,8 +548,8 @@ def rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tenso
     _need(pos, "pos", torch.int32, (rows,), index)
     if new is not None:
         _need(new, "new", torch.int32, (cache.seqs,), index)
-    if rope.rot > dim or rope.index != index:
-        raise ValueError("the table rotates more values than a head has, or is on another device")
+    if rope.rot > dim or rope.index != index or rope.axes != 1:
+        raise ValueError("the table rotates more values than a head has, has several axes, or is on another device")
     stream = _raw_stream(index)
     if out is None:
         out, ldo = torch.empty(shape, dtype=torch.float32, device=cache.device), q_heads * dim
@@ -522,6 +562,49 @@ def rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tenso
                                 q_heads, n, stream)
     if st != 0:
         raise MMQError("mmq_rope_append", st)
+    return out
+
+
+def norm_rope_append(cache: KVCache, rope: RopeTable, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+                     q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, eps: float = 1e-6,
+                     interleaved: bool = False, new: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """rope_append with a norm of every q and k head before the rotation (weights q_norm and
+    k_norm float32 [dim]; None: not normed), and positions with several axes.
+
+    pos is int32 [axes][seqs*n] for the table's axes (one axis: [seqs*n] will do); axis 0 goes
+    to cache.pos.  The returned q is float32 or, with out_dtype, of the cache's type, as
+    attn_prefill and attn_tree take it.  `out` may be q where it is float32."""
+    index, dim, heads = cache.index, cache.dim, cache.heads
+    if index != _current():
+        with torch.cuda.device(index):
+            return norm_rope_append(cache, rope, q, k, v, pos, q_norm, k_norm, eps, interleaved, new, out_dtype, out)
+    shape = q.shape
+    rows, q_heads, n = _q_shape(cache, shape)
+    if k.shape != (rows, heads, dim) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{rows}][{heads}][{dim}]")
+    ldq, ldk, ldv = _rows(q, "q", q_heads, dim, index), _rows(k, "k", heads, dim, index), _rows(v, "v", heads, dim, index)
+    _need(pos, "pos", torch.int32, (rows,) if rope.axes == 1 and pos.dim() == 1 else (rope.axes, rows), index)
+    if new is not None:
+        _need(new, "new", torch.int32, (cache.seqs,), index)
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None:
+            _need(t, name, torch.float32, (dim,), index)
+    if rope.rot > dim or rope.index != index:
+        raise ValueError("the table rotates more values than a head has, or is on another device")
+    dtype = _out_dtype(cache, out_dtype, out, torch.float32)
+    stream = _raw_stream(index)
+    if out is None:
+        out, ldo = torch.empty(shape, dtype=dtype, device=cache.device), q_heads * dim
+    else:
+        if out.shape != shape:
+            raise ValueError("out must have q's shape")
+        ldo = _rows(out, "out", q_heads, dim, index, dtype)
+    st = load().mmq_norm_rope_append(cache._ref, rope.ptr, rope.axis_ptr, rope.rot, rope.magnitude, int(interleaved), _at(q_norm), _at(k_norm), eps,
+                                     q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, pos.data_ptr(), rope.axes, _at(new),
+                                     out.data_ptr(), ldo, _DTYPE_IDS[dtype], q_heads, n, stream)
+    if st != 0:
+        raise MMQError("mmq_norm_rope_append", st)
     return out
 
 
@@ -596,6 +679,139 @@ def attn_decode(cache: KVCache, q: torch.Tensor, scale: float | None = None, new
     if st != 0:
         raise MMQError("mmq_attn_decode", st)
     return out
+
+
+def prefill_sizes(cache: KVCache, q_heads: int, new_tokens: int) -> int:
+    """Floats of attn_prefill's and attn_tree's workspace."""
+    nf = ctypes.c_int64(0)
+    with torch.cuda.device(cache.device):
+        st = load().mmq_prefill_sizes(cache._ref, q_heads, new_tokens, ctypes.byref(nf))
+    _check("mmq_prefill_sizes", st)
+    return nf.value
+
+
+def prefill_workspace(cache: KVCache, q_heads: int, new_tokens: int) -> AttnWorkspace:
+    return AttnWorkspace(cache.device, prefill_sizes(cache, q_heads, new_tokens))
+
+
+def _prefill_plan(cache, q, out, out_dtype, workspace):
+    """What attn_prefill and attn_tree share: (q heads, new tokens, row stride, out, workspace)."""
+    index, shape = cache.index, q.shape
+    plan = cache._work.get(("prefill", shape))
+    if plan is None:                                     # what depends on the shape alone
+        rows, q_heads, n = _q_shape(cache, shape)
+        if q_heads % cache.heads:
+            raise ValueError("q_heads must be a multiple of the cache's heads")
+        if n < 1:
+            raise ValueError("at least one new token per sequence")
+        plan = cache._work[("prefill", shape)] = (q_heads, n, prefill_sizes(cache, q_heads, n))
+    q_heads, n, floats = plan
+    ldq = _rows(q, "q", q_heads, cache.dim, index, cache.k.dtype)
+    dtype = _out_dtype(cache, out_dtype, out, cache.k.dtype)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=cache.device)
+    else:
+        _need(out, "out", dtype, shape, index)
+    if workspace is None or not workspace.fits(floats):
+        workspace = AttnWorkspace(cache.device, floats)
+    elif workspace.index != index:
+        raise ValueError(f"workspace must be on CUDA device {index}")
+    return q_heads, n, ldq, out, workspace
+
+
+def attn_prefill(cache: KVCache, q: torch.Tensor, scale: float | None = None, cap: float = 0.0, slopes: torch.Tensor | None = None,
+                 window: int = 0, prefix: torch.Tensor | None = None, first: torch.Tensor | None = None,
+                 new: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                 workspace: AttnWorkspace | None = None) -> torch.Tensor:
+    """Attention of every sequence's newest n tokens, any number of them, over the cache;
+    [seqs*n][q_heads][dim] of the cache's type, or float32 with out_dtype.
+
+    q of the cache's type [seqs*n][q_heads][dim] (norm_rope_append's out_dtype).  Row t of a
+    sequence stands at slot i = lens - n + t (new int32 [seqs] limits the rows as in
+    rope_append; rows past it get 0) and sees the entries up to its own, or up to prefix
+    (int32 [seqs]) where that is more; with `window` the last `window` of them; with first
+    (int32 [seqs*n]) those from that slot on, where the row's document begins.  cap > 0 turns
+    scores into cap tanh(score / cap); slopes (float32 [q_heads]) then adds slope * (j - i).
+    scale defaults to dim^-0.5.  Without `workspace` one is allocated for this call."""
+    index = cache.index
+    if index != _current():
+        with torch.cuda.device(index):
+            return attn_prefill(cache, q, scale, cap, slopes, window, prefix, first, new, out_dtype, out, workspace)
+    q_heads, n, ldq, out, workspace = _prefill_plan(cache, q, out, out_dtype, workspace)
+    if slopes is not None:
+        _need(slopes, "slopes", torch.float32, (q_heads,), index)
+    for t, name, size in ((prefix, "prefix", cache.seqs), (first, "first", cache.seqs * n), (new, "new", cache.seqs)):
+        if t is not None:
+            _need(t, name, torch.int32, (size,), index)
+    st = load().mmq_attn_prefill(cache._ref, q.data_ptr(), ldq, _at(new), _at(prefix), _at(first), _at(slopes), out.data_ptr(),
+                                 _DTYPE_IDS[out.dtype], q_heads, n, cache.dim ** -0.5 if scale is None else scale, cap, window,
+                                 workspace.ptr, _raw_stream(index))
+    if st != 0:
+        raise MMQError("mmq_attn_prefill", st)
+    return out
+
+
+def tree_words(parents: list[list[int]], width: int | None = None, device=None) -> torch.Tensor:
+    """attn_tree's words int64 [seqs][width] from every node's parent (an earlier node, or -1)."""
+    width = max((len(p) for p in parents), default=0) if width is None else width
+    if width > TREE_MAX or any(len(p) > width for p in parents):
+        raise ValueError(f"at most {TREE_MAX} nodes, and no more than the width")
+    rows = []
+    for nodes in parents:
+        words = []
+        for t, p in enumerate(nodes):
+            if not -1 <= p < t:
+                raise ValueError("a node's parent is an earlier node, or -1")
+            words.append((words[p] if p >= 0 else 0) | 1 << t)
+        rows.append([w - (1 << 64) if w >> 63 else w for w in words] + [0] * (width - len(words)))
+    return torch.tensor(rows, dtype=torch.int64).reshape(len(parents), width).to(device if device is not None else "cuda")
+
+
+def attn_tree(cache: KVCache, q: torch.Tensor, tree: torch.Tensor, scale: float | None = None, cap: float = 0.0,
+              first: torch.Tensor | None = None, new: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+              out: torch.Tensor | None = None, workspace: AttnWorkspace | None = None) -> torch.Tensor:
+    """Attention of a tree of n <= 64 drafted tokens per sequence, the cache's newest entries.
+
+    tree int64 [seqs][n] (tree_words): row t sees all entries before the nodes and node j where
+    bit j of its word is set.  Everything else as in attn_prefill."""
+    index = cache.index
+    if index != _current():
+        with torch.cuda.device(index):
+            return attn_tree(cache, q, tree, scale, cap, first, new, out_dtype, out, workspace)
+    q_heads, n, ldq, out, workspace = _prefill_plan(cache, q, out, out_dtype, workspace)
+    if n > TREE_MAX:
+        raise ValueError(f"1 to {TREE_MAX} nodes per sequence")
+    _need(tree, "tree", torch.int64, (cache.seqs, n), index)
+    for t, name, size in ((first, "first", cache.seqs * n), (new, "new", cache.seqs)):
+        if t is not None:
+            _need(t, name, torch.int32, (size,), index)
+    st = load().mmq_attn_tree(cache._ref, q.data_ptr(), ldq, tree.data_ptr(), _at(new), _at(first), out.data_ptr(), _DTYPE_IDS[out.dtype],
+                              q_heads, n, cache.dim ** -0.5 if scale is None else scale, cap, workspace.ptr, _raw_stream(index))
+    if st != 0:
+        raise MMQError("mmq_attn_tree", st)
+    return out
+
+
+def kv_keep(cache: KVCache, keep: torch.Tensor, count: torch.Tensor | None, nodes: int, new: torch.Tensor | None = None):
+    """Keep the accepted path of a tree: of every sequence's last `nodes` entries (new int32
+    [seqs]: of as many as it has), entry keep[i] moves to place i of them, for i < count.
+
+    keep int32 [seqs][m], ascending along a row; count int32 [seqs] (None: m each).  k, v and
+    the bookkeeping move in place.  Lower cache.lens by nodes - count once every layer that
+    shares it is done."""
+    index = cache.index
+    if index != _current():
+        with torch.cuda.device(index):
+            return kv_keep(cache, keep, count, nodes, new)
+    if keep.dim() != 2 or not 0 <= keep.shape[1] <= nodes <= TREE_MAX:
+        raise ValueError(f"keep must be [seqs][m], m <= nodes <= {TREE_MAX}")
+    _need(keep, "keep", torch.int32, (cache.seqs, keep.shape[1]), index)
+    for t, name in ((count, "count"), (new, "new")):
+        if t is not None:
+            _need(t, name, torch.int32, (cache.seqs,), index)
+    st = load().mmq_kv_keep(cache._ref, keep.data_ptr(), _at(count), _at(new), keep.shape[1], nodes, _raw_stream(index))
+    if st != 0:
+        raise MMQError("mmq_kv_keep", st)
 
 
 def _evict_ints(cache: KVCache, budget: int) -> int:
@@ -683,8 +899,10 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.
 
 
 # MMQ_ERR_INDEX: kernel ids and sites of csrc/mmq_cache.cuh
-_INDEX_KERNELS = {32: "rotary append", 33: "attention", 34: "eviction", 35: "verification"}
-_INDEX_SITES = {1: "a sequence's length", 2: "a page id", 3: "a count of new or drafted tokens", 4: "a drafted token"}
+_INDEX_KERNELS = {32: "rotary append", 33: "attention", 34: "eviction", 35: "verification", 36: "prompt or tree attention",
+                  37: "normed rotary append", 38: "keeping a path"}
+_INDEX_SITES = {1: "a sequence's length", 2: "a page id", 3: "a count of new or drafted tokens", 4: "a drafted token",
+                5: "an axis", 6: "a kept node"}
 _ERR_CUDA, _ERR_INDEX = -8, -11
 
 
@@ -699,12 +917,12 @@ def _failure(st: int, detail, info) -> str:
 def check_status(device: torch.device | None = None):
     """Synchronise the current stream and raise if a kernel reported an error.
 
-    The products and the decode-side operators have a status word each; where both hold an
-    error, the one raised has the products' status and names both."""
+    The products, the decode-side operators, and those for prompts and trees have a status
+    word each; where several hold an error, the one raised has the first's status and names all."""
     dev = device or torch.device("cuda", torch.cuda.current_device())
     first, what = 0, []
     with torch.cuda.device(dev):
-        for _ in range(2):                       # mmq_check_status clears what it reports
+        for _ in range(3):                       # mmq_check_status clears what it reports
             detail, info = (ctypes.c_int * 4)(), (ctypes.c_int * 4)()
             st = load().mmq_check_status(_stream(dev), detail)
             if st == 0:
