@@ -62,6 +62,33 @@ __device__ __forceinline__ float pow2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// two at a time
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// the largest of three; a NaN does not count
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float rcp(float x)
 {
     float y;
@@ -103,10 +130,12 @@ struct PrefillParams {
     int part_rows;             // rows of a part
     int chunks, ksteps;        // 64-value pieces and 16-value steps of a head
     int slots;                 // of the ring
+    int box;                   // rows of a tensor copy, 0: none are used
     float *part;               // [2*grid][part_rows][dim], then [2*grid][part_rows] (max, sum), then [grid] int2 (unit, last CTA)
     float2 *part_ml;
     int2 *joins;
     FastDiv page_div, group_div;
+    CUtensorMap k_map, v_map;  // [pages][heads][page_size][dim], boxes of 64 values of `box` entries
 };
 
 // What a unit's rows see.
@@ -290,7 +319,7 @@ struct PrefillWalk {
 template <typename T, int NQ, int TN>
 struct PrefillShape {
     static constexpr int RT = 128 * NQ;
-    static constexpr int kThreads = (4 * NQ + 1 + pre::LOADERS) * 32;
+    static constexpr int kThreads = (4 * NQ + 4) * 32;         // softmax; issuing, loading, an idle warp
     static constexpr int kBuf = 2;                             // S buffers: one per half, or two for the only half
     static constexpr int kO = kBuf * TN;                       // tensor-memory column of the sums
     static constexpr int kOPitch = (512 - kO) / NQ;
@@ -350,8 +379,10 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
     PrefillWalk<RT, TN> w(p);
     w.start();
 
+    // With 256 rows the softmax warps need more registers than an equal share (168): 2 * 208 + 88 = 3 * 168.
     if (warp < SOFT) {
         // ------------------------------------------------------------------ softmax: one row per thread
+        if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int half = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t o_col = tmem + lanes + S::kO + half * S::kOPitch;
@@ -440,8 +471,8 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     }
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < TN; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(x[k]));
-                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    for (int k = 0; k < TN; k += 2) top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                    const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     const bool raise = mx > m && !((mx - m) * c <= kLazy);
                     if (__any_sync(0xffffffffu, raise)) {
                         float f = 1.f;
@@ -467,13 +498,17 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                         }
                     }
                     const float mc = m == -INFINITY ? 0.f : m * c;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint64_t sum[2] = {0, 0};
                     const float off = kLift<T> - mc;           // m c is rounded once, the same wherever it is used
                     if (__all_sync(0xffffffffu, fabsf(mc) < 4096.f)) {
+                        const uint64_t c2 = pair(c, c), off2 = pair(off, off);
 #pragma unroll
                         for (int k = 0; k < TN; k += 2) {
-                            const float a = pow2(fmaf(__uint_as_float(x[k]), c, off)), b = pow2(fmaf(__uint_as_float(x[k + 1]), c, off));
-                            sum[k / 2 & 3] += a + b;
+                            float a, b;
+                            unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, off2), a, b);
+                            a = pow2(a);
+                            b = pow2(b);
+                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(a, b));
                             x[k / 2] = pack2<T>(a, b);
                         }
                     } else {                                   // m is taken off first in rows of such scores, and in these alone
@@ -484,11 +519,13 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                             const float u0 = __uint_as_float(x[k]), u1 = __uint_as_float(x[k + 1]);
                             const float a = pow2(large ? fmaf(u0 - ms, c, kLift<T>) : fmaf(u0, c, off));
                             const float b = pow2(large ? fmaf(u1 - ms, c, kLift<T>) : fmaf(u1, c, off));
-                            sum[k / 2 & 3] += a + b;
+                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(a, b));
                             x[k / 2] = pack2<T>(a, b);
                         }
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    float la, lb;
+                    unpair(add2(sum[0], sum[1]), la, lb);
+                    l += la + lb;
 #pragma unroll
                     for (int k = 0; k < TN / 2; k += 32) tmem_st32(s_col + k, reinterpret_cast<uint32_t(&)[32]>(x[k]));
                     tmem_st_wait();
@@ -559,6 +596,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
         if (join.x >= 0 && threadIdx.x == 0) p.joins[blockIdx.x] = join;
     } else if (warp == SOFT) {
         // ------------------------------------------------------------------ one thread issues the products
+        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         constexpr uint32_t kIdS = idesc<T>(TN, false);
         const uint32_t id_o = idesc<T>(p.ksteps * 16, true);
         int g = 0, runs = 0, slot = 0, phase = 0;              // slot: of the next tile's K
@@ -633,8 +671,11 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             mbar_wait(b_drain, 0, &never, KID_PREFILL, W_DRAIN);
         }
         __syncwarp();
+    } else if (warp > SOFT + LOADERS) {
+        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     } else {
         // ------------------------------------------------------------------ loaders
+        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         const int lw = warp - SOFT - 1;
         const int pieces = p.ksteps * 2;                       // 16-byte pieces of a row, past `dim` zeros
         const int step_row = 32 / pieces, step_piece = 32 - step_row * pieces;
@@ -730,6 +771,35 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             }
             push(b_qfull, -1);
             for (int tile = u.t0; tile < u.t1; ++tile) {
+                const bool cut = tile * TN < u.max_lo || (tile + 1) * TN > u.min_hi;
+                if (p.box && !cut) {                           // every entry is there: boxes of entries of one page
+                    const int boxes = TN / p.box;
+                    const bool mine = lane < boxes && lane % LOADERS == lw;
+                    int pg = 0, off = 0;
+                    if (mine) {
+                        const int e = tile * TN + lane * p.box, col = p.page_div.of(e);
+                        off = e - col * p.c.page_size;
+                        pg = cache_page(p.c, u.b, col, KID_PREFILL);
+                        if (pg < 0) pg = off = 0;
+                    }
+                    const int many = __popc(__ballot_sync(0xffffffffu, mine));
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (!waits(b_empty + 8 * slot, phase ^ 1, W_EMPTY)) return false;
+                        const uint32_t bar = b_full + 8 * slot, dst = ring + slot * slot_bytes + lane * p.box * 128;
+                        if (lane == 0) {
+                            if (many) mbar_arrive_expect_tx(bar, (uint32_t)(many * p.chunks * p.box * 128));
+                            else mbar_arrive(bar);
+                        }
+                        __syncwarp();
+                        if (mine)
+                            for (int ch = 0; ch < p.chunks; ++ch)
+                                tma_load_4d(dst + ch * (TN * 128), kv ? &p.v_map : &p.k_map, bar, ch * 64, off, u.h, pg);
+                        if (++slot == p.slots) slot = 0, phase ^= 1;
+                    }
+                    flush();                                   // what was copied otherwise before
+                    continue;
+                }
                 const T *ka[BATCH], *va[BATCH];
 #pragma unroll
                 for (int bt = 0; bt < BATCH; ++bt) {
@@ -744,7 +814,6 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                         va[bt] = static_cast<const T *>(p.c.v) + pg * p.c.v_page + u.h * p.c.v_head + off * p.c.v_slot;
                     }
                 }
-                const bool cut = tile * TN < u.max_lo || (tile + 1) * TN > u.min_hi;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     if (!waits(b_empty + 8 * slot, phase ^ 1, W_EMPTY)) return false;
@@ -758,9 +827,18 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             ++runs;
             return true;
         };
-        for (bool first = true; w.next(first); first = false)
-            if (w.u.t0 < w.u.t1 && !run(w.u)) break;
+        bool ok = true;
+        for (bool first = true; ok && w.next(first); first = false)
+            if (w.u.t0 < w.u.t1) ok = run(w.u);
         flush();
+        if (!ok && p.box) {                                    // a wait ran out: the copies under way still come to their end
+            uint32_t never = 0;
+            for (int i = 0; i < p.slots; ++i) {
+                const int before = i < slot ? phase : phase ^ 1;       // of the slot's last copy; none: over already
+                if (lane == 0) mbar_wait(b_full + 8 * i, (uint32_t)before, &never, KID_PREFILL, W_DRAIN);
+            }
+            __syncwarp();
+        }
     }
 done:
     tc_fence_before();
@@ -913,6 +991,32 @@ struct Call {
     float *work;
 };
 
+// Tensor maps of K and V, where boxes of at least eight entries fit the pages (and the swizzle's groups of eight rows).
+int make_maps(PrefillParams &p, const Plan &q)
+{
+    const mmq_kv_cache &c = p.c;
+    p.box = 0;
+    int box = 1;
+    while (2 * box <= q.tn && c.page_size % (2 * box) == 0) box *= 2;
+    if (box < 8 || c.dim < 64) return MMQ_OK;
+    const uint64_t dims[4] = {(uint64_t)c.dim, (uint64_t)c.page_size, (uint64_t)c.heads, (uint64_t)c.pages};
+    const uint32_t extent[4] = {64, (uint32_t)box, 1, 1};
+    for (int kv = 0; kv < 2; ++kv) {
+        uint64_t strides[3] = {(uint64_t)(kv ? c.v_slot : c.k_slot) * 2, (uint64_t)(kv ? c.v_head : c.k_head) * 2,
+                               (uint64_t)(kv ? c.v_page : c.k_page) * 2};
+        for (int i = 0; i < 3; ++i) {
+            if (dims[i + 1] == 1) strides[i] = 16;             // never used
+            if (strides[i] == 0 || strides[i] >= 1ull << 40) return MMQ_OK;
+        }
+        const int rc = make_tmap_4d(kv ? &p.v_map : &p.k_map, kv ? c.v : c.k,
+                                    c.dtype == MMQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides,
+                                    extent, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (rc != MMQ_OK) return rc;
+    }
+    p.box = box;
+    return MMQ_OK;
+}
+
 int attend(const mmq_kv_cache *cache, const Call &a, mmq_stream_t stream)
 {
     int rc = check_cache(cache);
@@ -958,6 +1062,7 @@ int attend(const mmq_kv_cache *cache, const Call &a, mmq_stream_t stream)
     p.joins = reinterpret_cast<int2 *>(p.part_ml + 2ll * q.grid * q.part_rows);
     p.page_div = FastDiv(cache->page_size);
     p.group_div = FastDiv(p.group);
+    if ((rc = make_maps(p, q)) != MMQ_OK) return rc;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return cache->dtype == MMQ_F16 ? launch_any<__half>(p, q, st) : launch_any<__nv_bfloat16>(p, q, st);
 }
