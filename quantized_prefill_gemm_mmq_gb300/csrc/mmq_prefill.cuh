@@ -34,11 +34,20 @@ namespace {
 
 namespace pre {
 constexpr int LOADERS = 2;            // warps
+constexpr int PARTS = 2;              // of a tile's P, each announced by itself
 constexpr int LAG = 2;                // copies a loader has under way before it waits for the oldest
 constexpr int MAX_SLOTS = 12;
 constexpr uint32_t SMEM = 232448 - 1024;            // dynamic, with slack for alignment
 
-enum { W_Q = 1, W_K, W_V, W_P, W_S, W_EMPTY, W_QEMPTY, W_PV, W_DRAIN };     // sites of waits
+enum { W_Q = 1, W_K, W_V, W_P, W_S, W_EMPTY, W_QEMPTY, W_PV, W_TURN, W_SCAN, W_DRAIN };     // sites of waits
+
+// By whole warps; the lanes may wait for different barriers: a wait for one that is over already takes some 200 cycles while
+// the tensor core reads shared memory, so several are better waited for in one go.
+__device__ __forceinline__ bool wait(uint32_t bar, int parity, volatile uint32_t *abort, int site)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, (uint32_t)parity, 1000))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)parity, abort, KID_PREFILL, site));
+}
 
 template <typename T>
 constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
@@ -62,6 +71,15 @@ __device__ __forceinline__ float pow2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// True in one thread of a converged warp, always the same.  Products issued under it take their descriptors from uniform
+// registers; under lane == 0 each of them took 156 cycles to issue (64 to execute).
+__device__ __forceinline__ bool elect()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // two at a time
 __device__ __forceinline__ uint64_t pair(float a, float b)
 {
@@ -135,7 +153,9 @@ struct PrefillParams {
     float2 *part_ml;
     int2 *joins;
     FastDiv page_div, group_div;
+    int q_box;                 // q rows come by tensor copies
     CUtensorMap k_map, v_map;  // [pages][heads][page_size][dim], boxes of 64 values of `box` entries
+    CUtensorMap q_map;         // [rows][q_heads][dim], boxes of 64 values of a group's heads of 128/group tokens
 };
 
 // What a unit's rows see.
@@ -160,17 +180,19 @@ __device__ __forceinline__ PrefillRow prefill_row(const PrefillParams &p, const 
     return r;
 }
 
-// Lengths and counts of sequence b.
+// Lengths and counts of sequence b: the loads first, then their checks.
 __device__ __forceinline__ void prefill_sequence(const PrefillParams &p, PrefillUnit &u)
 {
-    u.len = cache_len(p.c, u.b, KID_PREFILL);
-    u.n = new_count(p.new_len, u.b, p.new_tokens, KID_PREFILL);
-    if (u.n > u.len) {                            // more new tokens than entries: the first of them are not there
-        record_error(MMQ_ERR_INDEX, KID_PREFILL, SITE_LEN);
-        u.n = 0;
+    const int len = *(p.c.len + u.b), n = p.new_len ? *(p.new_len + u.b) : p.new_tokens, prefix = p.prefix ? *(p.prefix + u.b) : 0;
+    const int cap = p.c.cols * p.c.page_size;
+    u.len = (unsigned)len <= (unsigned)cap ? len : 0;
+    u.n = min(max(n, 0), p.new_tokens);
+    if (u.len != len || u.n != n || u.n > u.len) {
+        record_error(MMQ_ERR_INDEX, KID_PREFILL, u.n != n ? SITE_COUNT : SITE_LEN);
+        if (u.n > u.len) u.n = 0;                 // more new tokens than entries: none of them is there
     }
     u.ctx = u.len - u.n;
-    u.prefix = p.prefix ? min(max(*(p.prefix + u.b), 0), u.len) : 0;
+    u.prefix = min(max(prefix, 0), u.len);
 }
 
 // Tiles of unit (b, rt) as far as lengths, window and prefix say: the same for every head, and without reading `first`.
@@ -319,7 +341,7 @@ struct PrefillWalk {
 template <typename T, int NQ, int TN>
 struct PrefillShape {
     static constexpr int RT = 128 * NQ;
-    static constexpr int kThreads = (4 * NQ + 4) * 32;         // softmax; issuing, loading, an idle warp
+    static constexpr int kThreads = (4 * NQ + 4) * 32;         // softmax, two issuing and two loading warps
     static constexpr int kBuf = 2;                             // S buffers: one per half, or two for the only half
     static constexpr int kO = kBuf * TN;                       // tensor-memory column of the sums
     static constexpr int kOPitch = (512 - kO) / NQ;
@@ -331,11 +353,11 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 {
     using namespace pre;
     using S = PrefillShape<T, NQ, TN>;
-    constexpr int RT = S::RT, SOFT = 4 * NQ;                   // softmax warps; then the issuing warp, then the loaders
+    constexpr int RT = S::RT, SOFT = 4 * NQ;                   // softmax warps; then two issuing ones, then the loaders
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t s_bar[3 + 2 * MAX_SLOTS + 3 * 2];
+    __shared__ __align__(8) uint64_t s_bar[4 + 2 * MAX_SLOTS + 4 * 2 + 2 * PARTS];
     __shared__ uint32_t s_tmem, s_abort;
-    __shared__ uint32_t s_bad[MAX_SLOTS][LOADERS][TN / 32];    // entries of a V tile that were not finite and are taken as 0
+    __shared__ uint32_t s_bad[MAX_SLOTS][TN / 32];             // entries of a V tile that were not finite and are taken as 0
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile uint32_t *abort = &s_abort;
@@ -343,23 +365,26 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
     const uint32_t q_bytes = (uint32_t)p.chunks * (128 * 128), slot_bytes = (uint32_t)p.chunks * (TN * 128);
     const uint32_t ring = base + NQ * q_bytes;
     const uint32_t bar0 = smem_u32(s_bar);
-    const uint32_t b_qfull = bar0, b_qempty = bar0 + 8, b_drain = bar0 + 16;
-    const uint32_t b_full = bar0 + 24, b_empty = b_full + 8 * MAX_SLOTS;
-    const uint32_t b_s = b_empty + 8 * MAX_SLOTS, b_p = b_s + 16, b_pv = b_p + 16;
+    const uint32_t b_qfull = bar0, b_qempty = bar0 + 8, b_drain = bar0 + 16;       // b_drain: one per issuing warp
+    const uint32_t b_full = bar0 + 32, b_empty = b_full + 8 * MAX_SLOTS;
+    const uint32_t b_s = b_empty + 8 * MAX_SLOTS, b_pv = b_s + 16, b_turn = b_pv + 16, b_scan = b_turn + 16;
+    const uint32_t b_p = b_scan + 16;                          // [S buffer][part of P]
 
     if (threadIdx.x == 0) {
         s_abort = 0;
         mbar_init(b_qfull, LOADERS);
-        mbar_init(b_qempty, 1);
-        mbar_init(b_drain, 1);
+        mbar_init(b_qempty, NQ);
         for (int i = 0; i < MAX_SLOTS; ++i) {
             mbar_init(b_full + 8 * i, LOADERS);
-            mbar_init(b_empty + 8 * i, 1);
+            mbar_init(b_empty + 8 * i, NQ);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(b_drain + 8 * i, 1);
             mbar_init(b_s + 8 * i, 1);
-            mbar_init(b_p + 8 * i, 4);
             mbar_init(b_pv + 8 * i, 1);
+            mbar_init(b_turn + 8 * i, 1);
+            mbar_init(b_scan + 8 * i, 4);
+            for (int k = 0; k < PARTS; ++k) mbar_init(b_p + 8 * (i * PARTS + k), 4);
         }
         fence_mbar_init();
     }
@@ -374,7 +399,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
-    if (!p.whole && threadIdx.x == 0) p.joins[blockIdx.x] = make_int2(-1, 0);          // also if a wait runs out
+    if (!p.whole && warp == 0 && lane == 0) p.joins[blockIdx.x] = make_int2(-1, 0);          // also if a wait runs out
 
     PrefillWalk<RT, TN> w(p);
     w.start();
@@ -389,7 +414,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
         const int dcols = p.ksteps * 16;
         const bool general = p.cap_out != 0.f || p.slopes || !(p.scale_log2 > 0.f);
         const float c = general ? 1.f : p.scale_log2;
-        int g = 0, runs = 0, vslot = 1, vphase = 0;
+        int g = 0, runs = 0, scans = 0, vslot = 1, vphase = 0;
         int2 join = make_int2(-1, 0);
         for (bool first = true; w.next(first); first = false) {
             const PrefillUnit &u = w.u;
@@ -416,14 +441,59 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             for (int tile = u.t0; tile < u.t1; ++tile, ++g) {
                 const int sb = NQ == 2 ? half : g & 1, sph = NQ == 2 ? g & 1 : (g >> 1) & 1;
                 const uint32_t s_col = tmem + lanes + sb * TN;
-                if (!mbar_wait_warp(b_s + 8 * sb, sph, abort, KID_PREFILL, W_S)) goto done;
+                if (!wait(b_s + 8 * sb, sph, abort, W_S)) goto done;
                 tc_fence_after();
+                // In a tile that some row of the unit sees in part only, entries of V that are not finite are taken as 0
+                // (0 times them would be NaN in rows that do not see them) and noted: a row that sees one is not finite.
+                // The halves both look, whoever comes first: a value is noted before it is taken away.
+                const bool scan = tile * TN < u.max_lo || (tile + 1) * TN > u.min_hi;
+                if (scan) {
+                    if (!wait(b_full + 8 * vslot, vphase, abort, W_V)) goto done;
+                    constexpr int PER = 128 / TN;              // threads per entry
+                    const int e = (quarter * 32 + lane) / PER;
+                    const uint32_t at = ring + vslot * slot_bytes + e * 128;
+                    auto piece = [&](int k) { return at + (k >> 3) * (TN * 128) + (((k & 7) ^ (e & 7)) << 4); };
+                    uint32_t acc = 0;
+#pragma unroll 4
+                    for (int k = lane % PER; k < p.c.dim / 8; k += PER) {
+                        uint32_t v[4];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(piece(k)) : "memory");
+                        constexpr uint32_t one = kBf<T> ? 0x00800080u : 0x04000400u;       // on top of a full exponent: bit 15
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc |= (v[i] & 0x7fff7fffu) + one;
+                    }
+                    const bool bad = (acc & 0x80008000u) != 0;
+                    if (__any_sync(0xffffffffu, bad)) {
+                        if (bad) {
+                            atomicOr(&s_bad[vslot][e >> 5], 1u << (e & 31));
+                            __threadfence_block();
+                            for (int k = lane % PER; k < p.c.dim / 8; k += PER)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(piece(k)), "r"(0u) : "memory");
+                            fence_proxy_async_smem();
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(b_scan + 8 * half);
+                    if (!wait(b_scan + 8 * half, scans & 1, abort, W_SCAN)) goto done;
+                    ++scans;
+                }
                 if (any) {
                     uint32_t x[TN];
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto largest = [&](int k) {
 #pragma unroll
-                    for (int k = 0; k < TN; k += 32) tmem_ld32(s_col + k, reinterpret_cast<uint32_t(&)[32]>(x[k]));
+                        for (int j = k; j < k + 32; j += 2)
+                            top[j / 2 & 3] = max3(top[j / 2 & 3], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                    };
+                    const bool cut = tile * TN < max_lo || (tile + 1) * TN > min_hi;
+                    const bool plain = !general && !cut;
+                    tmem_ld32(s_col, reinterpret_cast<uint32_t(&)[32]>(x[0]));
 #pragma unroll
-                    for (int k = 0; k < TN; k += 32) tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
+                    for (int k = 0; k < TN; k += 32) {         // a piece's maximum while the next one is on the way
+                        tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
+                        if (k + 32 < TN) tmem_ld32(s_col + k + 32, reinterpret_cast<uint32_t(&)[32]>(x[(k + 32) % TN]));
+                        if (plain) largest(k);
+                    }
                     const int e0 = tile * TN;
                     if (general) {
                         const float bias = slope * (float)(e0 - u.ctx - t);
@@ -441,8 +511,8 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                                 x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), p.scale_log2, fmaf(slope, (float)k, bias)));
                         }
                     }
-                    if (e0 < max_lo || e0 + TN > min_hi) {
-                        uint32_t bits[TN / 32];
+                    uint32_t bits[TN / 32];                    // what the row sees of the tile
+                    if (cut) {
 #pragma unroll
                         for (int k = 0; k < TN / 32; ++k) {
                             const int a = min(max(see.lo - e0 - 32 * k, 0), 32), z = min(max(see.hi - e0 - 32 * k, 0), 32);
@@ -459,19 +529,15 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                             for (int j = 0; j < 32; ++j)
                                 if (!(bits[k] >> j & 1u)) x[32 * k + j] = 0xff800000u;
                         }
-                        // entries of V that are not finite were taken as 0 in this tile: a row that sees one is not finite
-                        if (!mbar_wait_warp(b_full + 8 * vslot, vphase, abort, KID_PREFILL, W_V)) goto done;
-#pragma unroll
-                        for (int k = 0; k < TN / 32; ++k) {
-                            uint32_t bad = 0;
-#pragma unroll
-                            for (int i = 0; i < LOADERS; ++i) bad |= *(volatile uint32_t *)&s_bad[vslot][i][k];
-                            poison |= (bad & bits[k]) != 0;
-                        }
                     }
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (scan) {                                // found below, before P is announced
 #pragma unroll
-                    for (int k = 0; k < TN; k += 2) top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                        for (int k = 0; k < TN / 32; ++k) poison |= (*(volatile uint32_t *)&s_bad[vslot][k] & (cut ? bits[k] : 0xffffffffu)) != 0;
+                    }
+                    if (!plain) {
+#pragma unroll
+                        for (int k = 0; k < TN; k += 32) largest(k);
+                    }
                     const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     const bool raise = mx > m && !((mx - m) * c <= kLazy);
                     if (__any_sync(0xffffffffu, raise)) {
@@ -484,7 +550,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                         }
                         if (tile != u.t0) {
                             if (NQ == 1) {                     // the last product may still be adding
-                                if (!mbar_wait_warp(b_pv, (g - 1) & 1, abort, KID_PREFILL, W_PV)) goto done;
+                                if (!wait(b_pv, (g - 1) & 1, abort, W_PV)) goto done;
                                 tc_fence_after();
                             }
                             for (int d = 0; d < dcols; d += 16) {
@@ -500,39 +566,48 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     const float mc = m == -INFINITY ? 0.f : m * c;
                     uint64_t sum[2] = {0, 0};
                     const float off = kLift<T> - mc;           // m c is rounded once, the same wherever it is used
-                    if (__all_sync(0xffffffffu, fabsf(mc) < 4096.f)) {
-                        const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+                    const bool large = !(fabsf(mc) < 4096.f), any_large = __any_sync(0xffffffffu, large);
+                    const float ms = m == -INFINITY ? 0.f : m;
+                    const uint64_t c2 = pair(c, c), off2 = pair(off, off);
 #pragma unroll
-                        for (int k = 0; k < TN; k += 2) {
-                            float a, b;
-                            unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, off2), a, b);
-                            a = pow2(a);
-                            b = pow2(b);
-                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(a, b));
-                            x[k / 2] = pack2<T>(a, b);
-                        }
-                    } else {                                   // m is taken off first in rows of such scores, and in these alone
-                        const bool large = !(fabsf(mc) < 4096.f);
-                        const float ms = m == -INFINITY ? 0.f : m;
+                    for (int part = 0; part < PARTS; ++part) {
+                        constexpr int W = TN / PARTS;
+                        if (!any_large) {
 #pragma unroll
-                        for (int k = 0; k < TN; k += 2) {
-                            const float u0 = __uint_as_float(x[k]), u1 = __uint_as_float(x[k + 1]);
-                            const float a = pow2(large ? fmaf(u0 - ms, c, kLift<T>) : fmaf(u0, c, off));
-                            const float b = pow2(large ? fmaf(u1 - ms, c, kLift<T>) : fmaf(u1, c, off));
-                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(a, b));
-                            x[k / 2] = pack2<T>(a, b);
+                            for (int k = part * W; k < (part + 1) * W; k += 2) {
+                                float a, b;
+                                unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, off2), a, b);
+                                a = pow2(a);
+                                b = pow2(b);
+                                sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(a, b));
+                                x[k / 2] = pack2<T>(a, b);
+                            }
+                        } else {                               // m is taken off first in rows of such scores, and in these alone
+#pragma unroll
+                            for (int k = part * W; k < (part + 1) * W; k += 2) {
+                                const float u0 = __uint_as_float(x[k]), u1 = __uint_as_float(x[k + 1]);
+                                const float a = pow2(large ? fmaf(u0 - ms, c, kLift<T>) : fmaf(u0, c, off));
+                                const float b = pow2(large ? fmaf(u1 - ms, c, kLift<T>) : fmaf(u1, c, off));
+                                sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(a, b));
+                                x[k / 2] = pack2<T>(a, b);
+                            }
                         }
+#pragma unroll
+                        for (int k = part * W / 2; k < (part + 1) * W / 2; k += 16)
+                            tmem_st16(s_col + k, reinterpret_cast<uint32_t(&)[16]>(x[k]));
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_p + 8 * (sb * PARTS + part));
                     }
                     float la, lb;
                     unpair(add2(sum[0], sum[1]), la, lb);
                     l += la + lb;
-#pragma unroll
-                    for (int k = 0; k < TN / 2; k += 32) tmem_st32(s_col + k, reinterpret_cast<uint32_t(&)[32]>(x[k]));
-                    tmem_st_wait();
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane < PARTS) mbar_arrive(b_p + 8 * (sb * PARTS + lane));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_p + 8 * sb);
                 vslot += 2;
                 if (vslot >= p.slots) {
                     vslot -= p.slots;
@@ -543,7 +618,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             // the run's sums
             const bool some = u.t0 < u.t1;
             if (some) {
-                if (!mbar_wait_warp(b_pv + 8 * half, NQ == 2 ? runs & 1 : (g - 1) & 1, abort, KID_PREFILL, W_PV)) goto done;
+                if (!wait(b_pv + 8 * half, NQ == 2 ? runs & 1 : (g - 1) & 1, abort, W_PV)) goto done;
                 tc_fence_after();
                 ++runs;
             }
@@ -593,64 +668,73 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 join = make_int2((u.b * p.row_tiles + u.rt) * p.c.heads + u.h, (int)((end * w.grid - 1) / w.total));
             }
         }
-        if (join.x >= 0 && threadIdx.x == 0) p.joins[blockIdx.x] = join;
-    } else if (warp == SOFT) {
-        // ------------------------------------------------------------------ one thread issues the products
+        if (join.x >= 0 && warp == 0 && lane == 0) p.joins[blockIdx.x] = join;
+    } else if (warp < SOFT + 2) {
+        // ------------------------------------------------------------------ one thread per half issues its products
         if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         constexpr uint32_t kIdS = idesc<T>(TN, false);
         const uint32_t id_o = idesc<T>(p.ksteps * 16, true);
+        const int i = warp - SOFT;                             // the half; with one half the second warp has nothing to do
         int g = 0, runs = 0, slot = 0, phase = 0;              // slot: of the next tile's K
-        auto product_s = [&](int i, int sb, int at) {          // half i, S buffer sb, K in slot `at`
-            const uint32_t a = base + i * q_bytes, b = ring + at * slot_bytes;
-            for (int k = 0; k < p.ksteps; ++k)
-                umma_f16(tmem + sb * TN, sdesc_k_sw128(a + (k >> 2) * (128 * 128) + (k & 3) * 32),
-                         sdesc_k_sw128(b + (k >> 2) * (TN * 128) + (k & 3) * 32), kIdS, k > 0);
-            umma_commit(b_s + 8 * sb);
-        };
-        auto product_o = [&](int i, int sb, int at, bool add) {
-            const uint32_t b = ring + at * slot_bytes;
+        constexpr int KSTEPS = S::kMaxDim / 16;
+        auto product_s = [&](int sb, int at, bool last) {      // S buffer sb, K in slot `at`
+            const uint64_t a = sdesc_k_sw128(base + i * q_bytes), b = sdesc_k_sw128(ring + at * slot_bytes);
+            if (elect()) {
 #pragma unroll
-            for (int k = 0; k < TN / 16; ++k)
-                umma_f16_ts(tmem + S::kO + i * S::kOPitch, tmem + sb * TN + 8 * k, sdesc_mn_sw128(b + k * 2048, TN * 128), id_o,
-                            add || k > 0);
+                for (int k = 0; k < KSTEPS; ++k)
+                    if (k < p.ksteps)
+                        umma_f16(tmem + sb * TN, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                                 b + (((k >> 2) * (TN * 128) + (k & 3) * 32) >> 4), kIdS, k > 0);
+                umma_commit(b_s + 8 * sb);
+                umma_commit(b_empty + 8 * at);
+                if (last) umma_commit(b_qempty);
+            }
+            __syncwarp();
+        };
+        auto product_o = [&](int sb, int at, int part, bool add, bool last) {
+            constexpr int STEPS = TN / 16 / PARTS;
+            const uint64_t b = sdesc_mn_sw128(ring + at * slot_bytes + part * STEPS * 2048, TN * 128);
+            if (elect()) {
+#pragma unroll
+                for (int k = 0; k < STEPS; ++k)
+                    umma_f16_ts(tmem + S::kO + i * S::kOPitch, tmem + sb * TN + 8 * (part * STEPS + k), b + ((k * 2048) >> 4), id_o,
+                                add || k > 0);
+                if (part == PARTS - 1) {
+                    umma_commit(b_empty + 8 * at);
+                    if (last) umma_commit(b_pv + 8 * i);
+                }
+            }
+            __syncwarp();
         };
         auto waits = [&](uint32_t bar, int parity, int site) {
-            const bool ok = mbar_wait(bar, (uint32_t)parity, abort, KID_PREFILL, site);
+            const bool ok = wait(bar, parity, abort, site);
             tc_fence_after();
             return ok;
         };
         auto run = [&](int nt) {
             if (!waits(b_qfull, runs & 1, W_Q) || !waits(b_full + 8 * slot, phase, W_K)) return false;
-            for (int i = 0; i < NQ; ++i) product_s(i, NQ == 2 ? i : g & 1, slot);
-            umma_commit(b_empty + 8 * slot);
-            if (nt == 1) umma_commit(b_qempty);
+            product_s(NQ == 2 ? i : g & 1, slot, nt == 1);
             for (int j = 0; j < nt; ++j, ++g) {
                 int vs = slot + 1, vp = phase;
                 if (vs >= p.slots) vs = 0, vp ^= 1;
                 int ks = vs + 1, kp = vp;
                 if (ks >= p.slots) ks = 0, kp ^= 1;
                 const bool more = j + 1 < nt;
-                if (NQ == 1 && more) {                         // the next scores, while this tile's are worked on
-                    if (!waits(b_full + 8 * ks, kp, W_K)) return false;
-                    product_s(0, (g + 1) & 1, ks);
-                    umma_commit(b_empty + 8 * ks);
-                    if (j + 2 == nt) umma_commit(b_qempty);
+                const int sb = NQ == 2 ? i : g & 1;
+                // V and the next K are waited for before P, so that nothing but P holds the products up
+                if (!waits(b_full + 8 * vs, vp, W_V)) return false;
+                if (more && !waits(b_full + 8 * ks, kp, W_K)) return false;
+                if (NQ == 1 && more) product_s((g + 1) & 1, ks, j + 2 == nt);      // while this tile's scores are worked on
+                if (NQ == 2 && !waits(b_turn + 8 * i, i == 0 ? (g & 1) ^ 1 : g & 1, W_TURN)) return false;
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) {
+                    if (!waits(b_p + 8 * (sb * PARTS + part), NQ == 2 ? g & 1 : (g >> 1) & 1, W_P)) return false;
+                    product_o(sb, vs, part, j > 0 || part > 0, NQ == 1 || !more);
                 }
-                for (int i = 0; i < NQ; ++i) {
-                    const int sb = NQ == 2 ? i : g & 1;
-                    if (!waits(b_p + 8 * sb, NQ == 2 ? g & 1 : (g >> 1) & 1, W_P)) return false;
-                    if (i == 0 && !waits(b_full + 8 * vs, vp, W_V)) return false;
-                    product_o(i, sb, vs, j > 0);
-                    if (i == NQ - 1) umma_commit(b_empty + 8 * vs);
-                    if (NQ == 1 || !more) umma_commit(b_pv + 8 * i);
-                    if (NQ == 2 && more) {
-                        if (i == 0 && !waits(b_full + 8 * ks, kp, W_K)) return false;
-                        product_s(i, sb, ks);
-                        if (i == NQ - 1) {
-                            umma_commit(b_empty + 8 * ks);
-                            if (j + 2 == nt) umma_commit(b_qempty);
-                        }
-                    }
+                if (NQ == 2) {
+                    if (more) product_s(sb, ks, j + 2 == nt);
+                    if (lane == 0) mbar_arrive(b_turn + 8 * (i ^ 1));
+                    __syncwarp();
                 }
                 slot = ks;
                 phase = kp;
@@ -658,36 +742,27 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             ++runs;
             return true;
         };
-        for (bool first = true; w.next(first); first = false) {
-            const int nt = w.u.t1 - w.u.t0;
-            if (nt <= 0) continue;
-            bool ok = true;
-            if (lane == 0) ok = run(nt);
-            if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-        }
-        if (lane == 0) {                                       // nothing is under way when tensor memory is given back
-            umma_commit(b_drain);
+        if (i < NQ) {
+            for (bool first = true; w.next(first); first = false) {
+                const int nt = w.u.t1 - w.u.t0;
+                if (nt > 0 && !run(nt)) break;
+            }
+            if (elect()) umma_commit(b_drain + 8 * i);         // nothing is under way when tensor memory is given back
+            __syncwarp();
             uint32_t never = 0;
-            mbar_wait(b_drain, 0, &never, KID_PREFILL, W_DRAIN);
+            mbar_wait_warp(b_drain + 8 * i, 0, &never, KID_PREFILL, W_DRAIN);
         }
-        __syncwarp();
-    } else if (warp > SOFT + LOADERS) {
-        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     } else {
         // ------------------------------------------------------------------ loaders
         if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        const int lw = warp - SOFT - 1;
+        const int lw = warp - SOFT - 2;
         const int pieces = p.ksteps * 2;                       // 16-byte pieces of a row, past `dim` zeros
         const int step_row = 32 / pieces, step_piece = 32 - step_row * pieces;
         const int row0 = lane / pieces, piece0 = lane - row0 * pieces;
         constexpr int BATCH = TN / 32 / LOADERS;               // batches of 32 rows per warp and tile
-        struct Pending {
-            uint32_t bar;                                      // 0: nothing to announce
-            int slot;                                          // of a V tile to look through, or -1
-        };
-        Pending queue[LAG];
+        uint32_t queue[LAG];                                   // barriers of the copies under way, 0 for none
 #pragma unroll
-        for (int i = 0; i < LAG; ++i) queue[i] = {0u, -1};
+        for (int i = 0; i < LAG; ++i) queue[i] = 0;
         // 32 rows whose addresses the lanes hold (null: zeros), `pitch` bytes between their 64-value chunks
         auto copy_rows = [&](const T *at, uint32_t dst, int first_row, uint32_t pitch) {
             int row = row0, piece = piece0;
@@ -702,54 +777,26 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 if (piece >= pieces) piece -= pieces, ++row;
             }
         };
-        // An entry of V that is not finite, in a tile that some row sees in part only: taken as 0, and noted.
-        auto look_through = [&](int slot) {
-            const uint32_t at = ring + slot * slot_bytes;
-            for (int k = lane; k < TN / 32; k += 32) s_bad[slot][lw][k] = 0;
-            __syncwarp();
-            for (int bt = 0; bt < BATCH; ++bt) {
-                const int first_row = (bt * LOADERS + lw) * 32;
-                int row = row0, piece = piece0;
-                for (int i = 0; i < pieces; ++i) {
-                    const int rr = first_row + row;
-                    const uint32_t a = at + (piece >> 3) * (TN * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4);
-                    uint32_t v[4];
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
-                    constexpr uint32_t e = kBf<T> ? 0x7f80u : 0x7c00u;
-                    bool bad = false;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) bad |= (v[k] & e) == e || (v[k] & (e << 16)) == (e << 16);
-                    if (bad) {
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
-                        atomicOr(&s_bad[slot][lw][rr >> 5], 1u << (rr & 31));
-                    }
-                    row += step_row;
-                    piece += step_piece;
-                    if (piece >= pieces) piece -= pieces, ++row;
-                }
-            }
-        };
-        auto announce = [&](const Pending &d) {                // the oldest copies have arrived
-            if (d.bar == 0) return;
-            if (d.slot >= 0) look_through(d.slot);
+        auto announce = [&](uint32_t bar) {                    // the oldest copies have arrived
+            if (bar == 0) return;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(d.bar);
+            if (lane == 0) mbar_arrive(bar);
         };
-        auto push = [&](uint32_t bar, int slot) {
+        auto push = [&](uint32_t bar) {
             cp_commit();
             cp_wait<LAG>();
             announce(queue[0]);
 #pragma unroll
             for (int i = 0; i + 1 < LAG; ++i) queue[i] = queue[i + 1];
-            queue[LAG - 1] = {bar, slot};
+            queue[LAG - 1] = bar;
         };
         auto flush = [&]() {
             cp_wait<0>();
 #pragma unroll
             for (int i = 0; i < LAG; ++i) {
                 announce(queue[i]);
-                queue[i] = {0u, -1};
+                queue[i] = 0;
             }
         };
         // Before a wait that others may have to end with what is still under way here.
@@ -761,25 +808,38 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
         int runs = 0, slot = 0, phase = 0;
         auto run = [&](const PrefillUnit &u) {
             if (!waits(b_qempty, (runs & 1) ^ 1, W_QEMPTY)) return false;
-            for (int bt = lw; bt < RT / 32; bt += LOADERS) {
-                const int r = u.rt * RT + bt * 32 + lane, t = p.group_div.of(min(r, p.rows - 1));
-                const bool live = r < p.rows && t < u.n;
-                const T *at = live ? static_cast<const T *>(p.q) + ((int64_t)u.b * p.new_tokens + t) * p.ldq +
-                                         (int64_t)(u.h * p.group + (r - t * p.group)) * p.c.dim
-                                   : nullptr;
-                copy_rows(at, base + (bt >> 2) * q_bytes, (bt & 3) * 32, 128 * 128);
+            if (p.q_box) {                                     // rows of other sequences, or zeros, in place of rows that are not there
+                if (lane == 0) {
+                    if (lw == 0) mbar_arrive_expect_tx(b_qfull, (uint32_t)(NQ * p.chunks * (128 * 128)));
+                    else mbar_arrive(b_qfull);
+                }
+                __syncwarp();
+                if (lw == 0 && lane < NQ * p.chunks) {
+                    const int i = lane / p.chunks, ch = lane - i * p.chunks;
+                    tma_load_4d(base + i * q_bytes + ch * (128 * 128), &p.q_map, b_qfull, ch * 64, u.h * p.group,
+                                u.b * p.new_tokens + p.group_div.of(u.rt * RT + i * 128), 0);
+                }
+            } else {
+                for (int bt = lw; bt < RT / 32; bt += LOADERS) {
+                    const int r = u.rt * RT + bt * 32 + lane, t = p.group_div.of(min(r, p.rows - 1));
+                    const bool live = r < p.rows && t < u.n;
+                    const T *at = live ? static_cast<const T *>(p.q) + ((int64_t)u.b * p.new_tokens + t) * p.ldq +
+                                             (int64_t)(u.h * p.group + (r - t * p.group)) * p.c.dim
+                                       : nullptr;
+                    copy_rows(at, base + (bt >> 2) * q_bytes, (bt & 3) * 32, 128 * 128);
+                }
+                push(b_qfull);
             }
-            push(b_qfull, -1);
             for (int tile = u.t0; tile < u.t1; ++tile) {
-                const bool cut = tile * TN < u.max_lo || (tile + 1) * TN > u.min_hi;
-                if (p.box && !cut) {                           // every entry is there: boxes of entries of one page
+                if (p.box) {                                   // boxes of entries of one page
                     const int boxes = TN / p.box;
                     const bool mine = lane < boxes && lane % LOADERS == lw;
                     int pg = 0, off = 0;
                     if (mine) {
                         const int e = tile * TN + lane * p.box, col = p.page_div.of(e);
                         off = e - col * p.c.page_size;
-                        pg = cache_page(p.c, u.b, col, KID_PREFILL);
+                        // past the length lies a page that does not exist: zeros
+                        pg = e < u.len ? cache_page(p.c, u.b, col, KID_PREFILL) : (int)p.c.pages;
                         if (pg < 0) pg = off = 0;
                     }
                     const int many = __popc(__ballot_sync(0xffffffffu, mine));
@@ -787,6 +847,8 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     for (int kv = 0; kv < 2; ++kv) {
                         if (!waits(b_empty + 8 * slot, phase ^ 1, W_EMPTY)) return false;
                         const uint32_t bar = b_full + 8 * slot, dst = ring + slot * slot_bytes + lane * p.box * 128;
+                        if (lw == 0 && lane < TN / 32) s_bad[slot][lane] = 0;
+                        __syncwarp();
                         if (lane == 0) {
                             if (many) mbar_arrive_expect_tx(bar, (uint32_t)(many * p.chunks * p.box * 128));
                             else mbar_arrive(bar);
@@ -820,7 +882,8 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 #pragma unroll
                     for (int bt = 0; bt < BATCH; ++bt)
                         copy_rows(kv ? va[bt] : ka[bt], ring + slot * slot_bytes, (bt * LOADERS + lw) * 32, TN * 128);
-                    push(b_full + 8 * slot, kv && cut ? slot : -1);
+                    if (lw == 0 && lane < TN / 32) s_bad[slot][lane] = 0;
+                    push(b_full + 8 * slot);
                     if (++slot == p.slots) slot = 0, phase ^= 1;
                 }
             }
@@ -831,12 +894,13 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
         for (bool first = true; ok && w.next(first); first = false)
             if (w.u.t0 < w.u.t1) ok = run(w.u);
         flush();
-        if (!ok && p.box) {                                    // a wait ran out: the copies under way still come to their end
+        if (!ok && (p.box || p.q_box)) {                                // a wait ran out: the copies under way still come to their end
             uint32_t never = 0;
             for (int i = 0; i < p.slots; ++i) {
                 const int before = i < slot ? phase : phase ^ 1;       // of the slot's last copy; none: over already
-                if (lane == 0) mbar_wait(b_full + 8 * i, (uint32_t)before, &never, KID_PREFILL, W_DRAIN);
+                if (lane == 0 && p.box) mbar_wait(b_full + 8 * i, (uint32_t)before, &never, KID_PREFILL, W_DRAIN);
             }
+            if (lane == 0 && p.q_box) mbar_wait(b_qfull, (uint32_t)(runs & 1), &never, KID_PREFILL, W_DRAIN);
             __syncwarp();
         }
     }
@@ -943,7 +1007,10 @@ inline int make_plan(const mmq_kv_cache *c, int q_heads, int new_tokens, Plan &q
     const int64_t units = (int64_t)c->seqs * c->heads * q.row_tiles, cap = (int64_t)c->cols * c->page_size;
     if (units > 0x7fffffff || units * ((cap + q.tn - 1) / q.tn) > 0x7fffffff) return MMQ_ERR_SHAPE;
     const int sms = sm_count();
-    q.whole = q.row_tiles > 1 && units >= 3ll * sms;
+#ifndef WHOLE
+#define WHOLE 3
+#endif
+    q.whole = q.row_tiles > 1 && units >= (long long)WHOLE * sms;
     q.grid = q.whole ? (int)units : sms;
     q.part_rows = q.rows < q.rt ? q.rows : q.rt;
     q.floats = q.whole ? 4 : 2ll * sms * q.part_rows * (c->dim + 2) + 2ll * sms;
@@ -991,14 +1058,26 @@ struct Call {
     float *work;
 };
 
-// Tensor maps of K and V, where boxes of at least eight entries fit the pages (and the swizzle's groups of eight rows).
+// Tensor maps of K and V, where boxes of at least eight entries fit the pages (and the swizzle's groups of eight rows), and of
+// q, where a box holds whole tokens.
 int make_maps(PrefillParams &p, const Plan &q)
 {
     const mmq_kv_cache &c = p.c;
-    p.box = 0;
+    const CUtensorMapDataType type = c.dtype == MMQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (c.dim < 64) return MMQ_OK;                             // a box is 64 values wide
+    if (128 % p.group == 0) {
+        const uint64_t dims[4] = {(uint64_t)c.dim, (uint64_t)p.q_heads, (uint64_t)c.seqs * p.new_tokens, 1};
+        const uint64_t strides[3] = {(uint64_t)c.dim * 2, (uint64_t)p.ldq * 2, 16};
+        const uint32_t extent[4] = {64, (uint32_t)p.group, (uint32_t)(128 / p.group), 1};
+        if (strides[1] < 1ull << 40) {
+            const int rc = make_tmap_4d(&p.q_map, p.q, type, dims, strides, extent, CU_TENSOR_MAP_SWIZZLE_128B);
+            if (rc != MMQ_OK) return rc;
+            p.q_box = 1;
+        }
+    }
     int box = 1;
     while (2 * box <= q.tn && c.page_size % (2 * box) == 0) box *= 2;
-    if (box < 8 || c.dim < 64) return MMQ_OK;
+    if (box < 8) return MMQ_OK;
     const uint64_t dims[4] = {(uint64_t)c.dim, (uint64_t)c.page_size, (uint64_t)c.heads, (uint64_t)c.pages};
     const uint32_t extent[4] = {64, (uint32_t)box, 1, 1};
     for (int kv = 0; kv < 2; ++kv) {
@@ -1008,9 +1087,7 @@ int make_maps(PrefillParams &p, const Plan &q)
             if (dims[i + 1] == 1) strides[i] = 16;             // never used
             if (strides[i] == 0 || strides[i] >= 1ull << 40) return MMQ_OK;
         }
-        const int rc = make_tmap_4d(kv ? &p.v_map : &p.k_map, kv ? c.v : c.k,
-                                    c.dtype == MMQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides,
-                                    extent, CU_TENSOR_MAP_SWIZZLE_128B);
+        const int rc = make_tmap_4d(kv ? &p.v_map : &p.k_map, kv ? c.v : c.k, type, dims, strides, extent, CU_TENSOR_MAP_SWIZZLE_128B);
         if (rc != MMQ_OK) return rc;
     }
     p.box = box;
