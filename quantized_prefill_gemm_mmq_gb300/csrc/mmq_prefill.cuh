@@ -37,9 +37,9 @@ constexpr int LOADERS = 2;            // warps
 constexpr int PARTS = 2;              // of a tile's P, each announced by itself
 constexpr int LAG = 2;                // copies a loader has under way before it waits for the oldest
 constexpr int MAX_SLOTS = 12;
-constexpr uint32_t SMEM = 232448 - 1024;            // dynamic, with slack for alignment
+constexpr uint32_t SMEM = 230400;     // dynamic, with slack for alignment
 
-enum { W_Q = 1, W_K, W_V, W_P, W_S, W_EMPTY, W_QEMPTY, W_PV, W_TURN, W_SCAN, W_DRAIN };     // sites of waits
+enum { W_Q = 1, W_K, W_V, W_P, W_S, W_EMPTY, W_QEMPTY, W_PV, W_TURN, W_SCAN, W_NEXT, W_DRAIN };     // sites of waits
 
 // By whole warps; the lanes may wait for different barriers: a wait for one that is over already takes some 200 cycles while
 // the tensor core reads shared memory, so several are better waited for in one go.
@@ -71,6 +71,27 @@ __device__ __forceinline__ float pow2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Asks for a CTA of this launch that has not started: its index comes to `at` (16 bytes) and counts on the barrier.
+__device__ __forceinline__ void ask_next(uint32_t at, uint32_t bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(at), "r"(bar) : "memory");
+}
+// The answer: the index of the CTA whose work this one has taken over, or -1 when all have started.
+__device__ __forceinline__ int answer(uint32_t at)
+{
+    uint32_t got, x = 0;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(got), "+r"(x)
+        : "r"(at)
+        : "memory");
+    return got ? (int)x : -1;
+}
+
 // True in one thread of a converged warp, always the same.  Products issued under it take their descriptors from uniform
 // registers; under lane == 0 each of them took 156 cycles to issue (64 to execute).
 __device__ __forceinline__ bool elect()
@@ -107,11 +128,126 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// NaN if one of them is
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float rcp(float x)
 {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 64 columns of the warp's 32 lanes, to be used after tmem_ld_wait on each 32 of them: one load takes as long as its columns,
+// four of 32 columns one after the other a wait each
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[64])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+                 "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+                   "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+                   "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+                   "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+                   "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[128])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+                 "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+                 "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+                 "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+                 "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+                 "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+                   "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+                   "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+                   "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+                   "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+                   "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+                   "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+                   "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+                   "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+                   "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+                   "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+                   "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+                   "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+                 : "r"(at)
+                 : "memory");
+}
+
+// 32 scores (of the columns at `at`) under a cap, in powers of two: cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)).  Four share a reciprocal (8
+// cycles a warp, an exponential 4); e^ is held below 2^30, where the fraction no longer counts, so that their product is
+// finite, and a NaN, which that would hide, is looked for first.
+__device__ __forceinline__ void cap32(uint32_t at, uint32_t (&y)[32], float cap_in, float cap_out)
+{
+    float nan = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) nan = max3_nan(nan, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+    const bool any_nan = __any_sync(0xffffffffu, nan != nan);
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+        float d[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = 1.f + fminf(pow2(__uint_as_float(y[k + j]) * cap_in), 0x1p30f);
+        const float lo = d[0] * d[1], hi = d[2] * d[3], r = rcp(lo * hi) * (-2.f * cap_out), rlo = r * hi, rhi = r * lo;
+        const float z[4] = {fmaf(rlo, d[1], cap_out), fmaf(rlo, d[0], cap_out), fmaf(rhi, d[3], cap_out), fmaf(rhi, d[2], cap_out)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[k + j] = __float_as_uint(z[j]);
+    }
+    if (any_nan) {
+        uint32_t was[32];
+        tmem_ld32(at, was);
+        tmem_ld_wait(was);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] = was[j] << 1 > 0xff000000u ? was[j] : y[j];
+    }
+}
+
+// eight columns of the warp's lanes times f
+__device__ __forceinline__ void scale8(uint32_t at, float f)
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at)
+                 : "memory");
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// 32 bytes to where 16 or (wide) 32 bytes are aligned: a whole sector by one thread
+__device__ __forceinline__ void store32(void *dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g, uint32_t h,
+                                        int wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g),
+                     "r"(h)
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(dst)[0] = make_uint4(a, b, c, d);
+        static_cast<uint4 *>(dst)[1] = make_uint4(e, f, g, h);
+    }
 }
 
 // kind::f16 descriptor: f16 or bf16 operands, f32 sums, A K-major; B K-major or (mn) with its N values contiguous
@@ -142,6 +278,7 @@ struct PrefillParams {
     float scale_log2;          // scale * log2(e)
     float cap_in, cap_out;     // 2 log2(e) scale / cap, cap log2(e); cap_out 0: no cap
     int out_f32, window;
+    int out_wide, part_wide;   // rows of out, and of the parts, begin on 32 bytes
     int new_tokens, group, q_heads;
     int rows, row_tiles;       // rows per sequence and key-value head, units of them
     int whole;                 // one unit per CTA
@@ -236,11 +373,11 @@ __device__ __forceinline__ void prefill_bounds(const PrefillParams &p, PrefillUn
     if (lo >= hi || u.t0 >= u.t1) u.t0 = u.t1 = 0;
 }
 
-// Runs of tiles that a CTA takes, one unit (or part of one) after the other.  Every warp walks them by itself.  Units are
+// Runs of tiles that a CTA takes, one unit (or part of one) after the other.  Every warp walks them by itself, in shared
+// memory, since registers are short while tiles are worked on; a step is made in registers.  Units are
 // numbered (sequence, rows, head): the heads of one (sequence, rows) pair have the same span of tiles.
 template <int RT, int TN>
 struct PrefillWalk {
-    const PrefillParams &p;
     PrefillUnit u;
     int left;                  // tiles still to come
     int at;                    // tile within the unit's span where the next run starts
@@ -249,24 +386,26 @@ struct PrefillWalk {
     int total, grid;           // split: tiles of all units, CTAs that have some
     int place;                 // split: tiles of all units up to the run's end
     int rest;                  // tiles of the unit after the run
+    // whole: a CTA that is done takes over the next unit whose CTA has not started; one loader asks when
+    // its copies for the unit are on their way (asked a unit ahead, units that take longest last wait for busy CTAs)
+    uint32_t answers, b_next;               // two answers of 16 bytes; their barriers: come (2), read by every warp (2)
+    int asked;                              // answers taken
+    bool asks;
 
-    __device__ __forceinline__ explicit PrefillWalk(const PrefillParams &q) : p(q) {}
     __device__ __forceinline__ static int count(int2 s) { return max(1, s.y - s.x); }        // an empty unit still has outputs
 
-    __device__ __forceinline__ void start()
+    __device__ __forceinline__ void start(const PrefillParams &p, uint32_t answers_, uint32_t b_next_, bool asks_)
     {
+        answers = answers_;
+        b_next = b_next_;
+        asked = 0;
+        asks = asks_;
         at = place = 0;
-        if (p.whole) {
-            const int per = p.c.seqs * p.c.heads;
-            const int back = (int)blockIdx.x / per, bh = (int)blockIdx.x - back * per;
-            u.rt = p.row_tiles - 1 - back;
-            u.b = bh / p.c.heads;
-            u.h = bh - u.b * p.c.heads;
-            prefill_sequence(p, u);
-            span = prefill_span<RT, TN>(p, u);
-            left = count(span);
-            return;
-        }
+        if (!p.whole) split(p);
+    }
+
+    __device__ __forceinline__ void split(const PrefillParams &p)
+    {
         const int lane = threadIdx.x & 31, pairs = p.c.seqs * p.row_tiles;
         auto tiles_of = [&](int i) {
             if (i >= pairs) return 0;
@@ -310,8 +449,42 @@ struct PrefillWalk {
     }
 
     // The next run, false when there is none.
-    __device__ __forceinline__ bool next(bool first)
+    __device__ __forceinline__ bool step(const PrefillParams &p, bool first, volatile uint32_t *abort)
     {
+        if (p.whole) {
+            const uint32_t b_taken = b_next + 16;
+            const int lane = threadIdx.x & 31;
+            int id = (int)blockIdx.x;
+            if (!first) {
+                const int buf = asked & 1, round = (asked >> 1) & 1;
+                if (asks) {
+                    if (!pre::wait(b_taken + 8 * buf, round ^ 1, abort, pre::W_NEXT)) return false;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(b_next + 8 * buf, 16);
+                        pre::ask_next(answers + 16 * buf, b_next + 8 * buf);
+                    }
+                    __syncwarp();
+                }
+                if (!pre::wait(b_next + 8 * buf, round, abort, pre::W_NEXT)) return false;
+                id = pre::answer(answers + 16 * buf);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_taken + 8 * buf);
+                ++asked;
+                if (id < 0) return false;
+            }
+            const int per = p.c.seqs * p.c.heads, back = id / per, bh = id - back * per;
+            u.rt = p.row_tiles - 1 - back;                    // the longest first
+            u.b = bh / p.c.heads;
+            u.h = bh - u.b * p.c.heads;
+            prefill_sequence(p, u);
+            span = prefill_span<RT, TN>(p, u);
+            begins = ends = true;
+            u.t0 = span.x;
+            u.t1 = span.y;
+            prefill_bounds<RT, TN>(p, u);
+            return true;
+        }
         if (left <= 0) return false;
         if (!first) {
             at = 0;
@@ -336,6 +509,21 @@ struct PrefillWalk {
         prefill_bounds<RT, TN>(p, u);
         return true;
     }
+
+    // The same for a walk in shared memory.
+    __device__ __forceinline__ void keep(PrefillWalk &at_) const
+    {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) at_ = *this;
+        __syncwarp();
+    }
+    __device__ __forceinline__ bool next(const PrefillParams &p, bool first, volatile uint32_t *abort)
+    {
+        PrefillWalk w = *this;
+        const bool more = w.step(p, first, abort);
+        w.keep(*this);
+        return more;
+    }
 };
 
 template <typename T, int NQ, int TN>
@@ -355,7 +543,9 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
     using S = PrefillShape<T, NQ, TN>;
     constexpr int RT = S::RT, SOFT = 4 * NQ;                   // softmax warps; then two issuing ones, then the loaders
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t s_bar[4 + 2 * MAX_SLOTS + 4 * 2 + 2 * PARTS];
+    __shared__ __align__(8) uint64_t s_bar[4 + 2 * MAX_SLOTS + 4 * 2 + 2 * PARTS + 4];
+    __shared__ __align__(16) uint4 s_answers[2];
+    __shared__ PrefillWalk<RT, TN> s_walk[SOFT + 4];
     __shared__ uint32_t s_tmem, s_abort;
     __shared__ uint32_t s_bad[MAX_SLOTS][TN / 32];             // entries of a V tile that were not finite and are taken as 0
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -369,6 +559,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
     const uint32_t b_full = bar0 + 32, b_empty = b_full + 8 * MAX_SLOTS;
     const uint32_t b_s = b_empty + 8 * MAX_SLOTS, b_pv = b_s + 16, b_turn = b_pv + 16, b_scan = b_turn + 16;
     const uint32_t b_p = b_scan + 16;                          // [S buffer][part of P]
+    const uint32_t b_next = b_p + 16 * PARTS;                  // two, and two that their answers are read
 
     if (threadIdx.x == 0) {
         s_abort = 0;
@@ -384,6 +575,8 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             mbar_init(b_pv + 8 * i, 1);
             mbar_init(b_turn + 8 * i, 1);
             mbar_init(b_scan + 8 * i, 4);
+            mbar_init(b_next + 8 * i, 1);
+            mbar_init(b_next + 16 + 8 * i, SOFT + NQ + LOADERS);
             for (int k = 0; k < PARTS; ++k) mbar_init(b_p + 8 * (i * PARTS + k), 4);
         }
         fence_mbar_init();
@@ -401,13 +594,17 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
     const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
     if (!p.whole && warp == 0 && lane == 0) p.joins[blockIdx.x] = make_int2(-1, 0);          // also if a wait runs out
 
-    PrefillWalk<RT, TN> w(p);
-    w.start();
+    PrefillWalk<RT, TN> &w = s_walk[warp];
+    {
+        PrefillWalk<RT, TN> begin;
+        begin.start(p, smem_u32(s_answers), b_next, warp == SOFT + 2);
+        begin.keep(w);
+    }
 
-    // With 256 rows the softmax warps need more registers than an equal share (168): 2 * 208 + 88 = 3 * 168.
+    // With 256 rows the softmax warps need more registers than an equal share (168): 2 * 216 + 72 = 3 * 168.
     if (warp < SOFT) {
         // ------------------------------------------------------------------ softmax: one row per thread
-        if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int half = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t o_col = tmem + lanes + S::kO + half * S::kOPitch;
@@ -416,7 +613,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
         const float c = general ? 1.f : p.scale_log2;
         int g = 0, runs = 0, scans = 0, vslot = 1, vphase = 0;
         int2 join = make_int2(-1, 0);
-        for (bool first = true; w.next(first); first = false) {
+        for (bool first = true; w.next(p, first, abort); first = false) {
             const PrefillUnit &u = w.u;
             const int r = u.rt * RT + half * 128 + quarter * 32 + lane;
             const int t = p.group_div.of(min(r, p.rows - 1));
@@ -436,13 +633,23 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             const int min_hi = __reduce_min_sync(0xffffffffu, live ? see.hi : 0x7fffffff);
             const float slope = p.slopes && live ? p.slopes[head] * 1.44269504088896341f : 0.f;
             float m = -INFINITY, l = 0.f;
-            bool poison = false;
+            bool poison = false, any_large = false;            // any_large: of the warp, see below
 
             for (int tile = u.t0; tile < u.t1; ++tile, ++g) {
                 const int sb = NQ == 2 ? half : g & 1, sph = NQ == 2 ? g & 1 : (g >> 1) & 1;
                 const uint32_t s_col = tmem + lanes + sb * TN;
-                if (!wait(b_s + 8 * sb, sph, abort, W_S)) goto done;
-                tc_fence_after();
+                const int e0 = tile * TN;
+                auto sees = [&](int k) {                       // which of the tile's k-th 32 entries this row sees
+                    const int a = min(max(see.lo - e0 - 32 * k, 0), 32), z = min(max(see.hi - e0 - 32 * k, 0), 32);
+                    const uint32_t from = a == 32 ? 0u : 0xffffffffu << a, to = z == 32 ? 0xffffffffu : (1u << z) - 1u;
+                    uint32_t nodes = 0;
+                    if (p.tree) {
+                        const int d = e0 + 32 * k - u.ctx;     // node of the word's first entry
+                        if (d >= 0 && d < 64) nodes = (uint32_t)(word >> d);
+                        else if (d < 0 && d > -32) nodes = (uint32_t)(word << -d);
+                    }
+                    return from & (to | nodes);
+                };
                 // In a tile that some row of the unit sees in part only, entries of V that are not finite are taken as 0
                 // (0 times them would be NaN in rows that do not see them) and noted: a row that sees one is not finite.
                 // The halves both look, whoever comes first: a value is noted before it is taken away.
@@ -476,67 +683,49 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     if (lane == 0) mbar_arrive(b_scan + 8 * half);
                     if (!wait(b_scan + 8 * half, scans & 1, abort, W_SCAN)) goto done;
                     ++scans;
+#pragma unroll 1
+                    for (int k = 0; k < TN / 32; ++k) poison |= (*(volatile uint32_t *)&s_bad[vslot][k] & sees(k)) != 0;
                 }
+                if (!wait(b_s + 8 * sb, sph, abort, W_S)) goto done;
+                tc_fence_after();
                 if (any) {
+                    // Scores that need more than the plain softmax are worked over where they lie, 32 at a time: few tiles
+                    // (or all, with a cap or a bias), and unrolled beside the rest the code would not stay in its cache.
+                    const bool cut = e0 < max_lo || e0 + TN > min_hi;
+                    if (general || cut) {
+#pragma unroll 1
+                        for (int k = 0; k < TN; k += 32) {
+                            uint32_t y[32];
+                            tmem_ld32(s_col + k, y);
+                            tmem_ld_wait(y);
+                            if (p.cap_out != 0.f) cap32(s_col + k, y, p.cap_in, p.cap_out);
+                            else if (general)
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * p.scale_log2);
+                            if (p.slopes) {
+                                const float bias = slope * (float)(e0 + k - u.ctx - t);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) + fmaf(slope, (float)j, bias));
+                            }
+                            if (cut) {
+                                const uint32_t bits = sees(k / 32);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (!(bits >> j & 1u)) y[j] = 0xff800000u;
+                            }
+                            tmem_st32(s_col + k, y);
+                        }
+                        tmem_st_wait();
+                    }
                     uint32_t x[TN];
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    auto largest = [&](int k) {
+                    tmem_ld(s_col, x);
+#pragma unroll
+                    for (int k = 0; k < TN; k += 32) {
+                        tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
 #pragma unroll
                         for (int j = k; j < k + 32; j += 2)
                             top[j / 2 & 3] = max3(top[j / 2 & 3], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-                    };
-                    const bool cut = tile * TN < max_lo || (tile + 1) * TN > min_hi;
-                    const bool plain = !general && !cut;
-                    tmem_ld32(s_col, reinterpret_cast<uint32_t(&)[32]>(x[0]));
-#pragma unroll
-                    for (int k = 0; k < TN; k += 32) {         // a piece's maximum while the next one is on the way
-                        tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
-                        if (k + 32 < TN) tmem_ld32(s_col + k + 32, reinterpret_cast<uint32_t(&)[32]>(x[(k + 32) % TN]));
-                        if (plain) largest(k);
-                    }
-                    const int e0 = tile * TN;
-                    if (general) {
-                        const float bias = slope * (float)(e0 - u.ctx - t);
-                        if (p.cap_out != 0.f) {
-                            // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
-#pragma unroll
-                            for (int k = 0; k < TN; ++k) {
-                                const float e = pow2(__uint_as_float(x[k]) * p.cap_in);
-                                const float y = fmaf(-2.f * p.cap_out, rcp(1.f + e), p.cap_out);
-                                x[k] = __float_as_uint(y + fmaf(slope, (float)k, bias));
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < TN; ++k)
-                                x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), p.scale_log2, fmaf(slope, (float)k, bias)));
-                        }
-                    }
-                    uint32_t bits[TN / 32];                    // what the row sees of the tile
-                    if (cut) {
-#pragma unroll
-                        for (int k = 0; k < TN / 32; ++k) {
-                            const int a = min(max(see.lo - e0 - 32 * k, 0), 32), z = min(max(see.hi - e0 - 32 * k, 0), 32);
-                            const uint32_t from = a == 32 ? 0u : 0xffffffffu << a, to = z == 32 ? 0xffffffffu : (1u << z) - 1u;
-                            bits[k] = from & to;
-                            if (p.tree) {
-                                const int d = e0 + 32 * k - u.ctx;          // node of the word's first entry
-                                uint32_t nodes = 0;
-                                if (d >= 0 && d < 64) nodes = (uint32_t)(word >> d);
-                                else if (d < 0 && d > -32) nodes = (uint32_t)(word << -d);
-                                bits[k] |= nodes & from;
-                            }
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!(bits[k] >> j & 1u)) x[32 * k + j] = 0xff800000u;
-                        }
-                    }
-                    if (scan) {                                // found below, before P is announced
-#pragma unroll
-                        for (int k = 0; k < TN / 32; ++k) poison |= (*(volatile uint32_t *)&s_bad[vslot][k] & (cut ? bits[k] : 0xffffffffu)) != 0;
-                    }
-                    if (!plain) {
-#pragma unroll
-                        for (int k = 0; k < TN; k += 32) largest(k);
                     }
                     const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     const bool raise = mx > m && !((mx - m) * c <= kLazy);
@@ -548,49 +737,53 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                             m = mx;
                             l *= f;
                         }
+                        any_large = __any_sync(0xffffffffu, m != -INFINITY && !(fabsf(m * c) < 4096.f));
                         if (tile != u.t0) {
                             if (NQ == 1) {                     // the last product may still be adding
                                 if (!wait(b_pv, (g - 1) & 1, abort, W_PV)) goto done;
                                 tc_fence_after();
                             }
-                            for (int d = 0; d < dcols; d += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(o_col + d, o);
-                                tmem_ld_wait16(o);
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                                tmem_st16(o_col + d, o);
-                            }
+#pragma unroll 1
+                            for (int d = 0; d < dcols; d += 8) scale8(o_col + d, f);
                         }
                     }
                     const float mc = m == -INFINITY ? 0.f : m * c;
                     uint64_t sum[2] = {0, 0};
-                    const float off = kLift<T> - mc;           // m c is rounded once, the same wherever it is used
-                    const bool large = !(fabsf(mc) < 4096.f), any_large = __any_sync(0xffffffffu, large);
-                    const float ms = m == -INFINITY ? 0.f : m;
-                    const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+                    float by = c, off = kLift<T> - mc;         // m c is rounded once, the same wherever it is used
+                    if (any_large) {                           // m is taken off first in rows of such scores, and in these alone
+                        const bool large = !(fabsf(mc) < 4096.f);
+                        const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+                        for (int k = 0; k < TN; k += 32) {
+                            uint32_t y[32];
+                            tmem_ld32(s_col + k, y);
+                            tmem_ld_wait(y);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float s = __uint_as_float(y[j]);
+                                y[j] = __float_as_uint(large ? fmaf(s - ms, c, kLift<T>) : fmaf(s, c, off));
+                            }
+                            tmem_st32(s_col + k, y);
+                        }
+                        tmem_st_wait();
+                        tmem_ld(s_col, x);
+#pragma unroll
+                        for (int k = 0; k < TN; k += 32) tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
+                        by = 1.f;
+                        off = 0.f;
+                    }
+                    const uint64_t by2 = pair(by, by), off2 = pair(off, off);
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
                         constexpr int W = TN / PARTS;
-                        if (!any_large) {
 #pragma unroll
-                            for (int k = part * W; k < (part + 1) * W; k += 2) {
-                                float a, b;
-                                unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, off2), a, b);
-                                a = pow2(a);
-                                b = pow2(b);
-                                sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(a, b));
-                                x[k / 2] = pack2<T>(a, b);
-                            }
-                        } else {                               // m is taken off first in rows of such scores, and in these alone
-#pragma unroll
-                            for (int k = part * W; k < (part + 1) * W; k += 2) {
-                                const float u0 = __uint_as_float(x[k]), u1 = __uint_as_float(x[k + 1]);
-                                const float a = pow2(large ? fmaf(u0 - ms, c, kLift<T>) : fmaf(u0, c, off));
-                                const float b = pow2(large ? fmaf(u1 - ms, c, kLift<T>) : fmaf(u1, c, off));
-                                sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(a, b));
-                                x[k / 2] = pack2<T>(a, b);
-                            }
+                        for (int k = part * W; k < (part + 1) * W; k += 2) {
+                            float a, b;
+                            unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), by2, off2), a, b);
+                            a = pow2(a);
+                            b = pow2(b);
+                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(a, b));
+                            x[k / 2] = pack2<T>(a, b);
                         }
 #pragma unroll
                         for (int k = part * W / 2; k < (part + 1) * W / 2; k += 16)
@@ -631,30 +824,33 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             const float f = !whole ? 1.f : l > 0.f ? 1.f / l : l;   // a NaN stays one
             const bool sums = some && !(l == 0.f);
             if (__any_sync(0xffffffffu, r < p.rows)) {
-                for (int d = 0; d < p.c.dim; d += 16) {
-                    uint32_t o[16];
+#pragma unroll 1
+                for (int d = 0; d < p.c.dim; d += 64) {
+                    uint32_t o[64];                            // the columns past the last are there, whatever they hold
                     if (some) {
-                        tmem_ld16(o_col + d, o);
-                        tmem_ld_wait16(o);
+                        tmem_ld(o_col + d, o);
+                        tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(o[0]));
+                        tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(o[32]));
                     }
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) o[k] = sums ? __float_as_uint(__uint_as_float(o[k]) * f) : 0u;
                     if (r < p.rows) {
+                        if (!whole || p.out_f32) {
+                            float *dst = whole ? static_cast<float *>(p.out) + row * p.c.dim : p.part + (part * p.part_rows + in_part) * p.c.dim;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = sums ? __float_as_uint(__uint_as_float(o[k]) * f) : 0u;
+                            for (int e = 0; e < 64; e += 8)
+                                if (d + e < p.c.dim) store32(dst + d + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7], whole ? p.out_wide : p.part_wide);
+                        } else {
+                            T *dst = static_cast<T *>(p.out) + row * p.c.dim;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 8) {
-                            if (d + e >= p.c.dim) break;
-                            if (!whole || p.out_f32) {
-                                float *dst = whole ? static_cast<float *>(p.out) + row * p.c.dim + d + e
-                                                   : p.part + (part * p.part_rows + in_part) * p.c.dim + d + e;
-                                *reinterpret_cast<uint4 *>(dst) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                                *reinterpret_cast<uint4 *>(dst + 4) = make_uint4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
-                            } else {
-                                uint32_t h[4];
+                            for (int k = 0; k < 32; ++k) o[k] = pack2<T>(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    h[k] = pack2<T>(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
-                                *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * p.c.dim + d + e) =
-                                    make_uint4(h[0], h[1], h[2], h[3]);
+                            for (int e = 0; e < 64; e += 16) {
+                                const int k = e / 2;
+                                if (d + e + 8 < p.c.dim)
+                                    store32(dst + d + e, o[k], o[k + 1], o[k + 2], o[k + 3], o[k + 4], o[k + 5], o[k + 6], o[k + 7], p.out_wide);
+                                else if (d + e < p.c.dim)
+                                    *reinterpret_cast<uint4 *>(dst + d + e) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                             }
                         }
                     }
@@ -671,7 +867,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
         if (join.x >= 0 && warp == 0 && lane == 0) p.joins[blockIdx.x] = join;
     } else if (warp < SOFT + 2) {
         // ------------------------------------------------------------------ one thread per half issues its products
-        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         constexpr uint32_t kIdS = idesc<T>(TN, false);
         const uint32_t id_o = idesc<T>(p.ksteps * 16, true);
         const int i = warp - SOFT;                             // the half; with one half the second warp has nothing to do
@@ -743,7 +939,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             return true;
         };
         if (i < NQ) {
-            for (bool first = true; w.next(first); first = false) {
+            for (bool first = true; w.next(p, first, abort); first = false) {
                 const int nt = w.u.t1 - w.u.t0;
                 if (nt > 0 && !run(nt)) break;
             }
@@ -754,7 +950,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
         }
     } else {
         // ------------------------------------------------------------------ loaders
-        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int lw = warp - SOFT - 2;
         const int pieces = p.ksteps * 2;                       // 16-byte pieces of a row, past `dim` zeros
         const int step_row = 32 / pieces, step_piece = 32 - step_row * pieces;
@@ -891,15 +1087,18 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             return true;
         };
         bool ok = true;
-        for (bool first = true; ok && w.next(first); first = false)
+        for (bool first = true; ok && w.next(p, first, abort); first = false) {
             if (w.u.t0 < w.u.t1) ok = run(w.u);
+            flush();                                           // before a wait for warps that may wait for these copies
+        }
         flush();
-        if (!ok && (p.box || p.q_box)) {                                // a wait ran out: the copies under way still come to their end
+        if (!ok || *abort) {                                // a wait ran out: the copies under way still come to their end
             uint32_t never = 0;
             for (int i = 0; i < p.slots; ++i) {
                 const int before = i < slot ? phase : phase ^ 1;       // of the slot's last copy; none: over already
                 if (lane == 0 && p.box) mbar_wait(b_full + 8 * i, (uint32_t)before, &never, KID_PREFILL, W_DRAIN);
             }
+            if (lane == 0 && lw == 0 && p.whole) mbar_wait(b_next + 8 * (w.asked & 1), (uint32_t)(w.asked >> 1) & 1u, &never, KID_PREFILL, W_DRAIN);
             if (lane == 0 && p.q_box) mbar_wait(b_qfull, (uint32_t)(runs & 1), &never, KID_PREFILL, W_DRAIN);
             __syncwarp();
         }
@@ -1123,6 +1322,7 @@ int attend(const mmq_kv_cache *cache, const Call &a, mmq_stream_t stream)
         p.cap_out = a.cap * 1.44269504088896341f;
     }
     p.out_f32 = a.out_dtype == MMQ_F32;
+    p.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && (p.out_f32 || cache->dim % 16 == 0);
     p.window = a.window;
     p.new_tokens = a.new_tokens;
     p.group = a.q_heads / cache->heads;
@@ -1135,6 +1335,7 @@ int attend(const mmq_kv_cache *cache, const Call &a, mmq_stream_t stream)
     p.ksteps = q.ksteps;
     p.slots = q.slots;
     p.part = a.work;
+    p.part_wide = (reinterpret_cast<uintptr_t>(a.work) & 31) == 0;
     p.part_ml = reinterpret_cast<float2 *>(a.work + 2ll * q.grid * q.part_rows * cache->dim);
     p.joins = reinterpret_cast<int2 *>(p.part_ml + 2ll * q.grid * q.part_rows);
     p.page_div = FastDiv(cache->page_size);

@@ -626,3 +626,25 @@ def test_prompt_in_chunks_then_trees(ops, dtype):
     last = [ops.attn_prefill(c, step(c, [total + 9], [total + 4]), cap=cap) for c in (once, chain)]
     ops.check_status()
     assert torch.equal(*last)
+
+
+def test_capped_scores_that_are_not_finite(ops):
+    """A K entry that is NaN or infinite under a cap: NaN makes the rows that see it NaN and leaves the others, also where
+    they share everything but that entry; an infinite score counts as the cap."""
+    lens, N, dim = [300], 200, 64
+    for bad in (float("nan"), float("inf")):
+        cache = make_cache(ops, lens, 1, dim, 16, BF16)
+        q = queries(cache, lens, N, 1)
+        q[:, :, 0] = 1.0
+        want = ops.attn_prefill(cache, q.cuda(), cap=10.0)
+        pg, off = serve_ref.slot_place(cache.table.cpu(), 16, 0, 250)
+        cache.k[pg, 0, off, 0] = bad
+        got = ops.attn_prefill(cache, q.cuda(), cap=10.0)
+        ops.check_status()
+        assert torch.equal(got[:150], want[:150])
+        if bad != bad:
+            assert bool(torch.isnan(got[150:]).all())
+        else:
+            cache.k[pg, 0, off, 0] = 3e4                     # as good as infinite: tanh is 1 either way
+            cache.k[pg, 0, off, 1:] = 0
+            assert torch.equal(got, ops.attn_prefill(cache, q.cuda(), cap=10.0))
