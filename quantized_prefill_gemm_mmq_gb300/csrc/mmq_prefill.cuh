@@ -37,9 +37,9 @@ constexpr int LOADERS = 2;            // warps
 constexpr int PARTS = 2;              // of a tile's P, each announced by itself
 constexpr int LAG = 2;                // copies a loader has under way before it waits for the oldest
 constexpr int MAX_SLOTS = 12;
-constexpr uint32_t SMEM = 230400;     // dynamic, with slack for alignment
+constexpr uint32_t SMEM = 232448;     // all of it dynamic
 
-enum { W_Q = 1, W_K, W_V, W_P, W_S, W_EMPTY, W_QEMPTY, W_PV, W_TURN, W_SCAN, W_NEXT, W_DRAIN };     // sites of waits
+enum { W_Q = 1, W_K, W_V, W_P, W_S, W_EMPTY, W_QEMPTY, W_PV, W_TURN, W_SCAN, W_NEXT, W_RUN, W_DRAIN };     // sites of waits
 
 // By whole warps; the lanes may wait for different barriers: a wait for one that is over already takes some 200 cycles while
 // the tensor core reads shared memory, so several are better waited for in one go.
@@ -142,26 +142,7 @@ __device__ __forceinline__ float rcp(float x)
     return y;
 }
 
-// 64 columns of the warp's 32 lanes, to be used after tmem_ld_wait on each 32 of them: one load takes as long as its columns,
-// four of 32 columns one after the other a wait each
-__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[64])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-                 "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-                   "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-                   "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-                   "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-                   "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-                 : "r"(at)
-                 : "memory");
-}
+// Columns of the warp's 32 lanes, to be used after tmem_ld_wait on each 32 of them.
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[128])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
@@ -189,6 +170,24 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[128])
                    "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
                    "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
                    "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[64])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+                 "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+                   "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+                   "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+                   "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+                   "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
                  : "r"(at)
                  : "memory");
 }
@@ -221,6 +220,13 @@ __device__ __forceinline__ void cap32(uint32_t at, uint32_t (&y)[32], float cap_
     }
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // eight columns of the warp's lanes times f
 __device__ __forceinline__ void scale8(uint32_t at, float f)
 {
@@ -231,9 +237,7 @@ __device__ __forceinline__ void scale8(uint32_t at, float f)
                  : "memory");
 #pragma unroll
     for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f);
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+    tmem_st8(at, r);
 }
 
 // 32 bytes to where 16 or (wide) 32 bytes are aligned: a whole sector by one thread
@@ -373,9 +377,8 @@ __device__ __forceinline__ void prefill_bounds(const PrefillParams &p, PrefillUn
     if (lo >= hi || u.t0 >= u.t1) u.t0 = u.t1 = 0;
 }
 
-// Runs of tiles that a CTA takes, one unit (or part of one) after the other.  Every warp walks them by itself, in shared
-// memory, since registers are short while tiles are worked on; a step is made in registers.  Units are
-// numbered (sequence, rows, head): the heads of one (sequence, rows) pair have the same span of tiles.
+// Runs of tiles that a CTA takes, one unit (or part of one) after the other; one loader warp finds them and tells the other
+// warps.  Units are numbered (sequence, rows, head): the heads of one (sequence, rows) pair have the same span of tiles.
 template <int RT, int TN>
 struct PrefillWalk {
     PrefillUnit u;
@@ -386,23 +389,9 @@ struct PrefillWalk {
     int total, grid;           // split: tiles of all units, CTAs that have some
     int place;                 // split: tiles of all units up to the run's end
     int rest;                  // tiles of the unit after the run
-    // whole: a CTA that is done takes over the next unit whose CTA has not started; one loader asks when
-    // its copies for the unit are on their way (asked a unit ahead, units that take longest last wait for busy CTAs)
-    uint32_t answers, b_next;               // two answers of 16 bytes; their barriers: come (2), read by every warp (2)
-    int asked;                              // answers taken
-    bool asks;
+    int asked;                 // whole: units taken over
 
     __device__ __forceinline__ static int count(int2 s) { return max(1, s.y - s.x); }        // an empty unit still has outputs
-
-    __device__ __forceinline__ void start(const PrefillParams &p, uint32_t answers_, uint32_t b_next_, bool asks_)
-    {
-        answers = answers_;
-        b_next = b_next_;
-        asked = 0;
-        asks = asks_;
-        at = place = 0;
-        if (!p.whole) split(p);
-    }
 
     __device__ __forceinline__ void split(const PrefillParams &p)
     {
@@ -415,6 +404,7 @@ struct PrefillWalk {
             prefill_sequence(p, w);
             return count(prefill_span<RT, TN>(p, w));
         };
+        at = place = 0;
         int W = 0;
         for (int i = lane; i < pairs; i += 32) W += tiles_of(i);
         total = W = __reduce_add_sync(0xffffffffu, W) * p.c.heads;
@@ -448,43 +438,9 @@ struct PrefillWalk {
         span = prefill_span<RT, TN>(p, u);
     }
 
-    // The next run, false when there is none.
-    __device__ __forceinline__ bool step(const PrefillParams &p, bool first, volatile uint32_t *abort)
+    // The next run of a CTA with an equal share of all tiles, false when there is none.
+    __device__ __forceinline__ bool next_split(const PrefillParams &p, bool first)
     {
-        if (p.whole) {
-            const uint32_t b_taken = b_next + 16;
-            const int lane = threadIdx.x & 31;
-            int id = (int)blockIdx.x;
-            if (!first) {
-                const int buf = asked & 1, round = (asked >> 1) & 1;
-                if (asks) {
-                    if (!pre::wait(b_taken + 8 * buf, round ^ 1, abort, pre::W_NEXT)) return false;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(b_next + 8 * buf, 16);
-                        pre::ask_next(answers + 16 * buf, b_next + 8 * buf);
-                    }
-                    __syncwarp();
-                }
-                if (!pre::wait(b_next + 8 * buf, round, abort, pre::W_NEXT)) return false;
-                id = pre::answer(answers + 16 * buf);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_taken + 8 * buf);
-                ++asked;
-                if (id < 0) return false;
-            }
-            const int per = p.c.seqs * p.c.heads, back = id / per, bh = id - back * per;
-            u.rt = p.row_tiles - 1 - back;                    // the longest first
-            u.b = bh / p.c.heads;
-            u.h = bh - u.b * p.c.heads;
-            prefill_sequence(p, u);
-            span = prefill_span<RT, TN>(p, u);
-            begins = ends = true;
-            u.t0 = span.x;
-            u.t1 = span.y;
-            prefill_bounds<RT, TN>(p, u);
-            return true;
-        }
         if (left <= 0) return false;
         if (!first) {
             at = 0;
@@ -510,30 +466,68 @@ struct PrefillWalk {
         return true;
     }
 
-    // The same for a walk in shared memory.
-    __device__ __forceinline__ void keep(PrefillWalk &at_) const
+    // The next whole unit: the CTA's own, then those whose CTAs have not started.  It asks when its copies for the unit
+    // before are on their way: asked a unit ahead, long units wait for busy CTAs.  -1: none left, -2: a wait ran out.
+    __device__ __forceinline__ int next_whole(const PrefillParams &p, bool first, uint32_t answer_at, uint32_t bar, volatile uint32_t *abort)
     {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) at_ = *this;
-        __syncwarp();
+        int id = (int)blockIdx.x;
+        if (!first) {
+            if ((threadIdx.x & 31) == 0) {
+                mbar_arrive_expect_tx(bar, 16);
+                pre::ask_next(answer_at, bar);
+            }
+            __syncwarp();
+            if (!pre::wait(bar, asked & 1, abort, pre::W_NEXT)) return -2;
+            id = pre::answer(answer_at);
+            fence_proxy_async_smem();
+            __syncwarp();
+            ++asked;
+            if (id < 0) return -1;
+        }
+        const int per = p.c.seqs * p.c.heads, back = id / per, bh = id - back * per;
+        u.rt = p.row_tiles - 1 - back;                        // the longest first
+        u.b = bh / p.c.heads;
+        u.h = bh - u.b * p.c.heads;
+        prefill_sequence(p, u);
+        span = prefill_span<RT, TN>(p, u);
+        begins = ends = true;
+        u.t0 = span.x;
+        u.t1 = span.y;
+        prefill_bounds<RT, TN>(p, u);
+        return 0;
     }
-    __device__ __forceinline__ bool next(const PrefillParams &p, bool first, volatile uint32_t *abort)
-    {
-        PrefillWalk w = *this;
-        const bool more = w.step(p, first, abort);
-        w.keep(*this);
-        return more;
-    }
+};
+
+// What the warps of a CTA are told of a run.
+struct PrefillRun {
+    PrefillUnit u;
+    int flags;                 // 1: has the unit's first tile, 2: its last, 4: there is none any more
 };
 
 template <typename T, int NQ, int TN>
 struct PrefillShape {
     static constexpr int RT = 128 * NQ;
-    static constexpr int kThreads = (4 * NQ + 4) * 32;         // softmax, two issuing and two loading warps
+    static constexpr int SOFT = 4 * NQ;                        // softmax warps; then two issuing and two loading ones
+    static constexpr int kThreads = (SOFT + 4) * 32;
     static constexpr int kBuf = 2;                             // S buffers: one per half, or two for the only half
     static constexpr int kO = kBuf * TN;                       // tensor-memory column of the sums
     static constexpr int kOPitch = (512 - kO) / NQ;
     static constexpr int kMaxDim = kOPitch < 256 ? kOPitch / 64 * 64 : 256;
+};
+
+// Shared memory behind the tiles.
+template <int NQ, int TN>
+struct PrefillShared {
+    static constexpr int RUNS = 3;
+    uint64_t q_full, q_empty, drain[2];
+    uint64_t full[pre::MAX_SLOTS], empty[pre::MAX_SLOTS];
+    uint64_t s[2], pv[2], turn[2], scan[2], p[2 * pre::PARTS];          // p [S buffer][part of P]
+    uint64_t run_full[RUNS], run_empty[RUNS], next;
+    uint64_t pad;
+    uint4 answer;
+    PrefillRun run[RUNS];
+    uint32_t bad[pre::MAX_SLOTS][TN / 32];                     // entries of a V tile that were not finite and are taken as 0
+    uint32_t tmem, abort;
 };
 
 template <typename T, int NQ, int TN>
@@ -541,81 +535,77 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 {
     using namespace pre;
     using S = PrefillShape<T, NQ, TN>;
-    constexpr int RT = S::RT, SOFT = 4 * NQ;                   // softmax warps; then two issuing ones, then the loaders
-    extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t s_bar[4 + 2 * MAX_SLOTS + 4 * 2 + 2 * PARTS + 4];
-    __shared__ __align__(16) uint4 s_answers[2];
-    __shared__ PrefillWalk<RT, TN> s_walk[SOFT + 4];
-    __shared__ uint32_t s_tmem, s_abort;
-    __shared__ uint32_t s_bad[MAX_SLOTS][TN / 32];             // entries of a V tile that were not finite and are taken as 0
-    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    using Shared = PrefillShared<NQ, TN>;
+    constexpr int RT = S::RT, SOFT = S::SOFT;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    const uint32_t base = smem_u32(raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile uint32_t *abort = &s_abort;
-
     const uint32_t q_bytes = (uint32_t)p.chunks * (128 * 128), slot_bytes = (uint32_t)p.chunks * (TN * 128);
     const uint32_t ring = base + NQ * q_bytes;
-    const uint32_t bar0 = smem_u32(s_bar);
-    const uint32_t b_qfull = bar0, b_qempty = bar0 + 8, b_drain = bar0 + 16;       // b_drain: one per issuing warp
-    const uint32_t b_full = bar0 + 32, b_empty = b_full + 8 * MAX_SLOTS;
-    const uint32_t b_s = b_empty + 8 * MAX_SLOTS, b_pv = b_s + 16, b_turn = b_pv + 16, b_scan = b_turn + 16;
-    const uint32_t b_p = b_scan + 16;                          // [S buffer][part of P]
-    const uint32_t b_next = b_p + 16 * PARTS;                  // two, and two that their answers are read
+    Shared &sh = *reinterpret_cast<Shared *>(raw + NQ * q_bytes + p.slots * slot_bytes);
+    volatile uint32_t *abort = &sh.abort;
+    auto bar = [&](uint64_t &b) { return smem_u32(&b); };
 
     if (threadIdx.x == 0) {
-        s_abort = 0;
-        mbar_init(b_qfull, LOADERS);
-        mbar_init(b_qempty, NQ);
+        sh.abort = 0;
+        mbar_init(bar(sh.q_full), LOADERS);
+        mbar_init(bar(sh.q_empty), NQ);
         for (int i = 0; i < MAX_SLOTS; ++i) {
-            mbar_init(b_full + 8 * i, LOADERS);
-            mbar_init(b_empty + 8 * i, NQ);
+            mbar_init(bar(sh.full[i]), LOADERS);
+            mbar_init(bar(sh.empty[i]), NQ);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(b_drain + 8 * i, 1);
-            mbar_init(b_s + 8 * i, 1);
-            mbar_init(b_pv + 8 * i, 1);
-            mbar_init(b_turn + 8 * i, 1);
-            mbar_init(b_scan + 8 * i, 4);
-            mbar_init(b_next + 8 * i, 1);
-            mbar_init(b_next + 16 + 8 * i, SOFT + NQ + LOADERS);
-            for (int k = 0; k < PARTS; ++k) mbar_init(b_p + 8 * (i * PARTS + k), 4);
+            mbar_init(bar(sh.drain[i]), 1);
+            mbar_init(bar(sh.s[i]), 1);
+            mbar_init(bar(sh.pv[i]), 1);
+            mbar_init(bar(sh.turn[i]), 1);
+            mbar_init(bar(sh.scan[i]), 4);
+            for (int k = 0; k < PARTS; ++k) mbar_init(bar(sh.p[i * PARTS + k]), 4);
         }
+        for (int i = 0; i < Shared::RUNS; ++i) {
+            mbar_init(bar(sh.run_full[i]), 1);
+            mbar_init(bar(sh.run_empty[i]), SOFT + NQ + 1);
+        }
+        mbar_init(bar(sh.next), 1);
         fence_mbar_init();
     }
     // Tensor memory is taken after the launch before has ended: its blocks may still have to take theirs.
     pdl_wait();
     if (warp == SOFT) {
-        tmem_alloc(smem_u32(&s_tmem), 512);
+        tmem_alloc(smem_u32(&sh.tmem), 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();
-    const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
-    if (!p.whole && warp == 0 && lane == 0) p.joins[blockIdx.x] = make_int2(-1, 0);          // also if a wait runs out
+    const uint32_t tmem = *(volatile uint32_t *)&sh.tmem;
 
-    PrefillWalk<RT, TN> &w = s_walk[warp];
-    {
-        PrefillWalk<RT, TN> begin;
-        begin.start(p, smem_u32(s_answers), b_next, warp == SOFT + 2);
-        begin.keep(w);
-    }
+    // The next run, as told; false at the end, or when a wait ran out.
+    int run_at = 0, run_phase = 0;
+    auto hear = [&](PrefillRun &r) {
+        if (!wait(bar(sh.run_full[run_at]), run_phase, abort, W_RUN)) return false;
+        r = sh.run[run_at];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.run_empty[run_at]));
+        if (++run_at == Shared::RUNS) run_at = 0, run_phase ^= 1;
+        return (r.flags & 4) == 0;
+    };
 
-    // With 256 rows the softmax warps need more registers than an equal share (168): 2 * 216 + 72 = 3 * 168.
     if (warp < SOFT) {
         // ------------------------------------------------------------------ softmax: one row per thread
+        // With 256 rows these warps need more registers than an equal share (168): 2 * 216 + 72 = 3 * 168.
         if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int half = warp >> 2, quarter = warp & 3;
+        const int half = warp >> 2, quarter = warp & 3, in_half = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t o_col = tmem + lanes + S::kO + half * S::kOPitch;
-        const int dcols = p.ksteps * 16;
         const bool general = p.cap_out != 0.f || p.slopes || !(p.scale_log2 > 0.f);
         const float c = general ? 1.f : p.scale_log2;
         int g = 0, runs = 0, scans = 0, vslot = 1, vphase = 0;
-        int2 join = make_int2(-1, 0);
-        for (bool first = true; w.next(p, first, abort); first = false) {
-            const PrefillUnit &u = w.u;
-            const int r = u.rt * RT + half * 128 + quarter * 32 + lane;
+        PrefillRun run;
+        while (hear(run)) {
+            const PrefillUnit &u = run.u;
+            const int r = u.rt * RT + half * 128 + in_half;
             const int t = p.group_div.of(min(r, p.rows - 1));
             const bool live = r < p.rows && t < u.n;
             const int head = u.h * p.group + (min(r, p.rows - 1) - t * p.group);
@@ -632,19 +622,19 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             const int max_lo = __reduce_max_sync(0xffffffffu, live ? see.lo : 0);
             const int min_hi = __reduce_min_sync(0xffffffffu, live ? see.hi : 0x7fffffff);
             const float slope = p.slopes && live ? p.slopes[head] * 1.44269504088896341f : 0.f;
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, off = kLift<T>;      // off: kLift - m c
             bool poison = false, any_large = false;            // any_large: of the warp, see below
 
             for (int tile = u.t0; tile < u.t1; ++tile, ++g) {
                 const int sb = NQ == 2 ? half : g & 1, sph = NQ == 2 ? g & 1 : (g >> 1) & 1;
                 const uint32_t s_col = tmem + lanes + sb * TN;
                 const int e0 = tile * TN;
-                auto sees = [&](int k) {                       // which of the tile's k-th 32 entries this row sees
-                    const int a = min(max(see.lo - e0 - 32 * k, 0), 32), z = min(max(see.hi - e0 - 32 * k, 0), 32);
+                auto sees = [&](int k) {                       // which of the tile's 32 entries from the k-th on this row sees
+                    const int a = min(max(see.lo - e0 - k, 0), 32), z = min(max(see.hi - e0 - k, 0), 32);
                     const uint32_t from = a == 32 ? 0u : 0xffffffffu << a, to = z == 32 ? 0xffffffffu : (1u << z) - 1u;
                     uint32_t nodes = 0;
                     if (p.tree) {
-                        const int d = e0 + 32 * k - u.ctx;     // node of the word's first entry
+                        const int d = e0 + k - u.ctx;          // node of the first of them
                         if (d >= 0 && d < 64) nodes = (uint32_t)(word >> d);
                         else if (d < 0 && d > -32) nodes = (uint32_t)(word << -d);
                     }
@@ -653,16 +643,16 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 // In a tile that some row of the unit sees in part only, entries of V that are not finite are taken as 0
                 // (0 times them would be NaN in rows that do not see them) and noted: a row that sees one is not finite.
                 // The halves both look, whoever comes first: a value is noted before it is taken away.
-                const bool scan = tile * TN < u.max_lo || (tile + 1) * TN > u.min_hi;
+                const bool scan = e0 < u.max_lo || e0 + TN > u.min_hi;
                 if (scan) {
-                    if (!wait(b_full + 8 * vslot, vphase, abort, W_V)) goto done;
+                    if (!wait(bar(sh.full[vslot]), vphase, abort, W_V)) goto done;
                     constexpr int PER = 128 / TN;              // threads per entry
-                    const int e = (quarter * 32 + lane) / PER;
-                    const uint32_t at = ring + vslot * slot_bytes + e * 128;
-                    auto piece = [&](int k) { return at + (k >> 3) * (TN * 128) + (((k & 7) ^ (e & 7)) << 4); };
+                    const int at = in_half, e = at / PER;
+                    const uint32_t row = ring + vslot * slot_bytes + e * 128;
+                    auto piece = [&](int k) { return row + (k >> 3) * (TN * 128) + (((k & 7) ^ (e & 7)) << 4); };
                     uint32_t acc = 0;
 #pragma unroll 4
-                    for (int k = lane % PER; k < p.c.dim / 8; k += PER) {
+                    for (int k = at % PER; k < p.c.dim / 8; k += PER) {
                         uint32_t v[4];
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(piece(k)) : "memory");
                         constexpr uint32_t one = kBf<T> ? 0x00800080u : 0x04000400u;       // on top of a full exponent: bit 15
@@ -672,87 +662,116 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     const bool bad = (acc & 0x80008000u) != 0;
                     if (__any_sync(0xffffffffu, bad)) {
                         if (bad) {
-                            atomicOr(&s_bad[vslot][e >> 5], 1u << (e & 31));
+                            atomicOr(&sh.bad[vslot][e >> 5], 1u << (e & 31));
                             __threadfence_block();
-                            for (int k = lane % PER; k < p.c.dim / 8; k += PER)
+                            for (int k = at % PER; k < p.c.dim / 8; k += PER)
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(piece(k)), "r"(0u) : "memory");
                             fence_proxy_async_smem();
                         }
                         __syncwarp();
                     }
-                    if (lane == 0) mbar_arrive(b_scan + 8 * half);
-                    if (!wait(b_scan + 8 * half, scans & 1, abort, W_SCAN)) goto done;
+                    if (lane == 0) mbar_arrive(bar(sh.scan[half]));
+                    if (!wait(bar(sh.scan[half]), scans & 1, abort, W_SCAN)) goto done;
                     ++scans;
 #pragma unroll 1
-                    for (int k = 0; k < TN / 32; ++k) poison |= (*(volatile uint32_t *)&s_bad[vslot][k] & sees(k)) != 0;
+                    for (int k = 0; k < TN; k += 32) poison |= (*(volatile uint32_t *)&sh.bad[vslot][k / 32] & sees(k)) != 0;
                 }
-                if (!wait(b_s + 8 * sb, sph, abort, W_S)) goto done;
+                vslot += 2;
+                if (vslot >= p.slots) {
+                    vslot -= p.slots;
+                    vphase ^= 1;
+                }
+                if (!wait(bar(sh.s[sb]), sph, abort, W_S)) goto done;
                 tc_fence_after();
-                if (any) {
-                    // Scores that need more than the plain softmax are worked over where they lie, 32 at a time: few tiles
-                    // (or all, with a cap or a bias), and unrolled beside the rest the code would not stay in its cache.
-                    const bool cut = e0 < max_lo || e0 + TN > min_hi;
-                    if (general || cut) {
+                if (!any) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane < PARTS) mbar_arrive(bar(sh.p[sb * PARTS + lane]));
+                    continue;
+                }
+                // Scores that need more than the plain softmax are worked over where they lie, 32 at a time: few tiles (or all,
+                // with a cap or a bias), and unrolled beside the rest the code would not stay in its cache.
+                const bool cut = e0 < max_lo || e0 + TN > min_hi;
+                if (general || cut) {
 #pragma unroll 1
-                        for (int k = 0; k < TN; k += 32) {
-                            uint32_t y[32];
-                            tmem_ld32(s_col + k, y);
-                            tmem_ld_wait(y);
-                            if (p.cap_out != 0.f) cap32(s_col + k, y, p.cap_in, p.cap_out);
-                            else if (general)
+                    for (int k = 0; k < TN; k += 32) {
+                        uint32_t y[32];
+                        tmem_ld32(s_col + k, y);
+                        tmem_ld_wait(y);
+                        if (p.cap_out != 0.f) cap32(s_col + k, y, p.cap_in, p.cap_out);
+                        else if (general)
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * p.scale_log2);
-                            if (p.slopes) {
-                                const float bias = slope * (float)(e0 + k - u.ctx - t);
+                            for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * p.scale_log2);
+                        if (p.slopes) {
+                            const float bias = slope * (float)(e0 + k - u.ctx - t);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) + fmaf(slope, (float)j, bias));
-                            }
-                            if (cut) {
-                                const uint32_t bits = sees(k / 32);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if (!(bits >> j & 1u)) y[j] = 0xff800000u;
-                            }
-                            tmem_st32(s_col + k, y);
+                            for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) + fmaf(slope, (float)j, bias));
                         }
-                        tmem_st_wait();
+                        if (cut) {
+                            const uint32_t bits = sees(k);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!(bits >> j & 1u)) y[j] = 0xff800000u;
+                        }
+                        tmem_st32(s_col + k, y);
                     }
-                    uint32_t x[TN];
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tmem_st_wait();
+                }
+                // Scores are read once: the tensor core's own traffic in tensor memory goes first.  The first part's exponentials
+                // are begun with the maximum so far, while the tile's is found; where that has to be raised, which is rare, they
+                // are done again.
+                uint32_t x[TN];
+                auto load = [&]() {
                     tmem_ld(s_col, x);
 #pragma unroll
-                    for (int k = 0; k < TN; k += 32) {
-                        tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
+                    for (int k = 0; k < TN; k += 32) tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
+                };
+                uint64_t sum[2], by2, off2;
+                auto power = [&](int k0, int k1) {             // scores to P, in place of the first half of them
 #pragma unroll
-                        for (int j = k; j < k + 32; j += 2)
-                            top[j / 2 & 3] = max3(top[j / 2 & 3], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                    for (int j = k0; j < k1; j += 2) {
+                        float a, b;
+                        unpair(fma2(pair(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), by2, off2), a, b);
+                        a = pow2(a);
+                        b = pow2(b);
+                        sum[j / 2 & 1] = add2(sum[j / 2 & 1], pair(a, b));
+                        x[j / 2] = pack2<T>(a, b);
                     }
+                };
+                load();
+                by2 = pair(c, c);
+                off2 = pair(off, off);
+#pragma unroll 1
+                for (bool again = false;; again = true) {
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < TN; k += 2) top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                    sum[0] = sum[1] = 0;
+                    power(0, TN / PARTS);
                     const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     const bool raise = mx > m && !((mx - m) * c <= kLazy);
-                    if (__any_sync(0xffffffffu, raise)) {
-                        float f = 1.f;
-                        if (raise) {
-                            const bool exact = fabsf(m * c) < 4096.f && fabsf(mx * c) < 4096.f;
-                            f = pow2(exact ? __fmul_rn(m, c) - __fmul_rn(mx, c) : (m - mx) * c);
-                            m = mx;
-                            l *= f;
-                        }
-                        any_large = __any_sync(0xffffffffu, m != -INFINITY && !(fabsf(m * c) < 4096.f));
-                        if (tile != u.t0) {
-                            if (NQ == 1) {                     // the last product may still be adding
-                                if (!wait(b_pv, (g - 1) & 1, abort, W_PV)) goto done;
-                                tc_fence_after();
-                            }
-#pragma unroll 1
-                            for (int d = 0; d < dcols; d += 8) scale8(o_col + d, f);
-                        }
+                    if (again || !__any_sync(0xffffffffu, raise || any_large)) break;
+                    float f = 1.f;
+                    if (raise) {
+                        const bool exact = fabsf(m * c) < 4096.f && fabsf(mx * c) < 4096.f;
+                        f = pow2(exact ? __fmul_rn(m, c) - __fmul_rn(mx, c) : (m - mx) * c);
+                        m = mx;
+                        l *= f;
+                        off = kLift<T> - m * c;                // m c is rounded once, the same wherever it is used
                     }
-                    const float mc = m == -INFINITY ? 0.f : m * c;
-                    uint64_t sum[2] = {0, 0};
-                    float by = c, off = kLift<T> - mc;         // m c is rounded once, the same wherever it is used
+                    const bool large = m != -INFINITY && !(fabsf(m * c) < 4096.f);
+                    any_large = __any_sync(0xffffffffu, large);
+                    if (tile != u.t0 && __any_sync(0xffffffffu, raise)) {
+                        if (NQ == 1) {                         // the last product may still be adding
+                            if (!wait(bar(sh.pv[0]), (g - 1) & 1, abort, W_PV)) goto done;
+                            tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int d = 0; d < p.ksteps * 16; d += 8) scale8(o_col + d, f);
+                    }
+                    by2 = pair(c, c);
+                    off2 = pair(off, off);
                     if (any_large) {                           // m is taken off first in rows of such scores, and in these alone
-                        const bool large = !(fabsf(mc) < 4096.f);
-                        const float ms = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
                         for (int k = 0; k < TN; k += 32) {
                             uint32_t y[32];
@@ -761,94 +780,72 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 #pragma unroll
                             for (int j = 0; j < 32; ++j) {
                                 const float s = __uint_as_float(y[j]);
-                                y[j] = __float_as_uint(large ? fmaf(s - ms, c, kLift<T>) : fmaf(s, c, off));
+                                y[j] = __float_as_uint(large ? fmaf(s - m, c, kLift<T>) : fmaf(s, c, off));
                             }
                             tmem_st32(s_col + k, y);
                         }
                         tmem_st_wait();
-                        tmem_ld(s_col, x);
-#pragma unroll
-                        for (int k = 0; k < TN; k += 32) tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
-                        by = 1.f;
-                        off = 0.f;
+                        by2 = pair(1.f, 1.f);
+                        off2 = 0;
                     }
-                    const uint64_t by2 = pair(by, by), off2 = pair(off, off);
+                    load();
+                }
 #pragma unroll
-                    for (int part = 0; part < PARTS; ++part) {
-                        constexpr int W = TN / PARTS;
+                for (int part = 0; part < PARTS; ++part) {
+                    constexpr int W = TN / PARTS;
+                    if (part > 0) power(part * W, (part + 1) * W);
 #pragma unroll
-                        for (int k = part * W; k < (part + 1) * W; k += 2) {
-                            float a, b;
-                            unpair(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), by2, off2), a, b);
-                            a = pow2(a);
-                            b = pow2(b);
-                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair(a, b));
-                            x[k / 2] = pack2<T>(a, b);
-                        }
-#pragma unroll
-                        for (int k = part * W / 2; k < (part + 1) * W / 2; k += 16)
-                            tmem_st16(s_col + k, reinterpret_cast<uint32_t(&)[16]>(x[k]));
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(b_p + 8 * (sb * PARTS + part));
-                    }
-                    float la, lb;
-                    unpair(add2(sum[0], sum[1]), la, lb);
-                    l += la + lb;
-                } else {
+                    for (int k = part * W / 2; k < (part + 1) * W / 2; k += 16) tmem_st16(s_col + k, reinterpret_cast<uint32_t(&)[16]>(x[k]));
+                    tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane < PARTS) mbar_arrive(b_p + 8 * (sb * PARTS + lane));
+                    if (lane == 0) mbar_arrive(bar(sh.p[sb * PARTS + part]));
                 }
-                vslot += 2;
-                if (vslot >= p.slots) {
-                    vslot -= p.slots;
-                    vphase ^= 1;
-                }
+                float la, lb;
+                unpair(add2(sum[0], sum[1]), la, lb);
+                l += la + lb;
             }
 
             // the run's sums
             const bool some = u.t0 < u.t1;
             if (some) {
-                if (!wait(b_pv + 8 * half, NQ == 2 ? runs & 1 : (g - 1) & 1, abort, W_PV)) goto done;
+                if (!wait(bar(sh.pv[half]), NQ == 2 ? runs & 1 : (g - 1) & 1, abort, W_PV)) goto done;
                 tc_fence_after();
                 ++runs;
             }
             if (poison) l = NAN;
             if (!live) l = 0.f;
-            const bool whole = w.begins && w.ends;
+            const bool whole = (run.flags & 3) == 3;
             const int64_t row = ((int64_t)u.b * p.new_tokens + t) * p.q_heads + head;
-            const int in_part = half * 128 + quarter * 32 + lane;
-            const int64_t part = 2ll * blockIdx.x + (w.begins ? 1 : 0);
+            const int64_t part = (2ll * blockIdx.x + (run.flags & 1)) * p.part_rows + half * 128 + in_half;
             const float f = !whole ? 1.f : l > 0.f ? 1.f / l : l;   // a NaN stays one
             const bool sums = some && !(l == 0.f);
             if (__any_sync(0xffffffffu, r < p.rows)) {
+                const bool wide = whole ? p.out_wide : p.part_wide;
 #pragma unroll 1
-                for (int d = 0; d < p.c.dim; d += 64) {
-                    uint32_t o[64];                            // the columns past the last are there, whatever they hold
+                for (int d = 0; d < p.c.dim; d += 32) {
+                    uint32_t o[32];                            // the columns past the last are there, whatever they hold
                     if (some) {
-                        tmem_ld(o_col + d, o);
-                        tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(o[0]));
-                        tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(o[32]));
+                        tmem_ld32(o_col + d, o);
+                        tmem_ld_wait(o);
                     }
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) o[k] = sums ? __float_as_uint(__uint_as_float(o[k]) * f) : 0u;
+                    for (int k = 0; k < 32; ++k) o[k] = sums ? __float_as_uint(__uint_as_float(o[k]) * f) : 0u;
                     if (r < p.rows) {
                         if (!whole || p.out_f32) {
-                            float *dst = whole ? static_cast<float *>(p.out) + row * p.c.dim : p.part + (part * p.part_rows + in_part) * p.c.dim;
+                            float *dst = whole ? static_cast<float *>(p.out) + row * p.c.dim : p.part + part * p.c.dim;
 #pragma unroll
-                            for (int e = 0; e < 64; e += 8)
-                                if (d + e < p.c.dim) store32(dst + d + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7], whole ? p.out_wide : p.part_wide);
+                            for (int e = 0; e < 32; e += 8)
+                                if (d + e < p.c.dim) store32(dst + d + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7], wide);
                         } else {
                             T *dst = static_cast<T *>(p.out) + row * p.c.dim;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = pack2<T>(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+                            for (int k = 0; k < 16; ++k) o[k] = pack2<T>(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
 #pragma unroll
-                            for (int e = 0; e < 64; e += 16) {
+                            for (int e = 0; e < 32; e += 16) {
                                 const int k = e / 2;
                                 if (d + e + 8 < p.c.dim)
-                                    store32(dst + d + e, o[k], o[k + 1], o[k + 2], o[k + 3], o[k + 4], o[k + 5], o[k + 6], o[k + 7], p.out_wide);
+                                    store32(dst + d + e, o[k], o[k + 1], o[k + 2], o[k + 3], o[k + 4], o[k + 5], o[k + 6], o[k + 7], wide);
                                 else if (d + e < p.c.dim)
                                     *reinterpret_cast<uint4 *>(dst + d + e) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                             }
@@ -856,15 +853,10 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     }
                     __syncwarp();
                 }
-                if (!whole && r < p.rows) p.part_ml[part * p.part_rows + in_part] = make_float2(m, l);
+                if (!whole && r < p.rows) p.part_ml[part] = make_float2(m, l);
             }
             tc_fence_before();
-            if (w.begins && !w.ends) {                         // the CTA's last run: who has the rest of the unit
-                const long long end = w.place + w.rest;        // the owner of tile x is the last CTA that starts at or before it
-                join = make_int2((u.b * p.row_tiles + u.rt) * p.c.heads + u.h, (int)((end * w.grid - 1) / w.total));
-            }
         }
-        if (join.x >= 0 && warp == 0 && lane == 0) p.joins[blockIdx.x] = join;
     } else if (warp < SOFT + 2) {
         // ------------------------------------------------------------------ one thread per half issues its products
         if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -881,9 +873,9 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     if (k < p.ksteps)
                         umma_f16(tmem + sb * TN, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
                                  b + (((k >> 2) * (TN * 128) + (k & 3) * 32) >> 4), kIdS, k > 0);
-                umma_commit(b_s + 8 * sb);
-                umma_commit(b_empty + 8 * at);
-                if (last) umma_commit(b_qempty);
+                umma_commit(bar(sh.s[sb]));
+                umma_commit(bar(sh.empty[at]));
+                if (last) umma_commit(bar(sh.q_empty));
             }
             __syncwarp();
         };
@@ -896,19 +888,19 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     umma_f16_ts(tmem + S::kO + i * S::kOPitch, tmem + sb * TN + 8 * (part * STEPS + k), b + ((k * 2048) >> 4), id_o,
                                 add || k > 0);
                 if (part == PARTS - 1) {
-                    umma_commit(b_empty + 8 * at);
-                    if (last) umma_commit(b_pv + 8 * i);
+                    umma_commit(bar(sh.empty[at]));
+                    if (last) umma_commit(bar(sh.pv[i]));
                 }
             }
             __syncwarp();
         };
-        auto waits = [&](uint32_t bar, int parity, int site) {
-            const bool ok = wait(bar, parity, abort, site);
+        auto waits = [&](uint64_t &b, int parity, int site) {
+            const bool ok = wait(bar(b), parity, abort, site);
             tc_fence_after();
             return ok;
         };
-        auto run = [&](int nt) {
-            if (!waits(b_qfull, runs & 1, W_Q) || !waits(b_full + 8 * slot, phase, W_K)) return false;
+        auto work = [&](int nt) {
+            if (!waits(sh.q_full, runs & 1, W_Q) || !waits(sh.full[slot], phase, W_K)) return false;
             product_s(NQ == 2 ? i : g & 1, slot, nt == 1);
             for (int j = 0; j < nt; ++j, ++g) {
                 int vs = slot + 1, vp = phase;
@@ -917,19 +909,20 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 if (ks >= p.slots) ks = 0, kp ^= 1;
                 const bool more = j + 1 < nt;
                 const int sb = NQ == 2 ? i : g & 1;
-                // V and the next K are waited for before P, so that nothing but P holds the products up
-                if (!waits(b_full + 8 * vs, vp, W_V)) return false;
-                if (more && !waits(b_full + 8 * ks, kp, W_K)) return false;
+                // V and the next K are waited for before P, so that nothing but P holds the products up.  The halves take
+                // turns, a tile's products at a time: otherwise both wait for scores, then both for the tensor core.
+                if (!waits(sh.full[vs], vp, W_V)) return false;
+                if (more && !waits(sh.full[ks], kp, W_K)) return false;
                 if (NQ == 1 && more) product_s((g + 1) & 1, ks, j + 2 == nt);      // while this tile's scores are worked on
-                if (NQ == 2 && !waits(b_turn + 8 * i, i == 0 ? (g & 1) ^ 1 : g & 1, W_TURN)) return false;
+                if (NQ == 2 && !waits(sh.turn[i], i == 0 ? (g & 1) ^ 1 : g & 1, W_TURN)) return false;
 #pragma unroll
                 for (int part = 0; part < PARTS; ++part) {
-                    if (!waits(b_p + 8 * (sb * PARTS + part), NQ == 2 ? g & 1 : (g >> 1) & 1, W_P)) return false;
+                    if (!waits(sh.p[sb * PARTS + part], NQ == 2 ? g & 1 : (g >> 1) & 1, W_P)) return false;
                     product_o(sb, vs, part, j > 0 || part > 0, NQ == 1 || !more);
                 }
                 if (NQ == 2) {
                     if (more) product_s(sb, ks, j + 2 == nt);
-                    if (lane == 0) mbar_arrive(b_turn + 8 * (i ^ 1));
+                    if (lane == 0) mbar_arrive(bar(sh.turn[i ^ 1]));
                     __syncwarp();
                 }
                 slot = ks;
@@ -939,17 +932,18 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             return true;
         };
         if (i < NQ) {
-            for (bool first = true; w.next(p, first, abort); first = false) {
-                const int nt = w.u.t1 - w.u.t0;
-                if (nt > 0 && !run(nt)) break;
+            PrefillRun run;
+            while (hear(run)) {
+                const int nt = run.u.t1 - run.u.t0;
+                if (nt > 0 && !work(nt)) break;
             }
-            if (elect()) umma_commit(b_drain + 8 * i);         // nothing is under way when tensor memory is given back
+            if (elect()) umma_commit(bar(sh.drain[i]));        // nothing is under way when tensor memory is given back
             __syncwarp();
             uint32_t never = 0;
-            mbar_wait_warp(b_drain + 8 * i, 0, &never, KID_PREFILL, W_DRAIN);
+            mbar_wait_warp(bar(sh.drain[i]), 0, &never, KID_PREFILL, W_DRAIN);
         }
     } else {
-        // ------------------------------------------------------------------ loaders
+        // ------------------------------------------------------------------ loaders; the first finds the runs
         if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int lw = warp - SOFT - 2;
         const int pieces = p.ksteps * 2;                       // 16-byte pieces of a row, past `dim` zeros
@@ -962,6 +956,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
         // 32 rows whose addresses the lanes hold (null: zeros), `pitch` bytes between their 64-value chunks
         auto copy_rows = [&](const T *at, uint32_t dst, int first_row, uint32_t pitch) {
             int row = row0, piece = piece0;
+#pragma unroll 1
             for (int i = 0; i < pieces; ++i) {
                 const T *src = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, (unsigned long long)at, row));
                 const bool there = src != nullptr && piece * 8 < p.c.dim;
@@ -973,19 +968,19 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 if (piece >= pieces) piece -= pieces, ++row;
             }
         };
-        auto announce = [&](uint32_t bar) {                    // the oldest copies have arrived
-            if (bar == 0) return;
+        auto announce = [&](uint32_t b) {                      // the oldest copies have arrived
+            if (b == 0) return;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
+            if (lane == 0) mbar_arrive(b);
         };
-        auto push = [&](uint32_t bar) {
+        auto push = [&](uint32_t b) {
             cp_commit();
             cp_wait<LAG>();
             announce(queue[0]);
 #pragma unroll
             for (int i = 0; i + 1 < LAG; ++i) queue[i] = queue[i + 1];
-            queue[LAG - 1] = bar;
+            queue[LAG - 1] = b;
         };
         auto flush = [&]() {
             cp_wait<0>();
@@ -996,26 +991,27 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             }
         };
         // Before a wait that others may have to end with what is still under way here.
-        auto waits = [&](uint32_t bar, int parity, int site) {
-            if (__shfl_sync(0xffffffffu, mbar_try_wait(bar, (uint32_t)parity) ? 1 : 0, 0)) return true;
+        auto waits = [&](uint64_t &b, int parity, int site) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), (uint32_t)parity))) return true;
             flush();
-            return mbar_wait_warp(bar, (uint32_t)parity, abort, KID_PREFILL, site);
+            return wait(bar(b), parity, abort, site);
         };
         int runs = 0, slot = 0, phase = 0;
-        auto run = [&](const PrefillUnit &u) {
-            if (!waits(b_qempty, (runs & 1) ^ 1, W_QEMPTY)) return false;
+        auto load = [&](const PrefillUnit &u) {
+            if (!waits(sh.q_empty, (runs & 1) ^ 1, W_QEMPTY)) return false;
             if (p.q_box) {                                     // rows of other sequences, or zeros, in place of rows that are not there
                 if (lane == 0) {
-                    if (lw == 0) mbar_arrive_expect_tx(b_qfull, (uint32_t)(NQ * p.chunks * (128 * 128)));
-                    else mbar_arrive(b_qfull);
+                    if (lw == 0) mbar_arrive_expect_tx(bar(sh.q_full), (uint32_t)(NQ * p.chunks * (128 * 128)));
+                    else mbar_arrive(bar(sh.q_full));
                 }
                 __syncwarp();
                 if (lw == 0 && lane < NQ * p.chunks) {
                     const int i = lane / p.chunks, ch = lane - i * p.chunks;
-                    tma_load_4d(base + i * q_bytes + ch * (128 * 128), &p.q_map, b_qfull, ch * 64, u.h * p.group,
+                    tma_load_4d(base + i * q_bytes + ch * (128 * 128), &p.q_map, bar(sh.q_full), ch * 64, u.h * p.group,
                                 u.b * p.new_tokens + p.group_div.of(u.rt * RT + i * 128), 0);
                 }
             } else {
+#pragma unroll 1
                 for (int bt = lw; bt < RT / 32; bt += LOADERS) {
                     const int r = u.rt * RT + bt * 32 + lane, t = p.group_div.of(min(r, p.rows - 1));
                     const bool live = r < p.rows && t < u.n;
@@ -1024,7 +1020,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                                        : nullptr;
                     copy_rows(at, base + (bt >> 2) * q_bytes, (bt & 3) * 32, 128 * 128);
                 }
-                push(b_qfull);
+                push(bar(sh.q_full));
             }
             for (int tile = u.t0; tile < u.t1; ++tile) {
                 if (p.box) {                                   // boxes of entries of one page
@@ -1041,18 +1037,18 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     const int many = __popc(__ballot_sync(0xffffffffu, mine));
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
-                        if (!waits(b_empty + 8 * slot, phase ^ 1, W_EMPTY)) return false;
-                        const uint32_t bar = b_full + 8 * slot, dst = ring + slot * slot_bytes + lane * p.box * 128;
-                        if (lw == 0 && lane < TN / 32) s_bad[slot][lane] = 0;
+                        if (!waits(sh.empty[slot], phase ^ 1, W_EMPTY)) return false;
+                        const uint32_t b = bar(sh.full[slot]), dst = ring + slot * slot_bytes + lane * p.box * 128;
+                        if (lw == 0 && lane < TN / 32) sh.bad[slot][lane] = 0;
                         __syncwarp();
                         if (lane == 0) {
-                            if (many) mbar_arrive_expect_tx(bar, (uint32_t)(many * p.chunks * p.box * 128));
-                            else mbar_arrive(bar);
+                            if (many) mbar_arrive_expect_tx(b, (uint32_t)(many * p.chunks * p.box * 128));
+                            else mbar_arrive(b);
                         }
                         __syncwarp();
                         if (mine)
                             for (int ch = 0; ch < p.chunks; ++ch)
-                                tma_load_4d(dst + ch * (TN * 128), kv ? &p.v_map : &p.k_map, bar, ch * 64, off, u.h, pg);
+                                tma_load_4d(dst + ch * (TN * 128), kv ? &p.v_map : &p.k_map, b, ch * 64, off, u.h, pg);
                         if (++slot == p.slots) slot = 0, phase ^= 1;
                     }
                     flush();                                   // what was copied otherwise before
@@ -1074,12 +1070,12 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (!waits(b_empty + 8 * slot, phase ^ 1, W_EMPTY)) return false;
+                    if (!waits(sh.empty[slot], phase ^ 1, W_EMPTY)) return false;
 #pragma unroll
                     for (int bt = 0; bt < BATCH; ++bt)
                         copy_rows(kv ? va[bt] : ka[bt], ring + slot * slot_bytes, (bt * LOADERS + lw) * 32, TN * 128);
-                    if (lw == 0 && lane < TN / 32) s_bad[slot][lane] = 0;
-                    push(b_full + 8 * slot);
+                    if (lw == 0 && lane < TN / 32) sh.bad[slot][lane] = 0;
+                    push(bar(sh.full[slot]));
                     if (++slot == p.slots) slot = 0, phase ^= 1;
                 }
             }
@@ -1087,19 +1083,55 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             return true;
         };
         bool ok = true;
-        for (bool first = true; ok && w.next(p, first, abort); first = false) {
-            if (w.u.t0 < w.u.t1) ok = run(w.u);
-            flush();                                           // before a wait for warps that may wait for these copies
+        int asking = -1;                                       // whole: phase of an answer that has not come
+        if (lw == 0) {
+            PrefillWalk<RT, TN> w;
+            w.asked = 0;
+            if (!p.whole) w.split(p);
+            int2 join = make_int2(-1, 0);
+            for (bool first = true; ok; first = false) {
+                int none = 0;
+                if (p.whole) {
+                    const int st = w.next_whole(p, first, smem_u32(&sh.answer), bar(sh.next), abort);
+                    if (st == -2) asking = w.asked & 1;
+                    if (st == -2) break;
+                    none = st;
+                } else if (!w.next_split(p, first)) {
+                    none = -1;
+                }
+                if (!none && w.begins && !w.ends) {            // the CTA's last run: who has the rest of the unit
+                    const long long end = w.place + w.rest;    // the owner of tile x is the last CTA that starts at or before it
+                    join = make_int2((w.u.b * p.row_tiles + w.u.rt) * p.c.heads + w.u.h, (int)((end * w.grid - 1) / w.total));
+                }
+                if (!waits(sh.run_empty[run_at], run_phase ^ 1, W_RUN)) break;
+                if (lane == 0) {
+                    sh.run[run_at].u = w.u;
+                    sh.run[run_at].flags = none ? 4 : (w.begins ? 1 : 0) | (w.ends ? 2 : 0);
+                    mbar_arrive(bar(sh.run_full[run_at]));
+                }
+                __syncwarp();
+                if (++run_at == Shared::RUNS) run_at = 0, run_phase ^= 1;
+                if (none) break;
+                if (w.u.t0 < w.u.t1) ok = load(w.u);
+                flush();                                       // before a wait for warps that may wait for these copies
+            }
+            if (!p.whole && lane == 0) p.joins[blockIdx.x] = ok && !*abort ? join : make_int2(-1, 0);
+        } else {
+            PrefillRun run;
+            while (ok && hear(run)) {
+                if (run.u.t0 < run.u.t1) ok = load(run.u);
+                flush();
+            }
         }
         flush();
-        if (!ok || *abort) {                                // a wait ran out: the copies under way still come to their end
+        if (!ok || *abort) {                                   // a wait ran out: the copies under way still come to their end
             uint32_t never = 0;
             for (int i = 0; i < p.slots; ++i) {
                 const int before = i < slot ? phase : phase ^ 1;       // of the slot's last copy; none: over already
-                if (lane == 0 && p.box) mbar_wait(b_full + 8 * i, (uint32_t)before, &never, KID_PREFILL, W_DRAIN);
+                if (lane == 0 && p.box) mbar_wait(bar(sh.full[i]), (uint32_t)before, &never, KID_PREFILL, W_DRAIN);
             }
-            if (lane == 0 && lw == 0 && p.whole) mbar_wait(b_next + 8 * (w.asked & 1), (uint32_t)(w.asked >> 1) & 1u, &never, KID_PREFILL, W_DRAIN);
-            if (lane == 0 && p.q_box) mbar_wait(b_qfull, (uint32_t)(runs & 1), &never, KID_PREFILL, W_DRAIN);
+            if (lane == 0 && asking >= 0) mbar_wait(bar(sh.next), (uint32_t)asking, &never, KID_PREFILL, W_DRAIN);
+            if (lane == 0 && p.q_box) mbar_wait(bar(sh.q_full), (uint32_t)(runs & 1), &never, KID_PREFILL, W_DRAIN);
             __syncwarp();
         }
     }
@@ -1214,9 +1246,11 @@ inline int make_plan(const mmq_kv_cache *c, int q_heads, int new_tokens, Plan &q
     q.part_rows = q.rows < q.rt ? q.rows : q.rt;
     q.floats = q.whole ? 4 : 2ll * sms * q.part_rows * (c->dim + 2) + 2ll * sms;
     const uint32_t slot = (uint32_t)q.chunks * q.tn * 128, queries = (uint32_t)q.chunks * q.rt * 128;
-    q.slots = (int)((SMEM - 1024 - queries) / slot);
+    const uint32_t rest = q.rt == 256 ? (q.tn == 128 ? sizeof(PrefillShared<2, 128>) : sizeof(PrefillShared<2, 64>))
+                                      : (q.tn == 128 ? sizeof(PrefillShared<1, 128>) : sizeof(PrefillShared<1, 64>));
+    q.slots = (int)((SMEM - rest - queries) / slot);
     if (q.slots > MAX_SLOTS) q.slots = MAX_SLOTS;
-    q.smem = queries + q.slots * slot + 1024;
+    q.smem = queries + q.slots * slot + rest;
     return MMQ_OK;
 }
 
@@ -1234,7 +1268,7 @@ int launch(const PrefillParams &p, const Plan &q, cudaStream_t stream)
     int rc = launch_pdl(prefill_kernel<T, NQ, TN>, dim3((unsigned)q.grid), PrefillShape<T, NQ, TN>::kThreads, q.smem, stream, 0, p);
     if (rc != MMQ_OK || q.whole) return rc;
     const int by = (q.part_rows + 3) / 4;
-    return launch_pdl(prefill_join_kernel<T>, dim3((unsigned)q.grid, (unsigned)(by < 16 ? by : 16)), 128, 0, stream, 0, p, q.rt);
+    return launch_pdl(prefill_join_kernel<T>, dim3((unsigned)q.grid, (unsigned)(by < 64 ? by : 64)), 128, 0, stream, 0, p, q.rt);
 }
 
 template <typename T>
