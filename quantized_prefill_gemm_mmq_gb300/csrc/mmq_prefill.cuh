@@ -109,12 +109,6 @@ __device__ __forceinline__ uint64_t pair(float a, float b)
     return r;
 }
 __device__ __forceinline__ void unpair(uint64_t x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t r;
@@ -569,6 +563,13 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
         mbar_init(bar(sh.next), 1);
         fence_mbar_init();
     }
+    if (threadIdx.x == 32) {                                   // the maps are part of the launch
+        if (p.q_box) tma_prefetch(&p.q_map);
+        if (p.box) {
+            tma_prefetch(&p.k_map);
+            tma_prefetch(&p.v_map);
+        }
+    }
     // Tensor memory is taken after the launch before has ended: its blocks may still have to take theirs.
     pdl_wait();
     if (warp == SOFT) {
@@ -695,6 +696,8 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 if (general || cut) {
 #pragma unroll 1
                     for (int k = 0; k < TN; k += 32) {
+                        const bool cut32 = e0 + k < max_lo || e0 + k + 32 > min_hi;
+                        if (!general && !cut32) continue;
                         uint32_t y[32];
                         tmem_ld32(s_col + k, y);
                         tmem_ld_wait(y);
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 #pragma unroll
                             for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) + fmaf(slope, (float)j, bias));
                         }
-                        if (cut) {
+                        if (cut32) {
                             const uint32_t bits = sees(k);
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
@@ -726,27 +729,23 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 #pragma unroll
                     for (int k = 0; k < TN; k += 32) tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
                 };
-                uint64_t sum[2], by2, off2;
+                uint64_t sum;
+                float by = c, add = off;
                 auto power = [&](int k0, int k1) {             // scores to P, in place of the first half of them
 #pragma unroll
                     for (int j = k0; j < k1; j += 2) {
-                        float a, b;
-                        unpair(fma2(pair(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), by2, off2), a, b);
-                        a = pow2(a);
-                        b = pow2(b);
-                        sum[j / 2 & 1] = add2(sum[j / 2 & 1], pair(a, b));
+                        const float a = pow2(fmaf(__uint_as_float(x[j]), by, add)), b = pow2(fmaf(__uint_as_float(x[j + 1]), by, add));
+                        sum = add2(sum, pair(a, b));
                         x[j / 2] = pack2<T>(a, b);
                     }
                 };
                 load();
-                by2 = pair(c, c);
-                off2 = pair(off, off);
 #pragma unroll 1
                 for (bool again = false;; again = true) {
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int k = 0; k < TN; k += 2) top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-                    sum[0] = sum[1] = 0;
+                    sum = 0;
                     power(0, TN / PARTS);
                     const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     const bool raise = mx > m && !((mx - m) * c <= kLazy);
@@ -769,8 +768,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 #pragma unroll 1
                         for (int d = 0; d < p.ksteps * 16; d += 8) scale8(o_col + d, f);
                     }
-                    by2 = pair(c, c);
-                    off2 = pair(off, off);
+                    add = off;
                     if (any_large) {                           // m is taken off first in rows of such scores, and in these alone
 #pragma unroll 1
                         for (int k = 0; k < TN; k += 32) {
@@ -785,8 +783,8 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                             tmem_st32(s_col + k, y);
                         }
                         tmem_st_wait();
-                        by2 = pair(1.f, 1.f);
-                        off2 = 0;
+                        by = 1.f;
+                        add = 0.f;
                     }
                     load();
                 }
@@ -802,7 +800,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     if (lane == 0) mbar_arrive(bar(sh.p[sb * PARTS + part]));
                 }
                 float la, lb;
-                unpair(add2(sum[0], sum[1]), la, lb);
+                unpair(sum, la, lb);
                 l += la + lb;
             }
 
