@@ -34,6 +34,9 @@ namespace {
 
 namespace pre {
 constexpr int LOADERS = 2;            // warps
+#ifndef TURNS
+#define TURNS 1
+#endif
 constexpr int PARTS = 2;              // of a tile's P, each announced by itself
 constexpr int LAG = 2;                // copies a loader has under way before it waits for the oldest
 constexpr int MAX_SLOTS = 12;
@@ -137,36 +140,7 @@ __device__ __forceinline__ float rcp(float x)
 }
 
 // Columns of the warp's 32 lanes, to be used after tmem_ld_wait on each 32 of them.
-__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[128])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
-                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-                 "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
-                 "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
-                 "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
-                 "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
-                 "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-                   "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-                   "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-                   "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-                   "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
-                   "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
-                   "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
-                   "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
-                   "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
-                   "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
-                   "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
-                   "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
-                   "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
-                 : "r"(at)
-                 : "memory");
-}
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) { tmem_ld32(at, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[64])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
@@ -723,11 +697,17 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 // Scores are read once: the tensor core's own traffic in tensor memory goes first.  The first part's exponentials
                 // are begun with the maximum so far, while the tile's is found; where that has to be raised, which is rare, they
                 // are done again.
+                constexpr int W = TN / PARTS;
                 uint32_t x[TN];
-                auto load = [&]() {
-                    tmem_ld(s_col, x);
+                auto load = [&](int part) { tmem_ld(s_col + part * W, reinterpret_cast<uint32_t(&)[W]>(x[part * W])); };
+                auto loaded = [&](int part) {
 #pragma unroll
-                    for (int k = 0; k < TN; k += 32) tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
+                    for (int k = part * W; k < (part + 1) * W; k += 32) tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
+                };
+                float top[2];
+                auto largest = [&](int k0, int k1) {
+#pragma unroll
+                    for (int k = k0; k < k1; k += 2) top[k / 2 & 1] = max3(top[k / 2 & 1], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
                 };
                 uint64_t sum;
                 float by = c, add = off;
@@ -739,15 +719,18 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                         x[j / 2] = pack2<T>(a, b);
                     }
                 };
-                load();
 #pragma unroll 1
                 for (bool again = false;; again = true) {
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < TN; k += 2) top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                    load(0);
+                    loaded(0);
+                    load(1);                                   // under way during the first part's exponentials
+                    top[0] = top[1] = -INFINITY;
+                    largest(0, W);
                     sum = 0;
-                    power(0, TN / PARTS);
-                    const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+                    power(0, W);
+                    loaded(1);
+                    largest(W, TN);
+                    const float mx = fmaxf(top[0], top[1]);
                     const bool raise = mx > m && !((mx - m) * c <= kLazy);
                     if (again || !__any_sync(0xffffffffu, raise || any_large)) break;
                     float f = 1.f;
@@ -786,19 +769,25 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                         by = 1.f;
                         add = 0.f;
                     }
-                    load();
                 }
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part) {
-                    constexpr int W = TN / PARTS;
-                    if (part > 0) power(part * W, (part + 1) * W);
+                // P goes over scores that are read; a part is announced once it is stored, which the next exponentials cover.
+                auto store = [&](int part) {
 #pragma unroll
                     for (int k = part * W / 2; k < (part + 1) * W / 2; k += 16) tmem_st16(s_col + k, reinterpret_cast<uint32_t(&)[16]>(x[k]));
+                };
+                auto stored = [&](int part) {
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(sh.p[sb * PARTS + part]));
-                }
+                };
+                static_assert(PARTS == 2, "two parts");
+                store(0);
+                power(W, W + W / 2);
+                stored(0);
+                power(W + W / 2, TN);
+                store(1);
+                stored(1);
                 float la, lb;
                 unpair(sum, la, lb);
                 l += la + lb;
@@ -912,15 +901,15 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 if (!waits(sh.full[vs], vp, W_V)) return false;
                 if (more && !waits(sh.full[ks], kp, W_K)) return false;
                 if (NQ == 1 && more) product_s((g + 1) & 1, ks, j + 2 == nt);      // while this tile's scores are worked on
-                if (NQ == 2 && !waits(sh.turn[i], i == 0 ? (g & 1) ^ 1 : g & 1, W_TURN)) return false;
 #pragma unroll
                 for (int part = 0; part < PARTS; ++part) {
                     if (!waits(sh.p[sb * PARTS + part], NQ == 2 ? g & 1 : (g >> 1) & 1, W_P)) return false;
+                    if (NQ == 2 && TURNS && part == 0 && !waits(sh.turn[i], i == 0 ? (g & 1) ^ 1 : g & 1, W_TURN)) return false;
                     product_o(sb, vs, part, j > 0 || part > 0, NQ == 1 || !more);
                 }
                 if (NQ == 2) {
                     if (more) product_s(sb, ks, j + 2 == nt);
-                    if (lane == 0) mbar_arrive(bar(sh.turn[i ^ 1]));
+                    if (TURNS && lane == 0) mbar_arrive(bar(sh.turn[i ^ 1]));
                     __syncwarp();
                 }
                 slot = ks;
