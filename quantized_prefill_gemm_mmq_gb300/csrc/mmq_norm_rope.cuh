@@ -14,11 +14,18 @@
 // and the row's sines are computed once per block meanwhile.
 #pragma once
 
+#include <type_traits>
+
 namespace mmq {
 namespace {
 
 constexpr int NR_THREADS = 256;
-constexpr int NR_BATCH = 3;          // heads whose loads a thread has in flight
+#ifndef NRB
+#define NRB 2
+#define NRM 4
+#define NRS 1
+#endif
+constexpr int NR_BATCH = NRB, NR_BLOCKS = NRM;          // heads whose loads a thread has in flight
 
 struct NormRopeParams {
     mmq_kv_cache c;
@@ -38,8 +45,9 @@ struct NormRopeParams {
 
 // WIDE: rot is a multiple of 8, so that a thread's values are two aligned groups of four.
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(NR_THREADS, 4) norm_rope_kernel(const NormRopeParams p)
+__global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) norm_rope_kernel(const NormRopeParams p)
 {
+    enum { Q, K, V };
     __shared__ float s_cos[128], s_sin[128];
     pdl_wait();
     pdl_launch_dependents();
@@ -47,14 +55,12 @@ __global__ void __launch_bounds__(NR_THREADS, 4) norm_rope_kernel(const NormRope
     const int u = threadIdx.x & (p.group - 1), hl = threadIdx.x / p.group, lanes = blockDim.x / p.group;
     const int64_t row = blockIdx.x;
     const int b = (int)(row / p.new_tokens), t = (int)(row - (int64_t)b * p.new_tokens);
-    const int total = p.q_heads + 2 * p.c.heads;
-    const int h0 = blockIdx.y * p.heads_per_block, h1 = min(total, h0 + p.heads_per_block);
+    const int h0 = blockIdx.y * p.heads_per_block, h1 = min(p.q_heads + 2 * p.c.heads, h0 + p.heads_per_block);
     const bool owner = u * 8 < D;                                // groups are rounded up to a power of two
-    const bool turns = WIDE ? u * 8 < p.rot : true;
     // The thread's pairs are (a[j], b[j]).  Where they lie: WIDE in two runs of four (halves apart, or side by side),
     // else pair k = 4u + j at (k, k + half), (2k, 2k + 1) interleaved or past the rotated ones.
-    const bool apart = !p.interleaved && turns;
-    const int e0 = apart ? u * 4 : u * 8, e1 = apart ? half + u * 4 : u * 8 + 4;
+    const bool apart = !p.interleaved && u * 8 < p.rot;
+    const int d0 = apart ? u * 4 : u * 8, d1 = apart ? half + u * 4 : u * 8 + 4;
     auto place = [&](int j, int &x, int &y, bool rotated) {      // !WIDE
         const int k = u * 4 + j;
         x = rotated && k < half && !p.interleaved ? k : 2 * k;
@@ -62,16 +68,11 @@ __global__ void __launch_bounds__(NR_THREADS, 4) norm_rope_kernel(const NormRope
     };
     auto read = [&](const float *src, bool rotated, float (&a)[4], float (&c)[4]) {
         if constexpr (WIDE) {
+            const float4 x = *reinterpret_cast<const float4 *>(src + (rotated ? d0 : u * 8));
+            const float4 y = *reinterpret_cast<const float4 *>(src + (rotated ? d1 : u * 8 + 4));
             const bool ap = rotated && apart;
-            const float4 x = *reinterpret_cast<const float4 *>(src + (ap ? e0 : u * 8));
-            const float4 y = *reinterpret_cast<const float4 *>(src + (ap ? e1 : u * 8 + 4));
-            if (ap) {
-                a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
-                c[0] = y.x, c[1] = y.y, c[2] = y.z, c[3] = y.w;
-            } else {
-                a[0] = x.x, c[0] = x.y, a[1] = x.z, c[1] = x.w;
-                a[2] = y.x, c[2] = y.y, a[3] = y.z, c[3] = y.w;
-            }
+            a[0] = x.x, a[1] = ap ? x.y : x.z, a[2] = ap ? x.z : y.x, a[3] = ap ? x.w : y.z;
+            c[0] = ap ? y.x : x.y, c[1] = ap ? y.y : x.w, c[2] = ap ? y.z : y.y, c[3] = y.w;
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -82,46 +83,80 @@ __global__ void __launch_bounds__(NR_THREADS, 4) norm_rope_kernel(const NormRope
             }
         }
     };
-    const int n = new_count(p.new_len, b, p.new_tokens, KID_NORM);
-    const int len = cache_len(p.c, b, KID_NORM);
-    const int slot = len - n + t;
-    const bool live = t < n;
-    bool store = live;
-    int64_t page = 0;
-    int off = 0;
-    if (live) {
-        if (slot < 0) {
-            record_error(MMQ_ERR_INDEX, KID_NORM, SITE_LEN);
-            store = false;
+    // eight values to f32, or rounded to the cache's type
+    auto write = [&](auto *dst, bool rotated, const float (&a)[4], const float (&c)[4]) {
+        using O = typename std::remove_pointer<decltype(dst)>::type;
+        if constexpr (WIDE) {
+            const bool ap = rotated && apart;
+            const float4 x = make_float4(a[0], ap ? a[1] : c[0], ap ? a[2] : a[1], ap ? a[3] : c[1]);
+            const float4 y = make_float4(ap ? c[0] : a[2], ap ? c[1] : c[2], ap ? c[2] : a[3], c[3]);
+            if constexpr (std::is_same<O, float>::value) {
+                *reinterpret_cast<float4 *>(dst + (rotated ? d0 : u * 8)) = x;
+                *reinterpret_cast<float4 *>(dst + (rotated ? d1 : u * 8 + 4)) = y;
+            } else {
+                const uint2 w0 = make_uint2(pack2<O>(x.x, x.y), pack2<O>(x.z, x.w)), w1 = make_uint2(pack2<O>(y.x, y.y), pack2<O>(y.z, y.w));
+                if (!ap) {
+                    *reinterpret_cast<uint4 *>(dst + u * 8) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                } else {
+                    *reinterpret_cast<uint2 *>(dst + d0) = w0;
+                    *reinterpret_cast<uint2 *>(dst + d1) = w1;
+                }
+            }
         } else {
-            const int col = p.page_div.of(slot);
-            off = slot - col * p.c.page_size;
-            const int pg = cache_page(p.c, b, col, KID_NORM);
-            store = pg >= 0;
-            page = pg;
-        }
-    }
-    float a[NR_BATCH][4], c[NR_BATCH][4];
-    auto load = [&](int hb) {
 #pragma unroll
-        for (int i = 0; i < NR_BATCH; ++i) {
-            const int h = hb + i * lanes;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[i][j] = c[i][j] = 0.f;
-            if (h >= h1 || !live || !owner) continue;
-            const bool is_v = h >= p.q_heads + p.c.heads;
-            const float *src = h < p.q_heads ? p.q + row * p.ldq + (int64_t)h * D
-                               : !is_v       ? p.k + row * p.ldk + (int64_t)(h - p.q_heads) * D
-                                             : p.v + row * p.ldv + (int64_t)(h - p.q_heads - p.c.heads) * D;
-            read(src, !is_v, a[i], c[i]);
+            for (int j = 0; j < 4; ++j) {
+                int x, y;
+                place(j, x, y, rotated);
+                if constexpr (std::is_same<O, float>::value) dst[x] = a[j], dst[y] = c[j];
+                else dst[x] = to_cache<O>(a[j]), dst[y] = to_cache<O>(c[j]);
+            }
         }
     };
-    load(h0 + hl);
-    float qa[4], qc[4], ka[4], kc[4];
+    const int n = new_count(p.new_len, b, p.new_tokens, KID_NORM);
+    if (t >= n) {                                                // a row that is not there: q is 0
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int h = h0 + hl; h < min(h1, p.q_heads); h += lanes) {
+            if (!owner) continue;
+            if (p.q_f32) write(static_cast<float *>(p.q_out) + row * p.ldo + (int64_t)h * D, true, zero, zero);
+            else write(static_cast<T *>(p.q_out) + row * p.ldo + (int64_t)h * D, true, zero, zero);
+        }
+        return;
+    }
+    float a[NR_BATCH][4], c[NR_BATCH][4];
+    // heads h + i lanes < end of rows at src
+    auto load = [&](const float *src, int h, int end, bool rotated) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) qa[j] = qc[j] = ka[j] = kc[j] = 1.f;
-    if (owner && p.q_norm) read(p.q_norm, true, qa, qc);
-    if (owner && p.k_norm) read(p.k_norm, true, ka, kc);
+        for (int i = 0; i < NR_BATCH; ++i) {
+            if (h + i * lanes < end && owner) {
+                read(src + (int64_t)(h + i * lanes) * D, rotated, a[i], c[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[i][j] = c[i][j] = 0.f;
+            }
+        }
+    };
+    // the block's heads of each kind
+    const int kv = p.c.heads, q0 = min(h0, p.q_heads), q1 = min(h1, p.q_heads);
+    const int k0 = min(max(h0 - p.q_heads, 0), kv), k1 = min(max(h1 - p.q_heads, 0), kv);
+    const int v0 = min(max(h0 - p.q_heads - kv, 0), kv), v1 = min(max(h1 - p.q_heads - kv, 0), kv);
+    const float *q_src = p.q + row * p.ldq, *k_src = p.k + row * p.ldk, *v_src = p.v + row * p.ldv;
+    const int first = q0 < q1 ? Q : k0 < k1 ? K : V;             // its first heads come while the sines are computed
+    load(first == Q ? q_src : first == K ? k_src : v_src, (first == Q ? q0 : first == K ? k0 : v0) + hl, first == Q ? q1 : first == K ? k1 : v1,
+         first != V);
+
+    const int slot = cache_len(p.c, b, KID_NORM) - n + t;
+    bool store = slot >= 0;
+    int64_t page = 0;
+    int off = 0;
+    if (store) {
+        const int col = p.page_div.of(slot);
+        off = slot - col * p.c.page_size;
+        const int pg = cache_page(p.c, b, col, KID_NORM);
+        store = pg >= 0;
+        page = pg;
+    } else {
+        record_error(MMQ_ERR_INDEX, KID_NORM, SITE_LEN);
+    }
     const int first_pos = *(p.pos + row);
     for (int i = threadIdx.x; i < half; i += blockDim.x) {
         int ax = p.axis ? *(p.axis + i) : 0;
@@ -137,91 +172,67 @@ __global__ void __launch_bounds__(NR_THREADS, 4) norm_rope_kernel(const NormRope
         s_sin[i] = sine * p.magnitude;
     }
     __syncthreads();
-    float cs[4], sn[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const bool r = u * 4 + j < half;
-        cs[j] = r ? s_cos[u * 4 + j] : 1.f;
-        sn[j] = r ? s_sin[u * 4 + j] : 0.f;
-    }
 
-    // every thread takes the same number of steps: the shuffles need whole warps
-    for (int hb = h0; hb < h1; hb += lanes * NR_BATCH) {
-        if (hb != h0) load(hb + hl);
-#pragma unroll
-        for (int i = 0; i < NR_BATCH; ++i) {
-            const int h = hb + hl + i * lanes;
-            const bool is_v = h >= p.q_heads + p.c.heads, is_q = h < p.q_heads;
-            const bool normed = is_q ? p.q_norm != nullptr : !is_v && p.k_norm != nullptr;
-            float ss = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) ss = fmaf(a[i][j], a[i][j], fmaf(c[i][j], c[i][j], ss));
-            for (int o = p.group >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (h >= h1 || !owner) continue;
-            float y0[4], y1[4];
-            const float r = normed ? rsqrtf(ss * p.inv_dim + p.eps) : 1.f;
+    // All threads take the same number of steps: the shuffles need whole warps.
+    auto heads = [&](auto kind_, const float *src, int from, int to) {
+        constexpr int kind = decltype(kind_)::value;
+        if (from >= to) return;
+        // y0 = r (x0 w0 cos - x1 w1 sin), y1 = r (x0 w0 sin + x1 w1 cos); pairs that do not turn have cos 1, sin 0
+        const float *weight = kind == Q ? p.q_norm : p.k_norm;
+        const bool normed = kind != V && weight != nullptr;
+        float c0[4], s0[4], c1[4], s1[4];
+        if (kind != V) {
+            float w0[4] = {1.f, 1.f, 1.f, 1.f}, w1[4] = {1.f, 1.f, 1.f, 1.f};
+            if (normed && owner) read(weight, true, w0, w1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float v0 = a[i][j], v1 = c[i][j];
-                if (normed) {
-                    v0 = v0 * r * (is_q ? qa[j] : ka[j]);
-                    v1 = v1 * r * (is_q ? qc[j] : kc[j]);
-                }
-                y0[j] = is_v ? v0 : v0 * cs[j] - v1 * sn[j];
-                y1[j] = is_v ? v1 : v0 * sn[j] + v1 * cs[j];
-                // pairs that do not turn pass as they are
-                if (!is_v && u * 4 + j >= half) {
-                    y0[j] = v0;
-                    y1[j] = v1;
-                }
-                if (!live) y0[j] = y1[j] = 0.f;
-            }
-            if (!is_q && !store) continue;
-            const int kh = is_v ? h - p.q_heads - p.c.heads : h - p.q_heads;
-            const bool as_f32 = is_q && p.q_f32;
-            T *dst = is_q   ? static_cast<T *>(p.q_out) + (as_f32 ? 0 : row * p.ldo + (int64_t)h * D)
-                     : is_v ? static_cast<T *>(p.c.v) + page * p.c.v_page + kh * p.c.v_head + off * p.c.v_slot
-                            : static_cast<T *>(p.c.k) + page * p.c.k_page + kh * p.c.k_head + off * p.c.k_slot;
-            float *dst32 = static_cast<float *>(p.q_out) + row * p.ldo + (int64_t)h * D;
-            if constexpr (WIDE) {
-                const bool ap = !is_v && apart;
-                float4 x = ap ? make_float4(y0[0], y0[1], y0[2], y0[3]) : make_float4(y0[0], y1[0], y0[1], y1[1]);
-                float4 y = ap ? make_float4(y1[0], y1[1], y1[2], y1[3]) : make_float4(y0[2], y1[2], y0[3], y1[3]);
-                const int d0 = ap ? e0 : u * 8, d1 = ap ? e1 : u * 8 + 4;
-                if (as_f32) {
-                    *reinterpret_cast<float4 *>(dst32 + d0) = x;
-                    *reinterpret_cast<float4 *>(dst32 + d1) = y;
-                } else {
-                    const uint2 w0 = make_uint2(pack2<T>(x.x, x.y), pack2<T>(x.z, x.w));
-                    const uint2 w1 = make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
-                    if (!ap) {
-                        *reinterpret_cast<uint4 *>(dst + d0) = make_uint4(w0.x, w0.y, w1.x, w1.y);
-                    } else {
-                        *reinterpret_cast<uint2 *>(dst + d0) = w0;
-                        *reinterpret_cast<uint2 *>(dst + d1) = w1;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    int x, y;
-                    place(j, x, y, !is_v);
-                    if (as_f32) {
-                        dst32[x] = y0[j];
-                        dst32[y] = y1[j];
-                    } else {
-                        dst[x] = to_cache<T>(y0[j]);
-                        dst[y] = to_cache<T>(y1[j]);
-                    }
-                }
-            }
-            if (!is_q && !is_v && u == 0) {
-                const int64_t e = (page * p.c.heads + kh) * p.c.page_size + off;
-                if (p.c.weight) p.c.weight[e] = 0.f;
-                if (p.c.pos) p.c.pos[e] = first_pos;
+                const bool turns = u * 4 + j < half;
+                const float cs = turns ? s_cos[u * 4 + j] : 1.f, sn = turns ? s_sin[u * 4 + j] : 0.f;
+                c0[j] = w0[j] * cs, s0[j] = w0[j] * sn, c1[j] = w1[j] * cs, s1[j] = w1[j] * sn;
             }
         }
-    }
+        for (int hb = from; hb < to; hb += lanes * NR_BATCH) {
+            if (kind != first || hb != from) load(src, hb + hl, to, kind != V);
+#pragma unroll
+            for (int i = 0; i < NR_BATCH; ++i) {
+                const int h = hb + hl + i * lanes;
+                if (normed) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) ss = fmaf(a[i][j], a[i][j], fmaf(c[i][j], c[i][j], ss));
+                    for (int o = p.group >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float r = rsqrtf(ss * p.inv_dim + p.eps);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[i][j] *= r, c[i][j] *= r;
+                }
+                if (h >= to || !owner) continue;
+                if (kind != V) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x0 = a[i][j], x1 = c[i][j];
+                        a[i][j] = x0 * c0[j] - x1 * s1[j];
+                        c[i][j] = x0 * s0[j] + x1 * c1[j];
+                    }
+                }
+                if (kind == Q) {
+                    if (p.q_f32) write(static_cast<float *>(p.q_out) + row * p.ldo + (int64_t)h * D, true, a[i], c[i]);
+                    else write(static_cast<T *>(p.q_out) + row * p.ldo + (int64_t)h * D, true, a[i], c[i]);
+                } else if (store) {
+                    write(kind == V ? static_cast<T *>(p.c.v) + page * p.c.v_page + h * p.c.v_head + off * p.c.v_slot
+                                    : static_cast<T *>(p.c.k) + page * p.c.k_page + h * p.c.k_head + off * p.c.k_slot,
+                          kind != V, a[i], c[i]);
+                    if (kind == K && u == 0) {
+                        const int64_t e = (page * kv + h) * p.c.page_size + off;
+                        if (p.c.weight) p.c.weight[e] = 0.f;
+                        if (p.c.pos) p.c.pos[e] = first_pos;
+                    }
+                }
+            }
+        }
+    };
+    heads(std::integral_constant<int, Q>{}, q_src, q0, q1);
+    heads(std::integral_constant<int, K>{}, k_src, k0, k1);
+    heads(std::integral_constant<int, V>{}, v_src, v0, v1);
 }
 
 template <typename T>
@@ -235,6 +246,7 @@ int launch_norm_rope(NormRopeParams &p, cudaStream_t stream)
     // spread over blocks down to one pass of the block's groups each.
     int64_t parts = ((int64_t)sm_count() * 4 + p.rows - 1) / p.rows;
     const int most = (total + lanes - 1) / lanes;
+    if (parts < NRS) parts = NRS;
     if (parts > most) parts = most;
     p.heads_per_block = (int)((total + parts - 1) / parts);
     p.heads_per_block = (p.heads_per_block + lanes - 1) / lanes * lanes;
