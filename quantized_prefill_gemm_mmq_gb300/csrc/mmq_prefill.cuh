@@ -34,9 +34,6 @@ namespace {
 
 namespace pre {
 constexpr int LOADERS = 2;            // warps
-#ifndef TURNS
-#define TURNS 1
-#endif
 constexpr int PARTS = 2;              // of a tile's P, each announced by itself
 constexpr int LAG = 2;                // copies a loader has under way before it waits for the oldest
 constexpr int MAX_SLOTS = 12;
@@ -354,7 +351,7 @@ struct PrefillWalk {
     int at;                    // tile within the unit's span where the next run starts
     int2 span;
     bool begins, ends;         // the run has the unit's first, last tile
-    int total, grid;           // split: tiles of all units, CTAs that have some
+    int each, extra;           // split: CTA c has each + (c < extra) tiles of all units
     int place;                 // split: tiles of all units up to the run's end
     int rest;                  // tiles of the unit after the run
     int asked;                 // whole: units taken over
@@ -373,17 +370,18 @@ struct PrefillWalk {
             return count(prefill_span<RT, TN>(p, w));
         };
         at = place = 0;
-        int W = 0;
-        for (int i = lane; i < pairs; i += 32) W += tiles_of(i);
-        total = W = __reduce_add_sync(0xffffffffu, W) * p.c.heads;
-        grid = min(W, (int)gridDim.x);
-        left = 0;
-        if ((int)blockIdx.x >= grid) return;
-        place = (int)((long long)W * blockIdx.x / grid);
-        left = (int)((long long)W * (blockIdx.x + 1) / grid) - place;
+        const int first32 = tiles_of(lane);
+        int W = first32;
+        for (int i = lane + 32; i < pairs; i += 32) W += tiles_of(i);
+        W = __reduce_add_sync(0xffffffffu, W) * p.c.heads;
+        each = W / (int)gridDim.x;
+        extra = W - each * (int)gridDim.x;
+        place = each * (int)blockIdx.x + min((int)blockIdx.x, extra);
+        left = each + ((int)blockIdx.x < extra ? 1 : 0);
+        if (left == 0) return;
         int before = 0;                                       // tiles before pair i0
         for (int i0 = 0;; i0 += 32) {
-            const int mine = tiles_of(i0 + lane);
+            const int mine = i0 == 0 ? first32 : tiles_of(i0 + lane);
             int upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -404,6 +402,13 @@ struct PrefillWalk {
         }
         prefill_sequence(p, u);
         span = prefill_span<RT, TN>(p, u);
+    }
+
+    // The CTA that has tile x.
+    __device__ __forceinline__ int owner(int x) const
+    {
+        const int first = (each + 1) * extra;
+        return x < first ? x / (each + 1) : extra + (x - first) / each;
     }
 
     // The next run of a CTA with an equal share of all tiles, false when there is none.
@@ -904,12 +909,12 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 #pragma unroll
                 for (int part = 0; part < PARTS; ++part) {
                     if (!waits(sh.p[sb * PARTS + part], NQ == 2 ? g & 1 : (g >> 1) & 1, W_P)) return false;
-                    if (NQ == 2 && TURNS && part == 0 && !waits(sh.turn[i], i == 0 ? (g & 1) ^ 1 : g & 1, W_TURN)) return false;
+                    if (NQ == 2 && part == 0 && !waits(sh.turn[i], i == 0 ? (g & 1) ^ 1 : g & 1, W_TURN)) return false;
                     product_o(sb, vs, part, j > 0 || part > 0, NQ == 1 || !more);
                 }
                 if (NQ == 2) {
                     if (more) product_s(sb, ks, j + 2 == nt);
-                    if (TURNS && lane == 0) mbar_arrive(bar(sh.turn[i ^ 1]));
+                    if (lane == 0) mbar_arrive(bar(sh.turn[i ^ 1]));
                     __syncwarp();
                 }
                 slot = ks;
@@ -1038,7 +1043,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                                 tma_load_4d(dst + ch * (TN * 128), kv ? &p.v_map : &p.k_map, b, ch * 64, off, u.h, pg);
                         if (++slot == p.slots) slot = 0, phase ^= 1;
                     }
-                    flush();                                   // what was copied otherwise before
+                    flush();                                   // what was copied otherwise
                     continue;
                 }
                 const T *ka[BATCH], *va[BATCH];
@@ -1087,8 +1092,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     none = -1;
                 }
                 if (!none && w.begins && !w.ends) {            // the CTA's last run: who has the rest of the unit
-                    const long long end = w.place + w.rest;    // the owner of tile x is the last CTA that starts at or before it
-                    join = make_int2((w.u.b * p.row_tiles + w.u.rt) * p.c.heads + w.u.h, (int)((end * w.grid - 1) / w.total));
+                    join = make_int2((w.u.b * p.row_tiles + w.u.rt) * p.c.heads + w.u.h, w.owner(w.place + w.rest - 1));
                 }
                 if (!waits(sh.run_empty[run_at], run_phase ^ 1, W_RUN)) break;
                 if (lane == 0) {
@@ -1223,12 +1227,13 @@ inline int make_plan(const mmq_kv_cache *c, int q_heads, int new_tokens, Plan &q
     q.chunks = (c->dim + 63) / 64;
     q.ksteps = (c->dim + 15) / 16;
     const int64_t units = (int64_t)c->seqs * c->heads * q.row_tiles, cap = (int64_t)c->cols * c->page_size;
-    if (units > 0x7fffffff || units * ((cap + q.tn - 1) / q.tn) > 0x7fffffff) return MMQ_ERR_SHAPE;
+    if (units > 0x7fffff00 || units * ((cap + q.tn - 1) / q.tn) > 0x7fffff00) return MMQ_ERR_SHAPE;
     const int sms = sm_count();
-#ifndef WHOLE
-#define WHOLE 3
-#endif
-    q.whole = q.row_tiles > 1 && units >= (long long)WHOLE * sms;
+    // A unit per CTA where that keeps the device busy, or where no sequence is so long that cutting it would pay for the
+    // joining launch (5 us): 2048 rows of four heads over 8192 entries (256 units) take 255 us, cut into equal parts 274;
+    // one token over 513 entries of 32 heads 20 and 21.
+    const int64_t waves = (units + sms - 1) / sms;
+    q.whole = (q.row_tiles > 1 && (units >= 3 * sms || units * 5 >= waves * sms * 4)) || cap <= 6 * q.tn;
     q.grid = q.whole ? (int)units : sms;
     q.part_rows = q.rows < q.rt ? q.rows : q.rt;
     q.floats = q.whole ? 4 : 2ll * sms * q.part_rows * (c->dim + 2) + 2ll * sms;
