@@ -663,7 +663,15 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 }
                 if (!wait(bar(sh.s[sb]), sph, abort, W_S)) goto done;
                 tc_fence_after();
+                // With two S buffers the scores come before the last tile's product has been added.  Its barrier is waited for in
+                // every tile before P is announced: one that is left out would be taken for the next but one.
+                auto added = [&]() {
+                    const bool ok = g == 0 || wait(bar(sh.pv[0]), (g - 1) & 1, abort, W_PV);
+                    tc_fence_after();
+                    return ok;
+                };
                 if (!any) {
+                    if (NQ == 1 && !added()) goto done;
                     tc_fence_before();
                     __syncwarp();
                     if (lane < PARTS) mbar_arrive(bar(sh.p[sb * PARTS + lane]));
@@ -749,10 +757,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     const bool large = m != -INFINITY && !(fabsf(m * c) < 4096.f);
                     any_large = __any_sync(0xffffffffu, large);
                     if (tile != u.t0 && __any_sync(0xffffffffu, raise)) {
-                        if (NQ == 1) {                         // the last product may still be adding
-                            if (!wait(bar(sh.pv[0]), (g - 1) & 1, abort, W_PV)) goto done;
-                            tc_fence_after();
-                        }
+                        if (NQ == 1 && !added()) goto done;    // the last product may still be adding
 #pragma unroll 1
                         for (int d = 0; d < p.ksteps * 16; d += 8) scale8(o_col + d, f);
                     }
@@ -787,6 +792,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     if (lane == 0) mbar_arrive(bar(sh.p[sb * PARTS + part]));
                 };
                 static_assert(PARTS == 2, "two parts");
+                if (NQ == 1 && !added()) goto done;
                 store(0);
                 power(W, W + W / 2);
                 stored(0);

@@ -648,3 +648,15 @@ def test_capped_scores_that_are_not_finite(ops):
             cache.k[pg, 0, off, 0] = 3e4                     # as good as infinite: tanh is 1 either way
             cache.k[pg, 0, off, 1:] = 0
             assert torch.equal(got, ops.attn_prefill(cache, q.cuda(), cap=10.0))
+
+
+@pytest.mark.parametrize("lens,H,group,dim,page", [([5000], 8, 1, 128, 7), ([5000], 8, 1, 128, 16), ([3000, 100], 8, 4, 128, 64), ([4000], 4, 2, 256, 24)])
+def test_many_calls_in_a_row_agree(ops, lens, H, group, dim, page):
+    """Few rows and cut units, back to back: whatever the warps' timing, the same bits."""
+    cache = make_cache(ops, lens, H, dim, page, BF16)
+    q = queries(cache, lens, 1, group).cuda()
+    want = check(ops, cache, queries(cache, lens, 1, group), lens)
+    work = ops.prefill_workspace(cache, H * group, 1)
+    outs = torch.stack([ops.attn_prefill(cache, q, workspace=work) for _ in range(600)])
+    ops.check_status()
+    assert bool((outs == want).all())
