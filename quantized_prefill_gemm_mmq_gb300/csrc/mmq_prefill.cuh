@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     const uint32_t row = ring + vslot * slot_bytes + e * 128;
                     auto piece = [&](int k) { return row + (k >> 3) * (TN * 128) + (((k & 7) ^ (e & 7)) << 4); };
                     uint32_t acc = 0;
-#pragma unroll 4
+#pragma unroll 1
                     for (int k = at % PER; k < p.c.dim / 8; k += PER) {
                         uint32_t v[4];
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(piece(k)) : "memory");
@@ -1290,25 +1290,22 @@ struct Call {
 };
 
 // Tensor maps of K and V, where boxes of at least eight entries fit the pages (and the swizzle's groups of eight rows), and of
-// q, where a box holds whole tokens.
-int make_maps(PrefillParams &p, const Plan &q)
+// q, where a box holds whole tokens.  A layout that has no map is copied row by row.
+void make_maps(PrefillParams &p, const Plan &q)
 {
     const mmq_kv_cache &c = p.c;
     const CUtensorMapDataType type = c.dtype == MMQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (c.dim < 64) return MMQ_OK;                             // a box is 64 values wide
-    if (128 % p.group == 0) {
+    if (c.dim < 64) return;                                    // a box is 64 values wide
+    constexpr uint64_t kMostStride = 1ull << 40;
+    if (128 % p.group == 0 && (uint64_t)p.ldq * 2 < kMostStride) {
         const uint64_t dims[4] = {(uint64_t)c.dim, (uint64_t)p.q_heads, (uint64_t)c.seqs * p.new_tokens, 1};
         const uint64_t strides[3] = {(uint64_t)c.dim * 2, (uint64_t)p.ldq * 2, 16};
         const uint32_t extent[4] = {64, (uint32_t)p.group, (uint32_t)(128 / p.group), 1};
-        if (strides[1] < 1ull << 40) {
-            const int rc = make_tmap_4d(&p.q_map, p.q, type, dims, strides, extent, CU_TENSOR_MAP_SWIZZLE_128B);
-            if (rc != MMQ_OK) return rc;
-            p.q_box = 1;
-        }
+        p.q_box = make_tmap_4d(&p.q_map, p.q, type, dims, strides, extent, CU_TENSOR_MAP_SWIZZLE_128B) == MMQ_OK;
     }
     int box = 1;
     while (2 * box <= q.tn && c.page_size % (2 * box) == 0) box *= 2;
-    if (box < 8) return MMQ_OK;
+    if (box < 8) return;
     const uint64_t dims[4] = {(uint64_t)c.dim, (uint64_t)c.page_size, (uint64_t)c.heads, (uint64_t)c.pages};
     const uint32_t extent[4] = {64, (uint32_t)box, 1, 1};
     for (int kv = 0; kv < 2; ++kv) {
@@ -1316,13 +1313,11 @@ int make_maps(PrefillParams &p, const Plan &q)
                                (uint64_t)(kv ? c.v_page : c.k_page) * 2};
         for (int i = 0; i < 3; ++i) {
             if (dims[i + 1] == 1) strides[i] = 16;             // never used
-            if (strides[i] == 0 || strides[i] >= 1ull << 40) return MMQ_OK;
+            if (strides[i] == 0 || strides[i] >= kMostStride) return;
         }
-        const int rc = make_tmap_4d(kv ? &p.v_map : &p.k_map, kv ? c.v : c.k, type, dims, strides, extent, CU_TENSOR_MAP_SWIZZLE_128B);
-        if (rc != MMQ_OK) return rc;
+        if (make_tmap_4d(kv ? &p.v_map : &p.k_map, kv ? c.v : c.k, type, dims, strides, extent, CU_TENSOR_MAP_SWIZZLE_128B) != MMQ_OK) return;
     }
     p.box = box;
-    return MMQ_OK;
 }
 
 int attend(const mmq_kv_cache *cache, const Call &a, mmq_stream_t stream)
@@ -1372,7 +1367,7 @@ int attend(const mmq_kv_cache *cache, const Call &a, mmq_stream_t stream)
     p.joins = reinterpret_cast<int2 *>(p.part_ml + 2ll * q.grid * q.part_rows);
     p.page_div = FastDiv(cache->page_size);
     p.group_div = FastDiv(p.group);
-    if ((rc = make_maps(p, q)) != MMQ_OK) return rc;
+    make_maps(p, q);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return cache->dtype == MMQ_F16 ? launch_any<__half>(p, q, st) : launch_any<__nv_bfloat16>(p, q, st);
 }

@@ -660,3 +660,48 @@ def test_many_calls_in_a_row_agree(ops, lens, H, group, dim, page):
     outs = torch.stack([ops.attn_prefill(cache, q, workspace=work) for _ in range(600)])
     ops.check_status()
     assert bool((outs == want).all())
+
+
+def test_units_taken_over_in_graphs_and_on_two_streams(ops):
+    """Calls with more units than the device has multiprocessors (CTAs take over units of those that have not started):
+    captured and replayed, and two at once on streams of their own."""
+    lens, N = [900, 950], 900
+    caches = [make_cache(ops, lens, 32, 64, 16, dt) for dt in (BF16, F16)]
+    qs = [queries(c, lens, N, 2).cuda() for c in caches]
+    want = [ops.attn_prefill(c, q, window=300) for c, q in zip(caches, qs)]
+    out = [torch.empty_like(w) for w in want]
+    work = [ops.prefill_workspace(c, 64, N) for c in caches]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        for i in range(2):
+            ops.attn_prefill(caches[i], qs[i], window=300, out=out[i], workspace=work[i])
+    for _ in range(5):
+        for o in out:
+            o.fill_(3)
+        g.replay()
+        assert all(torch.equal(o, w) for o, w in zip(out, want))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for o in out:
+        o.fill_(3)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                ops.attn_prefill(caches[i], qs[i], window=300, out=out[i], workspace=work[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(out, want))
+    ops.check_status()
+
+
+def test_layouts_without_tensor_copies(ops):
+    """Heads that share one key-value row (a stride of 0), and a cache of one page: the same as laid out plainly."""
+    g = torch.Generator().manual_seed(8)
+    one = torch.randn((2, 6, 1, 16, 64), generator=g).to(BF16).cuda()
+    table, lens = torch.arange(6, dtype=torch.int32).view(1, 6).cuda(), dev([90])
+    shared = ops.KVCache(*(x.expand(6, 3, 16, 64) for x in one), table, lens)
+    plain = ops.KVCache(*(x.expand(6, 3, 16, 64).contiguous() for x in one), table, lens)
+    q = queries(plain, [90], 20, 2).cuda()
+    assert torch.equal(ops.attn_prefill(shared, q), ops.attn_prefill(plain, q))
+    single = ops.KVCache(*(x[:1].expand(1, 3, 16, 64).contiguous() for x in one), table[:, :1].contiguous(), dev([13]))
+    check(ops, single, queries(single, [13], 5, 2), [13])
