@@ -1157,40 +1157,50 @@ __global__ void __launch_bounds__(128) prefill_join_kernel(const __grid_constant
     for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 4) {
         // the part that begins the unit is its CTA's second, the others are their CTAs' first
         auto at = [&](int i) { return (2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.part_rows + r; };
-        float top = -INFINITY;
-        for (int i = lane; i < n; i += 32) {
-            const float2 ml = p.part_ml[at(i)];
-            if (ml.y > 0.f) top = fmaxf(top, ml.x);
+        auto weighed = [&](int i) { return i < n ? p.part_ml[at(i)] : make_float2(-INFINITY, 0.f); };
+        constexpr int BATCH = 4;                               // parts whose sums are loaded together, the first before their weights
+        float4 v[BATCH][2];
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (i0 + i < n && (lane + 32 * e) * 4 < p.c.dim)
+                        v[i][e] = reinterpret_cast<const float4 *>(p.part + at(i0 + i) * p.c.dim)[lane + 32 * e];
+        };
+        float2 ml = weighed(lane);
+        load(0);
+        float top = ml.y > 0.f ? ml.x : -INFINITY;
+        for (int i = lane + 32; i < n; i += 32) {
+            const float2 w = weighed(i);
+            if (w.y > 0.f) top = fmaxf(top, w.x);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         float sum = 0.f;
         float4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         for (int i0 = 0; i0 < n; i0 += 32) {
+            if (i0 > 0) ml = weighed(i0 + lane);
             float wt = 0.f;
-            if (i0 + lane < n) {
-                const float2 ml = p.part_ml[at(i0 + lane)];
-                if (ml.y > 0.f) {
-                    const bool exact = fabsf(ml.x * c) < 4096.f && fabsf(top * c) < 4096.f;
-                    wt = pow2(exact ? __fmul_rn(ml.x, c) - __fmul_rn(top, c) : (ml.x - top) * c);
-                }
-                sum += ml.y > 0.f ? wt * ml.y : ml.y;          // 0, or a NaN
+            if (ml.y > 0.f) {
+                const bool exact = fabsf(ml.x * c) < 4096.f && fabsf(top * c) < 4096.f;
+                wt = pow2(exact ? __fmul_rn(ml.x, c) - __fmul_rn(top, c) : (ml.x - top) * c);
             }
-            const int k = min(32, n - i0);
-#pragma unroll 4
-            for (int i = 0; i < k; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, wt, i);
-                if (wi == 0.f) continue;
-                const float4 *src = reinterpret_cast<const float4 *>(p.part + at(i0 + i) * p.c.dim);
+            sum += ml.y > 0.f ? wt * ml.y : ml.y;              // 0, or a NaN
+            for (int j = 0; j < 32 && i0 + j < n; j += BATCH) {
+                if (i0 + j > 0) load(i0 + j);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int d = lane + 32 * e;
-                    if (d * 4 >= p.c.dim) continue;
-                    const float4 v = src[d];
-                    acc[e].x = fmaf(wi, v.x, acc[e].x);
-                    acc[e].y = fmaf(wi, v.y, acc[e].y);
-                    acc[e].z = fmaf(wi, v.z, acc[e].z);
-                    acc[e].w = fmaf(wi, v.w, acc[e].w);
+                for (int i = 0; i < BATCH; ++i) {
+                    const float wi = __shfl_sync(0xffffffffu, wt, j + i);
+                    if (wi == 0.f) continue;                   // not there, or nothing in it
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if ((lane + 32 * e) * 4 >= p.c.dim) continue;
+                        acc[e].x = fmaf(wi, v[i][e].x, acc[e].x);
+                        acc[e].y = fmaf(wi, v[i][e].y, acc[e].y);
+                        acc[e].z = fmaf(wi, v[i][e].z, acc[e].z);
+                        acc[e].w = fmaf(wi, v[i][e].w, acc[e].w);
+                    }
                 }
             }
         }
