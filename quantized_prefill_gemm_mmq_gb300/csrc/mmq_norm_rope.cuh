@@ -9,9 +9,14 @@
 //
 // Bound by memory: per row 4 + (4 or 2) bytes per q value and 6 per k and v
 // value.  Eight values of a head (four pairs) lie with one thread, a head with a
-// group of 1 to 32 neighbouring threads that add their squares by shuffles; a
-// block's groups take heads side by side, with several heads' loads under way,
-// and the row's sines are computed once per block meanwhile.
+// group of 1 to 32 neighbouring threads that add their squares by shuffles.  A
+// block takes a row (or part of its heads): its groups take heads side by side,
+// two ahead, and the row's sines are computed once while the first ones come.
+// q, k and v heads have a loop each, and the norm's weights are folded into the
+// sines and cosines: with one loop that asked for every head what it is, the
+// instructions took longer than the memory (4096 rows of 32 + 2*32 heads of 128,
+// f16: 89 us, and 62 now = 4.9 TB/s; three heads ahead 70 us, more blocks per row
+// 76).  512 rows and up are bound by memory, a single row (3.3 us) by latency.
 #pragma once
 
 #include <type_traits>
@@ -20,12 +25,8 @@ namespace mmq {
 namespace {
 
 constexpr int NR_THREADS = 256;
-#ifndef NRB
-#define NRB 2
-#define NRM 4
-#define NRS 1
-#endif
-constexpr int NR_BATCH = NRB, NR_BLOCKS = NRM;          // heads whose loads a thread has in flight
+constexpr int NR_BATCH = 2;          // heads whose loads a thread has in flight
+constexpr int NR_BLOCKS = 4;         // resident blocks per multiprocessor
 
 struct NormRopeParams {
     mmq_kv_cache c;
@@ -246,7 +247,6 @@ int launch_norm_rope(NormRopeParams &p, cudaStream_t stream)
     // spread over blocks down to one pass of the block's groups each.
     int64_t parts = ((int64_t)sm_count() * 4 + p.rows - 1) / p.rows;
     const int most = (total + lanes - 1) / lanes;
-    if (parts < NRS) parts = NRS;
     if (parts > most) parts = most;
     p.heads_per_block = (int)((total + parts - 1) / parts);
     p.heads_per_block = (p.heads_per_block + lanes - 1) / lanes * lanes;

@@ -11,20 +11,47 @@
 //
 // Work.  The `group` query heads that share a key-value head are rows beside the
 // tokens: row r is token r / group and head r % group.  A unit is 128 or 256
-// rows of one sequence and head.  K and V tiles are gathered through the page
-// table into a ring in shared memory, 128-byte swizzled; S = Q K^T and O += P V
-// run on the tensor core (tcgen05, accumulators in tensor memory), one thread
-// issuing; a warpgroup per 128 rows reads S (one row per thread), writes P over
-// it in the cache's type and keeps m and the sum in f32.  V is used as it lies:
-// its operand is the transposed form of the same swizzle.  With 256 rows the two
-// halves take turns, so that the tensor core works on one while the other's
-// exponentials are computed, and one K and V tile serves both; with up to 128
-// rows S has two buffers instead.
+// rows of one sequence and head.  What bounds it is the tensor core (4 dim flops
+// per row and entry) for prompts, memory (4 dim bytes per entry and head) for
+// few rows.
 //
-// Where units are many, every CTA takes one, the longest first.  Otherwise all
-// tiles of all units are numbered in a row and every CTA takes an equal part;
-// units that are cut leave (max, sum, sum p v) in the workspace, and a second
-// launch joins them in order.
+// Roles.  Q, K and V come through tensor copies (boxes of one page's entries; row
+// by row with cp.async where pages or strides allow none) into a ring in shared
+// memory, 128-byte swizzled.  S = Q K^T and O += P V run on the tensor core
+// (tcgen05, sums in tensor memory), one thread per 128 rows issuing; V is used
+// as it lies, its operand is the transposed form of the same swizzle.  One warp
+// of every four reads S of 32 rows, one row per thread, writes P over it in the
+// cache's type, and keeps maximum and sum in f32.  With 256 rows one K and V tile
+// serves both halves, and the halves take turns on the tensor core; with up to
+// 128 rows S has two buffers instead.  One loader warp finds the CTA's units and
+// tells the others.
+//
+// Units.  Where they are many every CTA takes one, the longest first, and then
+// those whose CTAs have not started (cluster launch control).  Otherwise all tiles
+// of all units are numbered in a row and every CTA takes an equal part; units that
+// are cut leave (max, sum, sum p v) in the workspace, and a second launch joins
+// them in order.  No result depends on timing.
+//
+// What the time went to, and what it took (a prompt of 4096 rows of 32 heads of
+// 128, f16, whose beginning sees itself whole; 149 GFLOP):
+//   330 us  everything copied row by row, one issuing thread for both halves
+//   232     tensor copies; registers moved from the other warps to the softmax
+//   204     products issued under elect.sync: an issue took 156 cycles, 64 now; the
+//           halves take turns (together they wait for scores, then for products)
+//   181     Q, and tiles that rows see in part, by tensor copies as well
+//   156     capped, biased and masked scores are worked over in tensor memory in a
+//           rolled loop: unrolled, the code did not stay in the instruction cache
+//   146     exponentials begin with the maximum so far; nothing is spilled (local
+//           memory shares its path with the tensor core's operands: 604 bytes of
+//           it cost 30 to 70 %)
+// It is 1.0 PFLOP/s, 0.52 of cuBLAS' burst rate; 2048 rows of four heads over a
+// window of 8192 entries, bf16, 245 us = 1.12 PFLOP/s (0.58), the tensor pipe 57 %
+// active.  A tile of 256 rows takes 3300 cycles, its products 2048: the chain scores
+// -> exponentials -> P -> products of one half is longer than the other half's
+// products.  Not kept: two threads per row (212 us: they swap maxima through shared
+// memory, where a word takes some 200 cycles while operands are read), reading the
+// scores twice instead of holding 128 of them (172), caps applied in registers
+// (671 us and 442 for 8192 rows under a cap: code size again).
 #pragma once
 
 #include <type_traits>
