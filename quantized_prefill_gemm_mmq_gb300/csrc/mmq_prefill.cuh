@@ -136,6 +136,18 @@ __device__ __forceinline__ uint64_t pair(float a, float b)
     return r;
 }
 __device__ __forceinline__ void unpair(uint64_t x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t r;
@@ -193,15 +205,30 @@ __device__ __forceinline__ void cap32(uint32_t at, uint32_t (&y)[32], float cap_
 #pragma unroll
     for (int j = 0; j < 32; j += 2) nan = max3_nan(nan, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
     const bool any_nan = __any_sync(0xffffffffu, nan != nan);
+    const uint64_t in2 = pair(cap_in, cap_in), one2 = pair(1.f, 1.f), out2 = pair(cap_out, cap_out);
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
+        // d = 1 + e^ of the elements 0 and 2, 1 and 3: the pairs' products are (lo, hi)
         float d[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = 1.f + fminf(pow2(__uint_as_float(y[k + j]) * cap_in), 0x1p30f);
-        const float lo = d[0] * d[1], hi = d[2] * d[3], r = rcp(lo * hi) * (-2.f * cap_out), rlo = r * hi, rhi = r * lo;
-        const float z[4] = {fmaf(rlo, d[1], cap_out), fmaf(rlo, d[0], cap_out), fmaf(rhi, d[3], cap_out), fmaf(rhi, d[2], cap_out)};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[k + j] = __float_as_uint(z[j]);
+        for (int j = 0; j < 4; j += 2) {
+            float a, b;
+            unpair(mul2(pair(__uint_as_float(y[k + j]), __uint_as_float(y[k + j + 1])), in2), a, b);
+            d[j] = fminf(pow2(a), 0x1p30f);
+            d[j + 1] = fminf(pow2(b), 0x1p30f);
+        }
+        const uint64_t even = add2(pair(d[0], d[2]), one2), odd = add2(pair(d[1], d[3]), one2), both = mul2(even, odd);
+        float lo, hi;
+        unpair(both, lo, hi);
+        const float r = rcp(lo * hi) * (-2.f * cap_out);
+        const uint64_t inv = mul2(pair(hi, lo), pair(r, r));
+        float z0, z1, z2, z3;
+        unpair(fma2(inv, odd, out2), z0, z2);
+        unpair(fma2(inv, even, out2), z1, z3);
+        y[k] = __float_as_uint(z0);
+        y[k + 1] = __float_as_uint(z1);
+        y[k + 2] = __float_as_uint(z2);
+        y[k + 3] = __float_as_uint(z3);
     }
     if (any_nan) {
         uint32_t was[32];
@@ -744,10 +771,10 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 #pragma unroll
                     for (int k = part * W; k < (part + 1) * W; k += 32) tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(x[k]));
                 };
-                float top[2];
+                float top;
                 auto largest = [&](int k0, int k1) {
 #pragma unroll
-                    for (int k = k0; k < k1; k += 2) top[k / 2 & 1] = max3(top[k / 2 & 1], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                    for (int k = k0; k < k1; k += 2) top = max3(top, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
                 };
                 uint64_t sum;
                 float by = c, add = off;
@@ -764,13 +791,13 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     load(0);
                     loaded(0);
                     load(1);                                   // under way during the first part's exponentials
-                    top[0] = top[1] = -INFINITY;
+                    top = -INFINITY;
                     largest(0, W);
                     sum = 0;
                     power(0, W);
                     loaded(1);
                     largest(W, TN);
-                    const float mx = fmaxf(top[0], top[1]);
+                    const float mx = top;
                     const bool raise = mx > m && !((mx - m) * c <= kLazy);
                     if (again || !__any_sync(0xffffffffu, raise || any_large)) break;
                     float f = 1.f;
