@@ -44,14 +44,17 @@
 //   146     exponentials begin with the maximum so far; nothing is spilled (local
 //           memory shares its path with the tensor core's operands: 604 bytes of
 //           it cost 30 to 70 %)
-// It is 1.0 PFLOP/s, 0.52 of cuBLAS' burst rate; 2048 rows of four heads over a
-// window of 8192 entries, bf16, 245 us = 1.12 PFLOP/s (0.58), the tensor pipe 57 %
+//   144     packed arithmetic under a cap, one chain for the maximum
+// It is 1.0 PFLOP/s, 0.54 of cuBLAS' burst rate; 2048 rows of four heads over a
+// window of 8192 entries, bf16, 233 us = 1.2 PFLOP/s (0.61), the tensor pipe 57 %
 // active.  A tile of 256 rows takes 3300 cycles, its products 2048: the chain scores
 // -> exponentials -> P -> products of one half is longer than the other half's
 // products.  Not kept: two threads per row (212 us: they swap maxima through shared
 // memory, where a word takes some 200 cycles while operands are read), reading the
 // scores twice instead of holding 128 of them (172), caps applied in registers
-// (671 us and 442 for 8192 rows under a cap: code size again).
+// (671 us and 442 for 8192 rows under a cap: code size again).  Trees of 48 nodes over 16 sequences of up to
+// 16384 entries (8 heads of 128, groups of four) take 146 us = 4.4 TB/s, one token
+// over 513 entries of 32 heads 20 us.
 #pragma once
 
 #include <type_traits>
@@ -1300,7 +1303,7 @@ inline int make_plan(const mmq_kv_cache *c, int q_heads, int new_tokens, Plan &q
     if (units > 0x7fffff00 || units * ((cap + q.tn - 1) / q.tn) > 0x7fffff00) return MMQ_ERR_SHAPE;
     const int sms = sm_count();
     // A unit per CTA where that keeps the device busy, or where no sequence is so long that cutting it would pay for the
-    // joining launch (5 us): 2048 rows of four heads over 8192 entries (256 units) take 255 us, cut into equal parts 274;
+    // joining launch (5 us): 2048 rows of four heads over 8192 entries (256 units) took 255 us, cut into equal parts 274;
     // one token over 513 entries of 32 heads 20 and 21.
     const int64_t waves = (units + sms - 1) / sms;
     q.whole = (q.row_tiles > 1 && (units >= 3 * sms || units * 5 >= waves * sms * 4)) || cap <= 6 * q.tn;
