@@ -705,3 +705,55 @@ def test_layouts_without_tensor_copies(ops):
     assert torch.equal(ops.attn_prefill(shared, q), ops.attn_prefill(plain, q))
     single = ops.KVCache(*(x[:1].expand(1, 3, 16, 64).contiguous() for x in one), table[:, :1].contiguous(), dev([13]))
     check(ops, single, queries(single, [13], 5, 2), [13])
+
+
+def test_many_ragged_sequences(ops):
+    """More sequences than a warp looks at in one go, empty ones among them, in caches long enough to be cut up."""
+    g = torch.Generator().manual_seed(12)
+    lens = torch.randint(0, 60, (75,), generator=g).tolist()
+    lens[3], lens[40], lens[74], lens[0] = 0, 1500, 900, 0
+    new = [min(n, 2) for n in lens]
+    cache = make_cache(ops, lens, 2, 64, 16, BF16)
+    got = check(ops, cache, queries(cache, lens, 2, 3), lens, new=new)
+    assert bool((got.view(75, 2, -1)[3] == 0).all())
+    parents, words = trees(75, 2)
+    check(ops, cache, queries(cache, lens, 2, 3), lens, new=new, tree=words)
+
+
+@pytest.mark.parametrize("H,group,N,dim", [(1, 128, 1, 64), (1, 128, 3, 128), (2, 96, 2, 160), (1, 5, 60, 184)])
+def test_wide_groups(ops, H, group, N, dim):
+    lens = [700, 90]
+    cache = make_cache(ops, lens, H, dim, 24, F16)
+    check(ops, cache, queries(cache, lens, N, group), lens)
+
+
+def test_limits_of_what_rows_see(ops):
+    """Prefixes past the length or negative, documents that begin before the cache, windows longer than anything."""
+    lens, N = [300, 64], 64
+    cache = make_cache(ops, lens, 1, 64, 16)
+    q = queries(cache, lens, N, 2)
+    check(ops, cache, q, lens, prefix=[1 << 30, -5], first=[[-3] * N, [t - 10 for t in range(N)]], window=(1 << 31) - 1)
+
+
+@pytest.mark.parametrize("out_dtype,offset", [(F32, 4), (BF16, 8)])
+def test_outputs_that_begin_on_16_bytes(ops, out_dtype, offset):
+    lens, N = [1100], 20
+    cache = make_cache(ops, lens, 2, 128, 16, BF16)
+    q = queries(cache, lens, N, 2).cuda()
+    want = ops.attn_prefill(cache, q, out_dtype=out_dtype)
+    buf = torch.full((N * 4 * 128 + 64,), 7.0, dtype=out_dtype).cuda()
+    out = buf[offset:offset + N * 4 * 128].view(N, 4, 128)
+    ops.attn_prefill(cache, q, out=out)
+    ops.check_status()
+    assert torch.equal(out, want) and bool((buf[:offset] == 7).all()) and bool((buf[offset + N * 4 * 128:] == 7).all())
+
+
+def test_keep_nothing_and_everything(ops):
+    cache = make_cache(ops, [40, 30], 2, 64, 16)
+    before = [x.clone() for x in (cache.k, cache.v, cache.weight)]
+    ops.kv_keep(cache, dev([[0, 1, 2, 3]] * 2), None, 4)                 # already in place
+    ops.kv_keep(cache, dev([[2, 3]] * 2), dev([0, 0]), 4)                # nothing stays
+    ops.kv_keep(cache, dev([[2, 3]] * 2), None, 4, new=dev([0, 0]))      # no nodes: indexes past them are reported
+    with pytest.raises(RuntimeError, match="a kept node"):
+        ops.check_status()
+    assert all(torch.equal(a, b) for a, b in zip((cache.k, cache.v, cache.weight), before))
