@@ -737,6 +737,8 @@ def attn_prefill(cache: KVCache, q: torch.Tensor, scale: float | None = None, ca
     if index != _current():
         with torch.cuda.device(index):
             return attn_prefill(cache, q, scale, cap, slopes, window, prefix, first, new, out_dtype, out, workspace)
+    if not -(1 << 31) <= window < 1 << 31:               # ctypes would cut it
+        raise ValueError("window must be 0 (none) to 2^31 - 1")
     q_heads, n, ldq, out, workspace = _prefill_plan(cache, q, out, out_dtype, workspace)
     if slopes is not None:
         _need(slopes, "slopes", torch.float32, (q_heads,), index)

@@ -757,3 +757,11 @@ def test_keep_nothing_and_everything(ops):
     with pytest.raises(RuntimeError, match="a kept node"):
         ops.check_status()
     assert all(torch.equal(a, b) for a, b in zip((cache.k, cache.v, cache.weight), before))
+
+
+@pytest.mark.parametrize("window", [1 << 31, (1 << 32) + 5, -(1 << 32) + 5])
+def test_windows_that_no_int32_holds(ops, window):
+    """Refused; the last two would be windows of five entries, cut to 32 bits."""
+    cache = make_cache(ops, [40], 1, 64, 16)
+    with pytest.raises(ValueError, match="window"):
+        ops.attn_prefill(cache, queries(cache, [40], 4, 2).cuda(), window=window)
