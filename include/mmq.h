@@ -692,10 +692,12 @@ int mmq_check_status(mmq_stream_t stream, int *detail);
  * kernel's pipeline wait may take before it gives up (wait_limit_us > 0; <= 0
  * restores the default of 2 s) and a mode: 0 = off; 1 = the production q4_K
  * kernels (mmq_gemm_q4K, mmq_gemm_q4K_splitk*, mmq_gemm_q5K) withhold the raw
- * weight copy of their second super-block (K >= 512), so the waits for it run
+ * weight copy of their second super-block (K >= 512), and prompt and tree
+ * attention (mmq_attn_prefill, mmq_attn_tree) the last tile of K of every run
+ * of tiles that a CTA takes, so the waits for it run
  * out: the kernel records MMQ_ERR_TIMEOUT (see mmq_check_status), stops every
- * role, drains the work it issued, frees its tensor memory and returns; its y
- * is undefined.  Synchronous with respect to the host.  Returns MMQ_OK,
+ * role, drains the work it issued, frees its tensor memory and returns; its
+ * output is undefined.  Synchronous with respect to the host.  Returns MMQ_OK,
  * MMQ_ERR_SHAPE (unknown mode) or MMQ_ERR_CUDA.  Leave it at mode 0 outside
  * tests.
  */

@@ -198,7 +198,7 @@ extern "C" int mmq_debug_fault_inject(int mode, int wait_limit_us)
         cudaGetLastError();
         return MMQ_ERR_CUDA;
     }
-    return MMQ_OK;
+    return mmq::set_prompt_faults(mode, lim);
 }
 
 // extra detail of the last failure reported by mmq_check_status (host side)

@@ -23,6 +23,8 @@ int launch_status();
 int take_serve_status(int (&h)[8]);
 // The same of the unit with the operators for prompts and trees of drafts.
 int take_prompt_status(int (&h)[8]);
+// mmq_debug_fault_inject for that unit.
+int set_prompt_faults(int mode, unsigned long long wait_limit_ns);
 
 // 2-D tiled tensor map over a row-major array: `inner` elements per row of
 // `elem_bytes` each, `rows` rows, `row_stride_bytes` apart; box of

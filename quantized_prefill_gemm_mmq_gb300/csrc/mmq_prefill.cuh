@@ -317,6 +317,7 @@ struct PrefillParams {
     int2 *joins;
     FastDiv page_div, group_div;
     int q_box;                 // q rows come by tensor copies
+    int withhold;              // test-only: the last K tile of a run never comes
     CUtensorMap k_map, v_map;  // [pages][heads][page_size][dim], boxes of 64 values of `box` entries
     CUtensorMap q_map;         // [rows][q_heads][dim], boxes of 64 values of a group's heads of 128/group tokens
 };
@@ -1051,7 +1052,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             flush();
             return wait(bar(b), parity, abort, site);
         };
-        int runs = 0, slot = 0, phase = 0;
+        int runs = 0, slot = 0, phase = 0;                     // runs: whose q is copied
         auto load = [&](const PrefillUnit &u) {
             if (!waits(sh.q_empty, (runs & 1) ^ 1, W_QEMPTY)) return false;
             if (p.q_box) {                                     // rows of other sequences, or zeros, in place of rows that are not there
@@ -1077,6 +1078,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 }
                 push(bar(sh.q_full));
             }
+            ++runs;
             for (int tile = u.t0; tile < u.t1; ++tile) {
                 if (p.box) {                                   // boxes of entries of one page
                     const int boxes = TN / p.box;
@@ -1096,12 +1098,13 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                         const uint32_t b = bar(sh.full[slot]), dst = ring + slot * slot_bytes + lane * p.box * 128;
                         if (lw == 0 && lane < TN / 32) sh.bad[slot][lane] = 0;
                         __syncwarp();
-                        if (lane == 0) {
+                        const bool skip = p.withhold && lw == 0 && kv == 0 && tile == u.t1 - 1;
+                        if (lane == 0 && !skip) {
                             if (many) mbar_arrive_expect_tx(b, (uint32_t)(many * p.chunks * p.box * 128));
                             else mbar_arrive(b);
                         }
                         __syncwarp();
-                        if (mine)
+                        if (mine && !skip)
                             for (int ch = 0; ch < p.chunks; ++ch)
                                 tma_load_4d(dst + ch * (TN * 128), kv ? &p.v_map : &p.k_map, b, ch * 64, off, u.h, pg);
                         if (++slot == p.slots) slot = 0, phase ^= 1;
@@ -1126,15 +1129,16 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     if (!waits(sh.empty[slot], phase ^ 1, W_EMPTY)) return false;
-#pragma unroll
-                    for (int bt = 0; bt < BATCH; ++bt)
-                        copy_rows(kv ? va[bt] : ka[bt], ring + slot * slot_bytes, (bt * LOADERS + lw) * 32, TN * 128);
                     if (lw == 0 && lane < TN / 32) sh.bad[slot][lane] = 0;
-                    push(bar(sh.full[slot]));
+                    if (!(p.withhold && lw == 0 && kv == 0 && tile == u.t1 - 1)) {
+#pragma unroll
+                        for (int bt = 0; bt < BATCH; ++bt)
+                            copy_rows(kv ? va[bt] : ka[bt], ring + slot * slot_bytes, (bt * LOADERS + lw) * 32, TN * 128);
+                        push(bar(sh.full[slot]));
+                    }
                     if (++slot == p.slots) slot = 0, phase ^= 1;
                 }
             }
-            ++runs;
             return true;
         };
         bool ok = true;
@@ -1178,14 +1182,16 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             }
         }
         flush();
-        if (!ok || *abort) {                                   // a wait ran out: the copies under way still come to their end
+        // A wait ran out: the copies under way still come to their end.  Each barrier is waited for in the phase of this warp's
+        // last copy; where one runs out here too (the other warp had no copy to add), all copies have had that time.
+        if (!ok || *abort) {
             uint32_t never = 0;
             for (int i = 0; i < p.slots; ++i) {
                 const int before = i < slot ? phase : phase ^ 1;       // of the slot's last copy; none: over already
                 if (lane == 0 && p.box) mbar_wait(bar(sh.full[i]), (uint32_t)before, &never, KID_PREFILL, W_DRAIN);
             }
             if (lane == 0 && asking >= 0) mbar_wait(bar(sh.next), (uint32_t)asking, &never, KID_PREFILL, W_DRAIN);
-            if (lane == 0 && p.q_box) mbar_wait(bar(sh.q_full), (uint32_t)(runs & 1), &never, KID_PREFILL, W_DRAIN);
+            if (lane == 0 && p.q_box && runs > 0) mbar_wait(bar(sh.q_full), (uint32_t)((runs - 1) & 1), &never, KID_PREFILL, W_DRAIN);
             __syncwarp();
         }
     }
@@ -1434,6 +1440,7 @@ int attend(const mmq_kv_cache *cache, const Call &a, mmq_stream_t stream)
     p.joins = reinterpret_cast<int2 *>(p.part_ml + 2ll * q.grid * q.part_rows);
     p.page_div = FastDiv(cache->page_size);
     p.group_div = FastDiv(p.group);
+    p.withhold = withheld();
     make_maps(p, q);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return cache->dtype == MMQ_F16 ? launch_any<__half>(p, q, st) : launch_any<__nv_bfloat16>(p, q, st);

@@ -23,6 +23,31 @@ int take_prompt_status(int (&h)[8])
     return MMQ_OK;
 }
 
+namespace {
+
+// mmq_debug_fault_inject's mode, of each device: part of the launch here, so that the kernels need not read it.
+std::atomic<int> g_withhold[64];
+
+int withheld()
+{
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 ? g_withhold[dev].load(std::memory_order_relaxed) : 0;
+}
+
+}  // namespace
+
+int set_prompt_faults(int mode, unsigned long long wait_limit_ns)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaMemcpyToSymbol(g_wait_limit_ns, &wait_limit_ns, sizeof(wait_limit_ns)) != cudaSuccess) {
+        cudaGetLastError();
+        return MMQ_ERR_CUDA;
+    }
+    if (dev < 64) g_withhold[dev].store(mode, std::memory_order_relaxed);
+    return MMQ_OK;
+}
+
 }  // namespace mmq
 
 #include "mmq_norm_rope.cuh"
