@@ -680,7 +680,8 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                 };
                 // In a tile that some row of the unit sees in part only, entries of V that are not finite are taken as 0
                 // (0 times them would be NaN in rows that do not see them) and noted: a row that sees one is not finite.
-                // The halves both look, whoever comes first: a value is noted before it is taken away.
+                // The halves both look, and both take away what either has noted (a half that comes second may find zeros
+                // already): a half's product reads V after that half's own stores, fenced before its P is announced.
                 const bool scan = e0 < u.max_lo || e0 + TN > u.min_hi;
                 if (scan) {
                     if (!wait(bar(sh.full[vslot]), vphase, abort, W_V)) goto done;
@@ -697,22 +698,24 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc |= (v[i] & 0x7fff7fffu) + one;
                     }
-                    const bool bad = (acc & 0x80008000u) != 0;
-                    if (__any_sync(0xffffffffu, bad)) {
-                        if (bad) {
-                            atomicOr(&sh.bad[vslot][e >> 5], 1u << (e & 31));
-                            __threadfence_block();
-                            for (int k = at % PER; k < p.c.dim / 8; k += PER)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(piece(k)), "r"(0u) : "memory");
-                            fence_proxy_async_smem();
-                        }
-                        __syncwarp();
-                    }
+                    if ((acc & 0x80008000u) != 0) atomicOr(&sh.bad[vslot][e >> 5], 1u << (e & 31));
+                    __syncwarp();
                     if (lane == 0) mbar_arrive(bar(sh.scan[half]));
                     if (!wait(bar(sh.scan[half]), scans & 1, abort, W_SCAN)) goto done;
                     ++scans;
+                    bool mine = false;                         // this thread's entry is noted
 #pragma unroll 1
-                    for (int k = 0; k < TN; k += 32) poison |= (*(volatile uint32_t *)&sh.bad[vslot][k / 32] & sees(k)) != 0;
+                    for (int k = 0; k < TN; k += 32) {
+                        const uint32_t bad = *(volatile uint32_t *)&sh.bad[vslot][k / 32];
+                        poison |= (bad & sees(k)) != 0;
+                        if ((e & ~31) == k) mine = (bad >> (e & 31) & 1u) != 0;
+                    }
+                    if (mine) {
+                        for (int k = at % PER; k < p.c.dim / 8; k += PER)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(piece(k)), "r"(0u) : "memory");
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
                 }
                 vslot += 2;
                 if (vslot >= p.slots) {

@@ -765,3 +765,42 @@ def test_windows_that_no_int32_holds(ops, window):
     cache = make_cache(ops, [40], 1, 64, 16)
     with pytest.raises(ValueError, match="window"):
         ops.attn_prefill(cache, queries(cache, [40], 4, 2).cuda(), window=window)
+
+
+@pytest.mark.parametrize("dtype,dim,group", [(BF16, 128, 1), (F16, 64, 4), (BF16, 192, 2)])
+def test_values_that_are_not_finite_in_tiles_that_two_halves_share(ops, dtype, dim, group):
+    """Every tile is seen in part and holds V entries that are not finite, in units whose two halves both look for them: rows
+    that see none are the same bit for bit in every one of many calls, the others not finite."""
+    lens, N, window = [900], 600, 40
+    cache = make_cache(ops, lens, 2, dim, 16, dtype)
+    q = queries(cache, lens, N, group).cuda()
+    want = ops.attn_prefill(cache, q, window=window)
+    where = [s for s in range(0, 900, 57)]
+    for i, s in enumerate(where):
+        pg, off = serve_ref.slot_place(cache.table.cpu(), 16, 0, s)
+        cache.v[pg, :, off, (i * 37) % dim] = (float("nan"), float("inf"), float("-inf"))[i % 3]
+    hit = torch.tensor([any(i - window < s <= i for s in where) for i in range(300, 900)]).cuda()
+    assert 100 < int(hit.sum()) < 500
+    outs = [ops.attn_prefill(cache, q, window=window) for _ in range(100)]
+    ops.check_status()
+    for got in outs:
+        assert torch.equal(got[~hit], want[~hit])
+        assert not bool(torch.isfinite(got[hit]).all(-1).any())
+
+
+@pytest.mark.parametrize("N,group,dim,page", [(40, 4, 128, 16), (40, 4, 128, 7), (40, 2, 256, 16)])
+def test_rows_that_are_not_there_may_hold_anything(ops, N, group, dim, page):
+    """q rows past the counts that are not finite: the others are the same bit for bit."""
+    lens, new = [300, 200], [25, 7]
+    cache = make_cache(ops, lens, 2, dim, page, BF16)
+    q = queries(cache, lens, N, group)
+    want = ops.attn_prefill(cache, q.cuda(), new=dev(new))
+    want_cap = ops.attn_prefill(cache, q.cuda(), new=dev(new), cap=5.0, window=100)
+    bad = q.view(2, N, 2 * group, dim).clone()
+    for b, n in enumerate(new):
+        bad[b, n:] = float("nan")
+        bad[b, n + 1::2] = float("inf")
+    bad = bad.view_as(q).cuda()
+    assert torch.equal(ops.attn_prefill(cache, bad, new=dev(new)), want)
+    assert torch.equal(ops.attn_prefill(cache, bad, new=dev(new), cap=5.0, window=100), want_cap)
+    ops.check_status()
