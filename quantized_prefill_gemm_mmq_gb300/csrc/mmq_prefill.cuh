@@ -916,286 +916,288 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             }
             tc_fence_before();
         }
-    } else if (warp < SOFT + 2) {
-        // ------------------------------------------------------------------ one thread per half issues its products
-        if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        constexpr uint32_t kIdS = idesc<T>(TN, false);
-        const uint32_t id_o = idesc<T>(p.ksteps * 16, true);
-        const int i = warp - SOFT;                             // the half; with one half the second warp has nothing to do
-        int g = 0, runs = 0, slot = 0, phase = 0;              // slot: of the next tile's K
-        constexpr int KSTEPS = S::kMaxDim / 16;
-        auto product_s = [&](int sb, int at, bool last) {      // S buffer sb, K in slot `at`
-            const uint64_t a = sdesc_k_sw128(base + i * q_bytes), b = sdesc_k_sw128(ring + at * slot_bytes);
-            if (elect()) {
-#pragma unroll
-                for (int k = 0; k < KSTEPS; ++k)
-                    if (k < p.ksteps)
-                        umma_f16(tmem + sb * TN, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
-                                 b + (((k >> 2) * (TN * 128) + (k & 3) * 32) >> 4), kIdS, k > 0);
-                umma_commit(bar(sh.s[sb]));
-                umma_commit(bar(sh.empty[at]));
-                if (last) umma_commit(bar(sh.q_empty));
-            }
-            __syncwarp();
-        };
-        auto product_o = [&](int sb, int at, int part, bool add, bool last) {
-            constexpr int STEPS = TN / 16 / PARTS;
-            const uint64_t b = sdesc_mn_sw128(ring + at * slot_bytes + part * STEPS * 2048, TN * 128);
-            if (elect()) {
-#pragma unroll
-                for (int k = 0; k < STEPS; ++k)
-                    umma_f16_ts(tmem + S::kO + i * S::kOPitch, tmem + sb * TN + 8 * (part * STEPS + k), b + ((k * 2048) >> 4), id_o,
-                                add || k > 0);
-                if (part == PARTS - 1) {
-                    umma_commit(bar(sh.empty[at]));
-                    if (last) umma_commit(bar(sh.pv[i]));
-                }
-            }
-            __syncwarp();
-        };
-        auto waits = [&](uint64_t &b, int parity, int site) {
-            const bool ok = wait(bar(b), parity, abort, site);
-            tc_fence_after();
-            return ok;
-        };
-        auto work = [&](int nt) {
-            if (!waits(sh.q_full, runs & 1, W_Q) || !waits(sh.full[slot], phase, W_K)) return false;
-            product_s(NQ == 2 ? i : g & 1, slot, nt == 1);
-            for (int j = 0; j < nt; ++j, ++g) {
-                int vs = slot + 1, vp = phase;
-                if (vs >= p.slots) vs = 0, vp ^= 1;
-                int ks = vs + 1, kp = vp;
-                if (ks >= p.slots) ks = 0, kp ^= 1;
-                const bool more = j + 1 < nt;
-                const int sb = NQ == 2 ? i : g & 1;
-                // V and the next K are waited for before P, so that nothing but P holds the products up.  The halves take
-                // turns, a tile's products at a time: otherwise both wait for scores, then both for the tensor core.
-                if (!waits(sh.full[vs], vp, W_V)) return false;
-                if (more && !waits(sh.full[ks], kp, W_K)) return false;
-                if (NQ == 1 && more) product_s((g + 1) & 1, ks, j + 2 == nt);      // while this tile's scores are worked on
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part) {
-                    if (!waits(sh.p[sb * PARTS + part], NQ == 2 ? g & 1 : (g >> 1) & 1, W_P)) return false;
-                    if (NQ == 2 && part == 0 && !waits(sh.turn[i], i == 0 ? (g & 1) ^ 1 : g & 1, W_TURN)) return false;
-                    product_o(sb, vs, part, j > 0 || part > 0, NQ == 1 || !more);
-                }
-                if (NQ == 2) {
-                    if (more) product_s(sb, ks, j + 2 == nt);
-                    if (lane == 0) mbar_arrive(bar(sh.turn[i ^ 1]));
-                    __syncwarp();
-                }
-                slot = ks;
-                phase = kp;
-            }
-            ++runs;
-            return true;
-        };
-        if (i < NQ) {
-            PrefillRun run;
-            while (hear(run)) {
-                const int nt = run.u.t1 - run.u.t0;
-                if (nt > 0 && !work(nt)) break;
-            }
-            if (elect()) umma_commit(bar(sh.drain[i]));        // nothing is under way when tensor memory is given back
-            __syncwarp();
-            uint32_t never = 0;
-            mbar_wait_warp(bar(sh.drain[i]), 0, &never, KID_PREFILL, W_DRAIN);
-        }
     } else {
-        // ------------------------------------------------------------------ loaders; the first finds the runs
+        // The other four warps give up theirs in one instruction, as a warpgroup has to.
         if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        const int lw = warp - SOFT - 2;
-        const int pieces = p.ksteps * 2;                       // 16-byte pieces of a row, past `dim` zeros
-        const int step_row = 32 / pieces, step_piece = 32 - step_row * pieces;
-        const int row0 = lane / pieces, piece0 = lane - row0 * pieces;
-        constexpr int BATCH = TN / 32 / LOADERS;               // batches of 32 rows per warp and tile
-        uint32_t queue[LAG];                                   // barriers of the copies under way, 0 for none
+        if (warp < SOFT + 2) {
+            // ------------------------------------------------------------------ one thread per half issues its products
+            constexpr uint32_t kIdS = idesc<T>(TN, false);
+            const uint32_t id_o = idesc<T>(p.ksteps * 16, true);
+            const int i = __shfl_sync(0xffffffffu, warp, 0) - SOFT;    // the half, uniform; with one half the second warp has nothing to do
+            int g = 0, runs = 0, slot = 0, phase = 0;              // slot: of the next tile's K
+            constexpr int KSTEPS = S::kMaxDim / 16;
+            auto product_s = [&](int sb, int at, bool last) {      // S buffer sb, K in slot `at`
+                const uint64_t a = sdesc_k_sw128(base + i * q_bytes), b = sdesc_k_sw128(ring + at * slot_bytes);
+                if (elect()) {
 #pragma unroll
-        for (int i = 0; i < LAG; ++i) queue[i] = 0;
-        // 32 rows whose addresses the lanes hold (null: zeros), `pitch` bytes between their 64-value chunks
-        auto copy_rows = [&](const T *at, uint32_t dst, int first_row, uint32_t pitch) {
-            int row = row0, piece = piece0;
-#pragma unroll 1
-            for (int i = 0; i < pieces; ++i) {
-                const T *src = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, (unsigned long long)at, row));
-                const bool there = src != nullptr && piece * 8 < p.c.dim;
-                const int rr = first_row + row;
-                cp16(dst + (piece >> 3) * pitch + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4),
-                     there ? static_cast<const void *>(src + piece * 8) : p.c.k, there ? 16u : 0u);
-                row += step_row;
-                piece += step_piece;
-                if (piece >= pieces) piece -= pieces, ++row;
-            }
-        };
-        auto announce = [&](uint32_t b) {                      // the oldest copies have arrived
-            if (b == 0) return;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b);
-        };
-        auto push = [&](uint32_t b) {
-            cp_commit();
-            cp_wait<LAG>();
-            announce(queue[0]);
-#pragma unroll
-            for (int i = 0; i + 1 < LAG; ++i) queue[i] = queue[i + 1];
-            queue[LAG - 1] = b;
-        };
-        auto flush = [&]() {
-            cp_wait<0>();
-#pragma unroll
-            for (int i = 0; i < LAG; ++i) {
-                announce(queue[i]);
-                queue[i] = 0;
-            }
-        };
-        // Before a wait that others may have to end with what is still under way here.
-        auto waits = [&](uint64_t &b, int parity, int site) {
-            if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), (uint32_t)parity))) return true;
-            flush();
-            return wait(bar(b), parity, abort, site);
-        };
-        int runs = 0, slot = 0, phase = 0;                     // runs: whose q is copied
-        auto load = [&](const PrefillUnit &u) {
-            if (!waits(sh.q_empty, (runs & 1) ^ 1, W_QEMPTY)) return false;
-            if (p.q_box) {                                     // rows of other sequences, or zeros, in place of rows that are not there
-                if (lane == 0) {
-                    if (lw == 0) mbar_arrive_expect_tx(bar(sh.q_full), (uint32_t)(NQ * p.chunks * (128 * 128)));
-                    else mbar_arrive(bar(sh.q_full));
+                    for (int k = 0; k < KSTEPS; ++k)
+                        if (k < p.ksteps)
+                            umma_f16(tmem + sb * TN, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                                     b + (((k >> 2) * (TN * 128) + (k & 3) * 32) >> 4), kIdS, k > 0);
+                    umma_commit(bar(sh.s[sb]));
+                    umma_commit(bar(sh.empty[at]));
+                    if (last) umma_commit(bar(sh.q_empty));
                 }
                 __syncwarp();
-                if (lw == 0 && lane < NQ * p.chunks) {
-                    const int i = lane / p.chunks, ch = lane - i * p.chunks;
-                    tma_load_4d(base + i * q_bytes + ch * (128 * 128), &p.q_map, bar(sh.q_full), ch * 64, u.h * p.group,
-                                u.b * p.new_tokens + p.group_div.of(u.rt * RT + i * 128), 0);
-                }
-            } else {
-#pragma unroll 1
-                for (int bt = lw; bt < RT / 32; bt += LOADERS) {
-                    const int r = u.rt * RT + bt * 32 + lane, t = p.group_div.of(min(r, p.rows - 1));
-                    const bool live = r < p.rows && t < u.n;
-                    const T *at = live ? static_cast<const T *>(p.q) + ((int64_t)u.b * p.new_tokens + t) * p.ldq +
-                                             (int64_t)(u.h * p.group + (r - t * p.group)) * p.c.dim
-                                       : nullptr;
-                    copy_rows(at, base + (bt >> 2) * q_bytes, (bt & 3) * 32, 128 * 128);
-                }
-                push(bar(sh.q_full));
-            }
-            ++runs;
-            for (int tile = u.t0; tile < u.t1; ++tile) {
-                if (p.box) {                                   // boxes of entries of one page
-                    const int boxes = TN / p.box;
-                    const bool mine = lane < boxes && lane % LOADERS == lw;
-                    int pg = 0, off = 0;
-                    if (mine) {
-                        const int e = tile * TN + lane * p.box, col = p.page_div.of(e);
-                        off = e - col * p.c.page_size;
-                        // past the length lies a page that does not exist: zeros
-                        pg = e < u.len ? cache_page(p.c, u.b, col, KID_PREFILL) : (int)p.c.pages;
-                        if (pg < 0) pg = off = 0;
+            };
+            auto product_o = [&](int sb, int at, int part, bool add, bool last) {
+                constexpr int STEPS = TN / 16 / PARTS;
+                const uint64_t b = sdesc_mn_sw128(ring + at * slot_bytes + part * STEPS * 2048, TN * 128);
+                if (elect()) {
+#pragma unroll
+                    for (int k = 0; k < STEPS; ++k)
+                        umma_f16_ts(tmem + S::kO + i * S::kOPitch, tmem + sb * TN + 8 * (part * STEPS + k), b + ((k * 2048) >> 4), id_o,
+                                    add || k > 0);
+                    if (part == PARTS - 1) {
+                        umma_commit(bar(sh.empty[at]));
+                        if (last) umma_commit(bar(sh.pv[i]));
                     }
-                    const int many = __popc(__ballot_sync(0xffffffffu, mine));
+                }
+                __syncwarp();
+            };
+            auto waits = [&](uint64_t &b, int parity, int site) {
+                const bool ok = wait(bar(b), parity, abort, site);
+                tc_fence_after();
+                return ok;
+            };
+            auto work = [&](int nt) {
+                if (!waits(sh.q_full, runs & 1, W_Q) || !waits(sh.full[slot], phase, W_K)) return false;
+                product_s(NQ == 2 ? i : g & 1, slot, nt == 1);
+                for (int j = 0; j < nt; ++j, ++g) {
+                    int vs = slot + 1, vp = phase;
+                    if (vs >= p.slots) vs = 0, vp ^= 1;
+                    int ks = vs + 1, kp = vp;
+                    if (ks >= p.slots) ks = 0, kp ^= 1;
+                    const bool more = j + 1 < nt;
+                    const int sb = NQ == 2 ? i : g & 1;
+                    // V and the next K are waited for before P, so that nothing but P holds the products up.  The halves take
+                    // turns, a tile's products at a time: otherwise both wait for scores, then both for the tensor core.
+                    if (!waits(sh.full[vs], vp, W_V)) return false;
+                    if (more && !waits(sh.full[ks], kp, W_K)) return false;
+                    if (NQ == 1 && more) product_s((g + 1) & 1, ks, j + 2 == nt);      // while this tile's scores are worked on
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) {
+                        if (!waits(sh.p[sb * PARTS + part], NQ == 2 ? g & 1 : (g >> 1) & 1, W_P)) return false;
+                        if (NQ == 2 && part == 0 && !waits(sh.turn[i], i == 0 ? (g & 1) ^ 1 : g & 1, W_TURN)) return false;
+                        product_o(sb, vs, part, j > 0 || part > 0, NQ == 1 || !more);
+                    }
+                    if (NQ == 2) {
+                        if (more) product_s(sb, ks, j + 2 == nt);
+                        if (lane == 0) mbar_arrive(bar(sh.turn[i ^ 1]));
+                        __syncwarp();
+                    }
+                    slot = ks;
+                    phase = kp;
+                }
+                ++runs;
+                return true;
+            };
+            if (i < NQ) {
+                PrefillRun run;
+                while (hear(run)) {
+                    const int nt = run.u.t1 - run.u.t0;
+                    if (nt > 0 && !work(nt)) break;
+                }
+                if (elect()) umma_commit(bar(sh.drain[i]));        // nothing is under way when tensor memory is given back
+                __syncwarp();
+                uint32_t never = 0;
+                mbar_wait_warp(bar(sh.drain[i]), 0, &never, KID_PREFILL, W_DRAIN);
+            }
+        } else {
+            // ------------------------------------------------------------------ loaders; the first finds the runs
+            const int lw = warp - SOFT - 2;
+            const int pieces = p.ksteps * 2;                       // 16-byte pieces of a row, past `dim` zeros
+            const int step_row = 32 / pieces, step_piece = 32 - step_row * pieces;
+            const int row0 = lane / pieces, piece0 = lane - row0 * pieces;
+            constexpr int BATCH = TN / 32 / LOADERS;               // batches of 32 rows per warp and tile
+            uint32_t queue[LAG];                                   // barriers of the copies under way, 0 for none
+#pragma unroll
+            for (int i = 0; i < LAG; ++i) queue[i] = 0;
+            // 32 rows whose addresses the lanes hold (null: zeros), `pitch` bytes between their 64-value chunks
+            auto copy_rows = [&](const T *at, uint32_t dst, int first_row, uint32_t pitch) {
+                int row = row0, piece = piece0;
+#pragma unroll 1
+                for (int i = 0; i < pieces; ++i) {
+                    const T *src = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, (unsigned long long)at, row));
+                    const bool there = src != nullptr && piece * 8 < p.c.dim;
+                    const int rr = first_row + row;
+                    cp16(dst + (piece >> 3) * pitch + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4),
+                         there ? static_cast<const void *>(src + piece * 8) : p.c.k, there ? 16u : 0u);
+                    row += step_row;
+                    piece += step_piece;
+                    if (piece >= pieces) piece -= pieces, ++row;
+                }
+            };
+            auto announce = [&](uint32_t b) {                      // the oldest copies have arrived
+                if (b == 0) return;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b);
+            };
+            auto push = [&](uint32_t b) {
+                cp_commit();
+                cp_wait<LAG>();
+                announce(queue[0]);
+#pragma unroll
+                for (int i = 0; i + 1 < LAG; ++i) queue[i] = queue[i + 1];
+                queue[LAG - 1] = b;
+            };
+            auto flush = [&]() {
+                cp_wait<0>();
+#pragma unroll
+                for (int i = 0; i < LAG; ++i) {
+                    announce(queue[i]);
+                    queue[i] = 0;
+                }
+            };
+            // Before a wait that others may have to end with what is still under way here.
+            auto waits = [&](uint64_t &b, int parity, int site) {
+                if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), (uint32_t)parity))) return true;
+                flush();
+                return wait(bar(b), parity, abort, site);
+            };
+            int runs = 0, slot = 0, phase = 0;                     // runs: whose q is copied
+            auto load = [&](const PrefillUnit &u) {
+                if (!waits(sh.q_empty, (runs & 1) ^ 1, W_QEMPTY)) return false;
+                if (p.q_box) {                                     // rows of other sequences, or zeros, in place of rows that are not there
+                    if (lane == 0) {
+                        if (lw == 0) mbar_arrive_expect_tx(bar(sh.q_full), (uint32_t)(NQ * p.chunks * (128 * 128)));
+                        else mbar_arrive(bar(sh.q_full));
+                    }
+                    __syncwarp();
+                    if (lw == 0 && lane < NQ * p.chunks) {
+                        const int i = lane / p.chunks, ch = lane - i * p.chunks;
+                        tma_load_4d(base + i * q_bytes + ch * (128 * 128), &p.q_map, bar(sh.q_full), ch * 64, u.h * p.group,
+                                    u.b * p.new_tokens + p.group_div.of(u.rt * RT + i * 128), 0);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int bt = lw; bt < RT / 32; bt += LOADERS) {
+                        const int r = u.rt * RT + bt * 32 + lane, t = p.group_div.of(min(r, p.rows - 1));
+                        const bool live = r < p.rows && t < u.n;
+                        const T *at = live ? static_cast<const T *>(p.q) + ((int64_t)u.b * p.new_tokens + t) * p.ldq +
+                                                 (int64_t)(u.h * p.group + (r - t * p.group)) * p.c.dim
+                                           : nullptr;
+                        copy_rows(at, base + (bt >> 2) * q_bytes, (bt & 3) * 32, 128 * 128);
+                    }
+                    push(bar(sh.q_full));
+                }
+                ++runs;
+                for (int tile = u.t0; tile < u.t1; ++tile) {
+                    if (p.box) {                                   // boxes of entries of one page
+                        const int boxes = TN / p.box;
+                        const bool mine = lane < boxes && lane % LOADERS == lw;
+                        int pg = 0, off = 0;
+                        if (mine) {
+                            const int e = tile * TN + lane * p.box, col = p.page_div.of(e);
+                            off = e - col * p.c.page_size;
+                            // past the length lies a page that does not exist: zeros
+                            pg = e < u.len ? cache_page(p.c, u.b, col, KID_PREFILL) : (int)p.c.pages;
+                            if (pg < 0) pg = off = 0;
+                        }
+                        const int many = __popc(__ballot_sync(0xffffffffu, mine));
+#pragma unroll
+                        for (int kv = 0; kv < 2; ++kv) {
+                            if (!waits(sh.empty[slot], phase ^ 1, W_EMPTY)) return false;
+                            const uint32_t b = bar(sh.full[slot]), dst = ring + slot * slot_bytes + lane * p.box * 128;
+                            if (lw == 0 && lane < TN / 32) sh.bad[slot][lane] = 0;
+                            __syncwarp();
+                            const bool skip = p.withhold && lw == 0 && kv == 0 && tile == u.t1 - 1;
+                            if (lane == 0 && !skip) {
+                                if (many) mbar_arrive_expect_tx(b, (uint32_t)(many * p.chunks * p.box * 128));
+                                else mbar_arrive(b);
+                            }
+                            __syncwarp();
+                            if (mine && !skip)
+                                for (int ch = 0; ch < p.chunks; ++ch)
+                                    tma_load_4d(dst + ch * (TN * 128), kv ? &p.v_map : &p.k_map, b, ch * 64, off, u.h, pg);
+                            if (++slot == p.slots) slot = 0, phase ^= 1;
+                        }
+                        flush();                                   // what was copied otherwise
+                        continue;
+                    }
+                    const T *ka[BATCH], *va[BATCH];
+#pragma unroll
+                    for (int bt = 0; bt < BATCH; ++bt) {
+                        const int e = tile * TN + (bt * LOADERS + lw) * 32 + lane;
+                        ka[bt] = va[bt] = nullptr;
+                        if (e < u.len) {
+                            const int col = p.page_div.of(e);
+                            int off = e - col * p.c.page_size;
+                            int64_t pg = cache_page(p.c, u.b, col, KID_PREFILL);
+                            if (pg < 0) pg = off = 0;
+                            ka[bt] = static_cast<const T *>(p.c.k) + pg * p.c.k_page + u.h * p.c.k_head + off * p.c.k_slot;
+                            va[bt] = static_cast<const T *>(p.c.v) + pg * p.c.v_page + u.h * p.c.v_head + off * p.c.v_slot;
+                        }
+                    }
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         if (!waits(sh.empty[slot], phase ^ 1, W_EMPTY)) return false;
-                        const uint32_t b = bar(sh.full[slot]), dst = ring + slot * slot_bytes + lane * p.box * 128;
                         if (lw == 0 && lane < TN / 32) sh.bad[slot][lane] = 0;
-                        __syncwarp();
-                        const bool skip = p.withhold && lw == 0 && kv == 0 && tile == u.t1 - 1;
-                        if (lane == 0 && !skip) {
-                            if (many) mbar_arrive_expect_tx(b, (uint32_t)(many * p.chunks * p.box * 128));
-                            else mbar_arrive(b);
+                        if (!(p.withhold && lw == 0 && kv == 0 && tile == u.t1 - 1)) {
+#pragma unroll
+                            for (int bt = 0; bt < BATCH; ++bt)
+                                copy_rows(kv ? va[bt] : ka[bt], ring + slot * slot_bytes, (bt * LOADERS + lw) * 32, TN * 128);
+                            push(bar(sh.full[slot]));
                         }
-                        __syncwarp();
-                        if (mine && !skip)
-                            for (int ch = 0; ch < p.chunks; ++ch)
-                                tma_load_4d(dst + ch * (TN * 128), kv ? &p.v_map : &p.k_map, b, ch * 64, off, u.h, pg);
                         if (++slot == p.slots) slot = 0, phase ^= 1;
                     }
-                    flush();                                   // what was copied otherwise
-                    continue;
                 }
-                const T *ka[BATCH], *va[BATCH];
-#pragma unroll
-                for (int bt = 0; bt < BATCH; ++bt) {
-                    const int e = tile * TN + (bt * LOADERS + lw) * 32 + lane;
-                    ka[bt] = va[bt] = nullptr;
-                    if (e < u.len) {
-                        const int col = p.page_div.of(e);
-                        int off = e - col * p.c.page_size;
-                        int64_t pg = cache_page(p.c, u.b, col, KID_PREFILL);
-                        if (pg < 0) pg = off = 0;
-                        ka[bt] = static_cast<const T *>(p.c.k) + pg * p.c.k_page + u.h * p.c.k_head + off * p.c.k_slot;
-                        va[bt] = static_cast<const T *>(p.c.v) + pg * p.c.v_page + u.h * p.c.v_head + off * p.c.v_slot;
+                return true;
+            };
+            bool ok = true;
+            int asking = -1;                                       // whole: phase of an answer that has not come
+            if (lw == 0) {
+                PrefillWalk<RT, TN> w;
+                w.asked = 0;
+                if (!p.whole) w.split(p);
+                int2 join = make_int2(-1, 0);
+                for (bool first = true; ok; first = false) {
+                    int none = 0;
+                    if (p.whole) {
+                        const int st = w.next_whole(p, first, smem_u32(&sh.answer), bar(sh.next), abort);
+                        if (st == -2) asking = w.asked & 1;
+                        if (st == -2) break;
+                        none = st;
+                    } else if (!w.next_split(p, first)) {
+                        none = -1;
                     }
+                    if (!none && w.begins && !w.ends) {            // the CTA's last run: who has the rest of the unit
+                        join = make_int2((w.u.b * p.row_tiles + w.u.rt) * p.c.heads + w.u.h, w.owner(w.place + w.rest - 1));
+                    }
+                    if (!waits(sh.run_empty[run_at], run_phase ^ 1, W_RUN)) break;
+                    if (lane == 0) {
+                        sh.run[run_at].u = w.u;
+                        sh.run[run_at].flags = none ? 4 : (w.begins ? 1 : 0) | (w.ends ? 2 : 0);
+                        mbar_arrive(bar(sh.run_full[run_at]));
+                    }
+                    __syncwarp();
+                    if (++run_at == Shared::RUNS) run_at = 0, run_phase ^= 1;
+                    if (none) break;
+                    if (w.u.t0 < w.u.t1) ok = load(w.u);
+                    flush();                                       // before a wait for warps that may wait for these copies
                 }
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (!waits(sh.empty[slot], phase ^ 1, W_EMPTY)) return false;
-                    if (lw == 0 && lane < TN / 32) sh.bad[slot][lane] = 0;
-                    if (!(p.withhold && lw == 0 && kv == 0 && tile == u.t1 - 1)) {
-#pragma unroll
-                        for (int bt = 0; bt < BATCH; ++bt)
-                            copy_rows(kv ? va[bt] : ka[bt], ring + slot * slot_bytes, (bt * LOADERS + lw) * 32, TN * 128);
-                        push(bar(sh.full[slot]));
-                    }
-                    if (++slot == p.slots) slot = 0, phase ^= 1;
+                if (!p.whole && lane == 0) p.joins[blockIdx.x] = ok && !*abort ? join : make_int2(-1, 0);
+            } else {
+                PrefillRun run;
+                while (ok && hear(run)) {
+                    if (run.u.t0 < run.u.t1) ok = load(run.u);
+                    flush();
                 }
             }
-            return true;
-        };
-        bool ok = true;
-        int asking = -1;                                       // whole: phase of an answer that has not come
-        if (lw == 0) {
-            PrefillWalk<RT, TN> w;
-            w.asked = 0;
-            if (!p.whole) w.split(p);
-            int2 join = make_int2(-1, 0);
-            for (bool first = true; ok; first = false) {
-                int none = 0;
-                if (p.whole) {
-                    const int st = w.next_whole(p, first, smem_u32(&sh.answer), bar(sh.next), abort);
-                    if (st == -2) asking = w.asked & 1;
-                    if (st == -2) break;
-                    none = st;
-                } else if (!w.next_split(p, first)) {
-                    none = -1;
+            flush();
+            // A wait ran out: the copies under way still come to their end.  Each barrier is waited for in the phase of this warp's
+            // last copy; where one runs out here too (the other warp had no copy to add), all copies have had that time.
+            if (!ok || *abort) {
+                uint32_t never = 0;
+                for (int i = 0; i < p.slots; ++i) {
+                    const int before = i < slot ? phase : phase ^ 1;       // of the slot's last copy; none: over already
+                    if (lane == 0 && p.box) mbar_wait(bar(sh.full[i]), (uint32_t)before, &never, KID_PREFILL, W_DRAIN);
                 }
-                if (!none && w.begins && !w.ends) {            // the CTA's last run: who has the rest of the unit
-                    join = make_int2((w.u.b * p.row_tiles + w.u.rt) * p.c.heads + w.u.h, w.owner(w.place + w.rest - 1));
-                }
-                if (!waits(sh.run_empty[run_at], run_phase ^ 1, W_RUN)) break;
-                if (lane == 0) {
-                    sh.run[run_at].u = w.u;
-                    sh.run[run_at].flags = none ? 4 : (w.begins ? 1 : 0) | (w.ends ? 2 : 0);
-                    mbar_arrive(bar(sh.run_full[run_at]));
-                }
+                if (lane == 0 && asking >= 0) mbar_wait(bar(sh.next), (uint32_t)asking, &never, KID_PREFILL, W_DRAIN);
+                if (lane == 0 && p.q_box && runs > 0) mbar_wait(bar(sh.q_full), (uint32_t)((runs - 1) & 1), &never, KID_PREFILL, W_DRAIN);
                 __syncwarp();
-                if (++run_at == Shared::RUNS) run_at = 0, run_phase ^= 1;
-                if (none) break;
-                if (w.u.t0 < w.u.t1) ok = load(w.u);
-                flush();                                       // before a wait for warps that may wait for these copies
             }
-            if (!p.whole && lane == 0) p.joins[blockIdx.x] = ok && !*abort ? join : make_int2(-1, 0);
-        } else {
-            PrefillRun run;
-            while (ok && hear(run)) {
-                if (run.u.t0 < run.u.t1) ok = load(run.u);
-                flush();
-            }
-        }
-        flush();
-        // A wait ran out: the copies under way still come to their end.  Each barrier is waited for in the phase of this warp's
-        // last copy; where one runs out here too (the other warp had no copy to add), all copies have had that time.
-        if (!ok || *abort) {
-            uint32_t never = 0;
-            for (int i = 0; i < p.slots; ++i) {
-                const int before = i < slot ? phase : phase ^ 1;       // of the slot's last copy; none: over already
-                if (lane == 0 && p.box) mbar_wait(bar(sh.full[i]), (uint32_t)before, &never, KID_PREFILL, W_DRAIN);
-            }
-            if (lane == 0 && asking >= 0) mbar_wait(bar(sh.next), (uint32_t)asking, &never, KID_PREFILL, W_DRAIN);
-            if (lane == 0 && p.q_box && runs > 0) mbar_wait(bar(sh.q_full), (uint32_t)((runs - 1) & 1), &never, KID_PREFILL, W_DRAIN);
-            __syncwarp();
         }
     }
 done:
