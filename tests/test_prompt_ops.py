@@ -270,6 +270,34 @@ def test_scores_that_rise_and_fall(ops):
     check(ops, cache, q, lens, scale=1.0, first=[[1000 + t for t in range(N)]])
 
 
+@pytest.mark.parametrize("extra", [0, 1000], ids=["one launch", "joined"])
+@pytest.mark.parametrize("units", range(8))
+def test_weights_of_tiles_whose_maxima_are_large(ops, units, extra):
+    """Scores of -4093 and -4084 in powers of two, exact to 2^-12: a tile's weights against another tile's.  f32 has steps of
+    2^-11 from 4096 on and of 2^-12 below, so that a maximum of which 7 is taken off may be rounded; then the weights of one
+    tile lie off by the rounding, together.  The entry that is looked at weighs 2^6 and some steps of 2^-12 more or less, which
+    f16 rounds by up to half a step; nothing else is rounded by more than the f32 sums and the exponentials (2^-18)."""
+    import math
+    step, scale = 2.0 ** -12, 0.693147182464599609375        # log 2 in f32: times log2(e) it is 1 in f32
+    cache = make_cache(ops, [256], 1, 64, 16, F16, extra=extra)
+    k, v = torch.zeros((256, 64)), torch.zeros((256, 64))
+    k[:128, 0], k[:128, 1], k[:128, 2] = -4092, -1, -3 * step            # the first tile's maximum: -(4093 + 3 steps)
+    k[7, 0], k[7, 1], k[7, 2] = -4094, 0, (units - 1) * step             # 1 less, and units + 2 steps
+    k[128:, 0] = -4084                                                   # the second tile's
+    v[7, 0] = 1
+    flat = cache.table[0, :16].long()
+    for pool, x in ((cache.k, k), (cache.v, v)):
+        pool[flat] = x.view(16, 1, 16, 64).to(F16).cuda()
+    q = torch.zeros((1, 1, 64), dtype=F16)
+    q[0, 0, :3] = 1
+    got = float(ops.attn_prefill(cache, q.cuda(), scale=scale, out_dtype=F32)[0, 0, 0])
+    ops.check_status()
+    s = [float(k[j, 0]) + float(k[j, 1]) + float(k[j, 2]) + 4084 for j in range(256)]
+    weights = [math.exp2(x * scale / math.log(2)) for x in s]
+    want = weights[7] / math.fsum(weights)
+    assert abs(got / want - 1) <= ref.HALF[F16] + 2.0 ** -18
+
+
 # --------------------------------------------------------------- how it is called ---
 
 def test_rows_out_and_workspace_of_the_caller(ops):
