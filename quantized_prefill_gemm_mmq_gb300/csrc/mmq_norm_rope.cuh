@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) norm_rope_kernel(const 
     auto heads = [&](auto kind_, const float *src, int from, int to) {
         constexpr int kind = decltype(kind_)::value;
         if (from >= to) return;
-        // y0 = r (x0 w0 cos - x1 w1 sin), y1 = r (x0 w0 sin + x1 w1 cos); pairs that do not turn have cos 1, sin 0
+        // y0 = r (x0 w0 cos - x1 w1 sin), y1 = r (x0 w0 sin + x1 w1 cos); pairs that do not turn have cos 1 and no sine (0 times
+        // a value that is not finite would be NaN in the other one)
         const float *weight = kind == Q ? p.q_norm : p.k_norm;
         const bool normed = kind != V && weight != nullptr;
         float c0[4], s0[4], c1[4], s1[4];
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) norm_rope_kernel(const 
             if (normed && owner) read(weight, true, w0, w1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool turns = u * 4 + j < half;
+                const bool turns = WIDE ? u * 4 < half : u * 4 + j < half;
                 const float cs = turns ? s_cos[u * 4 + j] : 1.f, sn = turns ? s_sin[u * 4 + j] : 0.f;
                 c0[j] = w0[j] * cs, s0[j] = w0[j] * sn, c1[j] = w1[j] * cs, s1[j] = w1[j] * sn;
             }
@@ -210,9 +211,10 @@ __global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) norm_rope_kernel(const 
                 if (kind != V) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        const bool turns = WIDE ? u * 4 < half : u * 4 + j < half;
                         const float x0 = a[i][j], x1 = c[i][j];
-                        a[i][j] = x0 * c0[j] - x1 * s1[j];
-                        c[i][j] = x0 * s0[j] + x1 * c1[j];
+                        a[i][j] = turns ? x0 * c0[j] - x1 * s1[j] : x0 * c0[j];
+                        c[i][j] = turns ? x0 * s0[j] + x1 * c1[j] : x1 * c1[j];
                     }
                 }
                 if (kind == Q) {

@@ -528,6 +528,39 @@ def test_norm_rope_without_norms_is_rope_append(ops):
     assert float((got - want).abs().max()) <= 2.0 ** -21 and float((a.k - b.k).abs().max()) <= 2.0 ** -9 and torch.equal(a.v, b.v)
 
 
+@pytest.mark.parametrize("dim,rot,inter,page", [(64, 32, False, 16), (128, 64, True, 7), (80, 40, True, 16), (72, 36, False, 5), (72, 34, True, 16)])
+def test_values_past_the_rotated_ones_are_left_alone(ops, dim, rot, inter, page):
+    """NaN, infinities and -0 in values that do not turn: without a norm they come out as they are, and no other value
+    changes; with one, a head of finite values beside them is what it was."""
+    g = torch.Generator().manual_seed(dim + rot)
+    q, k, v = (torch.randn((2, h, dim), generator=g) for h in (4, 2, 2))
+    for x in (q, k):
+        x[0, 0, rot + 1], x[0, 1, rot], x[1, 0, dim - 1] = float("nan"), float("inf"), float("-inf")
+        x[1, 1, rot::2] = -0.0
+    pos, table = dev([8, 39]), ops.rope_table(rot)
+    caches = [make_cache(ops, [9, 40], 2, dim, page) for _ in range(2)]
+    want = ops.rope_append(caches[0], table, q.cuda(), k.cuda(), v.cuda(), pos, interleaved=inter)
+    got = ops.norm_rope_append(caches[1], table, q.cuda(), k.cuda(), v.cuda(), pos, interleaved=inter)
+    ops.check_status()
+
+    def bits(x):                                             # of NaNs there are many: a product with 1 may give another one
+        x = torch.where(torch.isnan(x), torch.full_like(x, float("nan")), x).contiguous()
+        return x.view(torch.int32 if x.dtype == F32 else torch.int16)
+    assert torch.equal(bits(got[..., rot:]), bits(want[..., rot:])) and torch.equal(bits(got[..., rot:].cpu()), bits(q[..., rot:]))
+    assert float((got[..., :rot] - want[..., :rot]).abs().max()) <= 2.0 ** -21 * 8
+    for b in range(2):
+        pg, off = serve_ref.slot_place(caches[0].table.cpu(), page, b, [8, 39][b])
+        a, c = (x.k[pg, :, off] for x in caches)
+        assert torch.equal(bits(a[:, rot:]), bits(c[:, rot:])) and torch.equal(bits(c[:, rot:].cpu()), bits(k[b, :, rot:].to(F16)))
+    w = torch.ones(dim).cuda()
+    normed = ops.norm_rope_append(caches[1], table, q.cuda(), k.cuda(), v.cuda(), pos, q_norm=w, k_norm=w, interleaved=inter)
+    clean = ops.norm_rope_append(caches[1], table, torch.nan_to_num(q, 1.0, 1.0, 1.0).cuda(), k.cuda(), v.cuda(), pos, q_norm=w, k_norm=w,
+                                 interleaved=inter)
+    ops.check_status()
+    finite = torch.isfinite(q).all(-1).cuda()
+    assert torch.equal(normed[finite], clean[finite]) and bool(torch.isfinite(normed[finite]).all())
+
+
 def test_norm_of_zeros_and_huge_rows(ops):
     cache = make_cache(ops, [3], 1, 64, 16, BF16)
     q = torch.zeros((3, 1, 64))
