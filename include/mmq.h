@@ -572,7 +572,8 @@ int mmq_norm_rope_append(const mmq_kv_cache *cache, const int64_t *freq, const i
  * NaN or +Inf, is not finite.  Scores, maxima and sums are f32; p enters the
  * tensor core rounded to the cache's type (11 or 8 bits), and an f32 `out` is
  * not rounded besides.  Results do not depend on timing.
- * new_tokens >= 1, q_heads a multiple (1 .. 128) of heads, scale finite,
+ * new_tokens >= 1, q_heads a multiple (1 .. 128) of heads, scale finite (and
+ * scale * log2(e)),
  * 0 <= cap <= 1024, window >= 0.  A len outside 0..cols*page_size counts as 0, a
  * new_len outside 0..new_tokens is limited to it, one above len counts as 0;
  * all are reported as MMQ_ERR_INDEX.  Sequences may share pages.  Refused too

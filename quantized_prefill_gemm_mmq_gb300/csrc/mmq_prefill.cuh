@@ -1412,7 +1412,7 @@ int attend(const mmq_kv_cache *cache, const Call &a, mmq_stream_t stream)
     if (rc != MMQ_OK) return rc;
     Plan q;
     if ((rc = make_plan(cache, a.q_heads, a.new_tokens, q)) != MMQ_OK) return rc;
-    if ((a.out_dtype != MMQ_F32 && a.out_dtype != cache->dtype) || a.ldq < (int64_t)a.q_heads * cache->dim || !isfinite(a.scale) ||
+    if ((a.out_dtype != MMQ_F32 && a.out_dtype != cache->dtype) || a.ldq < (int64_t)a.q_heads * cache->dim || !isfinite(a.scale * 1.44269504088896341f) ||
         !(a.cap >= 0.f && a.cap <= 1024.f) || a.window < 0 || (a.q && a.q == a.out))
         return MMQ_ERR_SHAPE;
     if (cache->seqs == 0) return MMQ_OK;

@@ -47,6 +47,13 @@ def test_prefill_refusals(a):
 
 
 @needs_lib
+def test_scales_that_overflow_in_powers_of_two(a):
+    """Finite in f32, but not times log2(e): every score of 0 would be NaN."""
+    assert prefill(a, scale=3e38) == prefill(a, scale=-3e38) == prefill(a, scale=3e38, cap=5.0) == -1
+    assert prefill(a, scale=2e38, work="odd") == -2          # as far as the alignment
+
+
+@needs_lib
 def test_tree_refusals(a):
     lib, c, p, n = _lib.load(), a.cache(), a.p, a.null
     call = lambda tree=p, new=1, cache=c, qh=4: lib.mmq_attn_tree(cache, p, 256, tree, n, n, a.odd, 0, qh, new, 0.1, 0.0, p, n)  # noqa: E731

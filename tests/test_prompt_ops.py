@@ -865,3 +865,15 @@ def test_rows_that_are_not_there_may_hold_anything(ops, N, group, dim, page):
     assert torch.equal(ops.attn_prefill(cache, bad, new=dev(new)), want)
     assert torch.equal(ops.attn_prefill(cache, bad, new=dev(new), cap=5.0, window=100), want_cap)
     ops.check_status()
+
+
+@pytest.mark.parametrize("cap", [1e-30, 1e-39, 1e-44])
+def test_the_smallest_caps(ops, cap):
+    """Scores of a cap that is next to nothing are equal, those of 0 among them: means of the values."""
+    cache = make_cache(ops, [70], 1, 64, 16, BF16)
+    pg, off = serve_ref.slot_place(cache.table.cpu(), 16, 0, 3)
+    cache.k[pg, 0, off] = 0
+    q = queries(cache, [70], 20, 2)
+    got = check(ops, cache, q, [70], cap=cap, out_dtype=F32)
+    assert bool(torch.isfinite(got).all())
+    check(ops, cache, q, [70], cap=cap, scale=-1.0, out_dtype=F32)
