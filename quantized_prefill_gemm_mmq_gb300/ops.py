@@ -472,8 +472,9 @@ def rope_fixed(inv: list[float]) -> list[int]:
 
 def rope_axes(rot: int, sections: list[int], alternate: bool = False) -> list[int]:
     """Which axis each of the rot/2 pairs turns by: sections[a] pairs of axis a, one block after
-    the other; or alternating (pair i to axis i % axes) as long as that axis has pairs left,
-    the rest to axis 0."""
+    the other.  Alternating, pair i goes to axis i % axes where that axis has pairs left, else to
+    axis 0: sections[a] is then the most that axis a > 0 gets, rot/2 allowing (every axes-th pair
+    from a on), and axis 0 has what is left; [8, 12, 12] gives 11, 11 and 10 pairs."""
     if len(sections) < 1 or len(sections) > ROPE_AXES_MAX or min(sections) < 0 or sum(sections) != rot // 2:
         raise ValueError(f"sections must be 1 to {ROPE_AXES_MAX} counts that add up to rot/2")
     if not alternate:
