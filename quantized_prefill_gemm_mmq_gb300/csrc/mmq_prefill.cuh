@@ -81,7 +81,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, int parity, volatile uint32_t
 
 template <typename T>
 constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-// p carries 2^kLift: f16 keeps 11 bits down to 2^-20.5 of the row's largest, and 2^(kLift + 8.5) still fits
+// p carries 2^kLift: f16 keeps 11 bits down to 2^-21 of the row's largest, and 2^(kLift + 8) still fits
 template <typename T>
 constexpr float kLift = kBf<T> ? 0.f : 7.f;
 constexpr float kLazy = 8.f;
@@ -101,17 +101,25 @@ __device__ __forceinline__ float pow2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// A row's weights are 2^(s c - b), b being the whole number nearest to m c, or m c itself from kLarge on: with m c below that,
-// which is rounded, tiles before and after a raise and parts that are joined would lie off by up to 2^-12 of a power of two
-// against one another, a third of f16's rounding.
+// A row's weights are 2^(s c + lifted(m)), or 2^((s - m) c + kLift) where m c is kLarge or more.
 constexpr float kLarge = 4096.f;
-// What sums of weights with the maximum m are multiplied by to go with the maximum `to`.
+template <typename T>
+__device__ __forceinline__ float lifted(float m, float c) { return __fsub_rn(kLift<T>, __fmul_rn(m, c)); }
+// By how much kLift - m c lies above that exponent, which is rounded twice (the product, the difference): below kLarge by up to
+// 1.5 * 2^-12.
+template <typename T>
+__device__ __forceinline__ float lost(float m, float c)
+{
+    const float a = __fmul_rn(m, c);
+    return fabsf(a) < kLarge ? (kLift<T> - (lifted<T>(m, c) + a)) - fmaf(m, c, -a) : 0.f;
+}
+// What sums of weights with the maximum m are multiplied by to go with the maximum `to`.  The exponents' roundings count:
+// without them tiles before and after a raise, and parts that are joined, lie off by 2^-12 of a power of two against one
+// another, a third of f16's rounding.
+template <typename T>
 __device__ __forceinline__ float rescale(float m, float to, float c)
 {
-    const float a = m * c, b = to * c;
-    const bool whole_a = fabsf(a) < kLarge, whole_b = fabsf(b) < kLarge;
-    if (whole_a && whole_b) return pow2(rintf(a) - rintf(b));
-    return pow2((m - to) * c + (whole_a ? fmaf(-m, c, rintf(a)) : 0.f) - (whole_b ? fmaf(-to, c, rintf(b)) : 0.f));
+    return pow2(fmaf(m - to, c, lost<T>(m, c) - lost<T>(to, c)));
 }
 // Asks for a CTA of this launch that has not started: its index comes to `at` (16 bytes) and counts on the barrier.
 __device__ __forceinline__ void ask_next(uint32_t at, uint32_t bar)
@@ -646,7 +654,8 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
         // ------------------------------------------------------------------ softmax: one row per thread
         // With 256 rows these warps need more registers than an equal share (168): 2 * 216 + 72 = 3 * 168.
         if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int half = __shfl_sync(0xffffffffu, warp, 0) >> 2, quarter = warp & 3, in_half = quarter * 32 + lane;
+        const int soft = __shfl_sync(0xffffffffu, warp, 0);    // uniform: the barriers' addresses are, then
+        const int half = soft >> 2, quarter = soft & 3, in_half = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t o_col = tmem + lanes + S::kO + half * S::kOPitch;
         const bool general = p.cap_out != 0.f || p.slopes || !(p.scale_log2 > 0.f);
@@ -672,7 +681,7 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
             const int max_lo = __reduce_max_sync(0xffffffffu, live ? see.lo : 0);
             const int min_hi = __reduce_min_sync(0xffffffffu, live ? see.hi : 0x7fffffff);
             const float slope = p.slopes && live ? p.slopes[head] * 1.44269504088896341f : 0.f;
-            float m = -INFINITY, l = 0.f, off = kLift<T>;      // off: kLift - (m c as a whole number)
+            float m = -INFINITY, l = 0.f, off = kLift<T>;      // off: lifted(m)
             bool poison = false, any_large = false;            // any_large: of the warp, see below
 
             for (int tile = u.t0; tile < u.t1; ++tile, ++g) {
@@ -821,10 +830,10 @@ __global__ void __launch_bounds__(PrefillShape<T, NQ, TN>::kThreads, 1) prefill_
                     if (again || !__any_sync(0xffffffffu, raise || any_large)) break;
                     float f = 1.f;
                     if (raise) {
-                        f = rescale(m, mx, c);
+                        f = rescale<T>(m, mx, c);
                         m = mx;
                         l *= f;
-                        off = kLift<T> - rintf(m * c);         // exact: see rescale
+                        off = lifted<T>(m, c);
                     }
                     const bool large = m != -INFINITY && !(fabsf(m * c) < kLarge);
                     any_large = __any_sync(0xffffffffu, large);
@@ -1261,7 +1270,7 @@ __global__ void __launch_bounds__(128) prefill_join_kernel(const __grid_constant
         for (int i0 = 0; i0 < n; i0 += 32) {
             if (i0 > 0) ml = weighed(i0 + lane);
             float wt = 0.f;
-            if (ml.y > 0.f) wt = rescale(ml.x, top, c);
+            if (ml.y > 0.f) wt = rescale<T>(ml.x, top, c);
             sum += ml.y > 0.f ? wt * ml.y : ml.y;              // 0, or a NaN
             for (int j = 0; j < 32 && i0 + j < n; j += BATCH) {
                 if (i0 + j > 0) load(i0 + j);
