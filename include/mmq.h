@@ -571,7 +571,9 @@ int mmq_norm_rope_append(const mmq_kv_cache *cache, const int64_t *freq, const i
  * included); a row that sees a V entry which is not finite, or a score that is
  * NaN or +Inf, is not finite.  Scores, maxima and sums are f32; p enters the
  * tensor core rounded to the cache's type (11 or 8 bits), and an f32 `out` is
- * not rounded besides.  Results do not depend on timing.
+ * not rounded besides.  Results do not depend on timing.  Nothing is added to
+ * cache->weight (mmq_attn_decode can): a prompt's entries keep the weight 0 that
+ * their append gave them, and mmq_kv_evict ranks them by that.
  * new_tokens >= 1, q_heads a multiple (1 .. 128) of heads, scale finite (and
  * scale * log2(e)),
  * 0 <= cap <= 1024, window >= 0.  A len outside 0..cols*page_size counts as 0, a
@@ -608,7 +610,8 @@ int mmq_attn_tree(const mmq_kv_cache *cache, const void *q, int64_t ldq, const u
  * leaves its place as it was and is reported as MMQ_ERR_INDEX, as are a count
  * outside 0..width and a new_len outside 0..nodes, which are limited to that.
  * cache->len is not changed: the caller lowers it by n - count[b] once all
- * layers are done.  The pages of the last n entries must not be shared.
+ * layers are done.  A sequence of fewer than n entries is left as it is and
+ * reported.  The pages of the last n entries must not be shared.
  * 0 <= width <= nodes <= 64; keep int32 [seqs][width].
  */
 int mmq_kv_keep(const mmq_kv_cache *cache, const int32_t *keep, const int32_t *count, const int32_t *new_len, int width,
@@ -698,7 +701,8 @@ int mmq_check_status(mmq_stream_t stream, int *detail);
  * of tiles that a CTA takes, so the waits for it run
  * out: the kernel records MMQ_ERR_TIMEOUT (see mmq_check_status), stops every
  * role, drains the work it issued, frees its tensor memory and returns; its
- * output is undefined.  Synchronous with respect to the host.  Returns MMQ_OK,
+ * output is undefined.  (Captured launches of the two attentions keep the mode
+ * they were captured under.)  Synchronous with respect to the host.  Returns MMQ_OK,
  * MMQ_ERR_SHAPE (unknown mode) or MMQ_ERR_CUDA.  Leave it at mode 0 outside
  * tests.
  */

@@ -41,13 +41,15 @@
 //   181     Q, and tiles that rows see in part, by tensor copies as well
 //   156     capped, biased and masked scores are worked over in tensor memory in a
 //           rolled loop: unrolled, the code did not stay in the instruction cache
-//   146     exponentials begin with the maximum so far; nothing is spilled (local
-//           memory shares its path with the tensor core's operands: 604 bytes of
-//           it cost 30 to 70 %)
+//   146     exponentials begin with the maximum so far; the softmax spills nothing
+//           (local memory shares its path with the tensor core's operands: 604
+//           bytes of it cost 30 to 70 %)
 //   144     packed arithmetic under a cap, one chain for the maximum
-// It is 1.0 PFLOP/s, 0.54 of cuBLAS' burst rate; 2048 rows of four heads over a
-// window of 8192 entries, bf16, 233 us = 1.2 PFLOP/s (0.61), the tensor pipe 57 %
-// active.  A tile of 256 rows takes 3300 cycles, its products 2048: the chain scores
+//   138     the softmax's warp index uniform, and with it the barriers' addresses
+//           (8192 rows under a cap 430 us before, 401 after)
+// It is 1.08 PFLOP/s, 0.56 of cuBLAS' burst rate; 2048 rows of four heads over a
+// window of 8192 entries, bf16, 235 us = 1.2 PFLOP/s (0.61), the tensor pipe 60 %
+// active.  A tile of 256 rows took 3300 cycles (at 146 us), its products 2048: the chain scores
 // -> exponentials -> P -> products of one half is longer than the other half's
 // products.  Not kept: two threads per row (212 us: they swap maxima through shared
 // memory, where a word takes some 200 cycles while operands are read), reading the
@@ -1330,9 +1332,9 @@ inline int make_plan(const mmq_kv_cache *c, int q_heads, int new_tokens, Plan &q
     const int64_t units = (int64_t)c->seqs * c->heads * q.row_tiles, cap = (int64_t)c->cols * c->page_size;
     if (units > 0x7fffff00 || units * ((cap + q.tn - 1) / q.tn) > 0x7fffff00) return MMQ_ERR_SHAPE;
     const int sms = sm_count();
-    // A unit per CTA where that keeps the device busy, or where no sequence is so long that cutting it would pay for the
-    // joining launch (5 us): 2048 rows of four heads over 8192 entries (256 units) took 255 us, cut into equal parts 274;
-    // one token over 513 entries of 32 heads 20 and 21.
+    // A unit per CTA where that keeps the device busy (2048 rows of four heads over 8192 entries, 256 units: 255 us, cut into
+    // equal parts 274), or where no sequence can be so long that cutting it would pay for the joining launch (5 us; one token
+    // over 513 entries of 32 heads 20 and 21).  The lengths are on the device: the table's columns go for them.
     const int64_t waves = (units + sms - 1) / sms;
     q.whole = (q.row_tiles > 1 && (units >= 3 * sms || units * 5 >= waves * sms * 4)) || cap <= 6 * q.tn;
     q.grid = q.whole ? (int)units : sms;
@@ -1421,8 +1423,8 @@ int attend(const mmq_kv_cache *cache, const Call &a, mmq_stream_t stream)
     if (rc != MMQ_OK) return rc;
     Plan q;
     if ((rc = make_plan(cache, a.q_heads, a.new_tokens, q)) != MMQ_OK) return rc;
-    if ((a.out_dtype != MMQ_F32 && a.out_dtype != cache->dtype) || a.ldq < (int64_t)a.q_heads * cache->dim || !isfinite(a.scale * 1.44269504088896341f) ||
-        !(a.cap >= 0.f && a.cap <= 1024.f) || a.window < 0 || (a.q && a.q == a.out))
+    if ((a.out_dtype != MMQ_F32 && a.out_dtype != cache->dtype) || a.ldq < (int64_t)a.q_heads * cache->dim ||
+        !isfinite(a.scale * 1.44269504088896341f) || !(a.cap >= 0.f && a.cap <= 1024.f) || a.window < 0 || (a.q && a.q == a.out))
         return MMQ_ERR_SHAPE;
     if (cache->seqs == 0) return MMQ_OK;
     if (!a.q || !a.out || !a.work) return MMQ_ERR_NULL;

@@ -733,6 +733,7 @@ def attn_prefill(cache: KVCache, q: torch.Tensor, scale: float | None = None, ca
     (int32 [seqs]) where that is more; with `window` the last `window` of them; with first
     (int32 [seqs*n]) those from that slot on, where the row's document begins.  cap > 0 turns
     scores into cap tanh(score / cap); slopes (float32 [q_heads]) then adds slope * (j - i).
+    Nothing is added to cache.weight, which kv_evict ranks by (attn_decode can add to it).
     scale defaults to dim^-0.5.  Without `workspace` one is allocated for this call."""
     index = cache.index
     if index != _current():
