@@ -539,10 +539,11 @@ int mmq_attn_decode(const mmq_kv_cache *cache, const float *q, int64_t ldq, cons
  * axis[i] (int32 [rot/2], 0..axes-1; NULL with one axis): pos int32
  * [axes][seqs*new_tokens], of which axis 0 goes to the cache's `pos`.  An axis
  * outside 0..axes-1 counts as 0 and is reported as MMQ_ERR_INDEX.  The
- * squares are added in f32.  q_out is f32 or the cache's type (q_dtype),
- * rounded once, rows ldo values apart (multiples of 4, or of 8); it may be q
- * itself where it is f32 and ldo == ldq.  Everything else, ragged counts and
- * reported errors among it, is as in mmq_rope_append.  1 <= axes <= 8, eps >= 0.
+ * squares are added in f32: a head whose values pass 10^18 may become 0.
+ * q_out is f32 or the cache's type (q_dtype), rounded once, rows ldo values
+ * apart (multiples of 4, or of 8); it may be q itself where it is f32 and
+ * ldo == ldq.  Everything else, ragged counts and reported errors among it, is
+ * as in mmq_rope_append.  1 <= axes <= 8, eps >= 0.
  */
 int mmq_norm_rope_append(const mmq_kv_cache *cache, const int64_t *freq, const int32_t *axis, int rot, float magnitude,
                          int interleaved, const float *q_norm, const float *k_norm, float eps, const float *q, int64_t ldq,
@@ -571,12 +572,13 @@ int mmq_norm_rope_append(const mmq_kv_cache *cache, const int64_t *freq, const i
  * included); a row that sees a V entry which is not finite, or a score that is
  * NaN or +Inf, is not finite.  Scores, maxima and sums are f32; p enters the
  * tensor core rounded to the cache's type (11 or 8 bits), and an f32 `out` is
- * not rounded besides.  Results do not depend on timing.  Nothing is added to
+ * not rounded besides.  Sums of p v are not divided before their end, with p up
+ * to 2^8 (bf16) or 2^15 (f16): bf16 values past 2^119 over the number of entries
+ * may overflow f32.  Results do not depend on timing.  Nothing is added to
  * cache->weight (mmq_attn_decode can): a prompt's entries keep the weight 0 that
  * their append gave them, and mmq_kv_evict ranks them by that.
- * new_tokens >= 1, q_heads a multiple (1 .. 128) of heads, scale finite (and
- * scale * log2(e)),
- * 0 <= cap <= 1024, window >= 0.  A len outside 0..cols*page_size counts as 0, a
+ * new_tokens >= 1, q_heads a multiple (1 .. 128) of heads, scale * log2(e)
+ * finite, 0 <= cap <= 1024, window >= 0.  A len outside 0..cols*page_size counts as 0, a
  * new_len outside 0..new_tokens is limited to it, one above len counts as 0;
  * all are reported as MMQ_ERR_INDEX.  Sequences may share pages.  Refused too
  * (MMQ_ERR_SHAPE, by both calls) are more than 2^31-1 tiles: cols*page_size /
