@@ -104,7 +104,16 @@ def test_axes():
     assert ops.rope_axes(12, [2, 3, 1]) == [0, 0, 1, 1, 1, 2]
     assert ops.rope_axes(16, [4, 2, 2], alternate=True) == [0, 1, 2, 0, 1, 2, 0, 0]
     assert ops.rope_axes(8, [4]) == [0, 0, 0, 0]
-    # alternating, as far as the pairs reach: axis 1 has 1, 4, .. 31, axis 2 has 2, 5, .. 29
+    for rot, bad in ((12, [2, 3]), (12, [7, -1]), (12, []), (18, [1] * 9)):
+        with pytest.raises(ValueError):
+            ops.rope_axes(rot, bad)
+
+
+def test_axes_that_alternate_as_far_as_the_pairs_reach():
+    """Against axes written out: sections that the order cannot give in full, and one that it can."""
+    pytest.importorskip("torch")
+    from quantized_prefill_gemm_mmq_gb300 import ops
+    # axis 1 has 1, 4, .. 31, axis 2 has 2, 5, .. 29
     pairs = [0, 1, 2] * 10 + [0, 1]
     assert ops.rope_axes(64, [8, 12, 12], alternate=True) == pairs
     assert [pairs.count(a) for a in range(3)] == [11, 11, 10]
@@ -112,6 +121,3 @@ def test_axes():
     assert ops.rope_axes(16, [6, 0, 2], alternate=True) == [0, 0, 2, 0, 0, 2, 0, 0]
     # one that fits: 11 pairs of axis 1 end at 31, 10 of axis 2 at 29
     assert ops.rope_axes(64, [11, 11, 10], alternate=True) == pairs
-    for rot, bad in ((12, [2, 3]), (12, [7, -1]), (12, []), (18, [1] * 9)):
-        with pytest.raises(ValueError):
-            ops.rope_axes(rot, bad)
